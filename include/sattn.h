@@ -413,6 +413,90 @@ sattn_status sattn_compress_kv(const void *kv, const void *score, const float *a
                                int32_t ratio, int32_t overlap, sattn_dtype in_dtype,
                                sattn_dtype out_dtype, void *cuda_stream);
 
+/*
+ * Paged FP8 cache: keys and values of many sequences in e4m3, in pages of
+ * page_size tokens that lie anywhere in a pool, with one scale for each page
+ * and KV head.
+ *   k_cache, v_cache uint8 [num_pages, Hkv, page_size, d]: OCP e4m3 codes;
+ *   k_scale, v_scale float32 [num_pages, Hkv]: value = e4m3(code) * scale;
+ *   page_table int32 [B, max_pages]: position p of sequence b lies in row
+ *     p mod page_size of page page_table[b][p / page_size];
+ *   cu_seqlens int32 [B + 1]: the call's tokens of sequence b are rows
+ *     cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the packed arrays ([0] = 0,
+ *     non-decreasing, at most T; rows behind the last one are not read or
+ *     written);
+ *   kv_lens int32 [B]: positions that sequence b has, the call's own tokens
+ *     included: these are its last cu_seqlens[b + 1] - cu_seqlens[b] ones.
+ * All are device pointers; page_size is 16, 32, 64 or 128, d 64 or 128,
+ * max_pages * page_size and num_pages * Hkv * page_size below 2^31. A sequence
+ * whose lengths contradict one another or exceed the page table, and an
+ * entry of the table in use that is no page, are skipped and reported by
+ * sattn_check_device; entries behind a sequence's last position are not read.
+ *
+ * sattn_paged_fp8_append rotates the call's keys (and queries) by their
+ * positions and stores its keys and values.
+ *   k, v [T, Hkv, d], q [T, H, d] (dtype): the heads of a token are contiguous,
+ *     tokens lie k_stride, v_stride, q_stride elements apart (multiples of 16
+ *     bytes), so slices of one projection's output serve as they are.
+ *   cos_sin float32 [rope_rows, rd] or NULL with rd = 0: row p holds the rd / 2
+ *     cosines, then the rd / 2 sines of position p. The first rd columns of a
+ *     head are rotated: column i with i + rd / 2, or with interleaved = 1
+ *     column 2 i with 2 i + 1. rd is a multiple of 16. Positions reach
+ *     rope_rows - 1 at most (a sequence beyond is skipped and reported).
+ *   q may be NULL; otherwise q_out [T, H, d] (dtype, contiguous; q itself where
+ *     that is contiguous) receives the rotated queries (rd > 0).
+ * The rotation is computed in fp32 and rounded once: q_out to dtype, keys to
+ * e4m3. The scale s of a page and head is the least power of two, at least
+ * 2^-64, with amax <= 448 s over the rows that the page has taken: the page's
+ * row 0 starts it, later rows may raise it, and the codes held by the page are
+ * then recoded, e4m3(value * old / new), which is exact for values that stay
+ * in e4m3's normal range. code = e4m3(x / s), nearest even, saturating at
+ * +-448; NaN stays NaN and does not count for amax; an infinity is stored as
+ * the largest value. (A scale that the caller put into a page counts as the
+ * next power of two.) The same call made twice leaves the same cache.
+ * The pages that a call's tokens go to must be in one sequence's table only
+ * (their contents are unspecified otherwise); pages that are only read may be
+ * shared. Nothing else of the cache is touched.
+ */
+sattn_status sattn_paged_fp8_append(
+    const void *k, int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+    int64_t q_stride, void *q_out, const float *cos_sin, int32_t rope_rows, int32_t rd,
+    int32_t interleaved, uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+    const int32_t *page_table, const int32_t *cu_seqlens, const int32_t *kv_lens, int32_t B,
+    int32_t T, int32_t H, int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_size,
+    int32_t max_pages, sattn_dtype dtype, void *cuda_stream);
+
+/*
+ * Attention of the call's queries over the paged FP8 cache.
+ *   q [T, H, d] (dtype), tokens q_stride elements apart; o [T, H, d] (dtype,
+ *   contiguous), lse [T, H] float32 or NULL.
+ * Query i of sequence b sits at position p = kv_lens[b] - n + i (n its number
+ * of queries) and sees key j of the sequence iff 0 <= j < kv_lens[b], with
+ * causal j <= p, and with window_left >= 0 also j >= p - window_left. Query
+ * head h reads KV head h / (H / Hkv). Sinks as for the other entry points (key
+ * 0 is position 0). A row that sees nothing has o = 0 and lse = -inf (sink
+ * with NULL_LOGIT). Rows of skipped sequences, and rows behind the last
+ * sequence, are not written. Keys in an invalid page contribute nothing.
+ * Scales may be any finite values >= 0.
+ *   max_q_len >= every sequence's number of queries: a hint that chooses the
+ *     kernel; any value gives the same results.
+ *   workspace: NULL or a caller-owned device buffer of at least
+ *     sattn_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned; it receives
+ *     partial results and is free again when the call's work has run. Calls
+ *     that may overlap on the GPU need one each.
+ */
+size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
+sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,
+                                 const uint8_t *v_cache, const float *k_scale,
+                                 const float *v_scale, const int32_t *page_table,
+                                 const int32_t *cu_seqlens, const int32_t *kv_lens, int32_t B,
+                                 int32_t T, int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d,
+                                 int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                 int32_t causal, int32_t window_left, const float *sinks,
+                                 sattn_sink_mode sink_mode, float scale, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, sattn_dtype dtype,
+                                 void *cuda_stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *sattn_status_str(sattn_status s);
 

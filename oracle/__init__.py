@@ -453,3 +453,102 @@ def xattn_find_blocks(block_sum, threshold):
                 if cum >= target:
                     break
     return out
+
+
+# ------------------------------------------------------- paged FP8 cache
+
+def pow2_scale(amax):
+    """The least power of two s >= 2^-64 with amax <= 448 s, by search over the
+    powers; an infinite amax counts as float32's largest value."""
+    amax = np.minimum(np.asarray(amax, np.float64), np.finfo(np.float32).max)
+    powers = 2.0 ** np.arange(-64, 122)
+    return powers[np.searchsorted(448.0 * powers, amax, side="left")]
+
+
+def rotate(x, cos_sin, pos, interleaved):
+    """x [n, heads, d] with its first rd columns rotated by the angles of the
+    positions pos [n]: the table's rows are rd / 2 cosines, then rd / 2 sines."""
+    x = np.array(x, np.float64)
+    rd = cos_sin.shape[1]
+    for i in range(rd // 2):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + rd // 2)
+        c = cos_sin[pos, i].astype(np.float64)[:, None]
+        s = cos_sin[pos, rd // 2 + i].astype(np.float64)[:, None]
+        xa, xb = x[:, :, a].copy(), x[:, :, b].copy()
+        x[:, :, a] = xa * c - xb * s
+        x[:, :, b] = xb * c + xa * s
+    return x
+
+
+def paged_append(rows, codes, scale, page_table, cu_seqlens, kv_lens):
+    """Stores the packed rows [T, Hkv, d] (already rotated) token by token's
+    page: returns the new (codes [pages, Hkv, page, d], scale [pages, Hkv])."""
+    codes, scale = codes.copy(), scale.astype(np.float64)
+    page = codes.shape[2]
+    rows = np.asarray(rows, np.float64)
+    for b, total in enumerate(kv_lens):
+        t0, t1 = int(cu_seqlens[b]), int(cu_seqlens[b + 1])
+        first = int(total) - (t1 - t0)
+        for j in range(first // page, (int(total) - 1) // page + 1 if t1 > t0 else 0):
+            lo, hi = max(first, j * page), min(int(total), (j + 1) * page)
+            new = rows[t0 + lo - first: t0 + hi - first]          # [m, Hkv, d]
+            pid, r0 = int(page_table[b][j]), lo - j * page
+            for h in range(rows.shape[1]):
+                x = new[:, h]
+                with np.errstate(invalid="ignore"):
+                    amax = np.fmax.reduce(np.abs(x).ravel(), initial=0.0)
+                s = float(pow2_scale(amax))
+                if r0 > 0:
+                    old = scale[pid, h]
+                    s = max(s, float(2.0 ** np.ceil(np.log2(old))))
+                    if s != old:
+                        held = e4m3_decode(codes[pid, h, :r0]) * (old / s)
+                        codes[pid, h, :r0] = e4m3_encode(held)
+                codes[pid, h, r0: r0 + len(x)] = e4m3_encode(x / s)
+                scale[pid, h] = s
+    return codes, scale.astype(np.float32)
+
+
+def paged_attend(q, k_codes, v_codes, k_scale, v_scale, page_table, cu_seqlens, kv_lens, causal,
+                 window_left, sinks, sink_mode, scale):
+    """Literal masked softmax of every query row over its sequence's cached
+    rows. Rows behind the last sequence come back as NaN."""
+    T, H, d = q.shape
+    Hkv, page = k_codes.shape[1:3]
+    o = np.full((T, H, d), np.nan)
+    lse = np.full((T, H), np.nan)
+    for b, L in enumerate(int(x) for x in kv_lens):
+        t0, t1 = int(cu_seqlens[b]), int(cu_seqlens[b + 1])
+        n = t1 - t0
+        if n == 0:
+            continue
+        ids = np.asarray(page_table[b][: -(-L // page)], np.int64)
+        pos = L - n + np.arange(n)
+        j = np.arange(L)
+        seen = np.ones((n, L), bool)
+        if causal:
+            seen &= j[None] <= pos[:, None]
+        if window_left >= 0:
+            seen &= j[None] >= pos[:, None] - window_left
+        for g in range(Hkv):
+            k = (e4m3_decode(k_codes[ids, g]) * k_scale[ids, g].astype(np.float64)[:, None, None]
+                 ).reshape(-1, d)[:L]
+            v = (e4m3_decode(v_codes[ids, g]) * v_scale[ids, g].astype(np.float64)[:, None, None]
+                 ).reshape(-1, d)[:L]
+            for h in range(g * (H // Hkv), (g + 1) * (H // Hkv)):
+                s = q[t0:t1, h].astype(np.float64) @ k.T * scale
+                if sink_mode == 1 and L > 0:
+                    s[:, 0] += float(sinks[h])
+                s = np.where(seen, s, -np.inf)
+                top = s.max(axis=1, initial=-np.inf)
+                if sink_mode == 2:
+                    top = np.maximum(top, float(sinks[h]))
+                base = np.where(np.isneginf(top), 0.0, top)
+                p = np.exp(s - base[:, None])
+                z = p.sum(axis=1)
+                if sink_mode == 2:
+                    z = z + np.exp(float(sinks[h]) - base)
+                with np.errstate(divide="ignore", invalid="ignore"):
+                    o[t0:t1, h] = np.where(z[:, None] > 0, p @ v / z[:, None], 0.0)
+                    lse[t0:t1, h] = np.where(z > 0, base + np.log(z), -np.inf)
+    return o, lse

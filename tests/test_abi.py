@@ -194,3 +194,49 @@ def test_workspace_bytes_for_huge_batches(lib):
     assert lib.sattn_sparse_workspace_bytes(65536, 65536, 32, 128, 640) == 0
     assert lib.sattn_sparse_workspace_bytes(2 ** 31 - 1, 2, 32, 128, 640) == 0
     assert lib.sattn_sparse_workspace_bytes(2 ** 31 - 1, 2 ** 31 - 1, 32, 128, 640) == 0
+
+
+def test_paged_fp8_refusals(lib):
+    """Each call differs from an acceptable one in the one argument named."""
+    f, i64 = ctypes.c_void_p(0x1000), ctypes.c_int64
+    odd = ctypes.c_void_p(0x1008)
+
+    def append(**kw):
+        a = dict(k=f, ks=1024, v=f, vs=1024, q=f, qs=4096, qo=f, cos=f, rows=64, rd=128, inter=0,
+                 kc=f, vc=f, ksc=f, vsc=f, table=f, cu=f, lens=f, B=2, T=4, H=32, Hkv=8, d=128,
+                 pages=10, page=64, width=4, dtype=1)
+        a.update(kw)
+        for n in ("ks", "vs", "qs"):
+            a[n] = i64(a[n])
+        return lib.sattn_paged_fp8_append(*a.values(), None)
+
+    for bad in (dict(B=-1), dict(T=-1), dict(Hkv=0), dict(d=96), dict(page=48), dict(page=256),
+                dict(pages=0), dict(width=0), dict(width=1 << 26), dict(pages=1 << 27),
+                dict(dtype=2), dict(rd=24), dict(rd=144), dict(rd=-16), dict(inter=2),
+                dict(rows=-1), dict(H=0), dict(rd=0), dict(ks=1023), dict(ks=1028), dict(vs=512),
+                dict(qs=2048), dict(k=None), dict(v=None), dict(kc=None), dict(vc=None),
+                dict(ksc=None), dict(vsc=None), dict(table=None), dict(cu=None), dict(lens=None),
+                dict(cos=None), dict(qo=None), dict(k=odd), dict(v=odd), dict(q=odd), dict(qo=odd),
+                dict(cos=odd), dict(kc=odd), dict(vc=odd)):
+        assert append(**bad) == 1, bad
+    assert append(T=0, k=None) == 0 and append(B=0, k=None) == 0  # empty: no work
+
+    def fwd(**kw):
+        a = dict(q=f, qs=4096, kc=f, vc=f, ksc=f, vsc=f, table=f, cu=f, lens=f, B=2, T=4, n=1, H=32,
+                 Hkv=8, d=128, pages=10, page=64, width=4, causal=1, window=-1, sinks=f, mode=2,
+                 scale=0.1, o=f, lse=f, ws=None, wsb=0, dtype=1)
+        a.update(kw)
+        a["qs"] = i64(a["qs"])
+        return lib.sattn_paged_fp8_fwd(*a.values(), None)
+
+    for bad in (dict(B=-1), dict(T=-1), dict(n=-1), dict(H=0), dict(H=12), dict(Hkv=0), dict(d=32),
+                dict(page=8), dict(pages=0), dict(width=0), dict(causal=2), dict(sinks=None),
+                dict(mode=3), dict(scale=0.0), dict(scale=float("nan")), dict(scale=float("inf")),
+                dict(dtype=7), dict(qs=4095), dict(qs=4100), dict(q=None), dict(kc=None),
+                dict(vc=None), dict(ksc=None), dict(vsc=None), dict(table=None), dict(cu=None),
+                dict(lens=None), dict(o=None), dict(q=odd), dict(kc=odd), dict(vc=odd), dict(o=odd),
+                dict(ws=odd)):
+        assert fwd(**bad) == 1, bad
+    assert fwd(T=0, q=None) == 0 and fwd(B=0, q=None) == 0
+    size = lib.sattn_paged_fp8_workspace_bytes
+    assert size(0, 32, 8, 128) == 0 and size(1, 30, 8, 128) == 0 and size(1, 32, 8, 96) == 0

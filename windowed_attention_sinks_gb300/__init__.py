@@ -86,6 +86,16 @@ def lib() -> ctypes.CDLL:
     L.sattn_compress_kv.argtypes = [P, P, P, P, i64, i32, i32, i32, i32, i32, ctypes.c_int,
                                     ctypes.c_int, P]
     L.sattn_compress_kv.restype = ctypes.c_int
+    L.sattn_paged_fp8_append.argtypes = [P, i64, P, i64, P, i64, P, P, i32, i32, i32, P, P, P, P,
+                                         P, P, P, i32, i32, i32, i32, i32, i32, i32, i32,
+                                         ctypes.c_int, P]
+    L.sattn_paged_fp8_append.restype = ctypes.c_int
+    L.sattn_paged_fp8_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.sattn_paged_fp8_workspace_bytes.restype = sz
+    L.sattn_paged_fp8_fwd.argtypes = [P, i64, P, P, P, P, P, P, P, i32, i32, i32, i32, i32, i32,
+                                      i32, i32, i32, i32, i32, P, ctypes.c_int, f32, P, P, P, sz,
+                                      ctypes.c_int, P]
+    L.sattn_paged_fp8_fwd.restype = ctypes.c_int
     L.sattn_status_str.argtypes = [ctypes.c_int]
     L.sattn_status_str.restype = ctypes.c_char_p
     L.sattn_set_debug.argtypes = [ctypes.c_int]
@@ -342,6 +352,140 @@ def kv_ring_write(kv_cache, kv_new, start_pos, win, stream=None):
            lib().sattn_kv_ring_write(_ptr(kv_cache), _ptr(kv_new), _ptr(start_pos), B, S, N, d,
                                      int(win), _dtype_code(kv_cache), _stream(stream)))
     return kv_cache
+
+
+def _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens):
+    """Checks the tensors of a paged FP8 cache; returns (pages, Hkv, page, d, B, max_pages)."""
+    import torch
+
+    device = k_cache.device
+    for t, n, dt in ((k_cache, "k_cache", torch.uint8), (v_cache, "v_cache", torch.uint8),
+                     (k_scale, "k_scale", torch.float32), (v_scale, "v_scale", torch.float32),
+                     (page_table, "page_table", torch.int32),
+                     (cu_seqlens, "cu_seqlens", torch.int32), (kv_lens, "kv_lens", torch.int32)):
+        _need(t, n, dt, device)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must have one shape [pages, Hkv, page, d]")
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_scale and v_scale must be [pages, Hkv]")
+    B = kv_lens.shape[0]
+    if page_table.dim() != 2 or page_table.shape[0] != B or cu_seqlens.numel() != B + 1:
+        raise ValueError("page_table must be [B, max_pages], cu_seqlens [B + 1], kv_lens [B]")
+    return (*shape, B, page_table.shape[1])
+
+
+def _token_rows(t, name, T, heads, d, dtype, device):
+    """Checks [T, heads, d] whose heads are contiguous within a token; returns the token stride."""
+    if t.shape != (T, heads, d) or t.dtype != dtype or t.device != device:
+        raise ValueError("%s must be %s [%d, %d, %d] on %s" % (name, dtype, T, heads, d, device))
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    return st[0] if T > 1 else heads * d
+
+
+def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
+                     cos_sin=None, interleaved=False, q=None, q_out=None, stream=None):
+    """Store the new tokens' keys (rotated by their positions) and values in the
+    pages of an e4m3 cache (sattn_paged_fp8_append), updated in place.
+
+    k, v [T, Hkv, d] bf16 or fp32 (tokens may be strided, as slices of one
+    projection are); k_cache, v_cache uint8 [pages, Hkv, page, d]; k_scale,
+    v_scale fp32 [pages, Hkv]; page_table int32 [B, max_pages]; cu_seqlens int32
+    [B + 1]; kv_lens int32 [B], the lengths with the new tokens; cos_sin fp32
+    [positions, rd]. With q [T, H, d] returns the rotated queries, else None."""
+    import torch
+
+    pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                 cu_seqlens, kv_lens)
+    dev = k_cache.device
+    T = k.shape[0]
+    ks = _token_rows(k, "k", T, Hkv, d, k.dtype, dev)
+    vs = _token_rows(v, "v", T, Hkv, d, k.dtype, dev)
+    rows = rd = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", torch.float32, dev)
+        rows, rd = cos_sin.shape
+    H = qs = 0
+    if q is not None:
+        H = q.shape[1]
+        qs = _token_rows(q, "q", T, H, d, k.dtype, dev)
+        if q_out is None:
+            q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+        else:
+            _need(q_out, "q_out", q.dtype, dev)
+            if q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with torch.cuda.device(dev):
+        code = lib().sattn_paged_fp8_append(
+            k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, _ptr(q_out), _ptr(cos_sin), rows, rd,
+            1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
+            B, T, H, Hkv, d, pages, page, width, _dtype_code(k), _stream(stream))
+    _check("sattn_paged_fp8_append", code)
+    return q_out
+
+
+def paged_fp8_workspace_bytes(max_q_len, H, Hkv, d):
+    """Workspace bytes of paged_fp8_fwd (sattn_paged_fp8_workspace_bytes)."""
+    return int(lib().sattn_paged_fp8_workspace_bytes(int(max_q_len), int(H), int(Hkv), int(d)))
+
+
+def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
+                  max_q_len=None, causal=True, window_left=-1, sinks=None, sink_mode=SINK_NONE,
+                  scale=None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of q [T, H, d] (the last tokens of each sequence) over the
+    pages of an e4m3 cache (sattn_paged_fp8_fwd); the cache's tensors as for
+    paged_fp8_append. Returns (o, lse). Rows behind the last sequence are not
+    written. Without a workspace one is taken from torch's allocator, on the
+    current stream."""
+    import torch
+
+    pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table,
+                                                 cu_seqlens, kv_lens)
+    dev = k_cache.device
+    T, H = q.shape[0], q.shape[1]
+    qs = _token_rows(q, "q", T, H, d, q.dtype, dev)
+    if sinks is not None:
+        _need(sinks, "sinks", torch.float32, dev)
+        if sinks.numel() != H:
+            raise ValueError("sinks must be [H]")
+    if o is None:
+        o = torch.empty((T, H, d), dtype=q.dtype, device=dev)
+    else:
+        _need(o, "o", q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", torch.float32, dev)
+    if o.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError("o must be [T, H, d] and lse [T, H]")
+    n = T if max_q_len is None else int(max_q_len)
+    nb = 0
+    if workspace is None:
+        nb = lib().sattn_paged_fp8_workspace_bytes(n, H, Hkv, d) if q.dtype == torch.bfloat16 else 0
+        if nb:
+            if stream is None:
+                workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+            else:  # the allocator must know the stream that uses it
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", None, dev)
+        nb = workspace.numel() * workspace.element_size()
+    scale = float(d ** -0.5 if scale is None else scale)
+    with torch.cuda.device(dev):
+        code = lib().sattn_paged_fp8_fwd(
+            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+            v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
+            B, T, n, H, Hkv, d, pages, page, width, int(bool(causal)), int(window_left),
+            _ptr(sinks), int(sink_mode), scale, o.data_ptr(), lse.data_ptr(), _ptr(workspace), nb,
+            _dtype_code(q), _stream(stream))
+    _check("sattn_paged_fp8_fwd", code)
+    return o, lse
 
 
 def compress_kv(kv, score, ape, ratio, overlap, out=None, out_dtype=None, stream=None):

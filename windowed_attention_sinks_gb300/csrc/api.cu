@@ -163,6 +163,17 @@ bool finite_scale(float s) { return s == s && s - s == 0.0f && s > 0.0f; }
 // TMA tiles need 16-byte aligned base addresses.
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Shape of a paged cache: [num_pages, Hkv, page, d], a table of max_pages a sequence.
+bool valid_paged(int Hkv, int d, int num_pages, int page, int max_pages) {
+    return Hkv > 0 && (d == 64 || d == 128) && num_pages > 0 && max_pages > 0 &&
+           (page == 16 || page == 32 || page == 64 || page == 128) &&
+           (int64_t)max_pages * page <= INT32_MAX && (int64_t)num_pages * Hkv * page <= INT32_MAX;
+}
+// Rows of `heads` x d elements, `stride` apart, each on a 16-byte boundary.
+bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {
+    return stride >= (int64_t)heads * d && stride % unit == 0;
+}
+
 // sm_103 only: the fatbin carries sm_103a code and nothing else.
 sattn_status check_arch(const DevInfo *dev) {
     if (dev->cc_major != 10 || dev->cc_minor != 3) return SATTN_ERR_UNSUPPORTED;
@@ -173,7 +184,7 @@ sattn_status check_arch(const DevInfo *dev) {
 
 extern "C" {
 
-int32_t sattn_version(void) { return 103; }
+int32_t sattn_version(void) { return 104; }
 
 const char *sattn_status_str(sattn_status s) {
     switch (s) {
@@ -497,6 +508,84 @@ sattn_status sattn_kv_ring_write(void *kv_cache, const void *kv_new, const int32
     cudaStream_t s = as_stream(cuda_stream);
     return finish(launch_kv_ring_write(kv_cache, kv_new, start_pos, B, S, N, d, win, elem, *dev, s),
                   s);
+}
+
+sattn_status sattn_paged_fp8_append(
+    const void *k, int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+    int64_t q_stride, void *q_out, const float *cos_sin, int32_t rope_rows, int32_t rd,
+    int32_t interleaved, uint8_t *k_cache, uint8_t *v_cache, float *k_scale, float *v_scale,
+    const int32_t *page_table, const int32_t *cu_seqlens, const int32_t *kv_lens, int32_t B,
+    int32_t T, int32_t H, int32_t Hkv, int32_t d, int32_t num_pages, int32_t page_size,
+    int32_t max_pages, sattn_dtype dtype, void *cuda_stream) {
+    if (B < 0 || T < 0 || !valid_paged(Hkv, d, num_pages, page_size, max_pages) ||
+        !valid_dtype(dtype))
+        return SATTN_ERR_INVALID_ARG;
+    if (rd < 0 || rd > d || rd % 16 != 0 || rope_rows < 0 || (interleaved != 0 && interleaved != 1))
+        return SATTN_ERR_INVALID_ARG;
+    if (q && (H <= 0 || rd == 0)) return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;  // elements in 16 bytes
+    if (!valid_rows(k_stride, Hkv, d, unit) || !valid_rows(v_stride, Hkv, d, unit) ||
+        (q && !valid_rows(q_stride, H, d, unit)))
+        return SATTN_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return SATTN_OK;
+    if (!k || !v || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens ||
+        !kv_lens || (rd > 0 && !cos_sin) || (q && !q_out))
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) ||
+        !aligned16(cos_sin) || !aligned16(k_cache) || !aligned16(v_cache))
+        return SATTN_ERR_INVALID_ARG;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    PagedAppendArgs a{k, v, q, k_stride, v_stride, q_stride, q_out, cos_sin, rope_rows, rd,
+                      interleaved, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
+                      kv_lens, B, T, H, Hkv, d, num_pages, page_size, max_pages, (int)dtype,
+                      0, 0, 0};
+    return finish(launch_paged_append(a, *dev, s), s);
+}
+
+size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d) {
+    if (max_q_len <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+    return 0;
+}
+
+sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,
+                                 const uint8_t *v_cache, const float *k_scale,
+                                 const float *v_scale, const int32_t *page_table,
+                                 const int32_t *cu_seqlens, const int32_t *kv_lens, int32_t B,
+                                 int32_t T, int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d,
+                                 int32_t num_pages, int32_t page_size, int32_t max_pages,
+                                 int32_t causal, int32_t window_left, const float *sinks,
+                                 sattn_sink_mode sink_mode, float scale, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, sattn_dtype dtype,
+                                 void *cuda_stream) {
+    if (B < 0 || T < 0 || max_q_len < 0 || H <= 0 ||
+        !valid_paged(Hkv, d, num_pages, page_size, max_pages) || H % Hkv != 0)
+        return SATTN_ERR_INVALID_ARG;
+    if (causal != 0 && causal != 1) return SATTN_ERR_INVALID_ARG;
+    if (!valid_dtype(dtype) || !valid_sink(sink_mode, sinks) || !finite_scale(scale))
+        return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;
+    if (!valid_rows(q_stride, H, d, unit)) return SATTN_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return SATTN_OK;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !page_table || !cu_seqlens ||
+        !kv_lens || !o)
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) ||
+        (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return SATTN_ERR_INVALID_ARG;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    PagedArgs a{q, q_stride, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
+                B, T, max_q_len, H, Hkv, d, num_pages, page_size, max_pages, causal,
+                window_left < 0 ? -1 : window_left, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
+                (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
+    return finish(launch_paged_simt(a, *dev, s), s);
 }
 
 sattn_status sattn_compress_kv(const void *kv, const void *score, const float *ape, void *out,

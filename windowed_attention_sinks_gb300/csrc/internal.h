@@ -120,6 +120,43 @@ struct XattnArgs {
     int chunk;         // stage 1: keys per (m, l) output, outputs [C, M, H]; 0: one output
 };
 
+// Append to the paged e4m3 cache (strides in elements, between tokens).
+struct PagedAppendArgs {
+    const void *k, *v, *q;  // q may be nullptr: nothing to rotate
+    int64_t k_stride, v_stride, q_stride;
+    void *q_out;
+    const float *cos_sin;  // [rope_rows, rd]: rd / 2 cosines, rd / 2 sines
+    int rope_rows, rd, interleaved;
+    uint8_t *k_cache, *v_cache;  // [num_pages, Hkv, page, d]
+    float *k_scale, *v_scale;    // [num_pages, Hkv]
+    const int32_t *page_table, *cu_seqlens, *kv_lens;
+    int B, T, H, Hkv, d, num_pages, page, max_pages;
+    int dtype;
+    // set by the launcher
+    int by_token;
+    long long units;
+    unsigned unit_blocks;
+};
+
+// Attention over the paged e4m3 cache.
+struct PagedArgs {
+    const void *q;
+    int64_t q_stride;
+    const uint8_t *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int32_t *page_table, *cu_seqlens, *kv_lens;
+    int B, T, max_q_len, H, Hkv, d, num_pages, page, max_pages;
+    int causal, window_left;
+    const float *sinks;
+    int sink_mode;
+    float scale;
+    void *o;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int dtype;
+};
+
 // SIMT kernels: any dtype, d in {64, 128}.
 cudaError_t launch_window_simt(const WindowArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_sparse_simt(const SparseArgs &a, const DevInfo &dev, cudaStream_t s);
@@ -129,6 +166,8 @@ cudaError_t launch_topk_idxs(int32_t *out, const int32_t *start_pos, int B, int 
 cudaError_t launch_kv_ring_write(void *cache, const void *src, const int32_t *start_pos, int B,
                                  int S, int N, int d, int win, int elem_bytes, const DevInfo &dev,
                                  cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendArgs &a, const DevInfo &dev, cudaStream_t s);
+cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_stats(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_block_sum(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);

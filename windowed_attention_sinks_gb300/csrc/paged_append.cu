@@ -1,0 +1,322 @@
+// Append to a paged e4m3 cache, the position rotation applied on the way.
+//
+// For every new token at position p of its sequence and every KV head: the key
+// is rotated by the table's angles of p, and key and value go to row p mod page
+// of the page that the page table names for p / page, as e4m3 codes of x / s.
+// s is the scale of that page and head, the least power of two with
+// amax <= 448 s over everything the page holds. A page's first row sets s; rows
+// that join a page later may raise it, and then the codes already there are
+// recoded by old / new. With powers of two that is exact (a shift of the
+// exponent) until a code falls below the normal range, and x / s is exact too,
+// so a value is rounded once: relative error at most 2^-4 of e4m3, as with an
+// amax / 448 scale, of which a power of two costs at most one bit of range.
+//
+// One unit of work is (page touched, key or value, KV head): its amax must be
+// known before the first code is written, so NT threads hold the rows in
+// registers (up to 4 items of 16 columns each), take the amax over the group and
+// then write; rows beyond that are read again (they are in L2 by then). Two
+// ways to number the pages that a call touches, from its sizes alone:
+//   few tokens a sequence:  unit = token, dropped unless it is the first of
+//                           the call in its page; NT = 32;
+//   prompts:                sequence b owns the units from
+//                           cu[b] / page + 2 b on (a run of n tokens touches
+//                           at most n / page + 2 pages).
+// The queries of the same tokens are rotated by further blocks of the launch.
+// An item is 16 columns: the two 8-column halves that rotate into one another,
+// or 16 neighbours, so all global accesses are 8 or 16 bytes wide.
+#include "internal.h"
+#include "paged.cuh"
+
+namespace sattn {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int HELD = 4;  // items a thread keeps in registers
+
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
+    const float4 y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&v)[8]) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// First columns of the two halves of item c of a row.
+struct Cols {
+    int a, b;
+    bool turn;
+};
+__device__ __forceinline__ Cols item_cols(int c, int rd, int interleaved) {
+    const bool turn = 16 * c < rd;
+    if (turn && !interleaved) return Cols{8 * c, 8 * c + rd / 2, true};
+    return Cols{16 * c, 16 * c + 8, turn};
+}
+
+// Pairs (a[i], b[i]), or neighbours within a and within b, turned by the angles
+// 8c .. 8c + 7 of the row's table entry.
+__device__ __forceinline__ void turn(float (&a)[8], float (&b)[8], const float (&cs)[8],
+                                     const float (&sn)[8], int interleaved) {
+    if (!interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float x = a[i], y = b[i];
+            a[i] = x * cs[i] - y * sn[i];
+            b[i] = y * cs[i] + x * sn[i];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float x = a[2 * i], y = a[2 * i + 1];
+            a[2 * i] = x * cs[i] - y * sn[i];
+            a[2 * i + 1] = y * cs[i] + x * sn[i];
+            x = b[2 * i], y = b[2 * i + 1];
+            b[2 * i] = x * cs[4 + i] - y * sn[4 + i];
+            b[2 * i + 1] = y * cs[4 + i] + x * sn[4 + i];
+        }
+    }
+}
+
+__device__ __forceinline__ float amax16(const float (&a)[8], const float (&b)[8]) {
+    float m = 0.f;  // max.f32 drops a NaN operand: a NaN does not set the scale
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max3(m, fabsf(a[i]), fabsf(b[i]));
+    return m;
+}
+
+__device__ __forceinline__ uint2 code8(const float (&v)[8], float inv) {
+    return make_uint2(e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv),
+                      e4m3x4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv));
+}
+
+// The sequence and its checks that an append needs beyond load_seq's.
+__device__ __forceinline__ bool append_seq(const PagedAppendArgs &p, int b, PagedSeq &s,
+                                           unsigned &err) {
+    if (!load_seq(p.cu_seqlens, p.kv_lens, b, p.T, (long long)p.max_pages * p.page, s) ||
+        s.len < s.n) {
+        err |= DEVERR_SEQLENS;
+        return false;
+    }
+    if (p.rd > 0 && s.len > p.rope_rows) {
+        err |= DEVERR_INDEX;
+        return false;
+    }
+    return true;
+}
+
+template <typename T, int NT>
+__device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long u, float *red,
+                                            unsigned &err) {
+    const int tid = threadIdx.x % NT;
+    const int h = (int)(u % p.Hkv);
+    const bool is_v = u / p.Hkv & 1;
+    const long long x = u / p.Hkv >> 1;
+    // the pages's sequence and its first new position in the page
+    int b;
+    PagedSeq s;
+    int pos;
+    if (p.by_token) {
+        b = warp_find(p.B, x, [&](int i) { return (long long)__ldg(p.cu_seqlens + i); });
+        if (!append_seq(p, b, s, err)) return;
+        const int i = (int)x - s.t0;
+        if (i < 0 || i >= s.n) return;  // behind the last sequence
+        pos = s.len - s.n + i;
+        if (i > 0 && pos % p.page != 0) return;  // not the first in its page
+    } else {
+        b = warp_find(p.B, x, [&](int i) {
+            return (long long)(__ldg(p.cu_seqlens + i) / p.page) + 2ll * i;
+        });
+        if (!append_seq(p, b, s, err)) return;
+        const long long j = x - (s.t0 / p.page + 2ll * b);
+        const int p0 = s.len - s.n;
+        const long long first = j == 0 ? p0 : ((long long)(p0 / p.page) + j) * p.page;
+        if (s.n == 0 || first >= s.len) return;
+        pos = (int)first;
+    }
+    const int row0 = pos % p.page;
+    const int rows = min(p.page - row0, s.len - pos);
+    const int pid = __ldg(p.page_table + (size_t)b * p.max_pages + pos / p.page);
+    const T *src = static_cast<const T *>(is_v ? p.v : p.k) +
+                   (size_t)(s.t0 + pos - (s.len - s.n)) * (is_v ? p.v_stride : p.k_stride) +
+                   (size_t)h * p.d;
+    const size_t stride = is_v ? p.v_stride : p.k_stride;
+    const int ic = p.d / 16, items = rows * ic, rd = is_v ? 0 : p.rd;
+
+    auto fetch = [&](int it, float (&a)[8], float (&bb)[8]) {
+        const int r = it / ic, c = it % ic;
+        const Cols k = item_cols(c, rd, p.interleaved);
+        load8(src + r * stride + k.a, a);
+        load8(src + r * stride + k.b, bb);
+        if (k.turn) {
+            float cs[8], sn[8];
+            const float *e = p.cos_sin + (size_t)(pos + r) * p.rd + 8 * c;
+            load8(e, cs);
+            load8(e + p.rd / 2, sn);
+            turn(a, bb, cs, sn, p.interleaved);
+        }
+    };
+
+    float a[HELD][8], c[HELD][8];
+    float amax = 0.f;
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+        if (tid + k * NT < items) {
+            fetch(tid + k * NT, a[k], c[k]);
+            amax = fmaxf(amax, amax16(a[k], c[k]));
+        }
+    for (int it = tid + HELD * NT; it < items; it += NT) {
+        float y[8], z[8];
+        fetch(it, y, z);
+        amax = fmaxf(amax, amax16(y, z));
+    }
+    if (pid < 0 || pid >= p.num_pages) {  // the same for the whole unit
+        err |= DEVERR_INDEX;
+        return;
+    }
+    float *scale = (is_v ? p.v_scale : p.k_scale) + (size_t)pid * p.Hkv + h;
+    const float old = row0 > 0 ? *scale : 0.f;
+    amax = warp_max(amax);
+    if (NT > 32) {
+        constexpr int W = NT / 32;
+        const int group = threadIdx.x / NT;
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(NT) : "memory");
+        amax = red[group * W];
+#pragma unroll
+        for (int w = 1; w < W; ++w) amax = fmaxf(amax, red[group * W + w]);
+    } else {
+        __syncwarp();  // every lane has read the old scale
+    }
+    float now = pow2_scale(amax);
+    if (row0 > 0) {
+        // the held scale as a power of two (it is one already unless the caller
+        // filled the page): the least one not below it
+        const uint32_t ob = __float_as_uint(old);
+        const float held = old > 0.f ? __uint_as_float(min((ob + 0x7fffffu) & 0x7f800000u,
+                                                           (uint32_t)(127 + 120) << 23))
+                                     : LEAST_SCALE;
+        now = fmaxf(now, held);
+    }
+    const float inv = __frcp_rn(now);  // exact: a power of two in [2^-64, 2^120]
+    uint8_t *dst = (is_v ? p.v_cache : p.k_cache) + ((size_t)pid * p.Hkv + h) * p.page * p.d;
+    auto put = [&](int it, const float (&y)[8], const float (&z)[8]) {
+        const int r = it / ic;
+        const Cols k = item_cols(it % ic, rd, p.interleaved);
+        uint8_t *at = dst + (size_t)(row0 + r) * p.d;
+        *reinterpret_cast<uint2 *>(at + k.a) = code8(y, inv);
+        *reinterpret_cast<uint2 *>(at + k.b) = code8(z, inv);
+    };
+#pragma unroll
+    for (int k = 0; k < HELD; ++k)
+        if (tid + k * NT < items) put(tid + k * NT, a[k], c[k]);
+    for (int it = tid + HELD * NT; it < items; it += NT) {
+        float y[8], z[8];
+        fetch(it, y, z);
+        put(it, y, z);
+    }
+    if (row0 > 0 && now != old) {  // the page's earlier rows move to the new scale
+        const float ratio = old * inv;
+        for (int i = tid; i < row0 * p.d / 8; i += NT) {
+            uint2 w = reinterpret_cast<uint2 *>(dst)[i];
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 f = e4m3x2_to_f32((e < 2 ? w.x : w.y) >> (16 * (e & 1)));
+                v[2 * e] = f.x, v[2 * e + 1] = f.y;
+            }
+            reinterpret_cast<uint2 *>(dst)[i] = code8(v, ratio);
+        }
+    }
+    if (tid == 0) *scale = now;
+}
+
+// Rotated queries: 128 threads a token, a thread keeps its columns' angles for
+// several heads.
+template <typename T>
+__device__ __forceinline__ void rotate_queries(const PagedAppendArgs &p, long long t,
+                                               unsigned &err) {
+    if (t >= p.T) return;
+    const int b = warp_find(p.B, t, [&](int i) { return (long long)__ldg(p.cu_seqlens + i); });
+    PagedSeq s;
+    if (!append_seq(p, b, s, err)) return;
+    const int i = (int)t - s.t0;
+    if (i < 0 || i >= s.n) return;
+    const int pos = s.len - s.n + i;
+    const int ic = p.d / 16, c = threadIdx.x % ic;
+    const Cols k = item_cols(c, p.rd, p.interleaved);
+    float cs[8], sn[8];
+    if (k.turn) {
+        const float *e = p.cos_sin + (size_t)pos * p.rd + 8 * c;
+        load8(e, cs);
+        load8(e + p.rd / 2, sn);
+    }
+    for (int h = threadIdx.x % 128 / ic; h < p.H; h += 128 / ic) {
+        float a[8], bb[8];
+        const T *src = static_cast<const T *>(p.q) + (size_t)t * p.q_stride + (size_t)h * p.d;
+        T *dst = static_cast<T *>(p.q_out) + ((size_t)t * p.H + h) * p.d;
+        load8(src + k.a, a);
+        load8(src + k.b, bb);
+        if (k.turn) turn(a, bb, cs, sn, p.interleaved);
+        store8(dst + k.a, a);
+        store8(dst + k.b, bb);
+    }
+}
+
+template <typename T, int NT>
+__global__ void __launch_bounds__(THREADS) append_kernel(const PagedAppendArgs p, const DevCtx ctx) {
+    __shared__ float red[THREADS / 32];
+    unsigned err = 0;
+    if (blockIdx.x < p.unit_blocks) {
+        const long long u = (long long)blockIdx.x * (THREADS / NT) + threadIdx.x / NT;
+        if (u < p.units) append_unit<T, NT>(p, u, red, err);
+    } else {
+        rotate_queries<T>(p, (long long)(blockIdx.x - p.unit_blocks) * 2 + threadIdx.x / 128, err);
+    }
+    if (err && (threadIdx.x & 31) == 0) record_error(ctx, err);
+}
+
+template <typename T, int NT>
+cudaError_t launch(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
+    const long long ub = (p.units + THREADS / NT - 1) / (THREADS / NT);
+    const long long qb = p.q ? ((long long)p.T + 1) / 2 : 0;
+    if (ub + qb > INT_MAX) return cudaErrorInvalidValue;
+    p.unit_blocks = (unsigned)ub;
+    append_kernel<T, NT><<<(unsigned)(ub + qb), THREADS, 0, s>>>(p, make_ctx(dev));
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t pick(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
+    const long long slots = p.T / p.page + 2ll * p.B;
+    p.by_token = p.T <= slots;
+    p.units = (p.by_token ? p.T : slots) * 2 * p.Hkv;
+    // whole pages: as many threads as hold one in registers
+    const int want = p.by_token ? 32 : p.page * p.d / (16 * HELD);
+    if (want <= 32) return launch<T, 32>(p, dev, s);
+    if (want <= 64) return launch<T, 64>(p, dev, s);
+    if (want <= 128) return launch<T, 128>(p, dev, s);
+    return launch<T, 256>(p, dev, s);
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendArgs &a, const DevInfo &dev, cudaStream_t s) {
+    return a.dtype == SATTN_BF16 ? pick<__nv_bfloat16>(a, dev, s) : pick<float>(a, dev, s);
+}
+
+}  // namespace sattn
