@@ -428,7 +428,8 @@ sattn_status sattn_compress_kv(const void *kv, const void *score, const float *a
  *   kv_lens int32 [B]: positions that sequence b has, the call's own tokens
  *     included: these are its last cu_seqlens[b + 1] - cu_seqlens[b] ones.
  * All are device pointers; page_size is 16, 32, 64 or 128, d 64 or 128,
- * max_pages * page_size and num_pages * Hkv * page_size below 2^31. A sequence
+ * max_pages * page_size at most 2^30, num_pages * Hkv * page_size and T * H
+ * below 2^31. A sequence
  * whose lengths contradict one another or exceed the page table, and an
  * entry of the table in use that is no page, are skipped and reported by
  * sattn_check_device; entries behind a sequence's last position are not read.

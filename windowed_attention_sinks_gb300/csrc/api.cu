@@ -167,8 +167,9 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool valid_paged(int Hkv, int d, int num_pages, int page, int max_pages) {
     return Hkv > 0 && (d == 64 || d == 128) && num_pages > 0 && max_pages > 0 &&
            (page == 16 || page == 32 || page == 64 || page == 128) &&
-           (int64_t)max_pages * page <= INT32_MAX && (int64_t)num_pages * Hkv * page <= INT32_MAX;
+           (int64_t)max_pages * page <= (1 << 30) && (int64_t)num_pages * Hkv * page <= INT32_MAX;
 }
+bool paged_few_rows(int max_q_len, int G) { return (int64_t)max_q_len * G <= 32; }
 // Rows of `heads` x d elements, `stride` apart, each on a 16-byte boundary.
 bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {
     return stride >= (int64_t)heads * d && stride % unit == 0;
@@ -548,7 +549,8 @@ sattn_status sattn_paged_fp8_append(
 
 size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d) {
     if (max_q_len <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-    return 0;
+    if (!paged_few_rows(max_q_len, H / Hkv)) return 0;
+    return paged_decode_workspace(max_q_len, H / Hkv, d);
 }
 
 sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,
@@ -562,7 +564,8 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
                                  void *workspace, size_t workspace_bytes, sattn_dtype dtype,
                                  void *cuda_stream) {
     if (B < 0 || T < 0 || max_q_len < 0 || H <= 0 ||
-        !valid_paged(Hkv, d, num_pages, page_size, max_pages) || H % Hkv != 0)
+        !valid_paged(Hkv, d, num_pages, page_size, max_pages) || H % Hkv != 0 ||
+        (int64_t)T * H > INT32_MAX)
         return SATTN_ERR_INVALID_ARG;
     if (causal != 0 && causal != 1) return SATTN_ERR_INVALID_ARG;
     if (!valid_dtype(dtype) || !valid_sink(sink_mode, sinks) || !finite_scale(scale))
@@ -585,6 +588,8 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
                 B, T, max_q_len, H, Hkv, d, num_pages, page_size, max_pages, causal,
                 window_left < 0 ? -1 : window_left, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
                 (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
+    if (dtype == SATTN_BF16 && paged_few_rows(max_q_len, H / Hkv))
+        return finish(launch_paged_decode(a, *dev, s), s);
     return finish(launch_paged_simt(a, *dev, s), s);
 }
 

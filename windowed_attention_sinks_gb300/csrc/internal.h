@@ -167,6 +167,9 @@ cudaError_t launch_kv_ring_write(void *cache, const void *src, const int32_t *st
                                  int S, int N, int d, int win, int elem_bytes, const DevInfo &dev,
                                  cudaStream_t s);
 cudaError_t launch_paged_append(const PagedAppendArgs &a, const DevInfo &dev, cudaStream_t s);
+// bf16 queries, a few tokens a sequence; and its workspace (G = H / Hkv).
+cudaError_t launch_paged_decode(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
+size_t paged_decode_workspace(int max_q_len, int G, int d);
 cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_stats(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);

@@ -1,0 +1,833 @@
+// Attention of a few tokens a sequence over the paged e4m3 cache (tcgen05).
+//
+// o_r = sum_j softmax_j(scale <q_r, k_j>) v_j over a unit's R query rows (the
+// heads of a KV group times the call's tokens), 128 keys a tile. With so few
+// rows a key is used once or twice per byte, so the bound is reading the codes
+// from HBM, and everything is arranged around one pass over them:
+//
+//  * The codes go into the tensor core as they are; nothing is widened in
+//    shared memory. Both products are taken with the keys (then the columns of V) as the
+//    128 rows of the MMA and the query rows as its N columns:
+//      S^T [128 keys, 2R]   = K [128, D]   Q^T,
+//      O^T [D, 2R]         += V^T [D, 128] P^T   (V read column-major).
+//  * An e4m3 operand has 4 significant bits, so Q and P are split: x = hi +
+//    lo / 16 with hi = e4m3(x) and lo = e4m3(16 (x - hi)), side by side as 2R
+//    columns, joined again in fp32. hi + lo / 16 has 8 significant bits, a
+//    bf16's, for |x| from 2^-6 to 448, and an absolute error of at most 2^-14
+//    below that. The unit's Q is scaled by a power of two so that its largest value is
+//    in [128, 256): bf16 queries go in exactly down to 2^-14 of the largest.
+//    P is 2^(4 + e - m) <= 2^8 with e the exponent below, so the floor
+//    is 2^-18 .. 2^-22 of the largest weight. The extra columns are free: the
+//    MMA is a small part of the time a tile takes to arrive.
+//  * A thread holds one key, so the page's scales are scalars to it: the key's multiplies S, the
+//    value's goes into the exponent, e = scale log2(e) s + log2(v_scale), and
+//    V's codes need no scaling. The row sum divides it out again.
+//  * The running maximum m (of e) is moved only where a tile exceeds it by more
+//    than 2^4, so a tile costs one block vote instead of a reduction over its
+//    128 keys; O is rescaled in TMEM when it moves.
+//
+// One persistent CTA per SM (kernels that allocate TMEM run one) over an equal
+// piece of the tiles (paged_plan.cuh):
+//   warp 0      TMA: K and V tiles, one copy a page, two rings of STAGES tiles
+//   warp 1      MMA issuer
+//   warp 2      the pages' scales, a ring of SRING tiles ahead
+//   warp 3      Q of the next unit, split and swizzled; the rows' addresses
+//   warps 4-11  softmax: two groups of four take the tiles in turn, each with
+//               its own m, l, P and O^T, so that one's exponentials run beside
+//               the other's loads and votes; they are joined at the unit's end.
+#include <limits.h>
+#include <math.h>
+#include <stdio.h>
+
+#include "paged_plan.cuh"
+
+namespace sattn {
+namespace {
+
+constexpr int NTHREADS = 384;
+constexpr int SRING = 16;
+constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
+constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
+constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
+
+struct DecodeParams {
+    PlanArgs plan;
+    const __nv_bfloat16 *q;
+    int64_t q_stride;
+    const float *k_scale, *v_scale;
+    const int32_t *page_table;
+    int H, num_pages, page, page_shift, max_pages;
+    int rows_total;  // first row behind the pool: a copy from there reads zeros
+    float scale_l2;
+    const float *sinks;
+    int sink_mode;
+    __nv_bfloat16 *o;
+    float *lse;
+    uint8_t *ws;
+};
+
+template <int D, int R> struct Cfg {
+    static constexpr int N = 2 * R;
+    static constexpr uint32_t TILE_BYTES = TILE * D;
+    // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with few rows
+    static constexpr int STAGES = (R <= 16 ? 6 : 5) * (128 / D);
+    static constexpr int SBUF = 4;  // S buffers
+    static constexpr uint32_t O_COL = SBUF * N;
+    static constexpr uint32_t USED = O_COL + 2 * N;
+    static constexpr uint32_t COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+};
+
+template <int D, int R> struct alignas(1024) Smem {
+    using C = Cfg<D, R>;
+    uint8_t k[C::STAGES][C::TILE_BYTES];
+    uint8_t v[C::STAGES][C::TILE_BYTES];
+    uint8_t q[2][C::N * D];
+    uint8_t p[2][C::N * TILE];
+    float4 sc[SRING][8];        // page's k scale, log2 v scale, 1 / v scale, v scale > 0
+    float wmax[2][4][R];        // column maxima of the warps
+    float mx[2][2][R];          // unit parity, group: running maxima
+    float lx[2][2][4][R];       // and the warps' row sums
+    long long orow[2][R];       // output row of each query row, -1 past the last
+    int rpos[2][R];             // its position
+    float rsink[2][R];          // its sink (log2 units)
+    float qf[2];                // scale log2(e) / the power of two in Q
+    PlanStart plan;
+    uint64_t k_full[C::STAGES], k_empty[C::STAGES], v_full[C::STAGES], v_empty[C::STAGES];
+    uint64_t sc_full[SRING], sc_empty[SRING];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t s_full[C::SBUF], s_empty[C::SBUF], p_full[2], pv_done[2], o_empty, drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// ---------------------------------------------------------------- PTX used here alone
+
+// kind::f8f6f4, e4m3 x e4m3 -> f32; a_mn: A is stored with its M index contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn) {
+    return (1u << 4) | (a_mn << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Shared-memory descriptor of rows of W bytes (64 or 128) under W-byte swizzle,
+// in atoms of 8 rows.
+template <int W> __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+    if (W == 128) return smem_desc_sw128(addr, 16u, 1024u);
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)1 << 16;
+    d |= (uint64_t)(512u >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)4 << 61;  // swizzle: 64 B
+    return d;
+}
+// Byte offset of 16-byte unit u of row r in such a tile.
+template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint32_t u) {
+    if (W == 128) return sw128_offset(r, u);
+    return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
+}
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
+                                            int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld8(uint32_t a, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_ld4(uint32_t a, uint32_t *r) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ float redux_max(float x) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Barrier of one softmax group (128 threads) that also ORs a predicate.
+__device__ __forceinline__ bool group_any(int id, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---------------------------------------------------------------- page look-ups
+
+// Page of a unit's tile-relative page slot: its id where a visible key lies in
+// it, else -1 (not read); -2 for an entry that is no page.
+template <int R>
+__device__ __forceinline__ int page_of(const DecodeParams &p, const Unit<R> &u, int j) {
+    const int first = j << p.page_shift;
+    if (first > u.hi || first + p.page <= u.lo) return -1;
+    const int pid = __ldg(p.page_table + (size_t)u.b * p.max_pages + j);
+    return pid >= 0 && pid < p.num_pages ? pid : -2;
+}
+
+// ---------------------------------------------------------------- roles
+
+template <int D, int R>
+__device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                           Smem<D, R> &sm, const DevCtx &ctx) {
+    using C = Cfg<D, R>;
+    const int lane = threadIdx.x & 31;
+    const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);  // tiles a chunk
+    const uint32_t page_bytes = (uint32_t)p.page * D;
+    int t = 0;
+    bool ok = true;
+    unsigned bad = 0;
+    if (lane == 0) {
+        prefetch_tmap(tk);
+        prefetch_tmap(tv);
+    }
+    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const Unit<R> &u = it.u;
+        for (int c = u.begin; c < u.end && ok; c += chunk) {
+            const int j = (u.t_first + c) * per_tile + lane;
+            int pid = c + lane / per_tile < u.end ? page_of(p, u, j) : -1;
+            bad |= pid == -2;
+            const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
+            const int nt = min(chunk, u.end - c);
+            for (int i = 0; i < nt; ++i, ++t) {
+                const int st = t % C::STAGES, use = t / C::STAGES;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t full = smem_u32(kv ? &sm.v_full[st] : &sm.k_full[st]);
+                    const uint32_t empty = smem_u32(kv ? &sm.v_empty[st] : &sm.k_empty[st]);
+                    const uint32_t dst = smem_u32(kv ? sm.v[st] : sm.k[st]);
+                    bool go = true;
+                    if (lane == 0) {
+                        if (use >= 1) go = mbar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
+                        if (go) mbar_arrive_expect_tx(full, C::TILE_BYTES);
+                    }
+                    ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    // lane i * per_tile + s holds the page of the tile's slot s
+                    const int s = lane - i * per_tile;
+                    if (s >= 0 && s < per_tile)
+                        tma_load_2d(dst + (uint32_t)s * page_bytes, kv ? tv : tk, full, 0, row);
+                }
+                if (!ok) break;
+            }
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
+    // copies in flight land before the CTA leaves (at once on the normal path)
+    if (lane == 0) {
+        int zero = 0;
+        for (int i = 1; i <= C::STAGES && i <= t; ++i) {
+            mbar_wait(smem_u32(&sm.k_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
+                      &zero);
+            mbar_wait(smem_u32(&sm.v_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
+                      &zero);
+        }
+    }
+}
+
+template <int D, int R>
+__device__ void load_scales(const DecodeParams &p, Smem<D, R> &sm, const DevCtx &ctx) {
+    const int lane = threadIdx.x & 31;
+    const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
+    int t = 0;
+    bool ok = true;
+    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const Unit<R> &u = it.u;
+        for (int c = u.begin; c < u.end && ok; c += chunk) {
+            const int j = (u.t_first + c) * per_tile + lane;
+            const int pid = c + lane / per_tile < u.end ? page_of(p, u, j) : -1;
+            // a page that is not read hides its keys: e = -inf
+            float4 s = make_float4(0.f, -INFINITY, 0.f, 0.f);
+            if (pid >= 0) {
+                const size_t at = (size_t)pid * p.plan.Hkv + u.h;
+                const float vs = __ldg(p.v_scale + at);
+                s.x = __ldg(p.k_scale + at);
+                // a zero scale: weights as with the least scale, values dropped
+                const float e = vs > 0.f ? vs : LEAST_SCALE;
+                s.y = log2f(e);
+                s.z = 1.f / e;
+                s.w = vs > 0.f ? 1.f : 0.f;
+            }
+            const int nt = min(chunk, u.end - c);
+            for (int i = 0; i < nt && ok; ++i, ++t) {
+                const int st = t % SRING, use = t / SRING;
+                if (use >= 1) ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx,
+                                             &sm.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int sl = lane - i * per_tile;
+                if (sl >= 0 && sl < per_tile) sm.sc[st][sl] = s;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[st]));
+            }
+        }
+    }
+}
+
+// Q of a unit: scaled by a power of two, split into hi and 16 lo, K-major rows
+// hi 0 .. R-1, lo R .. 2R-1. A lane holds 8 columns, CH lanes a row.
+template <int D, int R>
+__device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx &ctx) {
+    constexpr int CH = D / 8, PER = R * CH / 32;  // items a lane
+    const int lane = threadIdx.x & 31;
+    const int G = p.plan.G;
+    bool ok = true;
+    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const Unit<R> &u = it.u;
+        const int w = it.index & 1;
+        uint4 x[PER];
+        float amax = 0.f;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (r < u.nrows) {
+                const int row = u.row0 + r;
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q + (size_t)(u.s.t0 + row / G) * p.q_stride +
+                    (size_t)(u.h * G + row % G) * D + 8 * c));
+            }
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = fabsf(__uint_as_float(v[e] << 16));
+                const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
+                if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
+                if (b < INFINITY) amax = fmaxf(amax, b);
+            }
+        }
+        amax = warp_max(amax);
+        // 2^k with amax 2^k in [128, 256), k within fp32's normal range
+        int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
+        k = amax > 0.f ? max(-120, min(k, 120)) : 0;
+        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+        if (it.index >= 2)
+            ok = mbar_wait(smem_u32(&sm.q_empty[w]), ((it.index >> 1) - 1) & 1, ctx, &sm.abort);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = __uint_as_float(v[e] << 16) * up;
+                const float b = __uint_as_float(v[e] & 0xffff0000u) * up;
+                uint32_t h = e4m3x2(a, b);
+                if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
+                if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
+                const float2 back = e4m3x2_to_f32(h);
+                hi[e >> 1] |= h << (16 * (e & 1));
+                lo[e >> 1] |= e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f) << (16 * (e & 1));
+            }
+            // 8 bytes: half of the 16-byte unit c / 2
+            *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(r, c >> 1) + 8 * (c & 1)) =
+                make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(R + r, c >> 1) + 8 * (c & 1)) =
+                make_uint2(lo[0], lo[1]);
+        }
+        for (int r = lane; r < R; r += 32) {
+            const int row = u.row0 + r, head = u.h * G + row % G;
+            const bool in = r < u.nrows;
+            sm.orow[w][r] = in ? (long long)(u.s.t0 + row / G) * p.H + head : -1;
+            sm.rpos[w][r] = u.pos(row, G);
+            sm.rsink[w][r] = in && p.sinks ? __ldg(p.sinks + head) * LOG2E : 0.f;
+        }
+        if (lane == 0) sm.qf[w] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[w]));
+    }
+}
+
+template <int D, int R>
+__device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
+                           const DevCtx &ctx) {
+    using C = Cfg<D, R>;
+    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, C::N, 0);
+    constexpr uint32_t IDESC_O = idesc_e4m3_f32(D, C::N, 1);
+    volatile int *abort = &sm.abort;
+    if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dk = desc_rows<D>(smem_u32(sm.k[0])), dv = desc_rows<D>(smem_u32(sm.v[0]));
+    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0])), dp = desc_rows<128>(smem_u32(sm.p[0]));
+    int done = 0;  // P V issued
+    // per group: whether its next P V is the unit's first, and the unit
+    struct Pending {
+        int unit;
+        bool first;
+    } pend[2] = {};
+    auto issue_pv = [&]() -> bool {
+        const int t = done, g = t & 1, st = t % C::STAGES;
+        const Pending pe = g ? pend[1] : pend[0];
+        if (!mbar_wait(smem_u32(&sm.v_full[st]), (t / C::STAGES) & 1, ctx, abort)) return false;
+        if (pe.first && pe.unit >= 1 &&
+            !mbar_wait(smem_u32(&sm.o_empty), (pe.unit - 1) & 1, ctx, abort))
+            return false;
+        if (!mbar_wait(smem_u32(&sm.p_full[g]), (t >> 1) & 1, ctx, abort)) return false;
+        tc_fence_after();
+        const uint64_t a = dv + (uint64_t)(st * (C::TILE_BYTES >> 4));
+        const uint64_t b = dp + (uint64_t)(g * (C::N * TILE >> 4));
+        const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::N;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V, 32 bytes of P
+            mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * 2), IDESC_O,
+                   kk > 0 || !pe.first);
+        tc_commit(smem_u32(&sm.v_empty[st]));
+        tc_commit(smem_u32(&sm.pv_done[g]));
+        ++done;
+        return true;
+    };
+    int t = 0;
+    int first_of[2] = {0, 0};  // first tile of the last two units
+    bool ok = true;
+    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const int w = it.index & 1, n = it.u.end - it.u.begin;
+        // Q of this unit takes the place of the unit before the last, whose
+        // end waits for all of its P V
+        const int must = it.index >= 1 ? (w ? first_of[0] : first_of[1]) : 0;
+        while (ok && done < must) ok = issue_pv();
+        if (!ok || !mbar_wait(smem_u32(&sm.q_full[w]), (it.index >> 1) & 1, ctx, abort)) break;
+        if (w) first_of[1] = t;
+        else first_of[0] = t;
+        for (int j = 0; j < n && ok; ++j, ++t) {
+            const int st = t % C::STAGES, sb = t % C::SBUF;
+            ok = mbar_wait(smem_u32(&sm.k_full[st]), (t / C::STAGES) & 1, ctx, abort);
+            if (ok && t >= C::SBUF)
+                ok = mbar_wait(smem_u32(&sm.s_empty[sb]), (t / C::SBUF - 1) & 1, ctx, abort);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = dk + (uint64_t)(st * (C::TILE_BYTES >> 4));
+            const uint64_t b = dq + (uint64_t)(w * (C::N * D >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+                mma_f8(tmem + (uint32_t)sb * C::N, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2),
+                       IDESC_S, kk > 0);
+            tc_commit(smem_u32(&sm.k_empty[st]));
+            tc_commit(smem_u32(&sm.s_full[sb]));
+            if (j == n - 1) tc_commit(smem_u32(&sm.q_empty[w]));
+            if (t - done >= 2) ok = issue_pv();
+            if (t & 1) pend[1] = Pending{it.index, j < 2};
+            else pend[0] = Pending{it.index, j < 2};
+        }
+    }
+    while (ok && done < t) ok = issue_pv();
+    tc_commit(smem_u32(&sm.drain));  // every MMA is done before TMEM goes
+    int zero = 0;
+    mbar_wait(smem_u32(&sm.drain), 0, ctx, &zero);
+}
+
+template <int D, int R>
+__device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
+    using C = Cfg<D, R>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = (warp - 4) >> 2, quarter = warp & 3;
+    const int key = quarter * 32 + lane;  // key of the tile = TMEM lane
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_tmem = tmem + C::O_COL + lanes;
+    const uint32_t pbuf = smem_u32(sm.p[g]);
+    volatile int *abort = &sm.abort;
+    const int bar_g = 1 + g, bar_all = 3;
+    // Once a wait has given up (ok), the warp goes through its remaining tiles
+    // without waiting and without writing to global memory: every warp reaches every
+    // named barrier, so none is left waiting there.
+    bool ok = true;
+    auto wait = [&](uint64_t &bar, int phase) {
+        ok = ok && mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+        ok = __all_sync(0xffffffffu, ok);
+    };
+    int t0 = 0;  // first tile of the unit
+    for (UnitIter<R> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
+        const Unit<R> &u = it.u;
+        const int w = it.index & 1, n = u.end - u.begin;
+        wait(sm.q_full[w], it.index >> 1);
+        const float qf = sm.qf[w];
+        float m[R], l[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) m[r] = NOTHING, l[r] = 0.f;
+        const int j0 = (g ^ t0) & 1;  // the group's first tile of the unit
+        for (int j = j0; j < n; j += 2) {
+            const int t = t0 + j, sb = t % C::SBUF, ss = t % SRING;
+            const int kpos = (u.t_first + u.begin + j) * TILE + key;
+            const int base = kpos - key;
+            wait(sm.sc_full[ss], t / SRING);
+            const float4 sc = sm.sc[ss][key >> p.page_shift];
+            wait(sm.s_full[sb], t / C::SBUF);
+            tc_fence_after();
+            const float f = sc.x * qf;
+            float x[R];  // e of this key for every row
+            {
+                const float flo = f * 0.0625f;
+                constexpr int CH = R < 16 ? R : 16;
+#pragma unroll
+                for (int c = 0; c < R; c += CH) {
+                    uint32_t hi[CH], lo[CH];
+                    if constexpr (CH == 8) {
+                        tmem_ld8(tmem + (uint32_t)sb * C::N + lanes + c, hi);
+                        tmem_ld8(tmem + (uint32_t)sb * C::N + lanes + R + c, lo);
+                    } else {
+                        tmem_ld16(tmem + (uint32_t)sb * C::N + lanes + c, hi);
+                        tmem_ld16(tmem + (uint32_t)sb * C::N + lanes + R + c, lo);
+                    }
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < CH; ++e)
+                        x[c + e] = fmaf(__uint_as_float(lo[e]), flo,
+                                        fmaf(__uint_as_float(hi[e]), f, sc.y));
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.s_empty[sb]));
+                mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+            }
+            if (p.sink_mode == 1 && kpos == 0) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) x[r] += sm.rsink[w][r];
+            }
+            if (base < u.ilo || base + TILE - 1 > u.ihi) {  // some row does not see some key
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int pos = sm.rpos[w][r];
+                    const bool in = kpos <= (p.plan.causal ? pos : u.hi) &&
+                                    (p.plan.wl < 0 || kpos >= pos - p.plan.wl);
+                    if (!in) x[r] = -INFINITY;
+                }
+                // values that no row sees may hold anything, NaN codes too: the MMA
+                // multiplies them by 0, so they are cleared
+                if (base < u.lo || base + TILE - 1 > u.hi) {
+                    const int st = t % C::STAGES;
+                    wait(sm.v_full[st], t / C::STAGES);
+                    if (kpos < u.lo || kpos > u.hi) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c)
+                            *reinterpret_cast<uint4 *>(sm.v[st] + key * D + 16 * c) =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int r = 0; r < R; ++r) top = fmaxf(top, x[r] - m[r]);
+            const bool move = group_any(bar_g, top > LIMIT - BASE);
+            if (move) {
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float c = redux_max(x[r]);
+                    if (lane == 0) sm.wmax[g][quarter][r] = c;
+                }
+                named_sync(bar_g, 128);
+                float alpha[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float c = fmaxf(fmaxf(sm.wmax[g][0][r], sm.wmax[g][1][r]),
+                                          fmaxf(sm.wmax[g][2][r], sm.wmax[g][3][r]));
+                    const float mn = fmaxf(m[r], c);
+                    alpha[r] = ex2(m[r] - mn);
+                    l[r] *= alpha[r];
+                    m[r] = mn;
+                }
+                if (j > j0) {
+                    wait(sm.pv_done[g], (t >> 1) - 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < C::N; c += 8) {
+                        uint32_t v[8];
+                        tmem_ld8(o_tmem + (uint32_t)(g * C::N + c), v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha[(c + e) % R]);
+                        tmem_st8(o_tmem + (uint32_t)(g * C::N + c), v);
+                    }
+                    tc_wait_st();
+                }
+            }
+            // P overwrites the group's last one, which its P V has read by now
+            // (waited for here because nothing else does when m stays)
+            if (t >= 2) wait(sm.pv_done[g], (t >> 1) - 1);
+#pragma unroll
+            for (int r = 0; r < R; r += 2) {
+                const float a = ex2(x[r] + (BASE - m[r]));
+                const float b = ex2(x[r + 1] + (BASE - m[r + 1]));
+                l[r] = fmaf(a, sc.z, l[r]);
+                l[r + 1] = fmaf(b, sc.z, l[r + 1]);
+                const float a0 = a * sc.w, b0 = b * sc.w;
+                const uint32_t h = e4m3x2(a0, b0);
+                const float2 back = e4m3x2_to_f32(h);
+                const uint32_t lo = e4m3x2((a0 - back.x) * 16.f, (b0 - back.y) * 16.f);
+                const uint32_t unit = (uint32_t)key >> 4, in = key & 15u;
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(r, unit) + in), "r"(h)
+                             : "memory");
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(r + 1, unit) + in),
+                             "r"(h >> 8)
+                             : "memory");
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(R + r, unit) + in),
+                             "r"(lo)
+                             : "memory");
+                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(R + r + 1, unit) + in),
+                             "r"(lo >> 8)
+                             : "memory");
+            }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g]));
+        }
+        // ---- the unit's end: join the groups, write rows or a part
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const float s = warp_sum(l[r]);
+            if (lane == 0) sm.lx[w][g][quarter][r] = s;
+        }
+        if (quarter == 0 && lane == 0) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) sm.mx[w][g][r] = m[r];
+        }
+        // last tile of each group in the unit, and its P V
+        bool has[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int jl = n - 1 - ((n - 1 + t0 + s) & 1);
+            has[s] = jl >= 0;
+            if (has[s]) wait(sm.pv_done[s], (t0 + jl) >> 1);
+        }
+        named_sync(bar_all, 256);
+        tc_fence_after();
+        const bool part = u.begin > 0 || u.end < u.ntiles;
+        const bool writes = D == 128 || lane < 16;  // 64 rows of O^T: 16 lanes of every 32
+        const int col = D == 128 ? key : quarter * 16 + lane;
+        const size_t slot = (size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1);
+        float *plse = reinterpret_cast<float *>(p.ws + plan_lse_offset()) + slot * R;
+        float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D;
+#pragma unroll 1
+        for (int r0 = g * (R / 2); r0 < (g + 1) * (R / 2); r0 += 4) {
+            uint32_t v[4][4];  // group 0 hi, lo, group 1 hi, lo
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if (!has[s]) continue;
+                tmem_ld4(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
+                tmem_ld4(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
+            }
+            tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = r0 + e;
+                const float m0 = sm.mx[w][0][r], m1 = sm.mx[w][1][r];
+                const float mm = fmaxf(m0, m1);
+                float acc = 0.f, z = 0.f;
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+                    const float ms = s ? m1 : m0;
+                    if (!has[s]) continue;
+                    const float wt = ex2(ms - mm);
+                    acc += wt * fmaf(__uint_as_float(v[2 * s + 1][e]), 0.0625f,
+                                     __uint_as_float(v[2 * s][e]));
+                    z += wt * ((sm.lx[w][s][0][r] + sm.lx[w][s][1][r]) +
+                               (sm.lx[w][s][2][r] + sm.lx[w][s][3][r]));
+                }
+                float lse2 = z == 0.f ? -INFINITY : mm - BASE + log2f(z);
+                float inv = z == 0.f ? 0.f : 1.f / z;
+                if (!ok) continue;
+                if (part) {
+                    if (writes) prow[(size_t)r * D + col] = acc * inv;
+                    if (key == 0) plse[r] = lse2;
+                    continue;
+                }
+                const long long row = sm.orow[w][r];
+                if (row < 0) continue;
+                if (p.sink_mode == 2) {  // the null logit joins the denominator
+                    const float s2 = sm.rsink[w][r];
+                    const float top = fmaxf(lse2, s2);
+                    if (top != -INFINITY) {
+                        const float all = top + log2f(ex2(lse2 - top) + ex2(s2 - top));
+                        inv *= ex2(lse2 - all);
+                        lse2 = lse2 != lse2 ? lse2 : all;
+                    }
+                }
+                if (writes) p.o[row * D + col] = __float2bfloat16_rn(acc * inv);
+                if (key == 0 && p.lse) p.lse[row] = lse2 * LN2;
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.o_empty));
+            mbar_arrive(smem_u32(&sm.q_empty[w]));
+        }
+        t0 += n;
+    }
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(NTHREADS, 1)
+decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+              const DecodeParams p, const DevCtx ctx) {
+    using C = Cfg<D, R>;
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    Smem<D, R> &sm = *reinterpret_cast<Smem<D, R> *>(dsmem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the join may be scheduled once every CTA is here; it waits for their end
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
+        if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), 1);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_full[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+        }
+        for (int i = 0; i < SRING; ++i) {
+            mbar_init(smem_u32(&sm.sc_full[i]), 1);
+            mbar_init(smem_u32(&sm.sc_empty[i]), 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.q_full[i]), 1);
+            mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);  // the MMAs and the softmax warps
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.pv_done[i]), 1);
+        }
+        for (int i = 0; i < C::SBUF; ++i) {
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.s_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&sm.o_empty), 8);
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem_base), C::COLS);
+        tmem_relinquish();
+    }
+    plan_start<R>(p.plan, sm.plan, ctx);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (p.plan.split && warp == 3) {  // this piece's note for the join
+        UnitIter<R> it(p.plan, sm.plan);
+        if (lane == 0) {
+            PlanNote n{};
+            if (it.live) {
+                n.cont = it.u.begin > 0;
+                n.through = it.u.begin > 0 && it.u.end < it.u.ntiles;
+                n.t0 = it.u.s.t0;
+                n.h = it.u.h;
+                n.row0 = it.u.row0;
+                n.nrows = it.u.nrows;
+            }
+            reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
+        }
+    }
+    const uint32_t tmem = sm.tmem_base;
+    if (warp == 0) {
+        load_tiles<D, R>(p, &tk, &tv, sm, ctx);
+    } else if (warp == 1) {
+        if (lane == 0) issue_mmas<D, R>(p, sm, tmem, ctx);
+        __syncwarp();
+    } else if (warp == 2) {
+        load_scales<D, R>(p, sm, ctx);
+    } else if (warp == 3) {
+        load_queries<D, R>(p, sm, ctx);
+    } else {
+        softmax<D, R>(p, sm, tmem, ctx);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, C::COLS);
+    }
+}
+
+template <int D, int R>
+cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
+    const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * a.page;
+    const uint64_t dims[2] = {(uint64_t)D, rows}, strides[1] = {(uint64_t)D};
+    const uint32_t box[2] = {(uint32_t)D, (uint32_t)a.page};
+    const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap tk, tv;
+    if (encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(a.k_cache),
+                          dims, strides, box, sw) != CUDA_SUCCESS ||
+        encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(a.v_cache),
+                          dims, strides, box, sw) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(Smem<D, R>);
+    static_assert(sizeof(Smem<D, R>) <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = ensure_smem_attr((const void *)decode_kernel<D, R>, smem, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
+    const bool split = a.workspace && a.workspace_bytes >= plan_workspace(R, D);
+    int shift = 4;
+    while ((1 << shift) < a.page) ++shift;
+    DecodeParams p{plan_args(a, split, 1), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
+                   a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, shift,
+                   a.max_pages, (int)rows, a.scale * LOG2E, a.sinks, a.sink_mode,
+                   static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace)};
+    if (verbose())
+        fprintf(stderr, "sattn: paged decode_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, R, grid,
+                smem, (int)split);
+    decode_kernel<D, R><<<grid, NTHREADS, smem, s>>>(tk, tv, p, make_ctx(dev));
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !split) return e;
+    return launch_paged_join(a, R, grid, s);
+}
+
+}  // namespace
+
+// Rows a unit for that many tokens a sequence: enough for a whole KV group's
+// where 32 are, so that its keys are read once.
+static int decode_rows(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+
+size_t paged_decode_workspace(int max_q_len, int G, int d) {
+    return plan_workspace(decode_rows((long long)max_q_len * G), d);
+}
+
+cudaError_t launch_paged_decode(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
+    const int r = decode_rows((long long)a.max_q_len * (a.H / a.Hkv));
+    if (a.d == 64) {
+        if (r == 8) return launch<64, 8>(a, dev, s);
+        return r == 16 ? launch<64, 16>(a, dev, s) : launch<64, 32>(a, dev, s);
+    }
+    if (r == 8) return launch<128, 8>(a, dev, s);
+    return r == 16 ? launch<128, 16>(a, dev, s) : launch<128, 32>(a, dev, s);
+}
+
+}  // namespace sattn

@@ -1,0 +1,234 @@
+// How the tensor-core kernels of the paged cache share out their work.
+//
+// A unit is up to ROWS query rows of one sequence and KV head (rows run
+// token-major over the tokens and the heads of the group, so any group size
+// fills a unit) with the 128-key tiles that any of them can see. Units are
+// numbered sequence by sequence, KV head by KV head; their tiles in a row form
+// one line of `total` tiles, cut into equal pieces, one a CTA. A piece may
+// begin and end inside a unit: a ragged batch then keeps every SM busy for the
+// same time, whatever its lengths, and one long sequence spreads over all SMs.
+// A unit that lies in one piece is finished there; the pieces of a unit that
+// is cut write partial results (normalised rows and their log2 denominators)
+// to the workspace, and a second, small launch joins them in a fixed order.
+// Everything is computed from the lengths on the device, so a call needs no
+// host copy of them and can be captured and replayed with other lengths.
+#pragma once
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace sattn {
+
+constexpr int TILE = 128;  // keys per tile
+
+struct PlanArgs {
+    const int32_t *cu, *lens;
+    int B, T, G, Hkv, page, causal, wl;
+    long long capacity;  // positions that the page table holds
+    int split;           // 0: no workspace, pieces end at unit boundaries
+    int min_tiles;       // least tiles a CTA takes, while there are fewer than CTAs x that
+};
+
+__host__ inline PlanArgs plan_args(const PagedArgs &a, int split, int min_tiles) {
+    return PlanArgs{a.cu_seqlens, a.kv_lens, a.B, a.T, a.H / a.Hkv, a.Hkv, a.page, a.causal,
+                    a.window_left, (long long)a.max_pages * a.page, split, min_tiles};
+}
+
+// One unit's rows and keys.
+template <int ROWS> struct Unit {
+    PagedSeq s;
+    int b, h, rt, nrt;     // sequence, KV head, row tile of its nrt
+    int row0, nrows;       // rows of the sequence's n * G that the unit takes
+    int lo, hi;            // first and last key that any of its rows sees
+    int ilo, ihi;          // keys that all of them see
+    int t_first, ntiles;   // tiles of the sequence; ntiles >= 1 (an empty unit's is masked)
+    int begin, end;        // the tiles of this piece, 0 .. ntiles
+
+    __device__ __forceinline__ int pos(int row, int G) const { return s.len - s.n + row / G; }
+
+    __device__ __forceinline__ void set_rows(const PlanArgs &p, int rt_) {
+        rt = rt_;
+        row0 = rt * ROWS;
+        nrows = min(ROWS, s.n * p.G - row0);
+        const int p0 = pos(row0, p.G), p1 = pos(row0 + nrows - 1, p.G);
+        lo = p.wl < 0 ? 0 : max(0, p0 - p.wl);
+        ilo = p.wl < 0 ? 0 : max(0, p1 - p.wl);
+        hi = p.causal ? p1 : s.len - 1;
+        ihi = p.causal ? p0 : s.len - 1;
+        t_first = lo / TILE;
+        ntiles = hi < lo ? 1 : hi / TILE - t_first + 1;
+    }
+};
+
+// Tiles of one head of a sequence.
+template <int ROWS>
+__device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u) {
+    long long sum = 0;
+    u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
+    for (int rt = 0; rt < u.nrt; ++rt) {
+        u.set_rows(p, rt);
+        sum += u.ntiles;
+    }
+    return sum;
+}
+
+template <int ROWS>
+__device__ __forceinline__ bool plan_seq(const PlanArgs &p, int b, Unit<ROWS> &u) {
+    u.b = b;
+    return load_seq(p.cu, p.lens, b, p.T, p.capacity, u.s);
+}
+
+// What a CTA starts from (in shared memory).
+struct PlanStart {
+    long long x0, x1;  // its tiles of the line
+    int b, h, rt, begin;
+    int pieces;
+    long long wsum[32];
+};
+
+// Called by the whole CTA (blockDim.x a multiple of 32); ends with a barrier.
+template <int ROWS>
+__device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int per = (p.B + blockDim.x - 1) / blockDim.x;
+    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    Unit<ROWS> u;
+    long long mine = 0;
+    bool bad = false;
+    for (int b = b0; b < b1; ++b) {
+        if (plan_seq(p, b, u)) mine += seq_tiles(p, u) * p.Hkv;
+        else bad = true;
+    }
+    if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) ps.wsum[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        if (w < warp) before += ps.wsum[w];
+        total += ps.wsum[w];
+    }
+    const long long most = (total + p.min_tiles - 1) / p.min_tiles;
+    const long long pieces = min((long long)gridDim.x, max(1ll, most));
+    const long long c = blockIdx.x;
+    const long long x0 = c < pieces ? total * c / pieces : total;
+    const long long x1 = c < pieces ? total * (c + 1) / pieces : total;
+    if (tid == 0) {
+        ps.x0 = x0;
+        ps.x1 = x1;
+        ps.pieces = (int)pieces;
+    }
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {  // this thread's sequences hold x0
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            if (!plan_seq(p, b, u)) continue;
+            const long long ph = seq_tiles(p, u);
+            if (x0 >= at + ph * p.Hkv) {
+                at += ph * p.Hkv;
+                continue;
+            }
+            const int h = (int)((x0 - at) / ph);
+            at += h * ph;
+            for (int rt = 0;; ++rt) {
+                u.set_rows(p, rt);
+                if (x0 < at + u.ntiles) {
+                    ps.b = b;
+                    ps.h = h;
+                    ps.rt = rt;
+                    ps.begin = (int)(x0 - at);
+                    break;
+                }
+                at += u.ntiles;
+            }
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// Walks the units of a CTA's piece; every role of the CTA runs its own.
+template <int ROWS> struct UnitIter {
+    Unit<ROWS> u;
+    long long pos, x1;  // line position of u's first tile here
+    int index;          // units seen
+    bool live;
+
+    __device__ __forceinline__ UnitIter(const PlanArgs &p, const PlanStart &ps) {
+        pos = ps.x0;
+        x1 = ps.x1;
+        index = 0;
+        live = pos < x1;
+        if (!live) return;
+        plan_seq(p, ps.b, u);
+        u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
+        u.h = ps.h;
+        u.set_rows(p, ps.rt);
+        u.begin = ps.begin;
+        if (!p.split && u.begin > 0) {  // the piece before finishes this unit
+            pos += u.ntiles - u.begin;
+            live = pos < x1;
+            if (live) {
+                step(p);
+                u.begin = 0;
+            }
+        }
+        if (live) clip(p);
+    }
+    __device__ __forceinline__ void clip(const PlanArgs &p) {
+        u.end = p.split ? (int)min((long long)u.ntiles, u.begin + (x1 - pos)) : u.ntiles;
+    }
+    __device__ __forceinline__ void step(const PlanArgs &p) {
+        if (u.rt + 1 < u.nrt) {
+            u.set_rows(p, u.rt + 1);
+            return;
+        }
+        if (u.h + 1 < p.Hkv) {
+            ++u.h;
+            u.set_rows(p, 0);
+            return;
+        }
+        u.h = 0;
+        for (int b = u.b + 1; b < p.B; ++b)  // ends: x1 lies within the line
+            if (plan_seq(p, b, u) && u.s.n > 0) break;
+        u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
+        u.set_rows(p, 0);
+    }
+    __device__ __forceinline__ void next(const PlanArgs &p) {
+        pos += u.end - u.begin;
+        ++index;
+        live = pos < x1;
+        if (!live) return;
+        step(p);
+        u.begin = 0;
+        clip(p);
+    }
+};
+
+// A piece's note for the join: whether it begins inside a unit, whether that
+// unit also goes on behind the piece, and which unit it is.
+struct PlanNote {
+    int cont, through, t0, h, row0, nrows, pad0, pad1;
+};
+
+// Workspace: PlanNote [pieces], lse2 [pieces][2][ROWS], rows [pieces][2][ROWS][D].
+// Part 0 of a piece is its first unit if that began earlier, part 1 its last
+// unit if that begins here and goes on.
+constexpr int MAX_PIECES = 256;
+__host__ __device__ constexpr size_t plan_lse_offset() { return MAX_PIECES * sizeof(PlanNote); }
+__host__ __device__ constexpr size_t plan_rows_offset(int rows) {
+    return plan_lse_offset() + (size_t)MAX_PIECES * 2 * rows * 4;
+}
+__host__ __device__ constexpr size_t plan_workspace(int rows, int d) {
+    return plan_rows_offset(rows) + (size_t)MAX_PIECES * 2 * rows * d * 4;
+}
+
+// Joins the pieces of cut units; a programmatic dependent of the kernel that
+// wrote them. `rows` rows of d columns per unit, `pieces` CTAs in that launch.
+cudaError_t launch_paged_join(const PagedArgs &a, int rows, int pieces, cudaStream_t s);
+
+}  // namespace sattn
