@@ -549,8 +549,8 @@ sattn_status sattn_paged_fp8_append(
 
 size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d) {
     if (max_q_len <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
-    if (!paged_few_rows(max_q_len, H / Hkv)) return 0;
-    return paged_decode_workspace(max_q_len, H / Hkv, d);
+    return paged_few_rows(max_q_len, H / Hkv) ? paged_decode_workspace(max_q_len, H / Hkv, d)
+                                              : paged_prefill_workspace(d);
 }
 
 sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,
@@ -588,9 +588,10 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
                 B, T, max_q_len, H, Hkv, d, num_pages, page_size, max_pages, causal,
                 window_left < 0 ? -1 : window_left, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
                 (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
-    if (dtype == SATTN_BF16 && paged_few_rows(max_q_len, H / Hkv))
-        return finish(launch_paged_decode(a, *dev, s), s);
-    return finish(launch_paged_simt(a, *dev, s), s);
+    if (dtype == SATTN_F32) return finish(launch_paged_simt(a, *dev, s), s);
+    return finish(paged_few_rows(max_q_len, H / Hkv) ? launch_paged_decode(a, *dev, s)
+                                                     : launch_paged_prefill(a, *dev, s),
+                  s);
 }
 
 sattn_status sattn_compress_kv(const void *kv, const void *score, const float *ape, void *out,

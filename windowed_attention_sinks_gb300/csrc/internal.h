@@ -170,6 +170,10 @@ cudaError_t launch_paged_append(const PagedAppendArgs &a, const DevInfo &dev, cu
 // bf16 queries, a few tokens a sequence; and its workspace (G = H / Hkv).
 cudaError_t launch_paged_decode(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
 size_t paged_decode_workspace(int max_q_len, int G, int d);
+// bf16 queries, many tokens a sequence; and its workspace.
+cudaError_t launch_paged_prefill(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
+size_t paged_prefill_workspace(int d);
+// fp32 queries.
 cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_stats(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);

@@ -132,14 +132,6 @@ template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint3
     if (W == 128) return sw128_offset(r, u);
     return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
 }
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
-                                            int y) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
-        : "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -186,18 +178,6 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// ---------------------------------------------------------------- page look-ups
-
-// Page of a unit's tile-relative page slot: its id where a visible key lies in
-// it, else -1 (not read); -2 for an entry that is no page.
-template <int R>
-__device__ __forceinline__ int page_of(const DecodeParams &p, const Unit<R> &u, int j) {
-    const int first = j << p.page_shift;
-    if (first > u.hi || first + p.page <= u.lo) return -1;
-    const int pid = __ldg(p.page_table + (size_t)u.b * p.max_pages + j);
-    return pid >= 0 && pid < p.num_pages ? pid : -2;
-}
-
 // ---------------------------------------------------------------- roles
 
 template <int D, int R>
@@ -218,7 +198,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         const Unit<R> &u = it.u;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
-            int pid = c + lane / per_tile < u.end ? page_of(p, u, j) : -1;
+            int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
             bad |= pid == -2;
             const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
             const int nt = min(chunk, u.end - c);
@@ -268,19 +248,8 @@ __device__ void load_scales(const DecodeParams &p, Smem<D, R> &sm, const DevCtx 
         const Unit<R> &u = it.u;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
-            const int pid = c + lane / per_tile < u.end ? page_of(p, u, j) : -1;
-            // a page that is not read hides its keys: e = -inf
-            float4 s = make_float4(0.f, -INFINITY, 0.f, 0.f);
-            if (pid >= 0) {
-                const size_t at = (size_t)pid * p.plan.Hkv + u.h;
-                const float vs = __ldg(p.v_scale + at);
-                s.x = __ldg(p.k_scale + at);
-                // a zero scale: weights as with the least scale, values dropped
-                const float e = vs > 0.f ? vs : LEAST_SCALE;
-                s.y = log2f(e);
-                s.z = 1.f / e;
-                s.w = vs > 0.f ? 1.f : 0.f;
-            }
+            const int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
+            const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
             for (int i = 0; i < nt && ok; ++i, ++t) {
                 const int st = t % SRING, use = t / SRING;
@@ -741,21 +710,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (p.plan.split && warp == 3) {  // this piece's note for the join
-        UnitIter<R> it(p.plan, sm.plan);
-        if (lane == 0) {
-            PlanNote n{};
-            if (it.live) {
-                n.cont = it.u.begin > 0;
-                n.through = it.u.begin > 0 && it.u.end < it.u.ntiles;
-                n.t0 = it.u.s.t0;
-                n.h = it.u.h;
-                n.row0 = it.u.row0;
-                n.nrows = it.u.nrows;
-            }
-            reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
-        }
-    }
+    if (p.plan.split && warp == 3 && lane == 0) write_note<R>(p.plan, sm.plan, p.ws);
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0) {
         load_tiles<D, R>(p, &tk, &tv, sm, ctx);
@@ -779,15 +734,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
 
 template <int D, int R>
 cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
-    const uint64_t rows = (uint64_t)a.num_pages * a.Hkv * a.page;
-    const uint64_t dims[2] = {(uint64_t)D, rows}, strides[1] = {(uint64_t)D};
-    const uint32_t box[2] = {(uint32_t)D, (uint32_t)a.page};
     const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap tk, tv;
-    if (encode_tensor_map(&tk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(a.k_cache),
-                          dims, strides, box, sw) != CUDA_SUCCESS ||
-        encode_tensor_map(&tv, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(a.v_cache),
-                          dims, strides, box, sw) != CUDA_SUCCESS)
+    if (!map_cache(&tk, a.k_cache, a, sw) || !map_cache(&tv, a.v_cache, a, sw))
         return cudaErrorInvalidValue;
     const size_t smem = sizeof(Smem<D, R>);
     static_assert(sizeof(Smem<D, R>) <= 227 * 1024, "shared memory of one CTA");
@@ -795,11 +744,9 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(R, D);
-    int shift = 4;
-    while ((1 << shift) < a.page) ++shift;
     DecodeParams p{plan_args(a, split, 1), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
-                   a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, shift,
-                   a.max_pages, (int)rows, a.scale * LOG2E, a.sinks, a.sink_mode,
+                   a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
+                   a.max_pages, a.num_pages * a.Hkv * a.page, a.scale * LOG2E, a.sinks, a.sink_mode,
                    static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace)};
     if (verbose())
         fprintf(stderr, "sattn: paged decode_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, R, grid,

@@ -14,6 +14,8 @@
 // host copy of them and can be captured and replayed with other lengths.
 #pragma once
 
+#include <math.h>
+
 #include "internal.h"
 #include "paged.cuh"
 
@@ -60,46 +62,57 @@ template <int ROWS> struct Unit {
     }
 };
 
-// Tiles of one head of a sequence.
-template <int ROWS>
-__device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u) {
-    long long sum = 0;
-    u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
-    for (int rt = 0; rt < u.nrt; ++rt) {
-        u.set_rows(p, rt);
-        sum += u.ntiles;
-    }
-    return sum;
-}
-
 template <int ROWS>
 __device__ __forceinline__ bool plan_seq(const PlanArgs &p, int b, Unit<ROWS> &u) {
     u.b = b;
-    return load_seq(p.cu, p.lens, b, p.T, p.capacity, u.s);
+    if (!load_seq(p.cu, p.lens, b, p.T, p.capacity, u.s)) return false;
+    u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
+    return true;
+}
+
+// Tiles of one head of a sequence: by one thread, or by a warp (then every lane has the sum).
+template <int ROWS, bool WARP>
+__device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u) {
+    long long sum = 0;
+    for (int rt = WARP ? threadIdx.x & 31 : 0; rt < u.nrt; rt += WARP ? 32 : 1) {
+        u.set_rows(p, rt);
+        sum += u.ntiles;
+    }
+    if (WARP) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    return sum;
 }
 
 // What a CTA starts from (in shared memory).
 struct PlanStart {
     long long x0, x1;  // its tiles of the line
     int b, h, rt, begin;
-    int pieces;
     long long wsum[32];
+    long long before;  // tiles before the sequences b0 .. b1 - 1, in which x0 lies
+    int b0, b1;
 };
 
 // Called by the whole CTA (blockDim.x a multiple of 32); ends with a barrier.
+// Small batches are summed a warp a sequence, since one may have many units;
+// large ones a thread a run of sequences.
 template <int ROWS>
 __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
-    const int per = (p.B + blockDim.x - 1) / blockDim.x;
-    const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+    const bool by_warp = p.B <= 2 * nw;
+    const int workers = by_warp ? nw : (int)blockDim.x, me = by_warp ? warp : tid;
+    const int per = (p.B + workers - 1) / workers;
+    const int b0 = (int)min((long long)p.B, (long long)me * per), b1 = min(p.B, b0 + per);
     Unit<ROWS> u;
     long long mine = 0;
     bool bad = false;
     for (int b = b0; b < b1; ++b) {
-        if (plan_seq(p, b, u)) mine += seq_tiles(p, u) * p.Hkv;
-        else bad = true;
+        if (!plan_seq(p, b, u)) bad = true;
+        else mine += (by_warp ? seq_tiles<ROWS, true>(p, u) : seq_tiles<ROWS, false>(p, u)) * p.Hkv;
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+    if (by_warp && lane != 31) mine = 0;  // a warp's sum counts once
     long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -121,31 +134,44 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
     if (tid == 0) {
         ps.x0 = x0;
         ps.x1 = x1;
-        ps.pieces = (int)pieces;
     }
-    if (x0 < x1 && x0 >= before && x0 < before + mine) {  // this thread's sequences hold x0
-        long long at = before;
-        for (int b = b0; b < b1; ++b) {
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+        ps.before = before;
+        ps.b0 = b0;
+        ps.b1 = b1;
+    }
+    __syncthreads();
+    if (warp == 0 && x0 < x1) {  // the sequence, head and unit of x0
+        long long at = ps.before, ph = 0;
+        int b = ps.b0;
+        for (; b < ps.b1; ++b) {
             if (!plan_seq(p, b, u)) continue;
-            const long long ph = seq_tiles(p, u);
-            if (x0 >= at + ph * p.Hkv) {
-                at += ph * p.Hkv;
-                continue;
+            ph = seq_tiles<ROWS, true>(p, u);
+            if (x0 < at + ph * p.Hkv) break;
+            at += ph * p.Hkv;
+        }
+        const int h = (int)((x0 - at) / ph);
+        at += h * ph;
+        for (int r0 = 0; r0 < u.nrt; r0 += 32) {
+            int nt = 0;
+            if (r0 + lane < u.nrt) {
+                u.set_rows(p, r0 + lane);
+                nt = u.ntiles;
             }
-            const int h = (int)((x0 - at) / ph);
-            at += h * ph;
-            for (int rt = 0;; ++rt) {
-                u.set_rows(p, rt);
-                if (x0 < at + u.ntiles) {
-                    ps.b = b;
-                    ps.h = h;
-                    ps.rt = rt;
-                    ps.begin = (int)(x0 - at);
-                    break;
-                }
-                at += u.ntiles;
+            long long upto = nt;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
-            break;
+            if (nt > 0 && x0 >= at + upto - nt && x0 < at + upto) {
+                ps.b = b;
+                ps.h = h;
+                ps.rt = r0 + lane;
+                ps.begin = (int)(x0 - (at + upto - nt));
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
+            if (x0 < at) break;
         }
     }
     __syncthreads();
@@ -165,7 +191,6 @@ template <int ROWS> struct UnitIter {
         live = pos < x1;
         if (!live) return;
         plan_seq(p, ps.b, u);
-        u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
         u.h = ps.h;
         u.set_rows(p, ps.rt);
         u.begin = ps.begin;
@@ -195,7 +220,6 @@ template <int ROWS> struct UnitIter {
         u.h = 0;
         for (int b = u.b + 1; b < p.B; ++b)  // ends: x1 lies within the line
             if (plan_seq(p, b, u) && u.s.n > 0) break;
-        u.nrt = (int)(((long long)u.s.n * p.G + ROWS - 1) / ROWS);
         u.set_rows(p, 0);
     }
     __device__ __forceinline__ void next(const PlanArgs &p) {
@@ -208,6 +232,49 @@ template <int ROWS> struct UnitIter {
         clip(p);
     }
 };
+
+// Page of a sequence's page slot j: its id where a key that the unit sees lies
+// in it, -1 where none does (the table is not read), -2 for an entry that is no page.
+template <int ROWS>
+__device__ __forceinline__ int page_of(const int32_t *table, int max_pages, int num_pages,
+                                       int shift, const Unit<ROWS> &u, int j) {
+    const int first = j << shift;
+    if (first > u.hi || first + (1 << shift) <= u.lo) return -1;
+    const int pid = __ldg(table + (size_t)u.b * max_pages + j);
+    return pid >= 0 && pid < num_pages ? pid : -2;
+}
+
+// A page's scales as the softmax takes them: the key scale, the log2 of the
+// value scale (-inf hides the page's keys), 1 / the value scale, and whether
+// that is not 0: with a zero value scale the keys are weighed as with the least
+// scale and the values dropped.
+__device__ __forceinline__ float4 page_scales(const float *k_scale, const float *v_scale, int pid,
+                                              int Hkv, int h) {
+    if (pid < 0) return make_float4(1.f, -INFINITY, 0.f, 0.f);
+    const size_t at = (size_t)pid * Hkv + h;
+    const float vs = __ldg(v_scale + at), e = vs > 0.f ? vs : LEAST_SCALE;
+    return make_float4(__ldg(k_scale + at), log2f(e), 1.f / e, vs > 0.f ? 1.f : 0.f);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
+                                            int y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+        : "memory");
+}
+
+// Tensor map of a cache [pages, Hkv, page, d] as rows of d bytes, one page and head a box.
+inline bool map_cache(CUtensorMap *m, const uint8_t *cache, const PagedArgs &a,
+                      CUtensorMapSwizzle sw) {
+    const uint64_t dims[2] = {(uint64_t)a.d, (uint64_t)a.num_pages * a.Hkv * a.page};
+    const uint64_t strides[1] = {(uint64_t)a.d};
+    const uint32_t box[2] = {(uint32_t)a.d, (uint32_t)a.page};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(cache), dims,
+                             strides, box, sw) == CUDA_SUCCESS;
+}
+inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 // A piece's note for the join: whether it begins inside a unit, whether that
 // unit also goes on behind the piece, and which unit it is.
@@ -225,6 +292,21 @@ __host__ __device__ constexpr size_t plan_rows_offset(int rows) {
 }
 __host__ __device__ constexpr size_t plan_workspace(int rows, int d) {
     return plan_rows_offset(rows) + (size_t)MAX_PIECES * 2 * rows * d * 4;
+}
+
+template <int ROWS>
+__device__ __forceinline__ void write_note(const PlanArgs &p, const PlanStart &ps, uint8_t *ws) {
+    UnitIter<ROWS> it(p, ps);
+    PlanNote n{};
+    if (it.live) {
+        n.cont = it.u.begin > 0;
+        n.through = it.u.begin > 0 && it.u.end < it.u.ntiles;
+        n.t0 = it.u.s.t0;
+        n.h = it.u.h;
+        n.row0 = it.u.row0;
+        n.nrows = it.u.nrows;
+    }
+    reinterpret_cast<PlanNote *>(ws)[blockIdx.x] = n;
 }
 
 // Joins the pieces of cut units; a programmatic dependent of the kernel that

@@ -1,0 +1,643 @@
+// Attention of many tokens a sequence over the paged e4m3 cache (tcgen05).
+//
+// A unit is 256 query rows (tokens times the heads of a KV group) in two halves
+// of 128, the rows of the MMAs; both halves use each 128-key tile. Here the
+// products bound the time, so operands are what the tensor core takes at full
+// rate with no loss: the codes are widened to f16 in shared memory, which holds every
+// e4m3 value, once a tile for 256 rows; Q is scaled by a power of two a row
+// and taken in f16 (exact for bf16 queries down to 2^-22 of the row's largest), and P is rounded to f16
+// (2^-12 relative; 2^(7 + e - m) <= 2^15, so weights keep that down to 2^-21 of
+// the largest and add at most 2^-32 of it below). S, O and the row sums are fp32.
+//
+//   S = Q K^T [128 x 128] into TMEM, a half each
+//   x = S * (scale log2(e) * k_scale) + log2(v_scale): the value's scale goes
+//       into the exponent, so V's codes need none; the row sum divides it out.
+//       Both are one number for a page, that is for 16 columns or more
+//   P = 2^(7 + x - m), f16, over S's own columns
+//   O += P V, P from TMEM
+// m moves only when a tile raises it by more than 2^8 (O is then rescaled).
+// TMEM: S / P 2 x 128 columns, O 2 x D: all 512 for D = 128, hence the shared
+// columns of S and P. The MMAs of one CTA run in the order of issue, so S of
+// the next tile may follow the P V that reads its columns.
+//
+// One persistent CTA per SM over an equal piece of the tiles (paged_plan.cuh):
+//   warp 0       TMA: code tiles of K and V in turn into two staging buffers
+//   warp 1       MMA issuer: PV(A, t), S(A, t + 1), PV(B, t), S(B, t + 1), ..., so
+//                that one half's softmax runs beside the other half's MMAs
+//   warp 2       the pages' scales
+//   warps 4-7    widening: codes to f16 tiles (two buffers each of K and V); Q
+//   warps 8-11, 12-15   softmax and epilogue of the halves, a thread a row
+// The softmax warps keep a row's 128 scores in registers (200 a thread by
+// setmaxnreg, the other warps 56: 512 x 128 in all).
+#include <float.h>
+#include <limits.h>
+#include <math.h>
+#include <stdio.h>
+
+#include "paged_plan.cuh"
+
+namespace sattn {
+namespace {
+
+constexpr int ROWS = 256;
+constexpr int NTHREADS = 512;
+constexpr int SRING = 8;
+constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
+constexpr float TAU = 8.f;        // m moves when x exceeds it by more
+constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
+
+struct PrefillParams {
+    PlanArgs plan;
+    const __nv_bfloat16 *q;
+    int64_t q_stride;
+    const float *k_scale, *v_scale;
+    const int32_t *page_table;
+    int H, num_pages, page, page_shift, max_pages;
+    int rows_total;  // first row behind the pool: a copy from there reads zeros
+    float scale_l2;
+    const float *sinks;
+    int sink_mode;
+    __nv_bfloat16 *o;
+    float *lse;
+    uint8_t *ws;
+};
+
+template <int D> struct alignas(1024) Smem {
+    static constexpr uint32_t HALF = 128 * 128;  // 128 rows of 64 f16
+    static constexpr int NH = D / 64;            // such column halves a tile
+    uint8_t q[2][NH * HALF];
+    uint8_t k16[2][NH * HALF];
+    uint8_t v16[2][NH * HALF];
+    uint8_t stage[2][TILE * D];
+    float4 sc[SRING][8];
+    float qf[ROWS];
+    PlanStart plan;
+    uint64_t s8_full[2], s8_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t sc_full[SRING], sc_empty[SRING];
+    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+    uint32_t tmem_base;
+    int abort;
+};
+constexpr uint32_t TMEM_COLS = 512, HALF_COLS = 256, O_COL = 128;
+
+// kind::f16, f16 operands, fp32 accumulate; b_mn: B is stored with N contiguous.
+__host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn) {
+    return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+template <int D>
+__device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
+                           Smem<D> &sm, const DevCtx &ctx) {
+    const int lane = threadIdx.x & 31;
+    const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
+    const uint32_t page_bytes = (uint32_t)p.page * D;
+    int t = 0;  // copies: K and V of a tile
+    bool ok = true;
+    bool bad = false;
+    if (lane == 0) {
+        prefetch_tmap(tk);
+        prefetch_tmap(tv);
+    }
+    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const Unit<ROWS> &u = it.u;
+        for (int c = u.begin; c < u.end && ok; c += chunk) {
+            const int j = (u.t_first + c) * per_tile + lane;
+            const int pid = c + lane / per_tile < u.end
+                                ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j)
+                                : -1;
+            bad |= pid == -2;
+            const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
+            const int nt = min(chunk, u.end - c);
+            for (int i = 0; i < 2 * nt && ok; ++i, ++t) {
+                const int st = t & 1, use = t >> 1;
+                const uint32_t full = smem_u32(&sm.s8_full[st]);
+                bool go = true;
+                if (lane == 0) {
+                    if (use >= 1)
+                        go = mbar_wait(smem_u32(&sm.s8_empty[st]), (use - 1) & 1, ctx, &sm.abort);
+                    if (go) mbar_arrive_expect_tx(full, TILE * D);
+                }
+                ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+                if (!ok) break;
+                const int s = lane - (i >> 1) * per_tile;
+                if (s >= 0 && s < per_tile)
+                    tma_load_2d(smem_u32(sm.stage[st]) + (uint32_t)s * page_bytes, i & 1 ? tv : tk,
+                                full, 0, row);
+            }
+        }
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
+    if (lane == 0) {  // copies in flight land before the CTA leaves
+        int zero = 0;
+        for (int i = 1; i <= 2 && i <= t; ++i)
+            mbar_wait(smem_u32(&sm.s8_full[(t - i) & 1]), ((t - i) >> 1) & 1, ctx, &zero);
+    }
+}
+
+template <int D>
+__device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
+    const int lane = threadIdx.x & 31;
+    const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
+    int t = 0;
+    bool ok = true;
+    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const Unit<ROWS> &u = it.u;
+        for (int c = u.begin; c < u.end && ok; c += chunk) {
+            const int j = (u.t_first + c) * per_tile + lane;
+            const int pid = c + lane / per_tile < u.end
+                                ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j)
+                                : -1;
+            const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
+            const int nt = min(chunk, u.end - c);
+            for (int i = 0; i < nt; ++i, ++t) {
+                const int st = t % SRING, use = t / SRING;
+                if (use >= 1)
+                    ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx, &sm.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const int sl = lane - i * per_tile;
+                if (sl >= 0 && sl < per_tile) sm.sc[st][sl] = s;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[st]));
+            }
+        }
+    }
+}
+
+// Widens tiles and prepares Q; 128 threads. Returns early when a wait gives up
+// (no named barriers here, so every warp may leave by itself).
+template <int D>
+__device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
+    constexpr int UR = D / 16;             // 16-code units a row
+    constexpr int PER = TILE * UR / 128;   // units a thread, a tile
+    const int tid = threadIdx.x - 128, lane = tid & 31, G = p.plan.G;
+    volatile int *abort = &sm.abort;
+    int t = 0;  // tiles
+    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
+        const Unit<ROWS> &u = it.u;
+        // ---- Q: D / 8 lanes a row, 8 columns each
+        if (it.index >= 1 && !mbar_wait(smem_u32(&sm.q_empty), (it.index - 1) & 1, ctx, abort))
+            return;
+        constexpr int LR = D / 8;
+#pragma unroll 4
+        for (int r = tid / LR; r < ROWS; r += 128 / LR) {
+            const int c = tid % LR;
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (r < u.nrows) {
+                const int row = u.row0 + r;
+                x = __ldg(reinterpret_cast<const uint4 *>(
+                    p.q + (size_t)(u.s.t0 + row / G) * p.q_stride +
+                    (size_t)(u.h * G + row % G) * D + 8 * c));
+            }
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            float amax = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = fabsf(__uint_as_float(v[e] << 16));
+                const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
+                if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
+                if (b < INFINITY) amax = fmaxf(amax, b);
+            }
+#pragma unroll
+            for (int o = LR / 2; o > 0; o >>= 1)
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            // 2^k with amax 2^k in [128, 256)
+            int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
+            k = amax > 0.f ? max(-120, min(k, 120)) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16x2(__uint_as_float(v[e] << 16) * up,
+                                  __uint_as_float(v[e] & 0xffff0000u) * up);
+            *reinterpret_cast<uint4 *>(sm.q[r >> 7] + (c >> 3) * Smem<D>::HALF +
+                                       sw128_offset(r & 127, c & 7)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+            if (c == 0) sm.qf[r] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(smem_u32(&sm.q_full));
+        // ---- tiles: K then V
+        for (int j = u.begin; j < u.end; ++j, ++t) {
+            const int b = t & 1, use = t >> 1, ss = t % SRING;
+            const int kpos0 = (u.t_first + j) * TILE;
+            const bool edge = kpos0 < u.lo || kpos0 + TILE - 1 > u.hi;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                if (!mbar_wait(smem_u32(&sm.s8_full[kv]), t & 1, ctx, abort)) return;
+                if (use >= 1 && !mbar_wait(smem_u32(kv ? &sm.v_empty[b] : &sm.k_empty[b]),
+                                           (use - 1) & 1, ctx, abort))
+                    return;
+                uint8_t *dst = kv ? sm.v16[b] : sm.k16[b];
+                if (kv && !mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
+#pragma unroll 4
+                for (int i = 0; i < PER; ++i) {
+                    const int idx = i * 128 + tid, r = idx / UR, un = idx % UR;
+                    uint4 x = *reinterpret_cast<const uint4 *>(sm.stage[kv] + idx * 16);
+                    // values that no row sees may hold anything, NaN codes too, and
+                    // the MMA multiplies them by 0; a zero scale drops the values
+                    if (kv && ((edge && (kpos0 + r < u.lo || kpos0 + r > u.hi)) ||
+                               sm.sc[ss][r >> p.page_shift].w == 0.f))
+                        x = make_uint4(0, 0, 0, 0);
+                    const uint4 a = make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16),
+                                               e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
+                    const uint4 c = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16),
+                                               e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
+                    // the second column half's lanes store in the other order, so that
+                    // the two halves' units fall into different banks
+                    const bool sw = D == 128 && un >= 4;
+                    uint8_t *half = dst + (un >> 2) * Smem<D>::HALF;
+                    const uint32_t u0 = 2 * (un & 3) + (sw ? 1 : 0);
+                    *reinterpret_cast<uint4 *>(half + sw128_offset(r, u0)) = sw ? c : a;
+                    *reinterpret_cast<uint4 *>(half + sw128_offset(r, u0 ^ 1)) = sw ? a : c;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(kv ? &sm.v_full[b] : &sm.k_full[b]));
+                mbar_arrive(smem_u32(&sm.s8_empty[kv]));
+                if (kv) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+                }
+            }
+        }
+    }
+}
+
+template <int D>
+__device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, const DevCtx &ctx) {
+    constexpr uint32_t IDESC_S = idesc_f16_f32(128, TILE, 0), IDESC_O = idesc_f16_f32(128, D, 1);
+    constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
+    volatile int *abort = &sm.abort;
+    if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0]), 16u, 1024u);
+    const uint64_t dk = smem_desc_sw128(smem_u32(sm.k16[0]), 16u, 1024u);
+    const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
+    auto wait = [&](uint64_t &bar, int phase) {
+        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+    };
+    auto issue_s = [&](int half, int b) {
+        const uint64_t a = dq + (uint64_t)(half * (BYTES >> 4)), k = dk + (uint64_t)(b * (BYTES >> 4));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32u) >> 4;
+            tc_mma_f16(tmem + (uint32_t)half * HALF_COLS, a + off, k + off, IDESC_S, kk > 0);
+        }
+        tc_commit(smem_u32(&sm.s_full[half]));
+    };
+    auto issue_pv = [&](int half, int b, bool first) {
+        const uint64_t v = dv + (uint64_t)(b * (BYTES >> 4));
+        const uint32_t s = tmem + (uint32_t)half * HALF_COLS;
+#pragma unroll
+        for (int kk = 0; kk < TILE / 16; ++kk)
+            tc_mma_f16_ts(s + O_COL, s + 8u * kk, v + (uint64_t)(kk * (2048u >> 4)), IDESC_O,
+                          kk > 0 || !first);
+        tc_commit(smem_u32(&sm.pv_done[half]));
+    };
+    int t = 0, pc[2] = {0, 0}, ec[2] = {0, 0};  // tiles; per half: P tiles, units
+    bool ok = true;
+    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+        const int n = it.u.end - it.u.begin;
+        const bool two = it.u.nrows > 128;
+        ok = wait(sm.q_full, it.index) && wait(sm.k_full[t & 1], t >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        issue_s(0, t & 1);
+        if (two) issue_s(1, t & 1);
+        tc_commit(smem_u32(&sm.k_empty[t & 1]));
+        if (n == 1) tc_commit(smem_u32(&sm.q_empty));
+        for (int j = 0; j < n && ok; ++j, ++t) {
+            const int b = t & 1, b1 = b ^ 1;
+            ok = wait(sm.v_full[b], t >> 1);
+            for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
+                // the first P V overwrites the O that the last unit's epilogue reads
+                if (j == 0 && ec[half] >= 1) ok = wait(sm.o_empty[half], ec[half] - 1);
+                ok = ok && wait(sm.p_full[half], pc[half]);
+                if (!ok) break;
+                ++pc[half];
+                tc_fence_after();
+                issue_pv(half, b, j == 0);
+                if (j + 1 < n) {
+                    if (half == 0 && !(ok = wait(sm.k_full[b1], (t + 1) >> 1))) break;
+                    tc_fence_after();
+                    issue_s(half, b1);
+                }
+            }
+            if (!ok) break;
+            tc_commit(smem_u32(&sm.v_empty[b]));
+            if (j + 1 < n) {
+                tc_commit(smem_u32(&sm.k_empty[b1]));
+                if (j + 2 == n) tc_commit(smem_u32(&sm.q_empty));
+            }
+        }
+        ++ec[0];
+        if (two) ++ec[1];
+    }
+    tc_commit(smem_u32(&sm.drain));  // every MMA is done before TMEM goes
+    int zero = 0;
+    mbar_wait(smem_u32(&sm.drain), 0, ctx, &zero);
+}
+
+template <int D, int CW>  // CW: columns that share a page's scales (16 or 32)
+__device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
+                        const DevCtx &ctx) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = (warp - 8) >> 2, quarter = warp & 3;
+    const int r = half * 128 + quarter * 32 + lane;  // row of the unit
+    const uint32_t tmem =
+        tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
+    volatile int *abort = &sm.abort;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1, ctx, abort));
+    };
+    int t0 = 0, sc_n = 0, units = 0;  // CTA's tiles; this half's tiles and units
+    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
+        const Unit<ROWS> &u = it.u;
+        const int n = u.end - u.begin, G = p.plan.G;
+        if (!wait(sm.q_full, it.index)) return;
+        const float qf = sm.qf[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty));
+        if (half && u.nrows <= 128) {  // nothing in this half: keep the scales' ring going
+            for (int j = 0; j < n; ++j) {
+                const int ss = (t0 + j) % SRING;
+                if (!wait(sm.sc_full[ss], (t0 + j) / SRING)) return;
+                if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+            }
+            t0 += n;
+            continue;
+        }
+        const int row = u.row0 + r, pos = u.pos(row, G), head = u.h * G + row % G;
+        const bool in = r < u.nrows;
+        // the row's keys; a row past the unit's last sees what it likes (not written)
+        const int hi = p.plan.causal ? pos : u.s.len - 1;
+        const int lo = p.plan.wl < 0 ? 0 : pos - p.plan.wl;
+        const float sink = p.sinks && in ? __ldg(p.sinks + head) * LOG2E : 0.f;
+        float m = NOTHING, l = 0.f;
+        for (int j = 0; j < n; ++j, ++sc_n) {
+            const int t = t0 + j, ss = t % SRING;
+            const int kpos0 = (u.t_first + u.begin + j) * TILE;
+            if (!wait(sm.sc_full[ss], t / SRING) || !wait(sm.s_full[half], sc_n)) return;
+            tc_fence_after();
+            uint32_t x[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + 32u * c, x[c]);
+            tc_wait_ld();
+            const bool mask = kpos0 < u.ilo || kpos0 + TILE - 1 > u.ihi;
+            const bool key0 = p.sink_mode == 1 && kpos0 == 0;
+            if (mask) {
+                const int a = lo - kpos0, z = hi - kpos0;  // visible columns a .. z
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * c + e < a || 32 * c + e > z) x[c][e] = __float_as_uint(-INFINITY);
+            }
+            // x = S f + log2 v_scale, a page's columns at a time. f is kept above 0 (a
+            // zero key scale makes it 0), since a masked S is -inf. With a key-0 sink
+            // x of column 0 is set apart.
+            float top = -INFINITY;
+            float fs[TILE / CW], vs[TILE / CW];
+#pragma unroll
+            for (int c = 0; c < TILE / CW; ++c) {
+                const float4 s = sm.sc[ss][(c * CW) >> p.page_shift];
+                fs[c] = fmaxf(s.x * qf, FLT_MIN);
+                vs[c] = s.y;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < CW; e += 2) {
+                    const int q = c * CW + e;
+                    mx = max3(mx, __uint_as_float(x[q >> 5][q & 31]),
+                              __uint_as_float(x[q >> 5][(q & 31) + 1]));
+                }
+                top = fmaxf(top, fmaf(mx, fs[c], vs[c]));
+            }
+            float x0 = 0.f;
+            if (key0) {
+                x0 = fmaf(__uint_as_float(x[0][0]), fs[0], vs[0]) + sink;
+                top = fmaxf(top, x0);
+            }
+            const bool move = top > m + TAU;
+            float alpha = 1.f;
+            if (move) {
+                alpha = ex2(m - top);
+                l *= alpha;
+                m = top;
+            }
+            if (j > 0 && __any_sync(0xffffffffu, move)) {
+                if (!wait(sm.pv_done[half], sc_n - 1)) return;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(tmem + O_COL + 32u * c, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st32(tmem + O_COL + 32u * c, o);
+                }
+            }
+            uint32_t pw[2][32];
+#pragma unroll
+            for (int c = 0; c < TILE / CW; ++c) {
+                const float4 s = sm.sc[ss][(c * CW) >> p.page_shift];
+                const float f = fs[c], off = vs[c] + (BASE - m);
+                const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
+                uint64_t sum = f2_pack(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < CW; e += 2) {
+                    const int q = c * CW + e;
+                    float a, b;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[q >> 5][q & 31]),
+                                             __uint_as_float(x[q >> 5][(q & 31) + 1])),
+                                     f2, off2),
+                              a, b);
+                    a = ex2(a);
+                    b = ex2(b);
+                    if (q == 0 && key0) a = ex2(x0 + (BASE - m));
+                    sum = f2_add(sum, f2_pack(a, b));
+                    pw[q >> 6][(q & 63) >> 1] = pack_f16x2(a, b);
+                }
+                float a, b;
+                f2_unpack(sum, a, b);
+                l = fmaf(a + b, s.z, l);
+            }
+            tmem_st32(tmem, pw[0]);
+            tmem_st32(tmem + 32u, pw[1]);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.p_full[half]));
+                mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+            }
+        }
+        t0 += n;
+        // ---- epilogue
+        if (!wait(sm.pv_done[half], sc_n - 1)) return;
+        tc_fence_after();
+        const bool part = u.begin > 0 || u.end < u.ntiles;
+        float lse2 = l == 0.f ? -INFINITY : m - BASE + log2f(l);
+        float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
+        float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
+        const size_t orow = (size_t)(u.s.t0 + row / G) * p.H + head;
+        if (in) {
+            if (part) {
+                reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot] = lse2;
+            } else {
+                if (p.sink_mode == 2) {  // the null logit joins the denominator
+                    const float mt = fmaxf(lse2, sink);
+                    if (mt != -INFINITY) {
+                        const float all = mt + log2f(ex2(lse2 - mt) + ex2(sink - mt));
+                        inv *= ex2(lse2 - all);
+                        lse2 = lse2 != lse2 ? lse2 : all;
+                    }
+                }
+                if (p.lse) p.lse[orow] = lse2 * LN2;
+            }
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tmem + O_COL + 32u * c, o);
+            tc_wait_ld();
+            if (!in) continue;
+            if (part) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(prow + 32 * c + e) = make_float4(
+                        __uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
+                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        w[i] = pack_bf16x2(__uint_as_float(o[e + 2 * i]) * inv,
+                                           __uint_as_float(o[e + 2 * i + 1]) * inv);
+                    *reinterpret_cast<uint4 *>(p.o + orow * D + 32 * c + e) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty[half]));
+        ++units;
+    }
+}
+
+template <int D, int CW>
+__global__ void __launch_bounds__(NTHREADS, 1)
+prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+               const PrefillParams p, const DevCtx ctx) {
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dsmem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
+        if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sm.s8_full[i]), 1);
+            mbar_init(smem_u32(&sm.s8_empty[i]), 128);
+            mbar_init(smem_u32(&sm.k_full[i]), 128);
+            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_full[i]), 128);
+            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_empty[i]), 4);
+        }
+        for (int i = 0; i < SRING; ++i) {
+            mbar_init(smem_u32(&sm.sc_full[i]), 1);
+            mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
+        }
+        mbar_init(smem_u32(&sm.q_full), 128);
+        mbar_init(smem_u32(&sm.q_empty), 1 + 8);  // the MMAs and the softmax warps
+        mbar_init(smem_u32(&sm.drain), 1);
+        sm.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+        tmem_relinquish();
+    }
+    plan_start<ROWS>(p.plan, sm.plan, ctx);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    // registers: 256 threads x 56 + 256 x 200 = the 512 x 128 of the launch
+    if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp == 0) {
+            load_tiles<D>(p, &tk, &tv, sm, ctx);
+        } else if (warp == 1) {
+            if (lane == 0) issue_mmas<D>(p, sm, tmem, ctx);
+            __syncwarp();
+        } else if (warp == 2) {
+            load_scales<D>(p, sm, ctx);
+        } else if (warp == 3) {
+            if (p.plan.split && lane == 0) write_note<ROWS>(p.plan, sm.plan, p.ws);
+            __syncwarp();
+        } else {
+            widen<D>(p, sm, ctx);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        softmax<D, CW>(p, sm, tmem, ctx);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+template <int D, int CW>
+cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
+    CUtensorMap tk, tv;
+    if (!map_cache(&tk, a.k_cache, a, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !map_cache(&tv, a.v_cache, a, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(Smem<D>);
+    static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = ensure_smem_attr((const void *)prefill_kernel<D, CW>, smem, dev);
+    if (e != cudaSuccess) return e;
+    const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
+    const bool split = a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D);
+    PrefillParams p{plan_args(a, split, 1), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
+                    a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page,
+                    page_shift(a.page), a.max_pages, a.num_pages * a.Hkv * a.page,
+                    a.scale * LOG2E, a.sinks, a.sink_mode, static_cast<__nv_bfloat16 *>(a.o),
+                    a.lse, static_cast<uint8_t *>(a.workspace)};
+    if (verbose())
+        fprintf(stderr, "sattn: paged prefill_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, CW,
+                grid, smem, (int)split);
+    prefill_kernel<D, CW><<<grid, NTHREADS, smem, s>>>(tk, tv, p, make_ctx(dev));
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !split) return e;
+    return launch_paged_join(a, ROWS, grid, s);
+}
+
+}  // namespace
+
+size_t paged_prefill_workspace(int d) { return plan_workspace(ROWS, d); }
+
+cudaError_t launch_paged_prefill(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
+    if (a.d == 64) return a.page == 16 ? launch<64, 16>(a, dev, s) : launch<64, 32>(a, dev, s);
+    return a.page == 16 ? launch<128, 16>(a, dev, s) : launch<128, 32>(a, dev, s);
+}
+
+}  // namespace sattn

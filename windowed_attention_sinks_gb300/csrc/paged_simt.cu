@@ -27,7 +27,7 @@ template <int E> __device__ __forceinline__ void load_codes(const uint8_t *p, fl
     }
 }
 
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, DevCtx ctx) {
     constexpr int E = D / 32;
     const int lane = threadIdx.x & 31;
@@ -47,10 +47,10 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
     const float qs = a.scale * LOG2E;
     const float sink = a.sinks ? __ldg(a.sinks + h) * LOG2E : 0.f;
     float q[E], acc[E];
-    const T *qrow = static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)h * D + lane * E;
+    const float *qrow = static_cast<const float *>(a.q) + (size_t)t * a.q_stride + (size_t)h * D + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        q[e] = to_f32(qrow[e]) * qs;
+        q[e] = qrow[e] * qs;
         acc[e] = 0.f;
     }
     float m = a.sink_mode == 2 ? sink : -INFINITY, l = a.sink_mode == 2 ? 1.f : 0.f;
@@ -84,25 +84,20 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
     if (bad && lane == 0) record_error(ctx, DEVERR_INDEX);
     // l > 0 unless the row saw nothing; a NaN logit makes l NaN and goes out as NaN
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    T *orow = static_cast<T *>(a.o) + (size_t)row * D + lane * E;
+    float *orow = static_cast<float *>(a.o) + (size_t)row * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) orow[e] = from_f32<T>(acc[e] * inv);
+    for (int e = 0; e < E; ++e) orow[e] = acc[e] * inv;
     if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-}
-
-template <typename T> cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
-    const long long blocks = ((long long)a.T * a.H + kWarps - 1) / kWarps;
-    if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    const DevCtx ctx = make_ctx(dev);
-    if (a.d == 64) paged_simt_kernel<T, 64><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a, ctx);
-    else paged_simt_kernel<T, 128><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a, ctx);
-    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
-    return a.dtype == SATTN_BF16 ? launch<__nv_bfloat16>(a, dev, s) : launch<float>(a, dev, s);
+    const long long blocks = ((long long)a.T * a.H + kWarps - 1) / kWarps;
+    const DevCtx ctx = make_ctx(dev);
+    if (a.d == 64) paged_simt_kernel<64><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a, ctx);
+    else paged_simt_kernel<128><<<(unsigned)blocks, kWarps * 32, 0, s>>>(a, ctx);
+    return cudaGetLastError();
 }
 
 }  // namespace sattn
