@@ -449,9 +449,10 @@ sattn_status sattn_compress_kv(const void *kv, const void *score, const float *a
  * The rotation is computed in fp32 and rounded once: q_out to dtype, keys to
  * e4m3. The scale s of a page and head is the least power of two, at least
  * 2^-64, with amax <= 448 s over the rows that the page has taken: the page's
- * row 0 starts it, later rows may raise it, and the codes held by the page are
- * then recoded, e4m3(value * old / new), which is exact for values that stay
- * in e4m3's normal range. code = e4m3(x / s), nearest even, saturating at
+ * row 0 starts it, later rows may raise it, and the codes in the page's other
+ * rows (all of them, so that one scale holds for the whole page) are then
+ * recoded, e4m3(value * old / new), which is exact for values that stay in
+ * e4m3's normal range. code = e4m3(x / s), nearest even, saturating at
  * +-448; NaN stays NaN and does not count for amax; an infinity is stored as
  * the largest value. (A scale that the caller put into a page counts as the
  * next power of two.) The same call made twice leaves the same cache.

@@ -502,8 +502,8 @@ def paged_append(rows, codes, scale, page_table, cu_seqlens, kv_lens):
                     old = scale[pid, h]
                     s = max(s, float(2.0 ** np.ceil(np.log2(old))))
                     if s != old:
-                        held = e4m3_decode(codes[pid, h, :r0]) * (old / s)
-                        codes[pid, h, :r0] = e4m3_encode(held)
+                        held = e4m3_decode(codes[pid, h]) * (old / s)
+                        codes[pid, h] = e4m3_encode(held)
                 codes[pid, h, r0: r0 + len(x)] = e4m3_encode(x / s)
                 scale[pid, h] = s
     return codes, scale.astype(np.float32)

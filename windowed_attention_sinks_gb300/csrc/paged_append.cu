@@ -229,9 +229,11 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
         fetch(it, y, z);
         put(it, y, z);
     }
-    if (row0 > 0 && now != old) {  // the page's earlier rows move to the new scale
+    if (row0 > 0 && now != old) {  // the page's other rows move to the new scale
         const float ratio = old * inv;
-        for (int i = tid; i < row0 * p.d / 8; i += NT) {
+        const int from = row0 * p.d / 8, count = rows * p.d / 8;
+        for (int k = tid; k < p.page * p.d / 8 - count; k += NT) {
+            const int i = k < from ? k : k + count;
             uint2 w = reinterpret_cast<uint2 *>(dst)[i];
             float v[8];
 #pragma unroll

@@ -28,7 +28,7 @@
 //
 // One persistent CTA per SM (kernels that allocate TMEM run one) over an equal
 // piece of the tiles (paged_plan.cuh):
-//   warp 0      TMA: K and V tiles, one copy a page, two rings of STAGES tiles
+//   warp 0      the units; TMA: K and V tiles, one copy a page, two rings of STAGES tiles
 //   warp 1      MMA issuer
 //   warp 2      the pages' scales, a ring of SRING tiles ahead
 //   warp 3      Q of the next unit, split and swizzled; the rows' addresses
@@ -46,6 +46,7 @@ namespace {
 
 constexpr int NTHREADS = 384;
 constexpr int SRING = 16;
+constexpr int UNITS = 6;  // units handed on ahead
 constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
 constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
 constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
@@ -92,6 +93,7 @@ template <int D, int R> struct alignas(1024) Smem {
     float rsink[2][R];          // its sink (log2 units)
     float qf[2];                // scale log2(e) / the power of two in Q
     PlanStart plan;
+    UnitRing<R, UNITS> units;
     uint64_t k_full[C::STAGES], k_empty[C::STAGES], v_full[C::STAGES], v_empty[C::STAGES];
     uint64_t sc_full[SRING], sc_empty[SRING];
     uint64_t q_full[2], q_empty[2];
@@ -163,14 +165,14 @@ __device__ __forceinline__ float redux_max(float x) {
     asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
     return r;
 }
-// Barrier of one softmax group (128 threads) that also ORs a predicate.
-__device__ __forceinline__ bool group_any(int id, bool v) {
+// Barrier of `THREADS` threads that also ORs a predicate.
+template <int THREADS> __device__ __forceinline__ bool sync_any(int id, bool v) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)v), "r"(id)
+        : "r"((uint32_t)v), "r"(id), "n"(THREADS)
         : "memory");
     return r != 0;
 }
@@ -194,8 +196,12 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         prefetch_tmap(tk);
         prefetch_tmap(tv);
     }
-    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+    UnitIter<R> it(p.plan, sm.plan);
+    if (p.plan.split && lane == 0) write_note(it, p.ws);
+    for (; it.live && ok; it.next(p.plan)) {
         const Unit<R> &u = it.u;
+        if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
             int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
@@ -225,6 +231,10 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
             }
         }
     }
+    if (lane == 0 && ok) {
+        Unit<R> last{};
+        sm.units.put(it.index, last, ctx, &sm.abort);
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     // copies in flight land before the CTA leaves (at once on the normal path)
     if (lane == 0) {
@@ -244,25 +254,30 @@ __device__ void load_scales(const DecodeParams &p, Smem<D, R> &sm, const DevCtx 
     const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
     int t = 0;
     bool ok = true;
-    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
-        const Unit<R> &u = it.u;
+    for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, &sm.abort));
+        if (!ok) break;
+        const Unit<R> &u = sm.units.u[i % UNITS];
+        if (u.begin == u.end) break;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
             const int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
             const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
-            for (int i = 0; i < nt && ok; ++i, ++t) {
+            for (int a = 0; a < nt && ok; ++a, ++t) {
                 const int st = t % SRING, use = t / SRING;
                 if (use >= 1) ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx,
                                              &sm.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const int sl = lane - i * per_tile;
+                const int sl = lane - a * per_tile;
                 if (sl >= 0 && sl < per_tile) sm.sc[st][sl] = s;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[st]));
             }
         }
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
     }
 }
 
@@ -274,9 +289,13 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
     const int lane = threadIdx.x & 31;
     const int G = p.plan.G;
     bool ok = true;
-    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
-        const Unit<R> &u = it.u;
-        const int w = it.index & 1;
+    for (int n = 0;; ++n) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(n, ctx, &sm.abort))) break;
+        const Unit<R> u = sm.units.u[n % UNITS];
+        __syncwarp();
+        if (lane == 0) sm.units.release(n);
+        if (u.begin == u.end) break;
+        const int w = n & 1;
         uint4 x[PER];
         float amax = 0.f;
 #pragma unroll
@@ -303,8 +322,8 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
         k = amax > 0.f ? max(-120, min(k, 120)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        if (it.index >= 2)
-            ok = mbar_wait(smem_u32(&sm.q_empty[w]), ((it.index >> 1) - 1) & 1, ctx, &sm.abort);
+        if (n >= 2)
+            ok = mbar_wait(smem_u32(&sm.q_empty[w]), ((n >> 1) - 1) & 1, ctx, &sm.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll
@@ -383,13 +402,16 @@ __device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
     int t = 0;
     int first_of[2] = {0, 0};  // first tile of the last two units
     bool ok = true;
-    for (UnitIter<R> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
-        const int w = it.index & 1, n = it.u.end - it.u.begin;
+    for (int i = 0; ok; ++i) {
+        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        const int w = i & 1, n = sm.units.u[i % UNITS].end - sm.units.u[i % UNITS].begin;
+        sm.units.release(i);
+        if (n == 0) break;
         // Q of this unit takes the place of the unit before the last, whose
         // end waits for all of its P V
-        const int must = it.index >= 1 ? (w ? first_of[0] : first_of[1]) : 0;
+        const int must = i >= 1 ? (w ? first_of[0] : first_of[1]) : 0;
         while (ok && done < must) ok = issue_pv();
-        if (!ok || !mbar_wait(smem_u32(&sm.q_full[w]), (it.index >> 1) & 1, ctx, abort)) break;
+        if (!ok || !mbar_wait(smem_u32(&sm.q_full[w]), (i >> 1) & 1, ctx, abort)) break;
         if (w) first_of[1] = t;
         else first_of[0] = t;
         for (int j = 0; j < n && ok; ++j, ++t) {
@@ -409,8 +431,8 @@ __device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
             tc_commit(smem_u32(&sm.s_full[sb]));
             if (j == n - 1) tc_commit(smem_u32(&sm.q_empty[w]));
             if (t - done >= 2) ok = issue_pv();
-            if (t & 1) pend[1] = Pending{it.index, j < 2};
-            else pend[0] = Pending{it.index, j < 2};
+            if (t & 1) pend[1] = Pending{i, j < 2};
+            else pend[0] = Pending{i, j < 2};
         }
     }
     while (ok && done < t) ok = issue_pv();
@@ -430,7 +452,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
     const uint32_t pbuf = smem_u32(sm.p[g]);
     volatile int *abort = &sm.abort;
     const int bar_g = 1 + g, bar_all = 3;
-    // Once a wait has given up (ok), the warp goes through its remaining tiles
+    // Once a wait has given up (ok), the warp goes through the rest of its unit
     // without waiting and without writing to global memory: every warp reaches every
     // named barrier, so none is left waiting there.
     bool ok = true;
@@ -439,10 +461,14 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         ok = __all_sync(0xffffffffu, ok);
     };
     int t0 = 0;  // first tile of the unit
-    for (UnitIter<R> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
-        const Unit<R> &u = it.u;
-        const int w = it.index & 1, n = u.end - u.begin;
-        wait(sm.q_full[w], it.index >> 1);
+    for (int i = 0;; ++i) {
+        // all eight warps go on, or none
+        ok = ok && sm.units.wait(i, ctx, abort);
+        if (sync_any<256>(bar_all, !ok)) break;
+        const Unit<R> &u = sm.units.u[i % UNITS];
+        const int w = i & 1, n = u.end - u.begin;
+        if (n == 0) break;
+        wait(sm.q_full[w], i >> 1);
         const float qf = sm.qf[w];
         float m[R], l[R];
 #pragma unroll
@@ -512,7 +538,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             float top = -INFINITY;
 #pragma unroll
             for (int r = 0; r < R; ++r) top = fmaxf(top, x[r] - m[r]);
-            const bool move = group_any(bar_g, top > LIMIT - BASE);
+            const bool move = sync_any<128>(bar_g, top > LIMIT - BASE);
             if (move) {
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
@@ -657,6 +683,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         if (lane == 0) {
             mbar_arrive(smem_u32(&sm.o_empty));
             mbar_arrive(smem_u32(&sm.q_empty[w]));
+            sm.units.release(i);
         }
         t0 += n;
     }
@@ -699,6 +726,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         }
         mbar_init(smem_u32(&sm.o_empty), 8);
         mbar_init(smem_u32(&sm.drain), 1);
+        sm.units.init(1 + 1 + 1 + 8);  // MMA issuer, scales, queries, softmax
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -710,7 +738,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (p.plan.split && warp == 3 && lane == 0) write_note<R>(p.plan, sm.plan, p.ws);
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0) {
         load_tiles<D, R>(p, &tk, &tv, sm, ctx);

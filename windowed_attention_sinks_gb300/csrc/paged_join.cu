@@ -2,11 +2,10 @@
 // cache kernels' workspace): lse = log sum_c 2^lse2_c (+ the null-logit sink,
 // once), o = sum_c 2^(lse2_c - lse) o_c, in the order of the pieces.
 //
-// One block a piece boundary; the block whose boundary is the first inside a
-// unit joins it, the others leave. A warp takes a row: lane c holds piece c's
-// denominator, the columns are spread over the lanes. The work is a few
-// hundred KB, so it is latency that counts: the block's notes are one load,
-// the parts' denominators a second and their rows a third.
+// A warp takes a row of the unit that a piece boundary cuts, if that boundary is the
+// first inside the unit (the others leave). Lane i holds piece i's denominator,
+// the columns are spread over the lanes. The work is a few MB at most, so it is
+// latency that counts: notes, denominators and rows are three rounds of loads.
 #include <math.h>
 
 #include "paged_plan.cuh"
@@ -21,62 +20,67 @@ __global__ void __launch_bounds__(THREADS)
 join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *sinks,
             int null_sink, __nv_bfloat16 *o, float *lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    __shared__ PlanNote notes[MAX_PIECES];
-    const PlanNote *src = reinterpret_cast<const PlanNote *>(ws);
+    const PlanNote *notes = reinterpret_cast<const PlanNote *>(ws);
+    const int lane = threadIdx.x & 31;
     const int c = blockIdx.x + 1;  // boundary between pieces c - 1 and c
-    for (int i = threadIdx.x; i < pieces; i += THREADS) notes[i] = src[i];
-    __syncthreads();
-    const PlanNote &me = notes[c];
-    if (!me.cont || (notes[c - 1].cont && notes[c - 1].through)) return;
+    const int r = blockIdx.y * (THREADS / 32) + (threadIdx.x >> 5);
+    // lane i: piece c + i of the unit is cut off in front; and goes on behind
+    const PlanNote me = notes[c];
+    if (!me.cont || r >= me.nrows) return;
+    const PlanNote prev = notes[c - 1];
+    if (prev.cont && prev.through) return;
     int parts = 2;  // the last of c - 1, the first of c, and on while they go through
-    for (int i = c; i + 1 < pieces && notes[i].through && notes[i + 1].cont; ++i) ++parts;
+    for (int i0 = c; me.through; i0 += 32) {
+        const bool on = i0 + lane < pieces && notes[i0 + lane].cont && notes[i0 + lane].through;
+        const unsigned run = __ballot_sync(0xffffffffu, on);
+        const int len = run == 0xffffffffu ? 32 : __ffs(~run) - 1;
+        parts += len;
+        if (len < 32) break;
+    }
     const float *plse = reinterpret_cast<const float *>(ws + plan_lse_offset());
     const float *prow = reinterpret_cast<const float *>(ws + plan_rows_offset(rows));
-    const int lane = threadIdx.x & 31;
     constexpr int E = D / 32;
     // piece i of the unit: part 1 of CTA c - 1, then part 0 of c, c + 1, ...
     auto slot = [&](int i) { return (size_t)(c - 1 + i) * 2 + (i == 0 ? 1 : 0); };
-    for (int r = threadIdx.x >> 5; r < me.nrows; r += THREADS / 32) {
-        const int row = me.row0 + r;
-        const int head = me.h * G + row % G;
-        const size_t out = (size_t)(me.t0 + row / G) * H + head;
-        const float sink = null_sink ? __ldg(sinks + head) * LOG2E : -INFINITY;
-        float m = sink;
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, plse[slot(i) * rows + r]);
-        m = warp_max(m);
-        float acc[E];
+    const int row = me.row0 + r;
+    const int head = me.h * G + row % G;
+    const size_t out = (size_t)(me.t0 + row / G) * H + head;
+    const float sink = null_sink ? __ldg(sinks + head) * LOG2E : -INFINITY;
+    float m = sink;
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, plse[slot(i) * rows + r]);
+    m = warp_max(m);
+    float acc[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.f;
-        float z = null_sink && m != -INFINITY ? ex2(sink - m) : 0.f;
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            // NaN denominators (a NaN key) stay: only -inf counts as nothing
-            const float l = i0 + lane < parts ? plse[slot(i0 + lane) * rows + r] : -INFINITY;
-            const float w = l == -INFINITY ? 0.f : ex2(l - m);
-            z += warp_sum(w);
-            const int cnt = min(32, parts - i0);
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    float z = null_sink && m != -INFINITY ? ex2(sink - m) : 0.f;
+    for (int i0 = 0; i0 < parts; i0 += 32) {
+        // NaN denominators (a NaN key) stay: only -inf counts as nothing
+        const float l = i0 + lane < parts ? plse[slot(i0 + lane) * rows + r] : -INFINITY;
+        const float w = l == -INFINITY ? 0.f : ex2(l - m);
+        z += warp_sum(w);
+        const int cnt = min(32, parts - i0);
 #pragma unroll 4
-            for (int i = 0; i < cnt; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                const float *p = prow + (slot(i0 + i) * rows + r) * D + lane * E;
-                if (E == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(p);
-                    acc[0] += wi * v.x, acc[1] += wi * v.y;
-                    acc[E - 2] += wi * v.z, acc[E - 1] += wi * v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(p);
-                    acc[0] += wi * v.x, acc[1] += wi * v.y;
-                }
+        for (int i = 0; i < cnt; ++i) {
+            const float wi = __shfl_sync(0xffffffffu, w, i);
+            const float *p = prow + (slot(i0 + i) * rows + r) * D + lane * E;
+            if (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(p);
+                acc[0] += wi * v.x, acc[1] += wi * v.y;
+                acc[E - 2] += wi * v.z, acc[E - 1] += wi * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(p);
+                acc[0] += wi * v.x, acc[1] += wi * v.y;
             }
         }
-        const float inv = z == 0.f ? 0.f : 1.f / z;
-        uint32_t w2[E / 2];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) w2[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-        __nv_bfloat16 *dst = o + out * D + lane * E;
-        if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w2[0], w2[E / 2 - 1]);
-        else *reinterpret_cast<uint32_t *>(dst) = w2[0];
-        if (lse && lane == 0) lse[out] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
     }
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    uint32_t w2[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w2[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    __nv_bfloat16 *dst = o + out * D + lane * E;
+    if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w2[0], w2[E / 2 - 1]);
+    else *reinterpret_cast<uint32_t *>(dst) = w2[0];
+    if (lse && lane == 0) lse[out] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
 }
 
 }  // namespace
@@ -84,7 +88,7 @@ join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *
 cudaError_t launch_paged_join(const PagedArgs &a, int rows, int pieces, cudaStream_t s) {
     if (pieces < 2) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(pieces - 1));
+    cfg.gridDim = dim3((unsigned)(pieces - 1), (unsigned)(rows / (THREADS / 32)));
     cfg.blockDim = dim3(THREADS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

@@ -177,7 +177,7 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
     __syncthreads();
 }
 
-// Walks the units of a CTA's piece; every role of the CTA runs its own.
+// Walks the units of a CTA's piece.
 template <int ROWS> struct UnitIter {
     Unit<ROWS> u;
     long long pos, x1;  // line position of u's first tile here
@@ -276,6 +276,34 @@ inline bool map_cache(CUtensorMap *m, const uint8_t *cache, const PagedArgs &a,
 }
 inline int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
+// The units in shared memory: the loading warp walks them and hands them on, the
+// other roles read what they need (their registers are for other things). A unit
+// without tiles ends the piece.
+template <int ROWS, int N> struct UnitRing {
+    Unit<ROWS> u[N];
+    uint64_t full[N], empty[N];
+
+    __device__ __forceinline__ void init(int readers) {
+        for (int i = 0; i < N; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), readers);
+        }
+    }
+    // One thread: unit number i (the last one has end == begin).
+    __device__ __forceinline__ bool put(int i, const Unit<ROWS> &x, const DevCtx &ctx,
+                                        volatile int *abort) {
+        if (i >= N && !mbar_wait(smem_u32(&empty[i % N]), (i / N - 1) & 1, ctx, abort))
+            return false;
+        u[i % N] = x;
+        mbar_arrive(smem_u32(&full[i % N]));
+        return true;
+    }
+    __device__ __forceinline__ bool wait(int i, const DevCtx &ctx, volatile int *abort) {
+        return mbar_wait(smem_u32(&full[i % N]), (i / N) & 1, ctx, abort);
+    }
+    __device__ __forceinline__ void release(int i) { mbar_arrive(smem_u32(&empty[i % N])); }
+};
+
 // A piece's note for the join: whether it begins inside a unit, whether that
 // unit also goes on behind the piece, and which unit it is.
 struct PlanNote {
@@ -295,8 +323,7 @@ __host__ __device__ constexpr size_t plan_workspace(int rows, int d) {
 }
 
 template <int ROWS>
-__device__ __forceinline__ void write_note(const PlanArgs &p, const PlanStart &ps, uint8_t *ws) {
-    UnitIter<ROWS> it(p, ps);
+__device__ __forceinline__ void write_note(const UnitIter<ROWS> &it, uint8_t *ws) {
     PlanNote n{};
     if (it.live) {
         n.cont = it.u.begin > 0;

@@ -21,12 +21,12 @@
 // the next tile may follow the P V that reads its columns.
 //
 // One persistent CTA per SM over an equal piece of the tiles (paged_plan.cuh):
-//   warp 0       TMA: code tiles of K and V in turn into two staging buffers
+//   warp 0       the units; TMA: code tiles of K and V in turn into two staging buffers
 //   warp 1       MMA issuer: PV(A, t), S(A, t + 1), PV(B, t), S(B, t + 1), ..., so
 //                that one half's softmax runs beside the other half's MMAs
 //   warp 2       the pages' scales
-//   warps 4-7    widening: codes to f16 tiles (two buffers each of K and V); Q
-//   warps 8-11, 12-15   softmax and epilogue of the halves, a thread a row
+//   warps 4-7    widening: codes to f16 tiles (two buffers each of K and V)
+//   warps 8-11, 12-15   Q, softmax and epilogue of the halves, a thread a row
 // The softmax warps keep a row's 128 scores in registers (200 a thread by
 // setmaxnreg, the other warps 56: 512 x 128 in all).
 #include <float.h>
@@ -42,6 +42,7 @@ namespace {
 constexpr int ROWS = 256;
 constexpr int NTHREADS = 512;
 constexpr int SRING = 8;
+constexpr int UNITS = 4;  // units handed on ahead
 constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
 constexpr float TAU = 8.f;        // m moves when x exceeds it by more
 constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
@@ -70,11 +71,12 @@ template <int D> struct alignas(1024) Smem {
     uint8_t v16[2][NH * HALF];
     uint8_t stage[2][TILE * D];
     float4 sc[SRING][8];
-    float qf[ROWS];
+    int zero[SRING];  // a visible page of the tile has a zero value scale
     PlanStart plan;
+    UnitRing<ROWS, UNITS> units;
     uint64_t s8_full[2], s8_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -102,8 +104,12 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
         prefetch_tmap(tk);
         prefetch_tmap(tv);
     }
-    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
+    UnitIter<ROWS> it(p.plan, sm.plan);
+    if (p.plan.split && lane == 0) write_note(it, p.ws);
+    for (; it.live && ok; it.next(p.plan)) {
         const Unit<ROWS> &u = it.u;
+        if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
             const int pid = c + lane / per_tile < u.end
@@ -130,6 +136,10 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
             }
         }
     }
+    if (lane == 0 && ok) {
+        Unit<ROWS> last{};
+        sm.units.put(it.index, last, ctx, &sm.abort);
+    }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     if (lane == 0) {  // copies in flight land before the CTA leaves
         int zero = 0;
@@ -144,8 +154,11 @@ __device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &c
     const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
     int t = 0;
     bool ok = true;
-    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
-        const Unit<ROWS> &u = it.u;
+    for (int i = 0; ok; ++i) {
+        ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, &sm.abort));
+        if (!ok) break;
+        const Unit<ROWS> &u = sm.units.u[i % UNITS];
+        if (u.begin == u.end) break;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
             const int pid = c + lane / per_tile < u.end
@@ -153,79 +166,54 @@ __device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &c
                                 : -1;
             const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
-            for (int i = 0; i < nt; ++i, ++t) {
+            for (int a = 0; a < nt; ++a, ++t) {
                 const int st = t % SRING, use = t / SRING;
                 if (use >= 1)
                     ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx, &sm.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const int sl = lane - i * per_tile;
-                if (sl >= 0 && sl < per_tile) sm.sc[st][sl] = s;
+                const int sl = lane - a * per_tile;
+                const bool here = sl >= 0 && sl < per_tile;
+                if (here) sm.sc[st][sl] = s;
+                const bool zero = __any_sync(0xffffffffu, here && pid >= 0 && s.w == 0.f);
+                if (lane == 0) sm.zero[st] = zero;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[st]));
             }
         }
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
     }
 }
 
-// Widens tiles and prepares Q; 128 threads. Returns early when a wait gives up
+// Widens tiles; 128 threads. Returns early when a wait gives up
 // (no named barriers here, so every warp may leave by itself).
 template <int D>
 __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
     constexpr int UR = D / 16;             // 16-code units a row
     constexpr int PER = TILE * UR / 128;   // units a thread, a tile
-    const int tid = threadIdx.x - 128, lane = tid & 31, G = p.plan.G;
+    const int tid = threadIdx.x - 128, lane = tid & 31;
     volatile int *abort = &sm.abort;
+    // unit i * 128 + tid of a tile: the row moves on by a multiple of 8, so its
+    // place in the swizzle stays. The second column half's lanes store their two
+    // 16-byte units in the other order, so that the halves' units fall into
+    // different banks.
+    const int r0 = tid / UR, un = tid % UR;
+    const bool sw = D == 128 && un >= 4;
+    const uint32_t half = (uint32_t)(un >> 2) * Smem<D>::HALF, first = 2 * (un & 3) + (sw ? 1 : 0);
+    const uint32_t at0 = half + sw128_offset(r0, first), at1 = half + sw128_offset(r0, first ^ 1);
     int t = 0;  // tiles
-    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
-        const Unit<ROWS> &u = it.u;
-        // ---- Q: D / 8 lanes a row, 8 columns each
-        if (it.index >= 1 && !mbar_wait(smem_u32(&sm.q_empty), (it.index - 1) & 1, ctx, abort))
-            return;
-        constexpr int LR = D / 8;
-#pragma unroll 4
-        for (int r = tid / LR; r < ROWS; r += 128 / LR) {
-            const int c = tid % LR;
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (r < u.nrows) {
-                const int row = u.row0 + r;
-                x = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + (size_t)(u.s.t0 + row / G) * p.q_stride +
-                    (size_t)(u.h * G + row % G) * D + 8 * c));
-            }
-            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
-            float amax = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = fabsf(__uint_as_float(v[e] << 16));
-                const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
-                if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
-                if (b < INFINITY) amax = fmaxf(amax, b);
-            }
-#pragma unroll
-            for (int o = LR / 2; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            // 2^k with amax 2^k in [128, 256)
-            int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
-            k = amax > 0.f ? max(-120, min(k, 120)) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = pack_f16x2(__uint_as_float(v[e] << 16) * up,
-                                  __uint_as_float(v[e] & 0xffff0000u) * up);
-            *reinterpret_cast<uint4 *>(sm.q[r >> 7] + (c >> 3) * Smem<D>::HALF +
-                                       sw128_offset(r & 127, c & 7)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-            if (c == 0) sm.qf[r] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
-        }
-        fence_proxy_async_smem();
-        mbar_arrive(smem_u32(&sm.q_full));
-        // ---- tiles: K then V
-        for (int j = u.begin; j < u.end; ++j, ++t) {
+    for (int i = 0;; ++i) {
+        if (!sm.units.wait(i, ctx, abort)) return;
+        const Unit<ROWS> &u = sm.units.u[i % UNITS];
+        const int begin = u.begin, end = u.end, lo = u.lo, hi = u.hi, t_first = u.t_first;
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
+        if (begin == end) return;
+        for (int j = begin; j < end; ++j, ++t) {
             const int b = t & 1, use = t >> 1, ss = t % SRING;
-            const int kpos0 = (u.t_first + j) * TILE;
-            const bool edge = kpos0 < u.lo || kpos0 + TILE - 1 > u.hi;
+            const int kpos0 = (t_first + j) * TILE;
+            const bool edge = kpos0 < lo || kpos0 + TILE - 1 > hi;
 #pragma unroll
             for (int kv = 0; kv < 2; ++kv) {
                 if (!mbar_wait(smem_u32(&sm.s8_full[kv]), t & 1, ctx, abort)) return;
@@ -233,35 +221,39 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
                                            (use - 1) & 1, ctx, abort))
                     return;
                 uint8_t *dst = kv ? sm.v16[b] : sm.k16[b];
-                if (kv && !mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
-#pragma unroll 4
-                for (int i = 0; i < PER; ++i) {
-                    const int idx = i * 128 + tid, r = idx / UR, un = idx % UR;
-                    uint4 x = *reinterpret_cast<const uint4 *>(sm.stage[kv] + idx * 16);
+                uint4 x[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    x[i] = *reinterpret_cast<const uint4 *>(sm.stage[kv] + (i * 128 + tid) * 16);
+                if (kv) {
                     // values that no row sees may hold anything, NaN codes too, and
                     // the MMA multiplies them by 0; a zero scale drops the values
-                    if (kv && ((edge && (kpos0 + r < u.lo || kpos0 + r > u.hi)) ||
-                               sm.sc[ss][r >> p.page_shift].w == 0.f))
-                        x = make_uint4(0, 0, 0, 0);
-                    const uint4 a = make_uint4(e4m3x2_to_f16x2(x.x), e4m3x2_to_f16x2(x.x >> 16),
-                                               e4m3x2_to_f16x2(x.y), e4m3x2_to_f16x2(x.y >> 16));
-                    const uint4 c = make_uint4(e4m3x2_to_f16x2(x.z), e4m3x2_to_f16x2(x.z >> 16),
-                                               e4m3x2_to_f16x2(x.w), e4m3x2_to_f16x2(x.w >> 16));
-                    // the second column half's lanes store in the other order, so that
-                    // the two halves' units fall into different banks
-                    const bool sw = D == 128 && un >= 4;
-                    uint8_t *half = dst + (un >> 2) * Smem<D>::HALF;
-                    const uint32_t u0 = 2 * (un & 3) + (sw ? 1 : 0);
-                    *reinterpret_cast<uint4 *>(half + sw128_offset(r, u0)) = sw ? c : a;
-                    *reinterpret_cast<uint4 *>(half + sw128_offset(r, u0 ^ 1)) = sw ? a : c;
+                    if (!mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
+                    if (edge || sm.zero[ss]) {
+#pragma unroll
+                        for (int i = 0; i < PER; ++i) {
+                            const int r = r0 + i * (128 / UR);
+                            if (kpos0 + r < lo || kpos0 + r > hi ||
+                                sm.sc[ss][r >> p.page_shift].w == 0.f)
+                                x[i] = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+                }
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
+                                               e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
+                    const uint4 c = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
+                                               e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
+                    uint8_t *row = dst + i * (128 / UR) * 128;
+                    *reinterpret_cast<uint4 *>(row + at0) = sw ? c : a;
+                    *reinterpret_cast<uint4 *>(row + at1) = sw ? a : c;
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(smem_u32(kv ? &sm.v_full[b] : &sm.k_full[b]));
                 mbar_arrive(smem_u32(&sm.s8_empty[kv]));
-                if (kv) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
-                }
             }
         }
     }
@@ -299,16 +291,21 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, c
     };
     int t = 0, pc[2] = {0, 0}, ec[2] = {0, 0};  // tiles; per half: P tiles, units
     bool ok = true;
-    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live && ok; it.next(p.plan)) {
-        const int n = it.u.end - it.u.begin;
-        const bool two = it.u.nrows > 128;
-        ok = wait(sm.q_full, it.index) && wait(sm.k_full[t & 1], t >> 1);
+    for (int i = 0; ok; ++i) {
+        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        const Unit<ROWS> &u = sm.units.u[i % UNITS];
+        const int n = u.end - u.begin;
+        const bool two = u.nrows > 128;
+        sm.units.release(i);
+        if (n == 0) break;
+        ok = wait(sm.k_full[t & 1], t >> 1);
+        for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
+            if (!(ok = wait(sm.q_full[half], ec[half]))) break;
+            tc_fence_after();
+            issue_s(half, t & 1);
+        }
         if (!ok) break;
-        tc_fence_after();
-        issue_s(0, t & 1);
-        if (two) issue_s(1, t & 1);
         tc_commit(smem_u32(&sm.k_empty[t & 1]));
-        if (n == 1) tc_commit(smem_u32(&sm.q_empty));
         for (int j = 0; j < n && ok; ++j, ++t) {
             const int b = t & 1, b1 = b ^ 1;
             ok = wait(sm.v_full[b], t >> 1);
@@ -330,7 +327,6 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, c
             tc_commit(smem_u32(&sm.v_empty[b]));
             if (j + 1 < n) {
                 tc_commit(smem_u32(&sm.k_empty[b1]));
-                if (j + 2 == n) tc_commit(smem_u32(&sm.q_empty));
             }
         }
         ++ec[0];
@@ -353,14 +349,12 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
-    int t0 = 0, sc_n = 0, units = 0;  // CTA's tiles; this half's tiles and units
-    for (UnitIter<ROWS> it(p.plan, sm.plan); it.live; it.next(p.plan)) {
-        const Unit<ROWS> &u = it.u;
+    int t0 = 0, sc_n = 0;  // CTA's tiles; this half's tiles
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
+        const Unit<ROWS> &u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin, G = p.plan.G;
-        if (!wait(sm.q_full, it.index)) return;
-        const float qf = sm.qf[r];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty));
+        if (n == 0) return;
         if (half && u.nrows <= 128) {  // nothing in this half: keep the scales' ring going
             for (int j = 0; j < n; ++j) {
                 const int ss = (t0 + j) % SRING;
@@ -368,6 +362,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
             }
             t0 += n;
+            __syncwarp();
+            if (lane == 0) sm.units.release(i);
             continue;
         }
         const int row = u.row0 + r, pos = u.pos(row, G), head = u.h * G + row % G;
@@ -376,6 +372,47 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         const int hi = p.plan.causal ? pos : u.s.len - 1;
         const int lo = p.plan.wl < 0 ? 0 : pos - p.plan.wl;
         const float sink = p.sinks && in ? __ldg(p.sinks + head) * LOG2E : 0.f;
+        // ---- the row's Q: a power of two times it in f16. The half's Q tile is free:
+        // this warp has seen the last S that reads it
+        float qf;
+        {
+            uint4 v[D / 8];
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                p.q + (size_t)(u.s.t0 + (in ? row / G : 0)) * p.q_stride +
+                (size_t)(in ? head : 0) * D);
+            float amax = 0.f;
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = fabsf(__uint_as_float(w[e] << 16));
+                    const float b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
+                    // NaN and inf set no scale
+                    amax = max3(amax, a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
+                }
+            }
+            // 2^k with amax 2^k in [128, 256)
+            int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
+            k = amax > 0.f ? max(-120, min(k, 120)) : 0;
+            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c) {
+                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up,
+                                      __uint_as_float(w[e] & 0xffff0000u) * up);
+                *reinterpret_cast<uint4 *>(sm.q[half] + (c >> 3) * Smem<D>::HALF +
+                                           sw128_offset(r & 127, c & 7)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sm.q_full[half]));
+        }
         float m = NOTHING, l = 0.f;
         for (int j = 0; j < n; ++j, ++sc_n) {
             const int t = t0 + j, ss = t % SRING;
@@ -506,14 +543,13 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             uint32_t o[32];
             tmem_ld32(tmem + O_COL + 32u * c, o);
             tc_wait_ld();
-            if (!in) continue;
-            if (part) {
+            if (in && part) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(prow + 32 * c + e) = make_float4(
                         __uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
                         __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
-            } else {
+            } else if (in) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 8) {
                     uint32_t w[4];
@@ -525,11 +561,13 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
+            __syncwarp();
         }
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty[half]));
-        ++units;
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.o_empty[half]));
+            sm.units.release(i);
+        }
     }
 }
 
@@ -553,6 +591,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.k_empty[i]), 1);
             mbar_init(smem_u32(&sm.v_full[i]), 128);
             mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.q_full[i]), 128);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.p_full[i]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
@@ -562,9 +601,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
         }
-        mbar_init(smem_u32(&sm.q_full), 128);
-        mbar_init(smem_u32(&sm.q_empty), 1 + 8);  // the MMAs and the softmax warps
         mbar_init(smem_u32(&sm.drain), 1);
+        sm.units.init(1 + 1 + 4 + 8);  // MMA issuer, scales, widening, softmax
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -587,10 +625,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             __syncwarp();
         } else if (warp == 2) {
             load_scales<D>(p, sm, ctx);
-        } else if (warp == 3) {
-            if (p.plan.split && lane == 0) write_note<ROWS>(p.plan, sm.plan, p.ws);
-            __syncwarp();
-        } else {
+        } else if (warp >= 4) {
             widen<D>(p, sm, ctx);
         }
     } else {
