@@ -21,6 +21,7 @@ __device__ unsigned g_error_word;
 // on its own 128-byte line.
 constexpr unsigned kClaimStride = 32;
 __device__ unsigned g_claims[kClaimCounters * kClaimStride];
+__device__ unsigned g_joins[kClaimCounters * kJoinPieces];
 
 namespace {
 
@@ -82,6 +83,8 @@ const DevInfo *device_info(cudaError_t *e) {
         d.err = static_cast<unsigned *>(p);
         if ((*e = cudaGetSymbolAddress(&p, g_claims)) != cudaSuccess) return nullptr;
         d.claims = static_cast<unsigned *>(p);
+        if ((*e = cudaGetSymbolAddress(&p, g_joins)) != cudaSuccess) return nullptr;
+        d.joins = static_cast<unsigned *>(p);
         if ((*e = cudaMemset(d.err, 0, sizeof(unsigned))) != cudaSuccess) return nullptr;
         if ((*e = cudaDeviceSynchronize()) != cudaSuccess) return nullptr;
         g_dev[dev] = d;
@@ -99,6 +102,11 @@ unsigned *launch_claim_counter(const DevInfo &dev, cudaStream_t s, cudaError_t *
     unsigned *c = dev.claims + (size_t)(next.fetch_add(1) % kClaimCounters) * kClaimStride;
     *e = cudaMemsetAsync(c, 0, sizeof(*c), s);
     return *e == cudaSuccess ? c : nullptr;
+}
+
+unsigned *next_join_counters(const DevInfo &dev) {
+    static std::atomic<unsigned> next{0};
+    return dev.joins + (size_t)(next.fetch_add(1) % kClaimCounters) * kJoinPieces;
 }
 
 cudaError_t ensure_smem_attr(const void *kernel, size_t bytes, const DevInfo &dev) {
@@ -217,6 +225,9 @@ sattn_status sattn_check_device(void *cuda_stream) {
     if (word) {
         unsigned zero = 0;
         if (cudaMemcpy(dev->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
+            return SATTN_ERR_CUDA;
+        if ((word & DEVERR_TIMEOUT) &&
+            cudaMemset(dev->joins, 0, sizeof(unsigned) * kClaimCounters * kJoinPieces) != cudaSuccess)
             return SATTN_ERR_CUDA;
     }
     if (word & DEVERR_TIMEOUT) return SATTN_ERR_TIMEOUT;

@@ -18,6 +18,7 @@ struct DevInfo {
     int cc_major = 0, cc_minor = 0;
     unsigned *err = nullptr;                 // device address of the error word
     unsigned *claims = nullptr;              // device address of the claim-counter ring
+    unsigned *joins = nullptr;               // and of the join-counter ring
 };
 
 // Per-device facts, initialised once per device (thread-safe).
@@ -35,6 +36,14 @@ struct DevCtx make_ctx(const DevInfo &dev);
 // issued.
 constexpr unsigned kClaimCounters = 256;
 unsigned *launch_claim_counter(const DevInfo &dev, cudaStream_t s, cudaError_t *e);
+
+// The kJoinPieces join counters of one launch of the paged decode kernel, the
+// next of a ring of kClaimCounters such sets. They are zero between launches: a
+// kernel's arrivals wrap them to zero again (sattn_check_device zeroes them
+// after a timeout, when a kernel may have left without arriving). The same limit
+// as for the claim counters holds.
+constexpr unsigned kJoinPieces = 256;
+unsigned *next_join_counters(const DevInfo &dev);
 
 // cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes) once per
 // (kernel, device, size), thread-safe.

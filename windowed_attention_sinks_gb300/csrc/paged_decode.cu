@@ -46,6 +46,7 @@ namespace {
 
 constexpr int NTHREADS = 384;
 constexpr int SRING = 16;
+constexpr int EXTRA = 2;  // a unit's own cost, in tiles
 constexpr int UNITS = 6;  // units handed on ahead
 constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
 constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
@@ -65,6 +66,7 @@ struct DecodeParams {
     __nv_bfloat16 *o;
     float *lse;
     uint8_t *ws;
+    unsigned *join;  // arrivals at each cut unit, by its first piece
 };
 
 template <int D, int R> struct Cfg {
@@ -91,6 +93,7 @@ template <int D, int R> struct alignas(1024) Smem {
     long long orow[2][R];       // output row of each query row, -1 past the last
     int rpos[2][R];             // its position
     float rsink[2][R];          // its sink (log2 units)
+    float wt[2][R];             // what a row of each group's O^T is multiplied by
     float qf[2];                // scale log2(e) / the power of two in Q
     PlanStart plan;
     UnitRing<R, UNITS> units;
@@ -99,14 +102,16 @@ template <int D, int R> struct alignas(1024) Smem {
     uint64_t q_full[2], q_empty[2];
     uint64_t s_full[C::SBUF], s_empty[C::SBUF], p_full[2], pv_done[2], o_empty, drain;
     uint32_t tmem_base;
-    int abort;
+    int abort, last;
 };
 
 // ---------------------------------------------------------------- PTX used here alone
 
-// kind::f8f6f4, e4m3 x e4m3 -> f32; a_mn: A is stored with its M index contiguous.
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn) {
-    return (1u << 4) | (a_mn << 15) | ((N >> 3) << 17) | ((M >> 4) << 24);
+// kind::f8f6f4, e4m3 x e4m3 -> f32; a_mn, b_mn: A is stored with its M index, B with its
+// N index contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn,
+                                                          uint32_t b_mn) {
+    return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                        uint32_t acc) {
@@ -117,22 +122,23 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Shared-memory descriptor of rows of W bytes (64 or 128) under W-byte swizzle,
-// in atoms of 8 rows.
+// Shared-memory descriptor of rows of W bytes (16, 32, 64, 128) under W-byte
+// swizzle (16: none), in atoms of 8 rows that follow one another. Rows are the M or
+// N index with K contiguous, or K with one such atom's M or N contiguous.
 template <int W> __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
-    if (W == 128) return smem_desc_sw128(addr, 16u, 1024u);
     uint64_t d = 0;
     d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)1 << 16;
-    d |= (uint64_t)(512u >> 4) << 32;
+    d |= (uint64_t)(W == 16 ? 8 : 1) << 16;  // unswizzled: 8-row groups of K 128 bytes apart
+    d |= (uint64_t)(8 * W >> 4) << 32;
     d |= (uint64_t)1 << 46;
-    d |= (uint64_t)4 << 61;  // swizzle: 64 B
+    d |= (uint64_t)(W == 128 ? 2 : W == 64 ? 4 : W == 32 ? 6 : 0) << 61;
     return d;
 }
-// Byte offset of 16-byte unit u of row r in such a tile.
+// Byte offset of 16-byte unit u of row r in such a tile: the address bits from 4
+// up are XORed with those from 7 up.
 template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint32_t u) {
-    if (W == 128) return sw128_offset(r, u);
-    return r * 64u + ((u ^ ((r >> 1) & 3u)) << 4);
+    const uint32_t a = r * W + (u << 4);
+    return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
@@ -197,8 +203,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         prefetch_tmap(tv);
     }
     UnitIter<R> it(p.plan, sm.plan);
-    if (p.plan.split && lane == 0) write_note(it, p.ws);
-    for (; it.live && ok; it.next(p.plan)) {
+    for (; it.live && ok; it.next(p.plan, sm.plan)) {
         const Unit<R> &u = it.u;
         if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -303,10 +308,10 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
             const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
             x[i] = make_uint4(0, 0, 0, 0);
             if (r < u.nrows) {
-                const int row = u.row0 + r;
+                const int row = u.row0 + r, tok = p.plan.token(row);
                 x[i] = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + (size_t)(u.s.t0 + row / G) * p.q_stride +
-                    (size_t)(u.h * G + row % G) * D + 8 * c));
+                    p.q + (size_t)(u.s.t0 + tok) * p.q_stride +
+                    (size_t)(u.h * G + row - tok * G) * D + 8 * c));
             }
             const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
@@ -349,10 +354,10 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                 make_uint2(lo[0], lo[1]);
         }
         for (int r = lane; r < R; r += 32) {
-            const int row = u.row0 + r, head = u.h * G + row % G;
+            const int row = u.row0 + r, tok = p.plan.token(row), head = u.h * G + row - tok * G;
             const bool in = r < u.nrows;
-            sm.orow[w][r] = in ? (long long)(u.s.t0 + row / G) * p.H + head : -1;
-            sm.rpos[w][r] = u.pos(row, G);
+            sm.orow[w][r] = in ? (long long)(u.s.t0 + tok) * p.H + head : -1;
+            sm.rpos[w][r] = u.s.len - u.s.n + tok;
             sm.rsink[w][r] = in && p.sinks ? __ldg(p.sinks + head) * LOG2E : 0.f;
         }
         if (lane == 0) sm.qf[w] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
@@ -366,12 +371,12 @@ template <int D, int R>
 __device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
                            const DevCtx &ctx) {
     using C = Cfg<D, R>;
-    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, C::N, 0);
-    constexpr uint32_t IDESC_O = idesc_e4m3_f32(D, C::N, 1);
+    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, C::N, 0, 0);
+    constexpr uint32_t IDESC_O = idesc_e4m3_f32(D, C::N, 1, 1);
     volatile int *abort = &sm.abort;
     if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
     const uint64_t dk = desc_rows<D>(smem_u32(sm.k[0])), dv = desc_rows<D>(smem_u32(sm.v[0]));
-    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0])), dp = desc_rows<128>(smem_u32(sm.p[0]));
+    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0])), dp = desc_rows<C::N>(smem_u32(sm.p[0]));
     int done = 0;  // P V issued
     // per group: whether its next P V is the unit's first, and the unit
     struct Pending {
@@ -391,9 +396,9 @@ __device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
         const uint64_t b = dp + (uint64_t)(g * (C::N * TILE >> 4));
         const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::N;
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V, 32 bytes of P
-            mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * 2), IDESC_O,
-                   kk > 0 || !pe.first);
+        for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V and of P
+            mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * (32 * C::N >> 4)),
+                   IDESC_O, kk > 0 || !pe.first);
         tc_commit(smem_u32(&sm.v_empty[st]));
         tc_commit(smem_u32(&sm.pv_done[g]));
         ++done;
@@ -441,6 +446,89 @@ __device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
     mbar_wait(smem_u32(&sm.drain), 0, ctx, &zero);
 }
 
+// Sums of each l[r] over the warp, to out[0 .. R-1]. Lanes halve the rows they
+// hold while they halve the lanes, so that R rows take about R shuffles instead of 5 R.
+template <int R> __device__ __forceinline__ void column_sums(float (&l)[R], float *out, int lane) {
+    int row = 0;
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        const int o = 16 >> k, n = R >> (k + 1);  // rows left after this step
+        if (n >= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int r = 0; r < n; ++r) {
+                const float send = up ? l[r] : l[r + n], keep = up ? l[r + n] : l[r];
+                l[r] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+            }
+            row += up ? n : 0;
+        } else {
+            l[0] += __shfl_xor_sync(0xffffffffu, l[0], o);
+        }
+    }
+    // lanes that differ in the bits below R's share hold the same row
+    out[row] = l[0];
+}
+
+// The null logit joins a row's denominator.
+__device__ __forceinline__ void with_null_sink(float sink, float &lse2, float &inv) {
+    const float top = fmaxf(lse2, sink);
+    if (top == -INFINITY) return;
+    const float all = top + log2f(ex2(lse2 - top) + ex2(sink - top));
+    inv *= ex2(lse2 - all);
+    lse2 = lse2 != lse2 ? lse2 : all;
+}
+
+// Joins the parts of a cut unit: lse = log sum_c 2^lse2_c (+ the null logit),
+// o = sum_c 2^(lse2_c - lse) o_c, in the order of the pieces. A warp a row:
+// lane c holds part c's denominator, the columns are spread over the lanes.
+template <int D, int R>
+__device__ void join_parts(const DecodeParams &p, int c0, int parts, const long long *orow,
+                           const float *rsink, int warp, int lane) {
+    const float *plse = reinterpret_cast<const float *>(p.ws + plan_lse_offset());
+    const float *prow = reinterpret_cast<const float *>(p.ws + plan_rows_offset(R));
+    constexpr int E = D / 32;
+    // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ...
+    auto slot = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+    for (int r = warp; r < R; r += 8) {
+        const long long row = orow[r];
+        if (row < 0) continue;
+        float m = -INFINITY;
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(plse + slot(i) * R + r));
+        m = warp_max(m);
+        float acc[E] = {};
+        float z = 0.f;
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            // only -inf counts as nothing: a NaN denominator (a NaN key) stays
+            const float l = i0 + lane < parts ? __ldcg(plse + slot(i0 + lane) * R + r) : -INFINITY;
+            const float wt = l == -INFINITY ? 0.f : ex2(l - m);
+            z += warp_sum(wt);
+            const int cnt = min(32, parts - i0);
+#pragma unroll 8
+            for (int i = 0; i < cnt; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, wt, i);
+                const float *at = prow + (slot(i0 + i) * R + r) * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(at));
+                    acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
+                    acc[2] = fmaf(wi, v.z, acc[2]), acc[3] = fmaf(wi, v.w, acc[3]);
+                } else {
+                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(at));
+                    acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
+                }
+            }
+        }
+        float lse2 = z == 0.f ? -INFINITY : m + log2f(z), inv = z == 0.f ? 0.f : 1.f / z;
+        if (p.sink_mode == 2) with_null_sink(rsink[r], lse2, inv);
+        __nv_bfloat16 *dst = p.o + row * D + lane * E;
+        if constexpr (E == 4)
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
+                                                         pack_bf16x2(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        if (p.lse && lane == 0) p.lse[row] = lse2 * LN2;
+    }
+}
+
 template <int D, int R>
 __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     using C = Cfg<D, R>;
@@ -449,7 +537,6 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
     const int key = quarter * 32 + lane;  // key of the tile = TMEM lane
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + C::O_COL + lanes;
-    const uint32_t pbuf = smem_u32(sm.p[g]);
     volatile int *abort = &sm.abort;
     const int bar_g = 1 + g, bar_all = 3;
     // Once a wait has given up (ok), the warp goes through the rest of its unit
@@ -575,40 +662,47 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             // P overwrites the group's last one, which its P V has read by now
             // (waited for here because nothing else does when m stays)
             if (t >= 2) wait(sm.pv_done[g], (t >> 1) - 1);
+            // the key's row of P: R hi codes, then R lo codes, 16 bytes a store
 #pragma unroll
-            for (int r = 0; r < R; r += 2) {
-                const float a = ex2(x[r] + (BASE - m[r]));
-                const float b = ex2(x[r + 1] + (BASE - m[r + 1]));
-                l[r] = fmaf(a, sc.z, l[r]);
-                l[r + 1] = fmaf(b, sc.z, l[r + 1]);
-                const float a0 = a * sc.w, b0 = b * sc.w;
-                const uint32_t h = e4m3x2(a0, b0);
-                const float2 back = e4m3x2_to_f32(h);
-                const uint32_t lo = e4m3x2((a0 - back.x) * 16.f, (b0 - back.y) * 16.f);
-                const uint32_t unit = (uint32_t)key >> 4, in = key & 15u;
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(r, unit) + in), "r"(h)
-                             : "memory");
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(r + 1, unit) + in),
-                             "r"(h >> 8)
-                             : "memory");
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(R + r, unit) + in),
-                             "r"(lo)
-                             : "memory");
-                asm volatile("st.shared.u8 [%0], %1;" ::"r"(pbuf + sw128_offset(R + r + 1, unit) + in),
-                             "r"(lo >> 8)
-                             : "memory");
+            for (int c = 0; c < R; c += 16) {
+                constexpr int CH = R < 16 ? R : 16;
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < CH; e += 2) {
+                    const int r = c + e;
+                    const float a = ex2(x[r] + (BASE - m[r]));
+                    const float b = ex2(x[r + 1] + (BASE - m[r + 1]));
+                    l[r] = fmaf(a, sc.z, l[r]);
+                    l[r + 1] = fmaf(b, sc.z, l[r + 1]);
+                    const float a0 = a * sc.w, b0 = b * sc.w;
+                    const uint32_t h = e4m3x2(a0, b0);
+                    const float2 back = e4m3x2_to_f32(h);
+                    const uint32_t g2 = e4m3x2((a0 - back.x) * 16.f, (b0 - back.y) * 16.f);
+                    if (e & 2) {
+                        hi[e >> 2] |= h << 16;
+                        lo[e >> 2] |= g2 << 16;
+                    } else {
+                        hi[e >> 2] = h;
+                        lo[e >> 2] = g2;
+                    }
+                }
+                if constexpr (R == 8) {
+                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, 0)) =
+                        make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                } else {
+                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, c / 16)) =
+                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, (R + c) / 16)) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
             }
             fence_proxy_async_smem();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[g]));
         }
-        // ---- the unit's end: join the groups, write rows or a part
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const float s = warp_sum(l[r]);
-            if (lane == 0) sm.lx[w][g][quarter][r] = s;
-        }
+        // ---- the unit's end: the groups' maxima, row sums and O^T, joined
+        column_sums<R>(l, sm.lx[w][g][quarter], lane);
         if (quarter == 0 && lane == 0) {
 #pragma unroll
             for (int r = 0; r < R; ++r) sm.mx[w][g][r] = m[r];
@@ -624,13 +718,37 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         named_sync(bar_all, 256);
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
-        const bool writes = D == 128 || lane < 16;  // 64 rows of O^T: 16 lanes of every 32
-        const int col = D == 128 ? key : quarter * 16 + lane;
         const size_t slot = (size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1);
-        float *plse = reinterpret_cast<float *>(p.ws + plan_lse_offset()) + slot * R;
-        float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D;
-#pragma unroll 1
-        for (int r0 = g * (R / 2); r0 < (g + 1) * (R / 2); r0 += 4) {
+        // a thread a row: what each group's O^T is multiplied by, and the denominator
+        const int me = threadIdx.x - 128;
+        if (me < R) {
+            const float m0 = sm.mx[w][0][me], m1 = sm.mx[w][1][me], mm = fmaxf(m0, m1);
+            const float w0 = has[0] ? ex2(m0 - mm) : 0.f, w1 = has[1] ? ex2(m1 - mm) : 0.f;
+            float z = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (has[0]) z = fmaf(w0, sm.lx[w][0][q][me], z);
+                if (has[1]) z = fmaf(w1, sm.lx[w][1][q][me], z);
+            }
+            float lse2 = z == 0.f ? -INFINITY : mm - BASE + log2f(z);
+            float inv = z == 0.f ? 0.f : 1.f / z;
+            if (part) {
+                if (ok) reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot * R + me] = lse2;
+            } else {
+                if (p.sink_mode == 2) with_null_sink(sm.rsink[w][me], lse2, inv);
+                const long long row = sm.orow[w][me];
+                if (ok && p.lse && row >= 0) p.lse[row] = lse2 * LN2;
+            }
+            sm.wt[0][me] = w0 * inv;
+            sm.wt[1][me] = w1 * inv;
+        }
+        named_sync(bar_all, 256);
+        const bool writes = (D == 128 || lane < 16) && ok;  // 64 rows of O^T: 16 lanes of every 32
+        const int col = D == 128 ? key : quarter * 16 + lane;
+        float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D + col;
+#pragma unroll
+        for (int k = 0; k < R / 2; k += 4) {
+            const int r0 = g * (R / 2) + k;
             uint32_t v[4][4];  // group 0 hi, lo, group 1 hi, lo
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -642,46 +760,38 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = r0 + e;
-                const float m0 = sm.mx[w][0][r], m1 = sm.mx[w][1][r];
-                const float mm = fmaxf(m0, m1);
-                float acc = 0.f, z = 0.f;
+                float acc = 0.f;
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    const float ms = s ? m1 : m0;
-                    if (!has[s]) continue;
-                    const float wt = ex2(ms - mm);
-                    acc += wt * fmaf(__uint_as_float(v[2 * s + 1][e]), 0.0625f,
-                                     __uint_as_float(v[2 * s][e]));
-                    z += wt * ((sm.lx[w][s][0][r] + sm.lx[w][s][1][r]) +
-                               (sm.lx[w][s][2][r] + sm.lx[w][s][3][r]));
-                }
-                float lse2 = z == 0.f ? -INFINITY : mm - BASE + log2f(z);
-                float inv = z == 0.f ? 0.f : 1.f / z;
-                if (!ok) continue;
+                for (int s = 0; s < 2; ++s)
+                    if (has[s])
+                        acc = fmaf(sm.wt[s][r],
+                                   fmaf(__uint_as_float(v[2 * s + 1][e]), 0.0625f,
+                                        __uint_as_float(v[2 * s][e])),
+                                   acc);
+                if (!writes) continue;
                 if (part) {
-                    if (writes) prow[(size_t)r * D + col] = acc * inv;
-                    if (key == 0) plse[r] = lse2;
-                    continue;
+                    prow[(size_t)r * D] = acc;
+                } else if (sm.orow[w][r] >= 0) {
+                    p.o[sm.orow[w][r] * D + col] = __float2bfloat16_rn(acc);
                 }
-                const long long row = sm.orow[w][r];
-                if (row < 0) continue;
-                if (p.sink_mode == 2) {  // the null logit joins the denominator
-                    const float s2 = sm.rsink[w][r];
-                    const float top = fmaxf(lse2, s2);
-                    if (top != -INFINITY) {
-                        const float all = top + log2f(ex2(lse2 - top) + ex2(s2 - top));
-                        inv *= ex2(lse2 - all);
-                        lse2 = lse2 != lse2 ? lse2 : all;
-                    }
-                }
-                if (writes) p.o[row * D + col] = __float2bfloat16_rn(acc * inv);
-                if (key == 0 && p.lse) p.lse[row] = lse2 * LN2;
             }
         }
         tc_fence_before();
         __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty));
+        if (part) {  // the last of the unit's pieces to get here joins them
+            __threadfence();
+            const bool bad = sync_any<256>(bar_all, !ok);
+            if (me == 0)
+                sm.last = atomicInc(p.join + u.c0, (unsigned)u.parts - 1) == (unsigned)u.parts - 1;
+            named_sync(bar_all, 256);
+            if (sm.last && !bad) {
+                __threadfence();
+                join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp - 4, lane);
+            }
+        }
+        __syncwarp();
         if (lane == 0) {
-            mbar_arrive(smem_u32(&sm.o_empty));
             mbar_arrive(smem_u32(&sm.q_empty[w]));
             sm.units.release(i);
         }
@@ -697,8 +807,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     extern __shared__ __align__(1024) uint8_t dsmem[];
     Smem<D, R> &sm = *reinterpret_cast<Smem<D, R> *>(dsmem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // the join may be scheduled once every CTA is here; it waits for their end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
@@ -771,17 +879,16 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(R, D);
-    DecodeParams p{plan_args(a, split, 1), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
+    DecodeParams p{plan_args(a, split, EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
                    a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
                    a.max_pages, a.num_pages * a.Hkv * a.page, a.scale * LOG2E, a.sinks, a.sink_mode,
-                   static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace)};
+                   static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace),
+                   next_join_counters(dev)};
     if (verbose())
         fprintf(stderr, "sattn: paged decode_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, R, grid,
                 smem, (int)split);
     decode_kernel<D, R><<<grid, NTHREADS, smem, s>>>(tk, tv, p, make_ctx(dev));
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !split) return e;
-    return launch_paged_join(a, R, grid, s);
+    return cudaGetLastError();
 }
 
 }  // namespace

@@ -3,13 +3,14 @@
 // A unit is up to ROWS query rows of one sequence and KV head (rows run
 // token-major over the tokens and the heads of the group, so any group size
 // fills a unit) with the 128-key tiles that any of them can see. Units are
-// numbered sequence by sequence, KV head by KV head; their tiles in a row form
-// one line of `total` tiles, cut into equal pieces, one a CTA. A piece may
+// numbered sequence by sequence, KV head by KV head; their tiles in a row, and
+// before each unit's tiles `extra` for what a unit costs by itself, form one
+// line that is cut into equal pieces, one a CTA. A piece may
 // begin and end inside a unit: a ragged batch then keeps every SM busy for the
 // same time, whatever its lengths, and one long sequence spreads over all SMs.
 // A unit that lies in one piece is finished there; the pieces of a unit that
 // is cut write partial results (normalised rows and their log2 denominators)
-// to the workspace, and a second, small launch joins them in a fixed order.
+// to the workspace, and they are joined in a fixed order.
 // Everything is computed from the lengths on the device, so a call needs no
 // host copy of them and can be captured and replayed with other lengths.
 #pragma once
@@ -28,12 +29,23 @@ struct PlanArgs {
     int B, T, G, Hkv, page, causal, wl;
     long long capacity;  // positions that the page table holds
     int split;           // 0: no workspace, pieces end at unit boundaries
-    int min_tiles;       // least tiles a CTA takes, while there are fewer than CTAs x that
+    int extra;           // a unit's own cost, in tiles
+    uint32_t g_mul, g_shift;
+
+    // row / G for 0 <= row < 2^31: with s = ceil(log2 G) and
+    // mul = 2^32 (2^s - G) / G + 1, row / G = (high(mul row) + row) >> s.
+    __device__ __forceinline__ int token(int row) const {
+        return (int)((__umulhi(g_mul, (uint32_t)row) + (uint32_t)row) >> g_shift);
+    }
 };
 
-__host__ inline PlanArgs plan_args(const PagedArgs &a, int split, int min_tiles) {
-    return PlanArgs{a.cu_seqlens, a.kv_lens, a.B, a.T, a.H / a.Hkv, a.Hkv, a.page, a.causal,
-                    a.window_left, (long long)a.max_pages * a.page, split, min_tiles};
+__host__ inline PlanArgs plan_args(const PagedArgs &a, int split, int extra) {
+    const uint32_t G = (uint32_t)(a.H / a.Hkv);
+    uint32_t s = 0;
+    while ((1ull << s) < G) ++s;
+    const uint32_t mul = (uint32_t)((((1ull << s) - G) << 32) / G + 1);
+    return PlanArgs{a.cu_seqlens, a.kv_lens, a.B, a.T, (int)G, a.Hkv, a.page, a.causal,
+                    a.window_left, (long long)a.max_pages * a.page, split, extra, mul, s};
 }
 
 // One unit's rows and keys.
@@ -45,14 +57,17 @@ template <int ROWS> struct Unit {
     int ilo, ihi;          // keys that all of them see
     int t_first, ntiles;   // tiles of the sequence; ntiles >= 1 (an empty unit's is masked)
     int begin, end;        // the tiles of this piece, 0 .. ntiles
+    int c0, parts;         // of a cut unit: its first piece, and how many
 
-    __device__ __forceinline__ int pos(int row, int G) const { return s.len - s.n + row / G; }
+    __device__ __forceinline__ int pos(const PlanArgs &p, int row) const {
+        return s.len - s.n + p.token(row);
+    }
 
     __device__ __forceinline__ void set_rows(const PlanArgs &p, int rt_) {
         rt = rt_;
         row0 = rt * ROWS;
         nrows = min(ROWS, s.n * p.G - row0);
-        const int p0 = pos(row0, p.G), p1 = pos(row0 + nrows - 1, p.G);
+        const int p0 = pos(p, row0), p1 = pos(p, row0 + nrows - 1);
         lo = p.wl < 0 ? 0 : max(0, p0 - p.wl);
         ilo = p.wl < 0 ? 0 : max(0, p1 - p.wl);
         hi = p.causal ? p1 : s.len - 1;
@@ -70,13 +85,13 @@ __device__ __forceinline__ bool plan_seq(const PlanArgs &p, int b, Unit<ROWS> &u
     return true;
 }
 
-// Tiles of one head of a sequence: by one thread, or by a warp (then every lane has the sum).
+// Line length of one head of a sequence: by one thread, or by a warp (then every lane has the sum).
 template <int ROWS, bool WARP>
 __device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u) {
     long long sum = 0;
     for (int rt = WARP ? threadIdx.x & 31 : 0; rt < u.nrt; rt += WARP ? 32 : 1) {
         u.set_rows(p, rt);
-        sum += u.ntiles;
+        sum += u.ntiles + p.extra;
     }
     if (WARP) {
 #pragma unroll
@@ -87,10 +102,11 @@ __device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u)
 
 // What a CTA starts from (in shared memory).
 struct PlanStart {
-    long long x0, x1;  // its tiles of the line
-    int b, h, rt, begin;
+    long long x0, x1;  // its piece of the line
+    long long total, ustart;  // the line; where the unit that holds x0 starts
+    int pieces, b, h, rt;
     long long wsum[32];
-    long long before;  // tiles before the sequences b0 .. b1 - 1, in which x0 lies
+    long long before;  // line before the sequences b0 .. b1 - 1, in which x0 lies
     int b0, b1;
 };
 
@@ -126,14 +142,21 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
         if (w < warp) before += ps.wsum[w];
         total += ps.wsum[w];
     }
-    const long long most = (total + p.min_tiles - 1) / p.min_tiles;
-    const long long pieces = min((long long)gridDim.x, max(1ll, most));
-    const long long c = blockIdx.x;
-    const long long x0 = c < pieces ? total * c / pieces : total;
-    const long long x1 = c < pieces ? total * (c + 1) / pieces : total;
+    const int pieces = (int)min((long long)gridDim.x, max(1ll, total));
+    const int c = min((int)blockIdx.x, pieces);
+    long long x0, x1;
+    if (total < (1 << 23)) {  // c <= 256: 32-bit division
+        x0 = (uint32_t)total * (uint32_t)c / (uint32_t)pieces;
+        x1 = (uint32_t)total * (uint32_t)min(c + 1, pieces) / (uint32_t)pieces;
+    } else {
+        x0 = total * c / pieces;
+        x1 = total * min(c + 1, pieces) / pieces;
+    }
     if (tid == 0) {
         ps.x0 = x0;
         ps.x1 = x1;
+        ps.total = total;
+        ps.pieces = pieces;
     }
     if (x0 < x1 && x0 >= before && x0 < before + mine) {
         ps.before = before;
@@ -150,13 +173,14 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
             if (x0 < at + ph * p.Hkv) break;
             at += ph * p.Hkv;
         }
-        const int h = (int)((x0 - at) / ph);
+        int h = 0;
+        while (x0 >= at + (h + 1) * ph) ++h;
         at += h * ph;
         for (int r0 = 0; r0 < u.nrt; r0 += 32) {
             int nt = 0;
             if (r0 + lane < u.nrt) {
                 u.set_rows(p, r0 + lane);
-                nt = u.ntiles;
+                nt = u.ntiles + p.extra;
             }
             long long upto = nt;
 #pragma unroll
@@ -168,7 +192,7 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
                 ps.b = b;
                 ps.h = h;
                 ps.rt = r0 + lane;
-                ps.begin = (int)(x0 - (at + upto - nt));
+                ps.ustart = at + upto - nt;
             }
             at += __shfl_sync(0xffffffffu, upto, 31);
             if (x0 < at) break;
@@ -180,34 +204,42 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
 // Walks the units of a CTA's piece.
 template <int ROWS> struct UnitIter {
     Unit<ROWS> u;
-    long long pos, x1;  // line position of u's first tile here
-    int index;          // units seen
+    long long ustart, x1;  // where u starts on the line
+    int index;             // units seen
     bool live;
 
     __device__ __forceinline__ UnitIter(const PlanArgs &p, const PlanStart &ps) {
-        pos = ps.x0;
         x1 = ps.x1;
         index = 0;
-        live = pos < x1;
+        live = ps.x0 < x1;
         if (!live) return;
         plan_seq(p, ps.b, u);
         u.h = ps.h;
         u.set_rows(p, ps.rt);
-        u.begin = ps.begin;
-        if (!p.split && u.begin > 0) {  // the piece before finishes this unit
-            pos += u.ntiles - u.begin;
-            live = pos < x1;
-            if (live) {
-                step(p);
-                u.begin = 0;
-            }
+        ustart = ps.ustart;
+        u.begin = (int)max(0ll, ps.x0 - ustart - p.extra);
+        if (!p.split && ps.x0 > ustart + p.extra) step(p);  // the piece before finishes it
+        clip(p, ps);
+    }
+    __device__ __forceinline__ int piece(const PlanStart &ps, long long x) const {
+        return (int)(((x + 1) * ps.pieces - 1) / ps.total);
+    }
+    // The tiles of u in this piece; none ends the piece.
+    __device__ __forceinline__ void clip(const PlanArgs &p, const PlanStart &ps) {
+        const long long t0 = ustart + p.extra;
+        live = live && t0 + u.begin < x1;
+        u.end = p.split ? (int)min((long long)u.ntiles, x1 - t0) : u.ntiles;
+        u.c0 = 0;
+        u.parts = 1;
+        if (live && (u.begin > 0 || u.end < u.ntiles)) {
+            u.c0 = piece(ps, t0);
+            u.parts = piece(ps, t0 + u.ntiles - 1) - u.c0 + 1;
         }
-        if (live) clip(p);
     }
-    __device__ __forceinline__ void clip(const PlanArgs &p) {
-        u.end = p.split ? (int)min((long long)u.ntiles, u.begin + (x1 - pos)) : u.ntiles;
-    }
+    // To the next unit of the line; there may be none behind this piece.
     __device__ __forceinline__ void step(const PlanArgs &p) {
+        ustart += u.ntiles + p.extra;
+        u.begin = 0;
         if (u.rt + 1 < u.nrt) {
             u.set_rows(p, u.rt + 1);
             return;
@@ -218,18 +250,18 @@ template <int ROWS> struct UnitIter {
             return;
         }
         u.h = 0;
-        for (int b = u.b + 1; b < p.B; ++b)  // ends: x1 lies within the line
+        int b = u.b + 1;
+        for (; b < p.B; ++b)
             if (plan_seq(p, b, u) && u.s.n > 0) break;
-        u.set_rows(p, 0);
+        if (b < p.B) u.set_rows(p, 0);
+        else live = false;
     }
-    __device__ __forceinline__ void next(const PlanArgs &p) {
-        pos += u.end - u.begin;
+    __device__ __forceinline__ void next(const PlanArgs &p, const PlanStart &ps) {
         ++index;
-        live = pos < x1;
+        live = u.end == u.ntiles;
         if (!live) return;
         step(p);
-        u.begin = 0;
-        clip(p);
+        if (live) clip(p, ps);
     }
 };
 
@@ -304,13 +336,13 @@ template <int ROWS, int N> struct UnitRing {
     __device__ __forceinline__ void release(int i) { mbar_arrive(smem_u32(&empty[i % N])); }
 };
 
-// A piece's note for the join: whether it begins inside a unit, whether that
-// unit also goes on behind the piece, and which unit it is.
+// A piece's note for the join launch: whether it begins inside a unit, whether
+// that unit also goes on behind the piece, and which unit it is.
 struct PlanNote {
     int cont, through, t0, h, row0, nrows, pad0, pad1;
 };
 
-// Workspace: PlanNote [pieces], lse2 [pieces][2][ROWS], rows [pieces][2][ROWS][D].
+// Workspace: PlanNote [pieces], lse2 [pieces][2][ROWS], rows [pieces][2][ROWS][D] (fp32).
 // Part 0 of a piece is its first unit if that began earlier, part 1 its last
 // unit if that begins here and goes on.
 constexpr int MAX_PIECES = 256;

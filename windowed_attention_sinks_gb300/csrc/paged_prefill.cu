@@ -42,6 +42,7 @@ namespace {
 constexpr int ROWS = 256;
 constexpr int NTHREADS = 512;
 constexpr int SRING = 8;
+constexpr int EXTRA = 3;  // a unit's own cost, in tiles
 constexpr int UNITS = 4;  // units handed on ahead
 constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
 constexpr float TAU = 8.f;        // m moves when x exceeds it by more
@@ -106,7 +107,7 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     }
     UnitIter<ROWS> it(p.plan, sm.plan);
     if (p.plan.split && lane == 0) write_note(it, p.ws);
-    for (; it.live && ok; it.next(p.plan)) {
+    for (; it.live && ok; it.next(p.plan, sm.plan)) {
         const Unit<ROWS> &u = it.u;
         if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
@@ -366,7 +367,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             if (lane == 0) sm.units.release(i);
             continue;
         }
-        const int row = u.row0 + r, pos = u.pos(row, G), head = u.h * G + row % G;
+        const int row = u.row0 + r, tok = p.plan.token(row), head = u.h * G + row - tok * G;
+        const int pos = u.s.len - u.s.n + tok;
         const bool in = r < u.nrows;
         // the row's keys; a row past the unit's last sees what it likes (not written)
         const int hi = p.plan.causal ? pos : u.s.len - 1;
@@ -378,7 +380,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         {
             uint4 v[D / 8];
             const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + (size_t)(u.s.t0 + (in ? row / G : 0)) * p.q_stride +
+                p.q + (size_t)(u.s.t0 + (in ? tok : 0)) * p.q_stride +
                 (size_t)(in ? head : 0) * D);
             float amax = 0.f;
 #pragma unroll
@@ -522,7 +524,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         float inv = l == 0.f ? 0.f : 1.f / l;
         const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
-        const size_t orow = (size_t)(u.s.t0 + row / G) * p.H + head;
+        const size_t orow = (size_t)(u.s.t0 + tok) * p.H + head;
         if (in) {
             if (part) {
                 reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot] = lse2;
@@ -652,7 +654,7 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D);
-    PrefillParams p{plan_args(a, split, 1), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
+    PrefillParams p{plan_args(a, split, EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
                     a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page,
                     page_shift(a.page), a.max_pages, a.num_pages * a.Hkv * a.page,
                     a.scale * LOG2E, a.sinks, a.sink_mode, static_cast<__nv_bfloat16 *>(a.o),
