@@ -354,35 +354,85 @@ def kv_ring_write(kv_cache, kv_new, start_pos, win, stream=None):
     return kv_cache
 
 
+class _OnDevice:
+    """`with _OnDevice(i, stream) as s`: device i current, s the raw handle of `stream`
+    (a torch stream) or of that device's current stream. A decode step makes
+    a few calls of some microseconds of GPU work each, so this costs nothing where
+    the device is current already."""
+
+    __slots__ = ("index", "stream", "guard")
+
+    def __init__(self, index, stream):
+        self.index, self.stream, self.guard = index, stream, None
+
+    def __enter__(self):
+        import torch
+
+        if torch._C._cuda_getDevice() != self.index:
+            self.guard = torch.cuda.device(self.index)
+            self.guard.__enter__()
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
 def _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens):
-    """Checks the tensors of a paged FP8 cache; returns (pages, Hkv, page, d, B, max_pages)."""
+    """Checks the tensors of a paged FP8 cache; returns (device index, pages, Hkv,
+    page, d, B, max_pages)."""
     import torch
 
-    device = k_cache.device
-    for t, n, dt in ((k_cache, "k_cache", torch.uint8), (v_cache, "v_cache", torch.uint8),
-                     (k_scale, "k_scale", torch.float32), (v_scale, "v_scale", torch.float32),
-                     (page_table, "page_table", torch.int32),
-                     (cu_seqlens, "cu_seqlens", torch.int32), (kv_lens, "kv_lens", torch.int32)):
-        _need(t, n, dt, device)
+    u8, f32, i32 = torch.uint8, torch.float32, torch.int32
+    dev = k_cache.get_device()
+    if dev < 0:
+        raise ValueError("k_cache must be a CUDA tensor")
+    if not (k_cache.dtype is u8 and v_cache.dtype is u8 and k_scale.dtype is f32
+            and v_scale.dtype is f32 and page_table.dtype is i32 and cu_seqlens.dtype is i32
+            and kv_lens.dtype is i32):
+        raise ValueError("caches must be uint8, scales float32, page_table, cu_seqlens and "
+                         "kv_lens int32")
+    if not (v_cache.get_device() == dev and k_scale.get_device() == dev
+            and v_scale.get_device() == dev and page_table.get_device() == dev
+            and cu_seqlens.get_device() == dev and kv_lens.get_device() == dev):
+        raise ValueError("the cache's tensors must be on one CUDA device")
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and page_table.is_contiguous()
+            and cu_seqlens.is_contiguous() and kv_lens.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape [pages, Hkv, page, d]")
-    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+    pages, Hkv, page, d = shape
+    if k_scale.shape != (pages, Hkv) or v_scale.shape != (pages, Hkv):
         raise ValueError("k_scale and v_scale must be [pages, Hkv]")
-    B = kv_lens.shape[0]
-    if page_table.dim() != 2 or page_table.shape[0] != B or cu_seqlens.numel() != B + 1:
+    table = page_table.shape
+    if (len(table) != 2 or kv_lens.shape != (table[0],) or cu_seqlens.shape != (table[0] + 1,)):
         raise ValueError("page_table must be [B, max_pages], cu_seqlens [B + 1], kv_lens [B]")
-    return (*shape, B, page_table.shape[1])
+    return dev, pages, Hkv, page, d, table[0], table[1]
 
 
-def _token_rows(t, name, T, heads, d, dtype, device):
+def _token_rows(t, name, T, heads, d, dtype, dev):
     """Checks [T, heads, d] whose heads are contiguous within a token; returns the token stride."""
-    if t.shape != (T, heads, d) or t.dtype != dtype or t.device != device:
-        raise ValueError("%s must be %s [%d, %d, %d] on %s" % (name, dtype, T, heads, d, device))
+    if t.shape != (T, heads, d) or t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError("%s must be %s [%d, %d, %d] on cuda:%d" % (name, dtype, T, heads, d, dev))
     st = t.stride()
-    if (st[2] != 1 and d > 1) or (st[1] != d and heads > 1):
+    if st[2] != 1 or (st[1] != d and heads > 1):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     return st[0] if T > 1 else heads * d
+
+
+def _out(t, name, shape, dtype, dev):
+    """Checks an output tensor, or makes one."""
+    import torch
+
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s on cuda:%d" % (name, dtype, shape, dev))
+    return t
 
 
 def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
@@ -397,35 +447,35 @@ def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     [positions, rd]. With q [T, H, d] returns the rotated queries, else None."""
     import torch
 
-    pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table,
-                                                 cu_seqlens, kv_lens)
-    dev = k_cache.device
-    T = k.shape[0]
-    ks = _token_rows(k, "k", T, Hkv, d, k.dtype, dev)
-    vs = _token_rows(v, "v", T, Hkv, d, k.dtype, dev)
-    rows = rd = 0
+    dev, pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale,
+                                                      page_table, cu_seqlens, kv_lens)
+    T, dt = k.shape[0], k.dtype
+    code = _dtype_code(k)
+    ks = _token_rows(k, "k", T, Hkv, d, dt, dev)
+    vs = _token_rows(v, "v", T, Hkv, d, dt, dev)
+    rows = rd = H = qs = 0
+    table = qp = qo = None
     if cos_sin is not None:
-        _need(cos_sin, "cos_sin", torch.float32, dev)
+        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or \
+                cos_sin.get_device() != dev or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 [positions, rd] on cuda:%d" % dev)
         rows, rd = cos_sin.shape
-    H = qs = 0
+        table = cos_sin.data_ptr()
     if q is not None:
         H = q.shape[1]
-        qs = _token_rows(q, "q", T, H, d, k.dtype, dev)
-        if q_out is None:
-            q_out = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-        else:
-            _need(q_out, "q_out", q.dtype, dev)
-            if q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
+        qs = _token_rows(q, "q", T, H, d, dt, dev)
+        q_out = _out(q_out, "q_out", (T, H, d), dt, dev)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with torch.cuda.device(dev):
-        code = lib().sattn_paged_fp8_append(
-            k.data_ptr(), ks, v.data_ptr(), vs, _ptr(q), qs, _ptr(q_out), _ptr(cos_sin), rows, rd,
+    with _OnDevice(dev, stream) as s:
+        rc = lib().sattn_paged_fp8_append(
+            k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qo, table, rows, rd,
             1 if interleaved else 0, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-            B, T, H, Hkv, d, pages, page, width, _dtype_code(k), _stream(stream))
-    _check("sattn_paged_fp8_append", code)
+            B, T, H, Hkv, d, pages, page, width, code, s)
+    if rc:
+        _check("sattn_paged_fp8_append", rc)
     return q_out
 
 
@@ -440,51 +490,47 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
     """Attention of q [T, H, d] (the last tokens of each sequence) over the
     pages of an e4m3 cache (sattn_paged_fp8_fwd); the cache's tensors as for
     paged_fp8_append. Returns (o, lse). Rows behind the last sequence are not
-    written. Without a workspace one is taken from torch's allocator, on the
-    current stream."""
+    written. Without a workspace one is taken from torch's allocator for the
+    stream that the call runs on."""
     import torch
 
-    pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale, page_table,
-                                                 cu_seqlens, kv_lens)
-    dev = k_cache.device
-    T, H = q.shape[0], q.shape[1]
-    qs = _token_rows(q, "q", T, H, d, q.dtype, dev)
+    dev, pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale,
+                                                      page_table, cu_seqlens, kv_lens)
+    T, H, dt = q.shape[0], q.shape[1], q.dtype
+    code = _dtype_code(q)
+    qs = _token_rows(q, "q", T, H, d, dt, dev)
+    sp = None
     if sinks is not None:
-        _need(sinks, "sinks", torch.float32, dev)
-        if sinks.numel() != H:
-            raise ValueError("sinks must be [H]")
-    if o is None:
-        o = torch.empty((T, H, d), dtype=q.dtype, device=dev)
-    else:
-        _need(o, "o", q.dtype, dev)
-    if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=dev)
-    else:
-        _need(lse, "lse", torch.float32, dev)
-    if o.shape != q.shape or lse.shape != q.shape[:2]:
-        raise ValueError("o must be [T, H, d] and lse [T, H]")
+        if sinks.shape != (H,) or sinks.dtype is not torch.float32 or sinks.get_device() != dev \
+                or not sinks.is_contiguous():
+            raise ValueError("sinks must be a contiguous float32 [H] on cuda:%d" % dev)
+        sp = sinks.data_ptr()
     n = T if max_q_len is None else int(max_q_len)
-    nb = 0
-    if workspace is None:
-        nb = lib().sattn_paged_fp8_workspace_bytes(n, H, Hkv, d) if q.dtype == torch.bfloat16 else 0
-        if nb:
-            if stream is None:
+    L = lib()
+    nb, ws = 0, None
+    with _OnDevice(dev, stream) as s:
+        o = _out(o, "o", (T, H, d), dt, dev)
+        lse = _out(lse, "lse", (T, H), torch.float32, dev)
+        if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise ValueError("workspace must be contiguous on cuda:%d" % dev)
+            nb, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+        elif dt is torch.bfloat16:
+            nb = L.sattn_paged_fp8_workspace_bytes(n, H, Hkv, d)
+            if nb and stream is None:
                 workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
-            else:  # the allocator must know the stream that uses it
+            elif nb:  # the allocator must know the stream that uses it
                 with torch.cuda.stream(stream):
                     workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
-    else:
-        _need(workspace, "workspace", None, dev)
-        nb = workspace.numel() * workspace.element_size()
-    scale = float(d ** -0.5 if scale is None else scale)
-    with torch.cuda.device(dev):
-        code = lib().sattn_paged_fp8_fwd(
+            ws = workspace.data_ptr() if nb else None
+        rc = L.sattn_paged_fp8_fwd(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
-            B, T, n, H, Hkv, d, pages, page, width, int(bool(causal)), int(window_left),
-            _ptr(sinks), int(sink_mode), scale, o.data_ptr(), lse.data_ptr(), _ptr(workspace), nb,
-            _dtype_code(q), _stream(stream))
-    _check("sattn_paged_fp8_fwd", code)
+            B, T, n, H, Hkv, d, pages, page, width, 1 if causal else 0, int(window_left),
+            sp, int(sink_mode), d ** -0.5 if scale is None else float(scale), o.data_ptr(),
+            lse.data_ptr(), ws, nb, code, s)
+    if rc:
+        _check("sattn_paged_fp8_fwd", rc)
     return o, lse
 
 
