@@ -1,0 +1,53 @@
+// tcgen05 pieces that the paged cache's kernels share: e4m3 MMAs and the
+// shared-memory layouts of their operands, and the row arithmetic of a sink.
+#pragma once
+
+#include <math.h>
+
+#include "common.cuh"
+
+namespace sattn {
+
+// kind::f8f6f4, e4m3 x e4m3 -> f32; a_mn, b_mn: A is stored with its M index, B with its
+// N index contiguous.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn,
+                                                          uint32_t b_mn) {
+    return (1u << 4) | (a_mn << 15) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Shared-memory descriptor of rows of W bytes (16, 32, 64, 128) under W-byte
+// swizzle (16: none), in atoms of 8 rows that follow one another. Rows are the M or
+// N index with K contiguous, or K with one such atom's M or N contiguous.
+template <int W> __device__ __forceinline__ uint64_t desc_rows(uint32_t addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(W == 16 ? 8 : 1) << 16;  // unswizzled: 8-row groups of K 128 bytes apart
+    d |= (uint64_t)(8 * W >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)(W == 128 ? 2 : W == 64 ? 4 : W == 32 ? 6 : 0) << 61;
+    return d;
+}
+// Byte offset of 16-byte unit u of row r in such a tile: the address bits from 4
+// up are XORed with those from 7 up.
+template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint32_t u) {
+    const uint32_t a = r * W + (u << 4);
+    return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
+}
+// The null logit joins a row's denominator.
+__device__ __forceinline__ void with_null_sink(float sink, float &lse2, float &inv) {
+    const float top = fmaxf(lse2, sink);
+    if (top == -INFINITY) return;
+    const float all = top + log2f(ex2(lse2 - top) + ex2(sink - top));
+    inv *= ex2(lse2 - all);
+    lse2 = lse2 != lse2 ? lse2 : all;
+}
+
+}  // namespace sattn

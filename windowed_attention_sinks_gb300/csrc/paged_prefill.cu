@@ -3,37 +3,43 @@
 // A unit is 256 query rows (tokens times the heads of a KV group) in two halves
 // of 128, the rows of the MMAs; both halves use each 128-key tile. Here the
 // products bound the time, so operands are what the tensor core takes at full
-// rate with no loss: the codes are widened to f16 in shared memory, which holds every
-// e4m3 value, once a tile for 256 rows; Q is scaled by a power of two a row
-// and taken in f16 (exact for bf16 queries down to 2^-22 of the row's largest), and P is rounded to f16
-// (2^-12 relative; 2^(7 + e - m) <= 2^15, so weights keep that down to 2^-21 of
-// the largest and add at most 2^-32 of it below). S, O and the row sums are fp32.
+// rate with next to no loss:
+//  * S = Q K^T takes K's codes as they are. Q is scaled by a power of two a row
+//    (its largest value then lies in [128, 256)) and split, q = hi + lo with
+//    hi = e4m3(q), lo = e4m3(q - hi): together 8 significant bits, exactly a
+//    bf16's, down to 2^-10 of the row's largest value, and an error of at most 2^-18 of that
+//    below. Both products go into one accumulator; two e4m3 MMAs take the time
+//    of one in f16.
+//  * O += P V: a probability needs more range than two e4m3 terms have, so V's
+//    codes are widened to f16 in shared memory (exact), once a tile for 256
+//    rows, and P is rounded to f16: 2^(7 + x - m) <= 2^15, so 2^-12
+//    relative down to 2^-21 of the largest weight and at most 2^-32 of it below.
+// S, O and the row sums are fp32.
 //
-//   S = Q K^T [128 x 128] into TMEM, a half each
+//   S [128 x 128] into TMEM, a half each
 //   x = S * (scale log2(e) * k_scale) + log2(v_scale): the value's scale goes
 //       into the exponent, so V's codes need none; the row sum divides it out.
 //       Both are one number for a page, that is for 16 columns or more
-//   P = 2^(7 + x - m), f16, over S's own columns
-//   O += P V, P from TMEM
+//   P = 2^(7 + x - m), f16, over S's own columns, 64 keys at a time so that
+//       the first half's P V runs beside the second half's exponentials
 // m moves only when a tile raises it by more than 2^8 (O is then rescaled).
 // TMEM: S / P 2 x 128 columns, O 2 x D: all 512 for D = 128, hence the shared
 // columns of S and P. The MMAs of one CTA run in the order of issue, so S of
 // the next tile may follow the P V that reads its columns.
 //
 // One persistent CTA per SM over an equal piece of the tiles (paged_plan.cuh):
-//   warp 0       the units; TMA: code tiles of K and V in turn into two staging buffers
+//   warp 0       the units; TMA: tiles of K and V, two rings of STAGES
 //   warp 1       MMA issuer: PV(A, t), S(A, t + 1), PV(B, t), S(B, t + 1), ..., so
 //                that one half's softmax runs beside the other half's MMAs
 //   warp 2       the pages' scales
-//   warps 4-7    widening: codes to f16 tiles (two buffers each of K and V)
+//   warps 4-7    widening: V's codes to f16 tiles (two buffers)
 //   warps 8-11, 12-15   Q, softmax and epilogue of the halves, a thread a row
-// The softmax warps keep a row's 128 scores in registers (200 a thread by
-// setmaxnreg, the other warps 56: 512 x 128 in all).
 #include <float.h>
 #include <limits.h>
 #include <math.h>
 #include <stdio.h>
 
+#include "paged_mma.cuh"
 #include "paged_plan.cuh"
 
 namespace sattn {
@@ -41,6 +47,7 @@ namespace {
 
 constexpr int ROWS = 256;
 constexpr int NTHREADS = 512;
+constexpr int STAGES = 3;
 constexpr int SRING = 8;
 constexpr int EXTRA = 3;  // a unit's own cost, in tiles
 constexpr int UNITS = 4;  // units handed on ahead
@@ -67,17 +74,18 @@ struct PrefillParams {
 template <int D> struct alignas(1024) Smem {
     static constexpr uint32_t HALF = 128 * 128;  // 128 rows of 64 f16
     static constexpr int NH = D / 64;            // such column halves a tile
-    uint8_t q[2][NH * HALF];
-    uint8_t k16[2][NH * HALF];
+    uint8_t q[2][2][128 * D];  // half; hi, lo
+    uint8_t k[STAGES][TILE * D];
+    uint8_t v[STAGES][TILE * D];
     uint8_t v16[2][NH * HALF];
-    uint8_t stage[2][TILE * D];
     float4 sc[SRING][8];
     int zero[SRING];  // a visible page of the tile has a zero value scale
     PlanStart plan;
     UnitRing<ROWS, UNITS> units;
-    uint64_t s8_full[2], s8_empty[2], k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t k_full[STAGES], k_empty[STAGES], v8_full[STAGES], v8_empty[STAGES];
+    uint64_t v_full[2], v_empty[2];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_empty[2], drain;
+    uint64_t q_full[2], s_full[2], p_full[2][2], pv_done[2], o_empty[2], drain;
     uint32_t tmem_base;
     int abort;
 };
@@ -86,6 +94,15 @@ constexpr uint32_t TMEM_COLS = 512, HALF_COLS = 256, O_COL = 128;
 // kind::f16, f16 operands, fp32 accumulate; b_mn: B is stored with N contiguous.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn) {
     return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -98,7 +115,7 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     const int lane = threadIdx.x & 31;
     const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
     const uint32_t page_bytes = (uint32_t)p.page * D;
-    int t = 0;  // copies: K and V of a tile
+    int t = 0;  // tiles
     bool ok = true;
     bool bad = false;
     if (lane == 0) {
@@ -119,21 +136,24 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
             bad |= pid == -2;
             const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
             const int nt = min(chunk, u.end - c);
-            for (int i = 0; i < 2 * nt && ok; ++i, ++t) {
-                const int st = t & 1, use = t >> 1;
-                const uint32_t full = smem_u32(&sm.s8_full[st]);
-                bool go = true;
-                if (lane == 0) {
-                    if (use >= 1)
-                        go = mbar_wait(smem_u32(&sm.s8_empty[st]), (use - 1) & 1, ctx, &sm.abort);
-                    if (go) mbar_arrive_expect_tx(full, TILE * D);
+            for (int i = 0; i < nt && ok; ++i, ++t) {
+                const int st = t % STAGES, use = t / STAGES;
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint32_t full = smem_u32(kv ? &sm.v8_full[st] : &sm.k_full[st]);
+                    const uint32_t empty = smem_u32(kv ? &sm.v8_empty[st] : &sm.k_empty[st]);
+                    const uint32_t dst = smem_u32(kv ? sm.v[st] : sm.k[st]);
+                    bool go = true;
+                    if (lane == 0) {
+                        if (use >= 1) go = mbar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
+                        if (go) mbar_arrive_expect_tx(full, TILE * D);
+                    }
+                    ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
+                    if (!ok) break;
+                    const int s = lane - i * per_tile;
+                    if (s >= 0 && s < per_tile)
+                        tma_load_2d(dst + (uint32_t)s * page_bytes, kv ? tv : tk, full, 0, row);
                 }
-                ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                const int s = lane - (i >> 1) * per_tile;
-                if (s >= 0 && s < per_tile)
-                    tma_load_2d(smem_u32(sm.stage[st]) + (uint32_t)s * page_bytes, i & 1 ? tv : tk,
-                                full, 0, row);
             }
         }
     }
@@ -144,8 +164,10 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     if (lane == 0) {  // copies in flight land before the CTA leaves
         int zero = 0;
-        for (int i = 1; i <= 2 && i <= t; ++i)
-            mbar_wait(smem_u32(&sm.s8_full[(t - i) & 1]), ((t - i) >> 1) & 1, ctx, &zero);
+        for (int i = 1; i <= STAGES && i <= t; ++i) {
+            mbar_wait(smem_u32(&sm.k_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
+            mbar_wait(smem_u32(&sm.v8_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
+        }
     }
 }
 
@@ -212,83 +234,79 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
         if (lane == 0) sm.units.release(i);
         if (begin == end) return;
         for (int j = begin; j < end; ++j, ++t) {
-            const int b = t & 1, use = t >> 1, ss = t % SRING;
+            const int b = t & 1, use = t >> 1, st = t % STAGES, ss = t % SRING;
             const int kpos0 = (t_first + j) * TILE;
             const bool edge = kpos0 < lo || kpos0 + TILE - 1 > hi;
+            if (!mbar_wait(smem_u32(&sm.v8_full[st]), (t / STAGES) & 1, ctx, abort)) return;
+            uint4 x[PER];
 #pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                if (!mbar_wait(smem_u32(&sm.s8_full[kv]), t & 1, ctx, abort)) return;
-                if (use >= 1 && !mbar_wait(smem_u32(kv ? &sm.v_empty[b] : &sm.k_empty[b]),
-                                           (use - 1) & 1, ctx, abort))
-                    return;
-                uint8_t *dst = kv ? sm.v16[b] : sm.k16[b];
-                uint4 x[PER];
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    x[i] = *reinterpret_cast<const uint4 *>(sm.stage[kv] + (i * 128 + tid) * 16);
-                if (kv) {
-                    // values that no row sees may hold anything, NaN codes too, and
-                    // the MMA multiplies them by 0; a zero scale drops the values
-                    if (!mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
-                    if (edge || sm.zero[ss]) {
-#pragma unroll
-                        for (int i = 0; i < PER; ++i) {
-                            const int r = r0 + i * (128 / UR);
-                            if (kpos0 + r < lo || kpos0 + r > hi ||
-                                sm.sc[ss][r >> p.page_shift].w == 0.f)
-                                x[i] = make_uint4(0, 0, 0, 0);
-                        }
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
-                }
+            for (int i = 0; i < PER; ++i)
+                x[i] = *reinterpret_cast<const uint4 *>(sm.v[st] + (i * 128 + tid) * 16);
+            // values that no row sees may hold anything, NaN codes too, and the MMA
+            // multiplies them by 0; a zero scale drops the values
+            if (!mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
+            if (edge || sm.zero[ss]) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
-                                               e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
-                    const uint4 c = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
-                                               e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
-                    uint8_t *row = dst + i * (128 / UR) * 128;
-                    *reinterpret_cast<uint4 *>(row + at0) = sw ? c : a;
-                    *reinterpret_cast<uint4 *>(row + at1) = sw ? a : c;
+                    const int r = r0 + i * (128 / UR);
+                    if (kpos0 + r < lo || kpos0 + r > hi ||
+                        sm.sc[ss][r >> p.page_shift].w == 0.f)
+                        x[i] = make_uint4(0, 0, 0, 0);
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(kv ? &sm.v_full[b] : &sm.k_full[b]));
-                mbar_arrive(smem_u32(&sm.s8_empty[kv]));
             }
+            if (use >= 1 && !mbar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
+            uint8_t *dst = sm.v16[b];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
+                                           e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
+                const uint4 c = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
+                                           e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
+                uint8_t *row = dst + i * (128 / UR) * 128;
+                *reinterpret_cast<uint4 *>(row + at0) = sw ? c : a;
+                *reinterpret_cast<uint4 *>(row + at1) = sw ? a : c;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(&sm.v_full[b]));
+            mbar_arrive(smem_u32(&sm.v8_empty[st]));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
         }
     }
 }
 
 template <int D>
 __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, const DevCtx &ctx) {
-    constexpr uint32_t IDESC_S = idesc_f16_f32(128, TILE, 0), IDESC_O = idesc_f16_f32(128, D, 1);
+    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, TILE, 0, 0);
+    constexpr uint32_t IDESC_O = idesc_f16_f32(128, D, 1);
     constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
     volatile int *abort = &sm.abort;
     if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
-    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0]), 16u, 1024u);
-    const uint64_t dk = smem_desc_sw128(smem_u32(sm.k16[0]), 16u, 1024u);
+    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0][0])), dk = desc_rows<D>(smem_u32(sm.k[0]));
     const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
     auto wait = [&](uint64_t &bar, int phase) {
         return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    auto issue_s = [&](int half, int b) {
-        const uint64_t a = dq + (uint64_t)(half * (BYTES >> 4)), k = dk + (uint64_t)(b * (BYTES >> 4));
+    auto issue_s = [&](int half, int st) {
+        const uint64_t k = dk + (uint64_t)(st * (TILE * D >> 4));
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((uint32_t)(kk >> 2) * HALF + (uint32_t)(kk & 3) * 32u) >> 4;
-            tc_mma_f16(tmem + (uint32_t)half * HALF_COLS, a + off, k + off, IDESC_S, kk > 0);
+        for (int kk = 0; kk < 2 * D / 32; ++kk) {  // hi, then lo
+            const int lo = kk / (D / 32), c = kk % (D / 32);
+            mma_f8(tmem + (uint32_t)half * HALF_COLS,
+                   dq + (uint64_t)((2 * half + lo) * (128 * D >> 4) + 2 * c),
+                   k + (uint64_t)(2 * c), IDESC_S, kk > 0);
         }
         tc_commit(smem_u32(&sm.s_full[half]));
     };
-    auto issue_pv = [&](int half, int b, bool first) {
+    auto issue_pv = [&](int half, int part, int b, bool first) {  // 64 keys
         const uint64_t v = dv + (uint64_t)(b * (BYTES >> 4));
         const uint32_t s = tmem + (uint32_t)half * HALF_COLS;
 #pragma unroll
-        for (int kk = 0; kk < TILE / 16; ++kk)
+        for (int k = 0; k < TILE / 32; ++k) {
+            const int kk = part * (TILE / 32) + k;
             tc_mma_f16_ts(s + O_COL, s + 8u * kk, v + (uint64_t)(kk * (2048u >> 4)), IDESC_O,
                           kk > 0 || !first);
-        tc_commit(smem_u32(&sm.pv_done[half]));
+        }
     };
     int t = 0, pc[2] = {0, 0}, ec[2] = {0, 0};  // tiles; per half: P tiles, units
     bool ok = true;
@@ -299,35 +317,39 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, c
         const bool two = u.nrows > 128;
         sm.units.release(i);
         if (n == 0) break;
-        ok = wait(sm.k_full[t & 1], t >> 1);
+        ok = wait(sm.k_full[t % STAGES], t / STAGES);
         for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
             if (!(ok = wait(sm.q_full[half], ec[half]))) break;
             tc_fence_after();
-            issue_s(half, t & 1);
+            issue_s(half, t % STAGES);
         }
         if (!ok) break;
-        tc_commit(smem_u32(&sm.k_empty[t & 1]));
+        tc_commit(smem_u32(&sm.k_empty[t % STAGES]));
         for (int j = 0; j < n && ok; ++j, ++t) {
-            const int b = t & 1, b1 = b ^ 1;
+            const int b = t & 1, next = (t + 1) % STAGES;
             ok = wait(sm.v_full[b], t >> 1);
             for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
                 // the first P V overwrites the O that the last unit's epilogue reads
                 if (j == 0 && ec[half] >= 1) ok = wait(sm.o_empty[half], ec[half] - 1);
-                ok = ok && wait(sm.p_full[half], pc[half]);
+                ok = ok && wait(sm.p_full[half][0], pc[half]);
                 if (!ok) break;
+                tc_fence_after();
+                issue_pv(half, 0, b, j == 0);
+                if (!(ok = wait(sm.p_full[half][1], pc[half]))) break;
                 ++pc[half];
                 tc_fence_after();
-                issue_pv(half, b, j == 0);
+                issue_pv(half, 1, b, j == 0);
+                tc_commit(smem_u32(&sm.pv_done[half]));
                 if (j + 1 < n) {
-                    if (half == 0 && !(ok = wait(sm.k_full[b1], (t + 1) >> 1))) break;
+                    if (half == 0 && !(ok = wait(sm.k_full[next], (t + 1) / STAGES))) break;
                     tc_fence_after();
-                    issue_s(half, b1);
+                    issue_s(half, next);
                 }
             }
             if (!ok) break;
             tc_commit(smem_u32(&sm.v_empty[b]));
             if (j + 1 < n) {
-                tc_commit(smem_u32(&sm.k_empty[b1]));
+                tc_commit(smem_u32(&sm.k_empty[next]));
             }
         }
         ++ec[0];
@@ -374,7 +396,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         const int hi = p.plan.causal ? pos : u.s.len - 1;
         const int lo = p.plan.wl < 0 ? 0 : pos - p.plan.wl;
         const float sink = p.sinks && in ? __ldg(p.sinks + head) * LOG2E : 0.f;
-        // ---- the row's Q: a power of two times it in f16. The half's Q tile is free:
+        // ---- the row's Q: a power of two times it, split. The half's Q tile is free:
         // this warp has seen the last S that reads it
         float qf;
         {
@@ -392,7 +414,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 for (int e = 0; e < 4; ++e) {
                     const float a = fabsf(__uint_as_float(w[e] << 16));
                     const float b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                    // NaN and inf set no scale
+                    // inf and NaN set no scale
                     amax = max3(amax, a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
                 }
             }
@@ -401,15 +423,28 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             k = amax > 0.f ? max(-120, min(k, 120)) : 0;
             const float up = __uint_as_float((uint32_t)(127 + k) << 23);
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
+            for (int c = 0; c < D / 16; ++c) {
+                const uint32_t w[8] = {v[2 * c].x,     v[2 * c].y,     v[2 * c].z,
+                                       v[2 * c].w,     v[2 * c + 1].x, v[2 * c + 1].y,
+                                       v[2 * c + 1].z, v[2 * c + 1].w};
+                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack_f16x2(__uint_as_float(w[e] << 16) * up,
-                                      __uint_as_float(w[e] & 0xffff0000u) * up);
-                *reinterpret_cast<uint4 *>(sm.q[half] + (c >> 3) * Smem<D>::HALF +
-                                           sw128_offset(r & 127, c & 7)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < 8; ++e) {
+                    const float a = __uint_as_float(w[e] << 16) * up;
+                    const float b = __uint_as_float(w[e] & 0xffff0000u) * up;
+                    uint32_t h = e4m3x2(a, b);
+                    if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
+                    if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
+                    const float2 back = e4m3x2_to_f32(h);
+                    const uint32_t l2 = e4m3x2(a - back.x, b - back.y);
+                    hi[e >> 1] = e & 1 ? hi[e >> 1] | h << 16 : h;
+                    lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+                }
+                const uint32_t at = sw_offset<D>(r & 127, c);
+                *reinterpret_cast<uint4 *>(sm.q[half][0] + at) =
+                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4 *>(sm.q[half][1] + at) =
+                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
             fence_proxy_async_smem();
@@ -421,43 +456,49 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             const int kpos0 = (u.t_first + u.begin + j) * TILE;
             if (!wait(sm.sc_full[ss], t / SRING) || !wait(sm.s_full[half], sc_n)) return;
             tc_fence_after();
-            uint32_t x[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tmem + 32u * c, x[c]);
-            tc_wait_ld();
             const bool mask = kpos0 < u.ilo || kpos0 + TILE - 1 > u.ihi;
             const bool key0 = p.sink_mode == 1 && kpos0 == 0;
-            if (mask) {
-                const int a = lo - kpos0, z = hi - kpos0;  // visible columns a .. z
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
+            // x = S f + log2 v_scale, a page's columns at a time. f is kept above 0 (a
+            // zero key scale makes it 0), since a masked S is -inf. A key-0 sink
+            // joins S itself. The scores are read from TMEM twice, 32 columns at a
+            // time, in loops: held in registers instead (128 of them, all unrolled)
+            // the code of this role outgrew the instruction cache and the MMA
+            // issuer starved: 5900 cycles a tile against XXXX.
+            auto load = [&](int c, uint32_t (&x)[32]) {
+                tmem_ld32(tmem + 32u * c, x);
+                tc_wait_ld();
+                if (mask) {
+                    const int a = lo - kpos0 - 32 * c, z = hi - kpos0 - 32 * c;  // visible: a .. z
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (32 * c + e < a || 32 * c + e > z) x[c][e] = __float_as_uint(-INFINITY);
-            }
-            // x = S f + log2 v_scale, a page's columns at a time. f is kept above 0 (a
-            // zero key scale makes it 0), since a masked S is -inf. With a key-0 sink
-            // x of column 0 is set apart.
-            float top = -INFINITY;
-            float fs[TILE / CW], vs[TILE / CW];
-#pragma unroll
-            for (int c = 0; c < TILE / CW; ++c) {
-                const float4 s = sm.sc[ss][(c * CW) >> p.page_shift];
-                fs[c] = fmaxf(s.x * qf, FLT_MIN);
-                vs[c] = s.y;
-                float mx = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < CW; e += 2) {
-                    const int q = c * CW + e;
-                    mx = max3(mx, __uint_as_float(x[q >> 5][q & 31]),
-                              __uint_as_float(x[q >> 5][(q & 31) + 1]));
+                        if (e < a || e > z) x[e] = __float_as_uint(-INFINITY);
                 }
-                top = fmaxf(top, fmaf(mx, fs[c], vs[c]));
-            }
-            float x0 = 0.f;
-            if (key0) {
-                x0 = fmaf(__uint_as_float(x[0][0]), fs[0], vs[0]) + sink;
-                top = fmaxf(top, x0);
+            };
+            auto scales = [&](int col) {
+                float4 s = sm.sc[ss][col >> p.page_shift];
+                s.x = fmaxf(s.x * qf, FLT_MIN);
+                return s;
+            };
+            auto add_sink = [&](uint32_t (&x)[32], float f) {
+                x[0] = __float_as_uint(__uint_as_float(x[0]) + sink / f);
+            };
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32];
+                load(c, x);
+#pragma unroll
+                for (int w = 0; w < 32; w += CW) {
+                    const float4 s = scales(32 * c + w);
+                    if (w == 0 && key0 && c == 0) add_sink(x, s.x);
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int e = w; e < w + CW; e += 4) {
+                        mx[0] = max3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                        mx[1] = max3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                    }
+                    top = fmaxf(top, fmaf(fmaxf(mx[0], mx[1]), s.x, s.y));
+                }
             }
             const bool move = top > m + TAU;
             float alpha = 1.f;
@@ -480,40 +521,42 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                     tmem_st32(tmem + O_COL + 32u * c, o);
                 }
             }
-            uint32_t pw[2][32];
+            // P of 32 keys takes the columns 16 c .., S's own that were read before
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32], pw[16];
+                load(c, x);
 #pragma unroll
-            for (int c = 0; c < TILE / CW; ++c) {
-                const float4 s = sm.sc[ss][(c * CW) >> p.page_shift];
-                const float f = fs[c], off = vs[c] + (BASE - m);
-                const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
-                uint64_t sum = f2_pack(0.f, 0.f);
+                for (int w = 0; w < 32; w += CW) {
+                    const float4 s = scales(32 * c + w);
+                    if (w == 0 && key0 && c == 0) add_sink(x, s.x);
+                    const float off = s.y + (BASE - m);
+                    const uint64_t f2 = f2_pack(s.x, s.x), off2 = f2_pack(off, off);
+                    uint64_t sum = f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < CW; e += 2) {
-                    const int q = c * CW + e;
+                    for (int e = w; e < w + CW; e += 2) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                         f2, off2),
+                                  a, b);
+                        a = ex2(a);
+                        b = ex2(b);
+                        sum = f2_add(sum, f2_pack(a, b));
+                        pw[e >> 1] = pack_f16x2(a, b);
+                    }
                     float a, b;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[q >> 5][q & 31]),
-                                             __uint_as_float(x[q >> 5][(q & 31) + 1])),
-                                     f2, off2),
-                              a, b);
-                    a = ex2(a);
-                    b = ex2(b);
-                    if (q == 0 && key0) a = ex2(x0 + (BASE - m));
-                    sum = f2_add(sum, f2_pack(a, b));
-                    pw[q >> 6][(q & 63) >> 1] = pack_f16x2(a, b);
+                    f2_unpack(sum, a, b);
+                    l = fmaf(a + b, s.z, l);
                 }
-                float a, b;
-                f2_unpack(sum, a, b);
-                l = fmaf(a + b, s.z, l);
+                tmem_st16(tmem + 16u * c, pw);
+                if (c & 1) {  // 64 keys more
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][c >> 1]));
+                }
             }
-            tmem_st32(tmem, pw[0]);
-            tmem_st32(tmem + 32u, pw[1]);
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&sm.p_full[half]));
-                mbar_arrive(smem_u32(&sm.sc_empty[ss]));
-            }
+            if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
         }
         t0 += n;
         // ---- epilogue
@@ -529,14 +572,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             if (part) {
                 reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot] = lse2;
             } else {
-                if (p.sink_mode == 2) {  // the null logit joins the denominator
-                    const float mt = fmaxf(lse2, sink);
-                    if (mt != -INFINITY) {
-                        const float all = mt + log2f(ex2(lse2 - mt) + ex2(sink - mt));
-                        inv *= ex2(lse2 - all);
-                        lse2 = lse2 != lse2 ? lse2 : all;
-                    }
-                }
+                if (p.sink_mode == 2) with_null_sink(sink, lse2, inv);
                 if (p.lse) p.lse[orow] = lse2 * LN2;
             }
         }
@@ -586,16 +622,19 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
         return;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.s8_full[i]), 1);
-            mbar_init(smem_u32(&sm.s8_empty[i]), 128);
-            mbar_init(smem_u32(&sm.k_full[i]), 128);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&sm.k_full[i]), 1);
             mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v8_full[i]), 1);
+            mbar_init(smem_u32(&sm.v8_empty[i]), 128);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.v_full[i]), 128);
             mbar_init(smem_u32(&sm.v_empty[i]), 1);
             mbar_init(smem_u32(&sm.q_full[i]), 128);
             mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.p_full[i]), 4);
+            mbar_init(smem_u32(&sm.p_full[i][0]), 4);
+            mbar_init(smem_u32(&sm.p_full[i][1]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
             mbar_init(smem_u32(&sm.o_empty[i]), 4);
         }
@@ -617,22 +656,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 56 + 256 x 200 = the 512 x 128 of the launch
-    if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-        if (warp == 0) {
-            load_tiles<D>(p, &tk, &tv, sm, ctx);
-        } else if (warp == 1) {
-            if (lane == 0) issue_mmas<D>(p, sm, tmem, ctx);
-            __syncwarp();
-        } else if (warp == 2) {
-            load_scales<D>(p, sm, ctx);
-        } else if (warp >= 4) {
-            widen<D>(p, sm, ctx);
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (warp == 0) {
+        load_tiles<D>(p, &tk, &tv, sm, ctx);
+    } else if (warp == 1) {
+        if (lane == 0) issue_mmas<D>(p, sm, tmem, ctx);
+        __syncwarp();
+    } else if (warp == 2) {
+        load_scales<D>(p, sm, ctx);
+    } else if (warp >= 8) {
         softmax<D, CW>(p, sm, tmem, ctx);
+    } else if (warp >= 4) {
+        widen<D>(p, sm, ctx);
     }
     tc_fence_before();
     __syncthreads();
@@ -645,7 +679,8 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
 template <int D, int CW>
 cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     CUtensorMap tk, tv;
-    if (!map_cache(&tk, a.k_cache, a, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+    if (!map_cache(&tk, a.k_cache, a,
+                   D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) ||
         !map_cache(&tv, a.v_cache, a, CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     const size_t smem = sizeof(Smem<D>);
