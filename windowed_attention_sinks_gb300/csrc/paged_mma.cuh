@@ -41,6 +41,16 @@ template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint3
     const uint32_t a = r * W + (u << 4);
     return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
 }
+// x = keep ? x : -inf. Volatile so that it stays behind the branch it is written in:
+// the compiler otherwise turns a branch around many selections into selections that
+// every tile pays for (3 ALU operations a score where whole tiles need none).
+__device__ __forceinline__ void hide_unless(uint32_t &x, bool keep) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tselp.b32 %0, %0, 0xff800000, p;\n\t}"
+        : "+r"(x)
+        : "r"((uint32_t)keep));
+}
+
 // The null logit joins a row's denominator.
 __device__ __forceinline__ void with_null_sink(float sink, float &lse2, float &inv) {
     const float top = fmaxf(lse2, sink);

@@ -59,6 +59,13 @@ template <int ROWS> struct Unit {
     int begin, end;        // the tiles of this piece, 0 .. ntiles
     int c0, parts;         // of a cut unit: its first piece, and how many
 
+    // The same piece in halves of tiles, less the halves that no row sees.
+    __device__ __forceinline__ int sub_begin() const {
+        return 2 * begin + (begin == 0 && (lo & (TILE - 1)) >= TILE / 2 ? 1 : 0);
+    }
+    __device__ __forceinline__ int sub_end() const {
+        return 2 * end - (end == ntiles && (hi & (TILE - 1)) < TILE / 2 ? 1 : 0);
+    }
     __device__ __forceinline__ int pos(const PlanArgs &p, int row) const {
         return s.len - s.n + p.token(row);
     }

@@ -16,21 +16,26 @@
 //    relative down to 2^-21 of the largest weight and at most 2^-32 of it below.
 // S, O and the row sums are fp32.
 //
-//   S [128 x 128] into TMEM, a half each
+// The keys are taken 64 at a time:
+//   S [128 x 64] of a half into TMEM, one of two buffers
 //   x = S * (scale log2(e) * k_scale) + log2(v_scale): the value's scale goes
 //       into the exponent, so V's codes need none; the row sum divides it out.
 //       Both are one number for a page, that is for 16 columns or more
-//   P = 2^(7 + x - m), f16, over S's own columns, 64 keys at a time so that
-//       the first half's P V runs beside the second half's exponentials
-// m moves only when a tile raises it by more than 2^8 (O is then rescaled).
-// TMEM: S / P 2 x 128 columns, O 2 x D: all 512 for D = 128, hence the shared
-// columns of S and P. The MMAs of one CTA run in the order of issue, so S of
-// the next tile may follow the P V that reads its columns.
+//   P = 2^(7 + x - m), f16, over the first columns of S's own buffer
+//   O += P V, P from TMEM
+// m is what it was unless a row exceeds it by more than 2^8, so P is computed
+// on trust in the one pass over S that also finds the maximum; where that was
+// wrong (O is then rescaled) the pass is repeated. TMEM: S / P 2 x 2 x 64
+// columns, O 2 x D: all 512 for D = 128, hence the shared columns of S and P.
+// The MMAs of one CTA run in the order of issue, so S of two steps ahead may
+// follow the P V that reads its columns.
 //
 // One persistent CTA per SM over an equal piece of the tiles (paged_plan.cuh):
 //   warp 0       the units; TMA: tiles of K and V, two rings of STAGES
-//   warp 1       MMA issuer: PV(A, t), S(A, t + 1), PV(B, t), S(B, t + 1), ..., so
-//                that one half's softmax runs beside the other half's MMAs
+//   warps 1, 3   MMA issuers of the halves: PV(k), S(k + 2), PV(k + 1), ...: the
+//                softmax finds its next S ready. (One MMA takes its thread about 65
+//                cycles to issue, about what the tensor core needs for it, so
+//                one thread for both halves would bound the kernel.)
 //   warp 2       the pages' scales
 //   warps 4-7    widening: V's codes to f16 tiles (two buffers)
 //   warps 8-11, 12-15   Q, softmax and epilogue of the halves, a thread a row
@@ -85,24 +90,16 @@ template <int D> struct alignas(1024) Smem {
     uint64_t k_full[STAGES], k_empty[STAGES], v8_full[STAGES], v8_empty[STAGES];
     uint64_t v_full[2], v_empty[2];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full[2], s_full[2], p_full[2][2], pv_done[2], o_empty[2], drain;
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_empty[2], drain[2];
     uint32_t tmem_base;
     int abort;
 };
 constexpr uint32_t TMEM_COLS = 512, HALF_COLS = 256, O_COL = 128;
+constexpr int SUB = 64;  // keys a step
 
 // kind::f16, f16 operands, fp32 accumulate; b_mn: B is stored with N contiguous.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn) {
     return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15])
-        : "memory");
 }
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -275,89 +272,89 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
     }
 }
 
+// The MMAs of one half.
 template <int D>
-__device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, const DevCtx &ctx) {
-    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, TILE, 0, 0);
+__device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, int half,
+                           const DevCtx &ctx) {
+    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, SUB, 0, 0);
     constexpr uint32_t IDESC_O = idesc_f16_f32(128, D, 1);
     constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
     volatile int *abort = &sm.abort;
-    if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
-    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0][0])), dk = desc_rows<D>(smem_u32(sm.k[0]));
+    if (ctx.stall) mbar_wait(smem_u32(&sm.drain[half]), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[half][0])), dk = desc_rows<D>(smem_u32(sm.k[0]));
     const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
+    const uint32_t cols = tmem + (uint32_t)half * HALF_COLS;
     auto wait = [&](uint64_t &bar, int phase) {
         return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    auto issue_s = [&](int half, int st) {
-        const uint64_t k = dk + (uint64_t)(st * (TILE * D >> 4));
-#pragma unroll
-        for (int kk = 0; kk < 2 * D / 32; ++kk) {  // hi, then lo
-            const int lo = kk / (D / 32), c = kk % (D / 32);
-            mma_f8(tmem + (uint32_t)half * HALF_COLS,
-                   dq + (uint64_t)((2 * half + lo) * (128 * D >> 4) + 2 * c),
-                   k + (uint64_t)(2 * c), IDESC_S, kk > 0);
-        }
-        tc_commit(smem_u32(&sm.s_full[half]));
-    };
-    auto issue_pv = [&](int half, int part, int b, bool first) {  // 64 keys
-        const uint64_t v = dv + (uint64_t)(b * (BYTES >> 4));
-        const uint32_t s = tmem + (uint32_t)half * HALF_COLS;
-#pragma unroll
-        for (int k = 0; k < TILE / 32; ++k) {
-            const int kk = part * (TILE / 32) + k;
-            tc_mma_f16_ts(s + O_COL, s + 8u * kk, v + (uint64_t)(kk * (2048u >> 4)), IDESC_O,
-                          kk > 0 || !first);
-        }
-    };
-    int t = 0, pc[2] = {0, 0}, ec[2] = {0, 0};  // tiles; per half: P tiles, units
+    int sc = 0, pc = 0, ec = 0;  // S, P V and units issued
+    int t0 = 0;                  // tiles before the unit's
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = sm.units.wait(i, ctx, abort))) break;
         const Unit<ROWS> &u = sm.units.u[i % UNITS];
-        const int n = u.end - u.begin;
-        const bool two = u.nrows > 128;
+        const int n = u.end - u.begin, s0 = u.sub_begin() - 2 * u.begin,
+                  s1 = u.sub_end() - 2 * u.begin;
+        const bool none = half && u.nrows <= 128;
         sm.units.release(i);
         if (n == 0) break;
-        ok = wait(sm.k_full[t % STAGES], t / STAGES);
-        for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
-            if (!(ok = wait(sm.q_full[half], ec[half]))) break;
-            tc_fence_after();
-            issue_s(half, t % STAGES);
+        if (none) {  // no rows in this half: its share in freeing the stages
+            for (int t = t0; t < t0 + n && ok; ++t) {
+                ok = wait(sm.k_full[t % STAGES], t / STAGES) && wait(sm.v_full[t & 1], t >> 1);
+                mbar_arrive(smem_u32(&sm.k_empty[t % STAGES]));
+                mbar_arrive(smem_u32(&sm.v_empty[t & 1]));
+            }
+            t0 += n;
+            continue;
         }
-        if (!ok) break;
-        tc_commit(smem_u32(&sm.k_empty[t % STAGES]));
-        for (int j = 0; j < n && ok; ++j, ++t) {
-            const int b = t & 1, next = (t + 1) % STAGES;
-            ok = wait(sm.v_full[b], t >> 1);
-            for (int half = 0; half < (two ? 2 : 1) && ok; ++half) {
+        auto issue_s = [&](int k) -> bool {
+            const int tile = t0 + (k >> 1), st = tile % STAGES;
+            if ((k == s0 || !(k & 1)) && !wait(sm.k_full[st], tile / STAGES)) return false;
+            tc_fence_after();
+            const uint64_t kd = dk + (uint64_t)(st * (TILE * D >> 4) + (k & 1) * (SUB * D >> 4));
+            const uint32_t s = cols + (uint32_t)((sc & 1) * SUB);
+#pragma unroll
+            for (int kk = 0; kk < 2 * D / 32; ++kk) {  // hi, then lo
+                const int lo = kk / (D / 32), c = kk % (D / 32);
+                mma_f8(s, dq + (uint64_t)(lo * (128 * D >> 4) + 2 * c), kd + (uint64_t)(2 * c),
+                       IDESC_S, kk > 0);
+            }
+            tc_commit(smem_u32(&sm.s_full[half][sc & 1]));
+            if ((k & 1) || k == s1 - 1) tc_commit(smem_u32(&sm.k_empty[st]));
+            ++sc;
+            return true;
+        };
+        ok = wait(sm.q_full[half], ec);
+        // step k of the loop: S of step k, then P V of step k - 2
+#pragma unroll 1
+        for (int k = s0; k < s1 + 2 && ok; ++k) {
+            if (k - 2 >= s0) {
+                const int kp = k - 2, tile = t0 + (kp >> 1), b = tile & 1;
+                if (kp == s0 || !(kp & 1)) ok = wait(sm.v_full[b], tile >> 1);
                 // the first P V overwrites the O that the last unit's epilogue reads
-                if (j == 0 && ec[half] >= 1) ok = wait(sm.o_empty[half], ec[half] - 1);
-                ok = ok && wait(sm.p_full[half][0], pc[half]);
+                if (kp == s0 && ec >= 1) ok = ok && wait(sm.o_empty[half], ec - 1);
+                ok = ok && wait(sm.p_full[half][pc & 1], pc >> 1);
                 if (!ok) break;
                 tc_fence_after();
-                issue_pv(half, 0, b, j == 0);
-                if (!(ok = wait(sm.p_full[half][1], pc[half]))) break;
-                ++pc[half];
-                tc_fence_after();
-                issue_pv(half, 1, b, j == 0);
+                const uint64_t vd =
+                    dv + (uint64_t)(b * (BYTES >> 4) + (kp & 1) * (SUB / 16 * 2048u >> 4));
+                const uint32_t pt = cols + (uint32_t)((pc & 1) * SUB);
+#pragma unroll
+                for (int kk = 0; kk < SUB / 16; ++kk)
+                    tc_mma_f16_ts(cols + O_COL, pt + 8u * kk, vd + (uint64_t)(kk * (2048u >> 4)),
+                                  IDESC_O, kk > 0 || kp > s0);
                 tc_commit(smem_u32(&sm.pv_done[half]));
-                if (j + 1 < n) {
-                    if (half == 0 && !(ok = wait(sm.k_full[next], (t + 1) / STAGES))) break;
-                    tc_fence_after();
-                    issue_s(half, next);
-                }
+                if ((kp & 1) || kp == s1 - 1) tc_commit(smem_u32(&sm.v_empty[b]));
+                ++pc;
             }
-            if (!ok) break;
-            tc_commit(smem_u32(&sm.v_empty[b]));
-            if (j + 1 < n) {
-                tc_commit(smem_u32(&sm.k_empty[next]));
-            }
+            if (k < s1) ok = issue_s(k);
         }
-        ++ec[0];
-        if (two) ++ec[1];
+        t0 += n;
+        ++ec;
     }
-    tc_commit(smem_u32(&sm.drain));  // every MMA is done before TMEM goes
+    tc_commit(smem_u32(&sm.drain[half]));  // every MMA is done before TMEM goes
     int zero = 0;
-    mbar_wait(smem_u32(&sm.drain), 0, ctx, &zero);
+    mbar_wait(smem_u32(&sm.drain[half]), 0, ctx, &zero);
 }
 
 template <int D, int CW>  // CW: columns that share a page's scales (16 or 32)
@@ -372,7 +369,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
-    int t0 = 0, sc_n = 0;  // CTA's tiles; this half's tiles
+    int t0 = 0, done = 0;  // CTA's tiles; this half's steps
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const Unit<ROWS> &u = sm.units.u[i % UNITS];
@@ -451,116 +448,107 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             mbar_arrive(smem_u32(&sm.q_full[half]));
         }
         float m = NOTHING, l = 0.f;
-        for (int j = 0; j < n; ++j, ++sc_n) {
-            const int t = t0 + j, ss = t % SRING;
-            const int kpos0 = (u.t_first + u.begin + j) * TILE;
-            if (!wait(sm.sc_full[ss], t / SRING) || !wait(sm.s_full[half], sc_n)) return;
+        const int s0 = u.sub_begin(), s1 = u.sub_end();
+#pragma unroll 1
+        for (int k = s0; k < s1; ++k, ++done) {
+            const int t = t0 + (k >> 1) - u.begin, ss = t % SRING;
+            const int kpos0 = u.t_first * TILE + k * SUB, in_tile = (k & 1) * SUB;
+            const uint32_t s_tmem = tmem + (uint32_t)((done & 1) * SUB);
+            if (k == s0 || !(k & 1))
+                if (!wait(sm.sc_full[ss], t / SRING)) return;
+            if (!wait(sm.s_full[half][done & 1], done >> 1)) return;
             tc_fence_after();
-            const bool mask = kpos0 < u.ilo || kpos0 + TILE - 1 > u.ihi;
+            const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
             const bool key0 = p.sink_mode == 1 && kpos0 == 0;
-            // x = S f + log2 v_scale, a page's columns at a time. f is kept above 0 (a
-            // zero key scale makes it 0), since a masked S is -inf. A key-0 sink
-            // joins S itself. The scores are read from TMEM twice, 32 columns at a
-            // time, in loops: held in registers instead (128 of them, all unrolled)
-            // the code of this role outgrew the instruction cache and the MMA
-            // issuer starved: 5900 cycles a tile against XXXX.
-            auto load = [&](int c, uint32_t (&x)[32]) {
-                tmem_ld32(tmem + 32u * c, x);
+            uint32_t pw[32];
+            float sum, top;
+#pragma unroll 1
+            for (;;) {
+                // P of the row's 64 keys with m as it is, their sum and the largest x - m
+                // (of a row without keys so far: x)
+                const float base = m == NOTHING ? BASE : BASE - m;
+                uint32_t xs[2][32];
+                tmem_ld32(s_tmem, xs[0]);
+                tmem_ld32(s_tmem + 32u, xs[1]);
                 tc_wait_ld();
                 if (mask) {
-                    const int a = lo - kpos0 - 32 * c, z = hi - kpos0 - 32 * c;  // visible: a .. z
+                    // bit e: the row sees key e
+                    const int a = max(0, lo - kpos0), z = min(SUB - 1, hi - kpos0);
+                    const uint64_t seen = a > z ? 0 : (~0ull >> (SUB - 1 - z)) & (~0ull << a);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (e < a || e > z) x[e] = __float_as_uint(-INFINITY);
+                    for (int e = 0; e < SUB; ++e)
+                        hide_unless(xs[e >> 5][e & 31],
+                                    (uint32_t)(seen >> (e & 32)) & (1u << (e & 31)));
                 }
-            };
-            auto scales = [&](int col) {
-                float4 s = sm.sc[ss][col >> p.page_shift];
-                s.x = fmaxf(s.x * qf, FLT_MIN);
-                return s;
-            };
-            auto add_sink = [&](uint32_t (&x)[32], float f) {
-                x[0] = __float_as_uint(__uint_as_float(x[0]) + sink / f);
-            };
-            float top = -INFINITY;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                load(c, x);
+                top = -INFINITY;
+                sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < 32; w += CW) {
-                    const float4 s = scales(32 * c + w);
-                    if (w == 0 && key0 && c == 0) add_sink(x, s.x);
-                    float mx[2] = {-INFINITY, -INFINITY};
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t(&x)[32] = xs[c];
 #pragma unroll
-                    for (int e = w; e < w + CW; e += 4) {
-                        mx[0] = max3(mx[0], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                        mx[1] = max3(mx[1], __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
-                    }
-                    top = fmaxf(top, fmaf(fmaxf(mx[0], mx[1]), s.x, s.y));
-                }
-            }
-            const bool move = top > m + TAU;
-            float alpha = 1.f;
-            if (move) {
-                alpha = ex2(m - top);
-                l *= alpha;
-                m = top;
-            }
-            if (j > 0 && __any_sync(0xffffffffu, move)) {
-                if (!wait(sm.pv_done[half], sc_n - 1)) return;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(tmem + O_COL + 32u * c, o);
-                    tc_wait_ld();
+                    for (int w = 0; w < 32; w += CW) {
+                        const float4 s = sm.sc[ss][(in_tile + 32 * c + w) >> p.page_shift];
+                        // above 0 (a zero key scale makes it 0): a masked S is -inf
+                        const float f = fmaxf(s.x * qf, FLT_MIN), off = s.y + base;
+                        const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
+                        uint64_t part = f2_pack(0.f, 0.f);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tmem_st32(tmem + O_COL + 32u * c, o);
-                }
-            }
-            // P of 32 keys takes the columns 16 c .., S's own that were read before
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32], pw[16];
-                load(c, x);
-#pragma unroll
-                for (int w = 0; w < 32; w += CW) {
-                    const float4 s = scales(32 * c + w);
-                    if (w == 0 && key0 && c == 0) add_sink(x, s.x);
-                    const float off = s.y + (BASE - m);
-                    const uint64_t f2 = f2_pack(s.x, s.x), off2 = f2_pack(off, off);
-                    uint64_t sum = f2_pack(0.f, 0.f);
-#pragma unroll
-                    for (int e = w; e < w + CW; e += 2) {
+                        for (int e = w; e < w + CW; e += 2) {
+                            float a, b;
+                            f2_unpack(
+                                f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
+                                       f2, off2),
+                                a, b);
+                            if (c == 0 && e == 0 && key0) a += sink;
+                            top = max3(top, a, b);
+                            a = ex2(a);
+                            b = ex2(b);
+                            part = f2_add(part, f2_pack(a, b));
+                            pw[16 * c + (e >> 1)] = pack_f16x2(a, b);
+                        }
                         float a, b;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                         f2, off2),
-                                  a, b);
-                        a = ex2(a);
-                        b = ex2(b);
-                        sum = f2_add(sum, f2_pack(a, b));
-                        pw[e >> 1] = pack_f16x2(a, b);
+                        f2_unpack(part, a, b);
+                        sum = fmaf(a + b, s.z, sum);
                     }
-                    float a, b;
-                    f2_unpack(sum, a, b);
-                    l = fmaf(a + b, s.z, l);
                 }
-                tmem_st16(tmem + 16u * c, pw);
-                if (c & 1) {  // 64 keys more
-                    tc_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][c >> 1]));
+                top -= BASE;
+                const bool move = m == NOTHING ? top > NOTHING : top > TAU;
+                if (!__any_sync(0xffffffffu, move)) break;
+                const float mn = !move ? m : m == NOTHING ? top : m + top;
+                const float alpha = move ? ex2(m - mn) : 1.f;
+                m = mn;
+                l *= alpha;
+                if (k > s0) {
+                    if (!wait(sm.pv_done[half], done - 1)) return;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(tmem + O_COL + 32u * c, o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tmem_st32(tmem + O_COL + 32u * c, o);
+                    }
                 }
             }
-            if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+            l += sum;
+            // one P V at a time may be outstanding, or the parity that the waits for
+            // it go by would be ambiguous (it is done by now as a rule)
+            if (done >= 1 && !wait(sm.pv_done[half], done - 1)) return;
+            tmem_st32(s_tmem, pw);
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.p_full[half][done & 1]));
+                if ((k & 1) || k == s1 - 1) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+            }
         }
         t0 += n;
         // ---- epilogue
-        if (!wait(sm.pv_done[half], sc_n - 1)) return;
+        if (!wait(sm.pv_done[half], done - 1)) return;
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
         float lse2 = l == 0.f ? -INFINITY : m - BASE + log2f(l);
@@ -624,15 +612,17 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 1);
-            mbar_init(smem_u32(&sm.k_empty[i]), 1);
+            mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both halves' MMAs
             mbar_init(smem_u32(&sm.v8_full[i]), 1);
             mbar_init(smem_u32(&sm.v8_empty[i]), 128);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.v_full[i]), 128);
-            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            mbar_init(smem_u32(&sm.v_empty[i]), 2);
+            mbar_init(smem_u32(&sm.drain[i]), 1);
             mbar_init(smem_u32(&sm.q_full[i]), 128);
-            mbar_init(smem_u32(&sm.s_full[i]), 1);
+            mbar_init(smem_u32(&sm.s_full[i][0]), 1);
+            mbar_init(smem_u32(&sm.s_full[i][1]), 1);
             mbar_init(smem_u32(&sm.p_full[i][0]), 4);
             mbar_init(smem_u32(&sm.p_full[i][1]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
@@ -642,8 +632,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
         }
-        mbar_init(smem_u32(&sm.drain), 1);
-        sm.units.init(1 + 1 + 4 + 8);  // MMA issuer, scales, widening, softmax
+        sm.units.init(2 + 1 + 4 + 8);  // MMA issuers, scales, widening, softmax
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -656,17 +645,22 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    if (warp == 0) {
-        load_tiles<D>(p, &tk, &tv, sm, ctx);
-    } else if (warp == 1) {
-        if (lane == 0) issue_mmas<D>(p, sm, tmem, ctx);
-        __syncwarp();
-    } else if (warp == 2) {
-        load_scales<D>(p, sm, ctx);
-    } else if (warp >= 8) {
+    // registers: 256 threads x 96 + 256 x 160 = the 512 x 128 of the launch
+    if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        if (warp == 0) {
+            load_tiles<D>(p, &tk, &tv, sm, ctx);
+        } else if (warp == 2) {
+            load_scales<D>(p, sm, ctx);
+        } else if (warp < 4) {
+            if (lane == 0) issue_mmas<D>(p, sm, tmem, warp >> 1, ctx);
+            __syncwarp();
+        } else {
+            widen<D>(p, sm, ctx);
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         softmax<D, CW>(p, sm, tmem, ctx);
-    } else if (warp >= 4) {
-        widen<D>(p, sm, ctx);
     }
     tc_fence_before();
     __syncthreads();
