@@ -89,7 +89,8 @@ template <int D, int R> struct alignas(1024) Smem {
     uint8_t p[2][C::N * TILE];
     float4 sc[SRING][8];        // page's k scale, log2 v scale, 1 / v scale, v scale > 0
     float wmax[2][4][R];        // column maxima of the warps
-    float mx[2][2][R];          // unit parity, group: running maxima
+    alignas(16) float mx[2][2][R];  // unit parity, group: running maxima
+    float alpha[2][R];          // what a move of them multiplies l and O by
     float lx[2][2][4][R];       // and the warps' row sums
     long long orow[2][R];       // output row of each query row, -1 past the last
     int rpos[2][R];             // its position
@@ -269,25 +270,36 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         if (lane == 0) sm.units.release(n);
         if (u.begin == u.end) break;
         const int w = n & 1;
-        uint4 x[PER];
-        float amax = 0.f;
+        // four items a lane in registers at a time; with more rows they are read
+        // again for the second pass (from L1)
+        constexpr int B = PER < 4 ? PER : 4;
+        uint4 x[B];
+        auto load = [&](int i0) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (r < u.nrows) {
+            for (int i = 0; i < B; ++i) {
+                const int r = ((i0 + i) * 32 + lane) / CH, c = ((i0 + i) * 32 + lane) % CH;
                 const int row = u.row0 + r, tok = p.plan.token(row);
-                x[i] = __ldg(reinterpret_cast<const uint4 *>(
-                    p.q + (size_t)(u.s.t0 + tok) * p.q_stride +
-                    (size_t)(u.h * G + row - tok * G) * D + 8 * c));
+                x[i] = make_uint4(0, 0, 0, 0);
+                if (r < u.nrows)
+                    x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                        p.q + (size_t)(u.s.t0 + tok) * p.q_stride +
+                        (size_t)(u.h * G + row - tok * G) * D + 8 * c));
             }
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        };
+        float amax = 0.f;
+#pragma unroll 1
+        for (int i0 = 0; i0 < PER; i0 += B) {
+            load(i0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = fabsf(__uint_as_float(v[e] << 16));
-                const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
-                if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
-                if (b < INFINITY) amax = fmaxf(amax, b);
+            for (int i = 0; i < B; ++i) {
+                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float a = fabsf(__uint_as_float(v[e] << 16));
+                    const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
+                    if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
+                    if (b < INFINITY) amax = fmaxf(amax, b);
+                }
             }
         }
         amax = warp_max(amax);
@@ -299,27 +311,31 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
             ok = mbar_wait(smem_u32(&sm.q_empty[w]), ((n >> 1) - 1) & 1, ctx, &sm.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+#pragma unroll 1
+        for (int i0 = 0; i0 < PER; i0 += B) {
+            if (PER > B) load(i0);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
+            for (int i = 0; i < B; ++i) {
+                const int r = ((i0 + i) * 32 + lane) / CH, c = ((i0 + i) * 32 + lane) % CH;
+                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float a = __uint_as_float(v[e] << 16) * up;
-                const float b = __uint_as_float(v[e] & 0xffff0000u) * up;
-                uint32_t h = e4m3x2(a, b);
-                if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
-                if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
-                const float2 back = e4m3x2_to_f32(h);
-                hi[e >> 1] |= h << (16 * (e & 1));
-                lo[e >> 1] |= e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f) << (16 * (e & 1));
+                for (int e = 0; e < 4; ++e) {
+                    const float a = __uint_as_float(v[e] << 16) * up;
+                    const float b = __uint_as_float(v[e] & 0xffff0000u) * up;
+                    uint32_t h = e4m3x2(a, b);
+                    if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
+                    if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
+                    const float2 back = e4m3x2_to_f32(h);
+                    hi[e >> 1] |= h << (16 * (e & 1));
+                    lo[e >> 1] |= e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f) << (16 * (e & 1));
+                }
+                // 8 bytes: half of the 16-byte unit c / 2
+                *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(r, c >> 1) + 8 * (c & 1)) =
+                    make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(R + r, c >> 1) + 8 * (c & 1)) =
+                    make_uint2(lo[0], lo[1]);
             }
-            // 8 bytes: half of the 16-byte unit c / 2
-            *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(r, c >> 1) + 8 * (c & 1)) =
-                make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(R + r, c >> 1) + 8 * (c & 1)) =
-                make_uint2(lo[0], lo[1]);
         }
         for (int r = lane; r < R; r += 32) {
             const int row = u.row0 + r, tok = p.plan.token(row), head = u.h * G + row - tok * G;
@@ -509,16 +525,21 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
     int t0 = 0;  // first tile of the unit
     for (int i = 0;; ++i) {
         // all eight warps go on, or none
+        const int w = i & 1;
+        if (key < R) sm.mx[w][g][key] = NOTHING;
         ok = ok && sm.units.wait(i, ctx, abort);
         if (sync_any<256>(bar_all, !ok)) break;
         const Unit<R> &u = sm.units.u[i % UNITS];
-        const int w = i & 1, n = u.end - u.begin;
+        const int n = u.end - u.begin;
         if (n == 0) break;
         wait(sm.q_full[w], i >> 1);
         const float qf = sm.qf[w];
-        float m[R], l[R];
+        // m is the group's and lies in shared memory: 32 rows of it would not fit
+        // beside the scores and sums in registers
+        const float4 *m4 = reinterpret_cast<const float4 *>(sm.mx[w][g]);
+        float l[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) m[r] = NOTHING, l[r] = 0.f;
+        for (int r = 0; r < R; ++r) l[r] = 0.f;
         const int j0 = (g ^ t0) & 1;  // the group's first tile of the unit
         for (int j = j0; j < n; j += 2) {
             const int t = t0 + j, sb = t % C::SBUF, ss = t % SRING;
@@ -566,7 +587,9 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     const int pos = sm.rpos[w][r];
                     const bool in = kpos <= (p.plan.causal ? pos : u.hi) &&
                                     (p.plan.wl < 0 || kpos >= pos - p.plan.wl);
-                    if (!in) x[r] = -INFINITY;
+                    uint32_t b = __float_as_uint(x[r]);
+                    hide_unless(b, in);
+                    x[r] = __uint_as_float(b);
                 }
                 // values that no row sees may hold anything, NaN codes too: the MMA
                 // multiplies them by 0, so they are cleared
@@ -583,7 +606,10 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             }
             float top = -INFINITY;
 #pragma unroll
-            for (int r = 0; r < R; ++r) top = fmaxf(top, x[r] - m[r]);
+            for (int r = 0; r < R; r += 4) {
+                const float4 m = m4[r / 4];
+                top = max3(max3(top, x[r] - m.x, x[r + 1] - m.y), x[r + 2] - m.z, x[r + 3] - m.w);
+            }
             const bool move = sync_any<128>(bar_g, top > LIMIT - BASE);
             if (move) {
 #pragma unroll
@@ -592,27 +618,27 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     if (lane == 0) sm.wmax[g][quarter][r] = c;
                 }
                 named_sync(bar_g, 128);
-                float alpha[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const float c = fmaxf(fmaxf(sm.wmax[g][0][r], sm.wmax[g][1][r]),
-                                          fmaxf(sm.wmax[g][2][r], sm.wmax[g][3][r]));
-                    const float mn = fmaxf(m[r], c);
-                    alpha[r] = ex2(m[r] - mn);
-                    l[r] *= alpha[r];
-                    m[r] = mn;
+                if (key < R) {
+                    const float c = fmaxf(fmaxf(sm.wmax[g][0][key], sm.wmax[g][1][key]),
+                                          fmaxf(sm.wmax[g][2][key], sm.wmax[g][3][key]));
+                    const float m = sm.mx[w][g][key], mn = fmaxf(m, c);
+                    sm.alpha[g][key] = ex2(m - mn);
+                    sm.mx[w][g][key] = mn;
                 }
+                named_sync(bar_g, 128);
+#pragma unroll
+                for (int r = 0; r < R; ++r) l[r] *= sm.alpha[g][r];
                 if (j > j0) {
                     wait(sm.pv_done[g], (t >> 1) - 1);
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < C::N; c += 8) {
                         uint32_t v[8];
                         tmem_ld8(o_tmem + (uint32_t)(g * C::N + c), v);
                         tc_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha[(c + e) % R]);
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[g][(c + e) % R]);
                         tmem_st8(o_tmem + (uint32_t)(g * C::N + c), v);
                     }
                     tc_wait_st();
@@ -629,8 +655,9 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
 #pragma unroll
                 for (int e = 0; e < CH; e += 2) {
                     const int r = c + e;
-                    const float a = ex2(x[r] + (BASE - m[r]));
-                    const float b = ex2(x[r + 1] + (BASE - m[r + 1]));
+                    const float4 m = m4[r / 4];
+                    const float a = ex2(x[r] + (BASE - (e & 2 ? m.z : m.x)));
+                    const float b = ex2(x[r + 1] + (BASE - (e & 2 ? m.w : m.y)));
                     l[r] = fmaf(a, sc.z, l[r]);
                     l[r + 1] = fmaf(b, sc.z, l[r + 1]);
                     const float a0 = a * sc.w, b0 = b * sc.w;
@@ -662,10 +689,6 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         }
         // ---- the unit's end: the groups' maxima, row sums and O^T, joined
         column_sums<R>(l, sm.lx[w][g][quarter], lane);
-        if (quarter == 0 && lane == 0) {
-#pragma unroll
-            for (int r = 0; r < R; ++r) sm.mx[w][g][r] = m[r];
-        }
         // last tile of each group in the unit, and its P V
         bool has[2];
 #pragma unroll

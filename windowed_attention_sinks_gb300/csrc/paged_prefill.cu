@@ -23,9 +23,10 @@
 //       Both are one number for a page, that is for 16 columns or more
 //   P = 2^(7 + x - m), f16, over the first columns of S's own buffer
 //   O += P V, P from TMEM
-// m is what it was unless a row exceeds it by more than 2^8, so P is computed
-// on trust in the one pass over S that also finds the maximum; where that was
-// wrong (O is then rescaled) the pass is repeated. TMEM: S / P 2 x 2 x 64
+// m is the maximum of a row's first keys and stays unless 64 keys' P sum up to more than
+// 2^15: P is computed on trust in one pass over S that looks for no maximum,
+// and where the sum says that this was wrong m moves, O is rescaled and the pass
+// is repeated. TMEM: S / P 2 x 2 x 64
 // columns, O 2 x D: all 512 for D = 128, hence the shared columns of S and P.
 // The MMAs of one CTA run in the order of issue, so S of two steps ahead may
 // follow the P V that reads its columns.
@@ -57,7 +58,7 @@ constexpr int SRING = 8;
 constexpr int EXTRA = 3;  // a unit's own cost, in tiles
 constexpr int UNITS = 4;  // units handed on ahead
 constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
-constexpr float TAU = 8.f;        // m moves when x exceeds it by more
+constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
 constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
 
 struct PrefillParams {
@@ -90,7 +91,7 @@ template <int D> struct alignas(1024) Smem {
     uint64_t k_full[STAGES], k_empty[STAGES], v8_full[STAGES], v8_empty[STAGES];
     uint64_t v_full[2], v_empty[2];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_empty[2], drain[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -345,6 +346,7 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, i
                                   IDESC_O, kk > 0 || kp > s0);
                 tc_commit(smem_u32(&sm.pv_done[half]));
                 if ((kp & 1) || kp == s1 - 1) tc_commit(smem_u32(&sm.v_empty[b]));
+                if (kp == s1 - 1) tc_commit(smem_u32(&sm.o_full[half]));
                 ++pc;
             }
             if (k < s1) ok = issue_s(k);
@@ -369,7 +371,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
-    int t0 = 0, done = 0;  // CTA's tiles; this half's steps
+    int t0 = 0, done = 0, units = 0;  // CTA's tiles; this half's steps and units
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const Unit<ROWS> &u = sm.units.u[i % UNITS];
@@ -460,14 +462,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             tc_fence_after();
             const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
             const bool key0 = p.sink_mode == 1 && kpos0 == 0;
-            uint32_t pw[32];
-            float sum, top;
-#pragma unroll 1
-            for (;;) {
-                // P of the row's 64 keys with m as it is, their sum and the largest x - m
-                // (of a row without keys so far: x)
-                const float base = m == NOTHING ? BASE : BASE - m;
-                uint32_t xs[2][32];
+            uint32_t xs[2][32];
+            auto load = [&]() {
                 tmem_ld32(s_tmem, xs[0]);
                 tmem_ld32(s_tmem + 32u, xs[1]);
                 tc_wait_ld();
@@ -480,46 +476,34 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         hide_unless(xs[e >> 5][e & 31],
                                     (uint32_t)(seen >> (e & 32)) & (1u << (e & 31)));
                 }
-                top = -INFINITY;
-                sum = 0.f;
+            };
+            // a page's scale as S and x take it: f above 0 (a zero key scale makes it
+            // 0), since a masked S is -inf
+            auto scales = [&](int col) {
+                float4 s = sm.sc[ss][(in_tile + col) >> p.page_shift];
+                s.x = fmaxf(s.x * qf, FLT_MIN);
+                return s;
+            };
+            // m from the row's 64 keys, and O and l in its terms
+            auto move = [&]() -> bool {
+                float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    uint32_t(&x)[32] = xs[c];
+                for (int w = 0; w < SUB; w += CW) {
+                    const float4 s = scales(w);
+                    float mx = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < 32; w += CW) {
-                        const float4 s = sm.sc[ss][(in_tile + 32 * c + w) >> p.page_shift];
-                        // above 0 (a zero key scale makes it 0): a masked S is -inf
-                        const float f = fmaxf(s.x * qf, FLT_MIN), off = s.y + base;
-                        const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(off, off);
-                        uint64_t part = f2_pack(0.f, 0.f);
-#pragma unroll
-                        for (int e = w; e < w + CW; e += 2) {
-                            float a, b;
-                            f2_unpack(
-                                f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])),
-                                       f2, off2),
-                                a, b);
-                            if (c == 0 && e == 0 && key0) a += sink;
-                            top = max3(top, a, b);
-                            a = ex2(a);
-                            b = ex2(b);
-                            part = f2_add(part, f2_pack(a, b));
-                            pw[16 * c + (e >> 1)] = pack_f16x2(a, b);
-                        }
-                        float a, b;
-                        f2_unpack(part, a, b);
-                        sum = fmaf(a + b, s.z, sum);
-                    }
+                    for (int e = w; e < w + CW; e += 2)
+                        mx = max3(mx, __uint_as_float(xs[e >> 5][e & 31]),
+                                  __uint_as_float(xs[e >> 5][(e & 31) + 1]));
+                    top = fmaxf(top, fmaf(mx, s.x, s.y));
+                    if (w == 0 && key0)
+                        top = fmaxf(top, fmaf(__uint_as_float(xs[0][0]), s.x, s.y) + sink);
                 }
-                top -= BASE;
-                const bool move = m == NOTHING ? top > NOTHING : top > TAU;
-                if (!__any_sync(0xffffffffu, move)) break;
-                const float mn = !move ? m : m == NOTHING ? top : m + top;
-                const float alpha = move ? ex2(m - mn) : 1.f;
+                const float mn = fmaxf(m, top), alpha = ex2(m - mn);
                 m = mn;
                 l *= alpha;
                 if (k > s0) {
-                    if (!wait(sm.pv_done[half], done - 1)) return;
+                    if (!wait(sm.pv_done[half], done - 1)) return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -532,11 +516,48 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         tmem_st32(tmem + O_COL + 32u * c, o);
                     }
                 }
+                return true;
+            };
+            load();
+            if (__any_sync(0xffffffffu, m == NOTHING) && !move()) return;
+            uint32_t pw[32];
+            float sum;
+#pragma unroll 1
+            for (;;) {
+                // P of the row's 64 keys with m as it is, and their sum
+                const float base = m == NOTHING ? BASE : BASE - m;
+                float raw = 0.f;
+                sum = 0.f;
+#pragma unroll
+                for (int w = 0; w < SUB; w += CW) {
+                    const float4 s = scales(w);
+                    const float off = s.y + base;
+                    const uint64_t f2 = f2_pack(s.x, s.x), off2 = f2_pack(off, off);
+                    uint64_t part = f2_pack(0.f, 0.f);
+#pragma unroll
+                    for (int e = w; e < w + CW; e += 2) {
+                        float a, b;
+                        f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e >> 5][e & 31]),
+                                                 __uint_as_float(xs[e >> 5][(e & 31) + 1])),
+                                         f2, off2),
+                                  a, b);
+                        if (e == 0 && key0) a += sink;
+                        a = ex2(a);
+                        b = ex2(b);
+                        part = f2_add(part, f2_pack(a, b));
+                        pw[e >> 1] = pack_f16x2(a, b);
+                    }
+                    float a, b;
+                    f2_unpack(part, a, b);
+                    raw += a + b;
+                    sum = fmaf(a + b, s.z, sum);
+                }
+                // no value is above the sum, so below the limit none has left f16's range
+                if (!__any_sync(0xffffffffu, raw > SUM_LIMIT)) break;
+                load();
+                if (!move()) return;
             }
             l += sum;
-            // one P V at a time may be outstanding, or the parity that the waits for
-            // it go by would be ambiguous (it is done by now as a rule)
-            if (done >= 1 && !wait(sm.pv_done[half], done - 1)) return;
             tmem_st32(s_tmem, pw);
             tc_wait_st();
             tc_fence_before();
@@ -548,7 +569,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         }
         t0 += n;
         // ---- epilogue
-        if (!wait(sm.pv_done[half], done - 1)) return;
+        if (!wait(sm.o_full[half], units)) return;
+        ++units;
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
         float lse2 = l == 0.f ? -INFINITY : m - BASE + log2f(l);
@@ -626,6 +648,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.p_full[i][0]), 4);
             mbar_init(smem_u32(&sm.p_full[i][1]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_full[i]), 1);
             mbar_init(smem_u32(&sm.o_empty[i]), 4);
         }
         for (int i = 0; i < SRING; ++i) {
@@ -645,9 +668,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 96 + 256 x 160 = the 512 x 128 of the launch
+    // registers: 256 threads x 64 + 256 x 192 = the 512 x 128 of the launch
     if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             load_tiles<D>(p, &tk, &tv, sm, ctx);
         } else if (warp == 2) {
@@ -659,7 +682,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             widen<D>(p, sm, ctx);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         softmax<D, CW>(p, sm, tmem, ctx);
     }
     tc_fence_before();
