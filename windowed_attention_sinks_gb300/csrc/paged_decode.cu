@@ -28,13 +28,17 @@
 //
 // One persistent CTA per SM (kernels that allocate TMEM run one) over an equal
 // piece of the tiles (paged_plan.cuh):
-//   warp 0      the units; TMA: K and V tiles, one copy a page, two rings of STAGES tiles
-//   warp 1      MMA issuer
-//   warp 2      the pages' scales, a ring of SRING tiles ahead
-//   warp 3      Q of the next unit, split and swizzled; the rows' addresses
-//   warps 4-11  softmax: two groups of four take the tiles in turn, each with
-//               its own m, l, P and O^T, so that one's exponentials run beside
-//               the other's loads and votes; they are joined at the unit's end.
+//   warp 0      the units; TMA: K and V tiles, one copy a page, two rings of
+//               STAGES tiles; the pages' scales
+//   warps 1, 2  MMA issuers: S, and P V. (Every wait of such a thread costs it 100 to
+//               200 cycles even if it is met; one thread for both took 1900 cycles a
+//               tile, more than the tile takes to arrive.)
+//   warp 3      Q of the next units, split and swizzled; the rows' addresses
+//   warps 4-11  softmax: two groups of four, each with its own m, l, P and O^T.
+//               They take the tiles of a unit in turn, so that one's exponentials
+//               run beside the other's loads and votes, and are joined at its
+//               end; a unit of at most SOLO tiles is one group's alone, and the
+//               groups take such units in turn.
 #include <limits.h>
 #include <math.h>
 #include <stdio.h>
@@ -48,7 +52,8 @@ namespace {
 constexpr int NTHREADS = 384;
 constexpr int SRING = 16;
 constexpr int EXTRA = 2;  // a unit's own cost, in tiles
-constexpr int UNITS = 6;  // units handed on ahead
+constexpr int UNITS = 8;  // units handed on ahead
+constexpr int SOLO = 2;   // tiles of a unit that one group takes alone
 constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
 constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
 constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
@@ -76,6 +81,7 @@ template <int D, int R> struct Cfg {
     // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with few rows
     static constexpr int STAGES = (R <= 16 ? 6 : 5) * (128 / D);
     static constexpr int SBUF = 4;  // S buffers
+    static constexpr int QB = R <= 16 ? 4 : 2;  // units whose Q is at hand
     static constexpr uint32_t O_COL = SBUF * N;
     static constexpr uint32_t USED = O_COL + 2 * N;
     static constexpr uint32_t COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
@@ -85,26 +91,27 @@ template <int D, int R> struct alignas(1024) Smem {
     using C = Cfg<D, R>;
     uint8_t k[C::STAGES][C::TILE_BYTES];
     uint8_t v[C::STAGES][C::TILE_BYTES];
-    uint8_t q[2][C::N * D];
+    uint8_t q[C::QB][C::N * D];
     uint8_t p[2][C::N * TILE];
     float4 sc[SRING][8];        // page's k scale, log2 v scale, 1 / v scale, v scale > 0
     float wmax[2][4][R];        // column maxima of the warps
-    alignas(16) float mx[2][2][R];  // unit parity, group: running maxima
-    float alpha[2][R];          // what a move of them multiplies l and O by
-    float lx[2][2][4][R];       // and the warps' row sums
-    long long orow[2][R];       // output row of each query row, -1 past the last
-    int rpos[2][R];             // its position
-    float rsink[2][R];          // its sink (log2 units)
-    float wt[2][R];             // what a row of each group's O^T is multiplied by
-    float qf[2];                // scale log2(e) / the power of two in Q
+    float alpha[2][R];          // what a move of m multiplies l and O by
+    // of a unit (by its Q buffer):
+    alignas(16) float mx[C::QB][2][R];  // the groups' running maxima
+    float lx[C::QB][2][4][R];   // the warps' row sums
+    float wt[C::QB][2][R];      // what a row of each group's O^T is multiplied by
+    long long orow[C::QB][R];   // output row of each query row, -1 past the last
+    int rpos[C::QB][R];         // its position
+    float rsink[C::QB][R];      // its sink (log2 units)
+    float qf[C::QB];            // scale log2(e) / the power of two in Q
     PlanStart plan;
     UnitRing<R, UNITS> units;
     uint64_t k_full[C::STAGES], k_empty[C::STAGES], v_full[C::STAGES], v_empty[C::STAGES];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full[2], q_empty[2];
-    uint64_t s_full[C::SBUF], s_empty[C::SBUF], p_full[2], pv_done[2], o_empty, drain;
+    uint64_t q_full[C::QB], q_empty[C::QB];
+    uint64_t s_full[C::SBUF], s_empty[C::SBUF], p_full[2], pv_done[2], o_empty[2], both, drain[2];
     uint32_t tmem_base;
-    int abort, last;
+    int abort, last[3];  // last: of a group alone, of both
 };
 
 // ---------------------------------------------------------------- PTX used here alone
@@ -177,13 +184,21 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
+            // a page a lane
             const int j = (u.t_first + c) * per_tile + lane;
-            int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
+            const int pid =
+                c + lane / per_tile < u.end
+                    ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j)
+                    : -1;
             bad |= pid == -2;
             const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
+            const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
             for (int i = 0; i < nt; ++i, ++t) {
                 const int st = t % C::STAGES, use = t / C::STAGES;
+                // lane i * per_tile + k holds the page of the tile's slot k
+                const int k = lane - i * per_tile;
+                const bool here = k >= 0 && k < per_tile;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
                     const uint32_t full = smem_u32(kv ? &sm.v_full[st] : &sm.k_full[st]);
@@ -196,12 +211,18 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
                     }
                     ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
                     if (!ok) break;
-                    // lane i * per_tile + s holds the page of the tile's slot s
-                    const int s = lane - i * per_tile;
-                    if (s >= 0 && s < per_tile)
-                        tma_load_2d(dst + (uint32_t)s * page_bytes, kv ? tv : tk, full, 0, row);
+                    if (here)
+                        tma_load_2d(dst + (uint32_t)k * page_bytes, kv ? tv : tk, full, 0, row);
                 }
                 if (!ok) break;
+                const int ss = t % SRING;
+                if (t >= SRING)
+                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_empty[ss]),
+                                                           (t / SRING - 1) & 1, ctx, &sm.abort));
+                if (!ok) break;
+                if (here) sm.sc[ss][k] = s;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[ss]));
             }
         }
     }
@@ -222,43 +243,11 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
     }
 }
 
-template <int D, int R>
-__device__ void load_scales(const DecodeParams &p, Smem<D, R> &sm, const DevCtx &ctx) {
-    const int lane = threadIdx.x & 31;
-    const int per_tile = TILE >> p.page_shift, chunk = 32 >> (7 - p.page_shift);
-    int t = 0;
-    bool ok = true;
-    for (int i = 0; ok; ++i) {
-        ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, &sm.abort));
-        if (!ok) break;
-        const Unit<R> &u = sm.units.u[i % UNITS];
-        if (u.begin == u.end) break;
-        for (int c = u.begin; c < u.end && ok; c += chunk) {
-            const int j = (u.t_first + c) * per_tile + lane;
-            const int pid = c + lane / per_tile < u.end ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j) : -1;
-            const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
-            const int nt = min(chunk, u.end - c);
-            for (int a = 0; a < nt && ok; ++a, ++t) {
-                const int st = t % SRING, use = t / SRING;
-                if (use >= 1) ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx,
-                                             &sm.abort);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const int sl = lane - a * per_tile;
-                if (sl >= 0 && sl < per_tile) sm.sc[st][sl] = s;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[st]));
-            }
-        }
-        __syncwarp();
-        if (lane == 0) sm.units.release(i);
-    }
-}
-
 // Q of a unit: scaled by a power of two, split into hi and 16 lo, K-major rows
 // hi 0 .. R-1, lo R .. 2R-1. A lane holds 8 columns, CH lanes a row.
 template <int D, int R>
 __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx &ctx) {
+    using C = Cfg<D, R>;
     constexpr int CH = D / 8, PER = R * CH / 32;  // items a lane
     const int lane = threadIdx.x & 31;
     const int G = p.plan.G;
@@ -269,7 +258,7 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         __syncwarp();
         if (lane == 0) sm.units.release(n);
         if (u.begin == u.end) break;
-        const int w = n & 1;
+        const int w = n % C::QB;
         // four items a lane in registers at a time; with more rows they are read
         // again for the second pass (from L1)
         constexpr int B = PER < 4 ? PER : 4;
@@ -307,8 +296,8 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
         k = amax > 0.f ? max(-120, min(k, 120)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        if (n >= 2)
-            ok = mbar_wait(smem_u32(&sm.q_empty[w]), ((n >> 1) - 1) & 1, ctx, &sm.abort);
+        if (n >= C::QB)
+            ok = mbar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll 1
@@ -352,82 +341,90 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
 }
 
 template <int D, int R>
-__device__ void issue_mmas(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem,
-                           const DevCtx &ctx) {
+__device__ void issue_s(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     using C = Cfg<D, R>;
-    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, C::N, 0, 0);
-    constexpr uint32_t IDESC_O = idesc_e4m3_f32(D, C::N, 1, 1);
+    constexpr uint32_t IDESC = idesc_e4m3_f32(128, C::N, 0, 0);
     volatile int *abort = &sm.abort;
-    if (ctx.stall) mbar_wait(smem_u32(&sm.drain), 0, ctx, abort);  // test hook: runs out
-    const uint64_t dk = desc_rows<D>(smem_u32(sm.k[0])), dv = desc_rows<D>(smem_u32(sm.v[0]));
-    const uint64_t dq = desc_rows<D>(smem_u32(sm.q[0])), dp = desc_rows<C::N>(smem_u32(sm.p[0]));
-    int done = 0;  // P V issued
-    // per group: whether its next P V is the unit's first, and the unit
-    struct Pending {
-        int unit;
-        bool first;
-    } pend[2] = {};
-    auto issue_pv = [&]() -> bool {
-        const int t = done, g = t & 1, st = t % C::STAGES;
-        const Pending pe = g ? pend[1] : pend[0];
-        if (!mbar_wait(smem_u32(&sm.v_full[st]), (t / C::STAGES) & 1, ctx, abort)) return false;
-        if (pe.first && pe.unit >= 1 &&
-            !mbar_wait(smem_u32(&sm.o_empty), (pe.unit - 1) & 1, ctx, abort))
-            return false;
-        if (!mbar_wait(smem_u32(&sm.p_full[g]), (t >> 1) & 1, ctx, abort)) return false;
-        tc_fence_after();
-        const uint64_t a = dv + (uint64_t)(st * (C::TILE_BYTES >> 4));
-        const uint64_t b = dp + (uint64_t)(g * (C::N * TILE >> 4));
-        const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::N;
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V and of P
-            mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * (32 * C::N >> 4)),
-                   IDESC_O, kk > 0 || !pe.first);
-        tc_commit(smem_u32(&sm.v_empty[st]));
-        tc_commit(smem_u32(&sm.pv_done[g]));
-        ++done;
-        return true;
+    if (ctx.stall) mbar_wait(smem_u32(&sm.drain[0]), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dk = desc_rows<D>(smem_u32(sm.k[0])), dq = desc_rows<D>(smem_u32(sm.q[0]));
+    auto wait = [&](uint64_t &bar, int phase) {
+        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
     int t = 0;
-    int first_of[2] = {0, 0};  // first tile of the last two units
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = sm.units.wait(i, ctx, abort))) break;
-        const int w = i & 1, n = sm.units.u[i % UNITS].end - sm.units.u[i % UNITS].begin;
+        const int w = i % C::QB, n = sm.units.u[i % UNITS].end - sm.units.u[i % UNITS].begin;
         sm.units.release(i);
         if (n == 0) break;
-        // Q of this unit takes the place of the unit before the last, whose
-        // end waits for all of its P V
-        const int must = i >= 1 ? (w ? first_of[0] : first_of[1]) : 0;
-        while (ok && done < must) ok = issue_pv();
-        if (!ok || !mbar_wait(smem_u32(&sm.q_full[w]), (i >> 1) & 1, ctx, abort)) break;
-        if (w) first_of[1] = t;
-        else first_of[0] = t;
+        ok = wait(sm.q_full[w], i / C::QB);
+        const uint64_t b = dq + (uint64_t)(w * (C::N * D >> 4));
         for (int j = 0; j < n && ok; ++j, ++t) {
             const int st = t % C::STAGES, sb = t % C::SBUF;
-            ok = mbar_wait(smem_u32(&sm.k_full[st]), (t / C::STAGES) & 1, ctx, abort);
-            if (ok && t >= C::SBUF)
-                ok = mbar_wait(smem_u32(&sm.s_empty[sb]), (t / C::SBUF - 1) & 1, ctx, abort);
+            ok = wait(sm.k_full[st], t / C::STAGES) &&
+                 (t < C::SBUF || wait(sm.s_empty[sb], t / C::SBUF - 1));
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = dk + (uint64_t)(st * (C::TILE_BYTES >> 4));
-            const uint64_t b = dq + (uint64_t)(w * (C::N * D >> 4));
 #pragma unroll
             for (int kk = 0; kk < D / 32; ++kk)
                 mma_f8(tmem + (uint32_t)sb * C::N, a + (uint64_t)(kk * 2), b + (uint64_t)(kk * 2),
-                       IDESC_S, kk > 0);
-            tc_commit(smem_u32(&sm.k_empty[st]));
+                       IDESC, kk > 0);
             tc_commit(smem_u32(&sm.s_full[sb]));
+            tc_commit(smem_u32(&sm.k_empty[st]));
             if (j == n - 1) tc_commit(smem_u32(&sm.q_empty[w]));
-            if (t - done >= 2) ok = issue_pv();
-            if (t & 1) pend[1] = Pending{i, j < 2};
-            else pend[0] = Pending{i, j < 2};
         }
     }
-    while (ok && done < t) ok = issue_pv();
-    tc_commit(smem_u32(&sm.drain));  // every MMA is done before TMEM goes
+    tc_commit(smem_u32(&sm.drain[0]));  // every MMA is done before TMEM goes
     int zero = 0;
-    mbar_wait(smem_u32(&sm.drain), 0, ctx, &zero);
+    mbar_wait(smem_u32(&sm.drain[0]), 0, ctx, &zero);
+}
+
+// The group that takes tile t, the j-th of unit i with n tiles.
+__device__ __forceinline__ int group_of(int i, int n, int t) { return (n <= SOLO ? i : t) & 1; }
+
+template <int D, int R>
+__device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
+    using C = Cfg<D, R>;
+    constexpr uint32_t IDESC = idesc_e4m3_f32(D, C::N, 1, 1);
+    volatile int *abort = &sm.abort;
+    const uint64_t dv = desc_rows<D>(smem_u32(sm.v[0])), dp = desc_rows<C::N>(smem_u32(sm.p[0]));
+    auto wait = [&](uint64_t &bar, int phase) {
+        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+    };
+    int t = 0, done0 = 0, done1 = 0, units0 = 0, units1 = 0;  // of group 0 and 1
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        const int n = sm.units.u[i % UNITS].end - sm.units.u[i % UNITS].begin;
+        sm.units.release(i);
+        if (n == 0) break;
+        for (int j = 0; j < n && ok; ++j, ++t) {
+            const int st = t % C::STAGES, g = group_of(i, n, t);
+            const bool first = n <= SOLO ? j == 0 : j < 2;  // of the group in this unit
+            ok = wait(sm.v_full[st], t / C::STAGES);
+            // the first P V overwrites the O that an earlier unit's end reads
+            const int units = g ? units1 : units0, done = g ? done1 : done0;
+            if (first && units >= 1) ok = ok && wait(sm.o_empty[g], units - 1);
+            ok = ok && wait(sm.p_full[g], done);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t a = dv + (uint64_t)(st * (C::TILE_BYTES >> 4));
+            const uint64_t b = dp + (uint64_t)(g * (C::N * TILE >> 4));
+            const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::N;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V and of P
+                mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * (32 * C::N >> 4)),
+                       IDESC, kk > 0 || !first);
+            tc_commit(smem_u32(&sm.pv_done[g]));
+            tc_commit(smem_u32(&sm.v_empty[st]));
+            if (g) ++done1, units1 += first;
+            else ++done0, units0 += first;
+        }
+    }
+    tc_commit(smem_u32(&sm.drain[1]));
+    int zero = 0;
+    mbar_wait(smem_u32(&sm.drain[1]), 0, ctx, &zero);
 }
 
 // Sums of each l[r] over the warp, to out[0 .. R-1]. Lanes halve the rows they
@@ -458,13 +455,13 @@ template <int R> __device__ __forceinline__ void column_sums(float (&l)[R], floa
 // lane c holds part c's denominator, the columns are spread over the lanes.
 template <int D, int R>
 __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long long *orow,
-                           const float *rsink, int warp, int lane) {
+                           const float *rsink, int warp, int warps, int lane) {
     const float *plse = reinterpret_cast<const float *>(p.ws + plan_lse_offset());
     const float *prow = reinterpret_cast<const float *>(p.ws + plan_rows_offset(R));
     constexpr int E = D / 32;
     // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ...
     auto slot = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
-    for (int r = warp; r < R; r += 8) {
+    for (int r = warp; r < R; r += warps) {
         const long long row = orow[r];
         if (row < 0) continue;
         float m = -INFINITY;
@@ -513,26 +510,44 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_tmem = tmem + C::O_COL + lanes;
     volatile int *abort = &sm.abort;
-    const int bar_g = 1 + g, bar_all = 3;
+    const int bar_g = 1 + g;
     // Once a wait has given up (ok), the warp goes through the rest of its unit
-    // without waiting and without writing to global memory: every warp reaches every
-    // named barrier, so none is left waiting there.
+    // without waiting and without writing to global memory: every warp of the group
+    // reaches every named barrier, so none is left waiting there. Between the groups
+    // there are bounded waits alone.
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {
         ok = ok && mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
         ok = __all_sync(0xffffffffu, ok);
     };
-    int t0 = 0;  // first tile of the unit
+    int t0 = 0, done = 0, meets = 0;  // tiles before the unit; the group's; meetings of both
     for (int i = 0;; ++i) {
-        // all eight warps go on, or none
-        const int w = i & 1;
-        if (key < R) sm.mx[w][g][key] = NOTHING;
+        const int w = i % C::QB;
         ok = ok && sm.units.wait(i, ctx, abort);
-        if (sync_any<256>(bar_all, !ok)) break;
+        if (sync_any<128>(bar_g, !ok)) break;  // the group's four warps go on, or none
         const Unit<R> &u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
         if (n == 0) break;
-        wait(sm.q_full[w], i >> 1);
+        const bool solo = n <= SOLO;
+        if (solo && (i & 1) != g) {
+            t0 += n;
+            __syncwarp();
+            if (lane == 0) sm.units.release(i);
+            continue;
+        }
+        wait(sm.q_full[w], i / C::QB);
+        if (key < R) sm.mx[w][g][key] = NOTHING;
+        named_sync(bar_g, 128);
+        // the group's threads meet, or both groups'
+        auto meet = [&]() {
+            if (solo) {
+                named_sync(bar_g, 128);
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.both));
+                wait(sm.both, meets++);
+            }
+        };
         const float qf = sm.qf[w];
         // m is the group's and lies in shared memory: 32 rows of it would not fit
         // beside the scores and sums in registers
@@ -540,8 +555,9 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         float l[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = 0.f;
-        const int j0 = (g ^ t0) & 1;  // the group's first tile of the unit
-        for (int j = j0; j < n; j += 2) {
+        const int step = solo ? 1 : 2, j0 = solo ? 0 : (g ^ t0) & 1;
+#pragma unroll 1
+        for (int j = j0; j < n; j += step, ++done) {
             const int t = t0 + j, sb = t % C::SBUF, ss = t % SRING;
             const int kpos = (u.t_first + u.begin + j) * TILE + key;
             const int base = kpos - key;
@@ -591,17 +607,18 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     hide_unless(b, in);
                     x[r] = __uint_as_float(b);
                 }
-                // values that no row sees may hold anything, NaN codes too: the MMA
-                // multiplies them by 0, so they are cleared
-                if (base < u.lo || base + TILE - 1 > u.hi) {
-                    const int st = t % C::STAGES;
-                    wait(sm.v_full[st], t / C::STAGES);
-                    if (kpos < u.lo || kpos > u.hi) {
+            }
+            // values that no row sees may hold anything, NaN codes too, and the MMA
+            // multiplies them by 0: they are cleared, and so are those of a zero scale
+            const bool clear = kpos < u.lo || kpos > u.hi || sc.w == 0.f;
+            if (__any_sync(0xffffffffu, clear)) {
+                const int st = t % C::STAGES;
+                wait(sm.v_full[st], t / C::STAGES);
+                if (clear) {
 #pragma unroll
-                        for (int c = 0; c < D / 16; ++c)
-                            *reinterpret_cast<uint4 *>(sm.v[st] + key * D + 16 * c) =
-                                make_uint4(0, 0, 0, 0);
-                    }
+                    for (int c = 0; c < D / 16; ++c)
+                        *reinterpret_cast<uint4 *>(sm.v[st] + key * D + 16 * c) =
+                            make_uint4(0, 0, 0, 0);
                 }
             }
             float top = -INFINITY;
@@ -629,7 +646,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
 #pragma unroll
                 for (int r = 0; r < R; ++r) l[r] *= sm.alpha[g][r];
                 if (j > j0) {
-                    wait(sm.pv_done[g], (t >> 1) - 1);
+                    wait(sm.pv_done[g], done - 1);
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < C::N; c += 8) {
@@ -644,9 +661,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     tc_wait_st();
                 }
             }
-            // P overwrites the group's last one, which its P V has read by now
-            // (waited for here because nothing else does when m stays)
-            if (t >= 2) wait(sm.pv_done[g], (t >> 1) - 1);
+            // P overwrites the group's last one, which its P V has read by now as a rule
+            if (done >= 1) wait(sm.pv_done[g], done - 1);
             // the key's row of P: R hi codes, then R lo codes, 16 bytes a store
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
@@ -660,10 +676,10 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     const float b = ex2(x[r + 1] + (BASE - (e & 2 ? m.w : m.y)));
                     l[r] = fmaf(a, sc.z, l[r]);
                     l[r + 1] = fmaf(b, sc.z, l[r + 1]);
-                    const float a0 = a * sc.w, b0 = b * sc.w;
-                    const uint32_t h = e4m3x2(a0, b0);
-                    const float2 back = e4m3x2_to_f32(h);
-                    const uint32_t g2 = e4m3x2((a0 - back.x) * 16.f, (b0 - back.y) * 16.f);
+                    // by way of f16, whose 11 bits hold hi + lo / 16, in pairs
+                    const uint32_t ab = pack_f16x2(a, b), h = e4m3x2_of_f16x2(ab);
+                    const uint32_t g2 =
+                        e4m3x2_of_f16x2(sixteen_times_difference(ab, e4m3x2_to_f16x2(h)));
                     if (e & 2) {
                         hi[e >> 2] |= h << 16;
                         lo[e >> 2] |= g2 << 16;
@@ -689,22 +705,18 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         }
         // ---- the unit's end: the groups' maxima, row sums and O^T, joined
         column_sums<R>(l, sm.lx[w][g][quarter], lane);
-        // last tile of each group in the unit, and its P V
-        bool has[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const int jl = n - 1 - ((n - 1 + t0 + s) & 1);
-            has[s] = jl >= 0;
-            if (has[s]) wait(sm.pv_done[s], (t0 + jl) >> 1);
-        }
-        named_sync(bar_all, 256);
+        wait(sm.pv_done[g], done - 1);
+        tc_fence_before();
+        meet();
         tc_fence_after();
+        const bool has[2] = {!solo || g == 0, !solo || g == 1};
         const bool part = u.begin > 0 || u.end < u.ntiles;
         const size_t slot = (size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1);
         // a thread a row: what each group's O^T is multiplied by, and the denominator
-        const int me = threadIdx.x - 128;
+        const int me = solo ? key : threadIdx.x - 128;
         if (me < R) {
-            const float m0 = sm.mx[w][0][me], m1 = sm.mx[w][1][me], mm = fmaxf(m0, m1);
+            const float m0 = has[0] ? sm.mx[w][0][me] : NOTHING;
+            const float m1 = has[1] ? sm.mx[w][1][me] : NOTHING, mm = fmaxf(m0, m1);
             const float w0 = has[0] ? ex2(m0 - mm) : 0.f, w1 = has[1] ? ex2(m1 - mm) : 0.f;
             float z = 0.f;
 #pragma unroll
@@ -721,16 +733,16 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 const long long row = sm.orow[w][me];
                 if (ok && p.lse && row >= 0) p.lse[row] = lse2 * LN2;
             }
-            sm.wt[0][me] = w0 * inv;
-            sm.wt[1][me] = w1 * inv;
+            sm.wt[w][0][me] = w0 * inv;
+            sm.wt[w][1][me] = w1 * inv;
         }
-        named_sync(bar_all, 256);
+        meet();
         const bool writes = (D == 128 || lane < 16) && ok;  // 64 rows of O^T: 16 lanes of every 32
         const int col = D == 128 ? key : quarter * 16 + lane;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D + col;
-#pragma unroll
-        for (int k = 0; k < R / 2; k += 4) {
-            const int r0 = g * (R / 2) + k;
+        const int rows0 = solo ? 0 : g * (R / 2), rows1 = solo ? R : rows0 + R / 2;
+#pragma unroll 1
+        for (int r0 = rows0; r0 < rows1; r0 += 4) {
             uint32_t v[4][4];  // group 0 hi, lo, group 1 hi, lo
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -746,7 +758,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (has[s])
-                        acc = fmaf(sm.wt[s][r],
+                        acc = fmaf(sm.wt[w][s][r],
                                    fmaf(__uint_as_float(v[2 * s + 1][e]), 0.0625f,
                                         __uint_as_float(v[2 * s][e])),
                                    acc);
@@ -760,21 +772,31 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty));
+        // both groups have read both O^T, or the one group its own: eight arrivals each
+        if (lane == 0) {
+            for (int s = 0; s < 2; ++s)
+                if (has[s]) mbar_arrive_n(smem_u32(&sm.o_empty[s]), solo ? 2 : 1);
+        }
         if (part) {  // the last of the unit's pieces to get here joins them
             __threadfence();
-            const bool bad = sync_any<256>(bar_all, !ok);
+            meet();
             if (me == 0)
-                sm.last = atomicInc(p.join + u.c0, (unsigned)u.parts - 1) == (unsigned)u.parts - 1;
-            named_sync(bar_all, 256);
-            if (sm.last && !bad) {
+                sm.last[solo ? g : 2] =
+                    atomicInc(p.join + u.c0, (unsigned)u.parts - 1) == (unsigned)u.parts - 1 &&
+                    !*abort;
+            meet();
+            // (a group alone, or group 0 for both, has asked)
+            if (ok && sm.last[solo ? g : 2]) {
                 __threadfence();
-                join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp - 4, lane);
+                if (solo)
+                    join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp & 3, 4, lane);
+                else
+                    join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp - 4, 8, lane);
             }
         }
         __syncwarp();
         if (lane == 0) {
-            mbar_arrive(smem_u32(&sm.q_empty[w]));
+            mbar_arrive_n(smem_u32(&sm.q_empty[w]), solo ? 2 : 1);
             sm.units.release(i);
         }
         t0 += n;
@@ -804,19 +826,22 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 4);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::QB; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
             mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);  // the MMAs and the softmax warps
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.p_full[i]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.o_empty[i]), 8);
+            mbar_init(smem_u32(&sm.drain[i]), 1);
         }
         for (int i = 0; i < C::SBUF; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.s_empty[i]), 4);
         }
-        mbar_init(smem_u32(&sm.o_empty), 8);
-        mbar_init(smem_u32(&sm.drain), 1);
-        sm.units.init(1 + 1 + 1 + 8);  // MMA issuer, scales, queries, softmax
+        mbar_init(smem_u32(&sm.both), 8);
+        sm.units.init(2 + 1 + 8);  // MMA issuers, queries, softmax
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -831,11 +856,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     const uint32_t tmem = sm.tmem_base;
     if (warp == 0) {
         load_tiles<D, R>(p, &tk, &tv, sm, ctx);
-    } else if (warp == 1) {
-        if (lane == 0) issue_mmas<D, R>(p, sm, tmem, ctx);
+    } else if (warp < 3) {
+        if (lane == 0) {
+            if (warp == 1) issue_s<D, R>(sm, tmem, ctx);
+            else issue_pv<D, R>(sm, tmem, ctx);
+        }
         __syncwarp();
-    } else if (warp == 2) {
-        load_scales<D, R>(p, sm, ctx);
     } else if (warp == 3) {
         load_queries<D, R>(p, sm, ctx);
     } else {

@@ -4,6 +4,8 @@
 
 #include <math.h>
 
+#include <cuda_fp16.h>
+
 #include "common.cuh"
 
 namespace sattn {
@@ -41,6 +43,32 @@ template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint3
     const uint32_t a = r * W + (u << 4);
     return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
 }
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+    asm volatile(
+        "{\n\t.reg .b64 st;\n\t"
+        "mbarrier.arrive.release.cta.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(n)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+// Two f16 to two e4m3 codes, nearest even, saturating.
+__device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+// 16 (a - b) of two f16 pairs.
+__device__ __forceinline__ uint32_t sixteen_times_difference(uint32_t a, uint32_t b) {
+    const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&a),
+                                      *reinterpret_cast<const __half2 *>(&b)),
+                              __float2half2_rn(16.f));
+    return *reinterpret_cast<const uint32_t *>(&d);
+}
+
 // x = keep ? x : -inf. Volatile so that it stays behind the branch it is written in:
 // the compiler otherwise turns a branch around many selections into selections that
 // every tile pays for (3 ALU operations a score where whole tiles need none).

@@ -102,11 +102,6 @@ constexpr int SUB = 64;  // keys a step
 __host__ __device__ constexpr uint32_t idesc_f16_f32(uint32_t M, uint32_t N, uint32_t b_mn) {
     return (1u << 4) | (b_mn << 16) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
-}
-
 template <int D>
 __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const CUtensorMap *tv,
                            Smem<D> &sm, const DevCtx &ctx) {
