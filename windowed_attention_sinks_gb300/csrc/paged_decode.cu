@@ -179,9 +179,13 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         prefetch_tmap(tv);
     }
     UnitIter<R> it(p.plan, sm.plan);
+    int index = 0;
+#pragma unroll 1
     for (; it.live && ok; it.next(p.plan, sm.plan)) {
         const Unit<R> &u = it.u;
-        if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
+        if (u.begin == u.end) continue;
+        if (lane == 0) ok = sm.units.put(index, u, ctx, &sm.abort);
+        ++index;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             // a page a lane
@@ -194,6 +198,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
             const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
             const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
+#pragma unroll 1
             for (int i = 0; i < nt; ++i, ++t) {
                 const int st = t % C::STAGES, use = t / C::STAGES;
                 // lane i * per_tile + k holds the page of the tile's slot k
@@ -206,7 +211,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
                     const uint32_t dst = smem_u32(kv ? sm.v[st] : sm.k[st]);
                     bool go = true;
                     if (lane == 0) {
-                        if (use >= 1) go = mbar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
+                        if (use >= 1) go = bar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
                         if (go) mbar_arrive_expect_tx(full, C::TILE_BYTES);
                     }
                     ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
@@ -217,7 +222,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
                 if (!ok) break;
                 const int ss = t % SRING;
                 if (t >= SRING)
-                    ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.sc_empty[ss]),
+                    ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm.sc_empty[ss]),
                                                            (t / SRING - 1) & 1, ctx, &sm.abort));
                 if (!ok) break;
                 if (here) sm.sc[ss][k] = s;
@@ -228,16 +233,16 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
     }
     if (lane == 0 && ok) {
         Unit<R> last{};
-        sm.units.put(it.index, last, ctx, &sm.abort);
+        sm.units.put(index, last, ctx, &sm.abort);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     // copies in flight land before the CTA leaves (at once on the normal path)
     if (lane == 0) {
         int zero = 0;
         for (int i = 1; i <= C::STAGES && i <= t; ++i) {
-            mbar_wait(smem_u32(&sm.k_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
+            bar_wait(smem_u32(&sm.k_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
                       &zero);
-            mbar_wait(smem_u32(&sm.v_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
+            bar_wait(smem_u32(&sm.v_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
                       &zero);
         }
     }
@@ -297,7 +302,7 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         k = amax > 0.f ? max(-120, min(k, 120)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
         if (n >= C::QB)
-            ok = mbar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
+            ok = bar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll 1
@@ -345,10 +350,10 @@ __device__ void issue_s(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     using C = Cfg<D, R>;
     constexpr uint32_t IDESC = idesc_e4m3_f32(128, C::N, 0, 0);
     volatile int *abort = &sm.abort;
-    if (ctx.stall) mbar_wait(smem_u32(&sm.drain[0]), 0, ctx, abort);  // test hook: runs out
+    if (ctx.stall) bar_wait(smem_u32(&sm.drain[0]), 0, ctx, abort);  // test hook: runs out
     const uint64_t dk = desc_rows<D>(smem_u32(sm.k[0])), dq = desc_rows<D>(smem_u32(sm.q[0]));
     auto wait = [&](uint64_t &bar, int phase) {
-        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+        return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
     int t = 0;
     bool ok = true;
@@ -359,6 +364,7 @@ __device__ void issue_s(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
         if (n == 0) break;
         ok = wait(sm.q_full[w], i / C::QB);
         const uint64_t b = dq + (uint64_t)(w * (C::N * D >> 4));
+#pragma unroll 1
         for (int j = 0; j < n && ok; ++j, ++t) {
             const int st = t % C::STAGES, sb = t % C::SBUF;
             ok = wait(sm.k_full[st], t / C::STAGES) &&
@@ -377,7 +383,7 @@ __device__ void issue_s(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     }
     tc_commit(smem_u32(&sm.drain[0]));  // every MMA is done before TMEM goes
     int zero = 0;
-    mbar_wait(smem_u32(&sm.drain[0]), 0, ctx, &zero);
+    bar_wait(smem_u32(&sm.drain[0]), 0, ctx, &zero);
 }
 
 // The group that takes tile t, the j-th of unit i with n tiles.
@@ -390,7 +396,7 @@ __device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     volatile int *abort = &sm.abort;
     const uint64_t dv = desc_rows<D>(smem_u32(sm.v[0])), dp = desc_rows<C::N>(smem_u32(sm.p[0]));
     auto wait = [&](uint64_t &bar, int phase) {
-        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+        return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
     int t = 0, done0 = 0, done1 = 0, units0 = 0, units1 = 0;  // of group 0 and 1
     bool ok = true;
@@ -399,6 +405,7 @@ __device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
         const int n = sm.units.u[i % UNITS].end - sm.units.u[i % UNITS].begin;
         sm.units.release(i);
         if (n == 0) break;
+#pragma unroll 1
         for (int j = 0; j < n && ok; ++j, ++t) {
             const int st = t % C::STAGES, g = group_of(i, n, t);
             const bool first = n <= SOLO ? j == 0 : j < 2;  // of the group in this unit
@@ -424,7 +431,7 @@ __device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     }
     tc_commit(smem_u32(&sm.drain[1]));
     int zero = 0;
-    mbar_wait(smem_u32(&sm.drain[1]), 0, ctx, &zero);
+    bar_wait(smem_u32(&sm.drain[1]), 0, ctx, &zero);
 }
 
 // Sums of each l[r] over the warp, to out[0 .. R-1]. Lanes halve the rows they
@@ -489,7 +496,7 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
                 }
             }
         }
-        float lse2 = z == 0.f ? -INFINITY : m + log2f(z), inv = z == 0.f ? 0.f : 1.f / z;
+        float lse2 = z == 0.f ? -INFINITY : m + __log2f(z), inv = z == 0.f ? 0.f : __fdividef(1.f, z);
         if (p.sink_mode == 2) with_null_sink(rsink[r], lse2, inv);
         __nv_bfloat16 *dst = p.o + row * D + lane * E;
         if constexpr (E == 4)
@@ -517,7 +524,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
     // there are bounded waits alone.
     bool ok = true;
     auto wait = [&](uint64_t &bar, int phase) {
-        ok = ok && mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+        ok = ok && bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
         ok = __all_sync(0xffffffffu, ok);
     };
     int t0 = 0, done = 0, meets = 0;  // tiles before the unit; the group's; meetings of both
@@ -724,8 +731,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 if (has[0]) z = fmaf(w0, sm.lx[w][0][q][me], z);
                 if (has[1]) z = fmaf(w1, sm.lx[w][1][q][me], z);
             }
-            float lse2 = z == 0.f ? -INFINITY : mm - BASE + log2f(z);
-            float inv = z == 0.f ? 0.f : 1.f / z;
+            float lse2 = z == 0.f ? -INFINITY : mm - BASE + __log2f(z);
+            float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
             if (part) {
                 if (ok) reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot * R + me] = lse2;
             } else {
@@ -788,10 +795,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             // (a group alone, or group 0 for both, has asked)
             if (ok && sm.last[solo ? g : 2]) {
                 __threadfence();
-                if (solo)
-                    join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp & 3, 4, lane);
-                else
-                    join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w], warp - 4, 8, lane);
+                join_parts<D, R>(p, u.c0, u.parts, sm.orow[w], sm.rsink[w],
+                                 solo ? warp & 3 : warp - 4, solo ? 4 : 8, lane);
             }
         }
         __syncwarp();
@@ -869,6 +874,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::COLS);

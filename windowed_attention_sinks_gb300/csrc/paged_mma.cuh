@@ -43,6 +43,28 @@ template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint3
     const uint32_t a = r * W + (u << 4);
     return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
 }
+constexpr int TIMED_OUT = 2;
+
+// mbar_wait in as few instructions as it takes: it stands at dozens of places of
+// kernels whose roles share the instruction cache, and code that does not fit
+// there costs more than anything else in a short call. The limit is taken in 32 bits of
+// nanoseconds (4 s at most).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const DevCtx &ctx,
+                                         volatile int *abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t limit = (uint32_t)min(ctx.wait_ns, (uint64_t)4000000000u);
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort) return false;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (t - t0 <= limit);
+    *abort = TIMED_OUT;  // recorded at the kernel's end
+    return false;
+}
+
 __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
     asm volatile(
         "{\n\t.reg .b64 st;\n\t"
@@ -60,6 +82,11 @@ __device__ __forceinline__ uint32_t e4m3x2_of_f16x2(uint32_t h) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
+}
+__device__ __forceinline__ uint32_t difference_f16x2(uint32_t a, uint32_t b) {
+    const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&a),
+                              *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&d);
 }
 // 16 (a - b) of two f16 pairs.
 __device__ __forceinline__ uint32_t sixteen_times_difference(uint32_t a, uint32_t b) {
@@ -83,7 +110,7 @@ __device__ __forceinline__ void hide_unless(uint32_t &x, bool keep) {
 __device__ __forceinline__ void with_null_sink(float sink, float &lse2, float &inv) {
     const float top = fmaxf(lse2, sink);
     if (top == -INFINITY) return;
-    const float all = top + log2f(ex2(lse2 - top) + ex2(sink - top));
+    const float all = top + __log2f(ex2(lse2 - top) + ex2(sink - top));
     inv *= ex2(lse2 - all);
     lse2 = lse2 != lse2 ? lse2 : all;
 }

@@ -19,6 +19,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "paged_mma.cuh"
 
 namespace sattn {
 
@@ -92,19 +93,31 @@ __device__ __forceinline__ bool plan_seq(const PlanArgs &p, int b, Unit<ROWS> &u
     return true;
 }
 
-// Line length of one head of a sequence: by one thread, or by a warp (then every lane has the sum).
-template <int ROWS, bool WARP>
-__device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u) {
+// Line length of one head of a sequence: of its row tiles rt, rt + step, ...
+template <int ROWS>
+__device__ __forceinline__ long long seq_tiles(const PlanArgs &p, Unit<ROWS> &u, int rt, int step) {
     long long sum = 0;
-    for (int rt = WARP ? threadIdx.x & 31 : 0; rt < u.nrt; rt += WARP ? 32 : 1) {
+#pragma unroll 1
+    for (; rt < u.nrt; rt += step) {
         u.set_rows(p, rt);
         sum += u.ntiles + p.extra;
     }
-    if (WARP) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    }
     return sum;
+}
+__device__ __forceinline__ long long warp_sum64(long long v) {
+#pragma unroll 1
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+// Sums over the lanes up to this one.
+__device__ __forceinline__ long long warp_prefix(long long v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+    }
+    return v;
 }
 
 // What a CTA starts from (in shared memory).
@@ -116,6 +129,14 @@ struct PlanStart {
     long long before;  // line before the sequences b0 .. b1 - 1, in which x0 lies
     int b0, b1;
 };
+
+// The piece that position x of the line lies in.
+static __device__ __noinline__ int piece_of(long long x, int pieces, long long total) {
+    return (int)(((x + 1) * pieces - 1) / total);
+}
+static __device__ __noinline__ long long piece_start(long long total, int c, int pieces) {
+    return total * c / pieces;
+}
 
 // Called by the whole CTA (blockDim.x a multiple of 32); ends with a barrier.
 // Small batches are summed a warp a sequence, since one may have many units;
@@ -130,21 +151,21 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
     Unit<ROWS> u;
     long long mine = 0;
     bool bad = false;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         if (!plan_seq(p, b, u)) bad = true;
-        else mine += (by_warp ? seq_tiles<ROWS, true>(p, u) : seq_tiles<ROWS, false>(p, u)) * p.Hkv;
+        else mine += seq_tiles(p, u, by_warp ? lane : 0, by_warp ? 32 : 1) * p.Hkv;
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
-    if (by_warp && lane != 31) mine = 0;  // a warp's sum counts once
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+    if (by_warp) {  // the lanes' shares, counted once
+        mine = warp_sum64(mine);
+        if (lane != 31) mine = 0;
     }
+    const long long inc = warp_prefix(mine);
     if (lane == 31) ps.wsum[warp] = inc;
     __syncthreads();
     long long before = inc - mine, total = 0;
+#pragma unroll 1
     for (int w = 0; w < nw; ++w) {
         if (w < warp) before += ps.wsum[w];
         total += ps.wsum[w];
@@ -156,8 +177,8 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
         x0 = (uint32_t)total * (uint32_t)c / (uint32_t)pieces;
         x1 = (uint32_t)total * (uint32_t)min(c + 1, pieces) / (uint32_t)pieces;
     } else {
-        x0 = total * c / pieces;
-        x1 = total * min(c + 1, pieces) / pieces;
+        x0 = piece_start(total, c, pieces);
+        x1 = piece_start(total, min(c + 1, pieces), pieces);
     }
     if (tid == 0) {
         ps.x0 = x0;
@@ -174,27 +195,25 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
     if (warp == 0 && x0 < x1) {  // the sequence, head and unit of x0
         long long at = ps.before, ph = 0;
         int b = ps.b0;
+#pragma unroll 1
         for (; b < ps.b1; ++b) {
             if (!plan_seq(p, b, u)) continue;
-            ph = seq_tiles<ROWS, true>(p, u);
+            ph = warp_sum64(seq_tiles(p, u, lane, 32));
             if (x0 < at + ph * p.Hkv) break;
             at += ph * p.Hkv;
         }
         int h = 0;
+#pragma unroll 1
         while (x0 >= at + (h + 1) * ph) ++h;
         at += h * ph;
+#pragma unroll 1
         for (int r0 = 0; r0 < u.nrt; r0 += 32) {
             int nt = 0;
             if (r0 + lane < u.nrt) {
                 u.set_rows(p, r0 + lane);
                 nt = u.ntiles + p.extra;
             }
-            long long upto = nt;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
+            const long long upto = warp_prefix(nt);
             if (nt > 0 && x0 >= at + upto - nt && x0 < at + upto) {
                 ps.b = b;
                 ps.h = h;
@@ -212,12 +231,10 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
 template <int ROWS> struct UnitIter {
     Unit<ROWS> u;
     long long ustart, x1;  // where u starts on the line
-    int index;             // units seen
     bool live;
 
     __device__ __forceinline__ UnitIter(const PlanArgs &p, const PlanStart &ps) {
         x1 = ps.x1;
-        index = 0;
         live = ps.x0 < x1;
         if (!live) return;
         plan_seq(p, ps.b, u);
@@ -225,50 +242,45 @@ template <int ROWS> struct UnitIter {
         u.set_rows(p, ps.rt);
         ustart = ps.ustart;
         u.begin = (int)max(0ll, ps.x0 - ustart - p.extra);
-        if (!p.split && ps.x0 > ustart + p.extra) step(p);  // the piece before finishes it
+        // uncut, the unit is all of the piece's that its first tile lies in
+        if (!p.split && u.begin > 0) u.begin = u.ntiles;
         clip(p, ps);
     }
-    __device__ __forceinline__ int piece(const PlanStart &ps, long long x) const {
-        return (int)(((x + 1) * ps.pieces - 1) / ps.total);
-    }
-    // The tiles of u in this piece; none ends the piece.
+    // The tiles of u in this piece (there may be none of the first unit).
     __device__ __forceinline__ void clip(const PlanArgs &p, const PlanStart &ps) {
         const long long t0 = ustart + p.extra;
         live = live && t0 + u.begin < x1;
         u.end = p.split ? (int)min((long long)u.ntiles, x1 - t0) : u.ntiles;
         u.c0 = 0;
         u.parts = 1;
-        if (live && (u.begin > 0 || u.end < u.ntiles)) {
-            u.c0 = piece(ps, t0);
-            u.parts = piece(ps, t0 + u.ntiles - 1) - u.c0 + 1;
+        if (live && p.split && (u.begin > 0 || u.end < u.ntiles)) {
+            u.c0 = piece_of(t0, ps.pieces, ps.total);
+            u.parts = piece_of(t0 + u.ntiles - 1, ps.pieces, ps.total) - u.c0 + 1;
         }
     }
     // To the next unit of the line; there may be none behind this piece.
-    __device__ __forceinline__ void step(const PlanArgs &p) {
-        ustart += u.ntiles + p.extra;
-        u.begin = 0;
-        if (u.rt + 1 < u.nrt) {
-            u.set_rows(p, u.rt + 1);
-            return;
-        }
-        if (u.h + 1 < p.Hkv) {
-            ++u.h;
-            u.set_rows(p, 0);
-            return;
-        }
-        u.h = 0;
-        int b = u.b + 1;
-        for (; b < p.B; ++b)
-            if (plan_seq(p, b, u) && u.s.n > 0) break;
-        if (b < p.B) u.set_rows(p, 0);
-        else live = false;
-    }
     __device__ __forceinline__ void next(const PlanArgs &p, const PlanStart &ps) {
-        ++index;
         live = u.end == u.ntiles;
         if (!live) return;
-        step(p);
-        if (live) clip(p, ps);
+        ustart += u.ntiles + p.extra;
+        int rt = u.rt + 1;
+        if (rt == u.nrt) {
+            rt = 0;
+            if (++u.h == p.Hkv) {
+                u.h = 0;
+                int b = u.b + 1;
+#pragma unroll 1
+                for (; b < p.B; ++b)
+                    if (plan_seq(p, b, u) && u.s.n > 0) break;
+                if (b == p.B) {
+                    live = false;
+                    return;
+                }
+            }
+        }
+        u.set_rows(p, rt);
+        u.begin = 0;
+        clip(p, ps);
     }
 };
 
@@ -292,7 +304,7 @@ __device__ __forceinline__ float4 page_scales(const float *k_scale, const float 
     if (pid < 0) return make_float4(1.f, -INFINITY, 0.f, 0.f);
     const size_t at = (size_t)pid * Hkv + h;
     const float vs = __ldg(v_scale + at), e = vs > 0.f ? vs : LEAST_SCALE;
-    return make_float4(__ldg(k_scale + at), log2f(e), 1.f / e, vs > 0.f ? 1.f : 0.f);
+    return make_float4(__ldg(k_scale + at), __log2f(e), __fdividef(1.f, e), vs > 0.f ? 1.f : 0.f);
 }
 
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
@@ -331,14 +343,14 @@ template <int ROWS, int N> struct UnitRing {
     // One thread: unit number i (the last one has end == begin).
     __device__ __forceinline__ bool put(int i, const Unit<ROWS> &x, const DevCtx &ctx,
                                         volatile int *abort) {
-        if (i >= N && !mbar_wait(smem_u32(&empty[i % N]), (i / N - 1) & 1, ctx, abort))
+        if (i >= N && !bar_wait(smem_u32(&empty[i % N]), (i / N - 1) & 1, ctx, abort))
             return false;
         u[i % N] = x;
         mbar_arrive(smem_u32(&full[i % N]));
         return true;
     }
     __device__ __forceinline__ bool wait(int i, const DevCtx &ctx, volatile int *abort) {
-        return mbar_wait(smem_u32(&full[i % N]), (i / N) & 1, ctx, abort);
+        return bar_wait(smem_u32(&full[i % N]), (i / N) & 1, ctx, abort);
     }
     __device__ __forceinline__ void release(int i) { mbar_arrive(smem_u32(&empty[i % N])); }
 };

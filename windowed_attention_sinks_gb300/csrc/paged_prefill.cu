@@ -117,9 +117,13 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     }
     UnitIter<ROWS> it(p.plan, sm.plan);
     if (p.plan.split && lane == 0) write_note(it, p.ws);
+    int index = 0;
+#pragma unroll 1
     for (; it.live && ok; it.next(p.plan, sm.plan)) {
         const Unit<ROWS> &u = it.u;
-        if (lane == 0) ok = sm.units.put(it.index, u, ctx, &sm.abort);
+        if (u.begin == u.end) continue;
+        if (lane == 0) ok = sm.units.put(index, u, ctx, &sm.abort);
+        ++index;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
@@ -138,7 +142,7 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
                     const uint32_t dst = smem_u32(kv ? sm.v[st] : sm.k[st]);
                     bool go = true;
                     if (lane == 0) {
-                        if (use >= 1) go = mbar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
+                        if (use >= 1) go = bar_wait(empty, (use - 1) & 1, ctx, &sm.abort);
                         if (go) mbar_arrive_expect_tx(full, TILE * D);
                     }
                     ok = __shfl_sync(0xffffffffu, go ? 1 : 0, 0) != 0;
@@ -152,14 +156,14 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     }
     if (lane == 0 && ok) {
         Unit<ROWS> last{};
-        sm.units.put(it.index, last, ctx, &sm.abort);
+        sm.units.put(index, last, ctx, &sm.abort);
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     if (lane == 0) {  // copies in flight land before the CTA leaves
         int zero = 0;
         for (int i = 1; i <= STAGES && i <= t; ++i) {
-            mbar_wait(smem_u32(&sm.k_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
-            mbar_wait(smem_u32(&sm.v8_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
+            bar_wait(smem_u32(&sm.k_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
+            bar_wait(smem_u32(&sm.v8_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
         }
     }
 }
@@ -185,7 +189,7 @@ __device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &c
             for (int a = 0; a < nt; ++a, ++t) {
                 const int st = t % SRING, use = t / SRING;
                 if (use >= 1)
-                    ok = mbar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx, &sm.abort);
+                    ok = bar_wait(smem_u32(&sm.sc_empty[st]), (use - 1) & 1, ctx, &sm.abort);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const int sl = lane - a * per_tile;
@@ -230,14 +234,14 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
             const int b = t & 1, use = t >> 1, st = t % STAGES, ss = t % SRING;
             const int kpos0 = (t_first + j) * TILE;
             const bool edge = kpos0 < lo || kpos0 + TILE - 1 > hi;
-            if (!mbar_wait(smem_u32(&sm.v8_full[st]), (t / STAGES) & 1, ctx, abort)) return;
+            if (!bar_wait(smem_u32(&sm.v8_full[st]), (t / STAGES) & 1, ctx, abort)) return;
             uint4 x[PER];
 #pragma unroll
             for (int i = 0; i < PER; ++i)
                 x[i] = *reinterpret_cast<const uint4 *>(sm.v[st] + (i * 128 + tid) * 16);
             // values that no row sees may hold anything, NaN codes too, and the MMA
             // multiplies them by 0; a zero scale drops the values
-            if (!mbar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
+            if (!bar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
             if (edge || sm.zero[ss]) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
@@ -247,7 +251,7 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
                         x[i] = make_uint4(0, 0, 0, 0);
                 }
             }
-            if (use >= 1 && !mbar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
+            if (use >= 1 && !bar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
             uint8_t *dst = sm.v16[b];
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
@@ -276,12 +280,12 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, i
     constexpr uint32_t IDESC_O = idesc_f16_f32(128, D, 1);
     constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
     volatile int *abort = &sm.abort;
-    if (ctx.stall) mbar_wait(smem_u32(&sm.drain[half]), 0, ctx, abort);  // test hook: runs out
+    if (ctx.stall) bar_wait(smem_u32(&sm.drain[half]), 0, ctx, abort);  // test hook: runs out
     const uint64_t dq = desc_rows<D>(smem_u32(sm.q[half][0])), dk = desc_rows<D>(smem_u32(sm.k[0]));
     const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
     const uint32_t cols = tmem + (uint32_t)half * HALF_COLS;
     auto wait = [&](uint64_t &bar, int phase) {
-        return mbar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+        return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
     int sc = 0, pc = 0, ec = 0;  // S, P V and units issued
     int t0 = 0;                  // tiles before the unit's
@@ -351,7 +355,7 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, i
     }
     tc_commit(smem_u32(&sm.drain[half]));  // every MMA is done before TMEM goes
     int zero = 0;
-    mbar_wait(smem_u32(&sm.drain[half]), 0, ctx, &zero);
+    bar_wait(smem_u32(&sm.drain[half]), 0, ctx, &zero);
 }
 
 template <int D, int CW>  // CW: columns that share a page's scales (16 or 32)
@@ -364,7 +368,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
     volatile int *abort = &sm.abort;
     auto wait = [&](uint64_t &bar, int phase) {
-        return __all_sync(0xffffffffu, mbar_wait(smem_u32(&bar), phase & 1, ctx, abort));
+        return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
     int t0 = 0, done = 0, units = 0;  // CTA's tiles; this half's steps and units
     for (int i = 0;; ++i) {
@@ -393,52 +397,50 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         // ---- the row's Q: a power of two times it, split. The half's Q tile is free:
         // this warp has seen the last S that reads it
         float qf;
+        bool spoilt;
         {
-            uint4 v[D / 8];
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 p.q + (size_t)(u.s.t0 + (in ? tok : 0)) * p.q_stride +
                 (size_t)(in ? head : 0) * D);
-            float amax = 0.f;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+            uint32_t top = 0;  // the largest |q| of either half-word, as bf16 bits
 #pragma unroll
             for (int c = 0; c < D / 8; ++c) {
-                const uint32_t w[4] = {v[c].x, v[c].y, v[c].z, v[c].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float a = fabsf(__uint_as_float(w[e] << 16));
-                    const float b = fabsf(__uint_as_float(w[e] & 0xffff0000u));
-                    // inf and NaN set no scale
-                    amax = max3(amax, a < INFINITY ? a : 0.f, b < INFINITY ? b : 0.f);
-                }
+                const uint4 v = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
             }
-            // 2^k with amax 2^k in [128, 256)
-            int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
-            k = amax > 0.f ? max(-120, min(k, 120)) : 0;
+            top = max(top >> 16, top & 0xffffu);
+            spoilt = top >= 0x7f80u;  // an inf or a NaN
+            // 2^k with the largest |q| 2^k in [128, 256)
+            const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
             const float up = __uint_as_float((uint32_t)(127 + k) << 23);
+            // 64 columns at a time, read again (from L2): unrolled over all of them this
+            // would be as much code as the rest of the role
+#pragma unroll 1
+            for (int c0 = 0; c0 < D / 16; c0 += 4) {
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-                const uint32_t w[8] = {v[2 * c].x,     v[2 * c].y,     v[2 * c].z,
-                                       v[2 * c].w,     v[2 * c + 1].x, v[2 * c + 1].y,
-                                       v[2 * c + 1].z, v[2 * c + 1].w};
-                uint32_t hi[4], lo[4];
+                for (int c = c0; c < c0 + 4; ++c) {
+                    const uint4 v0 = in ? __ldg(src + 2 * c) : make_uint4(0, 0, 0, 0);
+                    const uint4 v1 = in ? __ldg(src + 2 * c + 1) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float a = __uint_as_float(w[e] << 16) * up;
-                    const float b = __uint_as_float(w[e] & 0xffff0000u) * up;
-                    uint32_t h = e4m3x2(a, b);
-                    if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
-                    if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
-                    const float2 back = e4m3x2_to_f32(h);
-                    const uint32_t l2 = e4m3x2(a - back.x, b - back.y);
-                    hi[e >> 1] = e & 1 ? hi[e >> 1] | h << 16 : h;
-                    lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+                    for (int e = 0; e < 8; ++e) {
+                        // by way of f16, which holds a scaled bf16 down to 2^-24
+                        const uint32_t ab = pack_f16x2(__uint_as_float(w[e] << 16) * up,
+                                                       __uint_as_float(w[e] & 0xffff0000u) * up);
+                        const uint32_t h = e4m3x2_of_f16x2(ab);
+                        const uint32_t l2 =
+                            e4m3x2_of_f16x2(difference_f16x2(ab, e4m3x2_to_f16x2(h)));
+                        hi[e >> 1] = e & 1 ? hi[e >> 1] | h << 16 : h;
+                        lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
+                    }
+                    const uint32_t at = sw_offset<D>(r & 127, c);
+                    *reinterpret_cast<uint4 *>(sm.q[half][0] + at) =
+                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(sm.q[half][1] + at) =
+                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                const uint32_t at = sw_offset<D>(r & 127, c);
-                *reinterpret_cast<uint4 *>(sm.q[half][0] + at) =
-                    make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4 *>(sm.q[half][1] + at) =
-                    make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
             qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
             fence_proxy_async_smem();
@@ -513,12 +515,13 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 }
                 return true;
             };
-            load();
-            if (__any_sync(0xffffffffu, m == NOTHING) && !move()) return;
             uint32_t pw[32];
             float sum;
+            bool moves = __any_sync(0xffffffffu, m == NOTHING);
 #pragma unroll 1
             for (;;) {
+                load();
+                if (moves && !move()) return;
                 // P of the row's 64 keys with m as it is, and their sum
                 const float base = m == NOTHING ? BASE : BASE - m;
                 float raw = 0.f;
@@ -548,9 +551,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                     sum = fmaf(a + b, s.z, sum);
                 }
                 // no value is above the sum, so below the limit none has left f16's range
-                if (!__any_sync(0xffffffffu, raw > SUM_LIMIT)) break;
-                load();
-                if (!move()) return;
+                moves = __any_sync(0xffffffffu, raw > SUM_LIMIT);
+                if (!moves) break;
             }
             l += sum;
             tmem_st32(s_tmem, pw);
@@ -568,8 +570,9 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         ++units;
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
-        float lse2 = l == 0.f ? -INFINITY : m - BASE + log2f(l);
-        float inv = l == 0.f ? 0.f : 1.f / l;
+        if (spoilt) l = NAN;
+        float lse2 = l == 0.f ? -INFINITY : m - BASE + __log2f(l);
+        float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
         const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
         const size_t orow = (size_t)(u.s.t0 + tok) * p.H + head;
@@ -682,6 +685,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     }
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
