@@ -12,9 +12,11 @@
 // amax / 448 scale, of which a power of two costs at most one bit of range.
 //
 // One unit of work is (page touched, key or value, KV head): its amax must be
-// known before the first code is written, so NT threads hold the rows in
-// registers (up to 4 items of 16 columns each), take the amax over the group and
-// then write; rows beyond that are read again (they are in L2 by then). Two
+// known before the first code is written, so NT threads hold the rows as they
+// were read (up to HELD items of 16 columns each), take the amax over the group
+// and then write, turning the keys a second time rather than keeping them in fp32: what
+// counts is how much is in flight, and that goes by the registers. Rows
+// beyond HELD are read again (they are in L2 by then). Two
 // ways to number the pages that a call touches, from its sizes alone:
 //   few tokens a sequence:  unit = token, dropped unless it is the first of
 //                           the call in its page; NT = 32;
@@ -31,22 +33,39 @@ namespace sattn {
 namespace {
 
 constexpr int THREADS = 256;
-constexpr int HELD = 4;  // items a thread keeps in registers
-
-__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 y = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight values as they lie in memory.
+template <typename T> struct Raw8;
+template <> struct Raw8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
     }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+        v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <> struct Raw8<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) {
+        a = __ldg(reinterpret_cast<const uint4 *>(p));
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+// Items that a thread holds: 128 bytes.
+template <typename T> constexpr int HELD = sizeof(T) == 2 ? 4 : 2;
+__device__ __forceinline__ void load8(const float *p, float (&v)[8]) {
+    Raw8<float> r;
+    r.load(p);
+    r.get(v);
 }
 __device__ __forceinline__ void store8(float *p, const float (&v)[8]) {
     reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -157,12 +176,18 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
     const size_t stride = is_v ? p.v_stride : p.k_stride;
     const int ic = p.d / 16, items = rows * ic, rd = is_v ? 0 : p.rd;
 
-    auto fetch = [&](int it, float (&a)[8], float (&bb)[8]) {
+    using Raw = Raw8<T>;
+    auto fetch = [&](int it, Raw &a, Raw &b2) {
         const int r = it / ic, c = it % ic;
         const Cols k = item_cols(c, rd, p.interleaved);
-        load8(src + r * stride + k.a, a);
-        load8(src + r * stride + k.b, bb);
-        if (k.turn) {
+        a.load(src + r * stride + k.a);
+        b2.load(src + r * stride + k.b);
+    };
+    auto values = [&](int it, const Raw &x, const Raw &y, float (&a)[8], float (&bb)[8]) {
+        x.get(a);
+        y.get(bb);
+        const int r = it / ic, c = it % ic;
+        if (16 * c < rd) {
             float cs[8], sn[8];
             const float *e = p.cos_sin + (size_t)(pos + r) * p.rd + 8 * c;
             load8(e, cs);
@@ -171,17 +196,25 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
         }
     };
 
-    float a[HELD][8], c[HELD][8];
+    constexpr int N = HELD<T>;
+    Raw ra[N], rb[N];
     float amax = 0.f;
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
+    for (int k = 0; k < N; ++k)
+        if (tid + k * NT < items) fetch(tid + k * NT, ra[k], rb[k]);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
         if (tid + k * NT < items) {
-            fetch(tid + k * NT, a[k], c[k]);
-            amax = fmaxf(amax, amax16(a[k], c[k]));
+            float y[8], z[8];
+            values(tid + k * NT, ra[k], rb[k], y, z);
+            amax = fmaxf(amax, amax16(y, z));
         }
-    for (int it = tid + HELD * NT; it < items; it += NT) {
+#pragma unroll 1
+    for (int it = tid + N * NT; it < items; it += NT) {
+        Raw x0, x1;
         float y[8], z[8];
-        fetch(it, y, z);
+        fetch(it, x0, x1);
+        values(it, x0, x1, y, z);
         amax = fmaxf(amax, amax16(y, z));
     }
     if (pid < 0 || pid >= p.num_pages) {  // the same for the whole unit
@@ -222,11 +255,18 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
         *reinterpret_cast<uint2 *>(at + k.b) = code8(z, inv);
     };
 #pragma unroll
-    for (int k = 0; k < HELD; ++k)
-        if (tid + k * NT < items) put(tid + k * NT, a[k], c[k]);
-    for (int it = tid + HELD * NT; it < items; it += NT) {
+    for (int k = 0; k < N; ++k)
+        if (tid + k * NT < items) {
+            float y[8], z[8];
+            values(tid + k * NT, ra[k], rb[k], y, z);
+            put(tid + k * NT, y, z);
+        }
+#pragma unroll 1
+    for (int it = tid + N * NT; it < items; it += NT) {
+        Raw x0, x1;
         float y[8], z[8];
-        fetch(it, y, z);
+        fetch(it, x0, x1);
+        values(it, x0, x1, y, z);
         put(it, y, z);
     }
     if (row0 > 0 && now != old) {  // the page's other rows move to the new scale
@@ -247,47 +287,65 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
     if (tid == 0) *scale = now;
 }
 
-// Rotated queries: 128 threads a token, a thread keeps its columns' angles for
-// several heads.
+// Rotated queries: 64 threads a token; a thread keeps its columns' angles for
+// its heads, and loads up to HELD of them before it needs to know the
+// token's position.
 template <typename T>
 __device__ __forceinline__ void rotate_queries(const PagedAppendArgs &p, long long t,
                                                unsigned &err) {
     if (t >= p.T) return;
-    const int b = warp_find(p.B, t, [&](int i) { return (long long)__ldg(p.cu_seqlens + i); });
-    PagedSeq s;
-    if (!append_seq(p, b, s, err)) return;
-    const int i = (int)t - s.t0;
-    if (i < 0 || i >= s.n) return;
-    const int pos = s.len - s.n + i;
-    const int ic = p.d / 16, c = threadIdx.x % ic;
+    constexpr int N = HELD<T>;
+    const int ic = p.d / 16, c = threadIdx.x % ic, lanes = 64 / ic, h0 = threadIdx.x % 64 / ic;
     const Cols k = item_cols(c, p.rd, p.interleaved);
+    const T *src = static_cast<const T *>(p.q) + (size_t)t * p.q_stride;
+    T *dst = static_cast<T *>(p.q_out) + (size_t)t * p.H * p.d;
+    Raw8<T> a[N], b[N];
+    auto fetch = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (h + i * lanes < p.H) {
+                a[i].load(src + (size_t)(h + i * lanes) * p.d + k.a);
+                b[i].load(src + (size_t)(h + i * lanes) * p.d + k.b);
+            }
+    };
+    fetch(h0);
+    const int bs = warp_find(p.B, t, [&](int i) { return (long long)__ldg(p.cu_seqlens + i); });
+    PagedSeq s;
+    if (!append_seq(p, bs, s, err)) return;
+    const int i0 = (int)t - s.t0;
+    if (i0 < 0 || i0 >= s.n) return;
+    const int pos = s.len - s.n + i0;
     float cs[8], sn[8];
     if (k.turn) {
         const float *e = p.cos_sin + (size_t)pos * p.rd + 8 * c;
         load8(e, cs);
         load8(e + p.rd / 2, sn);
     }
-    for (int h = threadIdx.x % 128 / ic; h < p.H; h += 128 / ic) {
-        float a[8], bb[8];
-        const T *src = static_cast<const T *>(p.q) + (size_t)t * p.q_stride + (size_t)h * p.d;
-        T *dst = static_cast<T *>(p.q_out) + ((size_t)t * p.H + h) * p.d;
-        load8(src + k.a, a);
-        load8(src + k.b, bb);
-        if (k.turn) turn(a, bb, cs, sn, p.interleaved);
-        store8(dst + k.a, a);
-        store8(dst + k.b, bb);
+#pragma unroll 1
+    for (int h = h0; h < p.H; h += N * lanes) {
+        if (h > h0) fetch(h);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (h + i * lanes < p.H) {
+                float x[8], y[8];
+                a[i].get(x);
+                b[i].get(y);
+                if (k.turn) turn(x, y, cs, sn, p.interleaved);
+                store8(dst + (size_t)(h + i * lanes) * p.d + k.a, x);
+                store8(dst + (size_t)(h + i * lanes) * p.d + k.b, y);
+            }
     }
 }
 
 template <typename T, int NT>
-__global__ void __launch_bounds__(THREADS) append_kernel(const PagedAppendArgs p, const DevCtx ctx) {
+__global__ void __launch_bounds__(THREADS, 3) append_kernel(const PagedAppendArgs p, const DevCtx ctx) {
     __shared__ float red[THREADS / 32];
     unsigned err = 0;
     if (blockIdx.x < p.unit_blocks) {
         const long long u = (long long)blockIdx.x * (THREADS / NT) + threadIdx.x / NT;
         if (u < p.units) append_unit<T, NT>(p, u, red, err);
     } else {
-        rotate_queries<T>(p, (long long)(blockIdx.x - p.unit_blocks) * 2 + threadIdx.x / 128, err);
+        rotate_queries<T>(p, (long long)(blockIdx.x - p.unit_blocks) * 4 + threadIdx.x / 64, err);
     }
     if (err && (threadIdx.x & 31) == 0) record_error(ctx, err);
 }
@@ -295,7 +353,7 @@ __global__ void __launch_bounds__(THREADS) append_kernel(const PagedAppendArgs p
 template <typename T, int NT>
 cudaError_t launch(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
     const long long ub = (p.units + THREADS / NT - 1) / (THREADS / NT);
-    const long long qb = p.q ? ((long long)p.T + 1) / 2 : 0;
+    const long long qb = p.q ? ((long long)p.T + 3) / 4 : 0;
     if (ub + qb > INT_MAX) return cudaErrorInvalidValue;
     p.unit_blocks = (unsigned)ub;
     append_kernel<T, NT><<<(unsigned)(ub + qb), THREADS, 0, s>>>(p, make_ctx(dev));
@@ -308,7 +366,7 @@ cudaError_t pick(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
     p.by_token = p.T <= slots;
     p.units = (p.by_token ? p.T : slots) * 2 * p.Hkv;
     // whole pages: as many threads as hold one in registers
-    const int want = p.by_token ? 32 : p.page * p.d / (16 * HELD);
+    const int want = p.by_token ? 32 : p.page * p.d / (16 * HELD<T>);
     if (want <= 32) return launch<T, 32>(p, dev, s);
     if (want <= 64) return launch<T, 64>(p, dev, s);
     if (want <= 128) return launch<T, 128>(p, dev, s);

@@ -239,6 +239,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
     // copies in flight land before the CTA leaves (at once on the normal path)
     if (lane == 0) {
         int zero = 0;
+#pragma unroll 1
         for (int i = 1; i <= C::STAGES && i <= t; ++i) {
             bar_wait(smem_u32(&sm.k_full[(t - i) % C::STAGES]), ((t - i) / C::STAGES) & 1, ctx,
                       &zero);
@@ -264,6 +265,10 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         if (lane == 0) sm.units.release(n);
         if (u.begin == u.end) break;
         const int w = n % C::QB;
+        static_assert(R <= 32, "a row a lane");
+        const int row0 = u.row0 + lane, tok0 = p.plan.token(row0), head0 = u.h * G + row0 - tok0 * G;
+        const bool in = lane < R && lane < u.nrows;
+        const float sink = in && p.sinks ? __ldg(p.sinks + head0) * LOG2E : 0.f;
         // four items a lane in registers at a time; with more rows they are read
         // again for the second pass (from L1)
         constexpr int B = PER < 4 ? PER : 4;
@@ -280,7 +285,7 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                         (size_t)(u.h * G + row - tok * G) * D + 8 * c));
             }
         };
-        float amax = 0.f;
+        uint32_t top = 0;  // the largest finite |q| of either half-word, as bf16 bits
 #pragma unroll 1
         for (int i0 = 0; i0 < PER; i0 += B) {
             load(i0);
@@ -289,17 +294,14 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                 const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = fabsf(__uint_as_float(v[e] << 16));
-                    const float b = fabsf(__uint_as_float(v[e] & 0xffff0000u));
-                    if (a < INFINITY) amax = fmaxf(amax, a);  // NaN and inf set no scale
-                    if (b < INFINITY) amax = fmaxf(amax, b);
+                    const uint32_t a = v[e] & 0x7fff7fffu;  // inf and NaN set no scale
+                    top = __vmaxu2(top, a & __vcmpltu2(a, 0x7f807f80u));
                 }
             }
         }
-        amax = warp_max(amax);
-        // 2^k with amax 2^k in [128, 256), k within fp32's normal range
-        int k = 7 - ((int)(__float_as_uint(amax) >> 23) - 127);
-        k = amax > 0.f ? max(-120, min(k, 120)) : 0;
+        top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
+        // 2^k with the largest |q| 2^k in [128, 256), k within fp32's normal range
+        const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
         const float up = __uint_as_float((uint32_t)(127 + k) << 23);
         if (n >= C::QB)
             ok = bar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
@@ -315,14 +317,15 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                 uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float a = __uint_as_float(v[e] << 16) * up;
-                    const float b = __uint_as_float(v[e] & 0xffff0000u) * up;
-                    uint32_t h = e4m3x2(a, b);
-                    if (!(fabsf(a) < INFINITY)) h |= 0x7fu;  // inf and NaN spoil their own row
-                    if (!(fabsf(b) < INFINITY)) h |= 0x7f00u;
-                    const float2 back = e4m3x2_to_f32(h);
+                    // by way of f16, which holds a scaled bf16 down to 2^-24; inf and NaN
+                    // become NaN and spoil their own row
+                    const uint32_t ab = pack_f16x2(__uint_as_float(v[e] << 16) * up,
+                                                   __uint_as_float(v[e] & 0xffff0000u) * up) |
+                                        (__vcmpgeu2(v[e] & 0x7fff7fffu, 0x7f807f80u) & 0x7fff7fffu);
+                    const uint32_t h = e4m3x2_of_f16x2(ab);
                     hi[e >> 1] |= h << (16 * (e & 1));
-                    lo[e >> 1] |= e4m3x2((a - back.x) * 16.f, (b - back.y) * 16.f) << (16 * (e & 1));
+                    lo[e >> 1] |= e4m3x2_of_f16x2(sixteen_times_difference(ab, e4m3x2_to_f16x2(h)))
+                                  << (16 * (e & 1));
                 }
                 // 8 bytes: half of the 16-byte unit c / 2
                 *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(r, c >> 1) + 8 * (c & 1)) =
@@ -331,12 +334,10 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                     make_uint2(lo[0], lo[1]);
             }
         }
-        for (int r = lane; r < R; r += 32) {
-            const int row = u.row0 + r, tok = p.plan.token(row), head = u.h * G + row - tok * G;
-            const bool in = r < u.nrows;
-            sm.orow[w][r] = in ? (long long)(u.s.t0 + tok) * p.H + head : -1;
-            sm.rpos[w][r] = u.s.len - u.s.n + tok;
-            sm.rsink[w][r] = in && p.sinks ? __ldg(p.sinks + head) * LOG2E : 0.f;
+        if (lane < R) {
+            sm.orow[w][lane] = in ? (long long)(u.s.t0 + tok0) * p.H + head0 : -1;
+            sm.rpos[w][lane] = u.s.len - u.s.n + tok0;
+            sm.rsink[w][lane] = sink;
         }
         if (lane == 0) sm.qf[w] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
         fence_proxy_async_smem();
@@ -468,14 +469,17 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
     constexpr int E = D / 32;
     // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ...
     auto slot = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
+#pragma unroll 1
     for (int r = warp; r < R; r += warps) {
         const long long row = orow[r];
         if (row < 0) continue;
         float m = -INFINITY;
+#pragma unroll 1
         for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(plse + slot(i) * R + r));
         m = warp_max(m);
         float acc[E] = {};
         float z = 0.f;
+#pragma unroll 1
         for (int i0 = 0; i0 < parts; i0 += 32) {
             // only -inf counts as nothing: a NaN denominator (a NaN key) stays
             const float l = i0 + lane < parts ? __ldcg(plse + slot(i0 + lane) * R + r) : -INFINITY;
@@ -821,26 +825,31 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         return;
     }
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < C::STAGES; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 1);
             mbar_init(smem_u32(&sm.k_empty[i]), 1);
             mbar_init(smem_u32(&sm.v_full[i]), 1);
             mbar_init(smem_u32(&sm.v_empty[i]), 1);
         }
+#pragma unroll 1
         for (int i = 0; i < SRING; ++i) {
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 4);
         }
+#pragma unroll 1
         for (int i = 0; i < C::QB; ++i) {
             mbar_init(smem_u32(&sm.q_full[i]), 1);
             mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);  // the MMAs and the softmax warps
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.p_full[i]), 4);
             mbar_init(smem_u32(&sm.pv_done[i]), 1);
             mbar_init(smem_u32(&sm.o_empty[i]), 8);
             mbar_init(smem_u32(&sm.drain[i]), 1);
         }
+#pragma unroll 1
         for (int i = 0; i < C::SBUF; ++i) {
             mbar_init(smem_u32(&sm.s_full[i]), 1);
             mbar_init(smem_u32(&sm.s_empty[i]), 4);

@@ -335,6 +335,7 @@ template <int ROWS, int N> struct UnitRing {
     uint64_t full[N], empty[N];
 
     __device__ __forceinline__ void init(int readers) {
+#pragma unroll 1
         for (int i = 0; i < N; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), readers);

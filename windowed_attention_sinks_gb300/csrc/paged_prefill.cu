@@ -161,6 +161,7 @@ __device__ void load_tiles(const PrefillParams &p, const CUtensorMap *tk, const 
     if (__any_sync(0xffffffffu, bad) && lane == 0) record_error(ctx, DEVERR_INDEX);
     if (lane == 0) {  // copies in flight land before the CTA leaves
         int zero = 0;
+#pragma unroll 1
         for (int i = 1; i <= STAGES && i <= t; ++i) {
             bar_wait(smem_u32(&sm.k_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
             bar_wait(smem_u32(&sm.v8_full[(t - i) % STAGES]), ((t - i) / STAGES) & 1, ctx, &zero);
@@ -630,12 +631,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
         return;
     }
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < STAGES; ++i) {
             mbar_init(smem_u32(&sm.k_full[i]), 1);
             mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both halves' MMAs
             mbar_init(smem_u32(&sm.v8_full[i]), 1);
             mbar_init(smem_u32(&sm.v8_empty[i]), 128);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sm.v_full[i]), 128);
             mbar_init(smem_u32(&sm.v_empty[i]), 2);
@@ -649,6 +652,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.o_full[i]), 1);
             mbar_init(smem_u32(&sm.o_empty[i]), 4);
         }
+#pragma unroll 1
         for (int i = 0; i < SRING; ++i) {
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
