@@ -287,15 +287,20 @@ __device__ __forceinline__ void append_unit(const PagedAppendArgs &p, long long 
     if (tid == 0) *scale = now;
 }
 
-// Rotated queries: 64 threads a token; a thread keeps its columns' angles for
-// its heads, and loads up to HELD of them before it needs to know the
-// token's position.
+// Threads that rotate the queries of a token: 64, or 32 where so few items make
+// HELD for each of those.
+template <typename T> __host__ __device__ constexpr int query_threads(int H, int d) {
+    return H * (d / 16) <= 32 * HELD<T> ? 32 : 64;
+}
+
+// Rotated queries of a token; a thread keeps its columns' angles for its heads,
+// and loads up to HELD of them before it needs to know the token's position.
 template <typename T>
-__device__ __forceinline__ void rotate_queries(const PagedAppendArgs &p, long long t,
+__device__ __forceinline__ void rotate_queries(const PagedAppendArgs &p, long long t, int threads,
                                                unsigned &err) {
     if (t >= p.T) return;
     constexpr int N = HELD<T>;
-    const int ic = p.d / 16, c = threadIdx.x % ic, lanes = 64 / ic, h0 = threadIdx.x % 64 / ic;
+    const int ic = p.d / 16, c = threadIdx.x % ic, lanes = threads / ic, h0 = threadIdx.x % threads / ic;
     const Cols k = item_cols(c, p.rd, p.interleaved);
     const T *src = static_cast<const T *>(p.q) + (size_t)t * p.q_stride;
     T *dst = static_cast<T *>(p.q_out) + (size_t)t * p.H * p.d;
@@ -345,7 +350,9 @@ __global__ void __launch_bounds__(THREADS, 3) append_kernel(const PagedAppendArg
         const long long u = (long long)blockIdx.x * (THREADS / NT) + threadIdx.x / NT;
         if (u < p.units) append_unit<T, NT>(p, u, red, err);
     } else {
-        rotate_queries<T>(p, (long long)(blockIdx.x - p.unit_blocks) * 4 + threadIdx.x / 64, err);
+        const int n = query_threads<T>(p.H, p.d);
+        rotate_queries<T>(
+            p, (long long)(blockIdx.x - p.unit_blocks) * (THREADS / n) + threadIdx.x / n, n, err);
     }
     if (err && (threadIdx.x & 31) == 0) record_error(ctx, err);
 }
@@ -353,7 +360,8 @@ __global__ void __launch_bounds__(THREADS, 3) append_kernel(const PagedAppendArg
 template <typename T, int NT>
 cudaError_t launch(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
     const long long ub = (p.units + THREADS / NT - 1) / (THREADS / NT);
-    const long long qb = p.q ? ((long long)p.T + 3) / 4 : 0;
+    const int per = p.q ? THREADS / query_threads<T>(p.H, p.d) : 1;
+    const long long qb = p.q ? ((long long)p.T + per - 1) / per : 0;
     if (ub + qb > INT_MAX) return cudaErrorInvalidValue;
     p.unit_blocks = (unsigned)ub;
     append_kernel<T, NT><<<(unsigned)(ub + qb), THREADS, 0, s>>>(p, make_ctx(dev));
