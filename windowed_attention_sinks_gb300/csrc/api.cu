@@ -21,7 +21,7 @@ __device__ unsigned g_error_word;
 // on its own 128-byte line.
 constexpr unsigned kClaimStride = 32;
 __device__ unsigned g_claims[kClaimCounters * kClaimStride];
-__device__ unsigned g_joins[kClaimCounters * kJoinPieces];
+__device__ unsigned g_joins[kJoinSets * kJoinPieces];
 
 namespace {
 
@@ -104,9 +104,14 @@ unsigned *launch_claim_counter(const DevInfo &dev, cudaStream_t s, cudaError_t *
     return *e == cudaSuccess ? c : nullptr;
 }
 
-unsigned *next_join_counters(const DevInfo &dev) {
-    static std::atomic<unsigned> next{0};
-    return dev.joins + (size_t)(next.fetch_add(1) % kClaimCounters) * kJoinPieces;
+unsigned *next_join_counters(const DevInfo &dev, cudaStream_t s) {
+    static std::atomic<unsigned> next{0}, captured{0};
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    const bool eager =
+        cudaStreamIsCapturing(s, &st) == cudaSuccess && st == cudaStreamCaptureStatusNone;
+    const unsigned set = eager ? next.fetch_add(1) % kClaimCounters
+                               : kClaimCounters + captured.fetch_add(1) % kCapturedJoinSets;
+    return dev.joins + (size_t)set * kJoinPieces;
 }
 
 cudaError_t ensure_smem_attr(const void *kernel, size_t bytes, const DevInfo &dev) {
@@ -227,7 +232,7 @@ sattn_status sattn_check_device(void *cuda_stream) {
         if (cudaMemcpy(dev->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
             return SATTN_ERR_CUDA;
         if ((word & DEVERR_TIMEOUT) &&
-            cudaMemset(dev->joins, 0, sizeof(unsigned) * kClaimCounters * kJoinPieces) != cudaSuccess)
+            cudaMemset(dev->joins, 0, sizeof(unsigned) * kJoinSets * kJoinPieces) != cudaSuccess)
             return SATTN_ERR_CUDA;
     }
     if (word & DEVERR_TIMEOUT) return SATTN_ERR_TIMEOUT;
@@ -597,7 +602,8 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
     cudaStream_t s = as_stream(cuda_stream);
     PagedArgs a{q, q_stride, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens, kv_lens,
                 B, T, max_q_len, H, Hkv, d, num_pages, page_size, max_pages, causal,
-                window_left < 0 ? -1 : window_left, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
+                window_left < 0 || window_left >= 1 << 30 ? -1 : window_left,  // no position is as far
+                sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
                 (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
     if (dtype == SATTN_F32) return finish(launch_paged_simt(a, *dev, s), s);
     return finish(paged_few_rows(max_q_len, H / Hkv) ? launch_paged_decode(a, *dev, s)

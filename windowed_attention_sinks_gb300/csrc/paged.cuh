@@ -75,4 +75,10 @@ __device__ __forceinline__ float pow2_scale(float amax) {
     return e < 63 ? LEAST_SCALE : __uint_as_float((uint32_t)e << 23);
 }
 
+// A sink in log2 units. The largest finite values stay finite (the factor would
+// take them to infinity): key 0 alone has weight 1 whatever its bias.
+__device__ __forceinline__ float sink_log2(float s) {
+    return isinf(s) ? s : fminf(fmaxf(s * 1.4426950408889634f, -3e38f), 3e38f);
+}
+
 }  // namespace sattn

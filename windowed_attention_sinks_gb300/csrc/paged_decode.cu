@@ -14,8 +14,8 @@
 //    lo / 16 with hi = e4m3(x) and lo = e4m3(16 (x - hi)), side by side as 2R
 //    columns, joined again in fp32. hi + lo / 16 has 8 significant bits, a
 //    bf16's, for |x| from 2^-6 to 448, and an absolute error of at most 2^-14
-//    below that. The unit's Q is scaled by a power of two so that its largest value is
-//    in [128, 256): bf16 queries go in exactly down to 2^-14 of the largest.
+//    below that. Each row of Q is scaled by a power of two so that its largest value is
+//    in [128, 256): bf16 queries go in exactly down to 2^-14 of the row's largest.
 //    P is 2^(4 + e - m) <= 2^8 with e the exponent below, so the floor
 //    is 2^-18 .. 2^-22 of the largest weight. The extra columns are free: the
 //    MMA is a small part of the time a tile takes to arrive.
@@ -56,12 +56,12 @@ constexpr int UNITS = 8;  // units handed on ahead
 constexpr int SOLO = 2;   // tiles of a unit that one group takes alone
 constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
 constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
-constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
 
 struct DecodeParams {
     PlanArgs plan;
     const __nv_bfloat16 *q;
     int64_t q_stride;
+    const uint8_t *v_cache;
     const float *k_scale, *v_scale;
     const int32_t *page_table;
     int H, num_pages, page, page_shift, max_pages;
@@ -103,7 +103,7 @@ template <int D, int R> struct alignas(1024) Smem {
     long long orow[C::QB][R];   // output row of each query row, -1 past the last
     int rpos[C::QB][R];         // its position
     float rsink[C::QB][R];      // its sink (log2 units)
-    float qf[C::QB];            // scale log2(e) / the power of two in Q
+    alignas(16) float qf[C::QB][R];  // its scale log2(e) / the power of two in its Q
     PlanStart plan;
     UnitRing<R, UNITS> units;
     uint64_t k_full[C::STAGES], k_empty[C::STAGES], v_full[C::STAGES], v_empty[C::STAGES];
@@ -249,7 +249,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
     }
 }
 
-// Q of a unit: scaled by a power of two, split into hi and 16 lo, K-major rows
+// Q of a unit: each row scaled by a power of two, split into hi and 16 lo, K-major rows
 // hi 0 .. R-1, lo R .. 2R-1. A lane holds 8 columns, CH lanes a row.
 template <int D, int R>
 __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx &ctx) {
@@ -268,12 +268,11 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
         static_assert(R <= 32, "a row a lane");
         const int row0 = u.row0 + lane, tok0 = p.plan.token(row0), head0 = u.h * G + row0 - tok0 * G;
         const bool in = lane < R && lane < u.nrows;
-        const float sink = in && p.sinks ? __ldg(p.sinks + head0) * LOG2E : 0.f;
-        // four items a lane in registers at a time; with more rows they are read
-        // again for the second pass (from L1)
-        constexpr int B = PER < 4 ? PER : 4;
-        uint4 x[B];
-        auto load = [&](int i0) {
+        const float sink = in && p.sinks ? sink_log2(__ldg(p.sinks + head0)) : 0.f;
+        constexpr int B = PER < 4 ? PER : 4;  // items in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < PER; i0 += B) {
+            uint4 x[B];
 #pragma unroll
             for (int i = 0; i < B; ++i) {
                 const int r = ((i0 + i) * 32 + lane) / CH, c = ((i0 + i) * 32 + lane) % CH;
@@ -284,36 +283,27 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                         p.q + (size_t)(u.s.t0 + tok) * p.q_stride +
                         (size_t)(u.h * G + row - tok * G) * D + 8 * c));
             }
-        };
-        uint32_t top = 0;  // the largest finite |q| of either half-word, as bf16 bits
-#pragma unroll 1
-        for (int i0 = 0; i0 < PER; i0 += B) {
-            load(i0);
+            if (i0 == 0 && n >= C::QB)
+                ok = bar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
 #pragma unroll
             for (int i = 0; i < B; ++i) {
+                const int r = ((i0 + i) * 32 + lane) / CH, c = ((i0 + i) * 32 + lane) % CH;
                 const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t top = 0;  // the row's largest finite |q|, as bf16 bits
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t a = v[e] & 0x7fff7fffu;  // inf and NaN set no scale
                     top = __vmaxu2(top, a & __vcmpltu2(a, 0x7f807f80u));
                 }
-            }
-        }
-        top = __reduce_max_sync(0xffffffffu, max(top >> 16, top & 0xffffu));
-        // 2^k with the largest |q| 2^k in [128, 256), k within fp32's normal range
-        const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
-        const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-        if (n >= C::QB)
-            ok = bar_wait(smem_u32(&sm.q_empty[w]), (n / C::QB - 1) & 1, ctx, &sm.abort);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-#pragma unroll 1
-        for (int i0 = 0; i0 < PER; i0 += B) {
-            if (PER > B) load(i0);
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int r = ((i0 + i) * 32 + lane) / CH, c = ((i0 + i) * 32 + lane) % CH;
-                const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                for (int o = 1; o < CH; o <<= 1)
+                    top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = max(top >> 16, top & 0xffffu);
+                // 2^k with the largest |q| 2^k in [128, 256), k within fp32's normal range
+                const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
+                const float up = __uint_as_float((uint32_t)(127 + k) << 23);
                 uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -332,14 +322,16 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                     make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2 *>(sm.q[w] + sw_offset<D>(R + r, c >> 1) + 8 * (c & 1)) =
                     make_uint2(lo[0], lo[1]);
+                if (c == 0)
+                    sm.qf[w][r] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
             }
         }
+        if (!ok) break;
         if (lane < R) {
             sm.orow[w][lane] = in ? (long long)(u.s.t0 + tok0) * p.H + head0 : -1;
             sm.rpos[w][lane] = u.s.len - u.s.n + tok0;
             sm.rsink[w][lane] = sink;
         }
-        if (lane == 0) sm.qf[w] = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.q_full[w]));
@@ -458,13 +450,13 @@ template <int R> __device__ __forceinline__ void column_sums(float (&l)[R], floa
     out[row] = l[0];
 }
 
-// Joins the parts of a cut unit: lse = log sum_c 2^lse2_c (+ the null logit),
-// o = sum_c 2^(lse2_c - lse) o_c, in the order of the pieces. A warp a row:
-// lane c holds part c's denominator, the columns are spread over the lanes.
+// Joins the parts of a cut unit: w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
+// null logit), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces. A warp a row:
+// lane c holds part c's sums, the columns are spread over the lanes.
 template <int D, int R>
 __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long long *orow,
                            const float *rsink, int warp, int warps, int lane) {
-    const float *plse = reinterpret_cast<const float *>(p.ws + plan_lse_offset());
+    const float2 *sums = part_sums(p.ws);
     const float *prow = reinterpret_cast<const float *>(p.ws + plan_rows_offset(R));
     constexpr int E = D / 32;
     // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ...
@@ -473,17 +465,19 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
     for (int r = warp; r < R; r += warps) {
         const long long row = orow[r];
         if (row < 0) continue;
-        float m = -INFINITY;
+        float m = NOTHING;
 #pragma unroll 1
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(plse + slot(i) * R + r));
+        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(sums + slot(i) * R + r).x);
         m = warp_max(m);
         float acc[E] = {};
         float z = 0.f;
 #pragma unroll 1
         for (int i0 = 0; i0 < parts; i0 += 32) {
-            // only -inf counts as nothing: a NaN denominator (a NaN key) stays
-            const float l = i0 + lane < parts ? __ldcg(plse + slot(i0 + lane) * R + r) : -INFINITY;
-            const float wt = l == -INFINITY ? 0.f : ex2(l - m);
+            float wt = 0.f;
+            if (i0 + lane < parts) {
+                const float2 s = __ldcg(sums + slot(i0 + lane) * R + r);
+                wt = s.y * ex2(s.x - m);
+            }
             z += warp_sum(wt);
             const int cnt = min(32, parts - i0);
 #pragma unroll 8
@@ -559,7 +553,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 wait(sm.both, meets++);
             }
         };
-        const float qf = sm.qf[w];
+        const float4 *qf4 = reinterpret_cast<const float4 *>(sm.qf[w]);
         // m is the group's and lies in shared memory: 32 rows of it would not fit
         // beside the scores and sums in registers
         const float4 *m4 = reinterpret_cast<const float4 *>(sm.mx[w][g]);
@@ -576,10 +570,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             const float4 sc = sm.sc[ss][key >> p.page_shift];
             wait(sm.s_full[sb], t / C::SBUF);
             tc_fence_after();
-            const float f = sc.x * qf;
             float x[R];  // e of this key for every row
             {
-                const float flo = f * 0.0625f;
                 constexpr int CH = R < 16 ? R : 16;
 #pragma unroll
                 for (int c = 0; c < R; c += CH) {
@@ -593,9 +585,14 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     }
                     tc_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < CH; ++e)
-                        x[c + e] = fmaf(__uint_as_float(lo[e]), flo,
-                                        fmaf(__uint_as_float(hi[e]), f, sc.y));
+                    for (int e = 0; e < CH; ++e) {
+                        const float4 f = qf4[(c + e) / 4];
+                        x[c + e] = fmaf(fmaf(__uint_as_float(lo[e]), 0.0625f,
+                                             __uint_as_float(hi[e])),
+                                        sc.x * (e % 4 == 0 ? f.x : e % 4 == 1 ? f.y
+                                                : e % 4 == 2 ? f.z : f.w),
+                                        sc.y);
+                    }
                 }
             }
             tc_fence_before();
@@ -621,15 +618,23 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             }
             // values that no row sees may hold anything, NaN codes too, and the MMA
             // multiplies them by 0: they are cleared, and so are those of a zero scale
-            const bool clear = kpos < u.lo || kpos > u.hi || sc.w == 0.f;
-            if (__any_sync(0xffffffffu, clear)) {
+            const bool some = kpos < u.ilo || kpos > u.ihi;  // not every row sees the key
+            if (__any_sync(0xffffffffu, some || sc.w == 0.f)) {
+                const bool clear = kpos < u.lo || kpos > u.hi || sc.w == 0.f;
                 const int st = t % C::STAGES;
                 wait(sm.v_full[st], t / C::STAGES);
-                if (clear) {
-#pragma unroll
-                    for (int c = 0; c < D / 16; ++c)
-                        *reinterpret_cast<uint4 *>(sm.v[st] + key * D + 16 * c) =
-                            make_uint4(0, 0, 0, 0);
+                if (some || clear) {
+                    uint4 *v = reinterpret_cast<uint4 *>(sm.v[st] + key * D);
+#pragma unroll 1
+                    for (int c = 0; c < D / 16; ++c) {
+                        uint4 y = v[c];
+                        if (clear) {
+                            v[c] = make_uint4(0, 0, 0, 0);
+                        } else if (without_nan(y)) {
+                            v[c] = y;
+                            sm.units.u[i % UNITS].nan_values = 1;
+                        }
+                    }
                 }
             }
             float top = -INFINITY;
@@ -683,8 +688,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 for (int e = 0; e < CH; e += 2) {
                     const int r = c + e;
                     const float4 m = m4[r / 4];
-                    const float a = ex2(x[r] + (BASE - (e & 2 ? m.z : m.x)));
-                    const float b = ex2(x[r + 1] + (BASE - (e & 2 ? m.w : m.y)));
+                    const float a = ex2(x[r] - (e & 2 ? m.z : m.x) + BASE);
+                    const float b = ex2(x[r + 1] - (e & 2 ? m.w : m.y) + BASE);
                     l[r] = fmaf(a, sc.z, l[r]);
                     l[r + 1] = fmaf(b, sc.z, l[r + 1]);
                     // by way of f16, whose 11 bits hold hi + lo / 16, in pairs
@@ -735,11 +740,12 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 if (has[0]) z = fmaf(w0, sm.lx[w][0][q][me], z);
                 if (has[1]) z = fmaf(w1, sm.lx[w][1][q][me], z);
             }
-            float lse2 = z == 0.f ? -INFINITY : mm - BASE + __log2f(z);
             float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
             if (part) {
-                if (ok) reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot * R + me] = lse2;
+                if (ok)
+                    part_sums(p.ws)[slot * R + me] = make_float2(mm, z * (1.f / (1 << (int)BASE)));
             } else {
+                float lse2 = z == 0.f ? -INFINITY : mm - BASE + __log2f(z);
                 if (p.sink_mode == 2) with_null_sink(sm.rsink[w][me], lse2, inv);
                 const long long row = sm.orow[w][me];
                 if (ok && p.lse && row >= 0) p.lse[row] = lse2 * LN2;
@@ -752,6 +758,17 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         const int col = D == 128 ? key : quarter * 16 + lane;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D + col;
         const int rows0 = solo ? 0 : g * (R / 2), rows1 = solo ? R : rows0 + R / 2;
+        uint32_t nan_rows = 0;  // rows whose column is NaN
+        if (u.nan_values && writes)
+            each_partial_key<D>(p, u, u.lo, u.hi, [&](int k, const uint8_t *codes) {
+                if ((__ldg(codes + col) & 0x7f) != 0x7f) return;
+#pragma unroll 1
+                for (int r = 0; r < R; ++r) {
+                    const int pos = sm.rpos[w][r];
+                    if (k <= (p.plan.causal ? pos : u.hi) && (p.plan.wl < 0 || k >= pos - p.plan.wl))
+                        nan_rows |= 1u << r;
+                }
+            });
 #pragma unroll 1
         for (int r0 = rows0; r0 < rows1; r0 += 4) {
             uint32_t v[4][4];  // group 0 hi, lo, group 1 hi, lo
@@ -774,6 +791,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                                         __uint_as_float(v[2 * s][e])),
                                    acc);
                 if (!writes) continue;
+                if (nan_rows >> r & 1) acc = NAN;
                 if (part) {
                     prow[(size_t)r * D] = acc;
                 } else if (sm.orow[w][r] >= 0) {
@@ -903,10 +921,10 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(R, D);
     DecodeParams p{plan_args(a, split, EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
-                   a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
+                   a.v_cache, a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
                    a.max_pages, a.num_pages * a.Hkv * a.page, a.scale * LOG2E, a.sinks, a.sink_mode,
                    static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace),
-                   next_join_counters(dev)};
+                   split ? next_join_counters(dev, s) : nullptr};
     if (verbose())
         fprintf(stderr, "sattn: paged decode_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, R, grid,
                 smem, (int)split);

@@ -1,9 +1,9 @@
 // Joins the partial results of units that were cut between CTAs (the paged
-// cache kernels' workspace): lse = log sum_c 2^lse2_c (+ the null-logit sink,
-// once), o = sum_c 2^(lse2_c - lse) o_c, in the order of the pieces.
+// cache kernels' workspace): w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
+// null-logit sink, once), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces.
 //
 // A warp takes a row of the unit that a piece boundary cuts, if that boundary is the
-// first inside the unit (the others leave). Lane i holds piece i's denominator,
+// first inside the unit (the others leave). Lane i holds piece i's sums,
 // the columns are spread over the lanes. The work is a few MB at most, so it is
 // latency that counts: notes, denominators and rows are three rounds of loads.
 #include <math.h>
@@ -37,7 +37,7 @@ join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *
         parts += len;
         if (len < 32) break;
     }
-    const float *plse = reinterpret_cast<const float *>(ws + plan_lse_offset());
+    const float2 *sums = reinterpret_cast<const float2 *>(ws + plan_sums_offset());
     const float *prow = reinterpret_cast<const float *>(ws + plan_rows_offset(rows));
     constexpr int E = D / 32;
     // piece i of the unit: part 1 of CTA c - 1, then part 0 of c, c + 1, ...
@@ -45,18 +45,20 @@ join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *
     const int row = me.row0 + r;
     const int head = me.h * G + row % G;
     const size_t out = (size_t)(me.t0 + row / G) * H + head;
-    const float sink = null_sink ? __ldg(sinks + head) * LOG2E : -INFINITY;
-    float m = sink;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, plse[slot(i) * rows + r]);
+    const float sink = null_sink ? sink_log2(__ldg(sinks + head)) : -INFINITY;
+    float m = fmaxf(sink, NOTHING);
+    for (int i = lane; i < parts; i += 32) m = fmaxf(m, sums[slot(i) * rows + r].x);
     m = warp_max(m);
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float z = null_sink && m != -INFINITY ? ex2(sink - m) : 0.f;
+    float z = ex2(sink - m);  // (0 without a sink)
     for (int i0 = 0; i0 < parts; i0 += 32) {
-        // NaN denominators (a NaN key) stay: only -inf counts as nothing
-        const float l = i0 + lane < parts ? plse[slot(i0 + lane) * rows + r] : -INFINITY;
-        const float w = l == -INFINITY ? 0.f : ex2(l - m);
+        float w = 0.f;
+        if (i0 + lane < parts) {
+            const float2 s = sums[slot(i0 + lane) * rows + r];
+            w = s.y * ex2(s.x - m);
+        }
         z += warp_sum(w);
         const int cnt = min(32, parts - i0);
 #pragma unroll 4

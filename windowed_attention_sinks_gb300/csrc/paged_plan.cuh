@@ -23,7 +23,8 @@
 
 namespace sattn {
 
-constexpr int TILE = 128;  // keys per tile
+constexpr int TILE = 128;           // keys per tile
+constexpr float NOTHING = -3.4e38f;  // maximum of a row that has seen no key yet
 
 struct PlanArgs {
     const int32_t *cu, *lens;
@@ -59,6 +60,7 @@ template <int ROWS> struct Unit {
     int t_first, ntiles;   // tiles of the sequence; ntiles >= 1 (an empty unit's is masked)
     int begin, end;        // the tiles of this piece, 0 .. ntiles
     int c0, parts;         // of a cut unit: its first piece, and how many
+    int nan_values;        // set where a key that not every row sees has NaN value codes
 
     // The same piece in halves of tiles, less the halves that no row sees.
     __device__ __forceinline__ int sub_begin() const {
@@ -82,6 +84,7 @@ template <int ROWS> struct Unit {
         ihi = p.causal ? p0 : s.len - 1;
         t_first = lo / TILE;
         ntiles = hi < lo ? 1 : hi / TILE - t_first + 1;
+        nan_values = 0;
     }
 };
 
@@ -204,7 +207,7 @@ __device__ void plan_start(const PlanArgs &p, PlanStart &ps, const DevCtx &ctx) 
         }
         int h = 0;
 #pragma unroll 1
-        while (x0 >= at + (h + 1) * ph) ++h;
+        while (h < p.Hkv - 1 && x0 >= at + (h + 1) * ph) ++h;
         at += h * ph;
 #pragma unroll 1
         for (int r0 = 0; r0 < u.nrt; r0 += 32) {
@@ -307,6 +310,36 @@ __device__ __forceinline__ float4 page_scales(const float *k_scale, const float 
     return make_float4(__ldg(k_scale + at), __log2f(e), __fdividef(1.f, e), vs > 0.f ? 1.f : 0.f);
 }
 
+// NaN value codes of keys that some rows of a unit see and others do not. The MMA
+// multiplies every key's values by every row's weight, and 0 * NaN is NaN, so such
+// codes are taken out of the tile (without_nan) and put back at the unit's end into
+// the rows that see them: each_partial_key calls at(key, codes) for the piece's
+// keys from `lo` to `hi` that not every row sees.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t x) {  // 0xff for each NaN code
+    return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+}
+__device__ __forceinline__ bool without_nan(uint4 &x) {
+    const uint4 n = make_uint4(nan_codes(x.x), nan_codes(x.y), nan_codes(x.z), nan_codes(x.w));
+    x = make_uint4(x.x & ~n.x, x.y & ~n.y, x.z & ~n.z, x.w & ~n.w);
+    return n.x | n.y | n.z | n.w;
+}
+template <int D, int ROWS, typename Params, typename F>
+__device__ __forceinline__ void each_partial_key(const Params &p, const Unit<ROWS> &u, int lo,
+                                                 int hi, F at) {
+    const int a = max(lo, (u.t_first + u.begin) * TILE);
+    const int z = min(hi, (u.t_first + u.end) * TILE - 1);
+#pragma unroll 1
+    for (int k = a; k <= z; ++k) {
+        if (k >= u.ilo && k <= u.ihi) k = u.ihi + 1;
+        if (k > z) break;
+        const int pid = __ldg(p.page_table + (size_t)u.b * p.max_pages + (k >> p.page_shift));
+        if (pid < 0 || pid >= p.num_pages) continue;
+        const size_t ph = (size_t)pid * p.plan.Hkv + u.h;
+        if (!(__ldg(p.v_scale + ph) > 0.f)) continue;  // its values are dropped
+        at(k, p.v_cache + (ph * p.page + (k & (p.page - 1))) * D);
+    }
+}
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *m, uint32_t bar, int x,
                                             int y) {
     asm volatile(
@@ -362,16 +395,21 @@ struct PlanNote {
     int cont, through, t0, h, row0, nrows, pad0, pad1;
 };
 
-// Workspace: PlanNote [pieces], lse2 [pieces][2][ROWS], rows [pieces][2][ROWS][D] (fp32).
+// Workspace: PlanNote [pieces], (m, z) [pieces][2][ROWS], rows [pieces][2][ROWS][D] (fp32).
 // Part 0 of a piece is its first unit if that began earlier, part 1 its last
-// unit if that begins here and goes on.
+// unit if that begins here and goes on. Of a part's row: its maximum m, its
+// denominator z = sum 2^(x - m) (as one number, m + log2 z, large logits would
+// swallow z), and o.
 constexpr int MAX_PIECES = 256;
-__host__ __device__ constexpr size_t plan_lse_offset() { return MAX_PIECES * sizeof(PlanNote); }
+__host__ __device__ constexpr size_t plan_sums_offset() { return MAX_PIECES * sizeof(PlanNote); }
 __host__ __device__ constexpr size_t plan_rows_offset(int rows) {
-    return plan_lse_offset() + (size_t)MAX_PIECES * 2 * rows * 4;
+    return plan_sums_offset() + (size_t)MAX_PIECES * 2 * rows * sizeof(float2);
 }
 __host__ __device__ constexpr size_t plan_workspace(int rows, int d) {
     return plan_rows_offset(rows) + (size_t)MAX_PIECES * 2 * rows * d * 4;
+}
+__device__ __forceinline__ float2 *part_sums(uint8_t *ws) {
+    return reinterpret_cast<float2 *>(ws + plan_sums_offset());
 }
 
 template <int ROWS>

@@ -59,12 +59,13 @@ constexpr int EXTRA = 3;  // a unit's own cost, in tiles
 constexpr int UNITS = 4;  // units handed on ahead
 constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
-constexpr float NOTHING = -1e30f;  // m of a row that has seen no key yet
+constexpr float FAR = 1 << 20;  // m up to which x - m may be taken in one rounding
 
 struct PrefillParams {
     PlanArgs plan;
     const __nv_bfloat16 *q;
     int64_t q_stride;
+    const uint8_t *v_cache;
     const float *k_scale, *v_scale;
     const int32_t *page_table;
     int H, num_pages, page, page_shift, max_pages;
@@ -226,32 +227,31 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
     int t = 0;  // tiles
     for (int i = 0;; ++i) {
         if (!sm.units.wait(i, ctx, abort)) return;
-        const Unit<ROWS> &u = sm.units.u[i % UNITS];
-        const int begin = u.begin, end = u.end, lo = u.lo, hi = u.hi, t_first = u.t_first;
-        __syncwarp();
-        if (lane == 0) sm.units.release(i);
-        if (begin == end) return;
-        for (int j = begin; j < end; ++j, ++t) {
+        Unit<ROWS> &u = sm.units.u[i % UNITS];
+        if (u.begin == u.end) return;
+        for (int j = u.begin; j < u.end; ++j, ++t) {
             const int b = t & 1, use = t >> 1, st = t % STAGES, ss = t % SRING;
-            const int kpos0 = (t_first + j) * TILE;
-            const bool edge = kpos0 < lo || kpos0 + TILE - 1 > hi;
+            const int kpos0 = (u.t_first + j) * TILE;
+            const bool edge = kpos0 < u.ilo || kpos0 + TILE - 1 > u.ihi;
             if (!bar_wait(smem_u32(&sm.v8_full[st]), (t / STAGES) & 1, ctx, abort)) return;
-            uint4 x[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                x[i] = *reinterpret_cast<const uint4 *>(sm.v[st] + (i * 128 + tid) * 16);
+            if (!bar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
+            uint4 *src = reinterpret_cast<uint4 *>(sm.v[st]) + tid;
             // values that no row sees may hold anything, NaN codes too, and the MMA
             // multiplies them by 0; a zero scale drops the values
-            if (!bar_wait(smem_u32(&sm.sc_full[ss]), (t / SRING) & 1, ctx, abort)) return;
             if (edge || sm.zero[ss]) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < PER; ++i) {
-                    const int r = r0 + i * (128 / UR);
-                    if (kpos0 + r < lo || kpos0 + r > hi ||
-                        sm.sc[ss][r >> p.page_shift].w == 0.f)
-                        x[i] = make_uint4(0, 0, 0, 0);
+                    const int r = r0 + i * (128 / UR), key = kpos0 + r;
+                    uint4 x = src[i * 128];
+                    if (key < u.lo || key > u.hi || sm.sc[ss][r >> p.page_shift].w == 0.f)
+                        src[i * 128] = make_uint4(0, 0, 0, 0);
+                    else if ((key < u.ilo || key > u.ihi) && without_nan(x))
+                        src[i * 128] = x, u.nan_values = 1;
                 }
             }
+            uint4 x[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) x[i] = src[i * 128];
             if (use >= 1 && !bar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
             uint8_t *dst = sm.v16[b];
 #pragma unroll
@@ -270,6 +270,7 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
         }
+        if (lane == 0) sm.units.release(i);
     }
 }
 
@@ -394,7 +395,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         // the row's keys; a row past the unit's last sees what it likes (not written)
         const int hi = p.plan.causal ? pos : u.s.len - 1;
         const int lo = p.plan.wl < 0 ? 0 : pos - p.plan.wl;
-        const float sink = p.sinks && in ? __ldg(p.sinks + head) * LOG2E : 0.f;
+        const float sink = p.sinks && in ? sink_log2(__ldg(p.sinks + head)) : 0.f;
         // ---- the row's Q: a power of two times it, split. The half's Q tile is free:
         // this warp has seen the last S that reads it
         float qf;
@@ -448,6 +449,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             mbar_arrive(smem_u32(&sm.q_full[half]));
         }
         float m = NOTHING, l = 0.f;
+        bool far = false;  // some row's m is so large that fp32 must subtract it exactly
         const int s0 = u.sub_begin(), s1 = u.sub_end();
 #pragma unroll 1
         for (int k = s0; k < s1; ++k, ++done) {
@@ -491,7 +493,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                     float mx = -INFINITY;
 #pragma unroll
                     for (int e = w; e < w + CW; e += 2)
-                        mx = max3(mx, __uint_as_float(xs[e >> 5][e & 31]),
+                        mx = max3(mx, e == 0 && key0 ? -INFINITY
+                                                     : __uint_as_float(xs[e >> 5][e & 31]),
                                   __uint_as_float(xs[e >> 5][(e & 31) + 1]));
                     top = fmaxf(top, fmaf(mx, s.x, s.y));
                     if (w == 0 && key0)
@@ -500,6 +503,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 const float mn = fmaxf(m, top), alpha = ex2(m - mn);
                 m = mn;
                 l *= alpha;
+                far = __any_sync(0xffffffffu, m != NOTHING && fabsf(m) > FAR);
                 if (k > s0) {
                     if (!wait(sm.pv_done[half], done - 1)) return false;
                     tc_fence_after();
@@ -520,18 +524,37 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             float sum;
             bool moves = __any_sync(0xffffffffu, m == NOTHING);
 #pragma unroll 1
-            for (;;) {
+            for (int pass = 0;; ++pass) {
                 load();
                 if (moves && !move()) return;
                 // P of the row's 64 keys with m as it is, and their sum
                 const float base = m == NOTHING ? BASE : BASE - m;
-                float raw = 0.f;
+                float raw = 0.f, fx[SUB / CW], off[SUB / CW];
+                bool bias = key0;
                 sum = 0.f;
 #pragma unroll
+                for (int w = 0; w < SUB / CW; ++w) {
+                    const float4 s = scales(w * CW);
+                    fx[w] = s.x, off[w] = s.y + base;
+                }
+                if (far) {  // x - m in two roundings, as move() has them: never above 0 there
+#pragma unroll
+                    for (int w = 0; w < SUB / CW; ++w) {
+                        const float4 s = scales(w * CW);
+#pragma unroll
+                        for (int e = w * CW; e < w * CW + CW; ++e) {
+                            float x = fmaf(__uint_as_float(xs[e >> 5][e & 31]), s.x, s.y);
+                            if (e == 0 && bias) x += sink;
+                            xs[e >> 5][e & 31] = __float_as_uint(x - m);
+                        }
+                        fx[w] = 1.f, off[w] = BASE;
+                    }
+                    bias = false;
+                }
+#pragma unroll
                 for (int w = 0; w < SUB; w += CW) {
-                    const float4 s = scales(w);
-                    const float off = s.y + base;
-                    const uint64_t f2 = f2_pack(s.x, s.x), off2 = f2_pack(off, off);
+                    const float f = fx[w / CW], o1 = off[w / CW];
+                    const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(o1, o1);
                     uint64_t part = f2_pack(0.f, 0.f);
 #pragma unroll
                     for (int e = w; e < w + CW; e += 2) {
@@ -540,7 +563,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                                                  __uint_as_float(xs[e >> 5][(e & 31) + 1])),
                                          f2, off2),
                                   a, b);
-                        if (e == 0 && key0) a += sink;
+                        if (e == 0 && bias) a += sink;
                         a = ex2(a);
                         b = ex2(b);
                         part = f2_add(part, f2_pack(a, b));
@@ -549,10 +572,11 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                     float a, b;
                     f2_unpack(part, a, b);
                     raw += a + b;
-                    sum = fmaf(a + b, s.z, sum);
+                    sum = fmaf(a + b, scales(w).z, sum);
                 }
-                // no value is above the sum, so below the limit none has left f16's range
-                moves = __any_sync(0xffffffffu, raw > SUM_LIMIT);
+                // no value is above the sum, so below the limit none has left f16's range;
+                // and after a move none is above 2^(BASE + 1/4), so there is no third pass
+                moves = pass == 0 && __any_sync(0xffffffffu, raw > SUM_LIMIT);
                 if (!moves) break;
             }
             l += sum;
@@ -572,15 +596,15 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
         if (spoilt) l = NAN;
-        float lse2 = l == 0.f ? -INFINITY : m - BASE + __log2f(l);
         float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
         const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
         const size_t orow = (size_t)(u.s.t0 + tok) * p.H + head;
         if (in) {
             if (part) {
-                reinterpret_cast<float *>(p.ws + plan_lse_offset())[slot] = lse2;
+                part_sums(p.ws)[slot] = make_float2(m, l * (1.f / (1 << (int)BASE)));
             } else {
+                float lse2 = l == 0.f ? -INFINITY : m - BASE + __log2f(l);
                 if (p.sink_mode == 2) with_null_sink(sink, lse2, inv);
                 if (p.lse) p.lse[orow] = lse2 * LN2;
             }
@@ -590,6 +614,19 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             uint32_t o[32];
             tmem_ld32(tmem + O_COL + 32u * c, o);
             tc_wait_ld();
+            if (u.nan_values && in) {
+                uint32_t cols = 0;  // columns that are NaN
+                each_partial_key<D>(p, u, max(lo, 0), hi, [&](int, const uint8_t *codes) {
+                    const uint32_t *at = reinterpret_cast<const uint32_t *>(codes) + 8 * c;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i)  // a bit a code
+                        cols |= ((nan_codes(__ldg(at + i)) & 0x08040201u) * 0x01010101u >> 24)
+                                << (4 * i);
+                });
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (cols >> e & 1) o[e] = 0x7fffffffu;
+            }
             if (in && part) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
@@ -710,7 +747,7 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D);
     PrefillParams p{plan_args(a, split, EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
-                    a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page,
+                    a.v_cache, a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page,
                     page_shift(a.page), a.max_pages, a.num_pages * a.Hkv * a.page,
                     a.scale * LOG2E, a.sinks, a.sink_mode, static_cast<__nv_bfloat16 *>(a.o),
                     a.lse, static_cast<uint8_t *>(a.workspace)};

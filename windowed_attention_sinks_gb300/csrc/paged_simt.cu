@@ -45,7 +45,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
     const int hi = a.causal ? pos : s.len - 1;
     const int lo = a.window_left < 0 ? 0 : max(0, pos - a.window_left);
     const float qs = a.scale * LOG2E;
-    const float sink = a.sinks ? __ldg(a.sinks + h) * LOG2E : 0.f;
+    const float sink = a.sinks ? sink_log2(__ldg(a.sinks + h)) : 0.f;
     float q[E], acc[E];
     const float *qrow = static_cast<const float *>(a.q) + (size_t)t * a.q_stride + (size_t)h * D + lane * E;
 #pragma unroll
