@@ -450,18 +450,29 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         }
         float m = NOTHING, l = 0.f;
         bool far = false;  // some row's m is so large that fp32 must subtract it exactly
+        bool fresh = true;  // some row has seen no key yet
         const int s0 = u.sub_begin(), s1 = u.sub_end();
+        const int first = u.t_first * TILE, tile0 = t0 - u.begin, ilo = u.ilo, ihi = u.ihi;
 #pragma unroll 1
         for (int k = s0; k < s1; ++k, ++done) {
-            const int t = t0 + (k >> 1) - u.begin, ss = t % SRING;
-            const int kpos0 = u.t_first * TILE + k * SUB, in_tile = (k & 1) * SUB;
+            const int t = tile0 + (k >> 1), ss = t % SRING;
+            const int kpos0 = first + k * SUB, in_tile = (k & 1) * SUB;
             const uint32_t s_tmem = tmem + (uint32_t)((done & 1) * SUB);
             if (k == s0 || !(k & 1))
                 if (!wait(sm.sc_full[ss], t / SRING)) return;
+            // the pages' scales as S and x take them: f above 0 (a zero key scale makes
+            // it 0), since a masked S is -inf
+            constexpr int NW = SUB / CW;
+            float sx[NW], sy[NW], sz[NW];
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const float4 s = sm.sc[ss][(in_tile + w * CW) >> p.page_shift];
+                sx[w] = fmaxf(s.x * qf, FLT_MIN), sy[w] = s.y, sz[w] = s.z;
+            }
+            const bool mask = kpos0 < ilo || kpos0 + SUB - 1 > ihi;
+            const bool key0 = p.sink_mode == 1 && kpos0 == 0;
             if (!wait(sm.s_full[half][done & 1], done >> 1)) return;
             tc_fence_after();
-            const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
-            const bool key0 = p.sink_mode == 1 && kpos0 == 0;
             uint32_t xs[2][32];
             auto load = [&]() {
                 tmem_ld32(s_tmem, xs[0]);
@@ -477,32 +488,25 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                                     (uint32_t)(seen >> (e & 32)) & (1u << (e & 31)));
                 }
             };
-            // a page's scale as S and x take it: f above 0 (a zero key scale makes it
-            // 0), since a masked S is -inf
-            auto scales = [&](int col) {
-                float4 s = sm.sc[ss][(in_tile + col) >> p.page_shift];
-                s.x = fmaxf(s.x * qf, FLT_MIN);
-                return s;
-            };
             // m from the row's 64 keys, and O and l in its terms
             auto move = [&]() -> bool {
                 float top = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < SUB; w += CW) {
-                    const float4 s = scales(w);
+                for (int w = 0; w < NW; ++w) {
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int e = w; e < w + CW; e += 2)
+                    for (int e = w * CW; e < w * CW + CW; e += 2)
                         mx = max3(mx, e == 0 && key0 ? -INFINITY
                                                      : __uint_as_float(xs[e >> 5][e & 31]),
                                   __uint_as_float(xs[e >> 5][(e & 31) + 1]));
-                    top = fmaxf(top, fmaf(mx, s.x, s.y));
+                    top = fmaxf(top, fmaf(mx, sx[w], sy[w]));
                     if (w == 0 && key0)
-                        top = fmaxf(top, fmaf(__uint_as_float(xs[0][0]), s.x, s.y) + sink);
+                        top = fmaxf(top, fmaf(__uint_as_float(xs[0][0]), sx[0], sy[0]) + sink);
                 }
                 const float mn = fmaxf(m, top), alpha = ex2(m - mn);
                 m = mn;
                 l *= alpha;
+                fresh = __any_sync(0xffffffffu, m == NOTHING);
                 far = __any_sync(0xffffffffu, m != NOTHING && fabsf(m) > FAR);
                 if (k > s0) {
                     if (!wait(sm.pv_done[half], done - 1)) return false;
@@ -522,28 +526,25 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             };
             uint32_t pw[32];
             float sum;
-            bool moves = __any_sync(0xffffffffu, m == NOTHING);
+            bool moves = fresh;
 #pragma unroll 1
             for (int pass = 0;; ++pass) {
                 load();
                 if (moves && !move()) return;
                 // P of the row's 64 keys with m as it is, and their sum
                 const float base = m == NOTHING ? BASE : BASE - m;
-                float raw = 0.f, fx[SUB / CW], off[SUB / CW];
+                float raw = 0.f;
                 bool bias = key0;
                 sum = 0.f;
+                float fx[NW], off[NW];
 #pragma unroll
-                for (int w = 0; w < SUB / CW; ++w) {
-                    const float4 s = scales(w * CW);
-                    fx[w] = s.x, off[w] = s.y + base;
-                }
+                for (int w = 0; w < NW; ++w) fx[w] = sx[w], off[w] = sy[w] + base;
                 if (far) {  // x - m in two roundings, as move() has them: never above 0 there
 #pragma unroll
-                    for (int w = 0; w < SUB / CW; ++w) {
-                        const float4 s = scales(w * CW);
+                    for (int w = 0; w < NW; ++w) {
 #pragma unroll
                         for (int e = w * CW; e < w * CW + CW; ++e) {
-                            float x = fmaf(__uint_as_float(xs[e >> 5][e & 31]), s.x, s.y);
+                            float x = fmaf(__uint_as_float(xs[e >> 5][e & 31]), sx[w], sy[w]);
                             if (e == 0 && bias) x += sink;
                             xs[e >> 5][e & 31] = __float_as_uint(x - m);
                         }
@@ -553,8 +554,8 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 }
 #pragma unroll
                 for (int w = 0; w < SUB; w += CW) {
-                    const float f = fx[w / CW], o1 = off[w / CW];
-                    const uint64_t f2 = f2_pack(f, f), off2 = f2_pack(o1, o1);
+                    const uint64_t f2 = f2_pack(fx[w / CW], fx[w / CW]);
+                    const uint64_t off2 = f2_pack(off[w / CW], off[w / CW]);
                     uint64_t part = f2_pack(0.f, 0.f);
 #pragma unroll
                     for (int e = w; e < w + CW; e += 2) {
@@ -572,7 +573,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                     float a, b;
                     f2_unpack(part, a, b);
                     raw += a + b;
-                    sum = fmaf(a + b, scales(w).z, sum);
+                    sum = fmaf(a + b, sz[w / CW], sum);
                 }
                 // no value is above the sum, so below the limit none has left f16's range;
                 // and after a move none is above 2^(BASE + 1/4), so there is no third pass
@@ -707,9 +708,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 64 + 256 x 192 = the 512 x 128 of the launch
+    // registers: 256 threads x 56 + 256 x 200 = the 512 x 128 of the launch
     if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {
             load_tiles<D>(p, &tk, &tv, sm, ctx);
         } else if (warp == 2) {
@@ -721,7 +722,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             widen<D>(p, sm, ctx);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         softmax<D, CW>(p, sm, tmem, ctx);
     }
     tc_fence_before();
