@@ -389,18 +389,28 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             if (lane == 0) sm.units.release(i);
             continue;
         }
-        const int row = u.row0 + r, tok = p.plan.token(row), head = u.h * G + row - tok * G;
-        const int pos = u.s.len - u.s.n + tok;
-        const bool in = r < u.nrows;
+        // What is needed now and then is computed now and then: a register that the
+        // steps do not have spills, and there is next to no L1 beside the tiles.
+        auto token = [&]() { return p.plan.token(u.row0 + r); };
+        auto in_unit = [&]() { return r < u.nrows; };
         // the row's keys; a row past the unit's last sees what it likes (not written)
-        const int hi = p.plan.causal ? pos : u.s.len - 1;
-        const int lo = p.plan.wl < 0 ? 0 : pos - p.plan.wl;
-        const float sink = p.sinks && in ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+        auto last_key = [&]() {
+            return p.plan.causal ? u.s.len - u.s.n + token() : u.s.len - 1;
+        };
+        auto first_key = [&]() {
+            return p.plan.wl < 0 ? 0 : max(0, u.s.len - u.s.n + token() - p.plan.wl);
+        };
+        auto sink = [&]() {
+            return p.sinks && in_unit()
+                       ? sink_log2(__ldg(p.sinks + u.h * G + u.row0 + r - token() * G))
+                       : 0.f;
+        };
         // ---- the row's Q: a power of two times it, split. The half's Q tile is free:
         // this warp has seen the last S that reads it
-        float qf;
-        bool spoilt;
+        float qf, l;
         {
+            const bool in = in_unit();
+            const int tok = token(), head = u.h * G + u.row0 + r - tok * G;
             const uint4 *src = reinterpret_cast<const uint4 *>(
                 p.q + (size_t)(u.s.t0 + (in ? tok : 0)) * p.q_stride +
                 (size_t)(in ? head : 0) * D);
@@ -412,7 +422,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                                              __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
             }
             top = max(top >> 16, top & 0xffffu);
-            spoilt = top >= 0x7f80u;  // an inf or a NaN
+            l = top >= 0x7f80u ? NAN : 0.f;  // an inf or a NaN spoils the row
             // 2^k with the largest |q| 2^k in [128, 256)
             const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
             const float up = __uint_as_float((uint32_t)(127 + k) << 23);
@@ -448,15 +458,14 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.q_full[half]));
         }
-        float m = NOTHING, l = 0.f;
+        float m = NOTHING;
         bool far = false;  // some row's m is so large that fp32 must subtract it exactly
         bool fresh = true;  // some row has seen no key yet
         const int s0 = u.sub_begin(), s1 = u.sub_end();
-        const int first = u.t_first * TILE, tile0 = t0 - u.begin, ilo = u.ilo, ihi = u.ihi;
 #pragma unroll 1
         for (int k = s0; k < s1; ++k, ++done) {
-            const int t = tile0 + (k >> 1), ss = t % SRING;
-            const int kpos0 = first + k * SUB, in_tile = (k & 1) * SUB;
+            const int t = t0 - u.begin + (k >> 1), ss = t % SRING;
+            const int kpos0 = u.t_first * TILE + k * SUB, in_tile = (k & 1) * SUB;
             const uint32_t s_tmem = tmem + (uint32_t)((done & 1) * SUB);
             if (k == s0 || !(k & 1))
                 if (!wait(sm.sc_full[ss], t / SRING)) return;
@@ -469,7 +478,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 const float4 s = sm.sc[ss][(in_tile + w * CW) >> p.page_shift];
                 sx[w] = fmaxf(s.x * qf, FLT_MIN), sy[w] = s.y, sz[w] = s.z;
             }
-            const bool mask = kpos0 < ilo || kpos0 + SUB - 1 > ihi;
+            const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
             const bool key0 = p.sink_mode == 1 && kpos0 == 0;
             if (!wait(sm.s_full[half][done & 1], done >> 1)) return;
             tc_fence_after();
@@ -480,7 +489,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 tc_wait_ld();
                 if (mask) {
                     // bit e: the row sees key e
-                    const int a = max(0, lo - kpos0), z = min(SUB - 1, hi - kpos0);
+                    const int a = max(0, first_key() - kpos0), z = min(SUB - 1, last_key() - kpos0);
                     const uint64_t seen = a > z ? 0 : (~0ull >> (SUB - 1 - z)) & (~0ull << a);
 #pragma unroll
                     for (int e = 0; e < SUB; ++e)
@@ -501,7 +510,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                                   __uint_as_float(xs[e >> 5][(e & 31) + 1]));
                     top = fmaxf(top, fmaf(mx, sx[w], sy[w]));
                     if (w == 0 && key0)
-                        top = fmaxf(top, fmaf(__uint_as_float(xs[0][0]), sx[0], sy[0]) + sink);
+                        top = fmaxf(top, fmaf(__uint_as_float(xs[0][0]), sx[0], sy[0]) + sink());
                 }
                 const float mn = fmaxf(m, top), alpha = ex2(m - mn);
                 m = mn;
@@ -545,7 +554,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
 #pragma unroll
                         for (int e = w * CW; e < w * CW + CW; ++e) {
                             float x = fmaf(__uint_as_float(xs[e >> 5][e & 31]), sx[w], sy[w]);
-                            if (e == 0 && bias) x += sink;
+                            if (e == 0 && bias) x += sink();
                             xs[e >> 5][e & 31] = __float_as_uint(x - m);
                         }
                         fx[w] = 1.f, off[w] = BASE;
@@ -564,7 +573,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                                                  __uint_as_float(xs[e >> 5][(e & 31) + 1])),
                                          f2, off2),
                                   a, b);
-                        if (e == 0 && bias) a += sink;
+                        if (e == 0 && bias) a += sink();
                         a = ex2(a);
                         b = ex2(b);
                         part = f2_add(part, f2_pack(a, b));
@@ -596,17 +605,18 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         ++units;
         tc_fence_after();
         const bool part = u.begin > 0 || u.end < u.ntiles;
-        if (spoilt) l = NAN;
         float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
         const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
-        const size_t orow = (size_t)(u.s.t0 + tok) * p.H + head;
+        const bool in = in_unit();
+        const int tok = token();
+        const size_t orow = (size_t)(u.s.t0 + tok) * p.H + u.h * G + u.row0 + r - tok * G;
         if (in) {
             if (part) {
                 part_sums(p.ws)[slot] = make_float2(m, l * (1.f / (1 << (int)BASE)));
             } else {
                 float lse2 = l == 0.f ? -INFINITY : m - BASE + __log2f(l);
-                if (p.sink_mode == 2) with_null_sink(sink, lse2, inv);
+                if (p.sink_mode == 2) with_null_sink(sink(), lse2, inv);
                 if (p.lse) p.lse[orow] = lse2 * LN2;
             }
         }
@@ -617,7 +627,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             tc_wait_ld();
             if (u.nan_values && in) {
                 uint32_t cols = 0;  // columns that are NaN
-                each_partial_key<D>(p, u, max(lo, 0), hi, [&](int, const uint8_t *codes) {
+                each_partial_key<D>(p, u, first_key(), last_key(), [&](int, const uint8_t *codes) {
                     const uint32_t *at = reinterpret_cast<const uint32_t *>(codes) + 8 * c;
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i)  // a bit a code
@@ -708,9 +718,9 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 56 + 256 x 200 = the 512 x 128 of the launch
+    // registers: 256 threads x 64 + 256 x 192 = the 512 x 128 of the launch
     if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0) {
             load_tiles<D>(p, &tk, &tv, sm, ctx);
         } else if (warp == 2) {
@@ -722,7 +732,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             widen<D>(p, sm, ctx);
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
         softmax<D, CW>(p, sm, tmem, ctx);
     }
     tc_fence_before();
