@@ -26,20 +26,29 @@
 // m is the maximum of a row's first keys and stays unless 64 keys' P sum up to more than
 // 2^15: P is computed on trust in one pass over S that looks for no maximum,
 // and where the sum says that this was wrong m moves, O is rescaled and the pass
-// is repeated. TMEM: S / P 2 x 2 x 64
-// columns, O 2 x D: all 512 for D = 128, hence the shared columns of S and P.
-// The MMAs of one CTA run in the order of issue, so S of two steps ahead may
-// follow the P V that reads its columns.
+// is repeated. TMEM: S / P 2 x 2 x 64 columns, O 2 x D: all 512 for D = 128, hence
+// the shared columns of S and P.
 //
 // One persistent CTA per SM over an equal piece of the tiles (paged_plan.cuh):
 //   warp 0       the units; TMA: tiles of K and V, two rings of STAGES
-//   warps 1, 3   MMA issuers of the halves: PV(k), S(k + 2), PV(k + 1), ...: the
-//                softmax finds its next S ready. (One MMA takes its thread about 65
-//                cycles to issue, about what the tensor core needs for it, so
-//                one thread for both halves would bound the kernel.)
+//   warps 1, 3   S of the halves, two steps ahead of the softmax
+//   warps 8, 10  P V of the halves
 //   warp 2       the pages' scales
 //   warps 4-7    widening: V's codes to f16 tiles (two buffers)
-//   warps 8-11, 12-15   Q, softmax and epilogue of the halves, a thread a row
+//   warps 12-15, 16-19   Q, softmax and epilogue of the halves, a thread a row
+//
+// Bound: the chain of a step, S ready -> 64 exponentials a thread -> P V -> the S
+// that takes P's columns, about 1900 cycles where the products need 1300. For 2048 tokens
+// behind 30720 cached ones (32 heads on 8, d = 128) 839 us, 1.27 PFLOP/s; the
+// products alone would take 549. Prompts of 61 .. 1500 tokens 211 us: a unit costs about
+// 15000 cycles by itself (Q, the first maximum, O). Measured against it:
+//   one thread for both products of a half            939 us (an MMA takes its
+//     thread 65 to 80 cycles to issue, a commit or a wait that is met 100 to 200)
+//   the same, every index kept up instead of computed   875 us
+//   S of 128 keys at once, in one buffer               1077 us
+//   two threads a row, 32 keys each                    1028 us (no registers left
+//     to have the next loads in flight)
+//   Q by the widening warps, one unit ahead             854 us, the prompts 309
 #include <float.h>
 #include <limits.h>
 #include <math.h>
@@ -52,10 +61,13 @@ namespace sattn {
 namespace {
 
 constexpr int ROWS = 256;
-constexpr int NTHREADS = 512;
+constexpr int NTHREADS = 640;
+constexpr int SOFTMAX = 12;  // first softmax warp
 constexpr int STAGES = 3;
 constexpr int SRING = 8;
-constexpr int EXTRA = 3;  // a unit's own cost, in tiles
+// A unit's own cost in tiles, of about 3800 cycles each: with 3, 4 and 5 the prompts
+// above take 221, 211 and 213 us.
+constexpr int EXTRA = 4;
 constexpr int UNITS = 4;  // units handed on ahead
 constexpr float BASE = 7.f;       // P = 2^(BASE + x - m)
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
@@ -92,7 +104,7 @@ template <int D> struct alignas(1024) Smem {
     uint64_t k_full[STAGES], k_empty[STAGES], v8_full[STAGES], v8_empty[STAGES];
     uint64_t v_full[2], v_empty[2];
     uint64_t sc_full[SRING], sc_empty[SRING];
-    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], o_full[2], o_empty[2], drain[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2], drain[4];
     uint32_t tmem_base;
     int abort;
 };
@@ -249,20 +261,26 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
                         src[i * 128] = x, u.nan_values = 1;
                 }
             }
-            uint4 x[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) x[i] = src[i * 128];
             if (use >= 1 && !bar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
-            uint8_t *dst = sm.v16[b];
+            constexpr int B = 4;  // units in registers at a time
+#pragma unroll 1
+            for (int i0 = 0; i0 < PER; i0 += B) {
+                uint4 x[B];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const uint4 a = make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
-                                           e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
-                const uint4 c = make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
-                                           e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
-                uint8_t *row = dst + i * (128 / UR) * 128;
-                *reinterpret_cast<uint4 *>(row + at0) = sw ? c : a;
-                *reinterpret_cast<uint4 *>(row + at1) = sw ? a : c;
+                for (int i = 0; i < B; ++i) x[i] = src[(i0 + i) * 128];
+                uint8_t *dst = sm.v16[b] + i0 * (128 / UR) * 128;
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const uint4 a =
+                        make_uint4(e4m3x2_to_f16x2(x[i].x), e4m3x2_to_f16x2(x[i].x >> 16),
+                                   e4m3x2_to_f16x2(x[i].y), e4m3x2_to_f16x2(x[i].y >> 16));
+                    const uint4 c =
+                        make_uint4(e4m3x2_to_f16x2(x[i].z), e4m3x2_to_f16x2(x[i].z >> 16),
+                                   e4m3x2_to_f16x2(x[i].w), e4m3x2_to_f16x2(x[i].w >> 16));
+                    uint8_t *row = dst + i * (128 / UR) * 128;
+                    *reinterpret_cast<uint4 *>(row + at0) = sw ? c : a;
+                    *reinterpret_cast<uint4 *>(row + at1) = sw ? a : c;
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.v_full[b]));
@@ -274,23 +292,18 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
     }
 }
 
-// The MMAs of one half.
+// S of one half: S of step x goes to buffer x & 1, when P V of step x - 2 has read its P.
 template <int D>
-__device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, int half,
-                           const DevCtx &ctx) {
-    constexpr uint32_t IDESC_S = idesc_e4m3_f32(128, SUB, 0, 0);
-    constexpr uint32_t IDESC_O = idesc_f16_f32(128, D, 1);
-    constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
+__device__ void issue_s(Smem<D> &sm, uint32_t tmem, int half, const DevCtx &ctx) {
+    constexpr uint32_t IDESC = idesc_e4m3_f32(128, SUB, 0, 0);
     volatile int *abort = &sm.abort;
     if (ctx.stall) bar_wait(smem_u32(&sm.drain[half]), 0, ctx, abort);  // test hook: runs out
     const uint64_t dq = desc_rows<D>(smem_u32(sm.q[half][0])), dk = desc_rows<D>(smem_u32(sm.k[0]));
-    const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
     const uint32_t cols = tmem + (uint32_t)half * HALF_COLS;
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    int sc = 0, pc = 0, ec = 0;  // S, P V and units issued
-    int t0 = 0;                  // tiles before the unit's
+    int x = 0, t = 0, ec = 0;  // steps, tiles, units
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = sm.units.wait(i, ctx, abort))) break;
@@ -301,58 +314,35 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, i
         sm.units.release(i);
         if (n == 0) break;
         if (none) {  // no rows in this half: its share in freeing the stages
-            for (int t = t0; t < t0 + n && ok; ++t) {
-                ok = wait(sm.k_full[t % STAGES], t / STAGES) && wait(sm.v_full[t & 1], t >> 1);
+            for (int j = 0; j < n && ok; ++j, ++t) {
+                ok = wait(sm.k_full[t % STAGES], t / STAGES);
                 mbar_arrive(smem_u32(&sm.k_empty[t % STAGES]));
-                mbar_arrive(smem_u32(&sm.v_empty[t & 1]));
             }
-            t0 += n;
             continue;
         }
-        auto issue_s = [&](int k) -> bool {
-            const int tile = t0 + (k >> 1), st = tile % STAGES;
-            if ((k == s0 || !(k & 1)) && !wait(sm.k_full[st], tile / STAGES)) return false;
+        ok = wait(sm.q_full[half], ec);
+#pragma unroll 1
+        for (int k = s0; k < s1 && ok; ++k, ++x) {
+            const int st = t % STAGES, b = x & 1;
+            // (and the tile's scales, so that who finds S finds them)
+            if (k == s0 || !(k & 1))
+                ok = wait(sm.k_full[st], t / STAGES) && wait(sm.sc_full[t % SRING], t / SRING);
+            if (x >= 2) ok = ok && wait(sm.pv_done[half][b], (x >> 1) - 1);
+            if (!ok) break;
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(st * (TILE * D >> 4) + (k & 1) * (SUB * D >> 4));
-            const uint32_t s = cols + (uint32_t)((sc & 1) * SUB);
 #pragma unroll
             for (int kk = 0; kk < 2 * D / 32; ++kk) {  // hi, then lo
                 const int lo = kk / (D / 32), c = kk % (D / 32);
-                mma_f8(s, dq + (uint64_t)(lo * (128 * D >> 4) + 2 * c), kd + (uint64_t)(2 * c),
-                       IDESC_S, kk > 0);
+                mma_f8(cols + (uint32_t)(b * SUB), dq + (uint64_t)(lo * (128 * D >> 4) + 2 * c),
+                       kd + (uint64_t)(2 * c), IDESC, kk > 0);
             }
-            tc_commit(smem_u32(&sm.s_full[half][sc & 1]));
-            if ((k & 1) || k == s1 - 1) tc_commit(smem_u32(&sm.k_empty[st]));
-            ++sc;
-            return true;
-        };
-        ok = wait(sm.q_full[half], ec);
-        // step k of the loop: S of step k, then P V of step k - 2
-#pragma unroll 1
-        for (int k = s0; k < s1 + 2 && ok; ++k) {
-            if (k - 2 >= s0) {
-                const int kp = k - 2, tile = t0 + (kp >> 1), b = tile & 1;
-                if (kp == s0 || !(kp & 1)) ok = wait(sm.v_full[b], tile >> 1);
-                // the first P V overwrites the O that the last unit's epilogue reads
-                if (kp == s0 && ec >= 1) ok = ok && wait(sm.o_empty[half], ec - 1);
-                ok = ok && wait(sm.p_full[half][pc & 1], pc >> 1);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd =
-                    dv + (uint64_t)(b * (BYTES >> 4) + (kp & 1) * (SUB / 16 * 2048u >> 4));
-                const uint32_t pt = cols + (uint32_t)((pc & 1) * SUB);
-#pragma unroll
-                for (int kk = 0; kk < SUB / 16; ++kk)
-                    tc_mma_f16_ts(cols + O_COL, pt + 8u * kk, vd + (uint64_t)(kk * (2048u >> 4)),
-                                  IDESC_O, kk > 0 || kp > s0);
-                tc_commit(smem_u32(&sm.pv_done[half]));
-                if ((kp & 1) || kp == s1 - 1) tc_commit(smem_u32(&sm.v_empty[b]));
-                if (kp == s1 - 1) tc_commit(smem_u32(&sm.o_full[half]));
-                ++pc;
+            tc_commit(smem_u32(&sm.s_full[half][b]));
+            if ((k & 1) || k == s1 - 1) {
+                tc_commit(smem_u32(&sm.k_empty[st]));
+                ++t;
             }
-            if (k < s1) ok = issue_s(k);
         }
-        t0 += n;
         ++ec;
     }
     tc_commit(smem_u32(&sm.drain[half]));  // every MMA is done before TMEM goes
@@ -360,11 +350,74 @@ __device__ void issue_mmas(const PrefillParams &p, Smem<D> &sm, uint32_t tmem, i
     bar_wait(smem_u32(&sm.drain[half]), 0, ctx, &zero);
 }
 
+// P V of one half.
+template <int D>
+__device__ void issue_pv(Smem<D> &sm, uint32_t tmem, int half, const DevCtx &ctx) {
+    constexpr uint32_t IDESC = idesc_f16_f32(128, D, 1);
+    constexpr uint32_t HALF = Smem<D>::HALF, BYTES = Smem<D>::NH * HALF;
+    volatile int *abort = &sm.abort;
+    const uint64_t dv = smem_desc_sw128(smem_u32(sm.v16[0]), HALF, 1024u);
+    const uint32_t cols = tmem + (uint32_t)half * HALF_COLS;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+    };
+    int x = 0, t = 0, ec = 0;  // steps, tiles, units
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        const Unit<ROWS> &u = sm.units.u[i % UNITS];
+        const int n = u.end - u.begin, s0 = u.sub_begin() - 2 * u.begin,
+                  s1 = u.sub_end() - 2 * u.begin;
+        const bool none = half && u.nrows <= 128;
+        sm.units.release(i);
+        if (n == 0) break;
+        if (none) {
+            for (int j = 0; j < n && ok; ++j, ++t) {
+                ok = wait(sm.v_full[t & 1], t >> 1);
+                mbar_arrive(smem_u32(&sm.v_empty[t & 1]));
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int k = s0; k < s1; ++k, ++x) {
+            const int vb = t & 1, b = x & 1;
+            if (k == s0 || !(k & 1)) ok = wait(sm.v_full[vb], t >> 1);
+            // the first P V overwrites the O that the last unit's epilogue reads
+            if (k == s0 && ec >= 1) ok = ok && wait(sm.o_empty[half], ec - 1);
+            ok = ok && wait(sm.p_full[half][b], x >> 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd =
+                dv + (uint64_t)(vb * (BYTES >> 4) + (k & 1) * (SUB / 16 * 2048u >> 4));
+            const uint32_t pt = cols + (uint32_t)(b * SUB);
+#pragma unroll
+            for (int kk = 0; kk < SUB / 16; ++kk)
+                tc_mma_f16_ts(cols + O_COL, pt + 8u * kk,
+                              vd + (uint64_t)(kk * (2048u >> 4)), IDESC, kk > 0 || k > s0);
+            tc_commit(smem_u32(&sm.pv_done[half][b]));
+            if ((k & 1) || k == s1 - 1) {
+                tc_commit(smem_u32(&sm.v_empty[vb]));
+                ++t;
+            }
+        }
+        tc_commit(smem_u32(&sm.o_full[half]));
+        ++ec;
+    }
+    tc_commit(smem_u32(&sm.drain[2 + half]));
+    int zero = 0;
+    bar_wait(smem_u32(&sm.drain[2 + half]), 0, ctx, &zero);
+}
+
+// The k with the largest |q| 2^k in [128, 256), from that |q|'s bf16 bits.
+__device__ __forceinline__ int up_shift(uint32_t top) {
+    return top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
+}
+
 template <int D, int CW>  // CW: columns that share a page's scales (16 or 32)
 __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         const DevCtx &ctx) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = (warp - 8) >> 2, quarter = warp & 3;
+    const int half = (warp - SOFTMAX) >> 2, quarter = warp & 3;
     const int r = half * 128 + quarter * 32 + lane;  // row of the unit
     const uint32_t tmem =
         tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
@@ -405,39 +458,52 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                        ? sink_log2(__ldg(p.sinks + u.h * G + u.row0 + r - token() * G))
                        : 0.f;
         };
-        // ---- the row's Q: a power of two times it, split. The half's Q tile is free:
-        // this warp has seen the last S that reads it
+        // ---- Q of the warp's 32 rows, a power of two times each, split. The half's Q tile
+        // is free: this warp has seen the last S that reads it. CH lanes a row, 16 bytes
+        // each, so that a load is whole lines (a row a thread: 4000 cycles more a unit)
         float qf, l;
         {
-            const bool in = in_unit();
-            const int tok = token(), head = u.h * G + u.row0 + r - tok * G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                p.q + (size_t)(u.s.t0 + (in ? tok : 0)) * p.q_stride +
-                (size_t)(in ? head : 0) * D);
-            uint32_t top = 0;  // the largest |q| of either half-word, as bf16 bits
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 v = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-            }
-            top = max(top >> 16, top & 0xffffu);
-            l = top >= 0x7f80u ? NAN : 0.f;  // an inf or a NaN spoils the row
-            // 2^k with the largest |q| 2^k in [128, 256)
-            const int k = top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
-            const float up = __uint_as_float((uint32_t)(127 + k) << 23);
-            // 64 columns at a time, read again (from L2): unrolled over all of them this
-            // would be as much code as the rest of the role
+            constexpr int CH = D / 8, RL = 32 / CH, ITEMS = 32 / RL, B = 8;  // RL: rows a load
+            const int c = lane % CH, first = r - lane + lane / CH;
+            // (in registers: a store to the tile would have them read again)
+            const int row0 = u.row0, rows = u.nrows, h0 = u.h * G;
+            const __nv_bfloat16 *src = p.q + (size_t)u.s.t0 * p.q_stride + 8 * c;
+            uint32_t mine = 0;  // of the thread's own row: its largest |q|, as bf16 bits
 #pragma unroll 1
-            for (int c0 = 0; c0 < D / 16; c0 += 4) {
+            for (int i0 = 0; i0 < ITEMS; i0 += B) {
+                uint4 x[B];
+                uint32_t top[B];
 #pragma unroll
-                for (int c = c0; c < c0 + 4; ++c) {
-                    const uint4 v0 = in ? __ldg(src + 2 * c) : make_uint4(0, 0, 0, 0);
-                    const uint4 v1 = in ? __ldg(src + 2 * c + 1) : make_uint4(0, 0, 0, 0);
-                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-                    uint32_t hi[4], lo[4];
+                for (int i = 0; i < B; ++i) {
+                    const int rr = first + (i0 + i) * RL, row = row0 + rr, tok = p.plan.token(row);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    if (rr < rows)
+                        x[i] = __ldg(reinterpret_cast<const uint4 *>(
+                            src + (size_t)tok * p.q_stride + (size_t)(h0 + row - tok * G) * D));
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
+                for (int i = 0; i < B; ++i)
+                    top[i] = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                      __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+#pragma unroll
+                for (int o = 1; o < CH; o <<= 1)
+#pragma unroll
+                    for (int i = 0; i < B; ++i)
+                        top[i] = __vmaxu2(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    top[i] = max(top[i] >> 16, top[i] & 0xffffu);
+                    const uint32_t of_row = __shfl_sync(0xffffffffu, top[i], lane % RL * CH);
+                    if (lane / RL == i0 + i) mine = of_row;
+                }
+#pragma unroll
+                for (int i = 0; i < B; ++i) {
+                    const int rr = first + (i0 + i) * RL;
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                    const float up = __uint_as_float((uint32_t)(127 + up_shift(top[i])) << 23);
+                    uint32_t hi[2], lo[2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
                         // by way of f16, which holds a scaled bf16 down to 2^-24
                         const uint32_t ab = pack_f16x2(__uint_as_float(w[e] << 16) * up,
                                                        __uint_as_float(w[e] & 0xffff0000u) * up);
@@ -447,14 +513,13 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         hi[e >> 1] = e & 1 ? hi[e >> 1] | h << 16 : h;
                         lo[e >> 1] = e & 1 ? lo[e >> 1] | l2 << 16 : l2;
                     }
-                    const uint32_t at = sw_offset<D>(r & 127, c);
-                    *reinterpret_cast<uint4 *>(sm.q[half][0] + at) =
-                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(sm.q[half][1] + at) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    const uint32_t at = sw_offset<D>(rr & 127, c >> 1) + 8 * (c & 1);
+                    *reinterpret_cast<uint2 *>(sm.q[half][0] + at) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2 *>(sm.q[half][1] + at) = make_uint2(lo[0], lo[1]);
                 }
             }
-            qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - k) << 23);
+            l = mine >= 0x7f80u ? NAN : 0.f;  // an inf or a NaN spoils the row
+            qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - up_shift(mine)) << 23);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.q_full[half]));
         }
@@ -462,13 +527,15 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
         bool far = false;  // some row's m is so large that fp32 must subtract it exactly
         bool fresh = true;  // some row has seen no key yet
         const int s0 = u.sub_begin(), s1 = u.sub_end();
+        int t = t0, kpos0 = u.t_first * TILE + s0 * SUB;  // tile, and the step's first key
 #pragma unroll 1
-        for (int k = s0; k < s1; ++k, ++done) {
-            const int t = t0 - u.begin + (k >> 1), ss = t % SRING;
-            const int kpos0 = u.t_first * TILE + k * SUB, in_tile = (k & 1) * SUB;
+        for (int k = s0; k < s1; ++k, ++done, t += !(k & 1), kpos0 += SUB) {
+            const int ss = t % SRING, in_tile = (k & 1) * SUB;
             const uint32_t s_tmem = tmem + (uint32_t)((done & 1) * SUB);
-            if (k == s0 || !(k & 1))
-                if (!wait(sm.sc_full[ss], t / SRING)) return;
+            const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
+            const bool key0 = p.sink_mode == 1 && kpos0 == 0;
+            if (!wait(sm.s_full[half][done & 1], done >> 1)) return;
+            tc_fence_after();
             // the pages' scales as S and x take them: f above 0 (a zero key scale makes
             // it 0), since a masked S is -inf
             constexpr int NW = SUB / CW;
@@ -478,10 +545,6 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 const float4 s = sm.sc[ss][(in_tile + w * CW) >> p.page_shift];
                 sx[w] = fmaxf(s.x * qf, FLT_MIN), sy[w] = s.y, sz[w] = s.z;
             }
-            const bool mask = kpos0 < u.ilo || kpos0 + SUB - 1 > u.ihi;
-            const bool key0 = p.sink_mode == 1 && kpos0 == 0;
-            if (!wait(sm.s_full[half][done & 1], done >> 1)) return;
-            tc_fence_after();
             uint32_t xs[2][32];
             auto load = [&]() {
                 tmem_ld32(s_tmem, xs[0]);
@@ -518,7 +581,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                 fresh = __any_sync(0xffffffffu, m == NOTHING);
                 far = __any_sync(0xffffffffu, m != NOTHING && fabsf(m) > FAR);
                 if (k > s0) {
-                    if (!wait(sm.pv_done[half], done - 1)) return false;
+                    if (!wait(sm.pv_done[half][(done - 1) & 1], (done - 1) >> 1)) return false;
                     tc_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
@@ -691,12 +754,14 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.v_full[i]), 128);
             mbar_init(smem_u32(&sm.v_empty[i]), 2);
             mbar_init(smem_u32(&sm.drain[i]), 1);
+            mbar_init(smem_u32(&sm.drain[2 + i]), 1);
             mbar_init(smem_u32(&sm.q_full[i]), 128);
             mbar_init(smem_u32(&sm.s_full[i][0]), 1);
             mbar_init(smem_u32(&sm.s_full[i][1]), 1);
             mbar_init(smem_u32(&sm.p_full[i][0]), 4);
             mbar_init(smem_u32(&sm.p_full[i][1]), 4);
-            mbar_init(smem_u32(&sm.pv_done[i]), 1);
+            mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
+            mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
             mbar_init(smem_u32(&sm.o_full[i]), 1);
             mbar_init(smem_u32(&sm.o_empty[i]), 4);
         }
@@ -705,7 +770,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.sc_full[i]), 1);
             mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
         }
-        sm.units.init(2 + 1 + 4 + 8);  // MMA issuers, scales, widening, softmax
+        sm.units.init(4 + 1 + 4 + 8);  // MMA issuers, scales, widening, softmax
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -718,21 +783,24 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 64 + 256 x 192 = the 512 x 128 of the launch
-    if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    // registers: 384 threads x 48 + 256 x 168 = the 640 x 96 of the launch
+    if (warp < SOFTMAX) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
         if (warp == 0) {
             load_tiles<D>(p, &tk, &tv, sm, ctx);
         } else if (warp == 2) {
             load_scales<D>(p, sm, ctx);
         } else if (warp < 4) {
-            if (lane == 0) issue_mmas<D>(p, sm, tmem, warp >> 1, ctx);
+            if (lane == 0) issue_s<D>(sm, tmem, warp >> 1, ctx);
             __syncwarp();
-        } else {
+        } else if (warp < 8) {
             widen<D>(p, sm, ctx);
+        } else if (!(warp & 1)) {
+            if (lane == 0) issue_pv<D>(sm, tmem, (warp >> 1) & 1, ctx);
+            __syncwarp();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         softmax<D, CW>(p, sm, tmem, ctx);
     }
     tc_fence_before();
