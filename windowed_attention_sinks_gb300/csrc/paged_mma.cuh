@@ -25,35 +25,6 @@ __device__ __forceinline__ void mma_f8(uint32_t d, uint64_t a, uint64_t b, uint3
         "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// A shared-memory descriptor in halves. Offsets go to the lower one alone (the address in
-// 16-byte units, far from its 14 bits' end): the thread that issues MMAs has no time for
-// 64-bit sums.
-struct Desc {
-    uint32_t lo, hi;
-    __device__ __forceinline__ Desc(uint32_t l, uint32_t h) : lo(l), hi(h) {}
-    __device__ __forceinline__ explicit Desc(uint64_t d) : lo((uint32_t)d), hi((uint32_t)(d >> 32)) {}
-    __device__ __forceinline__ Desc operator+(uint32_t x) const { return Desc(lo + x, hi); }
-};
-__device__ __forceinline__ void mma_f8(uint32_t d, Desc a, Desc b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n\t}" ::"r"(d),
-        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
-        : "memory");
-}
-// kind::f16 with A in TMEM.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, Desc b, uint32_t idesc,
-                                           uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-        "mov.b64 b, {%2, %3};\n\t"
-        "setp.ne.b32 p, %5, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(acc)
-        : "memory");
-}
 // Shared-memory descriptor of rows of W bytes (16, 32, 64, 128) under W-byte
 // swizzle (16: none), in atoms of 8 rows that follow one another. Rows are the M or
 // N index with K contiguous, or K with one such atom's M or N contiguous.
