@@ -485,7 +485,11 @@ sattn_status sattn_paged_fp8_append(
  * 0 is position 0). A row that sees nothing has o = 0 and lse = -inf (sink
  * with NULL_LOGIT). Rows of skipped sequences, and rows behind the last
  * sequence, are not written. Keys in an invalid page contribute nothing.
- * Scales may be any finite values >= 0.
+ * Scales may be any finite values >= 0. Codes of positions that a row does not
+ * see may hold anything; a NaN code of one that it sees goes out as NaN (a
+ * value's in its column, a key's or a query's in the whole row). Finite sinks
+ * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits
+ * down to 2^-10 of its largest element, a probability 8 bits (few rows) or 11.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the
  *     kernel; any value gives the same results.
  *   workspace: NULL or a caller-owned device buffer of at least
@@ -518,11 +522,13 @@ void sattn_set_debug(int on);
 sattn_status sattn_check_device(void *cuda_stream);
 
 /* Upper bound, in nanoseconds, on any single wait inside a kernel (default
- * one second). A value of 0 restores the default. */
+ * one second; the paged FP8 kernels wait four seconds at most). A value of 0
+ * restores the default. */
 void sattn_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook for the failure path of the tensor-core kernels (window,
- * block-sparse, gathered, gathered FP8, block-selection stats and sums). With
+ * block-sparse, gathered, gathered FP8, paged FP8, block-selection stats and
+ * sums). With
  * `on` nonzero, launches made afterwards start with their MMA-issuing thread
  * waiting for a barrier phase that nothing completes: that wait runs out
  * after the wait limit, the kernel records SATTN_ERR_TIMEOUT in the device
