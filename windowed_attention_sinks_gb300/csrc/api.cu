@@ -182,6 +182,12 @@ bool valid_paged(int Hkv, int d, int num_pages, int page, int max_pages) {
            (page == 16 || page == 32 || page == 64 || page == 128) &&
            (int64_t)max_pages * page <= (1 << 30) && (int64_t)num_pages * Hkv * page <= INT32_MAX;
 }
+// Whether a sequence's rows of a KV head are few enough for the decode kernel, which has
+// 32 at most by one read of the keys. Decode / prefill kernel, us, 32 heads on 8, d = 128:
+//   rows                        8          16          32          40
+//   32 x 1000..16000 keys   98.7 / 209  105 / 209   146 / 215   256 / 218
+//    4 x 8000               26.7 / 43    29 / 43     40 / 43     45 / 44
+//    1 x 4000               20.5 / 24    27 / 25     35 / 25     27 / 25
 bool paged_few_rows(int max_q_len, int G) { return (int64_t)max_q_len * G <= 32; }
 // Rows of `heads` x d elements, `stride` apart, each on a 16-byte boundary.
 bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {

@@ -451,58 +451,77 @@ template <int R> __device__ __forceinline__ void column_sums(float (&l)[R], floa
 }
 
 // Joins the parts of a cut unit: w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
-// null logit), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces. A warp a row:
-// lane c holds part c's sums, the columns are spread over the lanes.
+// null logit), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces. A warp takes RG
+// rows at a time, for as many loads in flight; lane c holds part c's sums, the
+// columns are spread over the lanes.
 template <int D, int R>
 __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long long *orow,
                            const float *rsink, int warp, int warps, int lane) {
     const float2 *sums = part_sums(p.ws);
     const float *prow = reinterpret_cast<const float *>(p.ws + plan_rows_offset(R));
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, RG = R / 8;
     // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ...
     auto slot = [&](int i) { return (size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0); };
 #pragma unroll 1
-    for (int r = warp; r < R; r += warps) {
-        const long long row = orow[r];
-        if (row < 0) continue;
-        float m = NOTHING;
+    for (int r0 = warp * RG; r0 < R; r0 += warps * RG) {
+        if (orow[r0] < 0) break;  // (rows past the unit's last are the last ones)
+        float m[RG], z[RG], acc[RG][E] = {};
+#pragma unroll
+        for (int g = 0; g < RG; ++g) m[g] = NOTHING, z[g] = 0.f;
 #pragma unroll 1
-        for (int i = lane; i < parts; i += 32) m = fmaxf(m, __ldcg(sums + slot(i) * R + r).x);
-        m = warp_max(m);
-        float acc[E] = {};
-        float z = 0.f;
+        for (int i = lane; i < parts; i += 32)
+#pragma unroll
+            for (int g = 0; g < RG; ++g)
+                m[g] = fmaxf(m[g], __ldcg(sums + slot(i) * R + r0 + g).x);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) m[g] = warp_max(m[g]);
 #pragma unroll 1
         for (int i0 = 0; i0 < parts; i0 += 32) {
-            float wt = 0.f;
-            if (i0 + lane < parts) {
-                const float2 s = __ldcg(sums + slot(i0 + lane) * R + r);
-                wt = s.y * ex2(s.x - m);
+            float wt[RG];
+#pragma unroll
+            for (int g = 0; g < RG; ++g) {
+                wt[g] = 0.f;
+                if (i0 + lane < parts) {
+                    const float2 s = __ldcg(sums + slot(i0 + lane) * R + r0 + g);
+                    wt[g] = s.y * ex2(s.x - m[g]);
+                }
             }
-            z += warp_sum(wt);
+#pragma unroll
+            for (int g = 0; g < RG; ++g) z[g] += warp_sum(wt[g]);
             const int cnt = min(32, parts - i0);
-#pragma unroll 8
+#pragma unroll (8 / RG)
             for (int i = 0; i < cnt; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, wt, i);
-                const float *at = prow + (slot(i0 + i) * R + r) * D + lane * E;
-                if constexpr (E == 4) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(at));
-                    acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
-                    acc[2] = fmaf(wi, v.z, acc[2]), acc[3] = fmaf(wi, v.w, acc[3]);
-                } else {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(at));
-                    acc[0] = fmaf(wi, v.x, acc[0]), acc[1] = fmaf(wi, v.y, acc[1]);
+#pragma unroll
+                for (int g = 0; g < RG; ++g) {
+                    const float wi = __shfl_sync(0xffffffffu, wt[g], i);
+                    const float *at = prow + (slot(i0 + i) * R + r0 + g) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(at));
+                        acc[g][0] = fmaf(wi, v.x, acc[g][0]), acc[g][1] = fmaf(wi, v.y, acc[g][1]);
+                        acc[g][2] = fmaf(wi, v.z, acc[g][2]), acc[g][3] = fmaf(wi, v.w, acc[g][3]);
+                    } else {
+                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(at));
+                        acc[g][0] = fmaf(wi, v.x, acc[g][0]), acc[g][1] = fmaf(wi, v.y, acc[g][1]);
+                    }
                 }
             }
         }
-        float lse2 = z == 0.f ? -INFINITY : m + __log2f(z), inv = z == 0.f ? 0.f : __fdividef(1.f, z);
-        if (p.sink_mode == 2) with_null_sink(rsink[r], lse2, inv);
-        __nv_bfloat16 *dst = p.o + row * D + lane * E;
-        if constexpr (E == 4)
-            *reinterpret_cast<uint2 *>(dst) = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv),
-                                                         pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-        if (p.lse && lane == 0) p.lse[row] = lse2 * LN2;
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            const long long row = orow[r0 + g];
+            float lse2 = z[g] == 0.f ? -INFINITY : m[g] + __log2f(z[g]);
+            float inv = z[g] == 0.f ? 0.f : __fdividef(1.f, z[g]);
+            if (p.sink_mode == 2) with_null_sink(rsink[r0 + g], lse2, inv);
+            if (row < 0) continue;
+            __nv_bfloat16 *dst = p.o + row * D + lane * E;
+            if constexpr (E == 4)
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(pack_bf16x2(acc[g][0] * inv, acc[g][1] * inv),
+                               pack_bf16x2(acc[g][2] * inv, acc[g][3] * inv));
+            else
+                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[g][0] * inv, acc[g][1] * inv);
+            if (p.lse && lane == 0) p.lse[row] = lse2 * LN2;
+        }
     }
 }
 
