@@ -23,9 +23,14 @@
 //   prompts:                sequence b owns the units from
 //                           cu[b] / page + 2 b on (a run of n tokens touches
 //                           at most n / page + 2 pages).
+// (256 single tokens: 7.3 us by tokens, 23 by sequences; prompts 106 and 54.)
 // The queries of the same tokens are rotated by further blocks of the launch.
 // An item is 16 columns: the two 8-column halves that rotate into one another,
 // or 16 neighbours, so all global accesses are 8 or 16 bytes wide.
+//
+// Bound by bytes in flight. 16 prompts of 33 .. 1777 tokens, bf16, 32 heads on 8, d = 128,
+// pages of 64: 54 us for 273 MB, 0.77 of the copy rate; four of 7001 .. 8192, fp32, 16
+// heads on 4, d = 64, pages of 16: 71 us, 0.68; 4 single tokens 3.9 us, latency.
 #include "internal.h"
 #include "paged.cuh"
 
@@ -373,7 +378,9 @@ cudaError_t pick(PagedAppendArgs p, const DevInfo &dev, cudaStream_t s) {
     const long long slots = p.T / p.page + 2ll * p.B;
     p.by_token = p.T <= slots;
     p.units = (p.by_token ? p.T : slots) * 2 * p.Hkv;
-    // whole pages: as many threads as hold one in registers
+    // whole pages: as many threads as hold one in registers. (Groups of 32, 64, 128, 256
+    // threads: the bf16 prompts above 58, 53, 54, 63 us, where this gives 128; the fp32
+    // ones 72, 79, 102, 147, where it gives 32.)
     const int want = p.by_token ? 32 : p.page * p.d / (16 * HELD<T>);
     if (want <= 32) return launch<T, 32>(p, dev, s);
     if (want <= 64) return launch<T, 64>(p, dev, s);

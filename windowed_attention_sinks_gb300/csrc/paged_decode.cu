@@ -39,6 +39,13 @@
 //               run beside the other's loads and votes, and are joined at its
 //               end; a unit of at most SOLO tiles is one group's alone, and the
 //               groups take such units in turn.
+//
+// Measured (32 heads on 8, d = 128, replayed graphs): 64 requests of 8001 .. 32768
+// positions 410 us, the copy rate; 32 of 301 .. 8192 54 us, 0.72 of it; one of 1000 13 us,
+// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 106 us, 0.67 (at a unit's
+// end the ring of tiles is full and HBM waits). 128 requests with a window of 127 (64
+// heads on 8, d = 64): 35 us, latency of units of two tiles. One thread for both
+// products took 486 and 64 us on the first two.
 #include <limits.h>
 #include <math.h>
 #include <stdio.h>
@@ -51,9 +58,10 @@ namespace {
 
 constexpr int NTHREADS = 384;
 constexpr int SRING = 16;
-constexpr int EXTRA = 2;  // a unit's own cost, in tiles
 constexpr int UNITS = 8;  // units handed on ahead
-constexpr int SOLO = 2;   // tiles of a unit that one group takes alone
+// Tiles of a unit that one group takes alone, at least 1 (a group needs a tile): with 1, 2
+// and 4 the windowed requests above take 37.5, 36.9 and 37.0 us.
+constexpr int SOLO = 2;
 constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
 constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
 
@@ -81,6 +89,9 @@ template <int D, int R> struct Cfg {
     // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with few rows
     static constexpr int STAGES = (R <= 16 ? 6 : 5) * (128 / D);
     static constexpr int SBUF = 4;  // S buffers
+    // A unit's own cost, in tiles. With 0, 2, 4 and 6: 32 requests 65, 56, 54, 54 us, drafted
+    // tokens 129, 120, 111, 106 us (their ends join and store four times the rows).
+    static constexpr int EXTRA = R <= 16 ? 4 : 6;
     static constexpr int QB = R <= 16 ? 4 : 2;  // units whose Q is at hand
     static constexpr uint32_t O_COL = SBUF * N;
     static constexpr uint32_t USED = O_COL + 2 * N;
@@ -939,7 +950,7 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = dev.sm_count < MAX_PIECES ? dev.sm_count : MAX_PIECES;
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(R, D);
-    DecodeParams p{plan_args(a, split, EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
+    DecodeParams p{plan_args(a, split, Cfg<D, R>::EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
                    a.v_cache, a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
                    a.max_pages, a.num_pages * a.Hkv * a.page, a.scale * LOG2E, a.sinks, a.sink_mode,
                    static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace),
