@@ -42,7 +42,7 @@
 //
 // Measured (32 heads on 8, d = 128, replayed graphs): 64 requests of 8001 .. 32768
 // positions 410 us, the copy rate; 32 of 301 .. 8192 54 us, 0.72 of it; one of 1000 13 us,
-// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 106 us, 0.67 (at a unit's
+// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 104 us, 0.68 (at a unit's
 // end the ring of tiles is full and HBM waits). 128 requests with a window of 127 (64
 // heads on 8, d = 64): 35 us, latency of units of two tiles. One thread for both
 // products took 486 and 64 us on the first two.
@@ -788,6 +788,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         const int col = D == 128 ? key : quarter * 16 + lane;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D + col;
         const int rows0 = solo ? 0 : g * (R / 2), rows1 = solo ? R : rows0 + R / 2;
+        constexpr int STEP = R / 2 < 8 ? R / 2 : 8;  // rows at a time
         uint32_t nan_rows = 0;  // rows whose column is NaN
         if (u.nan_values && writes)
             each_partial_key<D>(p, u, u.lo, u.hi, [&](int k, const uint8_t *codes) {
@@ -800,17 +801,22 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 }
             });
 #pragma unroll 1
-        for (int r0 = rows0; r0 < rows1; r0 += 4) {
-            uint32_t v[4][4];  // group 0 hi, lo, group 1 hi, lo
+        for (int r0 = rows0; r0 < rows1; r0 += STEP) {
+            uint32_t v[4][STEP];  // group 0 hi, lo, group 1 hi, lo
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (!has[s]) continue;
-                tmem_ld4(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
-                tmem_ld4(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
+                if constexpr (STEP == 8) {
+                    tmem_ld8(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
+                    tmem_ld8(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
+                } else {
+                    tmem_ld4(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
+                    tmem_ld4(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
+                }
             }
             tc_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < STEP; ++e) {
                 const int r = r0 + e;
                 float acc = 0.f;
 #pragma unroll
