@@ -41,10 +41,10 @@
 //               groups take such units in turn.
 //
 // Measured (32 heads on 8, d = 128, replayed graphs): 64 requests of 8001 .. 32768
-// positions 410 us, the copy rate; 32 of 301 .. 8192 54 us, 0.72 of it; one of 1000 13 us,
-// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 104 us, 0.68 (at a unit's
+// positions 410 us, the copy rate; 32 of 301 .. 8192 52 us, 0.75 of it; one of 1000 10.5 us,
+// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 101 us, 0.70 (at a unit's
 // end the ring of tiles is full and HBM waits). 128 requests with a window of 127 (64
-// heads on 8, d = 64): 35 us, latency of units of two tiles. One thread for both
+// heads on 8, d = 64): 34 us, latency of units of two tiles. One thread for both
 // products took 486 and 64 us on the first two.
 #include <limits.h>
 #include <math.h>
@@ -878,39 +878,37 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
     }
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < C::STAGES; ++i) {
-            mbar_init(smem_u32(&sm.k_full[i]), 1);
-            mbar_init(smem_u32(&sm.k_empty[i]), 1);
-            mbar_init(smem_u32(&sm.v_full[i]), 1);
-            mbar_init(smem_u32(&sm.v_empty[i]), 1);
+    if (warp == 2) {  // a lane a barrier: one thread would take longer than the plan
+        static_assert(C::STAGES <= 32 && SRING <= 32 && UNITS <= 32, "a lane a barrier");
+        if (lane < C::STAGES) {
+            mbar_init(smem_u32(&sm.k_full[lane]), 1);
+            mbar_init(smem_u32(&sm.k_empty[lane]), 1);
+            mbar_init(smem_u32(&sm.v_full[lane]), 1);
+            mbar_init(smem_u32(&sm.v_empty[lane]), 1);
         }
-#pragma unroll 1
-        for (int i = 0; i < SRING; ++i) {
-            mbar_init(smem_u32(&sm.sc_full[i]), 1);
-            mbar_init(smem_u32(&sm.sc_empty[i]), 4);
+        if (lane < SRING) {
+            mbar_init(smem_u32(&sm.sc_full[lane]), 1);
+            mbar_init(smem_u32(&sm.sc_empty[lane]), 4);
         }
-#pragma unroll 1
-        for (int i = 0; i < C::QB; ++i) {
-            mbar_init(smem_u32(&sm.q_full[i]), 1);
-            mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);  // the MMAs and the softmax warps
+        if (lane < C::QB) {
+            mbar_init(smem_u32(&sm.q_full[lane]), 1);
+            mbar_init(smem_u32(&sm.q_empty[lane]), 1 + 8);  // the MMAs and the softmax warps
         }
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.p_full[i]), 4);
-            mbar_init(smem_u32(&sm.pv_done[i]), 1);
-            mbar_init(smem_u32(&sm.o_empty[i]), 8);
-            mbar_init(smem_u32(&sm.drain[i]), 1);
+        if (lane < 2) {
+            mbar_init(smem_u32(&sm.p_full[lane]), 4);
+            mbar_init(smem_u32(&sm.pv_done[lane]), 1);
+            mbar_init(smem_u32(&sm.o_empty[lane]), 8);
+            mbar_init(smem_u32(&sm.drain[lane]), 1);
         }
-#pragma unroll 1
-        for (int i = 0; i < C::SBUF; ++i) {
-            mbar_init(smem_u32(&sm.s_full[i]), 1);
-            mbar_init(smem_u32(&sm.s_empty[i]), 4);
+        if (lane < C::SBUF) {
+            mbar_init(smem_u32(&sm.s_full[lane]), 1);
+            mbar_init(smem_u32(&sm.s_empty[lane]), 4);
         }
-        mbar_init(smem_u32(&sm.both), 8);
-        sm.units.init(2 + 1 + 8);  // MMA issuers, queries, softmax
-        sm.abort = 0;
+        if (lane == 0) {
+            mbar_init(smem_u32(&sm.both), 8);
+            sm.abort = 0;
+        }
+        sm.units.init(2 + 1 + 8, lane);  // MMA issuers, queries, softmax
         fence_mbar_init();
     }
     if (warp == 1) {

@@ -741,37 +741,34 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
     }
-    if (threadIdx.x == 0) {
-#pragma unroll 1
-        for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sm.k_full[i]), 1);
-            mbar_init(smem_u32(&sm.k_empty[i]), 2);  // both halves' MMAs
-            mbar_init(smem_u32(&sm.v8_full[i]), 1);
-            mbar_init(smem_u32(&sm.v8_empty[i]), 128);
+    if (warp == 2) {  // a lane a barrier: one thread would take longer than the plan
+        if (lane < STAGES) {
+            mbar_init(smem_u32(&sm.k_full[lane]), 1);
+            mbar_init(smem_u32(&sm.k_empty[lane]), 2);  // both halves' MMAs
+            mbar_init(smem_u32(&sm.v8_full[lane]), 1);
+            mbar_init(smem_u32(&sm.v8_empty[lane]), 128);
         }
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sm.v_full[i]), 128);
-            mbar_init(smem_u32(&sm.v_empty[i]), 2);
-            mbar_init(smem_u32(&sm.drain[i]), 1);
-            mbar_init(smem_u32(&sm.drain[2 + i]), 1);
-            mbar_init(smem_u32(&sm.q_full[i]), 128);
-            mbar_init(smem_u32(&sm.s_full[i][0]), 1);
-            mbar_init(smem_u32(&sm.s_full[i][1]), 1);
-            mbar_init(smem_u32(&sm.p_full[i][0]), 4);
-            mbar_init(smem_u32(&sm.p_full[i][1]), 4);
-            mbar_init(smem_u32(&sm.pv_done[i][0]), 1);
-            mbar_init(smem_u32(&sm.pv_done[i][1]), 1);
-            mbar_init(smem_u32(&sm.o_full[i]), 1);
-            mbar_init(smem_u32(&sm.o_empty[i]), 4);
+        if (lane < 2) {
+            mbar_init(smem_u32(&sm.v_full[lane]), 128);
+            mbar_init(smem_u32(&sm.v_empty[lane]), 2);
+            mbar_init(smem_u32(&sm.drain[lane]), 1);
+            mbar_init(smem_u32(&sm.drain[2 + lane]), 1);
+            mbar_init(smem_u32(&sm.q_full[lane]), 128);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
+                mbar_init(smem_u32(&sm.p_full[lane][b]), 4);
+                mbar_init(smem_u32(&sm.pv_done[lane][b]), 1);
+            }
+            mbar_init(smem_u32(&sm.o_full[lane]), 1);
+            mbar_init(smem_u32(&sm.o_empty[lane]), 4);
         }
-#pragma unroll 1
-        for (int i = 0; i < SRING; ++i) {
-            mbar_init(smem_u32(&sm.sc_full[i]), 1);
-            mbar_init(smem_u32(&sm.sc_empty[i]), 8 + 4);  // softmax and widening warps
+        if (lane < SRING) {
+            mbar_init(smem_u32(&sm.sc_full[lane]), 1);
+            mbar_init(smem_u32(&sm.sc_empty[lane]), 8 + 4);  // softmax and widening warps
         }
-        sm.units.init(4 + 1 + 4 + 8);  // MMA issuers, scales, widening, softmax
-        sm.abort = 0;
+        if (lane == 0) sm.abort = 0;
+        sm.units.init(4 + 1 + 4 + 8, lane);  // MMA issuers, scales, widening, softmax
         fence_mbar_init();
     }
     if (warp == 1) {

@@ -6,7 +6,7 @@
 // value counts codes * v_scale. Bound by the one-key-at-a-time chain (a
 // reduction over the warp, an exponential) rather than by memory: it is the
 // exact fp32 form, the bf16 kernels are the fast ones. 32 requests of 301 .. 8192
-// positions, 32 heads on 8, d = 128: 9.4 ms against their 54 us.
+// positions, 32 heads on 8, d = 128: 9.4 ms against their 52 us.
 #include <math.h>
 
 #include "internal.h"
