@@ -424,14 +424,15 @@ def _token_rows(t, name, T, heads, d, dtype, dev):
     return st[0] if T > 1 else heads * d
 
 
-def _out(t, name, shape, dtype, dev):
-    """Checks an output tensor, or makes one."""
+def _out(t, name, shape, dtype, device):
+    """Checks an output tensor, or makes one. (On a torch.device: from its index torch takes
+    some microseconds longer.)"""
     import torch
 
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous %s %s on cuda:%d" % (name, dtype, shape, dev))
+        return torch.empty(shape, dtype=dtype, device=device)
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s %s on %s" % (name, dtype, shape, device))
     return t
 
 
@@ -464,7 +465,7 @@ def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     if q is not None:
         H = q.shape[1]
         qs = _token_rows(q, "q", T, H, d, dt, dev)
-        q_out = _out(q_out, "q_out", (T, H, d), dt, dev)
+        q_out = _out(q_out, "q_out", (T, H, d), dt, k_cache.device)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -509,8 +510,9 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
     L = lib()
     nb, ws = 0, None
     with _OnDevice(dev, stream) as s:
-        o = _out(o, "o", (T, H, d), dt, dev)
-        lse = _out(lse, "lse", (T, H), torch.float32, dev)
+        device = k_cache.device
+        o = _out(o, "o", (T, H, d), dt, device)
+        lse = _out(lse, "lse", (T, H), torch.float32, device)
         if workspace is not None:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous on cuda:%d" % dev)
@@ -518,10 +520,10 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
         elif dt is torch.bfloat16:
             nb = L.sattn_paged_fp8_workspace_bytes(n, H, Hkv, d)
             if nb and stream is None:
-                workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+                workspace = torch.empty(nb, dtype=torch.uint8, device=device)
             elif nb:  # the allocator must know the stream that uses it
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+                    workspace = torch.empty(nb, dtype=torch.uint8, device=device)
             ws = workspace.data_ptr() if nb else None
         rc = L.sattn_paged_fp8_fwd(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),

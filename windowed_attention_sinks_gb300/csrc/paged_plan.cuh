@@ -158,6 +158,8 @@ __device__ __forceinline__ void plan_piece(PlanStart &ps, long long total, bool 
         ps.x1 = x1;
         ps.total = total;
         ps.pieces = pieces;
+        ps.b = ps.h = ps.rt = 0;  // (in bounds even if the lengths change meanwhile)
+        ps.ustart = x0;
     }
 }
 
@@ -220,6 +222,7 @@ __device__ __forceinline__ void plan_small(const PlanArgs &p, PlanStart &ps, con
     const long long mine = ph * p.Hkv, upto = warp_prefix(mine), before = upto - mine;
     long long x0, x1;
     plan_piece(ps, __shfl_sync(0xffffffffu, upto, 31), lane == 0, x0, x1);
+    __syncwarp();
     if (x0 >= x1) return;
     const int b = __ffs(__ballot_sync(0xffffffffu, x0 >= before && x0 < upto)) - 1;
     if (b < 0) return;
