@@ -496,6 +496,8 @@ sattn_status sattn_paged_fp8_append(
  *     sattn_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned; it receives
  *     partial results and is free again when the call's work has run. Calls
  *     that may overlap on the GPU need one each.
+ * After a timeout call sattn_check_device before the next of these calls: it
+ * also clears what the abandoned call left in its join counters.
  */
 size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
 sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,
