@@ -489,7 +489,10 @@ sattn_status sattn_paged_fp8_append(
  * see may hold anything; a NaN code of one that it sees goes out as NaN (a
  * value's in its column, a key's or a query's in the whole row). Finite sinks
  * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits
- * down to 2^-10 of its largest element, a probability 8 bits (few rows) or 11.
+ * down to 2^-10 of its largest element; a probability keeps 9 bits down to 2^-24 of the
+ * largest (few rows) or 11 down to 2^-21, and below that is off by at most 2^-32 of it.
+ * What counts here is the probability times its page's value scale. The denominator and
+ * lse take the unrounded ones.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the
  *     kernel; any value gives the same results.
  *   workspace: NULL or a caller-owned device buffer of at least

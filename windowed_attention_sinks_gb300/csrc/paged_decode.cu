@@ -9,16 +9,25 @@
 //    shared memory. Both products are taken with the keys (then the columns of V) as the
 //    128 rows of the MMA and the query rows as its N columns:
 //      S^T [128 keys, 2R]   = K [128, D]   Q^T,
-//      O^T [D, 2R]         += V^T [D, 128] P^T   (V read column-major).
-//  * An e4m3 operand has 4 significant bits, so Q and P are split: x = hi +
+//      O^T [D, 3R]         += V^T [D, 128] P^T   (V read column-major).
+//  * An e4m3 operand has 4 significant bits, so Q is split: x = hi +
 //    lo / 16 with hi = e4m3(x) and lo = e4m3(16 (x - hi)), side by side as 2R
 //    columns, joined again in fp32. hi + lo / 16 has 8 significant bits, a
 //    bf16's, for |x| from 2^-6 to 448, and an absolute error of at most 2^-14
 //    below that. Each row of Q is scaled by a power of two so that its largest value is
 //    in [128, 256): bf16 queries go in exactly down to 2^-14 of the row's largest.
-//    P is 2^(4 + e - m) <= 2^8 with e the exponent below, so the floor
-//    is 2^-18 .. 2^-22 of the largest weight. The extra columns are free: the
-//    MMA is a small part of the time a tile takes to arrive.
+//  * P needs range above all: a long tail of keys far below the largest weighs as much
+//    as that, and what P V loses of each, the row sum counts. So P goes in as
+//    e5m2 (kind::f8f6f4 takes its operands' types apart), in 3R columns: P = 2^(10 + e - m)
+//    <= 2^15, with e the exponent below, is rounded to 9 significant bits in f16
+//    and cut into t0 + t1 / 8 + t2 / 64. An e5m2 is an f16's upper byte, so each term is
+//    the next byte of what the ones before leave, exactly: 3 + 3 + 3 bits and no
+//    conversion. P keeps its 9 bits down to 2^-14, which is 2^-24 of the largest weight, and
+//    below that is off by at most 2^-23, 2^-33 of it. (Two e4m3 terms as for Q lose
+//    all below 2^-18 of the largest: 32768 equal keys 13 nats below another one's gave
+//    half of their share. A second pair of them for the rest of small P is right too, but its
+//    conversions take drafted tokens from 102 to 200 us; these terms to 104.)
+//  The extra columns are free: the MMA is a small part of the time a tile takes to arrive.
 //  * A thread holds one key, so the page's scales are scalars to it: the key's multiplies S, the
 //    value's goes into the exponent, e = scale log2(e) s + log2(v_scale), and
 //    V's codes need no scaling. The row sum divides it out again.
@@ -62,8 +71,10 @@ constexpr int UNITS = 8;  // units handed on ahead
 // Tiles of a unit that one group takes alone, at least 1 (a group needs a tile): with 1, 2
 // and 4 the windowed requests above take 37.5, 36.9 and 37.0 us.
 constexpr int SOLO = 2;
-constexpr float BASE = 4.f;   // P = 2^(BASE + e - m)
-constexpr float LIMIT = 8.f;  // m moves when BASE + e - m exceeds this
+// P = 2^(BASE + e - m). One more would halve the floor, and m moves sooner: with 9, 10 and 11 the
+// drafted tokens below take 103, 104 and 105 us, with four times their logits 116, 119 and 122.
+constexpr float BASE = 10.f;
+constexpr float LIMIT = 15.f;  // m moves when BASE + e - m exceeds this
 
 struct DecodeParams {
     PlanArgs plan;
@@ -84,17 +95,20 @@ struct DecodeParams {
 };
 
 template <int D, int R> struct Cfg {
-    static constexpr int N = 2 * R;
+    static constexpr int N = 2 * R;  // columns of S: Q's hi and lo
+    // Columns of O: P's three terms (a multiple of 16; the last 8 of 32 are not read), and
+    // the bytes of a key's row of P
+    static constexpr int NO = R == 8 ? 32 : 3 * R, PW = 4 * R;
     static constexpr uint32_t TILE_BYTES = TILE * D;
-    // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with few rows
+    // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with fewer rows
     static constexpr int STAGES = (R <= 16 ? 6 : 5) * (128 / D);
     static constexpr int SBUF = 4;  // S buffers
     // A unit's own cost, in tiles. With 0, 2, 4 and 6: 32 requests 65, 56, 54, 54 us, drafted
     // tokens 129, 120, 111, 106 us (their ends join and store four times the rows).
     static constexpr int EXTRA = R <= 16 ? 4 : 6;
-    static constexpr int QB = R <= 16 ? 4 : 2;  // units whose Q is at hand
+    static constexpr int QB = R <= 8 ? 4 : 2;  // units whose Q is at hand
     static constexpr uint32_t O_COL = SBUF * N;
-    static constexpr uint32_t USED = O_COL + 2 * N;
+    static constexpr uint32_t USED = O_COL + 2 * NO;
     static constexpr uint32_t COLS = USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
 };
 
@@ -103,7 +117,7 @@ template <int D, int R> struct alignas(1024) Smem {
     uint8_t k[C::STAGES][C::TILE_BYTES];
     uint8_t v[C::STAGES][C::TILE_BYTES];
     uint8_t q[C::QB][C::N * D];
-    uint8_t p[2][C::N * TILE];
+    uint8_t p[2][C::PW * TILE];
     float4 sc[SRING][8];        // page's k scale, log2 v scale, 1 / v scale, v scale > 0
     float wmax[2][4][R];        // column maxima of the warps
     float alpha[2][R];          // what a move of m multiplies l and O by
@@ -325,7 +339,7 @@ __device__ void load_queries(const DecodeParams &p, Smem<D, R> &sm, const DevCtx
                                         (__vcmpgeu2(v[e] & 0x7fff7fffu, 0x7f807f80u) & 0x7fff7fffu);
                     const uint32_t h = e4m3x2_of_f16x2(ab);
                     hi[e >> 1] |= h << (16 * (e & 1));
-                    lo[e >> 1] |= e4m3x2_of_f16x2(sixteen_times_difference(ab, e4m3x2_to_f16x2(h)))
+                    lo[e >> 1] |= e4m3x2_of_f16x2(times_difference<16>(ab, e4m3x2_to_f16x2(h)))
                                   << (16 * (e & 1));
                 }
                 // 8 bytes: half of the 16-byte unit c / 2
@@ -396,9 +410,9 @@ __device__ __forceinline__ int group_of(int i, int n, int t) { return (n <= SOLO
 template <int D, int R>
 __device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
     using C = Cfg<D, R>;
-    constexpr uint32_t IDESC = idesc_e4m3_f32(D, C::N, 1, 1);
+    constexpr uint32_t IDESC = idesc_e4m3_f32(D, C::NO, 1, 1) | B_E5M2;
     volatile int *abort = &sm.abort;
-    const uint64_t dv = desc_rows<D>(smem_u32(sm.v[0])), dp = desc_rows<C::N>(smem_u32(sm.p[0]));
+    const uint64_t dv = desc_rows<D>(smem_u32(sm.v[0])), dp = desc_rows<C::PW>(smem_u32(sm.p[0]));
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
@@ -421,11 +435,11 @@ __device__ void issue_pv(Smem<D, R> &sm, uint32_t tmem, const DevCtx &ctx) {
             if (!ok) break;
             tc_fence_after();
             const uint64_t a = dv + (uint64_t)(st * (C::TILE_BYTES >> 4));
-            const uint64_t b = dp + (uint64_t)(g * (C::N * TILE >> 4));
-            const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::N;
+            const uint64_t b = dp + (uint64_t)(g * (C::PW * TILE >> 4));
+            const uint32_t o = tmem + C::O_COL + (uint32_t)g * C::NO;
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)  // 32 keys: 32 rows of V and of P
-                mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * (32 * C::N >> 4)),
+                mma_f8(o, a + (uint64_t)(kk * (32 * D >> 4)), b + (uint64_t)(kk * (32 * C::PW >> 4)),
                        IDESC, kk > 0 || !first);
             tc_commit(smem_u32(&sm.pv_done[g]));
             tc_commit(smem_u32(&sm.v_empty[st]));
@@ -695,53 +709,54 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     wait(sm.pv_done[g], done - 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < C::N; c += 8) {
+                    for (int c = 0; c < 3 * R; c += 8) {
                         uint32_t v[8];
-                        tmem_ld8(o_tmem + (uint32_t)(g * C::N + c), v);
+                        tmem_ld8(o_tmem + (uint32_t)(g * C::NO + c), v);
                         tc_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             v[e] = __float_as_uint(__uint_as_float(v[e]) * sm.alpha[g][(c + e) % R]);
-                        tmem_st8(o_tmem + (uint32_t)(g * C::N + c), v);
+                        tmem_st8(o_tmem + (uint32_t)(g * C::NO + c), v);
                     }
                     tc_wait_st();
                 }
             }
             // P overwrites the group's last one, which its P V has read by now as a rule
             if (done >= 1) wait(sm.pv_done[g], done - 1);
-            // the key's row of P: R hi codes, then R lo codes, 16 bytes a store
+            // the key's row of P: R codes of each term, 16 bytes a store
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
                 constexpr int CH = R < 16 ? R : 16;
-                uint32_t hi[4], lo[4];
+                uint32_t t[3][4];
 #pragma unroll
-                for (int e = 0; e < CH; e += 2) {
-                    const int r = c + e;
-                    const float4 m = m4[r / 4];
-                    const float a = ex2(x[r] - (e & 2 ? m.z : m.x) + BASE);
-                    const float b = ex2(x[r + 1] - (e & 2 ? m.w : m.y) + BASE);
-                    l[r] = fmaf(a, sc.z, l[r]);
-                    l[r + 1] = fmaf(b, sc.z, l[r + 1]);
-                    // by way of f16, whose 11 bits hold hi + lo / 16, in pairs
-                    const uint32_t ab = pack_f16x2(a, b), h = e4m3x2_of_f16x2(ab);
-                    const uint32_t g2 =
-                        e4m3x2_of_f16x2(sixteen_times_difference(ab, e4m3x2_to_f16x2(h)));
-                    if (e & 2) {
-                        hi[e >> 2] |= h << 16;
-                        lo[e >> 2] |= g2 << 16;
-                    } else {
-                        hi[e >> 2] = h;
-                        lo[e >> 2] = g2;
+                for (int e = 0; e < CH; e += 4) {
+                    const float4 m = m4[(c + e) / 4];
+                    const float mm[4] = {m.x, m.y, m.z, m.w};
+                    uint32_t y[2][3];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int r = c + e + 2 * h;
+                        const float a = ex2(x[r] - mm[2 * h] + BASE);
+                        const float b = ex2(x[r + 1] - mm[2 * h + 1] + BASE);
+                        l[r] = fmaf(a, sc.z, l[r]);
+                        l[r + 1] = fmaf(b, sc.z, l[r + 1]);
+                        e5m2_terms(pack_f16x2(a, b), y[h]);
                     }
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)  // the upper bytes
+                        t[k][e >> 2] = __byte_perm(y[0][k], y[1][k], 0x7531);
                 }
                 if constexpr (R == 8) {
-                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, 0)) =
-                        make_uint4(hi[0], hi[1], lo[0], lo[1]);
+                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::PW>(key, 0)) =
+                        make_uint4(t[0][0], t[0][1], t[1][0], t[1][1]);
+                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::PW>(key, 1)) =
+                        make_uint4(t[2][0], t[2][1], 0, 0);
                 } else {
-                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, c / 16)) =
-                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::N>(key, (R + c) / 16)) =
-                        make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        *reinterpret_cast<uint4 *>(
+                            sm.p[g] + sw_offset<C::PW>(key, (k * R + c) / 16)) =
+                            make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
                 }
             }
             fence_proxy_async_smem();
@@ -802,16 +817,15 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             });
 #pragma unroll 1
         for (int r0 = rows0; r0 < rows1; r0 += STEP) {
-            uint32_t v[4][STEP];  // group 0 hi, lo, group 1 hi, lo
+            uint32_t v[6][STEP];  // the terms of group 0, of group 1
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (!has[s]) continue;
-                if constexpr (STEP == 8) {
-                    tmem_ld8(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
-                    tmem_ld8(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
-                } else {
-                    tmem_ld4(o_tmem + (uint32_t)(s * C::N + r0), v[2 * s]);
-                    tmem_ld4(o_tmem + (uint32_t)(s * C::N + R + r0), v[2 * s + 1]);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    const uint32_t at = o_tmem + (uint32_t)(s * C::NO + k * R + r0);
+                    if constexpr (STEP == 8) tmem_ld8(at, v[3 * s + k]);
+                    else tmem_ld4(at, v[3 * s + k]);
                 }
             }
             tc_wait_ld();
@@ -823,8 +837,9 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 for (int s = 0; s < 2; ++s)
                     if (has[s])
                         acc = fmaf(sm.wt[w][s][r],
-                                   fmaf(__uint_as_float(v[2 * s + 1][e]), 0.0625f,
-                                        __uint_as_float(v[2 * s][e])),
+                                   fmaf(fmaf(__uint_as_float(v[3 * s + 2][e]), 0.125f,
+                                             __uint_as_float(v[3 * s + 1][e])),
+                                        0.125f, __uint_as_float(v[3 * s][e])),
                                    acc);
                 if (!writes) continue;
                 if (nan_rows >> r & 1) acc = NAN;

@@ -10,6 +10,7 @@
 
 namespace sattn {
 
+constexpr uint32_t B_E5M2 = 1u << 10;  // in such a descriptor: B is e5m2
 // kind::f8f6f4, e4m3 x e4m3 -> f32; a_mn, b_mn: A is stored with its M index, B with its
 // N index contiguous.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N, uint32_t a_mn,
@@ -88,12 +89,22 @@ __device__ __forceinline__ uint32_t difference_f16x2(uint32_t a, uint32_t b) {
                               *reinterpret_cast<const __half2 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
-// 16 (a - b) of two f16 pairs.
-__device__ __forceinline__ uint32_t sixteen_times_difference(uint32_t a, uint32_t b) {
+// F (a - b) of two f16 pairs.
+template <int F> __device__ __forceinline__ uint32_t times_difference(uint32_t a, uint32_t b) {
     const __half2 d = __hmul2(__hsub2(*reinterpret_cast<const __half2 *>(&a),
                                       *reinterpret_cast<const __half2 *>(&b)),
-                              __float2half2_rn(16.f));
+                              __float2half2_rn((float)F));
     return *reinterpret_cast<const uint32_t *>(&d);
+}
+// Two f16 in [0, 2^15], rounded to 9 significant bits (to 2^-22 below 2^-14), as three
+// e5m2 each: t[0] + t[1] / 8 + t[2] / 64, in the upper bytes of t's halves. Each cut leaves
+// what an f16 holds exactly. A NaN is not kept.
+__device__ __forceinline__ void e5m2_terms(uint32_t x, uint32_t (&t)[3]) {
+    const uint32_t y = (x + 0x00020002u) & 0xfffcfffcu;
+    t[0] = y & 0xff00ff00u;
+    const uint32_t z = times_difference<8>(y, t[0]);
+    t[1] = z & 0xff00ff00u;
+    t[2] = times_difference<8>(z, t[1]);
 }
 
 // x = keep ? x : -inf. Volatile so that it stays behind the branch it is written in:
