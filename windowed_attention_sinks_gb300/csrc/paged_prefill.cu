@@ -324,11 +324,13 @@ __device__ void issue_s(Smem<D> &sm, uint32_t tmem, int half, const DevCtx &ctx)
 #pragma unroll 1
         for (int k = s0; k < s1 && ok; ++k, ++x) {
             const int st = t % STAGES, b = x & 1;
-            // (and the tile's scales, so that who finds S finds them)
+            // The tile's scales too, so that who finds S finds them: a commit orders the MMAs
+            // alone, so this thread arrives on S's barrier for what it has seen itself.
             if (k == s0 || !(k & 1))
                 ok = wait(sm.k_full[st], t / STAGES) && wait(sm.sc_full[t % SRING], t / SRING);
             if (x >= 2) ok = ok && wait(sm.pv_done[half][b], (x >> 1) - 1);
             if (!ok) break;
+            mbar_arrive(smem_u32(&sm.s_full[half][b]));
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(st * (TILE * D >> 4) + (k & 1) * (SUB * D >> 4));
 #pragma unroll
@@ -400,6 +402,8 @@ __device__ void issue_pv(Smem<D> &sm, uint32_t tmem, int half, const DevCtx &ctx
                 ++t;
             }
         }
+        // (the arrival: what the widening warps noted of the unit's values)
+        if (ok) mbar_arrive(smem_u32(&sm.o_full[half]));
         tc_commit(smem_u32(&sm.o_full[half]));
         ++ec;
     }
@@ -756,11 +760,11 @@ prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ C
             mbar_init(smem_u32(&sm.q_full[lane]), 128);
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
+                mbar_init(smem_u32(&sm.s_full[lane][b]), 2);  // the issuer and its MMAs
                 mbar_init(smem_u32(&sm.p_full[lane][b]), 4);
                 mbar_init(smem_u32(&sm.pv_done[lane][b]), 1);
             }
-            mbar_init(smem_u32(&sm.o_full[lane]), 1);
+            mbar_init(smem_u32(&sm.o_full[lane]), 2);
             mbar_init(smem_u32(&sm.o_empty[lane]), 4);
         }
         if (lane < SRING) {
