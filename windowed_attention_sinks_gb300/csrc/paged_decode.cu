@@ -122,9 +122,14 @@ template <int D, int R> struct alignas(1024) Smem {
     float wmax[2][4][R];        // column maxima of the warps
     float alpha[2][R];          // what a move of m multiplies l and O by
     // of a unit (by its Q buffer):
-    alignas(16) float mx[C::QB][2][R];  // the groups' running maxima
+    alignas(16) float mx[C::QB][2][R];  // the groups' running maxima m
+    // sums apart, where a group's last such unit is this one: their maxima and sums, of
+    // each warp, and the m that the group's other sums are in terms of
+    int apart[2];
+    float fn[2][4][R], fl[2][4][R], fm[2][R];
     float lx[C::QB][2][4][R];   // the warps' row sums
     float wt[C::QB][2][R];      // what a row of each group's O^T is multiplied by
+    float half[C::QB][R];       // and, where row sums are apart, before that
     long long orow[C::QB][R];   // output row of each query row, -1 past the last
     int rpos[C::QB][R];         // its position
     float rsink[C::QB][R];      // its sink (log2 units)
@@ -212,6 +217,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
         if (lane == 0) ok = sm.units.put(index, u, ctx, &sm.abort);
         ++index;
         ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        bool far = false;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             // a page a lane
             const int j = (u.t_first + c) * per_tile + lane;
@@ -221,7 +227,7 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
                     : -1;
             bad |= pid == -2;
             const int row = pid < 0 ? p.rows_total : (pid * p.plan.Hkv + u.h) * p.page;
-            const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
+            float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
             const int nt = min(chunk, u.end - c);
 #pragma unroll 1
             for (int i = 0; i < nt; ++i, ++t) {
@@ -250,6 +256,13 @@ __device__ void load_tiles(const DecodeParams &p, const CUtensorMap *tk, const C
                     ok = __all_sync(0xffffffffu, bar_wait(smem_u32(&sm.sc_empty[ss]),
                                                            (t / SRING - 1) & 1, ctx, &sm.abort));
                 if (!ok) break;
+                if (i == 0) {  // (behind the tile's copies: they are what takes long)
+                    far = far || __any_sync(0xffffffffu, pid >= 0 && far_log2(s.y));
+                    if (far) {
+                        s.z = -1.f;
+                        if (lane == 0) sm.units.u[(index - 1) % UNITS].far = 1;
+                    }
+                }
                 if (here) sm.sc[ss][k] = s;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.sc_full[ss]));
@@ -490,9 +503,9 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
 #pragma unroll 1
     for (int r0 = warp * RG; r0 < R; r0 += warps * RG) {
         if (orow[r0] < 0) break;  // (rows past the unit's last are the last ones)
-        float m[RG], z[RG], acc[RG][E] = {};
+        float m[RG], z[RG], acc[RG][E] = {}, first[RG];
 #pragma unroll
-        for (int g = 0; g < RG; ++g) m[g] = NOTHING, z[g] = 0.f;
+        for (int g = 0; g < RG; ++g) m[g] = NOTHING;
 #pragma unroll 1
         for (int i = lane; i < parts; i += 32)
 #pragma unroll
@@ -500,19 +513,33 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
                 m[g] = fmaxf(m[g], __ldcg(sums + slot(i) * R + r0 + g).x);
 #pragma unroll
         for (int g = 0; g < RG; ++g) m[g] = warp_max(m[g]);
+        auto weight = [&](int i, int g) {
+            if (i >= parts) return 0.f;
+            const float2 s = __ldcg(sums + slot(i) * R + r0 + g);
+            return s.y * ex2(s.x - m[g]);
+        };
+#pragma unroll
+        for (int g = 0; g < RG; ++g) first[g] = weight(lane, g);
+#pragma unroll
+        for (int g = 0; g < RG; ++g) z[g] = warp_sum(first[g]);
+#pragma unroll 1
+        for (int i0 = 32; i0 < parts; i0 += 32)
+#pragma unroll
+            for (int g = 0; g < RG; ++g) z[g] += warp_sum(weight(i0 + lane, g));
+        float inv[RG], lse2[RG];
+#pragma unroll
+        for (int g = 0; g < RG; ++g) {
+            lse2[g] = z[g] == 0.f ? -INFINITY : m[g] + __log2f(z[g]);
+            inv[g] = z[g] == 0.f ? 0.f : __fdividef(1.f, z[g]);
+            if (p.sink_mode == 2) with_null_sink(rsink[r0 + g], lse2[g], inv[g]);
+        }
+        // (the weights over their sum: values near fp32's largest do not overflow)
 #pragma unroll 1
         for (int i0 = 0; i0 < parts; i0 += 32) {
             float wt[RG];
 #pragma unroll
-            for (int g = 0; g < RG; ++g) {
-                wt[g] = 0.f;
-                if (i0 + lane < parts) {
-                    const float2 s = __ldcg(sums + slot(i0 + lane) * R + r0 + g);
-                    wt[g] = s.y * ex2(s.x - m[g]);
-                }
-            }
-#pragma unroll
-            for (int g = 0; g < RG; ++g) z[g] += warp_sum(wt[g]);
+            for (int g = 0; g < RG; ++g)
+                wt[g] = (i0 == 0 ? first[g] : weight(i0 + lane, g)) * inv[g];
             const int cnt = min(32, parts - i0);
 #pragma unroll (8 / RG)
             for (int i = 0; i < cnt; ++i) {
@@ -534,20 +561,86 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
 #pragma unroll
         for (int g = 0; g < RG; ++g) {
             const long long row = orow[r0 + g];
-            float lse2 = z[g] == 0.f ? -INFINITY : m[g] + __log2f(z[g]);
-            float inv = z[g] == 0.f ? 0.f : __fdividef(1.f, z[g]);
-            if (p.sink_mode == 2) with_null_sink(rsink[r0 + g], lse2, inv);
             if (row < 0) continue;
             __nv_bfloat16 *dst = p.o + row * D + lane * E;
             if constexpr (E == 4)
                 *reinterpret_cast<uint2 *>(dst) =
-                    make_uint2(pack_bf16x2(acc[g][0] * inv, acc[g][1] * inv),
-                               pack_bf16x2(acc[g][2] * inv, acc[g][3] * inv));
+                    make_uint2(pack_bf16x2(acc[g][0], acc[g][1]),
+                               pack_bf16x2(acc[g][2], acc[g][3]));
             else
-                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[g][0] * inv, acc[g][1] * inv);
-            if (p.lse && lane == 0) p.lse[row] = lse2 * LN2;
+                *reinterpret_cast<uint32_t *>(dst) = pack_bf16x2(acc[g][0], acc[g][1]);
+            if (p.lse && lane == 0) p.lse[row] = lse2[g] * LN2;
         }
     }
+}
+
+// A tile's share of a unit's row sums from the logits alone, a row at a time, for a warp
+// whose keys' S is at `at`. Its calls' cost is in not being inlined: see far_scale.
+template <int D, int R>
+__device__ __noinline__ void sum_apart(Smem<D, R> &sm, uint32_t at, float k_scale, bool hidden,
+                                       int kpos, int hi, int causal, int wl, int key0, int g, int w,
+                                       int start) {
+    const int lane = threadIdx.x & 31, quarter = threadIdx.x >> 5 & 3;
+    float *fn = sm.fn[g][quarter], *fl = sm.fl[g][quarter];
+    if (start) {  // the unit's number and 1
+        if (quarter == 0 && lane < R) sm.fm[g][lane] = sm.mx[w][g][lane];
+        if (lane < R) fn[lane] = NOTHING, fl[lane] = 0.f;
+        if (quarter == 0 && lane == 0) sm.apart[g] = start;
+        __syncwarp();
+    }
+#pragma unroll 1
+    for (int r = 0; r < R; ++r) {
+        const float high = tmem_ld1(at + r), low = tmem_ld1(at + R + r);
+        float y = fmaf(low, 0.0625f, high) * (k_scale * sm.qf[w][r]);
+        if (key0 && kpos == 0) y += sm.rsink[w][r];
+        const int pos = sm.rpos[w][r];
+        if (hidden || kpos > (causal ? pos : hi) || (wl >= 0 && kpos < pos - wl)) y = -INFINITY;
+        const float n = fn[r], nn = fmaxf(n, redux_max(y));
+        const float sum = warp_sum(ex2(y - nn + BASE));
+        __syncwarp();
+        if (lane == 0) {
+            fl[r] = fmaf(fl[r], ex2(n - nn), sum);
+            fn[r] = nn;
+        }
+    }
+    __syncwarp();
+}
+
+// A row's denominator z and what it is in terms of, with such sums beside its groups'.
+template <int D, int R>
+__device__ __noinline__ float2 join_apart(const Smem<D, R> &sm, int w, int row, int groups,
+                                          int stamp) {
+    float nn = NOTHING, z = 0.f;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+        for (int s = 0; s < 8; ++s) {
+            const int g = s >> 2, q = s & 3;
+            if (!(groups >> g & 1)) continue;
+            const bool apart = sm.apart[g] == stamp;
+            const float n = apart ? sm.fm[g][row] : sm.mx[w][g][row];
+            const float fn = apart ? sm.fn[g][q][row] : NOTHING;
+            if (pass == 0) {
+                nn = fmaxf(nn, fmaxf(n, fn));
+            } else {
+                z = fmaf(ex2(n - nn), sm.lx[w][g][q][row], z);
+                if (apart) z = fmaf(ex2(fn - nn), sm.fl[g][q][row], z);
+            }
+        }
+    return make_float2(nn, z);
+}
+
+// Rows r0 .. r1 - 1 of the groups' O^T times half.
+template <int D, int R>
+__device__ __noinline__ void scale_rows(const Smem<D, R> &sm, uint32_t o_tmem, int w, int r0,
+                                        int r1, int groups) {
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r)
+#pragma unroll 1
+        for (int k = 0; k < 6; ++k) {
+            const uint32_t at = o_tmem + (uint32_t)(k / 3 * Cfg<D, R>::NO + k % 3 * R + r);
+            if (groups >> k / 3 & 1) tmem_st1(at, tmem_ld1(at) * sm.half[w][r]);
+        }
 }
 
 template <int D, int R>
@@ -604,6 +697,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         float l[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) l[r] = 0.f;
+        bool apart = false;  // the row sums have a maximum of their own
         const int step = solo ? 1 : 2, j0 = solo ? 0 : (g ^ t0) & 1;
 #pragma unroll 1
         for (int j = j0; j < n; j += step, ++done) {
@@ -614,6 +708,12 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             const float4 sc = sm.sc[ss][key >> p.page_shift];
             wait(sm.s_full[sb], t / C::SBUF);
             tc_fence_after();
+            if (__builtin_expect(sc.z < 0.f, 0)) {
+                sum_apart<D, R>(sm, tmem + (uint32_t)sb * C::N + lanes, sc.x, sc.y == -INFINITY,
+                                kpos, u.hi, p.plan.causal, p.plan.wl, p.sink_mode == 1, g, w,
+                                apart ? 0 : i + 1);
+                apart = true;
+            }
             float x[R];  // e of this key for every row
             {
                 constexpr int CH = R < 16 ? R : 16;
@@ -681,6 +781,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     }
                 }
             }
+            const float sum_scale = apart ? 0.f : sc.z;
             float top = -INFINITY;
 #pragma unroll
             for (int r = 0; r < R; r += 4) {
@@ -703,8 +804,10 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     sm.mx[w][g][key] = mn;
                 }
                 named_sync(bar_g, 128);
+                if (!apart) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) l[r] *= sm.alpha[g][r];
+                    for (int r = 0; r < R; ++r) l[r] *= sm.alpha[g][r];
+                }
                 if (j > j0) {
                     wait(sm.pv_done[g], done - 1);
                     tc_fence_after();
@@ -738,8 +841,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                         const int r = c + e + 2 * h;
                         const float a = ex2(x[r] - mm[2 * h] + BASE);
                         const float b = ex2(x[r + 1] - mm[2 * h + 1] + BASE);
-                        l[r] = fmaf(a, sc.z, l[r]);
-                        l[r + 1] = fmaf(b, sc.z, l[r + 1]);
+                        l[r] = fmaf(a, sum_scale, l[r]);
+                        l[r + 1] = fmaf(b, sum_scale, l[r + 1]);
                         e5m2_terms(pack_f16x2(a, b), y[h]);
                     }
 #pragma unroll
@@ -771,6 +874,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         meet();
         tc_fence_after();
         const bool has[2] = {!solo || g == 0, !solo || g == 1};
+        const bool scaled = u.far;
         const bool part = u.begin > 0 || u.end < u.ntiles;
         const size_t slot = (size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1);
         // a thread a row: what each group's O^T is multiplied by, and the denominator
@@ -779,24 +883,32 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             const float m0 = has[0] ? sm.mx[w][0][me] : NOTHING;
             const float m1 = has[1] ? sm.mx[w][1][me] : NOTHING, mm = fmaxf(m0, m1);
             const float w0 = has[0] ? ex2(m0 - mm) : 0.f, w1 = has[1] ? ex2(m1 - mm) : 0.f;
-            float z = 0.f;
+            float z = 0.f, nn = mm, half = 1.f;
+            if (__builtin_expect(scaled, 0)) {
+                const float2 nz = join_apart<D, R>(
+                    sm, w, me, (has[0] ? 1 : 0) | (has[1] ? 2 : 0), i + 1);
+                nn = nz.x, z = nz.y;
+                // 2^(m - n) is a value scale's size: in two steps, as it may leave fp32's range
+                sm.half[w][me] = half = ex2(0.5f * (mm - nn));
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (has[0]) z = fmaf(w0, sm.lx[w][0][q][me], z);
-                if (has[1]) z = fmaf(w1, sm.lx[w][1][q][me], z);
+                for (int q = 0; q < 4; ++q) {
+                    if (has[0]) z = fmaf(w0, sm.lx[w][0][q][me], z);
+                    if (has[1]) z = fmaf(w1, sm.lx[w][1][q][me], z);
+                }
             }
             float inv = z == 0.f ? 0.f : __fdividef(1.f, z);
             if (part) {
                 if (ok)
-                    part_sums(p.ws)[slot * R + me] = make_float2(mm, z * (1.f / (1 << (int)BASE)));
+                    part_sums(p.ws)[slot * R + me] = make_float2(nn, z * (1.f / (1 << (int)BASE)));
             } else {
-                float lse2 = z == 0.f ? -INFINITY : mm - BASE + __log2f(z);
+                float lse2 = z == 0.f ? -INFINITY : nn - BASE + __log2f(z);
                 if (p.sink_mode == 2) with_null_sink(sm.rsink[w][me], lse2, inv);
                 const long long row = sm.orow[w][me];
                 if (ok && p.lse && row >= 0) p.lse[row] = lse2 * LN2;
             }
-            sm.wt[w][0][me] = w0 * inv;
-            sm.wt[w][1][me] = w1 * inv;
+            sm.wt[w][0][me] = w0 * inv * half;
+            sm.wt[w][1][me] = w1 * inv * half;
         }
         meet();
         const bool writes = (D == 128 || lane < 16) && ok;  // 64 rows of O^T: 16 lanes of every 32
@@ -804,6 +916,8 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(R)) + slot * R * D + col;
         const int rows0 = solo ? 0 : g * (R / 2), rows1 = solo ? R : rows0 + R / 2;
         constexpr int STEP = R / 2 < 8 ? R / 2 : 8;  // rows at a time
+        if (__builtin_expect(scaled, 0))
+            scale_rows<D, R>(sm, o_tmem, w, rows0, rows1, (has[0] ? 1 : 0) | (has[1] ? 2 : 0));
         uint32_t nan_rows = 0;  // rows whose column is NaN
         if (u.nan_values && writes)
             each_partial_key<D>(p, u, u.lo, u.hi, [&](int k, const uint8_t *codes) {
@@ -829,24 +943,28 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 }
             }
             tc_wait_ld();
+            float acc[STEP];
 #pragma unroll
             for (int e = 0; e < STEP; ++e) {
-                const int r = r0 + e;
-                float acc = 0.f;
+                acc[e] = 0.f;
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
                     if (has[s])
-                        acc = fmaf(sm.wt[w][s][r],
-                                   fmaf(fmaf(__uint_as_float(v[3 * s + 2][e]), 0.125f,
-                                             __uint_as_float(v[3 * s + 1][e])),
-                                        0.125f, __uint_as_float(v[3 * s][e])),
-                                   acc);
+                        acc[e] = fmaf(sm.wt[w][s][r0 + e],
+                                      fmaf(fmaf(__uint_as_float(v[3 * s + 2][e]), 0.125f,
+                                                __uint_as_float(v[3 * s + 1][e])),
+                                           0.125f, __uint_as_float(v[3 * s][e])),
+                                      acc[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < STEP; ++e) {
+                const int r = r0 + e;
                 if (!writes) continue;
-                if (nan_rows >> r & 1) acc = NAN;
+                if (nan_rows >> r & 1) acc[e] = NAN;
                 if (part) {
-                    prow[(size_t)r * D] = acc;
+                    prow[(size_t)r * D] = acc[e];
                 } else if (sm.orow[w][r] >= 0) {
-                    p.o[sm.orow[w][r] * D + col] = __float2bfloat16_rn(acc);
+                    p.o[sm.orow[w][r] * D + col] = __float2bfloat16_rn(acc[e]);
                 }
             }
         }
@@ -922,6 +1040,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
         if (lane == 0) {
             mbar_init(smem_u32(&sm.both), 8);
             sm.abort = 0;
+            sm.apart[0] = sm.apart[1] = 0;
         }
         sm.units.init(2 + 1 + 8, lane);  // MMA issuers, queries, softmax
         fence_mbar_init();

@@ -54,14 +54,18 @@ join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    float z = ex2(sink - m);  // (0 without a sink)
+    auto weight = [&](int i) {
+        if (i >= parts) return 0.f;
+        const float2 s = sums[slot(i) * rows + r];
+        return s.y * ex2(s.x - m);
+    };
+    const float first = weight(lane);
+    float z = ex2(sink - m) + warp_sum(first);  // (0 without a sink)
+    for (int i0 = 32; i0 < parts; i0 += 32) z += warp_sum(weight(i0 + lane));
+    // the weights over their sum, so that values near fp32's largest do not overflow
+    const float inv = z == 0.f ? 0.f : 1.f / z;
     for (int i0 = 0; i0 < parts; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < parts) {
-            const float2 s = sums[slot(i0 + lane) * rows + r];
-            w = s.y * ex2(s.x - m);
-        }
-        z += warp_sum(w);
+        const float w = (i0 == 0 ? first : weight(i0 + lane)) * inv;
         const int cnt = min(32, parts - i0);
 #pragma unroll 4
         for (int i = 0; i < cnt; ++i) {
@@ -77,10 +81,9 @@ join_kernel(const uint8_t *ws, int rows, int pieces, int H, int G, const float *
             }
         }
     }
-    const float inv = z == 0.f ? 0.f : 1.f / z;
     uint32_t w2[E / 2];
 #pragma unroll
-    for (int e = 0; e < E; e += 2) w2[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < E; e += 2) w2[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
     __nv_bfloat16 *dst = o + out * D + lane * E;
     if (E == 4) *reinterpret_cast<uint2 *>(dst) = make_uint2(w2[0], w2[E / 2 - 1]);
     else *reinterpret_cast<uint32_t *>(dst) = w2[0];

@@ -44,6 +44,18 @@ template <int W> __device__ __forceinline__ uint32_t sw_offset(uint32_t r, uint3
     const uint32_t a = r * W + (u << 4);
     return W == 16 ? a : a ^ ((a >> 3) & (W - 16));
 }
+__device__ __forceinline__ float tmem_ld1(uint32_t a) {
+    uint32_t r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(a));
+    tc_wait_ld();
+    return __uint_as_float(r);
+}
+__device__ __forceinline__ void tmem_st1(uint32_t a, float v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(a),
+                 "r"(__float_as_uint(v))
+                 : "memory");
+    tc_wait_st();
+}
 constexpr int TIMED_OUT = 2;
 
 // mbar_wait in as few instructions as it takes: it stands at dozens of places of

@@ -61,6 +61,7 @@ template <int ROWS> struct Unit {
     int begin, end;        // the tiles of this piece, 0 .. ntiles
     int c0, parts;         // of a cut unit: its first piece, and how many
     int nan_values;        // set where a key that not every row sees has NaN value codes
+    int far;               // set where a page's value scale is far (far_scale)
 
     // The same piece in halves of tiles, less the halves that no row sees.
     __device__ __forceinline__ int sub_begin() const {
@@ -84,7 +85,7 @@ template <int ROWS> struct Unit {
         ihi = p.causal ? p0 : s.len - 1;
         t_first = lo / TILE;
         ntiles = hi < lo ? 1 : hi / TILE - t_first + 1;
-        nan_values = 0;
+        nan_values = far = 0;
     }
 };
 
@@ -364,6 +365,15 @@ __device__ __forceinline__ int page_of(const int32_t *table, int max_pages, int 
 // value scale (-inf hides the page's keys), 1 / the value scale, and whether
 // that is not 0: with a zero value scale the keys are weighed as with the least
 // scale and the values dropped.
+//
+// The log2 goes into the exponent of the probabilities, e = x + log2 s with x the logit, and
+// 1 / s takes it out of what they add to the row sum l. With scales from 2^-64 to 2^24 a
+// probability that is flushed to 0 (2^-126 with e's maximum at 1 or more) would have
+// added 2^-38 of the sum at most. For a scale beyond (far_scale) 1 / s may be infinite or 0
+// and such a loss the whole sum, so in a unit with such a page 2^(x - n) is summed apart,
+// with a maximum n of the logits alone: a second pass over S in small slow functions that
+// are not inlined (beside a hot loop such code costs more by being there than by running:
+// up to a tenth of a call that never takes it).
 __device__ __forceinline__ float4 page_scales(const float *k_scale, const float *v_scale, int pid,
                                               int Hkv, int h) {
     if (pid < 0) return make_float4(1.f, -INFINITY, 0.f, 0.f);
@@ -371,6 +381,11 @@ __device__ __forceinline__ float4 page_scales(const float *k_scale, const float 
     const float vs = __ldg(v_scale + at), e = vs > 0.f ? vs : LEAST_SCALE;
     return make_float4(__ldg(k_scale + at), __log2f(e), __fdividef(1.f, e), vs > 0.f ? 1.f : 0.f);
 }
+
+__device__ __forceinline__ bool far_scale(float s) {
+    return s > 0.f && !(s >= LEAST_SCALE && s <= 16777216.f);
+}
+__device__ __forceinline__ bool far_log2(float s) { return !(s >= -64.f && s <= 24.f); }
 
 // NaN value codes of keys that some rows of a unit see and others do not. The MMA
 // multiplies every key's values by every row's weight, and 0 * NaN is NaN, so such

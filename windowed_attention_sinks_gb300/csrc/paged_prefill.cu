@@ -191,7 +191,7 @@ __device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &c
     for (int i = 0; ok; ++i) {
         ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, &sm.abort));
         if (!ok) break;
-        const Unit<ROWS> &u = sm.units.u[i % UNITS];
+        Unit<ROWS> &u = sm.units.u[i % UNITS];
         if (u.begin == u.end) break;
         for (int c = u.begin; c < u.end && ok; c += chunk) {
             const int j = (u.t_first + c) * per_tile + lane;
@@ -199,6 +199,30 @@ __device__ void load_scales(const PrefillParams &p, Smem<D> &sm, const DevCtx &c
                                 ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift, u, j)
                                 : -1;
             const float4 s = page_scales(p.k_scale, p.v_scale, pid, p.plan.Hkv, u.h);
+            if (c == u.begin) {
+                // before the first, whether any of the unit's is far: eight pages a lane in flight
+                bool far = pid >= 0 && far_log2(s.y);
+                const int end = (u.t_first + u.end) * per_tile;
+#pragma unroll 1
+                for (int j1 = j + 32; j1 - lane < end; j1 += 256) {
+                    int id[8];
+                    float vs[8];
+#pragma unroll
+                    for (int a = 0; a < 8; ++a)
+                        id[a] = j1 + 32 * a < end
+                                    ? page_of(p.page_table, p.max_pages, p.num_pages, p.page_shift,
+                                              u, j1 + 32 * a)
+                                    : -1;
+#pragma unroll
+                    for (int a = 0; a < 8; ++a)
+                        vs[a] = id[a] < 0 ? 1.f
+                                          : __ldg(p.v_scale + (size_t)id[a] * p.plan.Hkv + u.h);
+#pragma unroll
+                    for (int a = 0; a < 8; ++a) far = far || far_scale(vs[a]);
+                }
+                far = __any_sync(0xffffffffu, far);
+                if (lane == 0 && far) u.far = 1;
+            }
             const int nt = min(chunk, u.end - c);
             for (int a = 0; a < nt; ++a, ++t) {
                 const int st = t % SRING, use = t / SRING;
@@ -255,10 +279,13 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
                 for (int i = 0; i < PER; ++i) {
                     const int r = r0 + i * (128 / UR), key = kpos0 + r;
                     uint4 x = src[i * 128];
-                    if (key < u.lo || key > u.hi || sm.sc[ss][r >> p.page_shift].w == 0.f)
+                    const bool hidden = key < u.lo || key > u.hi;
+                    if (hidden || sm.sc[ss][r >> p.page_shift].w == 0.f) {
                         src[i * 128] = make_uint4(0, 0, 0, 0);
-                    else if ((key < u.ilo || key > u.ihi) && without_nan(x))
-                        src[i * 128] = x, u.nan_values = 1;
+                    } else if ((key < u.ilo || key > u.ihi) && without_nan(x)) {
+                        src[i * 128] = x;
+                        u.nan_values = 1;
+                    }
                 }
             }
             if (use >= 1 && !bar_wait(smem_u32(&sm.v_empty[b]), (use - 1) & 1, ctx, abort)) return;
@@ -417,6 +444,107 @@ __device__ __forceinline__ int up_shift(uint32_t top) {
     return top ? max(-120, min(7 - ((int)(top >> 7) - 127), 120)) : 0;
 }
 
+// A unit whose row sums are taken apart (far_scale), for a thread's row r, from its Q on: m as
+// in the fast steps, but at its maximum in every step; l in terms of n, the maximum of the
+// logits alone. A key at a time, a column at a time: such calls are rare, and what the
+// fast loop carries along for them costs every call. Returns false if a wait gave up.
+template <int D>
+__device__ __noinline__ bool far_unit(const PrefillParams &p, Smem<D> &sm, const Unit<ROWS> &u,
+                                      uint32_t tmem, int half, int t, int done, int units, float qf,
+                                      float l, const DevCtx &ctx) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = half * 128 + (warp & 3) * 32 + lane;
+    const int tok = p.plan.token(u.row0 + r), head = u.h * p.plan.G + u.row0 + r - tok * p.plan.G;
+    const int pos = u.s.len - u.s.n + tok;
+    const int first = p.plan.wl < 0 ? 0 : max(0, pos - p.plan.wl);
+    const int last = p.plan.causal ? pos : u.s.len - 1;
+    const bool in = r < u.nrows;
+    const float sink = p.sinks && in ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, &sm.abort));
+    };
+    float m = NOTHING, n = NOTHING;
+    const int s0 = u.sub_begin(), s1 = u.sub_end();
+    int kpos0 = u.t_first * TILE + s0 * SUB;
+#pragma unroll 1
+    for (int k = s0; k < s1; ++k, ++done, t += !(k & 1), kpos0 += SUB) {
+        const int ss = t % SRING, b = done & 1;
+        const uint32_t s_tmem = tmem + (uint32_t)(b * SUB);
+        if (!wait(sm.s_full[half][b], done >> 1)) return false;
+        tc_fence_after();
+        // the logit of key e, and its page's log2 scale
+        auto logit = [&](int e, float &lv) {
+            const float4 s = sm.sc[ss][((k & 1) * SUB + e) >> p.page_shift];
+            const int key = kpos0 + e;
+            float y = tmem_ld1(s_tmem + (uint32_t)e) * (s.x * qf);
+            if (p.sink_mode == 1 && key == 0) y += sink;
+            lv = s.y;
+            return key < first || key > last || s.y == -INFINITY ? -INFINITY : y;
+        };
+        float top = m;
+#pragma unroll 1
+        for (int e = 0; e < SUB; ++e) {
+            float lv;
+            const float y = logit(e, lv), nn = fmaxf(n, y);
+            l = fmaf(l, ex2(n - nn), ex2(y - nn + BASE));
+            n = nn;
+            top = fmaxf(top, y + lv);
+        }
+        if (__any_sync(0xffffffffu, top > m) && k > s0) {
+            if (!wait(sm.pv_done[half][b ^ 1], (done - 1) >> 1)) return false;
+            tc_fence_after();
+            const float alpha = ex2(m - top);
+#pragma unroll 1
+            for (int c = 0; c < D; ++c)
+                tmem_st1(tmem + O_COL + (uint32_t)c, tmem_ld1(tmem + O_COL + (uint32_t)c) * alpha);
+        }
+        m = top;
+#pragma unroll 1
+        for (int e = 0; e < SUB; e += 2) {  // P over S's first columns, behind what is read
+            float lv0, lv1;
+            const float y0 = logit(e, lv0), y1 = logit(e + 1, lv1);
+            tmem_st1(s_tmem + (uint32_t)(e >> 1),
+                     __uint_as_float(pack_f16x2(ex2(y0 + lv0 - m + BASE), ex2(y1 + lv1 - m + BASE))));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(smem_u32(&sm.p_full[half][b]));
+            if ((k & 1) || k == s1 - 1) mbar_arrive(smem_u32(&sm.sc_empty[ss]));
+        }
+    }
+    if (!wait(sm.o_full[half], units)) return false;
+    tc_fence_after();
+    const bool part = u.begin > 0 || u.end < u.ntiles;
+    float inv = l == 0.f ? 0.f : __fdividef(1.f, l);
+    const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + r;
+    float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
+    const size_t orow = (size_t)(u.s.t0 + tok) * p.H + head;
+    if (in && part) {
+        part_sums(p.ws)[slot] = make_float2(n, l * (1.f / (1 << (int)BASE)));
+    } else if (in) {
+        float lse2 = l == 0.f ? -INFINITY : n - BASE + __log2f(l);
+        if (p.sink_mode == 2) with_null_sink(sink, lse2, inv);
+        if (p.lse) p.lse[orow] = lse2 * LN2;
+    }
+    // 2^(m - n) is a value scale's size: in two steps, as it may leave fp32's range
+    const float root = ex2(0.5f * (m - n));
+    inv *= root;
+#pragma unroll 1
+    for (int c = 0; c < D; ++c) {
+        float o = tmem_ld1(tmem + O_COL + (uint32_t)c) * root * inv;
+        if (u.nan_values && in)
+            each_partial_key<D>(p, u, first, last, [&](int, const uint8_t *codes) {
+                if ((__ldg(codes + c) & 0x7f) == 0x7f) o = NAN;
+            });
+        if (in && part) prow[c] = o;
+        else if (in) p.o[orow * D + c] = __float2bfloat16_rn(o);
+        __syncwarp();
+    }
+    tc_fence_before();
+    return true;
+}
+
 template <int D, int CW>  // CW: columns that share a page's scales (16 or 32)
 __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
                         const DevCtx &ctx) {
@@ -526,6 +654,19 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
             qf = p.scale_l2 * __uint_as_float((uint32_t)(127 - up_shift(mine)) << 23);
             fence_proxy_async_smem();
             mbar_arrive(smem_u32(&sm.q_full[half]));
+        }
+        // (the unit's scales are looked at before its first tile's are handed on)
+        if (!wait(sm.sc_full[t0 % SRING], t0 / SRING)) return;
+        if (__builtin_expect(u.far, 0)) {
+            if (!far_unit<D>(p, sm, u, tmem, half, t0, done, units, qf, l, ctx)) return;
+            done += u.sub_end() - u.sub_begin();
+            t0 += n;
+            ++units;
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sm.o_empty[half]));
+                sm.units.release(i);
+            }
+            continue;
         }
         float m = NOTHING;
         bool far = false;  // some row's m is so large that fp32 must subtract it exactly
@@ -736,7 +877,7 @@ __device__ void softmax(const PrefillParams &p, Smem<D> &sm, uint32_t tmem_base,
 template <int D, int CW>
 __global__ void __launch_bounds__(NTHREADS, 1)
 prefill_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
-               const PrefillParams p, const DevCtx ctx) {
+               const __grid_constant__ PrefillParams p, const __grid_constant__ DevCtx ctx) {
     extern __shared__ __align__(1024) uint8_t dsmem[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(dsmem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -3,7 +3,8 @@
 // Serves fp32 queries. Each lane holds d/32 neighbouring columns of the query and of the
 // accumulator; the row walks its visible positions lo .. hi with an online
 // softmax in the log2 domain. A key's logit is <q, codes> * k_scale * scale, a
-// value counts codes * v_scale. Bound by the one-key-at-a-time chain (a
+// value counts codes * v_scale, in terms of the power of two of the largest v_scale so
+// far (exact), so that sums of values near fp32's largest do not overflow. Bound by the one-key-at-a-time chain (a
 // reduction over the warp, an exponential) rather than by memory: it is the
 // exact fp32 form, the bf16 kernels are the fast ones. 32 requests of 301 .. 8192
 // positions, 32 heads on 8, d = 128: 9.4 ms against their 52 us.
@@ -55,6 +56,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
         acc[e] = 0.f;
     }
     float m = a.sink_mode == 2 ? sink : -INFINITY, l = a.sink_mode == 2 ? 1.f : 0.f;
+    float unit = 7.888609052210118e-31f, per_unit = 1.f / unit;  // 2^-100
     const int32_t *pages = a.page_table + (size_t)b * a.max_pages;
     bool bad = false;
     for (int j = lo; j <= hi; ++j) {
@@ -76,7 +78,15 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
         const float mn = fmaxf(m, x);
         const float alpha = m == -INFINITY ? 0.f : ex2(m - mn), p = ex2(x - mn);
         load_codes<E>(a.v_cache + at, kv);
-        const float pv = p * __ldg(a.v_scale + ph);
+        const float vs = __ldg(a.v_scale + ph);
+        if (vs >= 2.f * unit) {
+            const float larger = __uint_as_float(__float_as_uint(vs) & 0x7f800000u);
+            per_unit = 1.f / larger;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= unit * per_unit;
+            unit = larger;
+        }
+        const float pv = p * (vs * per_unit);
         l = l * alpha + p;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = acc[e] * alpha + pv * kv[e];
@@ -87,7 +97,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_simt_kernel(PagedArgs a, De
     const float inv = l == 0.f ? 0.f : 1.f / l;
     float *orow = static_cast<float *>(a.o) + (size_t)row * D + lane * E;
 #pragma unroll
-    for (int e = 0; e < E; ++e) orow[e] = acc[e] * inv;
+    for (int e = 0; e < E; ++e) orow[e] = acc[e] * inv * unit;
     if (a.lse && lane == 0) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
