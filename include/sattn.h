@@ -489,7 +489,7 @@ sattn_status sattn_paged_fp8_append(
  * page with a value scale above 2^24, or below 2^-64 but not 0, is computed by slower
  * code (2 to 4 times slower with a few rows, 7 with many). Codes of positions that a row does not
  * see may hold anything; a NaN code of one that it sees goes out as NaN (a
- * value's in its column, a key's or a query's in the whole row). Finite sinks
+ * value's in its column, also where its scale is 0; a key's or a query's in the whole row). Finite sinks
  * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits
  * down to 2^-10 of its largest element; a probability keeps 9 bits down to 2^-24 of the
  * largest (few rows) or 11 down to 2^-21, and below that is off by at most 2^-32 of it.

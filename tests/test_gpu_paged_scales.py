@@ -15,13 +15,15 @@ import windowed_attention_sinks_gb300 as sa
 
 from gpu_helpers import TOL_LSE
 from test_gpu_paged import DT, Batch, cuda, filled
+from test_gpu_paged_edges import seen
 
 pytestmark = pytest.mark.gpu
 
 LEAST, LARGEST = 2.0 ** -149, float(np.finfo(np.float32).max)
 
 
-def run(b, H, Hkv, d, vs, dtype="bf16", window=-1, causal=True, mode=0, equal=False):
+def run(b, H, Hkv, d, vs, dtype="bf16", window=-1, causal=True, mode=0, equal=False, nan=()):
+    """nan: (sequence, KV head, key, column) of NaN value codes."""
     rng = np.random.default_rng(b.T)
     kc, ks = filled(rng, b, Hkv, d)
     # values up to 1.875: with the largest scale they stay in fp32's range
@@ -39,11 +41,20 @@ def run(b, H, Hkv, d, vs, dtype="bf16", window=-1, causal=True, mode=0, equal=Fa
     ones = np.full_like(vc, 0x38)
     floor, _ = oracle.paged_attend(q, kc, ones, ks, np.where(vs == 0, 2.0 ** -64, vs), *where)
     floor *= 2.0 ** -32 * 1.875 * b.kv_lens.max()
-    o, lse = sa.paged_fp8_fwd(cuda(q, DT[dtype]), cuda(kc), cuda(vc), cuda(ks), cuda(vs),
+    held = vc.copy()
+    spoilt = np.zeros(ro.shape, bool)
+    masks = seen(b, window, causal)
+    for i, g, key, col in nan:
+        held[b.table[i, key // b.page], g, key % b.page, col] = 0x7F
+        rows = b.cu[i] + np.nonzero(masks[i][:, key])[0]
+        spoilt[rows, g * (H // Hkv):(g + 1) * (H // Hkv), col] = True
+    o, lse = sa.paged_fp8_fwd(cuda(q, DT[dtype]), cuda(kc), cuda(held), cuda(ks), cuda(vs),
                               *b.tensors(), max_q_len=int(b.n.max()), window_left=window,
                               causal=causal, sinks=cuda(sinks) if mode else None, sink_mode=mode)
     sa.check_device()
     got, gl = o.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.array_equal(np.isnan(got), spoilt)
+    got[spoilt] = ro[spoilt]
     assert np.isfinite(got).all()
     part = 2.0 ** -9 + 2.0 ** -12 if dtype == "bf16" else 1e-4
     tol = part * mean + floor + (2.0 ** -8 * np.abs(ro) + 2.0 ** -134 if dtype == "bf16" else 2.0 ** -149)
@@ -116,3 +127,18 @@ def test_one_far_page_in_a_long_sequence(keys, n):
         run(b, 8, 2, 128, vs)
         vs[b.table[0, at - 1 if at else 1]] = 0.0
         run(b, 8, 2, 128, vs, equal=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 4, 70])
+@pytest.mark.parametrize("window", [-1, 150])
+def test_nan_values_under_a_zero_scale(window, n, dtype):
+    """NaN times 0 is NaN: to the rows that see it, whatever the page's scale."""
+    b = batch(n)
+    vs = np.full((b.pages, 2), 0.25)
+    nan = []
+    for i, length in enumerate(b.kv_lens):
+        for g, key, col in ((0, int(length) // 2, 7), (1, int(length) - 1, 100)):
+            vs[b.table[i, key // 64], g] = 0.0
+            nan.append((i, g, key, col))
+    run(b, 8, 2, 128, vs, dtype, window=window, nan=nan)

@@ -606,6 +606,18 @@ __device__ __noinline__ void sum_apart(Smem<D, R> &sm, uint32_t at, float k_scal
     __syncwarp();
 }
 
+// Notes NaN codes of a value that is cleared for its scale of 0: NaN times 0 is NaN.
+template <int D, int R> __device__ __noinline__ void note_nan(const uint4 *v, bool zero,
+                                                                    Unit<R> &u) {
+    bool nan = false;
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+        uint4 y = v[c];
+        nan = without_nan(y) || nan;
+    }
+    if (nan && zero) u.nan_values = u.nan_zero = 1;
+}
+
 // A row's denominator z and what it is in terms of, with such sums beside its groups'.
 template <int D, int R>
 __device__ __noinline__ float2 join_apart(const Smem<D, R> &sm, int w, int row, int groups,
@@ -767,6 +779,10 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                 const bool clear = kpos < u.lo || kpos > u.hi || sc.w == 0.f;
                 const int st = t % C::STAGES;
                 wait(sm.v_full[st], t / C::STAGES);
+                const bool zero = sc.w == 0.f && kpos >= u.lo && kpos <= u.hi;
+                if (__builtin_expect(__any_sync(0xffffffffu, zero), 0))
+                    note_nan<D>(reinterpret_cast<const uint4 *>(sm.v[st] + key * D), zero,
+                                sm.units.u[i % UNITS]);
                 if (some || clear) {
                     uint4 *v = reinterpret_cast<uint4 *>(sm.v[st] + key * D);
 #pragma unroll 1

@@ -61,6 +61,7 @@ template <int ROWS> struct Unit {
     int begin, end;        // the tiles of this piece, 0 .. ntiles
     int c0, parts;         // of a cut unit: its first piece, and how many
     int nan_values;        // set where a key that not every row sees has NaN value codes
+    int nan_zero;          // and where one of a page with a value scale of 0 has
     int far;               // set where a page's value scale is far (far_scale)
 
     // The same piece in halves of tiles, less the halves that no row sees.
@@ -85,7 +86,7 @@ template <int ROWS> struct Unit {
         ihi = p.causal ? p0 : s.len - 1;
         t_first = lo / TILE;
         ntiles = hi < lo ? 1 : hi / TILE - t_first + 1;
-        nan_values = far = 0;
+        nan_values = nan_zero = far = 0;
     }
 };
 
@@ -391,7 +392,8 @@ __device__ __forceinline__ bool far_log2(float s) { return !(s >= -64.f && s <= 
 // multiplies every key's values by every row's weight, and 0 * NaN is NaN, so such
 // codes are taken out of the tile (without_nan) and put back at the unit's end into
 // the rows that see them: each_partial_key calls at(key, codes) for the piece's
-// keys from `lo` to `hi` that not every row sees.
+// keys from `lo` to `hi` that not every row sees. Pages with a value scale of 0 are
+// cleared altogether: where one has a NaN, for their other keys too.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t x) {  // 0xff for each NaN code
     return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
@@ -407,12 +409,15 @@ __device__ __forceinline__ void each_partial_key(const Params &p, const Unit<ROW
     const int z = min(hi, (u.t_first + u.end) * TILE - 1);
 #pragma unroll 1
     for (int k = a; k <= z; ++k) {
-        if (k >= u.ilo && k <= u.ihi) k = u.ihi + 1;
-        if (k > z) break;
+        const bool all_see = k >= u.ilo && k <= u.ihi;
+        if (all_see && !u.nan_zero) {
+            k = u.ihi;
+            continue;
+        }
         const int pid = __ldg(p.page_table + (size_t)u.b * p.max_pages + (k >> p.page_shift));
         if (pid < 0 || pid >= p.num_pages) continue;
         const size_t ph = (size_t)pid * p.plan.Hkv + u.h;
-        if (!(__ldg(p.v_scale + ph) > 0.f)) continue;  // its values are dropped
+        if (all_see && __ldg(p.v_scale + ph) > 0.f) continue;
         at(k, p.v_cache + (ph * p.page + (k & (p.page - 1))) * D);
     }
 }

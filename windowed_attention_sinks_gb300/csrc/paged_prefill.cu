@@ -281,6 +281,8 @@ __device__ void widen(const PrefillParams &p, Smem<D> &sm, const DevCtx &ctx) {
                     uint4 x = src[i * 128];
                     const bool hidden = key < u.lo || key > u.hi;
                     if (hidden || sm.sc[ss][r >> p.page_shift].w == 0.f) {
+                        // (NaN times a scale of 0 is NaN)
+                        if (!hidden && without_nan(x)) u.nan_values = u.nan_zero = 1;
                         src[i * 128] = make_uint4(0, 0, 0, 0);
                     } else if ((key < u.ilo || key > u.ihi) && without_nan(x)) {
                         src[i * 128] = x;
