@@ -7,9 +7,8 @@
  * host memory. Its state: on the host, a per-device cache of attributes and
  * device addresses, the tensor-map encoder entry point, the debug flag and
  * wait limit, and a launch counter; on each device, module-scope arrays built
- * into the library: the error word, a ring of 256 item-claim counters, the sets
- * of join counters of sattn_paged_fp8_fwd (8.3 MB) and the scratch array of
- * sattn_sparse_fwd_static_scratch.
+ * into the library: the error word, a ring of 256 item-claim counters and the
+ * scratch array of sattn_sparse_fwd_static_scratch.
  *
  * Claim counters: each call of sattn_window_fwd, sattn_block_sparse_fwd and
  * sattn_block_sparse_chunks_fwd takes the next counter of the ring (zeroed
@@ -18,11 +17,6 @@
  * counter and must not run at the same time on the GPU (different streams,
  * or CUDA graphs that captured them replayed concurrently); keep fewer than
  * 256 of these calls in flight at once. Calls on one stream never overlap.
- * Join counters: the same holds for calls of sattn_paged_fp8_fwd that have a
- * workspace and few rows (max_q_len * H / Hkv <= 32), with 256 sets for calls
- * made eagerly and 8192 others for calls made while a stream captures: a replay
- * never meets an eager call, and two captured calls share a set only if 8192
- * were captured from the one to the other.
  *
  * Execution: every compute call is asynchronous on `cuda_stream` (a
  * cudaStream_t; NULL selects the per-thread default stream, never the legacy
@@ -500,9 +494,7 @@ sattn_status sattn_paged_fp8_append(
  *   workspace: NULL or a caller-owned device buffer of at least
  *     sattn_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned; it receives
  *     partial results and is free again when the call's work has run. Calls
- *     that may overlap on the GPU need one each.
- * After a timeout call sattn_check_device before the next of these calls: it
- * also clears what the abandoned call left in its join counters.
+ *     that may overlap on the GPU need one each, and share nothing else.
  */
 size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
 sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,

@@ -21,7 +21,6 @@ __device__ unsigned g_error_word;
 // on its own 128-byte line.
 constexpr unsigned kClaimStride = 32;
 __device__ unsigned g_claims[kClaimCounters * kClaimStride];
-__device__ unsigned g_joins[kJoinSets * kJoinPieces];
 
 namespace {
 
@@ -83,8 +82,6 @@ const DevInfo *device_info(cudaError_t *e) {
         d.err = static_cast<unsigned *>(p);
         if ((*e = cudaGetSymbolAddress(&p, g_claims)) != cudaSuccess) return nullptr;
         d.claims = static_cast<unsigned *>(p);
-        if ((*e = cudaGetSymbolAddress(&p, g_joins)) != cudaSuccess) return nullptr;
-        d.joins = static_cast<unsigned *>(p);
         if ((*e = cudaMemset(d.err, 0, sizeof(unsigned))) != cudaSuccess) return nullptr;
         if ((*e = cudaDeviceSynchronize()) != cudaSuccess) return nullptr;
         g_dev[dev] = d;
@@ -102,16 +99,6 @@ unsigned *launch_claim_counter(const DevInfo &dev, cudaStream_t s, cudaError_t *
     unsigned *c = dev.claims + (size_t)(next.fetch_add(1) % kClaimCounters) * kClaimStride;
     *e = cudaMemsetAsync(c, 0, sizeof(*c), s);
     return *e == cudaSuccess ? c : nullptr;
-}
-
-unsigned *next_join_counters(const DevInfo &dev, cudaStream_t s) {
-    static std::atomic<unsigned> next{0}, captured{0};
-    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
-    const bool eager =
-        cudaStreamIsCapturing(s, &st) == cudaSuccess && st == cudaStreamCaptureStatusNone;
-    const unsigned set = eager ? next.fetch_add(1) % kClaimCounters
-                               : kClaimCounters + captured.fetch_add(1) % kCapturedJoinSets;
-    return dev.joins + (size_t)set * kJoinPieces;
 }
 
 cudaError_t ensure_smem_attr(const void *kernel, size_t bytes, const DevInfo &dev) {
@@ -236,9 +223,6 @@ sattn_status sattn_check_device(void *cuda_stream) {
     if (word) {
         unsigned zero = 0;
         if (cudaMemcpy(dev->err, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess)
-            return SATTN_ERR_CUDA;
-        if ((word & DEVERR_TIMEOUT) &&
-            cudaMemset(dev->joins, 0, sizeof(unsigned) * kJoinSets * kJoinPieces) != cudaSuccess)
             return SATTN_ERR_CUDA;
     }
     if (word & DEVERR_TIMEOUT) return SATTN_ERR_TIMEOUT;

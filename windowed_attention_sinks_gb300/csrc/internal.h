@@ -18,7 +18,6 @@ struct DevInfo {
     int cc_major = 0, cc_minor = 0;
     unsigned *err = nullptr;                 // device address of the error word
     unsigned *claims = nullptr;              // device address of the claim-counter ring
-    unsigned *joins = nullptr;               // and of the join-counter ring
 };
 
 // Per-device facts, initialised once per device (thread-safe).
@@ -36,18 +35,6 @@ struct DevCtx make_ctx(const DevInfo &dev);
 // issued.
 constexpr unsigned kClaimCounters = 256;
 unsigned *launch_claim_counter(const DevInfo &dev, cudaStream_t s, cudaError_t *e);
-
-// The kJoinPieces join counters of one launch of the paged decode kernel, built into the
-// library: the next of a ring of kClaimCounters such sets, or for a launch that is
-// being captured of a ring of kCapturedJoinSets, so that no later call meets a
-// replayed one. They are zero between launches: a kernel's arrivals wrap them to
-// zero again (sattn_check_device zeroes them after a timeout, when a kernel may
-// have left without arriving). Two launches with the same set must not overlap on
-// the GPU; the header states this limit.
-constexpr unsigned kJoinPieces = 256;
-constexpr unsigned kCapturedJoinSets = 8192;
-constexpr unsigned kJoinSets = kClaimCounters + kCapturedJoinSets;
-unsigned *next_join_counters(const DevInfo &dev, cudaStream_t s);
 
 // cudaFuncSetAttribute(kernel, MaxDynamicSharedMemorySize, bytes) once per
 // (kernel, device, size), thread-safe.

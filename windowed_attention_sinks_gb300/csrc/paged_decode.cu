@@ -91,7 +91,6 @@ struct DecodeParams {
     __nv_bfloat16 *o;
     float *lse;
     uint8_t *ws;
-    unsigned *join;  // arrivals at each cut unit, by its first piece
 };
 
 template <int D, int R> struct Cfg {
@@ -994,10 +993,11 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
         if (part) {  // the last of the unit's pieces to get here joins them
             __threadfence();
             meet();
-            if (me == 0)
-                sm.last[solo ? g : 2] =
-                    atomicInc(p.join + u.c0, (unsigned)u.parts - 1) == (unsigned)u.parts - 1 &&
-                    !*abort;
+            if (me == 0) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+                sm.last[solo ? g : 2] = atomicAdd(join_counters(p.ws) + u.c0, 1u) ==
+                                            (unsigned)u.parts - 1 && !*abort;
+            }
             meet();
             // (a group alone, or group 0 for both, has asked)
             if (ok && sm.last[solo ? g : 2]) {
@@ -1085,11 +1085,24 @@ decode_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CU
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
+    if (threadIdx.x == 0) {
+        // (no CTA ends before the counters are zero: they are the next call's then)
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, C::COLS);
     }
+}
+
+// Zeroes a call's join counters, which lie in its workspace so that no call meets another
+// one's: the decode kernel, its programmatic dependent, starts beside it and waits for it
+// before a piece arrives. (One request of 1000 positions: 11.4 us; with a memset in front
+// 14.5, with counters built into the library, which calls had to share, 10.7.)
+__global__ void __launch_bounds__(MAX_PIECES) zero_counters(uint8_t *ws) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    join_counters(ws)[threadIdx.x] = 0;
 }
 
 template <int D, int R>
@@ -1107,13 +1120,25 @@ cudaError_t launch(const PagedArgs &a, const DevInfo &dev, cudaStream_t s) {
     DecodeParams p{plan_args(a, split, Cfg<D, R>::EXTRA), static_cast<const __nv_bfloat16 *>(a.q), a.q_stride,
                    a.v_cache, a.k_scale, a.v_scale, a.page_table, a.H, a.num_pages, a.page, page_shift(a.page),
                    a.max_pages, a.num_pages * a.Hkv * a.page, a.scale * LOG2E, a.sinks, a.sink_mode,
-                   static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace),
-                   split ? next_join_counters(dev, s) : nullptr};
+                   static_cast<__nv_bfloat16 *>(a.o), a.lse, static_cast<uint8_t *>(a.workspace)};
     if (verbose())
         fprintf(stderr, "sattn: paged decode_kernel<%d, %d> grid=%d smem=%zu split=%d\n", D, R, grid,
                 smem, (int)split);
-    decode_kernel<D, R><<<grid, NTHREADS, smem, s>>>(tk, tv, p, make_ctx(dev));
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    if (split) {
+        zero_counters<<<1, MAX_PIECES, 0, s>>>(p.ws);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, decode_kernel<D, R>, tk, tv, p, make_ctx(dev));
 }
 
 }  // namespace

@@ -476,7 +476,8 @@ struct PlanNote {
     int cont, through, t0, h, row0, nrows, pad0, pad1;
 };
 
-// Workspace: PlanNote [pieces], (m, z) [pieces][2][ROWS], rows [pieces][2][ROWS][D] (fp32).
+// Workspace: PlanNote [pieces], or the join counters of the decode kernel [pieces];
+// (m, z) [pieces][2][ROWS], rows [pieces][2][ROWS][D] (fp32).
 // Part 0 of a piece is its first unit if that began earlier, part 1 its last
 // unit if that begins here and goes on. Of a part's row: its maximum m, its
 // denominator z = sum 2^(x - m) (as one number, m + log2 z, large logits would
@@ -488,6 +489,9 @@ __host__ __device__ constexpr size_t plan_rows_offset(int rows) {
 }
 __host__ __device__ constexpr size_t plan_workspace(int rows, int d) {
     return plan_rows_offset(rows) + (size_t)MAX_PIECES * 2 * rows * d * 4;
+}
+__device__ __forceinline__ unsigned *join_counters(uint8_t *ws) {
+    return reinterpret_cast<unsigned *>(ws);
 }
 __device__ __forceinline__ float2 *part_sums(uint8_t *ws) {
     return reinterpret_cast<float2 *>(ws + plan_sums_offset());
