@@ -127,3 +127,29 @@ def test_two_graphs_and_eager_calls_at_once():
     torch.cuda.synchronize()
     sa.check_device()
     assert [x.item() for x in bad] == [0, 0, 0]
+
+
+def test_outputs_that_a_call_makes_are_its_streams():
+    """Not in memory that the current stream has freed (and may still use there)."""
+    torch.manual_seed(0)
+    job = Job([(500, 3), (90, 2)], 7)
+    T, H, d = job.q.shape
+    k = torch.randn(T, 2, d, device="cuda").bfloat16()
+    cs = torch.randn(1024, d, device="cuda")
+    side = torch.cuda.Stream()
+
+    def calls(stream):
+        q = sa.paged_fp8_append(k, k, *job.cache, cos_sin=cs, q=job.q, stream=stream)
+        o, lse = sa.paged_fp8_fwd(job.q, *job.cache, max_q_len=3, stream=stream)
+        return q, o, lse
+
+    want = [t.clone() for t in calls(None)]
+    torch.cuda.synchronize()
+    freed = [torch.empty_like(t) for _ in range(8) for t in want]
+    addresses = {t.data_ptr() for t in freed}
+    del freed
+    got = calls(side)
+    side.synchronize()
+    sa.check_device(side)
+    assert all(t.data_ptr() not in addresses for t in got)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -424,13 +424,22 @@ def _token_rows(t, name, T, heads, d, dtype, dev):
     return st[0] if T > 1 else heads * d
 
 
-def _out(t, name, shape, dtype, device):
-    """Checks an output tensor, or makes one. (On a torch.device: from its index torch takes
-    some microseconds longer.)"""
+def _empty(shape, dtype, device, stream):
+    """A tensor that a call on `stream` writes. The allocator must know that stream: it hands out
+    memory that work queued on another one may still read. (On a torch.device: from its index
+    torch takes some microseconds longer.)"""
     import torch
 
-    if t is None:
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, name, shape, dtype, device, stream):
+    """Checks an output tensor, or makes one."""
+    if t is None:
+        return _empty(shape, dtype, device, stream)
     if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s %s on %s" % (name, dtype, shape, device))
     return t
@@ -445,7 +454,8 @@ def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     projection are); k_cache, v_cache uint8 [pages, Hkv, page, d]; k_scale,
     v_scale fp32 [pages, Hkv]; page_table int32 [B, max_pages]; cu_seqlens int32
     [B + 1]; kv_lens int32 [B], the lengths with the new tokens; cos_sin fp32
-    [positions, rd]. With q [T, H, d] returns the rotated queries, else None."""
+    [positions, rd]. With q [T, H, d] returns the rotated queries, else None; without
+    q_out they are taken from torch's allocator for the stream that the call runs on."""
     import torch
 
     dev, pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale,
@@ -465,7 +475,7 @@ def paged_fp8_append(k, v, k_cache, v_cache, k_scale, v_scale, page_table, cu_se
     if q is not None:
         H = q.shape[1]
         qs = _token_rows(q, "q", T, H, d, dt, dev)
-        q_out = _out(q_out, "q_out", (T, H, d), dt, k_cache.device)
+        q_out = _out(q_out, "q_out", (T, H, d), dt, k_cache.device, stream)
         qp, qo = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
@@ -491,8 +501,8 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
     """Attention of q [T, H, d] (the last tokens of each sequence) over the
     pages of an e4m3 cache (sattn_paged_fp8_fwd); the cache's tensors as for
     paged_fp8_append. Returns (o, lse). Rows behind the last sequence are not
-    written. Without a workspace one is taken from torch's allocator for the
-    stream that the call runs on."""
+    written. Without a workspace, o or lse they are taken from torch's allocator for
+    the stream that the call runs on."""
     import torch
 
     dev, pages, Hkv, page, d, B, width = _paged_cache(k_cache, v_cache, k_scale, v_scale,
@@ -511,20 +521,17 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
     nb, ws = 0, None
     with _OnDevice(dev, stream) as s:
         device = k_cache.device
-        o = _out(o, "o", (T, H, d), dt, device)
-        lse = _out(lse, "lse", (T, H), torch.float32, device)
+        o = _out(o, "o", (T, H, d), dt, device, stream)
+        lse = _out(lse, "lse", (T, H), torch.float32, device, stream)
         if workspace is not None:
             if workspace.get_device() != dev or not workspace.is_contiguous():
                 raise ValueError("workspace must be contiguous on cuda:%d" % dev)
             nb, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
         elif dt is torch.bfloat16:
             nb = L.sattn_paged_fp8_workspace_bytes(n, H, Hkv, d)
-            if nb and stream is None:
-                workspace = torch.empty(nb, dtype=torch.uint8, device=device)
-            elif nb:  # the allocator must know the stream that uses it
-                with torch.cuda.stream(stream):
-                    workspace = torch.empty(nb, dtype=torch.uint8, device=device)
-            ws = workspace.data_ptr() if nb else None
+            if nb:
+                workspace = _empty(nb, torch.uint8, device, stream)
+                ws = workspace.data_ptr()
         rc = L.sattn_paged_fp8_fwd(
             q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
             v_scale.data_ptr(), page_table.data_ptr(), cu_seqlens.data_ptr(), kv_lens.data_ptr(),
