@@ -137,6 +137,18 @@ def _stream(stream):
     return s.cuda_stream
 
 
+def _empty(shape, dtype, device, stream):
+    """A tensor that a call on `stream` writes. The allocator must know that stream: it hands out
+    memory that work queued on another one may still read. (On a torch.device: from its index
+    torch takes some microseconds longer.)"""
+    import torch
+
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _need(t, name, dtype=None, device=None):
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
@@ -161,9 +173,9 @@ def window_fwd(q, k, v, cu_seqlens, max_seqlen, window_left, window_right, causa
     if sinks is not None:
         _need(sinks, "sinks", torch.float32, q.device)
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+        lse = _empty((T, H), torch.float32, q.device, stream)
     scale = float(d ** -0.5 if scale is None else scale)
     code = lib().sattn_window_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens),
                                   cu_seqlens.numel() - 1, T, int(max_seqlen), H, Hkv, d,
@@ -192,9 +204,9 @@ def sparse_fwd(q, kv_cache, topk_idxs, sinks=None, sink_mode=SINK_NONE, scale=No
     if sinks is not None:
         _need(sinks, "sinks", torch.float32, q.device)
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, M, H), dtype=torch.float32, device=q.device)
+        lse = _empty((B, M, H), torch.float32, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = float(d ** -0.5 if scale is None else scale)
     code = lib().sattn_sparse_fwd(_ptr(q), _ptr(kv_cache), _ptr(topk_idxs), _ptr(sinks),
@@ -213,9 +225,9 @@ def quantize_kv_fp8(kv, rd, stream=None):
     d = kv.shape[-1]
     lead = tuple(kv.shape[:-1])
     rows = kv.numel() // d if d else 0
-    nope = torch.empty(lead + (d - rd,), dtype=torch.uint8, device=kv.device)
-    rope = torch.empty(lead + (rd,), dtype=torch.bfloat16, device=kv.device)
-    scale = torch.empty(lead, dtype=torch.float32, device=kv.device)
+    nope = _empty(lead + (d - rd,), torch.uint8, kv.device, stream)
+    rope = _empty(lead + (rd,), torch.bfloat16, kv.device, stream)
+    scale = _empty(lead, torch.float32, kv.device, stream)
     _check("sattn_quantize_kv_fp8",
            lib().sattn_quantize_kv_fp8(_ptr(kv), _ptr(nope), _ptr(rope), _ptr(scale), rows, d,
                                        int(rd), _dtype_code(kv), _stream(stream)))
@@ -242,9 +254,9 @@ def sparse_fp8_fwd(q, kv_nope, kv_rope, kv_scale, topk_idxs, sinks=None, sink_mo
     if sinks is not None:
         _need(sinks, "sinks", torch.float32, q.device)
     if o is None:
-        o = torch.empty_like(q)
+        o = _empty(q.shape, q.dtype, q.device, stream)
     if lse is None:
-        lse = torch.empty((B, M, H), dtype=torch.float32, device=q.device)
+        lse = _empty((B, M, H), torch.float32, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     scale = float(d ** -0.5 if scale is None else scale)
     code = lib().sattn_sparse_fp8_fwd(_ptr(q), _ptr(kv_nope), _ptr(kv_rope), _ptr(kv_scale),
@@ -263,9 +275,9 @@ def merge_lse(o_parts, lse_parts, H, sinks=None, out_dtype=None, o=None, lse=Non
     _need(o_parts, "o_parts", torch.float32)
     _need(lse_parts, "lse_parts", torch.float32, o_parts.device)
     if o is None:
-        o = torch.empty((R, d), dtype=out_dtype or torch.float32, device=o_parts.device)
+        o = _empty((R, d), out_dtype or torch.float32, o_parts.device, stream)
     if lse is None:
-        lse = torch.empty((R,), dtype=torch.float32, device=o_parts.device)
+        lse = _empty((R,), torch.float32, o_parts.device, stream)
     code = lib().sattn_merge_lse(_ptr(o_parts), _ptr(lse_parts), C, R, d, H, _ptr(sinks), _ptr(o),
                                  _ptr(lse), _dtype_code(o), _stream(stream))
     _check("sattn_merge_lse", code)
@@ -283,9 +295,9 @@ def block_sparse_fwd(q, k, v, block_mask, q_pos0, kv_begin, kv_end, causal=True,
         _need(t, n, q.dtype, q.device)
     _need(block_mask, "block_mask", torch.uint8, q.device)
     if o_part is None:
-        o_part = torch.empty((M, H, d), dtype=torch.float32, device=q.device)
+        o_part = _empty((M, H, d), torch.float32, q.device, stream)
     if lse_part is None:
-        lse_part = torch.empty((M, H), dtype=torch.float32, device=q.device)
+        lse_part = _empty((M, H), torch.float32, q.device, stream)
     scale = float(d ** -0.5 if scale is None else scale)
     code = lib().sattn_block_sparse_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(block_mask), M, Nctx, H,
                                         Hkv, d, int(q_pos0), int(kv_begin), int(kv_end),
@@ -309,9 +321,9 @@ def block_sparse_chunks_fwd(q, k, v, block_mask, q_pos0, kv_begin, kv_end, chunk
     _need(block_mask, "block_mask", torch.uint8, q.device)
     C = -(-(int(kv_end) - int(kv_begin)) // int(chunk)) if chunk > 0 else 0
     if o_parts is None:
-        o_parts = torch.empty((C, M, H, d), dtype=torch.float32, device=q.device)
+        o_parts = _empty((C, M, H, d), torch.float32, q.device, stream)
     if lse_parts is None:
-        lse_parts = torch.empty((C, M, H), dtype=torch.float32, device=q.device)
+        lse_parts = _empty((C, M, H), torch.float32, q.device, stream)
     scale = float(d ** -0.5 if scale is None else scale)
     code = lib().sattn_block_sparse_chunks_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(block_mask), M,
                                                Nctx, H, Hkv, d, int(q_pos0), int(kv_begin),
@@ -330,7 +342,7 @@ def build_topk_idxs(start_pos, M, K, win, ratio, out=None, stream=None):
     _need(start_pos, "start_pos", torch.int32)
     B = start_pos.numel()
     if out is None:
-        out = torch.empty((B, M, K), dtype=torch.int32, device=start_pos.device)
+        out = _empty((B, M, K), torch.int32, start_pos.device, stream)
     _need(out, "out", torch.int32, start_pos.device)
     _check("sattn_build_topk_idxs",
            lib().sattn_build_topk_idxs(_ptr(out), _ptr(start_pos), B, int(M), int(K), int(win),
@@ -422,18 +434,6 @@ def _token_rows(t, name, T, heads, d, dtype, dev):
     if st[2] != 1 or (st[1] != d and heads > 1):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     return st[0] if T > 1 else heads * d
-
-
-def _empty(shape, dtype, device, stream):
-    """A tensor that a call on `stream` writes. The allocator must know that stream: it hands out
-    memory that work queued on another one may still read. (On a torch.device: from its index
-    torch takes some microseconds longer.)"""
-    import torch
-
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _out(t, name, shape, dtype, device, stream):
@@ -563,7 +563,7 @@ def compress_kv(kv, score, ape, ratio, overlap, out=None, out_dtype=None, stream
         raise ValueError("score must match kv and ape must be [ratio, coff*d]")
     nwin = S // int(ratio)
     if out is None:
-        out = torch.empty((B, nwin, d), dtype=out_dtype or kv.dtype, device=kv.device)
+        out = _empty((B, nwin, d), out_dtype or kv.dtype, kv.device, stream)
     if out.dim() != 3 or tuple(out.shape) != (B, nwin, d) or out.stride(2) != 1 or \
             (nwin > 1 and out.stride(1) != d) or out.device != kv.device:
         raise ValueError("out must be [B, S // ratio, d] with contiguous rows")
@@ -587,9 +587,9 @@ def xattn_partial_stats(q, k, q_pos0, kv_begin, kv_end, causal, scale=None, m=No
     _need(q, "q", torch.bfloat16, q.device)
     _need(k, "k", torch.bfloat16, q.device)
     if m is None:
-        m = torch.empty((M, H), dtype=torch.float32, device=q.device)
+        m = _empty((M, H), torch.float32, q.device, stream)
     if l is None:
-        l = torch.empty((M, H), dtype=torch.float32, device=q.device)
+        l = _empty((M, H), torch.float32, q.device, stream)
     scale = float(d ** -0.5 if scale is None else scale)
     _check("sattn_xattn_partial_stats",
            lib().sattn_xattn_partial_stats(_ptr(q), _ptr(k), M, Nctx, H, Hkv, d, int(q_pos0),
@@ -607,9 +607,9 @@ def xattn_merge_stats(m_parts, l_parts, m=None, l=None, stream=None):
     C = m_parts.shape[0]
     R = m_parts[0].numel() if C else 0
     if m is None:
-        m = torch.empty(m_parts.shape[1:], dtype=torch.float32, device=m_parts.device)
+        m = _empty(m_parts.shape[1:], torch.float32, m_parts.device, stream)
     if l is None:
-        l = torch.empty(m_parts.shape[1:], dtype=torch.float32, device=m_parts.device)
+        l = _empty(m_parts.shape[1:], torch.float32, m_parts.device, stream)
     _check("sattn_xattn_merge_stats",
            lib().sattn_xattn_merge_stats(_ptr(m_parts), _ptr(l_parts), C, R, _ptr(m), _ptr(l),
                                          _stream(stream)))
@@ -629,8 +629,9 @@ def xattn_block_sum(q, k, m, l, q_pos0, kv_begin, kv_end, causal, scale=None, bl
     _need(m, "m", torch.float32, q.device)
     _need(l, "l", torch.float32, q.device)
     if block_sum is None:
-        block_sum = torch.zeros((H, -(-M // BLOCK), -(-Nctx // BLOCK)), dtype=torch.float32,
-                                device=q.device)
+        with torch.cuda.stream(stream):  # (None: the current one)
+            block_sum = torch.zeros((H, -(-M // BLOCK), -(-Nctx // BLOCK)), dtype=torch.float32,
+                                    device=q.device)
     _need(block_sum, "block_sum", torch.float32, q.device)
     scale = float(d ** -0.5 if scale is None else scale)
     _check("sattn_xattn_block_sum",
@@ -648,7 +649,7 @@ def xattn_find_blocks(block_sum, threshold, mask=None, stream=None):
     _need(block_sum, "block_sum", torch.float32)
     H, QB, KB = block_sum.shape
     if mask is None:
-        mask = torch.empty((H, QB, KB), dtype=torch.uint8, device=block_sum.device)
+        mask = _empty((H, QB, KB), torch.uint8, block_sum.device, stream)
     _check("sattn_xattn_find_blocks",
            lib().sattn_xattn_find_blocks(_ptr(block_sum), H, QB, KB, float(threshold), _ptr(mask),
                                          _stream(stream)))
@@ -674,16 +675,16 @@ def xattn_select_blocks(q, k, q_pos0, causal, threshold, scale=None, chunk=4096,
     _need(k, "k", torch.bfloat16, q.device)
     shape = (H, -(-M // BLOCK), -(-Nctx // BLOCK))
     if block_sum is None:
-        block_sum = torch.empty(shape, dtype=torch.float32, device=q.device)
+        block_sum = _empty(shape, torch.float32, q.device, stream)
     if mask is None:
-        mask = torch.empty(shape, dtype=torch.uint8, device=q.device)
+        mask = _empty(shape, torch.uint8, q.device, stream)
     _need(block_sum, "block_sum", torch.float32, q.device)
     _need(mask, "mask", torch.uint8, q.device)
     if tuple(block_sum.shape) != shape or tuple(mask.shape) != shape:
         raise ValueError("block_sum and mask must have shape %s" % (shape,))
     nb = xattn_select_workspace_bytes(M, H, Nctx, chunk)
     if workspace is None:
-        workspace = torch.empty(max(nb, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(nb, 16), torch.uint8, q.device, stream)
     _need(workspace, "workspace", None, q.device)
     scale = float(d ** -0.5 if scale is None else scale)
     _check("sattn_xattn_select_blocks",
