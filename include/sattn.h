@@ -490,7 +490,8 @@ sattn_status sattn_paged_fp8_append(
  * What counts here is the probability times its page's value scale, 0 as 2^-64. The denominator and
  * lse take the unrounded ones.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the
- *     kernel; any value gives the same results.
+ *     kernel (and the workspace's size); any value gives right results, in the
+ *     precision of its kernel. Too large a one costs up to twice the time.
  *   workspace: NULL or a caller-owned device buffer of at least
  *     sattn_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned; it receives
  *     partial results and is free again when the call's work has run. Calls

@@ -1,6 +1,7 @@
 """Paged FP8 calls on several streams: calls far apart in issue order, and a timeout that
 is taken note of on one stream while a call runs on another. Every call has its own
-workspace (filled with ones before: the call depends on nothing in it)."""
+workspace (filled with ones before: the call depends on nothing in it). And what the
+binding chooses by itself: memory for outputs, the kernel."""
 import numpy as np
 import pytest
 import torch
@@ -153,3 +154,15 @@ def test_outputs_that_a_call_makes_are_its_streams():
     sa.check_device(side)
     assert all(t.data_ptr() not in addresses for t in got)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_without_a_hint_the_kernel_is_chosen_by_the_mean_length(n):
+    """The kernels round differently: the same bits are the same kernel's."""
+    job = Job([(int(x), n) for x in np.linspace(500, 5000, 20)], 8)
+    o, lse = job.want()
+    other = sa.paged_fp8_fwd(job.q, *job.cache, max_q_len=100 if n < 40 else 1)[0]
+    got = sa.paged_fp8_fwd(job.q, *job.cache)
+    sa.check_device()
+    assert torch.equal(got[0], o) and torch.equal(got[1], lse)
+    assert not torch.equal(other, o)

@@ -500,7 +500,9 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
                   scale=None, o=None, lse=None, workspace=None, stream=None):
     """Attention of q [T, H, d] (the last tokens of each sequence) over the
     pages of an e4m3 cache (sattn_paged_fp8_fwd); the cache's tensors as for
-    paged_fp8_append. Returns (o, lse). Rows behind the last sequence are not
+    paged_fp8_append. Returns (o, lse). max_q_len, the most queries that a sequence
+    has (their mean if not given), chooses the kernel: a wrong one costs speed, up to
+    twice the time, and o is rounded otherwise. Rows behind the last sequence are not
     written. Without a workspace, o or lse they are taken from torch's allocator for
     the stream that the call runs on."""
     import torch
@@ -516,7 +518,8 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
                 or not sinks.is_contiguous():
             raise ValueError("sinks must be a contiguous float32 [H] on cuda:%d" % dev)
         sp = sinks.data_ptr()
-    n = T if max_q_len is None else int(max_q_len)
+    # the mean: single tokens must not count as one sequence of T
+    n = (-(-T // B) if B else 0) if max_q_len is None else int(max_q_len)
     L = lib()
     nb, ws = 0, None
     with _OnDevice(dev, stream) as s:
