@@ -142,3 +142,30 @@ def test_nan_values_under_a_zero_scale(window, n, dtype):
             vs[b.table[i, key // 64], g] = 0.0
             nan.append((i, g, key, col))
     run(b, 8, 2, 128, vs, dtype, window=window, nan=nan)
+
+
+@pytest.mark.parametrize("n", [1, 4, 40])
+def test_nan_values_under_a_zero_scale_of_a_long_sequence(n):
+    """Found again at the unit's end among 200000 keys of one piece, in ordinary and in far units:
+    within the limit of a wait."""
+    keys, d = 200000, 64
+    b = Batch([(keys, n)], 128)
+    kc = np.zeros((b.pages, 1, 128, d), np.uint8)
+    vc = np.full(kc.shape, 0x38, np.uint8)  # 1.0
+    q = torch.zeros(b.T, 2, d, dtype=torch.bfloat16, device="cuda")
+    for far in (0.25, 2.0 ** 40):
+        vs = np.full((b.pages, 1), 0.25, np.float32)
+        vs[b.table[0, 700]] = far
+        vs[b.table[0, 90]] = 0.0
+        spoilt = vc.copy()
+        spoilt[b.table[0, 90], 0, 17, 5] = 0x7F
+        o, lse = sa.paged_fp8_fwd(q, cuda(kc), cuda(spoilt), cuda(np.ones_like(vs)), cuda(vs),
+                                  *b.tensors(), max_q_len=n,
+                                  workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+        sa.check_device()
+        o = o.float().cpu().numpy()
+        assert np.isnan(o[..., 5]).all() and np.isnan(o).sum() == o[..., 5].size
+        L = keys + 1 + np.arange(n)  # keys that a row sees, all alike
+        want = (0.25 * (L - 256) + 128 * far) / L
+        assert np.abs(o[..., 0] / want[:, None] - 1).max() <= 2.0 ** -7
+        assert np.abs(lse.cpu().numpy() - np.log(L)[:, None]).max() <= TOL_LSE

@@ -415,9 +415,12 @@ __device__ __forceinline__ void each_partial_key(const Params &p, const Unit<ROW
             continue;
         }
         const int pid = __ldg(p.page_table + (size_t)u.b * p.max_pages + (k >> p.page_shift));
-        if (pid < 0 || pid >= p.num_pages) continue;
         const size_t ph = (size_t)pid * p.plan.Hkv + u.h;
-        if (all_see && __ldg(p.v_scale + ph) > 0.f) continue;
+        if (pid < 0 || pid >= p.num_pages || (all_see && __ldg(p.v_scale + ph) > 0.f)) {
+            k |= p.page - 1;  // nothing there for such keys of the page: to the last of them
+            if (all_see) k = min(k, u.ihi);
+            continue;
+        }
         at(k, p.v_cache + (ph * p.page + (k & (p.page - 1))) * D);
     }
 }

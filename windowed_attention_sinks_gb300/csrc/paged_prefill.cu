@@ -532,13 +532,22 @@ __device__ __noinline__ bool far_unit(const PrefillParams &p, Smem<D> &sm, const
     // 2^(m - n) is a value scale's size: in two steps, as it may leave fp32's range
     const float root = ex2(0.5f * (m - n));
     inv *= root;
+    uint32_t nan[D / 32] = {};  // columns that are NaN
+    if ((u.nan_values || u.nan_zero) && in)
+        each_partial_key<D>(p, u, first, last, [&](int, const uint8_t *codes) {
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w)
+#pragma unroll 1
+                for (int e = 0; e < 32; ++e)
+                    nan[w] |= (__ldg(codes + 32 * w + e) & 0x7f) == 0x7f ? 1u << e : 0u;
+        });
 #pragma unroll 1
     for (int c = 0; c < D; ++c) {
         float o = tmem_ld1(tmem + O_COL + (uint32_t)c) * root * inv;
-        if (u.nan_values && in)
-            each_partial_key<D>(p, u, first, last, [&](int, const uint8_t *codes) {
-                if ((__ldg(codes + c) & 0x7f) == 0x7f) o = NAN;
-            });
+        uint32_t word = nan[0];
+#pragma unroll
+        for (int w = 1; w < D / 32; ++w) word = c >> 5 == w ? nan[w] : word;
+        if (word >> (c & 31) & 1) o = NAN;
         if (in && part) prow[c] = o;
         else if (in) p.o[orow * D + c] = __float2bfloat16_rn(o);
         __syncwarp();
