@@ -481,7 +481,7 @@ sattn_status sattn_paged_fp8_append(
  * sequence, are not written. Keys in an invalid page contribute nothing.
  * Scales may be any finite values >= 0; with bf16 queries a sequence and head that sees a
  * page with a value scale above 2^24, or below 2^-64 but not 0, is computed by slower
- * code (2 to 4 times slower with a few rows, 7 with many). Codes of positions that a row does not
+ * code (2 to 4 times slower with a few rows, 6 to 9 with many). Codes of positions that a row does not
  * see may hold anything; a NaN code of one that it sees goes out as NaN (a
  * value's in its column, also where its scale is 0; a key's or a query's in the whole row). Finite sinks
  * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits

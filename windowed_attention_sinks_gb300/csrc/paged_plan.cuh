@@ -372,9 +372,9 @@ __device__ __forceinline__ int page_of(const int32_t *table, int max_pages, int 
 // probability that is flushed to 0 (2^-126 with e's maximum at 1 or more) would have
 // added 2^-38 of the sum at most. For a scale beyond (far_scale) 1 / s may be infinite or 0
 // and such a loss the whole sum, so in a unit with such a page 2^(x - n) is summed apart,
-// with a maximum n of the logits alone: a second pass over S in small slow functions that
-// are not inlined (beside a hot loop such code costs more by being there than by running:
-// up to a tenth of a call that never takes it).
+// with a maximum n of the logits alone: a second pass over S in small slow code, kept out
+// of the hot loops (inside one it costs more by being there than by running: up to a tenth
+// of a call that never takes it).
 __device__ __forceinline__ float4 page_scales(const float *k_scale, const float *v_scale, int pid,
                                               int Hkv, int h) {
     if (pid < 0) return make_float4(1.f, -INFINITY, 0.f, 0.f);

@@ -449,9 +449,11 @@ __device__ __forceinline__ int up_shift(uint32_t top) {
 // A unit whose row sums are taken apart (far_scale), for a thread's row r, from its Q on: m as
 // in the fast steps, but at its maximum in every step; l in terms of n, the maximum of the
 // logits alone. A key at a time, a column at a time: such calls are rare, and what the
-// fast loop carries along for them costs every call. Returns false if a wait gave up.
+// fast loop carries along for them costs every call. (Beside that loop a unit's far form costs
+// little: chunk below 847 us, as a function that is called 862.) Returns false if a
+// wait gave up.
 template <int D>
-__device__ __noinline__ bool far_unit(const PrefillParams &p, Smem<D> &sm, const Unit<ROWS> &u,
+__device__ __forceinline__ bool far_unit(const PrefillParams &p, Smem<D> &sm, const Unit<ROWS> &u,
                                       uint32_t tmem, int half, int t, int done, int units, float qf,
                                       float l, const DevCtx &ctx) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
