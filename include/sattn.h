@@ -481,21 +481,22 @@ sattn_status sattn_paged_fp8_append(
  * sequence, are not written. Keys in an invalid page contribute nothing.
  * Scales may be any finite values >= 0; with bf16 queries a sequence and head that sees a
  * page with a value scale above 2^24, or below 2^-64 but not 0, is computed by slower
- * code (2 to 4 times slower with a few rows, 6 to 9 with many). Codes of positions that a row does not
- * see may hold anything; a NaN code of one that it sees goes out as NaN (a
- * value's in its column, also where its scale is 0; a key's or a query's in the whole row). Finite sinks
- * beyond 2e38 in size count as that. bf16 queries: a query row keeps 8 significant bits
- * down to 2^-10 of its largest element; a probability keeps 9 bits down to 2^-24 of the
- * largest (few rows) or 11 down to 2^-21, and below that is off by at most 2^-32 of it.
- * What counts here is the probability times its page's value scale, 0 as 2^-64. The denominator and
- * lse take the unrounded ones.
+ * code (2 to 4 times slower with a few rows, 6 to 9 with many). Codes of positions that a
+ * row does not see may hold anything; a NaN code of one that it sees goes out as NaN (a
+ * value's in its column, also where its scale is 0; a key's or a query's in the whole
+ * row). Finite sinks beyond 2e38 in size count as that.
+ * bf16 queries: a query row keeps 8 significant bits down to 2^-10 of its largest element;
+ * a probability keeps 11 bits down to 2^-21 of the largest (9 with 17 to 32 rows a KV head),
+ * and below that is off by at most 2^-32 of it. What counts here is the probability times
+ * its page's value scale, 0 as 2^-64. The denominator and lse take the unrounded ones.
+ * fp32 queries: everything in fp32, by a kernel that takes 100 times as long and more.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the
  *     kernel (and the workspace's size); any value gives right results, in the
- *     precision of its kernel. Too large a one costs up to twice the time.
+ *     precision of its kernel. A wrong one costs up to twice the time.
  *   workspace: NULL or a caller-owned device buffer of at least
  *     sattn_paged_fp8_workspace_bytes(...) bytes, 256-byte aligned; it receives
  *     partial results and is free again when the call's work has run. Calls
- *     that may overlap on the GPU need one each, and share nothing else.
+ *     that may overlap on the GPU need one each; they share the error word alone.
  */
 size_t sattn_paged_fp8_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
 sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t *k_cache,

@@ -172,9 +172,9 @@ bool valid_paged(int Hkv, int d, int num_pages, int page, int max_pages) {
 // Whether a sequence's rows of a KV head are few enough for the decode kernel, which has
 // 32 at most by one read of the keys. Decode / prefill kernel, us, 32 heads on 8, d = 128:
 //   rows                        8          16          32          40
-//   32 x 1000..16000 keys   98.7 / 209  105 / 209   146 / 215   256 / 218
-//    4 x 8000               26.7 / 43    29 / 43     40 / 43     45 / 44
-//    1 x 4000               20.5 / 24    27 / 25     35 / 25     27 / 25
+//   32 x 1000..16000 keys   94.3 / 222  100 / 223   123 / 228   220 / 229
+//    4 x 8000               21.6 / 41    24 / 41     32 / 42     40 / 42
+//    1 x 4000               16.4 / 23    22 / 23     29 / 23     24 / 23
 bool paged_few_rows(int max_q_len, int G) { return (int64_t)max_q_len * G <= 32; }
 // Rows of `heads` x d elements, `stride` apart, each on a 16-byte boundary.
 bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {

@@ -30,7 +30,9 @@
 //
 // Bound by bytes in flight. 16 prompts of 33 .. 1777 tokens, bf16, 32 heads on 8, d = 128,
 // pages of 64: 54 us for 273 MB, 0.77 of the copy rate; four of 7001 .. 8192, fp32, 16
-// heads on 4, d = 64, pages of 16: 71 us, 0.68; 4 single tokens 3.9 us, latency.
+// heads on 4, d = 64, pages of 16: 71 us, 0.68; 4 single tokens 3.9 us, latency. A group
+// loads its unit's rows, waits for them and stores once, with nothing of the next unit in
+// flight; three blocks an SM leave 80 registers a thread, of which 28 to 80 bytes spill.
 #include "internal.h"
 #include "paged.cuh"
 

@@ -9,7 +9,7 @@
 //    shared memory. Both products are taken with the keys (then the columns of V) as the
 //    128 rows of the MMA and the query rows as its N columns:
 //      S^T [128 keys, 2R]   = K [128, D]   Q^T,
-//      O^T [D, 3R]         += V^T [D, 128] P^T   (V read column-major).
+//      O^T [D, 4R]         += V^T [D, 128] P^T   (V read column-major).
 //  * An e4m3 operand has 4 significant bits, so Q is split: x = hi +
 //    lo / 16 with hi = e4m3(x) and lo = e4m3(16 (x - hi)), side by side as 2R
 //    columns, joined again in fp32. hi + lo / 16 has 8 significant bits, a
@@ -18,15 +18,15 @@
 //    in [128, 256): bf16 queries go in exactly down to 2^-14 of the row's largest.
 //  * P needs range above all: a long tail of keys far below the largest weighs as much
 //    as that, and what P V loses of each, the row sum counts. So P goes in as
-//    e5m2 (kind::f8f6f4 takes its operands' types apart), in 3R columns: P = 2^(10 + e - m)
-//    <= 2^15, with e the exponent below, is rounded to 9 significant bits in f16
-//    and cut into t0 + t1 / 8 + t2 / 64. An e5m2 is an f16's upper byte, so each term is
-//    the next byte of what the ones before leave, exactly: 3 + 3 + 3 bits and no
-//    conversion. P keeps its 9 bits down to 2^-14, which is 2^-24 of the largest weight, and
-//    below that is off by at most 2^-23, 2^-33 of it. (Two e4m3 terms as for Q lose
-//    all below 2^-18 of the largest: 32768 equal keys 13 nats below another one's gave
-//    half of their share. A second pair of them for the rest of small P is right too, but its
-//    conversions take drafted tokens from 102 to 200 us; these terms to 104.)
+//    e5m2 (kind::f8f6f4 takes its operands' types apart), in 4R columns: P = 2^(10 + e - m)
+//    <= 2^15, with e the exponent below, in f16 and cut into t0 + t1 / 8 + t2 / 64 + t3 / 512.
+//    An e5m2 is an f16's upper byte, so each term is the next byte of what the ones
+//    before leave: 3 + 3 + 3 + 2 bits, all that f16 has, and no conversion. With 32 rows three
+//    terms, of P rounded to 9 bits. Those bits hold down to 2^-14, which is 2^-24 of the
+//    largest weight; below that P is off by at most 2^-23, 2^-33 of it. (Two e4m3 terms as for
+//    Q lose all below 2^-18 of the largest: 32768 equal keys 13 nats below another one's
+//    gave half of their share. A second pair of them for the rest of small P is right too,
+//    but its conversions take drafted tokens from 102 to 200 us; these terms to 104.)
 //  The extra columns are free: the MMA is a small part of the time a tile takes to arrive.
 //  * A thread holds one key, so the page's scales are scalars to it: the key's multiplies S, the
 //    value's goes into the exponent, e = scale log2(e) s + log2(v_scale), and
@@ -50,11 +50,13 @@
 //               groups take such units in turn.
 //
 // Measured (32 heads on 8, d = 128, replayed graphs): 64 requests of 8001 .. 32768
-// positions 410 us, the copy rate; 32 of 301 .. 8192 52 us, 0.75 of it; one of 1000 10.5 us,
-// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 101 us, 0.70 (at a unit's
+// positions 411 us, the copy rate; 32 of 301 .. 8192 53.6 us, 0.73 of it; one of 1000 11.4 us,
+// all latency; 3 to 5 drafted tokens for 32 of 1000 .. 16000 109 us, 0.65 (at a unit's
 // end the ring of tiles is full and HBM waits). 128 requests with a window of 127 (64
-// heads on 8, d = 64): 34 us, latency of units of two tiles. One thread for both
-// products took 486 and 64 us on the first two.
+// heads on 8, d = 64): 36.8 us, latency of units of two tiles. Of these, sums apart for far
+// value scales cost 2 us of the last and 3 of the drafted tokens, and the counters' launch 1
+// of each. (When first built, one thread for both products took 486 and 64 us on the
+// first two, 410 and 57 with two.)
 #include <limits.h>
 #include <math.h>
 #include <stdio.h>
@@ -95,9 +97,9 @@ struct DecodeParams {
 
 template <int D, int R> struct Cfg {
     static constexpr int N = 2 * R;  // columns of S: Q's hi and lo
-    // Columns of O: P's three terms (a multiple of 16; the last 8 of 32 are not read), and
-    // the bytes of a key's row of P
-    static constexpr int NO = R == 8 ? 32 : 3 * R, PW = 4 * R;
+    // P's terms: a fourth costs the 32 rows of drafted tokens 11 us of 110, fewer rows nothing.
+    // Columns of O, and the bytes of a key's row of P (a power of two for the swizzle).
+    static constexpr int TERMS = R <= 16 ? 4 : 3, NO = TERMS * R, PW = 4 * R;
     static constexpr uint32_t TILE_BYTES = TILE * D;
     // what shared memory holds beside Q and P: 160 KB of tiles, 192 KB with fewer rows
     static constexpr int STAGES = (R <= 16 ? 6 : 5) * (128 / D);
@@ -574,7 +576,7 @@ __device__ void join_parts(const DecodeParams &p, int c0, int parts, const long 
 }
 
 // A tile's share of a unit's row sums from the logits alone, a row at a time, for a warp
-// whose keys' S is at `at`. Its calls' cost is in not being inlined: see far_scale.
+// whose keys' S is at `at`. (Not inlined: see page_scales.)
 template <int D, int R>
 __device__ __noinline__ void sum_apart(Smem<D, R> &sm, uint32_t at, float k_scale, bool hidden,
                                        int kpos, int hi, int causal, int wl, int key0, int g, int w,
@@ -648,9 +650,9 @@ __device__ __noinline__ void scale_rows(const Smem<D, R> &sm, uint32_t o_tmem, i
 #pragma unroll 1
     for (int r = r0; r < r1; ++r)
 #pragma unroll 1
-        for (int k = 0; k < 6; ++k) {
-            const uint32_t at = o_tmem + (uint32_t)(k / 3 * Cfg<D, R>::NO + k % 3 * R + r);
-            if (groups >> k / 3 & 1) tmem_st1(at, tmem_ld1(at) * sm.half[w][r]);
+        for (int k = 0; k < 2 * Cfg<D, R>::TERMS; ++k) {  // (the groups' columns lie side by side)
+            const uint32_t at = o_tmem + (uint32_t)(k * R + r);
+            if (groups >> k / Cfg<D, R>::TERMS & 1) tmem_st1(at, tmem_ld1(at) * sm.half[w][r]);
         }
 }
 
@@ -827,7 +829,7 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                     wait(sm.pv_done[g], done - 1);
                     tc_fence_after();
 #pragma unroll 1
-                    for (int c = 0; c < 3 * R; c += 8) {
+                    for (int c = 0; c < C::NO; c += 8) {
                         uint32_t v[8];
                         tmem_ld8(o_tmem + (uint32_t)(g * C::NO + c), v);
                         tc_wait_ld();
@@ -845,12 +847,12 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
 #pragma unroll
             for (int c = 0; c < R; c += 16) {
                 constexpr int CH = R < 16 ? R : 16;
-                uint32_t t[3][4];
+                uint32_t t[C::TERMS][4];
 #pragma unroll
                 for (int e = 0; e < CH; e += 4) {
                     const float4 m = m4[(c + e) / 4];
                     const float mm[4] = {m.x, m.y, m.z, m.w};
-                    uint32_t y[2][3];
+                    uint32_t y[2][C::TERMS];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int r = c + e + 2 * h;
@@ -861,17 +863,17 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
                         e5m2_terms(pack_f16x2(a, b), y[h]);
                     }
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)  // the upper bytes
+                    for (int k = 0; k < C::TERMS; ++k)  // the upper bytes
                         t[k][e >> 2] = __byte_perm(y[0][k], y[1][k], 0x7531);
                 }
                 if constexpr (R == 8) {
                     *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::PW>(key, 0)) =
                         make_uint4(t[0][0], t[0][1], t[1][0], t[1][1]);
                     *reinterpret_cast<uint4 *>(sm.p[g] + sw_offset<C::PW>(key, 1)) =
-                        make_uint4(t[2][0], t[2][1], 0, 0);
+                        make_uint4(t[2][0], t[2][1], t[3][0], t[3][1]);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
+                    for (int k = 0; k < C::TERMS; ++k)
                         *reinterpret_cast<uint4 *>(
                             sm.p[g] + sw_offset<C::PW>(key, (k * R + c) / 16)) =
                             make_uint4(t[k][0], t[k][1], t[k][2], t[k][3]);
@@ -946,15 +948,16 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             });
 #pragma unroll 1
         for (int r0 = rows0; r0 < rows1; r0 += STEP) {
-            uint32_t v[6][STEP];  // the terms of group 0, of group 1
+            constexpr int M = C::TERMS;
+            uint32_t v[2 * M][STEP];  // the terms of group 0, of group 1
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 if (!has[s]) continue;
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
+                for (int k = 0; k < M; ++k) {
                     const uint32_t at = o_tmem + (uint32_t)(s * C::NO + k * R + r0);
-                    if constexpr (STEP == 8) tmem_ld8(at, v[3 * s + k]);
-                    else tmem_ld4(at, v[3 * s + k]);
+                    if constexpr (STEP == 8) tmem_ld8(at, v[M * s + k]);
+                    else tmem_ld4(at, v[M * s + k]);
                 }
             }
             tc_wait_ld();
@@ -963,13 +966,14 @@ __device__ void softmax(const DecodeParams &p, Smem<D, R> &sm, uint32_t tmem, co
             for (int e = 0; e < STEP; ++e) {
                 acc[e] = 0.f;
 #pragma unroll
-                for (int s = 0; s < 2; ++s)
-                    if (has[s])
-                        acc[e] = fmaf(sm.wt[w][s][r0 + e],
-                                      fmaf(fmaf(__uint_as_float(v[3 * s + 2][e]), 0.125f,
-                                                __uint_as_float(v[3 * s + 1][e])),
-                                           0.125f, __uint_as_float(v[3 * s][e])),
-                                      acc[e]);
+                for (int s = 0; s < 2; ++s) {
+                    if (!has[s]) continue;
+                    float o = __uint_as_float(v[M * s + M - 1][e]);
+#pragma unroll
+                    for (int k = M - 2; k >= 0; --k)
+                        o = fmaf(o, 0.125f, __uint_as_float(v[M * s + k][e]));
+                    acc[e] = fmaf(sm.wt[w][s][r0 + e], o, acc[e]);
+                }
             }
 #pragma unroll
             for (int e = 0; e < STEP; ++e) {

@@ -108,15 +108,19 @@ template <int F> __device__ __forceinline__ uint32_t times_difference(uint32_t a
                               __float2half2_rn((float)F));
     return *reinterpret_cast<const uint32_t *>(&d);
 }
-// Two f16 in [0, 2^15], rounded to 9 significant bits (to 2^-22 below 2^-14), as three
-// e5m2 each: t[0] + t[1] / 8 + t[2] / 64, in the upper bytes of t's halves. Each cut leaves
-// what an f16 holds exactly. A NaN is not kept.
-__device__ __forceinline__ void e5m2_terms(uint32_t x, uint32_t (&t)[3]) {
-    const uint32_t y = (x + 0x00020002u) & 0xfffcfffcu;
-    t[0] = y & 0xff00ff00u;
-    const uint32_t z = times_difference<8>(y, t[0]);
-    t[1] = z & 0xff00ff00u;
-    t[2] = times_difference<8>(z, t[1]);
+// Two f16 in [0, 2^15] as N e5m2 each, t[0] + t[1] / 8 + t[2] / 64 (+ t[3] / 512), in the upper
+// bytes of t's halves. A term is the upper byte of what the ones before leave (times 8
+// each time), which an f16 holds: four have 3 + 3 + 3 + 2 bits, all of them; for three the
+// f16 are first rounded to 9 bits (to 2^-22 below 2^-14). A NaN is not kept.
+template <int N> __device__ __forceinline__ void e5m2_terms(uint32_t x, uint32_t (&t)[N]) {
+    static_assert(N == 3 || N == 4, "9 or 11 bits");
+    if constexpr (N == 3) x = (x + 0x00020002u) & 0xfffcfffcu;
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k) {
+        t[k] = x & 0xff00ff00u;
+        x = times_difference<8>(x, t[k]);
+    }
+    t[N - 1] = x;
 }
 
 // x = keep ? x : -inf. Volatile so that it stays behind the branch it is written in:

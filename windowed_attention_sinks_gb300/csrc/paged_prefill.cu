@@ -39,9 +39,11 @@
 //
 // Bound: the chain of a step, S ready -> 64 exponentials a thread -> P V -> the S
 // that takes P's columns, about 1900 cycles where the products need 1300. For 2048 tokens
-// behind 30720 cached ones (32 heads on 8, d = 128) 839 us, 1.27 PFLOP/s; the
-// products alone would take 549. Prompts of 61 .. 1500 tokens 211 us: a unit costs about
-// 15000 cycles by itself (Q, the first maximum, O). Measured against it:
+// behind 30720 cached ones (32 heads on 8, d = 128) 844 us, 1.26 PFLOP/s; the
+// products alone would take 549. Prompts of 61 .. 1500 tokens 220 us: a unit costs about
+// 15000 cycles by itself (Q, the first maximum, O); 8 us of them are the look at each unit's
+// value scales. 88 to 108 bytes a thread are spilled, in which role the compiler does not say.
+// Measured against 839 us for the first, before the units of far scales:
 //   one thread for both products of a half            939 us (an MMA takes its
 //     thread 65 to 80 cycles to issue, a commit or a wait that is met 100 to 200)
 //   the same, every index kept up instead of computed   875 us
