@@ -116,6 +116,15 @@ def test_scales_of_every_size_at_once(window, causal, mode, n, d, page):
     run(b, 6, 2, d, vs, window=window, causal=causal, mode=mode)
 
 
+@pytest.mark.parametrize("n,H", [(1, 64), (4, 16), (5, 12)])
+def test_scales_of_every_size_with_many_rows_of_few_tokens(n, H):
+    rng = np.random.default_rng(H)
+    b = batch(n)
+    vs = 2.0 ** rng.uniform(-149, 126, (b.pages, 2))
+    run(b, H, 2, 128, vs, mode=2)
+    run(b, H, 2, 128, np.where(rng.random(vs.shape) < 0.1, vs, 2.0 ** -5), window=300)
+
+
 @pytest.mark.parametrize("n", [1, 4, 70])
 @pytest.mark.parametrize("keys", [20000, 9000])
 def test_one_far_page_in_a_long_sequence(keys, n):

@@ -368,9 +368,10 @@ __device__ __forceinline__ int page_of(const int32_t *table, int max_pages, int 
 // scale and the values dropped.
 //
 // The log2 goes into the exponent of the probabilities, e = x + log2 s with x the logit, and
-// 1 / s takes it out of what they add to the row sum l. With scales from 2^-64 to 2^24 a
-// probability that is flushed to 0 (2^-126 with e's maximum at 1 or more) would have
-// added 2^-38 of the sum at most. For a scale beyond (far_scale) 1 / s may be infinite or 0
+// 1 / s takes it out of what they add to the row sum l. With scales from 2^-64 to 2^24 what
+// is flushed to 0, a probability or the sum at a move of m by more than 2^126, would have
+// added 2^-33 of the sum a key at most (2^-126 of e's maximum, 2^88 between the scales, 2^5
+// that m lags behind). For a scale beyond (far_scale) 1 / s may be infinite or 0
 // and such a loss the whole sum, so in a unit with such a page 2^(x - n) is summed apart,
 // with a maximum n of the logits alone: a second pass over S in small slow code, kept out
 // of the hot loops (inside one it costs more by being there than by running: up to a tenth
