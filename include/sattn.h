@@ -510,6 +510,125 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
                                  void *workspace, size_t workspace_bytes, sattn_dtype dtype,
                                  void *cuda_stream);
 
+/*
+ * Encoder states: what a vision, video or speech model does with the keys and
+ * values of its encoder.
+ *
+ * sattn_rope_axes turns queries and keys by positions with several axes (time,
+ * height, width).
+ *   q [T, H, d], k [T, Hkv, d] (dtype): the heads of a token are contiguous, tokens lie
+ *     q_stride, k_stride elements apart (multiples of 16 bytes), so slices of one
+ *     projection's output serve as they are; k may be NULL (Hkv and its strides are then
+ *     not looked at). q_out, k_out likewise, q_out_stride, k_out_stride apart; each may be its
+ *     input with the same stride (in place), otherwise they must not overlap the inputs
+ *     or one another.
+ *   positions int32 [axes, T]; inv_freq float32 [rd / 2]; axis uint8 [rd / 2]: column pair i
+ *     turns by the angle positions[axis[i]][t] * inv_freq[i] (an axis that is not there is
+ *     reported, the pair stays as it is). Pair i is column i with i + rd / 2, or with
+ *     interleaved = 1 column 2 i with 2 i + 1, of the first rd columns; the others are
+ *     copied. (a, b) becomes (a cos - b sin, b cos + a sin); with inverse = 1 (a cos + b sin,
+ *     b cos - a sin), which undoes it and takes gradients of the outputs to the inputs.
+ * Positions may be any int32. Angles are taken modulo a turn in 64 bits, right to 2^-25 of
+ * a turn for |position * inv_freq| below 2^32; the rest is fp32, rounded once to dtype. A
+ * non-finite inv_freq makes its columns NaN.
+ * Requirements: d a multiple of 8; rd a multiple of 16, 16 .. min(d, 256); 1 <= axes <= 255;
+ * T * axes and (H + Hkv) * d below 2^31; tensors 16-byte aligned.
+ */
+sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                             const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride,
+                             const int32_t *positions, const float *inv_freq,
+                             const uint8_t *axis, int32_t axes, int32_t T, int32_t H,
+                             int32_t Hkv, int32_t d, int32_t rd, int32_t interleaved,
+                             int32_t inverse, sattn_dtype dtype, void *cuda_stream);
+
+/*
+ * Attention of queries to encoder states of another length.
+ *   q [T, H, d], k, v [S, Hkv, d] (dtype), strides as above (of k and v too);
+ *   cu_seqlens int32 [B + 1]: the queries of sequence b are rows cu_seqlens[b] ..
+ *     cu_seqlens[b + 1] - 1 ([0] = 0, non-decreasing, at most T);
+ *   kv_starts, kv_lens int32 [B]: its states are rows kv_starts[b] .. kv_starts[b] +
+ *     kv_lens[b] - 1 of k and v. So states may be packed, padded, or shared: sequences may
+ *     name the same rows (several hypotheses over the same states can also be the queries
+ *     of one sequence: no order is kept between them, and their states are read once).
+ *   o [T, H, d] (dtype, contiguous), lse [T, H] float32 or NULL.
+ * Every query of a sequence sees all of its states. Query head h reads KV head
+ * h / (H / Hkv). Sinks as for the other entry points (key 0 is the sequence's first state;
+ * finite ones beyond 2e38 in size count as that). A row without states has o = 0 and lse =
+ * -inf (the sink with NULL_LOGIT). Rows of k and v outside a sequence's range may hold anything,
+ * NaN too. A sequence whose numbers contradict one another or the tensors' sizes is skipped
+ * and reported by sattn_check_device; its rows, and rows behind the last sequence, are not
+ * written.
+ *   max_q_len >= every sequence's number of queries: a hint that chooses the kernel's
+ *     form; any value gives right results.
+ *   workspace: NULL or a caller-owned device buffer of at least
+ *     sattn_cross_workspace_bytes(...) bytes, 256-byte aligned; it receives partial
+ *     results and is free again when the call's work has run. Calls that may overlap on
+ *     the GPU need one each. Without one, units of work are not cut, which is slower where there
+ *     are few.
+ * bf16: the tensor cores, probabilities rounded to bf16 for the product with V, the
+ * denominator and lse from the unrounded ones. fp32: everything in fp32, by a kernel that takes
+ * 100 times as long and more.
+ * Requirements: H % Hkv == 0, d in {64, 128}; for bf16 H / Hkv <= 128
+ * (SATTN_ERR_UNSUPPORTED otherwise); T * H below 2^31; tensors 16-byte aligned.
+ */
+size_t sattn_cross_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
+sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const int32_t *cu_seqlens,
+                             const int32_t *kv_starts, const int32_t *kv_lens, int32_t B,
+                             int32_t T, int32_t S, int32_t max_q_len, int32_t H, int32_t Hkv,
+                             int32_t d, const float *sinks, sattn_sink_mode sink_mode,
+                             float scale, void *o, float *lse, void *workspace,
+                             size_t workspace_bytes, sattn_dtype dtype, void *cuda_stream);
+
+/*
+ * What each state's key receives of that attention: weights float32 [Hkv, S],
+ *   weights[g][kv_starts[b] + j] = sum over the queries i of sequence b and the query heads
+ *   h of group g of exp(scale <q[i, h], k[kv_starts[b] + j, g]> (+ the key-0 sink) - lse[i, h]),
+ * added to what is there with accumulate = 1. Rows of no sequence are left as they are; a
+ * sequence without queries gives its rows 0. lse [T, H] is that of sattn_cross_fwd for the same
+ * arguments (a row with an infinite one weighs nothing). The row ranges of the sequences
+ * must not overlap (the weights of shared rows are unspecified): pass hypotheses over
+ * the same states as the queries of one sequence. Sums are fp32, in a fixed order: the
+ * same call gives the same bits. Everything else as for sattn_cross_fwd; the workspace's
+ * size is sattn_cross_key_weights_workspace_bytes().
+ */
+size_t sattn_cross_key_weights_workspace_bytes(void);
+sattn_status sattn_cross_key_weights(const void *q, int64_t q_stride, const void *k,
+                                     int64_t k_stride, const float *lse,
+                                     const int32_t *cu_seqlens, const int32_t *kv_starts,
+                                     const int32_t *kv_lens, int32_t B, int32_t T, int32_t S,
+                                     int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d,
+                                     const float *sinks, sattn_sink_mode sink_mode, float scale,
+                                     float *weights, int32_t accumulate, void *workspace,
+                                     size_t workspace_bytes, sattn_dtype dtype,
+                                     void *cuda_stream);
+
+/*
+ * Eviction by those weights: of each sequence and KV head the `keep` rows stay that
+ * are its first `first` or last `last` ones or, of the others, the heaviest (the lower row
+ * first among equal ones; a weight that is NaN or not above 0 counts as 0), in their order.
+ * A sequence of at most `keep` rows stays whole.
+ *   k, v [S, Hkv, d] (dtype, strides as above), weights float32 [Hkv, S], kv_starts, kv_lens
+ *     int32 [B] as above (ranges may overlap);
+ *   k_out, v_out [B * keep, Hkv, d] (contiguous): the rows of sequence b from row b * keep on,
+ *     each head's own; zeros behind the last one;
+ *   weights_out float32, rows_out int32 [Hkv, B * keep]: their weights and which rows of the
+ *     sequence they were; 0 and -1 behind the last one;
+ *   out_starts, out_lens int32 [B]: b * keep, and min(kv_lens[b], keep): the outputs are
+ *     states for the calls above as they are.
+ * A sequence whose range is not in [0, S) is reported and comes out with length 0. Outputs
+ * must not overlap inputs (SATTN_ERR_INVALID_ARG where they start at the same address).
+ * Requirements: keep >= 1, first, last >= 0, first + last <= keep, d in {64, 128},
+ * B * keep * Hkv below 2^31; k, v, k_out, v_out 16-byte aligned.
+ */
+sattn_status sattn_evict_keys(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const float *weights, const int32_t *kv_starts,
+                              const int32_t *kv_lens, int32_t B, int32_t S, int32_t Hkv,
+                              int32_t d, int32_t keep, int32_t first, int32_t last, void *k_out,
+                              void *v_out, float *weights_out, int32_t *rows_out,
+                              int32_t *out_starts, int32_t *out_lens, sattn_dtype dtype,
+                              void *cuda_stream);
+
 /* Human-readable name of a status code (static storage). */
 const char *sattn_status_str(sattn_status s);
 

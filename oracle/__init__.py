@@ -552,3 +552,91 @@ def paged_attend(q, k_codes, v_codes, k_scale, v_scale, page_table, cu_seqlens, 
                     o[t0:t1, h] = np.where(z[:, None] > 0, p @ v / z[:, None], 0.0)
                     lse[t0:t1, h] = np.where(z > 0, base + np.log(z), -np.inf)
     return o, lse
+
+
+# ------------------------------------------------------- encoder states
+
+def rope_axes(x, positions, inv_freq, axis, interleaved, inverse=False):
+    """x [T, heads, d] with its first rd = 2 len(inv_freq) columns turned: pair i by
+    positions[axis[i]] * inv_freq[i], the angle in exact integers over a 200-bit 2 pi."""
+    x = np.array(x, np.float64)
+    half = len(inv_freq)
+    bits = 200
+    # 2 pi to 60 digits, as an integer of 2^-200
+    two_pi = 628318530717958647692528676655900576839433879875021164194989 << bits
+    two_pi //= 10 ** 59
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        num, den = float(inv_freq[i]).as_integer_ratio()
+        ang = np.array([float(((int(p) * num << bits) // den) % two_pi) / 2.0 ** bits
+                        for p in positions[axis[i]]])
+        c, s = np.cos(ang)[:, None], np.sin(ang)[:, None]
+        if inverse:
+            s = -s
+        xa, xb = x[:, :, a].copy(), x[:, :, b].copy()
+        x[:, :, a] = xa * c - xb * s
+        x[:, :, b] = xb * c + xa * s
+    return x
+
+
+def cross_attend(q, k, v, cu_seqlens, kv_starts, kv_lens, sinks, sink_mode, scale):
+    """Literal softmax of every query row over its sequence's states. Rows of no sequence
+    come back as NaN."""
+    T, H, d = q.shape
+    Hkv = k.shape[1]
+    o, lse = np.full((T, H, d), np.nan), np.full((T, H), np.nan)
+    for b, (s0, L) in enumerate(zip(kv_starts, kv_lens)):
+        t0, t1 = int(cu_seqlens[b]), int(cu_seqlens[b + 1])
+        for h in range(H):
+            g = h // (H // Hkv)
+            keys, vals = (np.asarray(x[s0:s0 + L, g], np.float64) for x in (k, v))
+            for t in range(t0, t1):
+                x = keys @ np.asarray(q[t, h], np.float64) * scale
+                if sink_mode == 1 and L > 0:
+                    x[0] += float(sinks[h])
+                terms = np.append(x, float(sinks[h])) if sink_mode == 2 else x
+                if len(terms) == 0 or np.isneginf(terms.max()):
+                    o[t, h], lse[t, h] = 0.0, -np.inf
+                    continue
+                top = terms.max()
+                z = np.exp(terms - top).sum()
+                o[t, h] = np.exp(x - top) @ vals / z
+                lse[t, h] = top + np.log(z)
+    return o, lse
+
+
+def cross_key_weights(q, k, lse, cu_seqlens, kv_starts, kv_lens, weights, accumulate, sinks,
+                      sink_mode, scale):
+    """weights [Hkv, S] with the sequences' rows written, or added to."""
+    H, Hkv = q.shape[1], k.shape[1]
+    out = np.array(weights, np.float64)
+    for b, (s0, L) in enumerate(zip(kv_starts, kv_lens)):
+        rows = slice(int(cu_seqlens[b]), int(cu_seqlens[b + 1]))
+        for g in range(Hkv):
+            total = np.zeros(L)
+            for h in range(g * (H // Hkv), (g + 1) * (H // Hkv)):
+                x = np.asarray(q[rows, h], np.float64) @ np.asarray(k[s0:s0 + L, g], np.float64).T
+                x *= scale
+                if sink_mode == 1 and L > 0:
+                    x[:, 0] += float(sinks[h])
+                z = np.asarray(lse[rows, h], np.float64)
+                live = np.isfinite(z) | np.isnan(z)
+                total += np.exp(x[live] - z[live, None]).sum(0)
+            out[g, s0:s0 + L] = total + (out[g, s0:s0 + L] if accumulate else 0.0)
+    return out
+
+
+def evict_keys(weights, kv_starts, kv_lens, keep, first, last):
+    """Which rows of each sequence stay, int32 [Hkv, B * keep], -1 behind the last one."""
+    Hkv, B = weights.shape[0], len(kv_lens)
+    rows = np.full((Hkv, B * keep), -1, np.int32)
+    for b, (s0, L) in enumerate(zip(kv_starts, kv_lens)):
+        for h in range(Hkv):
+            w = np.asarray(weights[h, s0:s0 + L], np.float64)
+            with np.errstate(invalid="ignore"):
+                w = np.where(w > 0, w, 0.0)
+            stay = [j for j in range(L) if j < first or j >= L - last]
+            rest = sorted((j for j in range(L) if first <= j < L - last), key=lambda j: (-w[j], j))
+            kept = sorted((stay + rest)[:keep])
+            rows[h, b * keep: b * keep + len(kept)] = kept
+    return rows

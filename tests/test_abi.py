@@ -240,3 +240,80 @@ def test_paged_fp8_refusals(lib):
     assert fwd(T=0, q=None) == 0 and fwd(B=0, q=None) == 0
     size = lib.sattn_paged_fp8_workspace_bytes
     assert size(0, 32, 8, 128) == 0 and size(1, 30, 8, 128) == 0 and size(1, 32, 8, 96) == 0
+
+
+def test_encoder_state_refusals(lib):
+    """Each call differs from an acceptable one in the one argument named."""
+    f, i64 = ctypes.c_void_p(0x1000), ctypes.c_int64
+    g, odd = ctypes.c_void_p(0x2000), ctypes.c_void_p(0x1008)
+
+    def call(fn, strides, a, kw):
+        assert not set(kw) - set(a)
+        a = {**a, **kw}
+        for n in strides:
+            a[n] = i64(a[n])
+        return fn(*a.values(), None)
+
+    def rope(**kw):
+        return call(lib.sattn_rope_axes, ("qs", "qos", "ks", "kos"),
+                    dict(q=f, qs=4096, qo=g, qos=4096, k=f, ks=1024, ko=g, kos=1024, pos=f, freq=f,
+                         axis=f, axes=3, T=4, H=32, Hkv=8, d=128, rd=128, inter=0, inverse=0,
+                         dtype=1), kw)
+
+    for bad in (dict(axes=0), dict(axes=256), dict(T=-1), dict(H=0), dict(Hkv=0), dict(d=0),
+                dict(d=100), dict(rd=0), dict(rd=24), dict(rd=144), dict(rd=-16),
+                dict(d=512, rd=272, qs=16384, qos=16384, ks=4096, kos=4096), dict(inter=2),
+                dict(inverse=-1), dict(dtype=2), dict(qs=4095), dict(qs=4100), dict(ks=1023),
+                dict(qos=1024), dict(kos=1028), dict(q=None), dict(qo=None), dict(ko=None),
+                dict(pos=None), dict(freq=None), dict(axis=None), dict(q=odd), dict(qo=odd),
+                dict(k=odd), dict(ko=odd), dict(qo=f, qos=8192), dict(ko=f, kos=2048),
+                dict(T=1 << 30), dict(H=1 << 30, qs=1 << 38, qos=1 << 38)):
+        assert rope(**bad) == 1, bad
+    assert rope(T=0, q=None) == 0  # empty: no work
+
+    shape = dict(B=2, T=4, S=100, n=1, H=32, Hkv=8, d=128)
+    common = (dict(B=-1), dict(T=-1), dict(S=-1), dict(n=-1), dict(H=0), dict(H=12), dict(Hkv=0),
+              dict(d=96), dict(sinks=None), dict(mode=3), dict(scale=0.0),
+              dict(scale=float("nan")), dict(scale=float("inf")), dict(dtype=7), dict(qs=4095),
+              dict(qs=4100), dict(ks=1020), dict(ks=1028), dict(q=None), dict(k=None),
+              dict(cu=None), dict(starts=None), dict(lens=None), dict(q=odd), dict(k=odd),
+              dict(ws=odd))
+
+    def cross(**kw):
+        return call(lib.sattn_cross_fwd, ("qs", "ks", "vs"),
+                    dict(q=f, qs=4096, k=f, ks=1024, v=f, vs=1024, cu=f, starts=f, lens=f, **shape,
+                         sinks=f, mode=2, scale=0.1, o=f, lse=f, ws=None, wsb=0, dtype=1), kw)
+
+    for bad in common + (dict(v=None), dict(vs=512), dict(v=odd), dict(o=None), dict(o=odd)):
+        assert cross(**bad) == 1, bad
+    assert cross(T=0, q=None) == 0 and cross(B=0, q=None) == 0
+    assert cross(H=256, Hkv=1, qs=256 * 128) == 2  # more heads to a group than rows to a tile
+    size = lib.sattn_cross_workspace_bytes
+    assert size(0, 32, 8, 128) == 0 and size(1, 30, 8, 128) == 0 and size(1, 32, 8, 96) == 0
+
+    def weights(**kw):
+        return call(lib.sattn_cross_key_weights, ("qs", "ks"),
+                    dict(q=f, qs=4096, k=f, ks=1024, lse=f, cu=f, starts=f, lens=f, **shape,
+                         sinks=f, mode=1, scale=0.1, w=f, add=1, ws=None, wsb=0, dtype=1), kw)
+
+    for bad in common + (dict(lse=None), dict(w=None), dict(add=2)):
+        assert weights(**bad) == 1, bad
+    assert weights(S=0, k=None) == 0 and weights(B=0, q=None) == 0
+    assert weights(H=256, Hkv=1, qs=256 * 128) == 2
+
+    def evict(**kw):
+        return call(lib.sattn_evict_keys, ("ks", "vs"),
+                    dict(k=f, ks=1024, v=f, vs=1024, w=f, starts=f, lens=f, B=2, S=100, Hkv=8,
+                         d=128, keep=8, first=2, last=3, ko=ctypes.c_void_p(0x20000),
+                         vo=ctypes.c_void_p(0x30000), wo=g, rows=g, so=g, lo=g, dtype=1), kw)
+
+    for bad in (dict(B=-1), dict(S=-1), dict(Hkv=0), dict(d=32), dict(keep=0), dict(first=-1),
+                dict(last=-1), dict(first=6), dict(first=2 ** 31 - 1, last=2 ** 31 - 1),
+                dict(dtype=2), dict(ks=1020), dict(vs=1028), dict(keep=1 << 30),
+                dict(keep=1 << 27, B=2, Hkv=8), dict(k=None), dict(v=None), dict(w=None),
+                dict(starts=None), dict(lens=None), dict(ko=None), dict(vo=None), dict(wo=None),
+                dict(rows=None), dict(so=None), dict(lo=None), dict(k=odd), dict(v=odd),
+                dict(ko=odd), dict(vo=odd), dict(ko=f), dict(vo=f), dict(wo=f), dict(so=f),
+                dict(lo=f), dict(vo=ctypes.c_void_p(0x20000))):
+        assert evict(**bad) == 1, bad
+    assert evict(B=0, k=None) == 0

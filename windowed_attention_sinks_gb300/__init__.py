@@ -96,6 +96,23 @@ def lib() -> ctypes.CDLL:
                                       i32, i32, i32, i32, i32, P, ctypes.c_int, f32, P, P, P, sz,
                                       ctypes.c_int, P]
     L.sattn_paged_fp8_fwd.restype = ctypes.c_int
+    L.sattn_rope_axes.argtypes = [P, i64, P, i64, P, i64, P, i64, P, P, P, i32, i32, i32, i32, i32,
+                                  i32, i32, i32, ctypes.c_int, P]
+    L.sattn_rope_axes.restype = ctypes.c_int
+    L.sattn_cross_workspace_bytes.argtypes = [i32, i32, i32, i32]
+    L.sattn_cross_workspace_bytes.restype = sz
+    L.sattn_cross_fwd.argtypes = [P, i64, P, i64, P, i64, P, P, P, i32, i32, i32, i32, i32, i32,
+                                  i32, P, ctypes.c_int, f32, P, P, P, sz, ctypes.c_int, P]
+    L.sattn_cross_fwd.restype = ctypes.c_int
+    L.sattn_cross_key_weights_workspace_bytes.argtypes = []
+    L.sattn_cross_key_weights_workspace_bytes.restype = sz
+    L.sattn_cross_key_weights.argtypes = [P, i64, P, i64, P, P, P, P, i32, i32, i32, i32, i32,
+                                          i32, i32, P, ctypes.c_int, f32, P, i32, P, sz,
+                                          ctypes.c_int, P]
+    L.sattn_cross_key_weights.restype = ctypes.c_int
+    L.sattn_evict_keys.argtypes = [P, i64, P, i64, P, P, P, i32, i32, i32, i32, i32, i32, i32, P,
+                                   P, P, P, P, P, ctypes.c_int, P]
+    L.sattn_evict_keys.restype = ctypes.c_int
     L.sattn_status_str.argtypes = [ctypes.c_int]
     L.sattn_status_str.restype = ctypes.c_char_p
     L.sattn_set_debug.argtypes = [ctypes.c_int]
@@ -431,7 +448,7 @@ def _token_rows(t, name, T, heads, d, dtype, dev):
     if t.shape != (T, heads, d) or t.dtype is not dtype or t.get_device() != dev:
         raise ValueError("%s must be %s [%d, %d, %d] on cuda:%d" % (name, dtype, T, heads, d, dev))
     st = t.stride()
-    if st[2] != 1 or (st[1] != d and heads > 1):
+    if T > 0 and (st[2] != 1 or (st[1] != d and heads > 1)):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     return st[0] if T > 1 else heads * d
 
@@ -544,6 +561,217 @@ def paged_fp8_fwd(q, k_cache, v_cache, k_scale, v_scale, page_table, cu_seqlens,
     if rc:
         _check("sattn_paged_fp8_fwd", rc)
     return o, lse
+
+
+def _vector(t, name, n, dtype, dev):
+    """Checks a contiguous [n] of dtype on device index dev; returns its address."""
+    if t.shape != (n,) or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s [%d] on cuda:%d" % (name, dtype, n, dev))
+    return t.data_ptr()
+
+
+def _device_of(t, name):
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return dev
+
+
+def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False, q_out=None,
+              k_out=None, stream=None):
+    """Turn queries and keys by positions with several axes (sattn_rope_axes).
+
+    q [T, H, d], k [T, Hkv, d] or None, bf16 or fp32 (tokens may be strided, as slices of one
+    projection are); positions int32 [axes, T]; inv_freq fp32 [rd / 2]; axis uint8 [rd / 2],
+    the axis that each pair of columns turns by. inverse turns back (and takes gradients of
+    the outputs to the inputs). q_out, k_out may be q and k themselves; without them they are
+    taken from torch's allocator for the stream that the call runs on. Returns (q_out,
+    k_out)."""
+    import torch
+
+    dev = _device_of(q, "q")
+    T, H, d = q.shape
+    dt = q.dtype
+    code = _dtype_code(q)
+    qs = _token_rows(q, "q", T, H, d, dt, dev)
+    pshape = positions.shape
+    if len(pshape) != 2 or pshape[1] != T or positions.dtype is not torch.int32 or \
+            positions.get_device() != dev or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 [axes, %d] on cuda:%d" % (T, dev))
+    half = inv_freq.numel()
+    fp = _vector(inv_freq, "inv_freq", half, torch.float32, dev)
+    ap = _vector(axis, "axis", half, torch.uint8, dev)
+    Hkv = ks = kos = 0
+    kp = kop = None
+    with _OnDevice(dev, stream) as s:
+        if q_out is None:
+            q_out = _empty((T, H, d), dt, q.device, stream)
+            qos = H * d
+        else:
+            qos = _token_rows(q_out, "q_out", T, H, d, dt, dev)
+        if k is not None:
+            Hkv = k.shape[1]
+            ks = _token_rows(k, "k", T, Hkv, d, dt, dev)
+            kp = k.data_ptr()
+            if k_out is None:
+                k_out = _empty((T, Hkv, d), dt, q.device, stream)
+                kos = Hkv * d
+            else:
+                kos = _token_rows(k_out, "k_out", T, Hkv, d, dt, dev)
+            kop = k_out.data_ptr()
+        elif k_out is not None:
+            raise ValueError("k_out without k")
+        rc = lib().sattn_rope_axes(q.data_ptr(), qs, q_out.data_ptr(), qos, kp, ks, kop, kos,
+                                   positions.data_ptr(), fp, ap, pshape[0], T, H, Hkv, d,
+                                   2 * half, 1 if interleaved else 0, 1 if inverse else 0, code,
+                                   s)
+    if rc:
+        _check("sattn_rope_axes", rc)
+    return q_out, k_out
+
+
+def _states(q, k, cu_seqlens, kv_starts, kv_lens):
+    """Checks queries [T, H, d] and keys [S, Hkv, d] of B sequences; returns (device
+    index, T, S, H, Hkv, d, B, q's and k's token strides)."""
+    import torch
+
+    i32 = torch.int32
+    dev = _device_of(q, "q")
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q must be [T, H, d], k [S, Hkv, d]")
+    T, H, d = q.shape
+    S, Hkv = k.shape[0], k.shape[1]
+    B = kv_starts.numel()
+    for t, name, n in ((kv_starts, "kv_starts", B), (kv_lens, "kv_lens", B),
+                       (cu_seqlens, "cu_seqlens", B + 1)):
+        _vector(t, name, n, i32, dev)
+    return (dev, T, S, H, Hkv, d, B, _token_rows(q, "q", T, H, d, q.dtype, dev),
+            _token_rows(k, "k", S, Hkv, d, q.dtype, dev))
+
+
+def _workspace(t, nbytes, dev, device, stream):
+    """(tensor, address, bytes) of a given workspace, or of one of nbytes for this call."""
+    import torch
+
+    if t is not None:
+        if t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("workspace must be contiguous on cuda:%d" % dev)
+        return t, t.data_ptr(), t.numel() * t.element_size()
+    if not nbytes:
+        return None, None, 0
+    t = _empty(nbytes, torch.uint8, device, stream)
+    return t, t.data_ptr(), nbytes
+
+
+def cross_workspace_bytes(max_q_len, H, Hkv, d):
+    """Workspace bytes of cross_fwd (sattn_cross_workspace_bytes)."""
+    return int(lib().sattn_cross_workspace_bytes(int(max_q_len), int(H), int(Hkv), int(d)))
+
+
+def cross_fwd(q, k, v, cu_seqlens, kv_starts, kv_lens, max_q_len=None, sinks=None,
+              sink_mode=SINK_NONE, scale=None, o=None, lse=None, workspace=None, stream=None):
+    """Attention of q [T, H, d] to encoder states k, v [S, Hkv, d] of another length
+    (sattn_cross_fwd): sequence b's queries are rows cu_seqlens[b] .. cu_seqlens[b + 1] - 1, its
+    states rows kv_starts[b] .. kv_starts[b] + kv_lens[b] - 1 (int32; packed, padded or
+    shared). Returns (o, lse). max_q_len, the most queries that a sequence has (their mean
+    if not given), chooses the kernel's form. Rows behind the last sequence are not written.
+    Without a workspace, o or lse they are taken from torch's allocator for the stream that
+    the call runs on."""
+    import torch
+
+    dev, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
+    dt = q.dtype
+    code = _dtype_code(q)
+    vs = _token_rows(v, "v", S, Hkv, d, dt, dev)
+    sp = None if sinks is None else _vector(sinks, "sinks", H, torch.float32, dev)
+    n = (-(-T // B) if B else 0) if max_q_len is None else int(max_q_len)
+    L = lib()
+    with _OnDevice(dev, stream) as s:
+        device = q.device
+        o = _out(o, "o", (T, H, d), dt, device, stream)
+        lse = _out(lse, "lse", (T, H), torch.float32, device, stream)
+        nb = L.sattn_cross_workspace_bytes(n, H, Hkv, d) if code == BF16 else 0
+        workspace, wp, nb = _workspace(workspace, nb, dev, device, stream)
+        rc = L.sattn_cross_fwd(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+                               cu_seqlens.data_ptr(), kv_starts.data_ptr(), kv_lens.data_ptr(), B,
+                               T, S, n, H, Hkv, d, sp, int(sink_mode),
+                               d ** -0.5 if scale is None else float(scale), o.data_ptr(),
+                               lse.data_ptr(), wp, nb, code, s)
+    if rc:
+        _check("sattn_cross_fwd", rc)
+    return o, lse
+
+
+def cross_key_weights(q, k, lse, cu_seqlens, kv_starts, kv_lens, weights, max_q_len=None,
+                      accumulate=False, sinks=None, sink_mode=SINK_NONE, scale=None,
+                      workspace=None, stream=None):
+    """What each state's key receives of cross_fwd's attention, with that call's arguments
+    and its lse (sattn_cross_key_weights): written to the sequences' rows of weights fp32
+    [Hkv, S], or added to them. Returns weights."""
+    import torch
+
+    dev, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
+    code = _dtype_code(q)
+    device = q.device
+    for t, name, shape in ((lse, "lse", (T, H)), (weights, "weights", (Hkv, S))):
+        if t is None:
+            raise ValueError("%s is needed" % name)
+        _out(t, name, shape, torch.float32, device, stream)
+    sp = None if sinks is None else _vector(sinks, "sinks", H, torch.float32, dev)
+    n = (-(-T // B) if B else 0) if max_q_len is None else int(max_q_len)
+    L = lib()
+    with _OnDevice(dev, stream) as s:
+        nb = L.sattn_cross_key_weights_workspace_bytes() if code == BF16 else 0
+        workspace, wp, nb = _workspace(workspace, nb, dev, device, stream)
+        rc = L.sattn_cross_key_weights(q.data_ptr(), qs, k.data_ptr(), ks, lse.data_ptr(),
+                                       cu_seqlens.data_ptr(), kv_starts.data_ptr(),
+                                       kv_lens.data_ptr(), B, T, S, n, H, Hkv, d, sp,
+                                       int(sink_mode), d ** -0.5 if scale is None else float(scale),
+                                       weights.data_ptr(), 1 if accumulate else 0, wp, nb, code, s)
+    if rc:
+        _check("sattn_cross_key_weights", rc)
+    return weights
+
+
+def evict_keys(k, v, weights, kv_starts, kv_lens, keep, first=0, last=0, k_out=None, v_out=None,
+               weights_out=None, rows_out=None, out_starts=None, out_lens=None, stream=None):
+    """Keep each sequence's and KV head's `keep` heaviest rows of k, v [S, Hkv, d], in their
+    order, its `first` first and `last` last ones always (sattn_evict_keys); weights fp32
+    [Hkv, S]. Returns (k, v [B * keep, Hkv, d], weights [Hkv, B * keep], rows int32 [Hkv,
+    B * keep], kv_starts, kv_lens [B]): states for the other calls as they are."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
+    dev = _device_of(k, "k")
+    if k.dim() != 3:
+        raise ValueError("k must be [S, Hkv, d]")
+    S, Hkv, d = k.shape
+    dt = k.dtype
+    code = _dtype_code(k)
+    ks = _token_rows(k, "k", S, Hkv, d, dt, dev)
+    vs = _token_rows(v, "v", S, Hkv, d, dt, dev)
+    B, keep = kv_starts.numel(), int(keep)
+    _vector(kv_starts, "kv_starts", B, i32, dev)
+    _vector(kv_lens, "kv_lens", B, i32, dev)
+    device = k.device
+    if weights is None or keep < 1:
+        raise ValueError("weights are needed, and keep must be at least 1")
+    _out(weights, "weights", (Hkv, S), f32, device, stream)
+    with _OnDevice(dev, stream) as s:
+        k_out = _out(k_out, "k_out", (B * keep, Hkv, d), dt, device, stream)
+        v_out = _out(v_out, "v_out", (B * keep, Hkv, d), dt, device, stream)
+        weights_out = _out(weights_out, "weights_out", (Hkv, B * keep), f32, device, stream)
+        rows_out = _out(rows_out, "rows_out", (Hkv, B * keep), i32, device, stream)
+        out_starts = _out(out_starts, "out_starts", (B,), i32, device, stream)
+        out_lens = _out(out_lens, "out_lens", (B,), i32, device, stream)
+        rc = lib().sattn_evict_keys(k.data_ptr(), ks, v.data_ptr(), vs, weights.data_ptr(),
+                                    kv_starts.data_ptr(), kv_lens.data_ptr(), B, S, Hkv, d, keep,
+                                    int(first), int(last), k_out.data_ptr(), v_out.data_ptr(),
+                                    weights_out.data_ptr(), rows_out.data_ptr(),
+                                    out_starts.data_ptr(), out_lens.data_ptr(), code, s)
+    if rc:
+        _check("sattn_evict_keys", rc)
+    return k_out, v_out, weights_out, rows_out, out_starts, out_lens
 
 
 def compress_kv(kv, score, ape, ratio, overlap, out=None, out_dtype=None, stream=None):

@@ -181,6 +181,12 @@ bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {
     return stride >= (int64_t)heads * d && stride % unit == 0;
 }
 
+// Queries [T, H, d] and encoder states [S, Hkv, d] of B sequences.
+bool valid_states(int B, int T, int S, int max_q_len, int H, int Hkv, int d) {
+    return B >= 0 && T >= 0 && S >= 0 && max_q_len >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 &&
+           (d == 64 || d == 128) && (int64_t)T * H <= INT32_MAX;
+}
+
 // sm_103 only: the fatbin carries sm_103a code and nothing else.
 sattn_status check_arch(const DevInfo *dev) {
     if (dev->cc_major != 10 || dev->cc_minor != 3) return SATTN_ERR_UNSUPPORTED;
@@ -191,7 +197,7 @@ sattn_status check_arch(const DevInfo *dev) {
 
 extern "C" {
 
-int32_t sattn_version(void) { return 104; }
+int32_t sattn_version(void) { return 105; }
 
 const char *sattn_status_str(sattn_status s) {
     switch (s) {
@@ -599,6 +605,150 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
     return finish(paged_few_rows(max_q_len, H / Hkv) ? launch_paged_decode(a, *dev, s)
                                                      : launch_paged_prefill(a, *dev, s),
                   s);
+}
+
+sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                             const void *k, int64_t k_stride, void *k_out, int64_t k_out_stride,
+                             const int32_t *positions, const float *inv_freq,
+                             const uint8_t *axis, int32_t axes, int32_t T, int32_t H,
+                             int32_t Hkv, int32_t d, int32_t rd, int32_t interleaved,
+                             int32_t inverse, sattn_dtype dtype, void *cuda_stream) {
+    if (T < 0 || H <= 0 || d <= 0 || d % 8 != 0 || rd < 16 || rd % 16 != 0 || rd > d || rd > 256 ||
+        axes < 1 || axes > 255 || !valid_dtype(dtype))
+        return SATTN_ERR_INVALID_ARG;
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+        return SATTN_ERR_INVALID_ARG;
+    if (!k) Hkv = 0;
+    else if (Hkv <= 0) return SATTN_ERR_INVALID_ARG;
+    if (((int64_t)H + Hkv) * d > INT32_MAX || (int64_t)T * axes > INT32_MAX)
+        return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;
+    if (!valid_rows(q_stride, H, d, unit) || !valid_rows(q_out_stride, H, d, unit) ||
+        (k && (!valid_rows(k_stride, Hkv, d, unit) || !valid_rows(k_out_stride, Hkv, d, unit))))
+        return SATTN_ERR_INVALID_ARG;
+    if (T == 0) return SATTN_OK;
+    if (!q || !q_out || (k && !k_out) || !positions || !inv_freq || !axis)
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(q_out) || !aligned16(k) || (k && !aligned16(k_out)))
+        return SATTN_ERR_INVALID_ARG;
+    if (T > 1 && ((q == q_out && q_stride != q_out_stride) ||
+                  (k && k == k_out && k_stride != k_out_stride)))
+        return SATTN_ERR_INVALID_ARG;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    RopeArgs a{q, k, q_out, k_out, q_stride, k_stride, q_out_stride, k_out_stride, positions,
+               inv_freq, axis, axes, T, H, Hkv, d, rd, interleaved, inverse, (int)dtype};
+    return finish(launch_rope_axes(a, *dev, s), s);
+}
+
+size_t sattn_cross_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d) {
+    return 0;
+}
+
+sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const int32_t *cu_seqlens,
+                             const int32_t *kv_starts, const int32_t *kv_lens, int32_t B,
+                             int32_t T, int32_t S, int32_t max_q_len, int32_t H, int32_t Hkv,
+                             int32_t d, const float *sinks, sattn_sink_mode sink_mode,
+                             float scale, void *o, float *lse, void *workspace,
+                             size_t workspace_bytes, sattn_dtype dtype, void *cuda_stream) {
+    if (!valid_states(B, T, S, max_q_len, H, Hkv, d) || !valid_dtype(dtype) ||
+        !valid_sink(sink_mode, sinks) || !finite_scale(scale))
+        return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;
+    if (!valid_rows(q_stride, H, d, unit) || !valid_rows(k_stride, Hkv, d, unit) ||
+        !valid_rows(v_stride, Hkv, d, unit))
+        return SATTN_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) return SATTN_OK;
+    if (!q || !cu_seqlens || !kv_starts || !kv_lens || !o || (S > 0 && (!k || !v)))
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+        (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return SATTN_ERR_INVALID_ARG;
+    if (dtype == SATTN_BF16 && H / Hkv > 128) return SATTN_ERR_UNSUPPORTED;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    CrossArgs a{q, k, v, q_stride, k_stride, v_stride, cu_seqlens, kv_starts, kv_lens, B, T, S,
+                max_q_len, H, Hkv, d, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
+                (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
+    return finish(launch_cross_simt(a, *dev, s), s);
+}
+
+size_t sattn_cross_key_weights_workspace_bytes(void) { return 0; }
+
+sattn_status sattn_cross_key_weights(const void *q, int64_t q_stride, const void *k,
+                                     int64_t k_stride, const float *lse,
+                                     const int32_t *cu_seqlens, const int32_t *kv_starts,
+                                     const int32_t *kv_lens, int32_t B, int32_t T, int32_t S,
+                                     int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d,
+                                     const float *sinks, sattn_sink_mode sink_mode, float scale,
+                                     float *weights, int32_t accumulate, void *workspace,
+                                     size_t workspace_bytes, sattn_dtype dtype,
+                                     void *cuda_stream) {
+    if (!valid_states(B, T, S, max_q_len, H, Hkv, d) || !valid_dtype(dtype) ||
+        !valid_sink(sink_mode, sinks) || !finite_scale(scale))
+        return SATTN_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;
+    if (!valid_rows(q_stride, H, d, unit) || !valid_rows(k_stride, Hkv, d, unit))
+        return SATTN_ERR_INVALID_ARG;
+    if (B == 0 || S == 0) return SATTN_OK;
+    if ((T > 0 && (!q || !lse)) || !k || !cu_seqlens || !kv_starts || !kv_lens || !weights)
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) ||
+        (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)))
+        return SATTN_ERR_INVALID_ARG;
+    if (dtype == SATTN_BF16 && H / Hkv > 128) return SATTN_ERR_UNSUPPORTED;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    KeyWeightArgs a{q, k, q_stride, k_stride, lse, cu_seqlens, kv_starts, kv_lens, B, T, S,
+                    max_q_len, H, Hkv, d, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
+                    (int)sink_mode, scale, weights, accumulate, workspace, workspace_bytes,
+                    (int)dtype};
+    return finish(launch_weights_simt(a, *dev, s), s);
+}
+
+sattn_status sattn_evict_keys(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const float *weights, const int32_t *kv_starts,
+                              const int32_t *kv_lens, int32_t B, int32_t S, int32_t Hkv,
+                              int32_t d, int32_t keep, int32_t first, int32_t last, void *k_out,
+                              void *v_out, float *weights_out, int32_t *rows_out,
+                              int32_t *out_starts, int32_t *out_lens, sattn_dtype dtype,
+                              void *cuda_stream) {
+    if (B < 0 || S < 0 || Hkv <= 0 || (d != 64 && d != 128) || keep < 1 || first < 0 || last < 0 ||
+        (int64_t)first + last > keep || !valid_dtype(dtype))
+        return SATTN_ERR_INVALID_ARG;
+    if (B > 0 && ((int64_t)B * keep > INT32_MAX || (int64_t)B * keep * Hkv > INT32_MAX))
+        return SATTN_ERR_INVALID_ARG;
+    const int64_t unit = dtype == SATTN_BF16 ? 8 : 4;
+    if (!valid_rows(k_stride, Hkv, d, unit) || !valid_rows(v_stride, Hkv, d, unit))
+        return SATTN_ERR_INVALID_ARG;
+    if (B == 0) return SATTN_OK;
+    if ((S > 0 && (!k || !v || !weights)) || !kv_starts || !kv_lens || !k_out || !v_out ||
+        !weights_out || !rows_out || !out_starts || !out_lens)
+        return SATTN_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_out) || !aligned16(v_out) || k_out == k ||
+        v_out == v || k_out == v || v_out == k || k_out == v_out || weights_out == weights ||
+        out_starts == kv_starts || out_lens == kv_lens)
+        return SATTN_ERR_INVALID_ARG;
+    cudaError_t e;
+    const DevInfo *dev = device_info(&e);
+    if (!dev) return SATTN_ERR_CUDA;
+    if (sattn_status st = check_arch(dev)) return st;
+    cudaStream_t s = as_stream(cuda_stream);
+    EvictArgs a{k, v, k_stride, v_stride, weights, kv_starts, kv_lens, B, S, Hkv, d,
+                dtype == SATTN_BF16 ? 2 : 4, keep, first, last, k_out, v_out, weights_out,
+                rows_out, out_starts, out_lens};
+    return finish(launch_evict(a, *dev, s), s);
 }
 
 sattn_status sattn_compress_kv(const void *kv, const void *score, const float *ape, void *out,

@@ -157,6 +157,64 @@ struct PagedArgs {
     int dtype;
 };
 
+// Rotary positions with several axes (strides in elements, between tokens); k may be nullptr.
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const int32_t *positions;  // [axes, T]
+    const float *inv_freq;     // [rd / 2]
+    const uint8_t *axis;       // [rd / 2]
+    int axes, T, H, Hkv, d, rd, interleaved, inverse;
+    int dtype;
+};
+
+// Attention to encoder states: q [T, H, d], k and v [S, Hkv, d] (strides between tokens).
+struct CrossArgs {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *cu_seqlens, *kv_starts, *kv_lens;
+    int B, T, S, max_q_len, H, Hkv, d;
+    const float *sinks;
+    int sink_mode;
+    float scale;
+    void *o;
+    float *lse;
+    void *workspace;
+    size_t workspace_bytes;
+    int dtype;
+};
+
+// What each state's key receives of that attention: weights [Hkv, S].
+struct KeyWeightArgs {
+    const void *q, *k;
+    int64_t q_stride, k_stride;
+    const float *lse;
+    const int32_t *cu_seqlens, *kv_starts, *kv_lens;
+    int B, T, S, max_q_len, H, Hkv, d;
+    const float *sinks;
+    int sink_mode;
+    float scale;
+    float *weights;
+    int accumulate;
+    void *workspace;
+    size_t workspace_bytes;
+    int dtype;
+};
+
+// The `keep` rows of each sequence and KV head that stay.
+struct EvictArgs {
+    const void *k, *v;
+    int64_t k_stride, v_stride;
+    const float *weights;  // [Hkv, S]
+    const int32_t *kv_starts, *kv_lens;
+    int B, S, Hkv, d, elem, keep, first, last;
+    void *k_out, *v_out;   // [B * keep, Hkv, d]
+    float *weights_out;    // [Hkv, B * keep]
+    int32_t *rows_out;     // [Hkv, B * keep]
+    int32_t *out_starts, *out_lens;
+};
+
 // SIMT kernels: any dtype, d in {64, 128}.
 cudaError_t launch_window_simt(const WindowArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_sparse_simt(const SparseArgs &a, const DevInfo &dev, cudaStream_t s);
@@ -175,6 +233,10 @@ cudaError_t launch_paged_prefill(const PagedArgs &a, const DevInfo &dev, cudaStr
 size_t paged_prefill_workspace(int d);
 // fp32 queries.
 cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
+cudaError_t launch_rope_axes(const RopeArgs &a, const DevInfo &dev, cudaStream_t s);
+cudaError_t launch_cross_simt(const CrossArgs &a, const DevInfo &dev, cudaStream_t s);
+cudaError_t launch_weights_simt(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_stats(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_block_sum(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);
