@@ -645,7 +645,8 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
 }
 
 size_t sattn_cross_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d) {
-    return 0;
+    if (max_q_len <= 0 || H <= 0 || Hkv <= 0 || H % Hkv != 0 || (d != 64 && d != 128)) return 0;
+    return cross_tc_workspace(max_q_len, H / Hkv, d);
 }
 
 sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -677,7 +678,10 @@ sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int
     CrossArgs a{q, k, v, q_stride, k_stride, v_stride, cu_seqlens, kv_starts, kv_lens, B, T, S,
                 max_q_len, H, Hkv, d, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
                 (int)sink_mode, scale, o, lse, workspace, workspace_bytes, (int)dtype};
-    return finish(launch_cross_simt(a, *dev, s), s);
+    // (a tensor map needs a row)
+    return finish(dtype == SATTN_F32 || S == 0 ? launch_cross_simt(a, *dev, s)
+                                               : launch_cross_tc(a, *dev, s),
+                  s);
 }
 
 size_t sattn_cross_key_weights_workspace_bytes(void) { return 0; }

@@ -235,6 +235,9 @@ size_t paged_prefill_workspace(int d);
 cudaError_t launch_paged_simt(const PagedArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_rope_axes(const RopeArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_cross_simt(const CrossArgs &a, const DevInfo &dev, cudaStream_t s);
+// bf16; H / Hkv <= 128, S > 0; and its workspace (G = H / Hkv).
+cudaError_t launch_cross_tc(const CrossArgs &a, const DevInfo &dev, cudaStream_t s);
+size_t cross_tc_workspace(int max_q_len, int G, int d);
 cudaError_t launch_weights_simt(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_evict(const EvictArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);

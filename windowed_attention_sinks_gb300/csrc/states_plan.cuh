@@ -1,0 +1,237 @@
+// How the tensor-core kernels over encoder states share out their work.
+//
+// A unit is a tile of one sequence and KV head with all that it meets: a tile of query rows
+// with its steps over 128-key tiles (the attention), or a tile of 128 keys with its steps
+// over the query rows (KEYS: the key weights). Units are numbered sequence by sequence, KV
+// head by KV head; their steps in a row, and before each unit's steps `extra` for what a
+// unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
+// piece may begin and end inside a unit: a ragged batch then keeps every SM busy for the
+// same time, whatever its lengths, and a few units spread over all SMs. The
+// pieces of a unit that is cut leave partial results in the workspace, which a second
+// launch joins in a fixed order. Everything is computed from the lengths on the device, so a
+// call needs no host copy of them and can be captured and replayed with other lengths.
+#pragma once
+
+#include "internal.h"
+#include "paged_mma.cuh"
+#include "states.cuh"
+
+namespace sattn {
+
+constexpr int STATE_KEYS = 128;  // keys a tile
+
+struct LineArgs {
+    const int32_t *cu, *starts, *lens;
+    int B, T, S, Hkv;
+    int tokens;  // of a tile of query rows
+    int extra;   // a unit's own cost, in steps
+    int split;   // 0: no workspace, pieces end at unit boundaries
+};
+
+struct LineUnit {
+    StateSeq s;
+    int b, h, u, nu;     // sequence, KV head, unit of its nu
+    int steps;           // at least one (an empty one's is masked)
+    int begin, end;      // the steps of this piece, 0 .. steps
+    __device__ __forceinline__ bool cut() const { return begin > 0 || end < steps; }
+};
+
+// Sequence b's units; false if it has none.
+template <bool KEYS>
+__device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, bool &bad) {
+    u.b = b;
+    bad = !load_states(a.cu, a.starts, a.lens, b, a.T, a.S, u.s);
+    if (bad) return false;
+    const int keys = (int)(((long long)u.s.len + STATE_KEYS - 1) / STATE_KEYS);
+    const int rows = (int)(((long long)u.s.n + a.tokens - 1) / a.tokens);
+    u.nu = KEYS ? keys : rows;
+    u.steps = max(1, KEYS ? rows : keys);
+    return u.nu > 0;
+}
+
+// What a CTA starts from (in shared memory).
+struct LineStart {
+    long long x0, x1, total, ustart;  // its piece of the line; where the unit that holds x0 starts
+    long long warps[32];
+    int pieces, b, h, u;
+};
+
+__device__ __forceinline__ long long line_cut(long long total, int c, int pieces) {
+    return total * c / pieces;
+}
+
+// Called by the whole CTA (a whole number of warps, 1024 threads at most); ends with a barrier.
+template <bool KEYS>
+__device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, const DevCtx &ctx) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;  // sequences a thread
+    const int b0 = (int)min((long long)a.B, (long long)tid * per), b1 = min(a.B, b0 + per);
+    LineUnit u;
+    long long mine = 0;
+    bool bad = false;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        bool wrong;
+        if (line_seq<KEYS>(a, b, u, wrong)) mine += (long long)a.Hkv * u.nu * (u.steps + a.extra);
+        bad |= wrong;
+    }
+    if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+    long long inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) ls.warps[warp] = inc;
+    __syncthreads();
+    long long before = inc - mine, total = 0;
+    for (int w = 0; w < nw; ++w) {
+        const long long v = ls.warps[w];
+        if (w < warp) before += v;
+        total += v;
+    }
+    const int pieces = (int)min((long long)gridDim.x, max(1ll, total));
+    const int c = min((int)blockIdx.x, pieces);
+    const long long x0 = line_cut(total, c, pieces), x1 = line_cut(total, min(c + 1, pieces), pieces);
+    if (tid == 0) {
+        ls.x0 = x0;
+        ls.x1 = x1;
+        ls.total = total;
+        ls.pieces = pieces;
+        if (x0 >= x1 || total == 0) ls.b = ls.h = ls.u = 0, ls.ustart = 0;
+    }
+    if (x0 < x1 && x0 >= before && x0 < before + mine) {
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            bool wrong;
+            if (!line_seq<KEYS>(a, b, u, wrong)) continue;
+            const long long one = u.steps + a.extra, all = one * u.nu * a.Hkv;
+            if (x0 >= before + all) {
+                before += all;
+                continue;
+            }
+            const long long i = (x0 - before) / one;  // unit of the sequence
+            ls.b = b;
+            ls.h = (int)(i / u.nu);
+            ls.u = (int)(i % u.nu);
+            ls.ustart = before + i * one;
+            break;
+        }
+    }
+    __syncthreads();
+}
+
+// Walks the units of a CTA's piece.
+template <bool KEYS> struct LineIter {
+    LineUnit u;
+    long long ustart, x1;  // where u starts on the line
+    bool live;
+
+    __device__ __forceinline__ LineIter(const LineArgs &a, const LineStart &ls) {
+        x1 = ls.x1;
+        live = ls.x0 < x1;
+        if (!live) return;
+        bool bad;
+        live = line_seq<KEYS>(a, ls.b, u, bad);
+        u.h = ls.h;
+        u.u = ls.u;
+        ustart = ls.ustart;
+        u.begin = (int)max(0ll, ls.x0 - ustart - a.extra);
+        // uncut, the unit is all of the piece's that its first step lies in
+        if (!a.split && u.begin > 0) u.begin = u.steps;
+        clip(a);
+    }
+    // The steps of u in this piece (there may be none of the first unit).
+    __device__ __forceinline__ void clip(const LineArgs &a) {
+        const long long t0 = ustart + a.extra;
+        live = live && t0 + u.begin < x1;
+        u.end = a.split ? (int)min((long long)u.steps, x1 - t0) : u.steps;
+    }
+    // To the next unit of the line; there may be none behind this piece.
+    __device__ __forceinline__ void next(const LineArgs &a) {
+        live = u.end == u.steps;
+        if (!live) return;
+        ustart += u.steps + a.extra;
+        if (++u.u == u.nu) {
+            u.u = 0;
+            if (++u.h == a.Hkv) {
+                u.h = 0;
+                int b = u.b + 1;
+                bool bad;
+#pragma unroll 1
+                while (b < a.B && !line_seq<KEYS>(a, b, u, bad)) ++b;
+                if (b >= a.B) {
+                    live = false;
+                    return;
+                }
+            }
+        }
+        u.begin = 0;
+        clip(a);
+    }
+};
+
+// The units in shared memory: the loading warp walks them and hands them on, the
+// other roles read what they need. A unit without steps ends the piece.
+template <int N> struct LineRing {
+    LineUnit u[N];
+    uint64_t full[N], empty[N];
+
+    __device__ __forceinline__ void init(int readers, int lane) {  // a warp
+        if (lane < N) {
+            mbar_init(smem_u32(&full[lane]), 1);
+            mbar_init(smem_u32(&empty[lane]), readers);
+        }
+    }
+    // One thread: unit number i.
+    __device__ __forceinline__ bool put(int i, const LineUnit &x, const DevCtx &ctx,
+                                        volatile int *abort) {
+        if (i >= N && !bar_wait(smem_u32(&empty[i % N]), (i / N - 1) & 1, ctx, abort)) return false;
+        u[i % N] = x;
+        mbar_arrive(smem_u32(&full[i % N]));
+        return true;
+    }
+    __device__ __forceinline__ bool wait(int i, const DevCtx &ctx, volatile int *abort) {
+        return bar_wait(smem_u32(&full[i % N]), (i / N) & 1, ctx, abort);
+    }
+    __device__ __forceinline__ void release(int i) { mbar_arrive(smem_u32(&empty[i % N])); }
+};
+
+// A count in shared memory that one thread raises and others wait for.
+__device__ __forceinline__ void count_set(uint32_t at, int v) {
+    asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+__device__ __forceinline__ int count_get(uint32_t at) {
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+// Waits until the count is at least n, as bar_wait waits for a phase.
+__device__ __forceinline__ bool count_wait(uint32_t at, int n, const DevCtx &ctx,
+                                           volatile int *abort) {
+    if (count_get(at) >= n) return true;
+    const uint32_t limit = (uint32_t)min(ctx.wait_ns, (uint64_t)4000000000u);
+    uint32_t t0, t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t0));
+#pragma unroll 1
+    do {
+        if (count_get(at) >= n) return true;
+        if (*abort) return false;
+        asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    } while (t - t0 <= limit);
+    *abort = TIMED_OUT;
+    return false;
+}
+
+// Rows of heads x d elements, `stride` elements apart, as boxes of 64 columns, `heads_box`
+// heads and `rows_box` rows.
+inline bool map_rows(CUtensorMap *m, const void *p, int64_t stride, int heads, int d, int rows,
+                     int heads_box, int rows_box) {
+    const uint64_t dims[3] = {(uint64_t)d, (uint64_t)heads, (uint64_t)rows};
+    const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)heads_box, (uint32_t)rows_box};
+    return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims,
+                             strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+}
+
+}  // namespace sattn
