@@ -684,7 +684,7 @@ sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int
                   s);
 }
 
-size_t sattn_cross_key_weights_workspace_bytes(void) { return 0; }
+size_t sattn_cross_key_weights_workspace_bytes(void) { return weights_tc_workspace(); }
 
 sattn_status sattn_cross_key_weights(const void *q, int64_t q_stride, const void *k,
                                      int64_t k_stride, const float *lse,
@@ -718,7 +718,9 @@ sattn_status sattn_cross_key_weights(const void *q, int64_t q_stride, const void
                     max_q_len, H, Hkv, d, sink_mode == SATTN_SINK_NONE ? nullptr : sinks,
                     (int)sink_mode, scale, weights, accumulate, workspace, workspace_bytes,
                     (int)dtype};
-    return finish(launch_weights_simt(a, *dev, s), s);
+    return finish(dtype == SATTN_F32 || T == 0 ? launch_weights_simt(a, *dev, s)
+                                               : launch_weights_tc(a, *dev, s),
+                  s);
 }
 
 sattn_status sattn_evict_keys(const void *k, int64_t k_stride, const void *v, int64_t v_stride,

@@ -239,6 +239,9 @@ cudaError_t launch_cross_simt(const CrossArgs &a, const DevInfo &dev, cudaStream
 cudaError_t launch_cross_tc(const CrossArgs &a, const DevInfo &dev, cudaStream_t s);
 size_t cross_tc_workspace(int max_q_len, int G, int d);
 cudaError_t launch_weights_simt(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s);
+// bf16; H / Hkv <= 128, S > 0, T > 0.
+cudaError_t launch_weights_tc(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s);
+size_t weights_tc_workspace();
 cudaError_t launch_evict(const EvictArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_compress_kv(const CompressArgs &a, const DevInfo &dev, cudaStream_t s);
 cudaError_t launch_xattn_stats(const XattnArgs &a, const DevInfo &dev, cudaStream_t s);

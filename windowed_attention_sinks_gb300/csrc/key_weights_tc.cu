@@ -1,0 +1,440 @@
+// Key weights of cross attention on the tensor cores (tcgen05), bf16.
+//
+// What a key receives is a sum over query rows, so the products are taken the other way round,
+// S^T = K Q^T: keys are the 128 rows of an MMA, a thread each, query rows its columns, and
+//   w += sum over columns of 2^(S^T scale log2(e) - lse log2(e))
+// stays in the thread: no sum across threads, no order that changes. Query rows are tokens
+// times the heads of a KV group, fetched as boxes of G heads and floor(N / G) tokens.
+//
+// A unit is 256 keys of a sequence and KV head, two tiles of 128, a group of warps each; a
+// step is a tile of N query rows, which both tiles use (a query tile comes from L2, and one
+// for 128 keys alone would take all of its bandwidth). N is 32, 64 or 128, by the rows that a
+// sequence has: single tokens then read the keys and next to nothing else.
+// One persistent CTA per SM over an equal piece of the line of units (states_plan.cuh);
+// the sums of a unit that is cut go to the workspace and are added up by a second launch.
+// Roles: warp 0 units and TMA; 1, 2 the products of the groups; 4-7, 8-11 the groups' sums.
+#include <math.h>
+#include <stdio.h>
+
+#include "paged_plan.cuh"
+#include "states_plan.cuh"
+
+namespace sattn {
+namespace {
+
+constexpr int NTHREADS = 384;
+constexpr int SUMS = 4;    // first warp of the sums
+constexpr int UNITS = 4;   // units handed on ahead
+constexpr int UNIT_KEYS = 2 * STATE_KEYS;
+constexpr uint32_t TMEM_COLS = 512;  // two groups, two buffers of 128 columns each
+
+struct WeightParams {
+    LineArgs line;
+    int H, G, rows;    // rows: of a query tile that hold tokens
+    uint32_t n;        // and columns of its product
+    const float *lse;
+    float scale_l2;
+    const float *sinks;  // of key 0, or nullptr
+    float *weights;
+    int accumulate;
+    uint8_t *ws;
+    uint32_t g_mul, g_shift;
+
+    // row / G for 0 <= row < 2^31 (as PlanArgs::token)
+    __device__ __forceinline__ int token(int row) const {
+        return (int)((__umulhi(g_mul, (uint32_t)row) + (uint32_t)row) >> g_shift);
+    }
+};
+
+template <int D> struct alignas(1024) Smem {
+    static constexpr int NH = D / 64;            // 64-column parts of a row
+    static constexpr uint32_t PART = 128 * 128;  // 128 rows of 64 bf16
+    static constexpr uint32_t TILE_BYTES = NH * PART;
+    static constexpr int KR = D == 128 ? 2 : 4;  // key tiles a group
+    static constexpr int QR = D == 128 ? 3 : 6;  // query tiles
+    uint8_t k[2][KR][TILE_BYTES];
+    uint8_t q[QR][TILE_BYTES];
+    float lse[2][2][128];  // group, step's parity: -lse log2(e), -inf where a row does not count
+    LineStart line;
+    LineRing<UNITS> units;
+    uint64_t k_full[2][KR], k_empty[2][KR], q_full[QR], q_empty[QR];
+    uint64_t s_full[2][2], s_empty[2][2], lse_full[2][2], drain[2];
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Workspace: PlanNote [pieces], sums [pieces][2][UNIT_KEYS] (part 0 of a piece is its first
+// unit if that began earlier, part 1 its last unit if that begins here and goes on). In a note
+// t0 is the unit's first row of the states, nrows its keys.
+constexpr size_t SUMS_OFFSET = MAX_PIECES * sizeof(PlanNote);
+constexpr size_t WORKSPACE = SUMS_OFFSET + (size_t)MAX_PIECES * 2 * UNIT_KEYS * sizeof(float);
+
+// Keys of the unit's tile g.
+__device__ __forceinline__ int keys_of(const LineUnit &u, int g) {
+    return min(STATE_KEYS, u.s.len - u.u * UNIT_KEYS - g * STATE_KEYS);
+}
+
+template <int D>
+__device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const CUtensorMap *tk,
+                           Smem<D> &sm, const DevCtx &ctx) {
+    using S = Smem<D>;
+    if ((threadIdx.x & 31) != 0) return;
+    volatile int *abort = &sm.abort;
+    prefetch_tmap(tq);
+    prefetch_tmap(tk);
+    LineIter<true> it(p.line, sm.line);
+    if (p.line.split) {
+        PlanNote n{};
+        if (it.live) {
+            const LineUnit &u = it.u;
+            n.cont = u.begin > 0;
+            n.through = u.begin > 0 && u.end < u.steps;
+            n.t0 = u.s.s0 + u.u * UNIT_KEYS;
+            n.h = u.h;
+            n.nrows = min(UNIT_KEYS, u.s.len - u.u * UNIT_KEYS);
+        }
+        reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
+    }
+    int kt[2] = {0, 0}, qt = 0, index = 0;  // loads; units
+    bool ok = true;
+#pragma unroll 1
+    for (; it.live && ok; it.next(p.line)) {
+        const LineUnit &u = it.u;
+        if (u.begin == u.end) continue;
+        ok = sm.units.put(index++, u, ctx, abort);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            if (!ok || keys_of(u, g) <= 0) continue;
+            const int st = kt[g] % S::KR, use = kt[g] / S::KR;
+            if (use >= 1) ok = bar_wait(smem_u32(&sm.k_empty[g][st]), (use - 1) & 1, ctx, abort);
+            if (!ok) continue;
+            const uint32_t bar = smem_u32(&sm.k_full[g][st]);
+            mbar_arrive_expect_tx(bar, S::TILE_BYTES);
+#pragma unroll
+            for (int c = 0; c < S::NH; ++c)
+                tma_load_3d(smem_u32(sm.k[g][st]) + c * S::PART, tk, bar, 64 * c, u.h,
+                            u.s.s0 + u.u * UNIT_KEYS + g * STATE_KEYS);
+            ++kt[g];
+        }
+#pragma unroll 1
+        for (int j = u.begin; j < u.end && ok; ++j) {
+            const int st = qt % S::QR, use = qt / S::QR;
+            if (use >= 1) ok = bar_wait(smem_u32(&sm.q_empty[st]), (use - 1) & 1, ctx, abort);
+            if (!ok) break;
+            const uint32_t bar = smem_u32(&sm.q_full[st]);
+            mbar_arrive_expect_tx(bar, (uint32_t)(S::NH * p.rows * 128));
+#pragma unroll
+            for (int c = 0; c < S::NH; ++c)
+                tma_load_3d(smem_u32(sm.q[st]) + c * p.n * 128, tq, bar, 64 * c, u.h * p.G,
+                            u.s.t0 + j * p.line.tokens);
+            ++qt;
+        }
+    }
+    if (ok) {
+        LineUnit last{};
+        sm.units.put(index, last, ctx, abort);
+    }
+    int zero = 0;  // copies in flight land before the CTA leaves
+#pragma unroll 1
+    for (int st = 0; st < S::KR; ++st)
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if (st < kt[g])
+                bar_wait(smem_u32(&sm.k_full[g][st]), (kt[g] - 1 - st) / S::KR & 1, ctx, &zero);
+#pragma unroll 1
+    for (int st = 0; st < S::QR && st < qt; ++st)
+        bar_wait(smem_u32(&sm.q_full[st]), (qt - 1 - st) / S::QR & 1, ctx, &zero);
+}
+
+// The products of group g: one thread.
+template <int D>
+__device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int g, const DevCtx &ctx) {
+    using S = Smem<D>;
+    const uint32_t idesc = idesc_bf16_f32(128, p.n, 0, 0);
+    volatile int *abort = &sm.abort;
+    if (ctx.stall) bar_wait(smem_u32(&sm.drain[g]), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dk = desc_rows<128>(smem_u32(sm.k[g][0]));
+    const uint64_t dq = desc_rows<128>(smem_u32(sm.q[0]));
+    auto wait = [&](uint64_t &bar, int phase) {
+        return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
+    };
+    int kt = 0, qt = 0, x = 0;  // loads of keys and queries; this group's steps
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        const LineUnit &u = sm.units.u[i % UNITS];
+        const int n = u.end - u.begin;
+        const bool mine = keys_of(u, g) > 0;
+        sm.units.release(i);
+        if (n == 0) break;
+        const int ks = kt % S::KR;
+        if (mine) ok = wait(sm.k_full[g][ks], kt / S::KR);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j, ++qt) {
+            const int st = qt % S::QR;
+            ok = wait(sm.q_full[st], qt / S::QR);
+            if (!mine) {
+                if (ok) mbar_arrive(smem_u32(&sm.q_empty[st]));
+                continue;
+            }
+            const int b = x & 1;
+            if (x >= 2) ok = ok && wait(sm.s_empty[g][b], (x >> 1) - 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = dk + (uint64_t)(ks * (S::TILE_BYTES >> 4));
+            const uint64_t qd = dq + (uint64_t)(st * (S::TILE_BYTES >> 4));
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk)
+                tc_mma_f16(tmem + (uint32_t)((2 * g + b) * 128),
+                           kd + (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3)),
+                           qd + (uint64_t)((kk >> 2) * (p.n * 128 >> 4) + 2 * (kk & 3)), idesc,
+                           kk > 0);
+            tc_commit(smem_u32(&sm.s_full[g][b]));
+            tc_commit(smem_u32(&sm.q_empty[st]));
+            ++x;
+        }
+        if (mine) {
+            tc_commit(smem_u32(&sm.k_empty[g][ks]));
+            ++kt;
+        }
+    }
+    tc_commit(smem_u32(&sm.drain[g]));  // every MMA is done before TMEM goes
+    int zero = 0;
+    bar_wait(smem_u32(&sm.drain[g]), 0, ctx, &zero);
+}
+
+template <int D>
+__device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, const DevCtx &ctx) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = (warp - SUMS) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+    const uint32_t tmem = tmem_base + (uint32_t)(2 * g * 128) + ((uint32_t)(quarter * 32) << 16);
+    volatile int *abort = &sm.abort;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
+    };
+    const int tok = p.token(r), head = r - tok * p.G;  // of query row r
+    const float sx = p.scale_l2;
+    int x = 0;  // this group's steps
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
+        const LineUnit u = sm.units.u[i % UNITS];
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
+        if (u.begin == u.end) return;
+        const int keys = keys_of(u, g);
+        if (keys <= 0) continue;
+        const bool first = p.sinks && u.u == 0 && g == 0 && quarter == 0;  // lane 0 has key 0
+        const size_t at = (size_t)u.h * p.line.S + u.s.s0 + u.u * UNIT_KEYS + g * STATE_KEYS + r;
+        float old = 0.f;
+        if (p.accumulate && !u.cut() && r < keys) old = p.weights[at];
+        // -lse log2(e) of query row r of step j
+        auto row = [&](int j) -> float {
+            const int t = j * p.line.tokens + tok;
+            if (r >= p.rows || t >= u.s.n) return INFINITY;
+            return __ldg(p.lse + (size_t)(u.s.t0 + t) * p.H + u.h * p.G + head);
+        };
+        float next = row(u.begin), w = 0.f;
+#pragma unroll 1
+        for (int j = u.begin; j < u.end; ++j, ++x) {
+            const int b = x & 1;
+            sm.lse[g][b][r] = isinf(next) ? -INFINITY : -next * LOG2E;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.lse_full[g][b]));
+            if (j + 1 < u.end) next = row(j + 1);
+            if (!wait(sm.lse_full[g][b], x >> 1)) return;
+            if (!wait(sm.s_full[g][b], x >> 1)) return;
+            tc_fence_after();
+            const int cols = min(p.line.tokens, u.s.n - j * p.line.tokens) * p.G;
+            float sum = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+                uint32_t xs[32];
+                tmem_ld32(tmem + (uint32_t)(b * 128 + c), xs);
+                tc_wait_ld();
+                const float4 *ls = reinterpret_cast<const float4 *>(sm.lse[g][b] + c);
+                if (cols - c < 32) {  // columns of no row may hold anything
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) hide_unless(xs[e], e < cols - c);
+                }
+                if (first) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int q = c + e, h = q - p.token(q) * p.G;
+                        const float s = lane == 0 ? sink_log2(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
+                        const float y = fmaf(__uint_as_float(xs[e]), sx, sm.lse[g][b][q]);
+                        sum += ex2(y == -INFINITY ? y : y + s);  // (whatever the sink)
+                    }
+                    continue;
+                }
+                uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+                const uint64_t f2 = f2_pack(sx, sx);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                    const float4 l = ls[e >> 2];
+                    float a0, a1, a2, a3;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1])), f2,
+                                     f2_pack(l.x, l.y)), a0, a1);
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e + 2]), __uint_as_float(xs[e + 3])),
+                                     f2, f2_pack(l.z, l.w)), a2, a3);
+                    part[0] = f2_add(part[0], f2_pack(ex2(a0), ex2(a1)));
+                    part[1] = f2_add(part[1], f2_pack(ex2(a2), ex2(a3)));
+                }
+                float a0, a1;
+                f2_unpack(f2_add(part[0], part[1]), a0, a1);
+                sum += a0 + a1;
+            }
+            w += sum;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[g][b]));
+        }
+        if (u.cut()) {
+            float *part = reinterpret_cast<float *>(p.ws + SUMS_OFFSET) +
+                          ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * UNIT_KEYS;
+            part[g * STATE_KEYS + r] = w;
+        } else if (r < keys) {
+            p.weights[at] = old + w;
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1)
+weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
+               const __grid_constant__ WeightParams p, const __grid_constant__ DevCtx ctx) {
+    extern __shared__ __align__(1024) uint8_t dsmem[];
+    using S = Smem<D>;
+    S &sm = *reinterpret_cast<S *>(dsmem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
+        if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
+        return;
+    }
+    if (warp == 2) {  // a lane a barrier
+        if (lane < 2) {
+#pragma unroll
+            for (int i = 0; i < S::KR; ++i) {
+                mbar_init(smem_u32(&sm.k_full[lane][i]), 1);
+                mbar_init(smem_u32(&sm.k_empty[lane][i]), 1);
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
+                mbar_init(smem_u32(&sm.s_empty[lane][b]), 4);
+                mbar_init(smem_u32(&sm.lse_full[lane][b]), 4);
+            }
+            mbar_init(smem_u32(&sm.drain[lane]), 1);
+        }
+        if (lane < S::QR) {
+            mbar_init(smem_u32(&sm.q_full[lane]), 1);
+            mbar_init(smem_u32(&sm.q_empty[lane]), 2);
+        }
+        if (lane == 0) sm.abort = 0;
+        sm.units.init(2 + 8, lane);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
+        tmem_relinquish();
+    }
+    line_start<true>(p.line, sm.line, ctx);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    if (warp == 0) {
+        load_tiles<D>(p, &tq, &tk, sm, ctx);
+        __syncwarp();
+    } else if (warp < 3) {
+        if (lane == 0) issue<D>(p, sm, tmem, warp - 1, ctx);
+        __syncwarp();
+    } else if (warp >= SUMS) {
+        sum_up<D>(p, sm, tmem, ctx);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+}
+
+// Adds up the sums of units that were cut, in the order of their pieces: block i takes the unit
+// that the boundary behind piece i cuts, if that is the first inside the unit.
+__global__ void __launch_bounds__(UNIT_KEYS)
+add_kernel(const uint8_t *ws, int pieces, int S, float *weights, int accumulate) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PlanNote *notes = reinterpret_cast<const PlanNote *>(ws);
+    const float *sums = reinterpret_cast<const float *>(ws + SUMS_OFFSET);
+    const int c = blockIdx.x + 1, key = threadIdx.x;
+    const PlanNote me = notes[c], prev = notes[c - 1];
+    if (!me.cont || key >= me.nrows || (prev.cont && prev.through)) return;
+    float w = sums[((size_t)(c - 1) * 2 + 1) * UNIT_KEYS + key] + sums[(size_t)c * 2 * UNIT_KEYS + key];
+    bool on = me.through;
+    for (int i = c + 1; on && i < pieces; ++i) {
+        w += sums[(size_t)i * 2 * UNIT_KEYS + key];
+        on = notes[i].through;
+    }
+    float *at = weights + (size_t)me.h * S + me.t0 + key;
+    *at = accumulate ? *at + w : w;
+}
+
+template <int D>
+cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
+    const int G = a.H / a.Hkv, n = max(1, a.max_q_len);
+    const long long need = (long long)n * G;
+    WeightParams p{};
+    p.H = a.H;
+    p.G = G;
+    p.n = need <= 32 ? 32 : need <= 64 ? 64 : 128;
+    const int tokens = min((int)p.n / G, n);
+    p.rows = tokens * G;
+    p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 1,
+                      a.workspace && a.workspace_bytes >= WORKSPACE};
+    p.lse = a.lse;
+    p.scale_l2 = a.scale * LOG2E;
+    p.sinks = a.sink_mode == 1 ? a.sinks : nullptr;
+    p.weights = a.weights;
+    p.accumulate = a.accumulate;
+    p.ws = static_cast<uint8_t *>(a.workspace);
+    const uint32_t g = (uint32_t)G;
+    while ((1ull << p.g_shift) < g) ++p.g_shift;
+    p.g_mul = (uint32_t)((((1ull << p.g_shift) - g) << 32) / g + 1);
+    CUtensorMap tq, tk;
+    if (!map_rows(&tq, a.q, a.q_stride, a.H, D, a.T, G, tokens) ||
+        !map_rows(&tk, a.k, a.k_stride, a.Hkv, D, a.S, 1, STATE_KEYS))
+        return cudaErrorInvalidValue;
+    static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of one CTA");
+    cudaError_t e = ensure_smem_attr((const void *)weights_kernel<D>, sizeof(Smem<D>), dev);
+    if (e != cudaSuccess) return e;
+    const int grid = min(dev.sm_count, MAX_PIECES);
+    if (verbose())
+        fprintf(stderr, "sattn: weights_kernel<%d> grid=%d n=%u rows=%d split=%d\n", D, grid, p.n,
+                p.rows, p.line.split);
+    weights_kernel<D><<<grid, NTHREADS, sizeof(Smem<D>), s>>>(tq, tk, p, make_ctx(dev));
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !p.line.split || grid < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(grid - 1));
+    cfg.blockDim = dim3(UNIT_KEYS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, add_kernel, static_cast<const uint8_t *>(p.ws), grid, a.S,
+                              a.weights, a.accumulate);
+}
+
+}  // namespace
+
+size_t weights_tc_workspace() { return WORKSPACE; }
+
+cudaError_t launch_weights_tc(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
+    return a.d == 64 ? launch<64>(a, dev, s) : launch<128>(a, dev, s);
+}
+
+}  // namespace sattn

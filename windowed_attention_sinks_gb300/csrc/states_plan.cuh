@@ -1,8 +1,8 @@
 // How the tensor-core kernels over encoder states share out their work.
 //
 // A unit is a tile of one sequence and KV head with all that it meets: a tile of query rows
-// with its steps over 128-key tiles (the attention), or a tile of 128 keys with its steps
-// over the query rows (KEYS: the key weights). Units are numbered sequence by sequence, KV
+// with its steps over 128-key tiles (the attention), or 256 keys with their steps over tiles
+// of query rows (KEYS: the key weights). Units are numbered sequence by sequence, KV
 // head by KV head; their steps in a row, and before each unit's steps `extra` for what a
 // unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
 // piece may begin and end inside a unit: a ragged batch then keeps every SM busy for the
@@ -18,7 +18,7 @@
 
 namespace sattn {
 
-constexpr int STATE_KEYS = 128;  // keys a tile
+constexpr int STATE_KEYS = 128;  // keys a tile; a unit of keys has two
 
 struct LineArgs {
     const int32_t *cu, *starts, *lens;
@@ -42,7 +42,8 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
     u.b = b;
     bad = !load_states(a.cu, a.starts, a.lens, b, a.T, a.S, u.s);
     if (bad) return false;
-    const int keys = (int)(((long long)u.s.len + STATE_KEYS - 1) / STATE_KEYS);
+    constexpr int TILE_KEYS = KEYS ? 2 * STATE_KEYS : STATE_KEYS;
+    const int keys = (int)(((long long)u.s.len + TILE_KEYS - 1) / TILE_KEYS);
     const int rows = (int)(((long long)u.s.n + a.tokens - 1) / a.tokens);
     u.nu = KEYS ? keys : rows;
     u.steps = max(1, KEYS ? rows : keys);
