@@ -74,7 +74,8 @@ template <int D> struct alignas(1024) Smem {
     uint64_t q_full, q_empty, mg_full, mg_empty;
     uint64_t s_full[2], s_free[2], p_full[2][2], p0_done[2], o_full[2], o_empty[2], drain[4];
     uint32_t tmem_base;
-    int issued;  // loads into the ring so far
+    int issued;    // loads into the ring so far
+    int s_issued[2];  // S of units that both halves work on, so far
     int abort;
 };
 
@@ -221,10 +222,10 @@ __device__ __forceinline__ bool landed(Smem<D> &sm, int t, const DevCtx &ctx, vo
            bar_wait(smem_u32(&sm.full[st]), use & 1, ctx, abort);
 }
 
-// S of one half, a tile at a time, when P V of the half's tile before has read its P.
+// S of one half, a tile at a time, when P V of the half's tile before has read its P. A warp.
 template <int D, bool FEW>
 __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int half,
-                                        const DevCtx &ctx) {
+                        const DevCtx &ctx) {
     using S = Smem<D>;
     constexpr uint32_t IDESC = idesc_bf16_f32(128, STATE_KEYS, 0, 0);
     volatile int *abort = &sm.abort;
@@ -235,53 +236,62 @@ __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int ha
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    int x = 0, t0 = 0;  // this half's tiles; loads before the unit
+    int x = 0, y = 0, t0 = 0;  // this half's tiles; of both halves; loads before the unit
     bool ok = true;
     for (int i = 0; ok; ++i) {
-        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
         const LineUnit &u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
-        const bool none = !FEW && half && u.s.n - u.u * p.line.tokens <= p.tokens;
-        sm.units.release(i);
+        const bool both = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
+        const bool none = !FEW && half && !both;
+        __syncwarp();
+        if (elect_one()) sm.units.release(i);
         if (n == 0) break;
         if (none) {  // no rows in this half: its share in freeing the ring
             for (int j = 0; j < n && ok; ++j) {
                 const int t = t0 + 2 * j;
-                ok = landed(sm, t, ctx, abort);
-                mbar_arrive(smem_u32(&sm.empty[t % S::R]));
+                ok = __all_sync(0xffffffffu, landed(sm, t, ctx, abort));
+                if (elect_one()) mbar_arrive(smem_u32(&sm.empty[t % S::R]));
             }
         }
-        ok = ok && wait(sm.q_full, i);  // (also where it is not used: no phase is passed over)
-        if (none || (FEW && half >= n)) mbar_arrive(smem_u32(&sm.q_empty));
+        // (also where it is not used: no phase is passed over)
+        ok = __all_sync(0xffffffffu, ok && wait(sm.q_full, i));
+        if (none || (FEW && half >= n))
+            if (elect_one()) mbar_arrive(smem_u32(&sm.q_empty));
         const int step = FEW ? 2 : 1;
 #pragma unroll 1
         for (int j = FEW ? half : 0; j < n && ok && !none; j += step, ++x) {
             const int t = t0 + 2 * j, st = t % S::R;
             ok = landed(sm, t, ctx, abort);
             if (x >= 1) ok = ok && wait(sm.s_free[half], x - 1);
-            if (!ok) break;
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(st * (S::TILE_BYTES >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t at = (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3));
-                tc_mma_f16(cols, dq + at, kd + at, IDESC, kk > 0);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t at = (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3));
+                    tc_mma_f16(cols, dq + at, kd + at, IDESC, kk > 0);
+                }
+                if (both) count_set(smem_u32(&sm.s_issued[half]), y + 1);
+                tc_commit(smem_u32(&sm.s_full[half]));
+                tc_commit(smem_u32(&sm.empty[st]));
+                if (j + step >= n) tc_commit(smem_u32(&sm.q_empty));
             }
-            tc_commit(smem_u32(&sm.s_full[half]));
-            tc_commit(smem_u32(&sm.empty[st]));
-            if (j + step >= n) tc_commit(smem_u32(&sm.q_empty));
+            y += both;
         }
         t0 += 2 * n;
     }
-    tc_commit(smem_u32(&sm.drain[half]));  // every MMA is done before TMEM goes
+    __syncwarp();
+    if (elect_one()) tc_commit(smem_u32(&sm.drain[half]));  // every MMA is done before TMEM goes
     int zero = 0;
     bar_wait(smem_u32(&sm.drain[half]), 0, ctx, &zero);
 }
 
-// P V of one half, 64 keys at a time.
+// P V of one half, 64 keys at a time. A warp.
 template <int D, bool FEW>
 __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int half,
-                                         const DevCtx &ctx) {
+                         const DevCtx &ctx) {
     using S = Smem<D>;
     constexpr uint32_t IDESC = idesc_bf16_f32(128, D, 0, 1);
     volatile int *abort = &sm.abort;
@@ -290,20 +300,23 @@ __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int h
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    int x = 0, x1 = 0, t0 = 1, ec = 0;  // tiles; of two chunks; V loads before the unit; units
+    // tiles; of two chunks; of both halves; V loads before the unit; units
+    int x = 0, x1 = 0, y = 0, t0 = 1, ec = 0;
     bool ok = true;
     for (int i = 0; ok; ++i) {
-        if (!(ok = sm.units.wait(i, ctx, abort))) break;
+        if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
         const LineUnit u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
-        const bool none = !FEW && half && u.s.n - u.u * p.line.tokens <= p.tokens;
-        sm.units.release(i);
+        const bool both = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
+        const bool none = !FEW && half && !both;
+        __syncwarp();
+        if (elect_one()) sm.units.release(i);
         if (n == 0) break;
         if (none) {
             for (int j = 0; j < n && ok; ++j) {
                 const int t = t0 + 2 * j;
-                ok = landed(sm, t, ctx, abort);
-                mbar_arrive(smem_u32(&sm.empty[t % S::R]));
+                ok = __all_sync(0xffffffffu, landed(sm, t, ctx, abort));
+                if (elect_one()) mbar_arrive(smem_u32(&sm.empty[t % S::R]));
             }
         }
         const int first = FEW ? half : 0;
@@ -313,31 +326,42 @@ __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int h
             ok = landed(sm, t, ctx, abort);
             // the first P V overwrites the O that the last unit's epilogue reads
             if (j == first && ec >= 1) ok = ok && wait(sm.o_empty[half], ec - 1);
+            // The halves take turns, P V and the S behind it of one, then of the other: left to
+            // themselves they fall into step, both at their softmax while the products wait.
+            if (both) {
+                if (half == 0 || j + 1 < n)
+                    ok = ok && count_wait(smem_u32(&sm.s_issued[half ^ 1]), y + 1 + half, ctx, abort);
+                ++y;
+            }
             const uint64_t vd = dv + (uint64_t)(st * (S::TILE_BYTES >> 4));
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                if (c < nch && ok) ok = wait(sm.p_full[half][c], c ? x1++ : x);
-                if (c < nch && ok) {
-                    tc_fence_after();
+                if (c >= nch) break;
+                ok = ok && wait(sm.p_full[half][c], c ? x1++ : x);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < CHUNK / 16; ++kk)
                         tc_mma_f16_ts(cols + O_COL, cols + (uint32_t)(c * CHUNK + 8 * kk),
                                       vd + (uint64_t)((c * (CHUNK / 16) + kk) * (2048u >> 4)), IDESC,
                                       c > 0 || kk > 0 || j > first);
                     if (c == 0) tc_commit(smem_u32(&sm.p0_done[half]));
+                    if (c == nch - 1) {
+                        tc_commit(smem_u32(&sm.s_free[half]));
+                        tc_commit(smem_u32(&sm.empty[st]));
+                    }
                 }
             }
-            if (!ok) break;
-            tc_commit(smem_u32(&sm.s_free[half]));
-            tc_commit(smem_u32(&sm.empty[st]));
         }
         if (ok && !none && first < n) {
-            tc_commit(smem_u32(&sm.o_full[half]));
+            if (elect_one()) tc_commit(smem_u32(&sm.o_full[half]));
             ++ec;
         }
         t0 += 2 * n;
     }
-    tc_commit(smem_u32(&sm.drain[2 + half]));
+    __syncwarp();
+    if (elect_one()) tc_commit(smem_u32(&sm.drain[2 + half]));
     int zero = 0;
     bar_wait(smem_u32(&sm.drain[2 + half]), 0, ctx, &zero);
 }
@@ -617,7 +641,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm.mg_full), p.warps);
             mbar_init(smem_u32(&sm.mg_empty), p.warps);
             sm.abort = 0;
-            sm.issued = 0;
+            sm.issued = sm.s_issued[0] = sm.s_issued[1] = 0;
         }
         sm.units.init(4 + 1 + 2 * p.warps, lane);  // MMA issuers, tails, softmax
         fence_mbar_init();
@@ -645,9 +669,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         } else if (warp == 2) {
             clear_tails<D>(sm, ctx);
         } else if (warp < 4) {
-            if (lane == 0) issue_s<D, FEW>(p, sm, tmem, warp >> 1, ctx);
+            issue_s<D, FEW>(p, sm, tmem, warp >> 1, ctx);
         } else if (warp < 6) {
-            if (lane == 0) issue_pv<D, FEW>(p, sm, tmem, warp & 1, ctx);
+            issue_pv<D, FEW>(p, sm, tmem, warp & 1, ctx);
         }
         __syncwarp();
     } else {

@@ -198,6 +198,16 @@ template <int N> struct LineRing {
     __device__ __forceinline__ void release(int i) { mbar_arrive(smem_u32(&empty[i % N])); }
 };
 
+// One lane of a converged warp, the same each time. MMAs are issued by whole warps that branch
+// on this: their operands then stay in uniform registers (issued in a role of a single
+// thread, each MMA takes that thread 65 to 115 cycles).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(e));
+    return e != 0;
+}
+
 // A count in shared memory that one thread raises and others wait for.
 __device__ __forceinline__ void count_set(uint32_t at, int v) {
     asm volatile("st.release.cta.shared::cta.b32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
