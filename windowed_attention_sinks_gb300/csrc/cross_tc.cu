@@ -72,10 +72,9 @@ template <int D> struct alignas(1024) Smem {
     float2 ml[FEW_ROWS];  // FEW: half 1's m and l
     uint64_t full[R], empty[R], raw[R];
     uint64_t q_full, q_empty, mg_full, mg_empty;
-    uint64_t s_full[2], s_free[2], p_full[2][2], p0_done[2], o_full[2], o_empty[2], drain[4];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2], drain[4];
     uint32_t tmem_base;
-    int issued;    // loads into the ring so far
-    int s_issued[2];  // S of units that both halves work on, so far
+    int issued;  // loads into the ring so far
     int abort;
 };
 
@@ -227,7 +226,7 @@ template <int D, bool FEW>
 __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int half,
                         const DevCtx &ctx) {
     using S = Smem<D>;
-    constexpr uint32_t IDESC = idesc_bf16_f32(128, STATE_KEYS, 0, 0);
+    constexpr uint32_t IDESC = idesc_bf16_f32(128, CHUNK, 0, 0);
     volatile int *abort = &sm.abort;
     if (ctx.stall) bar_wait(smem_u32(&sm.drain[half]), 0, ctx, abort);  // test hook: runs out
     const uint64_t dq = desc_rows<128>(smem_u32(sm.q[FEW ? 0 : half]));
@@ -236,14 +235,13 @@ __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int ha
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    int x = 0, y = 0, t0 = 0;  // this half's tiles; of both halves; loads before the unit
+    int x = 0, t0 = 0;  // this half's steps; loads before the unit
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
-        const LineUnit &u = sm.units.u[i % UNITS];
+        const LineUnit u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
-        const bool both = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
-        const bool none = !FEW && half && !both;
+        const bool none = !FEW && half && u.s.n - u.u * p.line.tokens <= p.tokens;
         __syncwarp();
         if (elect_one()) sm.units.release(i);
         if (n == 0) break;
@@ -260,25 +258,30 @@ __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int ha
             if (elect_one()) mbar_arrive(smem_u32(&sm.q_empty));
         const int step = FEW ? 2 : 1;
 #pragma unroll 1
-        for (int j = FEW ? half : 0; j < n && ok && !none; j += step, ++x) {
-            const int t = t0 + 2 * j, st = t % S::R;
+        for (int j = FEW ? half : 0; j < n && ok && !none; j += step) {
+            const int t = t0 + 2 * j, st = t % S::R, nch = chunks(u, u.begin + j);
             ok = landed(sm, t, ctx, abort);
-            if (x >= 1) ok = ok && wait(sm.s_free[half], x - 1);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            tc_fence_after();
-            const uint64_t kd = dk + (uint64_t)(st * (S::TILE_BYTES >> 4));
-            if (elect_one()) {
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c, ++x) {
+                const int b = x & 1;
+                if (x >= 2) ok = ok && wait(sm.pv_done[half][b], (x >> 1) - 1);
+                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                tc_fence_after();
+                const uint64_t kd =
+                    dk + (uint64_t)(st * (S::TILE_BYTES >> 4) + c * (CHUNK * 128 >> 4));
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t at = (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3));
-                    tc_mma_f16(cols, dq + at, kd + at, IDESC, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t at = (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3));
+                        tc_mma_f16(cols + (uint32_t)(b * CHUNK), dq + at, kd + at, IDESC, kk > 0);
+                    }
+                    tc_commit(smem_u32(&sm.s_full[half][b]));
+                    if (c == nch - 1) {
+                        tc_commit(smem_u32(&sm.empty[st]));
+                        if (j + step >= n) tc_commit(smem_u32(&sm.q_empty));
+                    }
                 }
-                if (both) count_set(smem_u32(&sm.s_issued[half]), y + 1);
-                tc_commit(smem_u32(&sm.s_full[half]));
-                tc_commit(smem_u32(&sm.empty[st]));
-                if (j + step >= n) tc_commit(smem_u32(&sm.q_empty));
             }
-            y += both;
         }
         t0 += 2 * n;
     }
@@ -300,15 +303,13 @@ __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int h
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    // tiles; of two chunks; of both halves; V loads before the unit; units
-    int x = 0, x1 = 0, y = 0, t0 = 1, ec = 0;
+    int x = 0, t0 = 1, ec = 0;  // this half's steps; V loads before the unit; units
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
         const LineUnit u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
-        const bool both = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
-        const bool none = !FEW && half && !both;
+        const bool none = !FEW && half && u.s.n - u.u * p.line.tokens <= p.tokens;
         __syncwarp();
         if (elect_one()) sm.units.release(i);
         if (n == 0) break;
@@ -321,36 +322,27 @@ __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int h
         }
         const int first = FEW ? half : 0;
 #pragma unroll 1
-        for (int j = first; j < n && ok && !none; j += FEW ? 2 : 1, ++x) {
+        for (int j = first; j < n && ok && !none; j += FEW ? 2 : 1) {
             const int t = t0 + 2 * j, st = t % S::R, nch = chunks(u, u.begin + j);
             ok = landed(sm, t, ctx, abort);
             // the first P V overwrites the O that the last unit's epilogue reads
             if (j == first && ec >= 1) ok = ok && wait(sm.o_empty[half], ec - 1);
-            // The halves take turns, P V and the S behind it of one, then of the other: left to
-            // themselves they fall into step, both at their softmax while the products wait.
-            if (both) {
-                if (half == 0 || j + 1 < n)
-                    ok = ok && count_wait(smem_u32(&sm.s_issued[half ^ 1]), y + 1 + half, ctx, abort);
-                ++y;
-            }
-            const uint64_t vd = dv + (uint64_t)(st * (S::TILE_BYTES >> 4));
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (c >= nch) break;
-                ok = ok && wait(sm.p_full[half][c], c ? x1++ : x);
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c, ++x) {
+                const int b = x & 1;
+                ok = ok && wait(sm.p_full[half][b], x >> 1);
                 if (!(ok = __all_sync(0xffffffffu, ok))) break;
                 tc_fence_after();
+                const uint64_t vd =
+                    dv + (uint64_t)(st * (S::TILE_BYTES >> 4) + c * (CHUNK * 128 >> 4));
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < CHUNK / 16; ++kk)
-                        tc_mma_f16_ts(cols + O_COL, cols + (uint32_t)(c * CHUNK + 8 * kk),
-                                      vd + (uint64_t)((c * (CHUNK / 16) + kk) * (2048u >> 4)), IDESC,
+                        tc_mma_f16_ts(cols + O_COL, cols + (uint32_t)(b * CHUNK + 8 * kk),
+                                      vd + (uint64_t)(kk * (2048u >> 4)), IDESC,
                                       c > 0 || kk > 0 || j > first);
-                    if (c == 0) tc_commit(smem_u32(&sm.p0_done[half]));
-                    if (c == nch - 1) {
-                        tc_commit(smem_u32(&sm.s_free[half]));
-                        tc_commit(smem_u32(&sm.empty[st]));
-                    }
+                    tc_commit(smem_u32(&sm.pv_done[half][b]));
+                    if (c == nch - 1) tc_commit(smem_u32(&sm.empty[st]));
                 }
             }
         }
@@ -387,7 +379,7 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
     };
     const int tok = p.token(r);
     const float sx = p.scale_l2;
-    int x = 0, units = 0, merges = 0;  // this half's tiles and units
+    int x = 0, units = 0, merges = 0;  // this half's steps and units
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const LineUnit u = sm.units.u[i % UNITS];
@@ -405,15 +397,14 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
         bool fresh = true;  // some row has seen no key yet
         const int first = u.begin + (FEW ? half : 0);
 #pragma unroll 1
-        for (int j = first; j < u.end; j += FEW ? 2 : 1, ++x) {
+        for (int j = first; j < u.end; j += FEW ? 2 : 1) {
             const int nch = chunks(u, j);
-            if (!wait(sm.s_full[half], x)) return;
-            if (x >= 1 && !wait(sm.p0_done[half], x - 1)) return;  // (met: no phase passed over)
-            tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < nch; ++c) {
+            for (int c = 0; c < nch; ++c, ++x) {
+                if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
+                tc_fence_after();
                 const int kpos0 = j * STATE_KEYS + c * CHUNK;
-                const uint32_t s_tmem = tmem + (uint32_t)(c * CHUNK);
+                const uint32_t s_tmem = tmem + (uint32_t)((x & 1) * CHUNK);
                 const int there = u.s.len - kpos0;  // keys from here on
                 const bool key0 = p.sink_mode == 1 && kpos0 == 0;
                 uint32_t xs[2][32];
@@ -441,8 +432,7 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
                     fresh = __any_sync(0xffffffffu, m == NOTHING);
                     far = __any_sync(0xffffffffu, m != NOTHING && fabsf(m) > FAR);
                     if (j > first || c > 0) {
-                        // (S of this tile was issued behind the P V of the one before)
-                        if (c && !wait(sm.p0_done[half], x)) return false;
+                        if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
                         tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < D / 32; ++q) {
@@ -503,7 +493,7 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][c]));
+                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][x & 1]));
             }
         }
         // ---- epilogue
@@ -625,11 +615,12 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm.raw[lane]), 1);
         }
         if (lane < 2) {
-            mbar_init(smem_u32(&sm.s_full[lane]), 1);
-            mbar_init(smem_u32(&sm.s_free[lane]), 1);
-            mbar_init(smem_u32(&sm.p_full[lane][0]), p.warps);
-            mbar_init(smem_u32(&sm.p_full[lane][1]), p.warps);
-            mbar_init(smem_u32(&sm.p0_done[lane]), 1);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
+                mbar_init(smem_u32(&sm.p_full[lane][b]), p.warps);
+                mbar_init(smem_u32(&sm.pv_done[lane][b]), 1);
+            }
             mbar_init(smem_u32(&sm.o_full[lane]), 1);
             mbar_init(smem_u32(&sm.o_empty[lane]), p.warps);
             mbar_init(smem_u32(&sm.drain[lane]), 1);
@@ -641,7 +632,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm.mg_full), p.warps);
             mbar_init(smem_u32(&sm.mg_empty), p.warps);
             sm.abort = 0;
-            sm.issued = sm.s_issued[0] = sm.s_issued[1] = 0;
+            sm.issued = 0;
         }
         sm.units.init(4 + 1 + 2 * p.warps, lane);  // MMA issuers, tails, softmax
         fence_mbar_init();
