@@ -146,7 +146,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
         bar_wait(smem_u32(&sm.q_full[st]), (qt - 1 - st) / S::QR & 1, ctx, &zero);
 }
 
-// The products of group g: one thread.
+// The products of group g: a warp.
 template <int D>
 __device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int g, const DevCtx &ctx) {
     using S = Smem<D>;
@@ -161,11 +161,12 @@ __device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int g, 
     int kt = 0, qt = 0, x = 0;  // loads of keys and queries; this group's steps
     bool ok = true;
     for (int i = 0; ok; ++i) {
-        if (!(ok = sm.units.wait(i, ctx, abort))) break;
-        const LineUnit &u = sm.units.u[i % UNITS];
+        if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
+        const LineUnit u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
         const bool mine = keys_of(u, g) > 0;
-        sm.units.release(i);
+        __syncwarp();
+        if (elect_one()) sm.units.release(i);
         if (n == 0) break;
         const int ks = kt % S::KR;
         if (mine) ok = wait(sm.k_full[g][ks], kt / S::KR);
@@ -173,32 +174,33 @@ __device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int g, 
         for (int j = 0; j < n && ok; ++j, ++qt) {
             const int st = qt % S::QR;
             ok = wait(sm.q_full[st], qt / S::QR);
+            const int b = x & 1;
+            if (mine && x >= 2) ok = ok && wait(sm.s_empty[g][b], (x >> 1) - 1);
+            if (!(ok = __all_sync(0xffffffffu, ok))) break;
             if (!mine) {
-                if (ok) mbar_arrive(smem_u32(&sm.q_empty[st]));
+                if (elect_one()) mbar_arrive(smem_u32(&sm.q_empty[st]));
                 continue;
             }
-            const int b = x & 1;
-            if (x >= 2) ok = ok && wait(sm.s_empty[g][b], (x >> 1) - 1);
-            if (!ok) break;
             tc_fence_after();
             const uint64_t kd = dk + (uint64_t)(ks * (S::TILE_BYTES >> 4));
             const uint64_t qd = dq + (uint64_t)(st * (S::TILE_BYTES >> 4));
+            if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-                tc_mma_f16(tmem + (uint32_t)((2 * g + b) * 128),
-                           kd + (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3)),
-                           qd + (uint64_t)((kk >> 2) * (p.n * 128 >> 4) + 2 * (kk & 3)), idesc,
-                           kk > 0);
-            tc_commit(smem_u32(&sm.s_full[g][b]));
-            tc_commit(smem_u32(&sm.q_empty[st]));
+                for (int kk = 0; kk < D / 16; ++kk)
+                    tc_mma_f16(tmem + (uint32_t)((2 * g + b) * 128),
+                               kd + (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3)),
+                               qd + (uint64_t)((kk >> 2) * (p.n * 128 >> 4) + 2 * (kk & 3)), idesc,
+                               kk > 0);
+                tc_commit(smem_u32(&sm.s_full[g][b]));
+                tc_commit(smem_u32(&sm.q_empty[st]));
+                if (j == n - 1) tc_commit(smem_u32(&sm.k_empty[g][ks]));
+            }
             ++x;
         }
-        if (mine) {
-            tc_commit(smem_u32(&sm.k_empty[g][ks]));
-            ++kt;
-        }
+        kt += mine;
     }
-    tc_commit(smem_u32(&sm.drain[g]));  // every MMA is done before TMEM goes
+    __syncwarp();
+    if (elect_one()) tc_commit(smem_u32(&sm.drain[g]));  // every MMA is done before TMEM goes
     int zero = 0;
     bar_wait(smem_u32(&sm.drain[g]), 0, ctx, &zero);
 }
@@ -347,8 +349,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         load_tiles<D>(p, &tq, &tk, sm, ctx);
         __syncwarp();
     } else if (warp < 3) {
-        if (lane == 0) issue<D>(p, sm, tmem, warp - 1, ctx);
-        __syncwarp();
+        issue<D>(p, sm, tmem, warp - 1, ctx);
     } else if (warp >= SUMS) {
         sum_up<D>(p, sm, tmem, ctx);
     }
