@@ -6,13 +6,14 @@
 // stays in the thread: no sum across threads, no order that changes. Query rows are tokens
 // times the heads of a KV group, fetched as boxes of G heads and floor(N / G) tokens.
 //
-// A unit is 256 keys of a sequence and KV head, two tiles of 128, a group of warps each; a
-// step is a tile of N query rows, which both tiles use (a query tile comes from L2, and one
-// for 128 keys alone would take all of its bandwidth). N is 32, 64 or 128, by the rows that a
-// sequence has: single tokens then read the keys and next to nothing else.
+// A unit is 512 keys of a sequence and KV head, four tiles of 128 with a group of four warps
+// each; a step is a tile of N query rows, which all four use: a query tile comes from L2, and one
+// for a tile of keys alone would take all of its bandwidth. N is 32, 64 or 128, by the rows
+// that a sequence has: single tokens then read the keys and next to nothing else.
 // One persistent CTA per SM over an equal piece of the line of units (states_plan.cuh);
 // the sums of a unit that is cut go to the workspace and are added up by a second launch.
-// Roles: warp 0 units and TMA; 1, 2 the products of the groups; 4-7, 8-11 the groups' sums.
+// Roles: warp 0 units and TMA; 1, 2 the products of two tiles each; 3 the rows' denominators;
+// 4-19 the tiles' sums.
 #include <math.h>
 #include <stdio.h>
 
@@ -22,11 +23,12 @@
 namespace sattn {
 namespace {
 
-constexpr int NTHREADS = 384;
+constexpr int NTHREADS = 640;
 constexpr int SUMS = 4;    // first warp of the sums
 constexpr int UNITS = 4;   // units handed on ahead
-constexpr int UNIT_KEYS = 2 * STATE_KEYS;
-constexpr uint32_t TMEM_COLS = 512;  // two groups, two buffers of 128 columns each
+constexpr int TILES = UNIT_TILES, UNIT_KEYS = TILES * STATE_KEYS;
+constexpr int LR = 4;                // steps whose denominators are ahead
+constexpr uint32_t TMEM_COLS = 512;  // 128 a tile
 
 struct WeightParams {
     LineArgs line;
@@ -50,15 +52,15 @@ template <int D> struct alignas(1024) Smem {
     static constexpr int NH = D / 64;            // 64-column parts of a row
     static constexpr uint32_t PART = 128 * 128;  // 128 rows of 64 bf16
     static constexpr uint32_t TILE_BYTES = NH * PART;
-    static constexpr int KR = D == 128 ? 2 : 4;  // key tiles a group
-    static constexpr int QR = D == 128 ? 3 : 6;  // query tiles
-    uint8_t k[2][KR][TILE_BYTES];
+    static constexpr int KR = D == 128 ? 1 : 2;  // tiles of keys ahead, for each of a unit's
+    static constexpr int QR = D == 128 ? 3 : 6;  // tiles of queries
+    uint8_t k[TILES][KR][TILE_BYTES];
     uint8_t q[QR][TILE_BYTES];
-    float lse[2][2][128];  // group, step's parity: -lse log2(e), -inf where a row does not count
+    float lse[LR][128];  // -lse log2(e), -inf where a row does not count
     LineStart line;
     LineRing<UNITS> units;
-    uint64_t k_full[2][KR], k_empty[2][KR], q_full[QR], q_empty[QR];
-    uint64_t s_full[2][2], s_empty[2][2], lse_full[2][2], drain[2];
+    uint64_t k_full[TILES][KR], k_empty[TILES][KR], q_full[QR], q_empty[QR];
+    uint64_t lse_full[LR], lse_empty[LR], s_full[TILES], s_empty[TILES], drain[2];
     uint32_t tmem_base;
     int abort;
 };
@@ -95,7 +97,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
         }
         reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
     }
-    int kt[2] = {0, 0}, qt = 0, index = 0;  // loads; units
+    int kt[TILES] = {}, qt = 0, index = 0;  // loads; units
     bool ok = true;
 #pragma unroll 1
     for (; it.live && ok; it.next(p.line)) {
@@ -103,7 +105,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
         if (u.begin == u.end) continue;
         ok = sm.units.put(index++, u, ctx, abort);
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < TILES; ++g) {
             if (!ok || keys_of(u, g) <= 0) continue;
             const int st = kt[g] % S::KR, use = kt[g] / S::KR;
             if (use >= 1) ok = bar_wait(smem_u32(&sm.k_empty[g][st]), (use - 1) & 1, ctx, abort);
@@ -138,7 +140,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
 #pragma unroll 1
     for (int st = 0; st < S::KR; ++st)
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < TILES; ++g)
             if (st < kt[g])
                 bar_wait(smem_u32(&sm.k_full[g][st]), (kt[g] - 1 - st) / S::KR & 1, ctx, &zero);
 #pragma unroll 1
@@ -146,77 +148,145 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
         bar_wait(smem_u32(&sm.q_full[st]), (qt - 1 - st) / S::QR & 1, ctx, &zero);
 }
 
-// The products of group g: a warp.
+// The denominators of the steps' query rows: a warp, four steps' loads at a time.
 template <int D>
-__device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int g, const DevCtx &ctx) {
+__device__ void load_lse(const WeightParams &p, Smem<D> &sm, const DevCtx &ctx) {
+    const int lane = threadIdx.x & 31;
+    volatile int *abort = &sm.abort;
+    int tok[4], head[4];  // of rows lane, lane + 32, ..
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        tok[e] = p.token(lane + 32 * e);
+        head[e] = lane + 32 * e - tok[e] * p.G;
+    }
+    int q = 0;  // steps
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
+        const LineUnit u = sm.units.u[i % UNITS];
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
+        if (u.begin == u.end) return;
+#pragma unroll 1
+        for (int j0 = u.begin; j0 < u.end; j0 += 4) {
+            float x[4][4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int t = (j0 + s) * p.line.tokens + tok[e];
+                    x[s][e] = INFINITY;
+                    if (j0 + s < u.end && lane + 32 * e < p.rows && t < u.s.n)
+                        x[s][e] = __ldg(p.lse + (size_t)(u.s.t0 + t) * p.H + u.h * p.G + head[e]);
+                }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (j0 + s >= u.end) break;
+                const int b = q % LR;
+                if (q >= LR && !__all_sync(0xffffffffu, bar_wait(smem_u32(&sm.lse_empty[b]),
+                                                                 (q / LR - 1) & 1, ctx, abort)))
+                    return;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    sm.lse[b][lane + 32 * e] = isinf(x[s][e]) ? -INFINITY : -x[s][e] * LOG2E;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.lse_full[b]));
+                ++q;
+            }
+        }
+    }
+}
+
+// The products of tiles 2 w and 2 w + 1: a warp.
+template <int D>
+__device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int w, const DevCtx &ctx) {
     using S = Smem<D>;
     const uint32_t idesc = idesc_bf16_f32(128, p.n, 0, 0);
     volatile int *abort = &sm.abort;
-    if (ctx.stall) bar_wait(smem_u32(&sm.drain[g]), 0, ctx, abort);  // test hook: runs out
-    const uint64_t dk = desc_rows<128>(smem_u32(sm.k[g][0]));
+    if (ctx.stall) bar_wait(smem_u32(&sm.drain[w]), 0, ctx, abort);  // test hook: runs out
+    const uint64_t dk = desc_rows<128>(smem_u32(sm.k[2 * w][0]));
     const uint64_t dq = desc_rows<128>(smem_u32(sm.q[0]));
     auto wait = [&](uint64_t &bar, int phase) {
         return bar_wait(smem_u32(&bar), phase & 1, ctx, abort);
     };
-    int kt = 0, qt = 0, x = 0;  // loads of keys and queries; this group's steps
+    int kt[2] = {0, 0}, x[2] = {0, 0}, qt = 0;  // the tiles' loads and steps; loads of queries
     bool ok = true;
     for (int i = 0; ok; ++i) {
         if (!(ok = __all_sync(0xffffffffu, sm.units.wait(i, ctx, abort)))) break;
         const LineUnit u = sm.units.u[i % UNITS];
         const int n = u.end - u.begin;
-        const bool mine = keys_of(u, g) > 0;
+        const int mine = keys_of(u, 2 * w + 1) > 0 ? 2 : keys_of(u, 2 * w) > 0 ? 1 : 0;  // tiles
         __syncwarp();
         if (elect_one()) sm.units.release(i);
         if (n == 0) break;
-        const int ks = kt % S::KR;
-        if (mine) ok = wait(sm.k_full[g][ks], kt / S::KR);
 #pragma unroll 1
         for (int j = 0; j < n && ok; ++j, ++qt) {
             const int st = qt % S::QR;
-            ok = wait(sm.q_full[st], qt / S::QR);
-            const int b = x & 1;
-            if (mine && x >= 2) ok = ok && wait(sm.s_empty[g][b], (x >> 1) - 1);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            if (!mine) {
-                if (elect_one()) mbar_arrive(smem_u32(&sm.q_empty[st]));
-                continue;
-            }
-            tc_fence_after();
-            const uint64_t kd = dk + (uint64_t)(ks * (S::TILE_BYTES >> 4));
-            const uint64_t qd = dq + (uint64_t)(st * (S::TILE_BYTES >> 4));
-            if (elect_one()) {
+            ok = __all_sync(0xffffffffu, wait(sm.q_full[st], qt / S::QR));
+            if (!mine && ok && elect_one()) mbar_arrive(smem_u32(&sm.q_empty[st]));
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    tc_mma_f16(tmem + (uint32_t)((2 * g + b) * 128),
-                               kd + (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3)),
-                               qd + (uint64_t)((kk >> 2) * (p.n * 128 >> 4) + 2 * (kk & 3)), idesc,
-                               kk > 0);
-                tc_commit(smem_u32(&sm.s_full[g][b]));
-                tc_commit(smem_u32(&sm.q_empty[st]));
-                if (j == n - 1) tc_commit(smem_u32(&sm.k_empty[g][ks]));
+            for (int a = 0; a < 2; ++a) {
+                if (a >= mine || !ok) continue;
+                const int g = 2 * w + a, ks = kt[a] % S::KR;
+                if (j == 0) ok = wait(sm.k_full[g][ks], kt[a] / S::KR);
+                if (x[a] >= 1) ok = ok && wait(sm.s_empty[g], x[a] - 1);
+                if (!(ok = __all_sync(0xffffffffu, ok))) continue;
+                tc_fence_after();
+                const uint64_t kd = dk + (uint64_t)((a * S::KR + ks) * (S::TILE_BYTES >> 4));
+                const uint64_t qd = dq + (uint64_t)(st * (S::TILE_BYTES >> 4));
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+                        tc_mma_f16(tmem + (uint32_t)(g * 128),
+                                   kd + (uint64_t)((kk >> 2) * (S::PART >> 4) + 2 * (kk & 3)),
+                                   qd + (uint64_t)((kk >> 2) * (p.n * 128 >> 4) + 2 * (kk & 3)),
+                                   idesc, kk > 0);
+                    tc_commit(smem_u32(&sm.s_full[g]));
+                    if (a == mine - 1) tc_commit(smem_u32(&sm.q_empty[st]));
+                    if (j == n - 1) tc_commit(smem_u32(&sm.k_empty[g][ks]));
+                }
+                ++x[a];
+                kt[a] += j == n - 1;
             }
-            ++x;
         }
-        kt += mine;
     }
     __syncwarp();
-    if (elect_one()) tc_commit(smem_u32(&sm.drain[g]));  // every MMA is done before TMEM goes
+    if (elect_one()) tc_commit(smem_u32(&sm.drain[w]));  // every MMA is done before TMEM goes
     int zero = 0;
-    bar_wait(smem_u32(&sm.drain[g]), 0, ctx, &zero);
+    bar_wait(smem_u32(&sm.drain[w]), 0, ctx, &zero);
 }
 
+// The sum of 2^(x sx + l) over 32 columns, l from shared memory.
+__device__ __forceinline__ float sum32(const uint32_t (&xs)[32], uint64_t sx, const float *lse) {
+    uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+        const float4 l = *reinterpret_cast<const float4 *>(lse + e);
+        float a0, a1, a2, a3;
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1])), sx,
+                         f2_pack(l.x, l.y)), a0, a1);
+        f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e + 2]), __uint_as_float(xs[e + 3])), sx,
+                         f2_pack(l.z, l.w)), a2, a3);
+        part[0] = f2_add(part[0], f2_pack(ex2(a0), ex2(a1)));
+        part[1] = f2_add(part[1], f2_pack(ex2(a2), ex2(a3)));
+    }
+    float a0, a1;
+    f2_unpack(f2_add(part[0], part[1]), a0, a1);
+    return a0 + a1;
+}
+
+// The sums of tile g.
 template <int D>
 __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, const DevCtx &ctx) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = (warp - SUMS) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
-    const uint32_t tmem = tmem_base + (uint32_t)(2 * g * 128) + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t tmem = tmem_base + (uint32_t)(g * 128) + ((uint32_t)(quarter * 32) << 16);
     volatile int *abort = &sm.abort;
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
-    const int tok = p.token(r), head = r - tok * p.G;  // of query row r
     const float sx = p.scale_l2;
-    int x = 0;  // this group's steps
+    const uint64_t sx2 = f2_pack(sx, sx);
+    int q = 0, x = 0;  // steps; this tile's steps
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const LineUnit u = sm.units.u[i % UNITS];
@@ -224,72 +294,74 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
         if (lane == 0) sm.units.release(i);
         if (u.begin == u.end) return;
         const int keys = keys_of(u, g);
-        if (keys <= 0) continue;
         const bool first = p.sinks && u.u == 0 && g == 0 && quarter == 0;  // lane 0 has key 0
         const size_t at = (size_t)u.h * p.line.S + u.s.s0 + u.u * UNIT_KEYS + g * STATE_KEYS + r;
-        float old = 0.f;
+        float old = 0.f, w = 0.f;
         if (p.accumulate && !u.cut() && r < keys) old = p.weights[at];
-        // -lse log2(e) of query row r of step j
-        auto row = [&](int j) -> float {
-            const int t = j * p.line.tokens + tok;
-            if (r >= p.rows || t >= u.s.n) return INFINITY;
-            return __ldg(p.lse + (size_t)(u.s.t0 + t) * p.H + u.h * p.G + head);
-        };
-        float next = row(u.begin), w = 0.f;
 #pragma unroll 1
-        for (int j = u.begin; j < u.end; ++j, ++x) {
-            const int b = x & 1;
-            sm.lse[g][b][r] = isinf(next) ? -INFINITY : -next * LOG2E;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.lse_full[g][b]));
-            if (j + 1 < u.end) next = row(j + 1);
-            if (!wait(sm.lse_full[g][b], x >> 1)) return;
-            if (!wait(sm.s_full[g][b], x >> 1)) return;
+        for (int j = u.begin; j < u.end; ++j, ++q) {
+            const int b = q % LR;
+            if (!wait(sm.lse_full[b], q / LR)) return;
+            if (keys <= 0) {  // no phase is passed over
+                if (lane == 0) mbar_arrive(smem_u32(&sm.lse_empty[b]));
+                continue;
+            }
+            if (!wait(sm.s_full[g], x)) return;
+            ++x;
             tc_fence_after();
+            const float *lse = sm.lse[b];
             const int cols = min(p.line.tokens, u.s.n - j * p.line.tokens) * p.G;
             float sum = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-                uint32_t xs[32];
-                tmem_ld32(tmem + (uint32_t)(b * 128 + c), xs);
+            if (cols > 96 && !first) {  // the next 32 columns come while these are summed
+                uint32_t xs[2][32];
+                tmem_ld32(tmem, xs[0]);
                 tc_wait_ld();
-                const float4 *ls = reinterpret_cast<const float4 *>(sm.lse[g][b] + c);
-                if (cols - c < 32) {  // columns of no row may hold anything
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) hide_unless(xs[e], e < cols - c);
+                for (int c = 0; c < 4; ++c) {
+                    if (c < 3) tmem_ld32(tmem + 32u * (c + 1), xs[(c + 1) & 1]);
+                    if (c == 3 && cols < 128) {  // columns of no row may hold anything
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) hide_unless(xs[1][e], 96 + e < cols);
+                    }
+                    sum += sum32(xs[c & 1], sx2, lse + 32 * c);
+                    if (c < 3) tc_wait_ld();
+                    if (c == 2) {  // S has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[g]));
+                    }
                 }
-                if (first) {
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < cols; c += 32) {
+                    uint32_t xs[32];
+                    tmem_ld32(tmem + (uint32_t)c, xs);
+                    tc_wait_ld();
+                    if (cols - c < 32) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) hide_unless(xs[e], e < cols - c);
+                    }
+                    if (!first) {
+                        sum += sum32(xs, sx2, lse + c);
+                        continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const int q = c + e, h = q - p.token(q) * p.G;
-                        const float s = lane == 0 ? sink_log2(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
-                        const float y = fmaf(__uint_as_float(xs[e]), sx, sm.lse[g][b][q]);
-                        sum += ex2(y == -INFINITY ? y : y + s);  // (whatever the sink)
+                        const int col = c + e, h = col - p.token(col) * p.G;
+                        const float z = lane == 0 ? sink_log2(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
+                        const float y = fmaf(__uint_as_float(xs[e]), sx, lse[col]);
+                        sum += ex2(y == -INFINITY ? y : y + z);  // (whatever the sink)
                     }
-                    continue;
                 }
-                uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-                const uint64_t f2 = f2_pack(sx, sx);
-#pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                    const float4 l = ls[e >> 2];
-                    float a0, a1, a2, a3;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e]), __uint_as_float(xs[e + 1])), f2,
-                                     f2_pack(l.x, l.y)), a0, a1);
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e + 2]), __uint_as_float(xs[e + 3])),
-                                     f2, f2_pack(l.z, l.w)), a2, a3);
-                    part[0] = f2_add(part[0], f2_pack(ex2(a0), ex2(a1)));
-                    part[1] = f2_add(part[1], f2_pack(ex2(a2), ex2(a3)));
-                }
-                float a0, a1;
-                f2_unpack(f2_add(part[0], part[1]), a0, a1);
-                sum += a0 + a1;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[g]));
             }
-            w += sum;
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[g][b]));
+            if (lane == 0) mbar_arrive(smem_u32(&sm.lse_empty[b]));
+            w += sum;
         }
+        if (keys <= 0) continue;
         if (u.cut()) {
             float *part = reinterpret_cast<float *>(p.ws + SUMS_OFFSET) +
                           ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * UNIT_KEYS;
@@ -314,26 +386,26 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         return;
     }
     if (warp == 2) {  // a lane a barrier
-        if (lane < 2) {
+        if (lane < TILES) {
 #pragma unroll
             for (int i = 0; i < S::KR; ++i) {
                 mbar_init(smem_u32(&sm.k_full[lane][i]), 1);
                 mbar_init(smem_u32(&sm.k_empty[lane][i]), 1);
             }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
-                mbar_init(smem_u32(&sm.s_empty[lane][b]), 4);
-                mbar_init(smem_u32(&sm.lse_full[lane][b]), 4);
-            }
-            mbar_init(smem_u32(&sm.drain[lane]), 1);
+            mbar_init(smem_u32(&sm.s_full[lane]), 1);
+            mbar_init(smem_u32(&sm.s_empty[lane]), 4);
+        }
+        if (lane < LR) {
+            mbar_init(smem_u32(&sm.lse_full[lane]), 1);
+            mbar_init(smem_u32(&sm.lse_empty[lane]), 4 * TILES);
         }
         if (lane < S::QR) {
             mbar_init(smem_u32(&sm.q_full[lane]), 1);
             mbar_init(smem_u32(&sm.q_empty[lane]), 2);
         }
+        if (lane < 2) mbar_init(smem_u32(&sm.drain[lane]), 1);
         if (lane == 0) sm.abort = 0;
-        sm.units.init(2 + 8, lane);
+        sm.units.init(2 + 1 + 4 * TILES, lane);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -350,7 +422,9 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         __syncwarp();
     } else if (warp < 3) {
         issue<D>(p, sm, tmem, warp - 1, ctx);
-    } else if (warp >= SUMS) {
+    } else if (warp == 3) {
+        load_lse<D>(p, sm, ctx);
+    } else {
         sum_up<D>(p, sm, tmem, ctx);
     }
     tc_fence_before();

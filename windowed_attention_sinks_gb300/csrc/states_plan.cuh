@@ -1,7 +1,7 @@
 // How the tensor-core kernels over encoder states share out their work.
 //
 // A unit is a tile of one sequence and KV head with all that it meets: a tile of query rows
-// with its steps over 128-key tiles (the attention), or 256 keys with their steps over tiles
+// with its steps over 128-key tiles (the attention), or 512 keys with their steps over tiles
 // of query rows (KEYS: the key weights). Units are numbered sequence by sequence, KV
 // head by KV head; their steps in a row, and before each unit's steps `extra` for what a
 // unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
@@ -18,7 +18,8 @@
 
 namespace sattn {
 
-constexpr int STATE_KEYS = 128;  // keys a tile; a unit of keys has two
+constexpr int STATE_KEYS = 128;  // keys a tile
+constexpr int UNIT_TILES = 4;    // and tiles in a unit of keys
 
 struct LineArgs {
     const int32_t *cu, *starts, *lens;
@@ -42,7 +43,7 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
     u.b = b;
     bad = !load_states(a.cu, a.starts, a.lens, b, a.T, a.S, u.s);
     if (bad) return false;
-    constexpr int TILE_KEYS = KEYS ? 2 * STATE_KEYS : STATE_KEYS;
+    constexpr int TILE_KEYS = KEYS ? UNIT_TILES * STATE_KEYS : STATE_KEYS;
     const int keys = (int)(((long long)u.s.len + TILE_KEYS - 1) / TILE_KEYS);
     const int rows = (int)(((long long)u.s.n + a.tokens - 1) / a.tokens);
     u.nu = KEYS ? keys : rows;
@@ -53,7 +54,7 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
 // What a CTA starts from (in shared memory).
 struct LineStart {
     long long x0, x1, total, ustart;  // its piece of the line; where the unit that holds x0 starts
-    long long warps[32];
+    long long warps[20];
     int pieces, b, h, u;
 };
 
@@ -61,7 +62,7 @@ __device__ __forceinline__ long long line_cut(long long total, int c, int pieces
     return total * c / pieces;
 }
 
-// Called by the whole CTA (a whole number of warps, 1024 threads at most); ends with a barrier.
+// Called by the whole CTA (a whole number of warps, 640 threads at most); ends with a barrier.
 template <bool KEYS>
 __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, const DevCtx &ctx) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
