@@ -116,7 +116,7 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
     uint32_t raws = 0, on_raw = 0;      // bit i: raw[i]'s phase; slot i's last load counts there
     bool ok = true;
 #pragma unroll 1
-    for (; it.live && ok; it.next(p.line)) {
+    for (; it.live && ok; it.next(p.line, sm.line)) {
         const LineUnit &u = it.u;
         if (u.begin == u.end) continue;
         ok = sm.units.put(index, u, ctx, abort);

@@ -100,7 +100,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
     int kt[TILES] = {}, qt = 0, index = 0;  // loads; units
     bool ok = true;
 #pragma unroll 1
-    for (; it.live && ok; it.next(p.line)) {
+    for (; it.live && ok; it.next(p.line, sm.line)) {
         const LineUnit &u = it.u;
         if (u.begin == u.end) continue;
         ok = sm.units.put(index++, u, ctx, abort);

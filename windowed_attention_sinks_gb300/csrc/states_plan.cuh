@@ -34,6 +34,7 @@ struct LineUnit {
     int b, h, u, nu;     // sequence, KV head, unit of its nu
     int steps;           // at least one (an empty one's is masked)
     int begin, end;      // the steps of this piece, 0 .. steps
+    int c0, parts;       // of a cut unit: its first piece, and how many
     __device__ __forceinline__ bool cut() const { return begin > 0 || end < steps; }
 };
 
@@ -55,22 +56,79 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
 struct LineStart {
     long long x0, x1, total, ustart;  // its piece of the line; where the unit that holds x0 starts
     long long warps[20];
-    int pieces, b, h, u;
+    LineUnit u;
+    int pieces;
 };
 
+// a / b; the lines of small calls stay within 32 bits, whose division is several times as fast
+__device__ __forceinline__ long long line_div(long long a, long long b) {
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
 __device__ __forceinline__ long long line_cut(long long total, int c, int pieces) {
-    return total * c / pieces;
+    return line_div(total * c, pieces);
+}
+// The piece that position x of the line lies in.
+__device__ __forceinline__ int line_piece(const LineStart &ls, long long x) {
+    return (int)line_div((x + 1) * ls.pieces - 1, ls.total);
+}
+__device__ __forceinline__ long long warp_prefix64(long long v) {  // over the lanes up to this one
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long w = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += w;
+    }
+    return v;
+}
+
+// The CTA's piece of a line of that length.
+__device__ __forceinline__ void line_ends(LineStart &ls, long long total, bool writes,
+                                          long long &x0, long long &x1) {
+    const int pieces = (int)min((long long)gridDim.x, max(1ll, total));
+    const int c = min((int)blockIdx.x, pieces);
+    x0 = line_cut(total, c, pieces);
+    x1 = line_cut(total, min(c + 1, pieces), pieces);
+    if (writes) {
+        ls.x0 = x0;
+        ls.x1 = x1;
+        ls.total = total;
+        ls.pieces = pieces;
+    }
+}
+// The unit of position x0, which lies in sequence u.b, whose line starts at `before`.
+__device__ __forceinline__ void line_unit(const LineArgs &a, LineStart &ls, LineUnit &u,
+                                          long long x0, long long before) {
+    const long long one = u.steps + a.extra, i = line_div(x0 - before, one);
+    u.h = (int)line_div(i, u.nu);
+    u.u = (int)(i - (long long)u.h * u.nu);
+    ls.u = u;
+    ls.ustart = before + i * one;
 }
 
 // Called by the whole CTA (a whole number of warps, 640 threads at most); ends with a barrier.
+// Up to 32 sequences: one warp, a lane each, while the others set up what they need.
 template <bool KEYS>
 __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, const DevCtx &ctx) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+    LineUnit u;
+    bool bad = false;
+    long long x0, x1;
+    if (a.B <= 32) {
+        if (warp == 0) {
+            long long mine = 0;
+            if (lane < a.B && line_seq<KEYS>(a, lane, u, bad))
+                mine = (long long)a.Hkv * u.nu * (u.steps + a.extra);
+            if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+            const long long upto = warp_prefix64(mine), before = upto - mine;
+            line_ends(ls, __shfl_sync(0xffffffffu, upto, 31), lane == 0, x0, x1);
+            if (x0 < x1 && x0 >= before && x0 < upto) line_unit(a, ls, u, x0, before);
+        }
+        __syncthreads();
+        return;
+    }
     const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;  // sequences a thread
     const int b0 = (int)min((long long)a.B, (long long)tid * per), b1 = min(a.B, b0 + per);
-    LineUnit u;
     long long mine = 0;
-    bool bad = false;
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         bool wrong;
@@ -78,46 +136,24 @@ __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, con
         bad |= wrong;
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
-    long long inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
+    const long long inc = warp_prefix64(mine);
     if (lane == 31) ls.warps[warp] = inc;
     __syncthreads();
-    long long before = inc - mine, total = 0;
-    for (int w = 0; w < nw; ++w) {
-        const long long v = ls.warps[w];
-        if (w < warp) before += v;
-        total += v;
-    }
-    const int pieces = (int)min((long long)gridDim.x, max(1ll, total));
-    const int c = min((int)blockIdx.x, pieces);
-    const long long x0 = line_cut(total, c, pieces), x1 = line_cut(total, min(c + 1, pieces), pieces);
-    if (tid == 0) {
-        ls.x0 = x0;
-        ls.x1 = x1;
-        ls.total = total;
-        ls.pieces = pieces;
-        if (x0 >= x1 || total == 0) ls.b = ls.h = ls.u = 0, ls.ustart = 0;
-    }
+    const long long ws = warp_prefix64(lane < nw ? ls.warps[lane] : 0);
+    long long before = inc - mine;
+    if (warp > 0) before += __shfl_sync(0xffffffffu, ws, warp - 1);
+    line_ends(ls, __shfl_sync(0xffffffffu, ws, 31), tid == 0, x0, x1);
     if (x0 < x1 && x0 >= before && x0 < before + mine) {
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             bool wrong;
             if (!line_seq<KEYS>(a, b, u, wrong)) continue;
-            const long long one = u.steps + a.extra, all = one * u.nu * a.Hkv;
-            if (x0 >= before + all) {
-                before += all;
-                continue;
+            const long long all = (long long)a.Hkv * u.nu * (u.steps + a.extra);
+            if (x0 < before + all) {
+                line_unit(a, ls, u, x0, before);
+                break;
             }
-            const long long i = (x0 - before) / one;  // unit of the sequence
-            ls.b = b;
-            ls.h = (int)(i / u.nu);
-            ls.u = (int)(i % u.nu);
-            ls.ustart = before + i * one;
-            break;
+            before += all;
         }
     }
     __syncthreads();
@@ -133,24 +169,27 @@ template <bool KEYS> struct LineIter {
         x1 = ls.x1;
         live = ls.x0 < x1;
         if (!live) return;
-        bool bad;
-        live = line_seq<KEYS>(a, ls.b, u, bad);
-        u.h = ls.h;
-        u.u = ls.u;
+        u = ls.u;
         ustart = ls.ustart;
         u.begin = (int)max(0ll, ls.x0 - ustart - a.extra);
         // uncut, the unit is all of the piece's that its first step lies in
         if (!a.split && u.begin > 0) u.begin = u.steps;
-        clip(a);
+        clip(a, ls);
     }
     // The steps of u in this piece (there may be none of the first unit).
-    __device__ __forceinline__ void clip(const LineArgs &a) {
+    __device__ __forceinline__ void clip(const LineArgs &a, const LineStart &ls) {
         const long long t0 = ustart + a.extra;
         live = live && t0 + u.begin < x1;
         u.end = a.split ? (int)min((long long)u.steps, x1 - t0) : u.steps;
+        u.c0 = 0;
+        u.parts = 1;
+        if (live && a.split && u.cut()) {
+            u.c0 = line_piece(ls, t0);
+            u.parts = line_piece(ls, t0 + u.steps - 1) - u.c0 + 1;
+        }
     }
     // To the next unit of the line; there may be none behind this piece.
-    __device__ __forceinline__ void next(const LineArgs &a) {
+    __device__ __forceinline__ void next(const LineArgs &a, const LineStart &ls) {
         live = u.end == u.steps;
         if (!live) return;
         ustart += u.steps + a.extra;
@@ -169,7 +208,7 @@ template <bool KEYS> struct LineIter {
             }
         }
         u.begin = 0;
-        clip(a);
+        clip(a, ls);
     }
 };
 
