@@ -17,10 +17,14 @@
 // One persistent CTA per SM over an equal piece of the line of units (states_plan.cuh), two
 // halves that work in turn, so that one's softmax runs beside the other's products:
 //   many rows   a unit is 256 rows; both halves use every tile
-//   FEW         a unit is 64 rows at most; the halves take every other tile and are
-//               joined through shared memory at the unit's end. Twice as many tiles are in
-//               work at a time: what bounds is the memory, and a tile's chain of products
-//               and exponentials is longer than its load.
+//   FEW         a unit is FEW (32 or 64) rows at most; the halves take every other tile, and
+//               the rows stand in the MMA's 128 more than once, so that each warp of a
+//               half takes some of a step's keys: its P is 0 for the others, and the O of its lanes
+//               a sum over its own keys. Every warp runs a softmax of its own (eight in
+//               all, or four with 64 rows); they are joined at a unit's end. What bounds is the
+//               memory, and a tile's chain of products and exponentials, a row a thread,
+//               takes longer than its load. The pieces of a unit that is cut between
+//               CTAs are joined by the last of them to arrive.
 // Roles: warp 0 units and TMA; 1, 3 S of the halves; 4, 5 P V; 2 the last V tile's rows;
 // 8-11, 12-15 softmax and epilogue, a thread a row.
 #include <math.h>
@@ -36,7 +40,6 @@ constexpr int NTHREADS = 512;
 constexpr int SOFTMAX = 8;   // first softmax warp
 constexpr int UNITS = 4;     // units handed on ahead
 constexpr int CHUNK = 64;    // keys whose P is handed on at a time
-constexpr int FEW_ROWS = 64;
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
 constexpr float FAR = 1 << 20;  // m up to which x - m may be taken in one rounding
 constexpr uint32_t TMEM_COLS = 512, HALF_COLS = 256, O_COL = 128;
@@ -45,7 +48,6 @@ struct CrossParams {
     LineArgs line;
     int H, G, tokens;  // tokens: of a half's rows
     int rows;          // tokens * G
-    int warps;         // softmax warps of a half that have rows
     float scale_l2;
     const float *sinks;
     int sink_mode;
@@ -65,16 +67,17 @@ template <int D> struct alignas(1024) Smem {
     static constexpr uint32_t PART = 128 * 128;           // 128 rows of 64 bf16
     static constexpr uint32_t TILE_BYTES = NH * PART;
     static constexpr int R = D == 128 ? 5 : 12;           // ring of K and V tiles
-    uint8_t q[2][TILE_BYTES];  // (FEW: q[1] takes half 1's O at a unit's end)
+    uint8_t q[2][TILE_BYTES];  // (FEW: q[1] takes the warps' O at a unit's end)
     uint8_t kv[R][TILE_BYTES];
     LineStart line;
     LineRing<UNITS> units;
-    float2 ml[FEW_ROWS];  // FEW: half 1's m and l
+    float2 ml[256];  // FEW: the warps' m and l
     uint64_t full[R], empty[R], raw[R];
-    uint64_t q_full, q_empty, mg_full, mg_empty;
+    uint64_t q_full, q_empty, meet;
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2], drain[4];
     uint32_t tmem_base;
     int issued;  // loads into the ring so far
+    int last;    // FEW: whether this piece joins the unit's
     int abort;
 };
 
@@ -88,18 +91,15 @@ __device__ __forceinline__ int chunks(const LineUnit &u, int j) {
     return j * STATE_KEYS + CHUNK < u.s.len ? 2 : 1;
 }
 
-template <int D, bool FEW>
+template <int D, int FEW>
 __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
                                            const CUtensorMap *tk, const CUtensorMap *tv,
                                            Smem<D> &sm, const DevCtx &ctx) {
     using S = Smem<D>;
     if ((threadIdx.x & 31) != 0) return;
     volatile int *abort = &sm.abort;
-    prefetch_tmap(tq);
-    prefetch_tmap(tk);
-    prefetch_tmap(tv);
     LineIter<false> it(p.line, sm.line);
-    if (p.line.split) {
+    if (!FEW && p.line.split) {
         PlanNote n{};
         if (it.live) {
             const LineUnit &u = it.u;
@@ -148,14 +148,15 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
                 const uint32_t bar = smem_u32(&sm.q_full);
                 const int tok = u.s.t0 + u.u * p.line.tokens;
                 const bool two = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
-                mbar_arrive_expect_tx(bar, (two ? 2 : 1) * S::NH * p.rows * 128);
+                constexpr int COPIES = FEW ? 128 / FEW : 2;
+                mbar_arrive_expect_tx(bar, (FEW ? COPIES : two ? 2 : 1) * S::NH * p.rows * 128);
 #pragma unroll
-                for (int half = 0; half < (FEW ? 1 : 2); ++half)
-                    if (half == 0 || two)
+                for (int i = 0; i < COPIES; ++i)
+                    if (FEW || i == 0 || two)
 #pragma unroll
                         for (int c = 0; c < S::NH; ++c)
-                            tma_load_3d(smem_u32(sm.q[half]) + c * S::PART, tq, bar, 64 * c,
-                                        u.h * p.G, tok + half * p.tokens);
+                            tma_load_3d(smem_u32(sm.q[FEW ? 0 : i]) + c * S::PART + i * FEW * 128, tq,
+                                        bar, 64 * c, u.h * p.G, tok + (FEW ? 0 : i * p.tokens));
                 ++queries;
             }
         }
@@ -222,7 +223,7 @@ __device__ __forceinline__ bool landed(Smem<D> &sm, int t, const DevCtx &ctx, vo
 }
 
 // S of one half, a tile at a time, when P V of the half's tile before has read its P. A warp.
-template <int D, bool FEW>
+template <int D, int FEW>
 __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int half,
                         const DevCtx &ctx) {
     using S = Smem<D>;
@@ -292,7 +293,7 @@ __device__ void issue_s(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int ha
 }
 
 // P V of one half, 64 keys at a time. A warp.
-template <int D, bool FEW>
+template <int D, int FEW>
 __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int half,
                          const DevCtx &ctx) {
     using S = Smem<D>;
@@ -358,138 +359,179 @@ __device__ void issue_pv(const CrossParams &p, Smem<D> &sm, uint32_t tmem, int h
     bar_wait(smem_u32(&sm.drain[2 + half]), 0, ctx, &zero);
 }
 
-// 16-byte piece c of row r of the O that half 1 leaves for half 0 (no two rows of a warp in one bank).
-template <int D> __device__ __forceinline__ float4 *merge_at(Smem<D> &sm, int r, int c) {
-    constexpr int N = D / 4;
-    return reinterpret_cast<float4 *>(sm.q[1]) + r * N + (c ^ (r & (N - 1)));
+__device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(a),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+}
+// C columns of S, as W calls of a width that there is; and C / 2 of P.
+template <int C> __device__ __forceinline__ void load_s(uint32_t at, uint32_t (&x)[C]) {
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i) {
+        uint32_t r[16];
+        tmem_ld16(at + 16u * i, r);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[16 * i + e] = r[e];
+    }
+}
+template <> __device__ __forceinline__ void load_s<64>(uint32_t at, uint32_t (&x)[64]) {
+    tmem_ld32(at, *reinterpret_cast<uint32_t (*)[32]>(&x[0]));
+    tmem_ld32(at + 32u, *reinterpret_cast<uint32_t (*)[32]>(&x[32]));
+}
+template <int C> __device__ __forceinline__ void store_p(uint32_t at, const uint32_t (&w)[C / 2]) {
+#pragma unroll
+    for (int i = 0; i < C / 16; ++i) tmem_st8(at + 8u * i, w + 8 * i);
+}
+template <> __device__ __forceinline__ void store_p<64>(uint32_t at, const uint32_t (&w)[32]) {
+    tmem_st32(at, w);
 }
 
-template <int D, bool FEW>
-__device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
-                                        const DevCtx &ctx) {
-    constexpr int ROWS = FEW ? FEW_ROWS : 256;
+// A row's running softmax over its columns of S, C at a time.
+struct Row {
+    float m, l;
+    bool far;    // some row's m is so large that fp32 must subtract it exactly
+    bool fresh;  // some row has seen no key yet
+};
+
+// One step: P of the C columns x, packed, and their sum into l. `there`: how many of the
+// columns are keys; key0: the first is the sequence's first, with a biased logit. rescale(alpha)
+// is called (by whole warps) where m moves and O with it; returns false if that gave up.
+template <int C, typename F>
+__device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], uint32_t (&pw)[C / 2], float sx,
+                                      int there, bool key0, float sink, F rescale) {
+    if (there < C) {
+#pragma unroll
+        for (int e = 0; e < C; ++e) hide_unless(x[e], e < there);
+    }
+    bool moves = row.fresh;
+    float sum;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+        if (moves) {  // m from these columns, and O and l in its terms
+            float mx = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < C; e += 2)
+                mx = max3(mx, e == 0 && key0 ? -INFINITY : __uint_as_float(x[e]),
+                          __uint_as_float(x[e + 1]));
+            float top = mx * sx;
+            if (key0) top = fmaxf(top, __uint_as_float(x[0]) * sx + sink);
+            const float mn = fmaxf(row.m, top), alpha = ex2(row.m - mn);
+            row.m = mn;
+            row.l *= alpha;
+            row.fresh = __any_sync(0xffffffffu, row.m == NOTHING);
+            row.far = __any_sync(0xffffffffu, row.m != NOTHING && fabsf(row.m) > FAR);
+            if (!rescale(alpha)) return false;
+        }
+        // P with m as it is, and its sum
+        const float off = row.m == NOTHING ? 0.f : -row.m;
+        if (row.far) {  // x - m in two roundings, as above: never above 0 there
+            sum = 0.f;
+#pragma unroll
+            for (int e = 0; e < C; e += 2) {
+                float a = __uint_as_float(x[e]) * sx;
+                if (e == 0 && key0) a += sink;
+                a = ex2(a + off);
+                const float b = ex2(__uint_as_float(x[e + 1]) * sx + off);
+                sum += a + b;
+                pw[e >> 1] = pack_bf16x2(a, b);
+            }
+        } else {
+            const uint64_t f2 = f2_pack(sx, sx), off2 = f2_pack(off, off);
+            uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
+#pragma unroll
+            for (int e = 0; e < C; e += 2) {
+                float a, b;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[e]), __uint_as_float(x[e + 1])), f2, off2),
+                          a, b);
+                if (e == 0 && key0) a += sink;
+                a = ex2(a);
+                b = ex2(b);
+                part[e >> 1 & 1] = f2_add(part[e >> 1 & 1], f2_pack(a, b));
+                pw[e >> 1] = pack_bf16x2(a, b);
+            }
+            float a, b;
+            f2_unpack(f2_add(part[0], part[1]), a, b);
+            sum = a + b;
+        }
+        // (after a move no value is above 2^(1/4), so there is no third pass)
+        moves = pass == 0 && __any_sync(0xffffffffu, sum > SUM_LIMIT);
+        if (!moves) break;
+    }
+    row.l += sum;
+    return true;
+}
+
+// O of the warp's lanes times alpha.
+template <int D> __device__ __forceinline__ void scale_o(uint32_t at, float alpha) {
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        tmem_ld32(at + 32u * q, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+        tmem_st32(at + 32u * q, o);
+    }
+}
+
+template <int D>
+__device__ void softmax_many(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
+                             const DevCtx &ctx) {
+    constexpr int ROWS = 256;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = (warp - SOFTMAX) >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;  // row of the half
     const uint32_t tmem = tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
     volatile int *abort = &sm.abort;
-    if (quarter >= p.warps) return;  // no rows
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
     const int tok = p.token(r);
-    const float sx = p.scale_l2;
-    int x = 0, units = 0, merges = 0;  // this half's steps and units
+    int x = 0, units = 0;  // this half's steps and units
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const LineUnit u = sm.units.u[i % UNITS];
         __syncwarp();
         if (lane == 0) sm.units.release(i);
-        const int n = u.end - u.begin;
-        if (n == 0) return;
-        const int tokens = u.s.n - u.u * p.line.tokens - (FEW ? 0 : half * p.tokens);
-        if (FEW ? half >= n : tokens <= 0) continue;
+        if (u.begin == u.end) return;
+        const int tokens = u.s.n - u.u * p.line.tokens - half * p.tokens;
+        if (tokens <= 0) continue;
         const bool in = r < p.rows && tok < tokens;
         const int head = u.h * p.G + r - tok * p.G;
         const float sink = p.sinks && in ? sink_log2(__ldg(p.sinks + head)) : 0.f;
-        float m = NOTHING, l = 0.f;
-        bool far = false;   // some row's m is so large that fp32 must subtract it exactly
-        bool fresh = true;  // some row has seen no key yet
-        const int first = u.begin + (FEW ? half : 0);
+        Row row = {NOTHING, 0.f, false, true};
 #pragma unroll 1
-        for (int j = first; j < u.end; j += FEW ? 2 : 1) {
+        for (int j = u.begin; j < u.end; ++j) {
             const int nch = chunks(u, j);
 #pragma unroll 1
             for (int c = 0; c < nch; ++c, ++x) {
-                if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
-                tc_fence_after();
                 const int kpos0 = j * STATE_KEYS + c * CHUNK;
                 const uint32_t s_tmem = tmem + (uint32_t)((x & 1) * CHUNK);
-                const int there = u.s.len - kpos0;  // keys from here on
-                const bool key0 = p.sink_mode == 1 && kpos0 == 0;
-                uint32_t xs[2][32];
-                auto load = [&]() {
-                    tmem_ld32(s_tmem, xs[0]);
-                    tmem_ld32(s_tmem + 32u, xs[1]);
-                    tc_wait_ld();
-                    if (there < CHUNK) {
-#pragma unroll
-                        for (int e = 0; e < CHUNK; ++e) hide_unless(xs[e >> 5][e & 31], e < there);
-                    }
-                };
-                // m from the row's 64 keys, and O and l in its terms
-                auto move = [&]() -> bool {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int e = 0; e < CHUNK; e += 2)
-                        mx = max3(mx, e == 0 && key0 ? -INFINITY : __uint_as_float(xs[e >> 5][e & 31]),
-                                  __uint_as_float(xs[e >> 5][(e & 31) + 1]));
-                    float top = mx * sx;
-                    if (key0) top = fmaxf(top, __uint_as_float(xs[0][0]) * sx + sink);
-                    const float mn = fmaxf(m, top), alpha = ex2(m - mn);
-                    m = mn;
-                    l *= alpha;
-                    fresh = __any_sync(0xffffffffu, m == NOTHING);
-                    far = __any_sync(0xffffffffu, m != NOTHING && fabsf(m) > FAR);
-                    if (j > first || c > 0) {
-                        if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int q = 0; q < D / 32; ++q) {
-                            uint32_t o[32];
-                            tmem_ld32(tmem + O_COL + 32u * q, o);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                            tmem_st32(tmem + O_COL + 32u * q, o);
-                        }
-                    }
-                    return true;
-                };
-                uint32_t pw[32];
-                float sum;
-                bool moves = fresh;
-#pragma unroll 1
-                for (int pass = 0;; ++pass) {
-                    load();
-                    if (moves && !move()) return;
-                    // P of the row's 64 keys with m as it is, and their sum
-                    float fx = sx, off = m == NOTHING ? 0.f : -m;
-                    bool bias = key0;
-                    if (far) {  // x - m in two roundings, as move() has them: never above 0 there
-#pragma unroll
-                        for (int e = 0; e < CHUNK; ++e) {
-                            float y = __uint_as_float(xs[e >> 5][e & 31]) * sx;
-                            if (e == 0 && bias) y += sink;
-                            xs[e >> 5][e & 31] = __float_as_uint(y + off);
-                        }
-                        fx = 1.f, off = 0.f, bias = false;
-                    }
-                    const uint64_t f2 = f2_pack(fx, fx), off2 = f2_pack(off, off);
-                    uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-                    for (int e = 0; e < CHUNK; e += 2) {
-                        float a, b;
-                        f2_unpack(f2_fma(f2_pack(__uint_as_float(xs[e >> 5][e & 31]),
-                                                 __uint_as_float(xs[e >> 5][(e & 31) + 1])),
-                                         f2, off2),
-                                  a, b);
-                        if (e == 0 && bias) a += sink;
-                        a = ex2(a);
-                        b = ex2(b);
-                        part[e >> 1 & 1] = f2_add(part[e >> 1 & 1], f2_pack(a, b));
-                        pw[e >> 1] = pack_bf16x2(a, b);
-                    }
-                    float a, b;
-                    f2_unpack(f2_add(part[0], part[1]), a, b);
-                    sum = a + b;
-                    // (after a move no value is above 2^(1/4), so there is no third pass)
-                    moves = pass == 0 && __any_sync(0xffffffffu, sum > SUM_LIMIT);
-                    if (!moves) break;
-                }
-                l += sum;
-                tmem_st32(s_tmem, pw);
+                if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
+                tc_fence_after();
+                uint32_t xs[CHUNK], pw[CHUNK / 2];
+                load_s(s_tmem, xs);
+                tc_wait_ld();
+                if (!weigh(row, xs, pw, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0,
+                           sink, [&](float alpha) {
+                               if (j == u.begin && c == 0) return true;  // no O yet
+                               if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
+                               tc_fence_after();
+                               scale_o<D>(tmem + O_COL, alpha);
+                               return true;
+                           }))
+                    return;
+                store_p<CHUNK>(s_tmem, pw);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -500,53 +542,17 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
         if (!wait(sm.o_full[half], units)) return;
         ++units;
         tc_fence_after();
-        const bool joined = FEW && n > 1;  // both halves worked on the unit
-        if (joined && half) {
-            if (merges >= 1 && !wait(sm.mg_empty, merges - 1)) return;
-            ++merges;
-            if (r < FEW_ROWS) sm.ml[r] = make_float2(m, l);
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tmem_ld32(tmem + O_COL + 32u * q, o);
-                tc_wait_ld();
-                if (r < FEW_ROWS)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        *merge_at<D>(sm, r, 8 * q + e) =
-                            make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                        __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_u32(&sm.mg_full));
-                mbar_arrive(smem_u32(&sm.o_empty[half]));
-            }
-            continue;
-        }
-        float a0 = 1.f, a1 = 0.f;  // the halves' weights
-        if (joined) {
-            if (!wait(sm.mg_full, merges)) return;
-            ++merges;
-            const float2 other = sm.ml[min(r, FEW_ROWS - 1)];
-            const float top = fmaxf(m, other.x);
-            a0 = ex2(m - top);
-            a1 = ex2(other.x - top);
-            m = top;
-            l = l * a0 + other.y * a1;
-        }
         const bool part = u.cut();
-        float inv = l == 0.f ? 0.f : 1.f / l;
-        const int rr = FEW ? r : half * p.rows + r;
-        const size_t slot = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + rr;
+        float inv = row.l == 0.f ? 0.f : 1.f / row.l;
+        const size_t slot =
+            ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * ROWS + half * p.rows + r;
         float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(ROWS)) + slot * D;
         const size_t orow =
-            (size_t)(u.s.t0 + u.u * p.line.tokens + (FEW ? 0 : half * p.tokens) + tok) * p.H + head;
+            (size_t)(u.s.t0 + u.u * p.line.tokens + half * p.tokens + tok) * p.H + head;
         if (in && part) {
-            part_sums(p.ws)[slot] = make_float2(m, l);
+            part_sums(p.ws)[slot] = make_float2(row.m, row.l);
         } else if (in) {
-            float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+            float lse2 = row.l == 0.f ? -INFINITY : row.m + log2f(row.l);
             if (p.sink_mode == 2) with_null_sink(sink, lse2, inv);
             if (p.lse) p.lse[orow] = lse2 * LN2;
         }
@@ -555,16 +561,6 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
             uint32_t o[32];
             tmem_ld32(tmem + O_COL + 32u * q, o);
             tc_wait_ld();
-            if (joined) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 v = *merge_at<D>(sm, min(r, FEW_ROWS - 1), 8 * q + e);
-                    o[4 * e] = __float_as_uint(__uint_as_float(o[4 * e]) * a0 + v.x * a1);
-                    o[4 * e + 1] = __float_as_uint(__uint_as_float(o[4 * e + 1]) * a0 + v.y * a1);
-                    o[4 * e + 2] = __float_as_uint(__uint_as_float(o[4 * e + 2]) * a0 + v.z * a1);
-                    o[4 * e + 3] = __float_as_uint(__uint_as_float(o[4 * e + 3]) * a0 + v.w * a1);
-                }
-            }
             if (in && part) {
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
@@ -587,14 +583,249 @@ __device__ void softmax(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-            if (joined) mbar_arrive(smem_u32(&sm.mg_empty));
-            mbar_arrive(smem_u32(&sm.o_empty[half]));
-        }
+        if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty[half]));
     }
 }
 
-template <int D, bool FEW>
+// A row's weights over `n` partial results with maxima m and sums z get(i): the maximum and sum
+// of all (and of a null logit); returns, in lane i < 32, part i's weight z_i 2^(m_i - m).
+template <typename G>
+__device__ __forceinline__ float join_weights(int n, float sink, bool null_sink, float &m, float &z,
+                                              G get) {
+    const int lane = threadIdx.x & 31;
+    float2 mine = lane < n ? get(lane) : make_float2(NOTHING, 0.f);
+    m = fmaxf(null_sink ? sink : NOTHING, mine.x);
+    for (int i = 32 + lane; i < n; i += 32) m = fmaxf(m, get(i).x);
+    m = warp_max(fmaxf(m, NOTHING));
+    const float w = mine.y * ex2(mine.x - m);
+    z = warp_sum(w);
+    for (int i = 32; i < n; i += 32) {
+        const float2 s = i + lane < n ? get(i + lane) : make_float2(NOTHING, 0.f);
+        z += warp_sum(s.y * ex2(s.x - m));
+    }
+    if (null_sink) z += ex2(sink - m);
+    return w;
+}
+
+template <int D> __device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *acc, int lane) {
+    constexpr int E = D / 32;
+    uint32_t w[E / 2];
+#pragma unroll
+    for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16x2(acc[e], acc[e + 1]);
+    if constexpr (E == 4) *reinterpret_cast<uint2 *>(o + lane * E) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t *>(o + lane * E) = w[0];
+}
+
+template <int D, int FEW>
+__device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
+                            const DevCtx &ctx) {
+    using S = Smem<D>;
+    constexpr int COPIES = 128 / FEW, C = CHUNK / COPIES;  // of the rows; a warp's columns of a step
+    constexpr int STREAMS = 2 * COPIES, E = D / 32;        // softmaxes of a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp - SOFTMAX;
+    const int half = w >> 2, quarter = warp & 3;
+    const int copy = quarter * 32 / FEW, r = (quarter * 32 + lane) % FEW, stream = half * COPIES + copy;
+    const uint32_t tmem = tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
+    volatile int *abort = &sm.abort;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
+    };
+    int met = 0;  // the eight warps meet; what they wrote before, all see behind it
+    auto arrive = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
+    };
+    auto meet = [&]() {
+        arrive();
+        return wait(sm.meet, met++);
+    };
+    // rows whose O fits into the buffer at once, and columns of each
+    const int cap = p.rows <= 8 ? 8 : p.rows <= 16 ? 16 : FEW;
+    const int width = min(D, (int)S::TILE_BYTES / (STREAMS * cap * 4));
+    float *const buffer = reinterpret_cast<float *>(sm.q[1]);
+    // 16-byte piece c of row r of a stream (the lanes that write in different banks)
+    auto piece = [&](int stream, int r, int c) {
+        const int n = width / 4, sw = min(n, 8) - 1;
+        return reinterpret_cast<float4 *>(buffer) + (stream * cap + r) * n + (c ^ (r & sw));
+    };
+    const int tok = p.token(r);
+    int x = 0, units = 0;  // this half's steps and units
+    bool split = false;    // a meeting that has been arrived at and not been waited for
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
+        const LineUnit u = sm.units.u[i % UNITS];
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
+        const int n = u.end - u.begin;
+        if (n == 0) return;
+        const int rows = min(p.tokens, u.s.n - u.u * p.line.tokens) * p.G;  // of the unit
+        const int head = u.h * p.G + r - tok * p.G;
+        const float sink = p.sink_mode == 1 && r < rows ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+        Row row = {NOTHING, 0.f, false, true};
+        const int first = u.begin + half;
+#pragma unroll 1
+        for (int j = first; j < u.end; j += 2) {
+            const int nch = chunks(u, j);
+#pragma unroll 1
+            for (int c = 0; c < nch; ++c, ++x) {
+                const int kpos0 = j * STATE_KEYS + c * CHUNK + copy * C;
+                const uint32_t s_tmem = tmem + (uint32_t)((x & 1) * CHUNK);
+                if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
+                tc_fence_after();
+                uint32_t xs[C], pw[C / 2];
+                load_s(s_tmem + (uint32_t)(copy * C), xs);
+                tc_wait_ld();
+                {  // the other warps' keys
+                    const uint32_t zero[C / 2] = {};
+#pragma unroll
+                    for (int k = 1; k < COPIES; ++k)
+                        store_p<C>(s_tmem + (uint32_t)(((copy + k) % COPIES) * (C / 2)), zero);
+                }
+                if (!weigh(row, xs, pw, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0,
+                           sink, [&](float alpha) {
+                               if (j == first && c == 0) return true;  // no O yet
+                               if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
+                               tc_fence_after();
+                               scale_o<D>(tmem + O_COL, alpha);
+                               return true;
+                           }))
+                    return;
+                store_p<C>(s_tmem + (uint32_t)(copy * (C / 2)), pw);
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][x & 1]));
+            }
+        }
+        // ---- the unit's end: the streams' O through shared memory, `width` columns at a time; then
+        // a warp takes a row, its columns spread over the lanes
+        const bool worked = half < n;
+        if (worked) {
+            if (!wait(sm.o_full[half], units)) return;
+            ++units;
+            tc_fence_after();
+        }
+        if (split && !wait(sm.meet, met++)) return;  // all have read what the buffer held
+        sm.ml[stream * FEW + r] = make_float2(row.m, row.l);
+        const bool cut = u.cut();
+        const size_t slot0 = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * FEW;
+        const int t0 = u.s.t0 + u.u * p.line.tokens;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += width) {
+            if (c0 > 0 && !meet()) return;
+#pragma unroll 1
+            for (int c = 0; c < width; c += 16) {
+                uint32_t o[16];
+                if (worked) {
+                    tmem_ld16(tmem + O_COL + (uint32_t)(c0 + c), o);
+                    tc_wait_ld();
+                }
+                if (r < rows) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *piece(stream, r, c / 4 + e) =
+                            worked ? make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
+                                                 __uint_as_float(o[4 * e + 2]),
+                                                 __uint_as_float(o[4 * e + 3]))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            }
+            if (c0 + width >= D && worked) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty[half]));
+            }
+            if (!meet()) return;
+#pragma unroll 1
+            for (int q = w; q < rows; q += 8) {
+                float m, z;
+                join_weights(STREAMS, 0.f, false, m, z, [&](int i) { return sm.ml[i * FEW + q]; });
+                const int tq = p.token(q), hq = u.h * p.G + q - tq * p.G;
+                const size_t orow = (size_t)(t0 + tq) * p.H + hq;
+                float lse2 = z == 0.f ? -INFINITY : m + log2f(z), inv = z == 0.f ? 0.f : 1.f / z;
+                if (!cut && p.sink_mode == 2) with_null_sink(sink_log2(__ldg(p.sinks + hq)), lse2, inv);
+                if (c0 == 0 && lane == 0) {
+                    // (a stream without keys has m = NOTHING, which no key may outweigh)
+                    if (cut) part_sums(p.ws)[slot0 + q] = make_float2(m, z);
+                    else if (p.lse) p.lse[orow] = lse2 * LN2;
+                }
+                float acc[E] = {};
+                const bool mine = lane * E < width;  // (fewer columns than lanes in a narrow pass)
+#pragma unroll
+                for (int st = 0; st < STREAMS; ++st) {
+                    // the unnormalised O weighs 2^(m_st - m)
+                    const float f = ex2(sm.ml[st * FEW + q].x - m);
+                    if (!mine) continue;
+                    const float *at = reinterpret_cast<const float *>(piece(st, q, lane * E / 4)) +
+                                      (lane * E & 3);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, at[e], acc[e]);
+                }
+                if (!mine) continue;
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] *= inv;
+                if (cut) {
+                    float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(FEW)) +
+                                  (slot0 + q) * D + c0 + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) prow[e] = acc[e];
+                } else {
+                    store_row<D>(p.o + orow * D + c0, acc, lane);
+                }
+            }
+        }
+        if (cut) {  // the last of the unit's pieces to get here joins them
+            __threadfence();
+            if (!meet()) return;
+            if (w == 0 && lane == 0) {
+                asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+                sm.last = atomicAdd(join_counters(p.ws) + u.c0, 1u) == (unsigned)u.parts - 1;
+            }
+            if (!meet()) return;
+            if (sm.last) {
+                __threadfence();
+                const float2 *sums = part_sums(p.ws);
+                const float *prows = reinterpret_cast<const float *>(p.ws + plan_rows_offset(FEW));
+                // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ..
+                auto slot = [&](int i) { return ((size_t)(u.c0 + i) * 2 + (i == 0 ? 1 : 0)) * FEW; };
+#pragma unroll 1
+                for (int q = w; q < rows; q += 8) {
+                    const int tq = p.token(q), hq = u.h * p.G + q - tq * p.G;
+                    const size_t orow = (size_t)(t0 + tq) * p.H + hq;
+                    const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + hq)) : 0.f;
+                    float m, z;
+                    auto get = [&](int i) { return __ldcg(sums + slot(i) + q); };
+                    const float a = join_weights(u.parts, null, p.sink_mode == 2, m, z, get);
+                    // (over their sum, so that values near fp32's largest do not overflow)
+                    const float inv = z == 0.f ? 0.f : 1.f / z;
+                    float acc[E] = {};
+                    for (int i0 = 0; i0 < u.parts; i0 += 32) {
+                        float f = a;
+                        if (i0 > 0) {
+                            const float2 s = i0 + lane < u.parts ? get(i0 + lane) : make_float2(m, 0.f);
+                            f = s.y * ex2(s.x - m);
+                        }
+                        f *= inv;
+                        const int cnt = min(32, u.parts - i0);
+#pragma unroll 4
+                        for (int k = 0; k < cnt; ++k) {
+                            const float fk = __shfl_sync(0xffffffffu, f, k);
+                            const float *at = prows + (slot(i0 + k) + q) * D + lane * E;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, __ldcg(at + e), acc[e]);
+                        }
+                    }
+                    store_row<D>(p.o + orow * D, acc, lane);
+                    if (p.lse && lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
+                }
+            }
+        }
+        arrive();
+        split = true;
+    }
+}
+
+template <int D, int FEW>
 __global__ void __launch_bounds__(NTHREADS, 1)
 cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
              const __grid_constant__ CUtensorMap tv, const __grid_constant__ CrossParams p,
@@ -603,7 +834,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     using S = Smem<D>;
     S &sm = *reinterpret_cast<S *>(dsmem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (!FEW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
@@ -618,35 +849,38 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 mbar_init(smem_u32(&sm.s_full[lane][b]), 1);
-                mbar_init(smem_u32(&sm.p_full[lane][b]), p.warps);
+                mbar_init(smem_u32(&sm.p_full[lane][b]), 4);
                 mbar_init(smem_u32(&sm.pv_done[lane][b]), 1);
             }
             mbar_init(smem_u32(&sm.o_full[lane]), 1);
-            mbar_init(smem_u32(&sm.o_empty[lane]), p.warps);
+            mbar_init(smem_u32(&sm.o_empty[lane]), 4);
             mbar_init(smem_u32(&sm.drain[lane]), 1);
             mbar_init(smem_u32(&sm.drain[2 + lane]), 1);
         }
         if (lane == 0) {
             mbar_init(smem_u32(&sm.q_full), 1);
             mbar_init(smem_u32(&sm.q_empty), 2);
-            mbar_init(smem_u32(&sm.mg_full), p.warps);
-            mbar_init(smem_u32(&sm.mg_empty), p.warps);
+            mbar_init(smem_u32(&sm.meet), 8);
             sm.abort = 0;
             sm.issued = 0;
         }
-        sm.units.init(4 + 1 + 2 * p.warps, lane);  // MMA issuers, tails, softmax
+        sm.units.init(4 + 1 + 8, lane);  // MMA issuers, tails, softmax
         fence_mbar_init();
-    }
-    if (warp == 1) {
+    } else if (warp == 1) {
         tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
         tmem_relinquish();
+    } else if (warp == 3 && lane < 3) {
+        prefetch_tmap(lane == 0 ? &tk : lane == 1 ? &tv : &tq);
+    } else if (warp >= SOFTMAX) {  // rows of Q that no box writes: their S is 0
+        constexpr int COPIES = FEW ? 128 / FEW : 2, ROWS = FEW ? FEW : 128;
+        const int free = (ROWS - p.rows) * 8;
+        for (int i = 0; i < COPIES * S::NH; ++i)
+            for (int e = threadIdx.x - SOFTMAX * 32; e < free; e += NTHREADS - SOFTMAX * 32)
+                *reinterpret_cast<uint4 *>(sm.q[FEW ? 0 : i / S::NH] + i % S::NH * S::PART +
+                                           ((FEW ? i / S::NH * FEW : 0) + p.rows) * 128 + e * 16) =
+                    make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
-    // rows of Q that no box writes: their S is 0
-    for (int half = 0; half < (FEW ? 1 : 2); ++half)
-        for (int c = 0; c < S::NH; ++c)
-            for (int e = p.rows * 8 + threadIdx.x; e < 128 * 8; e += NTHREADS)
-                *reinterpret_cast<uint4 *>(sm.q[half] + c * S::PART + e * 16) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
     line_start<false>(p.line, sm.line, ctx);
     tc_fence_before();
     __syncthreads();
@@ -667,31 +901,45 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         __syncwarp();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        softmax<D, FEW>(p, sm, tmem, ctx);
+        if constexpr (FEW) softmax_few<D, FEW>(p, sm, tmem, ctx);
+        else softmax_many<D>(p, sm, tmem, ctx);
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
+    if (threadIdx.x == 0) {
+        // (no CTA ends before the counters are zero: they are the next call's then)
+        if (FEW) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
-// Whether a sequence's rows of a KV head are few enough for the form in which the halves take
-// every other tile.
-bool few_rows(int max_q_len, int G) { return (long long)max(1, max_q_len) * G <= FEW_ROWS; }
+// Zeroes a call's join counters, which lie in its workspace so that no call meets another
+// one's: the kernel, its programmatic dependent, starts beside it and waits for it before a
+// piece arrives.
+__global__ void __launch_bounds__(MAX_PIECES) zero_cross_counters(uint8_t *ws) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    join_counters(ws)[threadIdx.x] = 0;
+}
 
-template <int D, bool FEW>
+// Rows of a unit in the FEW form, or 0 where a sequence has more of a KV head.
+int few_rows(int max_q_len, int G) {
+    const long long rows = (long long)max(1, max_q_len) * G;
+    return rows <= 32 ? 32 : rows <= 64 ? 64 : 0;
+}
+
+template <int D, int FEW>
 cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
-    constexpr int ROWS = FEW ? FEW_ROWS : 256;
+    constexpr int ROWS = FEW ? FEW : 256;
     const int G = a.H / a.Hkv;
     CrossParams p{};
     p.H = a.H;
     p.G = G;
-    p.tokens = FEW ? min(FEW_ROWS / G, max(1, a.max_q_len)) : 128 / G;
+    p.tokens = FEW ? min(FEW / G, max(1, a.max_q_len)) : 128 / G;
     p.rows = p.tokens * G;
-    p.warps = (p.rows + 31) / 32;
     p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
                       FEW ? p.tokens : 2 * p.tokens, FEW ? 1 : 3,
                       a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D)};
@@ -714,11 +962,24 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     const int grid = min(dev.sm_count, MAX_PIECES);
     if (verbose())
-        fprintf(stderr, "sattn: cross_kernel<%d, %d> grid=%d rows=%d split=%d\n", D, (int)FEW, grid,
+        fprintf(stderr, "sattn: cross_kernel<%d, %d> grid=%d rows=%d split=%d\n", D, FEW, grid,
                 p.rows, p.line.split);
-    cross_kernel<D, FEW><<<grid, NTHREADS, sizeof(Smem<D>), s>>>(tq, tk, tv, p, make_ctx(dev));
-    e = cudaGetLastError();
-    if (e != cudaSuccess || !p.line.split) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(NTHREADS);
+    cfg.dynamicSmemBytes = sizeof(Smem<D>);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    if (FEW && p.line.split) {
+        zero_cross_counters<<<1, MAX_PIECES, 0, s>>>(p.ws);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        cfg.numAttrs = 1;
+    }
+    e = cudaLaunchKernelEx(&cfg, cross_kernel<D, FEW>, tq, tk, tv, p, make_ctx(dev));
+    if (e != cudaSuccess || FEW || !p.line.split) return e;
     PagedArgs j{};  // what the join looks at
     j.H = a.H;
     j.Hkv = a.Hkv;
@@ -734,13 +995,19 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
 }  // namespace
 
 size_t cross_tc_workspace(int max_q_len, int G, int d) {
-    return plan_workspace(few_rows(max_q_len, G) ? FEW_ROWS : 256, d);
+    const int few = few_rows(max_q_len, G);
+    return plan_workspace(few ? few : 256, d);
 }
 
 cudaError_t launch_cross_tc(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
-    if (few_rows(a.max_q_len, a.H / a.Hkv))
-        return a.d == 64 ? launch<64, true>(a, dev, s) : launch<128, true>(a, dev, s);
-    return a.d == 64 ? launch<64, false>(a, dev, s) : launch<128, false>(a, dev, s);
+    const int few = few_rows(a.max_q_len, a.H / a.Hkv);
+    if (a.d == 64)
+        return few == 32   ? launch<64, 32>(a, dev, s)
+               : few == 64 ? launch<64, 64>(a, dev, s)
+                           : launch<64, 0>(a, dev, s);
+    return few == 32   ? launch<128, 32>(a, dev, s)
+           : few == 64 ? launch<128, 64>(a, dev, s)
+                       : launch<128, 0>(a, dev, s);
 }
 
 }  // namespace sattn
