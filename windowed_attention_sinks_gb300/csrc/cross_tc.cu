@@ -39,6 +39,7 @@ namespace {
 constexpr int NTHREADS = 512;
 constexpr int SOFTMAX = 8;   // first softmax warp
 constexpr int UNITS = 4;     // units handed on ahead
+constexpr int ADDERS = 2;    // warps that add up a unit's streams (FEW)
 constexpr int CHUNK = 64;    // keys whose P is handed on at a time
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
 constexpr float FAR = 1 << 20;  // m up to which x - m may be taken in one rounding
@@ -71,13 +72,12 @@ template <int D> struct alignas(1024) Smem {
     uint8_t kv[R][TILE_BYTES];
     LineStart line;
     LineRing<UNITS> units;
-    float2 ml[256];  // FEW: the warps' m and l
+    float2 ml[256];  // FEW: the streams' m and l
     uint64_t full[R], empty[R], raw[R];
-    uint64_t q_full, q_empty, meet;
+    uint64_t q_full, q_empty, meet, out_full, out_empty;
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], o_full[2], o_empty[2], drain[4];
     uint32_t tmem_base;
     int issued;  // loads into the ring so far
-    int last;    // FEW: whether this piece joins the unit's
     int abort;
 };
 
@@ -121,6 +121,23 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
         if (u.begin == u.end) continue;
         ok = sm.units.put(index, u, ctx, abort);
         const bool tail = ragged(u);
+        auto ask = [&]() {  // for the unit's queries
+            if (index >= 1) ok = ok && bar_wait(smem_u32(&sm.q_empty), (index - 1) & 1, ctx, abort);
+            if (!ok) return;
+            const uint32_t bar = smem_u32(&sm.q_full);
+            const int tok = u.s.t0 + u.u * p.line.tokens;
+            const bool two = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
+            constexpr int COPIES = FEW ? 128 / FEW : 2;
+            mbar_arrive_expect_tx(bar, (FEW ? COPIES : two ? 2 : 1) * S::NH * p.rows * 128);
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i)
+                if (FEW || i == 0 || two)
+#pragma unroll
+                    for (int c = 0; c < S::NH; ++c)
+                        tma_load_3d(smem_u32(sm.q[FEW ? 0 : i]) + c * S::PART + i * FEW * 128, tq, bar,
+                                    64 * c, u.h * p.G, tok + (FEW ? 0 : i * p.tokens));
+            ++queries;
+        };
 #pragma unroll 1
         for (int j = u.begin; j < u.end && ok; ++j) {
 #pragma unroll
@@ -141,23 +158,8 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
                     tma_load_3d(smem_u32(sm.kv[st]) + c * S::PART, kv ? tv : tk, bar, 64 * c, u.h,
                                 u.s.s0 + j * STATE_KEYS);
                 count_set(smem_u32(&sm.issued), t + 1);
-            }
-            if (j == u.begin && ok) {  // behind the first tile, which need not wait for it
-                if (index >= 1) ok = bar_wait(smem_u32(&sm.q_empty), (index - 1) & 1, ctx, abort);
-                if (!ok) break;
-                const uint32_t bar = smem_u32(&sm.q_full);
-                const int tok = u.s.t0 + u.u * p.line.tokens;
-                const bool two = !FEW && u.s.n - u.u * p.line.tokens > p.tokens;
-                constexpr int COPIES = FEW ? 128 / FEW : 2;
-                mbar_arrive_expect_tx(bar, (FEW ? COPIES : two ? 2 : 1) * S::NH * p.rows * 128);
-#pragma unroll
-                for (int i = 0; i < COPIES; ++i)
-                    if (FEW || i == 0 || two)
-#pragma unroll
-                        for (int c = 0; c < S::NH; ++c)
-                            tma_load_3d(smem_u32(sm.q[FEW ? 0 : i]) + c * S::PART + i * FEW * 128, tq,
-                                        bar, 64 * c, u.h * p.G, tok + (FEW ? 0 : i * p.tokens));
-                ++queries;
+                // Q behind the first K; later ones' behind the first tile, which need not wait for it
+                if (j == u.begin && kv == (index > 0)) ask();
             }
         }
         ++index;
@@ -616,41 +618,39 @@ template <int D> __device__ __forceinline__ void store_row(__nv_bfloat16 *o, con
     else *reinterpret_cast<uint32_t *>(o + lane * E) = w[0];
 }
 
+// Where the streams' O of a unit's rows lie in shared memory: `cap` rows, `width` columns at a time.
+template <int D, int FEW> struct Out {
+    static constexpr int STREAMS = 256 / FEW;
+    int cap, width;
+    float4 *buffer;
+    __device__ __forceinline__ Out(const CrossParams &p, Smem<D> &sm) {
+        cap = p.rows <= 8 ? 8 : p.rows <= 16 ? 16 : FEW;
+        width = min(D, (int)Smem<D>::TILE_BYTES / (STREAMS * cap * 4));
+        buffer = reinterpret_cast<float4 *>(sm.q[1]);
+    }
+    // 16-byte piece c of row r of a stream (neighbouring rows' in different banks)
+    __device__ __forceinline__ float4 *piece(int stream, int r, int c) const {
+        const int n = width / 4, sw = min(n, 8) - 1;
+        return buffer + (stream * cap + r) * n + (c ^ (r & sw));
+    }
+};
+
 template <int D, int FEW>
 __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_base,
                             const DevCtx &ctx) {
-    using S = Smem<D>;
     constexpr int COPIES = 128 / FEW, C = CHUNK / COPIES;  // of the rows; a warp's columns of a step
-    constexpr int STREAMS = 2 * COPIES, E = D / 32;        // softmaxes of a row
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp - SOFTMAX;
-    const int half = w >> 2, quarter = warp & 3;
+    constexpr int STREAMS = 2 * COPIES;                    // softmaxes of a row
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = (warp - SOFTMAX) >> 2, quarter = warp & 3;
     const int copy = quarter * 32 / FEW, r = (quarter * 32 + lane) % FEW, stream = half * COPIES + copy;
     const uint32_t tmem = tmem_base + (uint32_t)half * HALF_COLS + ((uint32_t)(quarter * 32) << 16);
     volatile int *abort = &sm.abort;
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
-    int met = 0;  // the eight warps meet; what they wrote before, all see behind it
-    auto arrive = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
-    };
-    auto meet = [&]() {
-        arrive();
-        return wait(sm.meet, met++);
-    };
-    // rows whose O fits into the buffer at once, and columns of each
-    const int cap = p.rows <= 8 ? 8 : p.rows <= 16 ? 16 : FEW;
-    const int width = min(D, (int)S::TILE_BYTES / (STREAMS * cap * 4));
-    float *const buffer = reinterpret_cast<float *>(sm.q[1]);
-    // 16-byte piece c of row r of a stream (the lanes that write in different banks)
-    auto piece = [&](int stream, int r, int c) {
-        const int n = width / 4, sw = min(n, 8) - 1;
-        return reinterpret_cast<float4 *>(buffer) + (stream * cap + r) * n + (c ^ (r & sw));
-    };
+    const Out<D, FEW> out(p, sm);
     const int tok = p.token(r);
-    int x = 0, units = 0;  // this half's steps and units
-    bool split = false;    // a meeting that has been arrived at and not been waited for
+    int x = 0, units = 0, meets = 0, outs = 0;  // this half's steps and units; all units, passes
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
         const LineUnit u = sm.units.u[i % UNITS];
@@ -660,7 +660,8 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
         if (n == 0) return;
         const int rows = min(p.tokens, u.s.n - u.u * p.line.tokens) * p.G;  // of the unit
         const int head = u.h * p.G + r - tok * p.G;
-        const float sink = p.sink_mode == 1 && r < rows ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+        // of key 0, or of the denominator
+        const float bias = p.sinks && r < rows ? sink_log2(__ldg(p.sinks + head)) : 0.f;
         Row row = {NOTHING, 0.f, false, true};
         const int first = u.begin + half;
 #pragma unroll 1
@@ -682,7 +683,7 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
                         store_p<C>(s_tmem + (uint32_t)(((copy + k) % COPIES) * (C / 2)), zero);
                 }
                 if (!weigh(row, xs, pw, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0,
-                           sink, [&](float alpha) {
+                           bias, [&](float alpha) {
                                if (j == first && c == 0) return true;  // no O yet
                                if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
                                tc_fence_after();
@@ -697,24 +698,38 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
                 if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[half][x & 1]));
             }
         }
-        // ---- the unit's end: the streams' O through shared memory, `width` columns at a time; then
-        // a warp takes a row, its columns spread over the lanes
-        const bool worked = half < n;
+        // ---- the unit's end. Every thread weighs its stream's O by 2^(m - the row's m) / the
+        // row's sum; they go through shared memory to the warps that add them up
+        const bool worked = half < n, cut = u.cut();
+        if (outs >= 1 && !wait(sm.out_empty, outs - 1)) return;  // the last unit's are added up
+        sm.ml[stream * FEW + r] = make_float2(row.m, row.l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.meet));
+        if (!wait(sm.meet, meets++)) return;
+        float m = NOTHING, z = 0.f;
+        {
+            float2 v[STREAMS];
+#pragma unroll
+            for (int st = 0; st < STREAMS; ++st) {
+                v[st] = sm.ml[st * FEW + r];
+                m = fmaxf(m, v[st].x);
+            }
+#pragma unroll
+            for (int st = 0; st < STREAMS; ++st) z = fmaf(v[st].y, ex2(v[st].x - m), z);
+        }
+        float lse2 = z == 0.f ? -INFINITY : m + __log2f(z), inv = z == 0.f ? 0.f : __fdividef(1.f, z);
+        if (!cut && p.sink_mode == 2) with_null_sink(bias, lse2, inv);
+        const float f = ex2(row.m - m) * inv;
         if (worked) {
             if (!wait(sm.o_full[half], units)) return;
             ++units;
             tc_fence_after();
         }
-        if (split && !wait(sm.meet, met++)) return;  // all have read what the buffer held
-        sm.ml[stream * FEW + r] = make_float2(row.m, row.l);
-        const bool cut = u.cut();
-        const size_t slot0 = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * FEW;
-        const int t0 = u.s.t0 + u.u * p.line.tokens;
 #pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += width) {
-            if (c0 > 0 && !meet()) return;
+        for (int c0 = 0; c0 < D; c0 += out.width, ++outs) {
+            if (c0 > 0 && !wait(sm.out_empty, outs - 1)) return;
 #pragma unroll 1
-            for (int c = 0; c < width; c += 16) {
+            for (int c = 0; c < out.width; c += 16) {
                 uint32_t o[16];
                 if (worked) {
                     tmem_ld16(tmem + O_COL + (uint32_t)(c0 + c), o);
@@ -723,105 +738,178 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
                 if (r < rows) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        *piece(stream, r, c / 4 + e) =
-                            worked ? make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                                 __uint_as_float(o[4 * e + 2]),
-                                                 __uint_as_float(o[4 * e + 3]))
+                        *out.piece(stream, r, c / 4 + e) =
+                            worked ? make_float4(__uint_as_float(o[4 * e]) * f,
+                                                 __uint_as_float(o[4 * e + 1]) * f,
+                                                 __uint_as_float(o[4 * e + 2]) * f,
+                                                 __uint_as_float(o[4 * e + 3]) * f)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
-            if (c0 + width >= D && worked) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sm.o_empty[half]));
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (worked && c0 + out.width >= D) mbar_arrive(smem_u32(&sm.o_empty[half]));
+                mbar_arrive(smem_u32(&sm.out_full));
             }
-            if (!meet()) return;
+        }
+    }
+}
+
+// E columns of fp32 that another CTA wrote.
+template <int E> __device__ __forceinline__ void load_row(const float *p, float (&v)[E]) {
+    if constexpr (E == 4) {
+        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    } else {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
+        v[0] = x.x, v[1] = x.y;
+    }
+}
+
+// Joins the parts of a cut unit, for its rows w, w + ADDERS, ...: two rows at a time, for the loads
+// in flight. Lane i holds part i's sums, the columns are spread over the lanes.
+template <int D, int FEW, typename F>
+__device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int parts, int rows, int w,
+                                           F orow) {
+    constexpr int E = D / 32, N = 2;
+    const int lane = threadIdx.x & 31;
+    const float2 *sums = part_sums(p.ws);
+    const float *prows = reinterpret_cast<const float *>(p.ws + plan_rows_offset(FEW));
+    // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ..
+    auto slot = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * FEW; };
 #pragma unroll 1
-            for (int q = w; q < rows; q += 8) {
-                float m, z;
-                join_weights(STREAMS, 0.f, false, m, z, [&](int i) { return sm.ml[i * FEW + q]; });
-                const int tq = p.token(q), hq = u.h * p.G + q - tq * p.G;
-                const size_t orow = (size_t)(t0 + tq) * p.H + hq;
-                float lse2 = z == 0.f ? -INFINITY : m + log2f(z), inv = z == 0.f ? 0.f : 1.f / z;
-                if (!cut && p.sink_mode == 2) with_null_sink(sink_log2(__ldg(p.sinks + hq)), lse2, inv);
-                if (c0 == 0 && lane == 0) {
-                    // (a stream without keys has m = NOTHING, which no key may outweigh)
-                    if (cut) part_sums(p.ws)[slot0 + q] = make_float2(m, z);
-                    else if (p.lse) p.lse[orow] = lse2 * LN2;
+    for (int q0 = w; q0 < rows; q0 += N * ADDERS) {
+        float m[N], z[N], inv[N], f[N], acc[N][E] = {};
+        size_t at[N];
+        int q[N];
+#pragma unroll
+        for (int a = 0; a < N; ++a) {  // (a row behind the last is the one before, not written)
+            q[a] = q0 + a * ADDERS < rows ? q0 + a * ADDERS : q0;
+            at[a] = orow(q[a]);
+        }
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+            const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + (int)(at[a] % p.H))) : 0.f;
+            f[a] = join_weights(parts, null, p.sink_mode == 2, m[a], z[a],
+                                [&](int i) { return __ldcg(sums + slot(i) + q[a]); });
+            // (over their sum, so that values near fp32's largest do not overflow)
+            inv[a] = z[a] == 0.f ? 0.f : 1.f / z[a];
+        }
+#pragma unroll 1
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+#pragma unroll
+            for (int a = 0; a < N; ++a) {
+                if (i0 > 0) {
+                    const float2 s = i0 + lane < parts ? __ldcg(sums + slot(i0 + lane) + q[a])
+                                                       : make_float2(m[a], 0.f);
+                    f[a] = s.y * ex2(s.x - m[a]);
                 }
+                f[a] *= inv[a];
+            }
+            const int cnt = min(32, parts - i0);
+#pragma unroll 1
+            for (int k = 0; k < cnt; k += 4) {
+                float x[4][N][E];
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                    for (int a = 0; a < N; ++a)
+                        load_row<E>(prows + (slot(i0 + min(k + d, cnt - 1)) + q[a]) * D + lane * E,
+                                    x[d][a]);
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                    for (int a = 0; a < N; ++a) {
+                        const float fk = __shfl_sync(0xffffffffu, f[a], min(k + d, 31));
+                        if (k + d < cnt)
+#pragma unroll
+                            for (int e = 0; e < E; ++e) acc[a][e] = fmaf(fk, x[d][a][e], acc[a][e]);
+                    }
+            }
+        }
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+            if (q0 + a * ADDERS >= rows) break;
+            store_row<D>(p.o + at[a] * D, acc[a], lane);
+            if (p.lse && lane == 0)
+                p.lse[at[a]] = z[a] == 0.f ? -INFINITY : (m[a] + log2f(z[a])) * LN2;
+        }
+    }
+}
+
+// Adds up the streams of a unit's rows, a warp a row, its columns spread over the lanes, and
+// writes them; the last of a cut unit's pieces joins them.
+template <int D, int FEW>
+__device__ void add_up(const CrossParams &p, Smem<D> &sm, int w, const DevCtx &ctx) {
+    constexpr int STREAMS = 256 / FEW, E = D / 32;
+    const int lane = threadIdx.x & 31;
+    volatile int *abort = &sm.abort;
+    auto wait = [&](uint64_t &bar, int phase) {
+        return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
+    };
+    const Out<D, FEW> out(p, sm);
+    int outs = 0;
+    for (int i = 0;; ++i) {
+        if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
+        const LineUnit u = sm.units.u[i % UNITS];
+        __syncwarp();
+        if (lane == 0) sm.units.release(i);
+        if (u.begin == u.end) return;
+        const int rows = min(p.tokens, u.s.n - u.u * p.line.tokens) * p.G;
+        const bool cut = u.cut();
+        const size_t slot0 = ((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * FEW;
+        const int t0 = u.s.t0 + u.u * p.line.tokens;
+        auto orow = [&](int q) {  // of the output
+            const int tq = p.token(q);
+            return (size_t)(t0 + tq) * p.H + u.h * p.G + q - tq * p.G;
+        };
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += out.width, ++outs) {
+            if (!wait(sm.out_full, outs)) return;
+#pragma unroll 1
+            for (int q = w; q < rows; q += ADDERS) {
+                const size_t at = orow(q);
+                if (c0 == 0) {  // the row's maximum and sum, as its threads have them too
+                    float m, z;
+                    const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + (int)(at % p.H))) : 0.f;
+                    join_weights(STREAMS, null, p.sink_mode == 2 && !cut, m, z,
+                                 [&](int st) { return sm.ml[st * FEW + q]; });
+                    if (lane == 0 && cut) part_sums(p.ws)[slot0 + q] = make_float2(m, z);
+                    else if (lane == 0 && p.lse) p.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
+                }
+                if (lane * E >= out.width) continue;
                 float acc[E] = {};
-                const bool mine = lane * E < width;  // (fewer columns than lanes in a narrow pass)
 #pragma unroll
                 for (int st = 0; st < STREAMS; ++st) {
-                    // the unnormalised O weighs 2^(m_st - m)
-                    const float f = ex2(sm.ml[st * FEW + q].x - m);
-                    if (!mine) continue;
-                    const float *at = reinterpret_cast<const float *>(piece(st, q, lane * E / 4)) +
-                                      (lane * E & 3);
+                    const float *x = reinterpret_cast<const float *>(out.piece(st, q, lane * E / 4)) +
+                                     (lane * E & 3);
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, at[e], acc[e]);
+                    for (int e = 0; e < E; ++e) acc[e] += x[e];
                 }
-                if (!mine) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] *= inv;
                 if (cut) {
                     float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(FEW)) +
                                   (slot0 + q) * D + c0 + lane * E;
 #pragma unroll
                     for (int e = 0; e < E; ++e) prow[e] = acc[e];
                 } else {
-                    store_row<D>(p.o + orow * D + c0, acc, lane);
+                    store_row<D>(p.o + at * D + c0, acc, lane);
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sm.out_empty));
         }
-        if (cut) {  // the last of the unit's pieces to get here joins them
-            __threadfence();
-            if (!meet()) return;
-            if (w == 0 && lane == 0) {
-                asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-                sm.last = atomicAdd(join_counters(p.ws) + u.c0, 1u) == (unsigned)u.parts - 1;
-            }
-            if (!meet()) return;
-            if (sm.last) {
-                __threadfence();
-                const float2 *sums = part_sums(p.ws);
-                const float *prows = reinterpret_cast<const float *>(p.ws + plan_rows_offset(FEW));
-                // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ..
-                auto slot = [&](int i) { return ((size_t)(u.c0 + i) * 2 + (i == 0 ? 1 : 0)) * FEW; };
-#pragma unroll 1
-                for (int q = w; q < rows; q += 8) {
-                    const int tq = p.token(q), hq = u.h * p.G + q - tq * p.G;
-                    const size_t orow = (size_t)(t0 + tq) * p.H + hq;
-                    const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + hq)) : 0.f;
-                    float m, z;
-                    auto get = [&](int i) { return __ldcg(sums + slot(i) + q); };
-                    const float a = join_weights(u.parts, null, p.sink_mode == 2, m, z, get);
-                    // (over their sum, so that values near fp32's largest do not overflow)
-                    const float inv = z == 0.f ? 0.f : 1.f / z;
-                    float acc[E] = {};
-                    for (int i0 = 0; i0 < u.parts; i0 += 32) {
-                        float f = a;
-                        if (i0 > 0) {
-                            const float2 s = i0 + lane < u.parts ? get(i0 + lane) : make_float2(m, 0.f);
-                            f = s.y * ex2(s.x - m);
-                        }
-                        f *= inv;
-                        const int cnt = min(32, u.parts - i0);
-#pragma unroll 4
-                        for (int k = 0; k < cnt; ++k) {
-                            const float fk = __shfl_sync(0xffffffffu, f, k);
-                            const float *at = prows + (slot(i0 + k) + q) * D + lane * E;
-#pragma unroll
-                            for (int e = 0; e < E; ++e) acc[e] = fmaf(fk, __ldcg(at + e), acc[e]);
-                        }
-                    }
-                    store_row<D>(p.o + orow * D, acc, lane);
-                    if (p.lse && lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
-                }
-            }
+        if (!cut) continue;
+        // the last of the pieces' warps w to get here joins their rows
+        __threadfence();
+        int last = 0;
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
+            last = atomicAdd(join_counters(p.ws) + w * MAX_PIECES + u.c0, 1u) == (unsigned)u.parts - 1;
         }
-        arrive();
-        split = true;
+        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
+        __threadfence();
+        join_parts<D, FEW>(p, u.c0, u.parts, rows, w, orow);
     }
 }
 
@@ -839,7 +927,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
     }
-    if (warp == 2) {  // a lane a barrier
+    if (warp == 0) {  // a lane a barrier
         if (lane < S::R) {
             mbar_init(smem_u32(&sm.full[lane]), 1);
             mbar_init(smem_u32(&sm.empty[lane]), FEW ? 1 : 2);  // the halves' MMAs
@@ -861,11 +949,14 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             mbar_init(smem_u32(&sm.q_full), 1);
             mbar_init(smem_u32(&sm.q_empty), 2);
             mbar_init(smem_u32(&sm.meet), 8);
+            mbar_init(smem_u32(&sm.out_full), 8);
+            mbar_init(smem_u32(&sm.out_empty), ADDERS);
             sm.abort = 0;
             sm.issued = 0;
         }
-        sm.units.init(4 + 1 + 8, lane);  // MMA issuers, tails, softmax
+        sm.units.init(4 + 1 + 8 + (FEW ? ADDERS : 0), lane);  // MMA issuers, tails, softmax
         fence_mbar_init();
+        __syncwarp();
     } else if (warp == 1) {
         tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
         tmem_relinquish();
@@ -881,14 +972,16 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
                     make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
-    line_start<false>(p.line, sm.line, ctx);
+    if (!line_by_warp(p.line))
+        line_start<false>(p.line, sm.line, reinterpret_cast<long long *>(sm.ml), ctx);
     tc_fence_before();
-    __syncthreads();
+    set_up(warp == 0);
     tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
-    // registers: 256 threads x 56 + 256 x 200 = the 512 x 128 of the launch
+    if (warp == 0 && line_by_warp(p.line)) line_start_warp<false>(p.line, sm.line, ctx);
+    const uint32_t tmem = warp == 0 ? 0u : sm.tmem_base;  // (the loader has not waited for it)
+    // registers: 256 threads x 88 + 256 x 168 = the 512 x 128 of the launch
     if (warp < SOFTMAX) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             load_tiles<D, FEW>(p, &tq, &tk, &tv, sm, ctx);
         } else if (warp == 2) {
@@ -897,11 +990,13 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
             issue_s<D, FEW>(p, sm, tmem, warp >> 1, ctx);
         } else if (warp < 6) {
             issue_pv<D, FEW>(p, sm, tmem, warp & 1, ctx);
+        } else if (FEW) {
+            add_up<D, FEW ? FEW : 32>(p, sm, warp - 6, ctx);
         }
         __syncwarp();
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        if constexpr (FEW) softmax_few<D, FEW>(p, sm, tmem, ctx);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        if constexpr (FEW > 0) softmax_few<D, FEW>(p, sm, tmem, ctx);
         else softmax_many<D>(p, sm, tmem, ctx);
     }
     tc_fence_before();
@@ -920,8 +1015,9 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 // Zeroes a call's join counters, which lie in its workspace so that no call meets another
 // one's: the kernel, its programmatic dependent, starts beside it and waits for it before a
 // piece arrives.
-__global__ void __launch_bounds__(MAX_PIECES) zero_cross_counters(uint8_t *ws) {
+__global__ void __launch_bounds__(ADDERS *MAX_PIECES) zero_cross_counters(uint8_t *ws) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    static_assert(ADDERS * sizeof(unsigned) <= sizeof(PlanNote), "the counters' part of the workspace");
     join_counters(ws)[threadIdx.x] = 0;
 }
 
@@ -940,9 +1036,10 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.G = G;
     p.tokens = FEW ? min(FEW / G, max(1, a.max_q_len)) : 128 / G;
     p.rows = p.tokens * G;
-    p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
-                      FEW ? p.tokens : 2 * p.tokens, FEW ? 1 : 3,
-                      a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D)};
+    const int grid = min(dev.sm_count, MAX_PIECES);
+    p.line = line_args(a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
+                       FEW ? p.tokens : 2 * p.tokens, FEW && D == 128 ? 1 : 3,
+                       a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D), grid);
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sinks;
     p.sink_mode = a.sink_mode;
@@ -960,7 +1057,6 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = ensure_smem_attr((const void *)cross_kernel<D, FEW>, sizeof(Smem<D>), dev);
     if (e != cudaSuccess) return e;
-    const int grid = min(dev.sm_count, MAX_PIECES);
     if (verbose())
         fprintf(stderr, "sattn: cross_kernel<%d, %d> grid=%d rows=%d split=%d\n", D, FEW, grid,
                 p.rows, p.line.split);
@@ -974,7 +1070,7 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     if (FEW && p.line.split) {
-        zero_cross_counters<<<1, MAX_PIECES, 0, s>>>(p.ws);
+        zero_cross_counters<<<1, ADDERS * MAX_PIECES, 0, s>>>(p.ws);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         cfg.numAttrs = 1;
     }

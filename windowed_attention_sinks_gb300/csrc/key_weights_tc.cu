@@ -82,8 +82,6 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
     using S = Smem<D>;
     if ((threadIdx.x & 31) != 0) return;
     volatile int *abort = &sm.abort;
-    prefetch_tmap(tq);
-    prefetch_tmap(tk);
     LineIter<true> it(p.line, sm.line);
     if (p.line.split) {
         PlanNote n{};
@@ -385,7 +383,7 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
     }
-    if (warp == 2) {  // a lane a barrier
+    if (warp == 0) {  // a lane a barrier
         if (lane < TILES) {
 #pragma unroll
             for (int i = 0; i < S::KR; ++i) {
@@ -407,16 +405,20 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
         if (lane == 0) sm.abort = 0;
         sm.units.init(2 + 1 + 4 * TILES, lane);
         fence_mbar_init();
-    }
-    if (warp == 1) {
+        __syncwarp();
+    } else if (warp == 1) {
         tmem_alloc(smem_u32(&sm.tmem_base), TMEM_COLS);
         tmem_relinquish();
+    } else if (warp == 2 && lane < 2) {
+        prefetch_tmap(lane == 0 ? &tk : &tq);
     }
-    line_start<true>(p.line, sm.line, ctx);
+    if (!line_by_warp(p.line))
+        line_start<true>(p.line, sm.line, reinterpret_cast<long long *>(sm.lse), ctx);
     tc_fence_before();
-    __syncthreads();
+    set_up(warp == 0);
     tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
+    if (warp == 0 && line_by_warp(p.line)) line_start_warp<true>(p.line, sm.line, ctx);
+    const uint32_t tmem = warp == 0 ? 0u : sm.tmem_base;  // (the loader has not waited for it)
     if (warp == 0) {
         load_tiles<D>(p, &tq, &tk, sm, ctx);
         __syncwarp();
@@ -466,8 +468,9 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.n = need <= 32 ? 32 : need <= 64 ? 64 : 128;
     const int tokens = min((int)p.n / G, n);
     p.rows = tokens * G;
-    p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 1,
-                      a.workspace && a.workspace_bytes >= WORKSPACE};
+    const int grid = min(dev.sm_count, MAX_PIECES);
+    p.line = line_args(a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 1,
+                       a.workspace && a.workspace_bytes >= WORKSPACE, grid);
     p.lse = a.lse;
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sink_mode == 1 ? a.sinks : nullptr;
@@ -484,7 +487,6 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
     static_assert(sizeof(Smem<D>) <= 227 * 1024, "shared memory of one CTA");
     cudaError_t e = ensure_smem_attr((const void *)weights_kernel<D>, sizeof(Smem<D>), dev);
     if (e != cudaSuccess) return e;
-    const int grid = min(dev.sm_count, MAX_PIECES);
     if (verbose())
         fprintf(stderr, "sattn: weights_kernel<%d> grid=%d n=%u rows=%d split=%d\n", D, grid, p.n,
                 p.rows, p.line.split);

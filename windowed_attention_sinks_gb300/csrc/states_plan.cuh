@@ -7,8 +7,8 @@
 // unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
 // piece may begin and end inside a unit: a ragged batch then keeps every SM busy for the
 // same time, whatever its lengths, and a few units spread over all SMs. The
-// pieces of a unit that is cut leave partial results in the workspace, which a second
-// launch joins in a fixed order. Everything is computed from the lengths on the device, so a
+// pieces of a unit that is cut leave partial results in the workspace, which are joined in a
+// fixed order. Everything is computed from the lengths on the device, so a
 // call needs no host copy of them and can be captured and replayed with other lengths.
 #pragma once
 
@@ -27,6 +27,7 @@ struct LineArgs {
     int tokens;  // of a tile of query rows
     int extra;   // a unit's own cost, in steps
     int split;   // 0: no workspace, pieces end at unit boundaries
+    uint32_t grid_mul, grid_shift;  // x / grid = (high(mul x) + x) >> shift for 0 <= x < 2^31
 };
 
 struct LineUnit {
@@ -45,8 +46,8 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
     bad = !load_states(a.cu, a.starts, a.lens, b, a.T, a.S, u.s);
     if (bad) return false;
     constexpr int TILE_KEYS = KEYS ? UNIT_TILES * STATE_KEYS : STATE_KEYS;
-    const int keys = (int)(((long long)u.s.len + TILE_KEYS - 1) / TILE_KEYS);
-    const int rows = (int)(((long long)u.s.n + a.tokens - 1) / a.tokens);
+    const int keys = (int)(((uint32_t)u.s.len + TILE_KEYS - 1) / TILE_KEYS);
+    const int rows = (int)(((uint32_t)u.s.n + a.tokens - 1) / (uint32_t)a.tokens);
     u.nu = KEYS ? keys : rows;
     u.steps = max(1, KEYS ? rows : keys);
     return u.nu > 0;
@@ -54,26 +55,37 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
 
 // What a CTA starts from (in shared memory).
 struct LineStart {
-    long long x0, x1, total, ustart;  // its piece of the line; where the unit that holds x0 starts
-    long long warps[20];
+    long long x0, x1;  // its piece of the line
+    long long ustart;  // where the unit that holds x0 starts
+    long long per;     // positions a piece
     LineUnit u;
-    int pieces;
 };
 
-// a / b; the lines of small calls stay within 32 bits, whose division is several times as fast
+// a / b for a >= 0, b > 0. Small ones (almost all) by way of fp32: the quotient of two numbers
+// below 2^22 is off by less than 1 there, and is put right. A CTA has four divisions, one
+// after the other, to make before its first load, of 150 to 200 cycles in integers.
 __device__ __forceinline__ long long line_div(long long a, long long b) {
-    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-__device__ __forceinline__ long long line_cut(long long total, int c, int pieces) {
-    return line_div(total * c, pieces);
+    if ((a | b) >> 22) return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+    int q = (int)__fdividef((float)(int)a, (float)(int)b);
+    const int r = (int)a - q * (int)b;
+    return q + (r >= (int)b) - (r < 0);
 }
 // The piece that position x of the line lies in.
 __device__ __forceinline__ int line_piece(const LineStart &ls, long long x) {
-    return (int)line_div((x + 1) * ls.pieces - 1, ls.total);
+    return (int)line_div(x, ls.per);
 }
 __device__ __forceinline__ long long warp_prefix64(long long v) {  // over the lanes up to this one
     const int lane = threadIdx.x & 31;
+    if (__all_sync(0xffffffffu, v < 1 << 26)) {
+        int x = (int)v;
 #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += w;
+        }
+        return x;
+    }
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long w = __shfl_up_sync(0xffffffffu, v, o);
         if (lane >= o) v += w;
@@ -82,17 +94,17 @@ __device__ __forceinline__ long long warp_prefix64(long long v) {  // over the l
 }
 
 // The CTA's piece of a line of that length.
-__device__ __forceinline__ void line_ends(LineStart &ls, long long total, bool writes,
-                                          long long &x0, long long &x1) {
-    const int pieces = (int)min((long long)gridDim.x, max(1ll, total));
-    const int c = min((int)blockIdx.x, pieces);
-    x0 = line_cut(total, c, pieces);
-    x1 = line_cut(total, min(c + 1, pieces), pieces);
+__device__ __forceinline__ void line_ends(const LineArgs &a, LineStart &ls, long long total,
+                                          bool writes, long long &x0, long long &x1) {
+    const long long up = total + gridDim.x - 1;
+    const long long per = up >> 31 ? up / gridDim.x
+                                   : (__umulhi(a.grid_mul, (uint32_t)up) + (uint32_t)up) >> a.grid_shift;
+    x0 = min(total, blockIdx.x * per);
+    x1 = min(total, x0 + per);
     if (writes) {
         ls.x0 = x0;
         ls.x1 = x1;
-        ls.total = total;
-        ls.pieces = pieces;
+        ls.per = per;
     }
 }
 // The unit of position x0, which lies in sequence u.b, whose line starts at `before`.
@@ -105,27 +117,50 @@ __device__ __forceinline__ void line_unit(const LineArgs &a, LineStart &ls, Line
     ls.ustart = before + i * one;
 }
 
-// Called by the whole CTA (a whole number of warps, 640 threads at most); ends with a barrier.
-// Up to 32 sequences: one warp, a lane each, while the others set up what they need.
+// Batches that one warp plans (line_start_warp), a lane a few sequences: the loading warp does it
+// while the others set up what they need, and starts its loads without meeting them.
+constexpr int LINE_WARP = 128;
+__device__ __forceinline__ bool line_by_warp(const LineArgs &a) { return a.B <= LINE_WARP; }
+
 template <bool KEYS>
-__device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, const DevCtx &ctx) {
+__device__ __forceinline__ void line_start_warp(const LineArgs &a, LineStart &ls, const DevCtx &ctx) {
+    const int lane = threadIdx.x & 31;
+    const int per = (a.B + 31) >> 5, b0 = min(a.B, lane * per), b1 = min(a.B, b0 + per);
+    LineUnit u;
+    bool bad = false, wrong;
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        if (line_seq<KEYS>(a, b, u, wrong)) mine += (long long)a.Hkv * u.nu * (u.steps + a.extra);
+        bad |= wrong;
+    }
+    if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+    const long long upto = warp_prefix64(mine);
+    long long before = upto - mine, x0, x1;
+    line_ends(a, ls, __shfl_sync(0xffffffffu, upto, 31), lane == 0, x0, x1);
+    if (x0 < x1 && x0 >= before && x0 < upto) {
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            if (per > 1 && !line_seq<KEYS>(a, b, u, wrong)) continue;
+            const long long all = (long long)a.Hkv * u.nu * (u.steps + a.extra);
+            if (x0 < before + all) {
+                line_unit(a, ls, u, x0, before);
+                break;
+            }
+            before += all;
+        }
+    }
+    __syncwarp();
+}
+
+// The same by the whole CTA (a whole number of warps, 640 threads at most), with a number a
+// warp in shared memory; ends with a barrier.
+template <bool KEYS>
+__device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, long long *warps,
+                                           const DevCtx &ctx) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
     LineUnit u;
     bool bad = false;
     long long x0, x1;
-    if (a.B <= 32) {
-        if (warp == 0) {
-            long long mine = 0;
-            if (lane < a.B && line_seq<KEYS>(a, lane, u, bad))
-                mine = (long long)a.Hkv * u.nu * (u.steps + a.extra);
-            if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
-            const long long upto = warp_prefix64(mine), before = upto - mine;
-            line_ends(ls, __shfl_sync(0xffffffffu, upto, 31), lane == 0, x0, x1);
-            if (x0 < x1 && x0 >= before && x0 < upto) line_unit(a, ls, u, x0, before);
-        }
-        __syncthreads();
-        return;
-    }
     const int per = (a.B + (int)blockDim.x - 1) / (int)blockDim.x;  // sequences a thread
     const int b0 = (int)min((long long)a.B, (long long)tid * per), b1 = min(a.B, b0 + per);
     long long mine = 0;
@@ -137,12 +172,12 @@ __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, con
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
     const long long inc = warp_prefix64(mine);
-    if (lane == 31) ls.warps[warp] = inc;
+    if (lane == 31) warps[warp] = inc;
     __syncthreads();
-    const long long ws = warp_prefix64(lane < nw ? ls.warps[lane] : 0);
+    const long long ws = warp_prefix64(lane < nw ? warps[lane] : 0);
     long long before = inc - mine;
     if (warp > 0) before += __shfl_sync(0xffffffffu, ws, warp - 1);
-    line_ends(ls, __shfl_sync(0xffffffffu, ws, 31), tid == 0, x0, x1);
+    line_ends(a, ls, __shfl_sync(0xffffffffu, ws, 31), tid == 0, x0, x1);
     if (x0 < x1 && x0 >= before && x0 < before + mine) {
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
@@ -157,6 +192,13 @@ __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, con
         }
     }
     __syncthreads();
+}
+
+// The CTA's set-up is done: the loading warp (0) arrives when its barriers are there and goes
+// on, the others wait for it and for one another.
+__device__ __forceinline__ void set_up(bool loader) {
+    if (loader) asm volatile("barrier.cta.arrive 1, %0;" ::"r"(blockDim.x) : "memory");
+    else asm volatile("barrier.cta.sync 1, %0;" ::"r"(blockDim.x) : "memory");
 }
 
 // Walks the units of a CTA's piece.
@@ -272,6 +314,14 @@ __device__ __forceinline__ bool count_wait(uint32_t at, int n, const DevCtx &ctx
     } while (t - t0 <= limit);
     *abort = TIMED_OUT;
     return false;
+}
+
+inline LineArgs line_args(const int32_t *cu, const int32_t *starts, const int32_t *lens, int B, int T,
+                          int S, int Hkv, int tokens, int extra, bool split, int grid) {
+    uint32_t s = 0;
+    while ((1ll << s) < grid) ++s;
+    const uint32_t mul = (uint32_t)((((1ull << s) - grid) << 32) / (uint32_t)grid + 1);
+    return LineArgs{cu, starts, lens, B, T, S, Hkv, tokens, extra, split, mul, s};
 }
 
 // Rows of heads x d elements, `stride` elements apart, as boxes of 64 columns, `heads_box`
