@@ -53,6 +53,7 @@ struct CrossParams {
     const float *sinks;
     int sink_mode;
     __nv_bfloat16 *o;
+    int o_wide;  // o is on a 32-byte boundary
     float *lse;
     uint8_t *ws;
     uint32_t g_mul, g_shift;
@@ -398,6 +399,14 @@ template <> __device__ __forceinline__ void store_p<64>(uint32_t at, const uint3
     tmem_st32(at, w);
 }
 
+// Eight words to a 32-byte boundary, a whole sector: rows are written a thread each, and
+// halves of sectors cost L2 a pass each.
+__device__ __forceinline__ void store32(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // A row's running softmax over its columns of S, C at a time.
 struct Row {
     float m, l;
@@ -563,22 +572,25 @@ __device__ void softmax_many(const CrossParams &p, Smem<D> &sm, uint32_t tmem_ba
             uint32_t o[32];
             tmem_ld32(tmem + O_COL + 32u * q, o);
             tc_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
             if (in && part) {
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<float4 *>(prow + 32 * q + e) = make_float4(
-                        __uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv,
-                        __uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv);
+                for (int e = 0; e < 32; e += 8) store32(prow + 32 * q + e, o + e);
             } else if (in) {
+                uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                    uint32_t w[4];
+                for (int e = 0; e < 16; ++e)
+                    w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                __nv_bfloat16 *at = p.o + orow * D + 32 * q;
+                if (p.o_wide) {
+                    store32(at, w);
+                    store32(at + 16, w + 8);
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        w[k] = pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv,
-                                           __uint_as_float(o[e + 2 * k + 1]) * inv);
-                    *reinterpret_cast<uint4 *>(p.o + orow * D + 32 * q + e) =
-                        make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4 *>(at + 2 * e) =
+                            make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                 }
             }
             __syncwarp();
@@ -1038,12 +1050,13 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.rows = p.tokens * G;
     const int grid = min(dev.sm_count, MAX_PIECES);
     p.line = line_args(a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
-                       FEW ? p.tokens : 2 * p.tokens, FEW && D == 128 ? 1 : 3,
+                       FEW ? p.tokens : 2 * p.tokens, FEW ? (D == 128 ? 1 : 3) : 2,
                        a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D), grid);
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sinks;
     p.sink_mode = a.sink_mode;
     p.o = static_cast<__nv_bfloat16 *>(a.o);
+    p.o_wide = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     p.lse = a.lse;
     p.ws = static_cast<uint8_t *>(a.workspace);
     const uint32_t g = (uint32_t)G;

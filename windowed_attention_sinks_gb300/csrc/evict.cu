@@ -3,11 +3,13 @@
 // evict_select: one block a sequence and KV head picks the `keep` rows that stay: the first
 // `first` and the last `last` rows, and of the others the heaviest, the lower row first
 // among equal ones. Weights count as max(w, 0) (NaN as 0), so their bits order them;
-// the least bits T that still stay are found digit by digit (11, 11 and 10 bits, from the
-// top) from histograms of the rows that agree with T so far. Then each warp counts its run of
-// rows above T and equal to T, one scan over the warps places them, and the kept rows are
-// written in ascending order. The weights are read once into shared memory (the first
-// CACHED of a head) and four times from there.
+// the least bits T that still stay are found from histograms of the range that they can lie in,
+// in 2048 parts, until a part is one number: three rounds at most, of which the later ones
+// meet few rows. (Digits of the bits themselves as bins, where most rows share few exponents
+// and queue for few bins: 30 us instead of what follows.) Then each warp counts its run of rows above T
+// and equal to T, one scan over the warps places them, and the kept rows are written in
+// ascending order. The weights are read once into shared memory (the first CACHED of a head)
+// and four times from there.
 // evict_gather: copies the kept rows of k and v, 16 bytes an item, in the order of the
 // output, and zeros behind a sequence's last one.
 #include "internal.h"
@@ -15,55 +17,58 @@
 namespace sattn {
 namespace {
 
-constexpr int SELECT = 1024, CACHED = 16384, BINS = 2048;
+constexpr int SELECT = 1024, WARPS = SELECT / 32, CACHED = 16384, LOG_BINS = 11,
+              BINS = 1 << LOG_BINS;
+constexpr uint32_t ALWAYS = 0xffffffffu;
 constexpr int GATHER = 256, AHEAD = 4;
 
 struct SelectSmem {
-    uint32_t w[CACHED];
+    alignas(16) uint32_t w[CACHED];
     int bins[BINS];
-    int warp_gt[32], warp_eq[32];
+    int warp_gt[WARPS], warp_eq[WARPS];
+    uint32_t warp_most[WARPS];
     int digit, above;
 };
 
 __device__ __forceinline__ uint32_t order_bits(float w) { return w > 0.f ? __float_as_uint(w) : 0u; }
 
 // Which bin, counted from the top, holds the k-th row (k >= 1)? `above`: rows in higher bins.
-// The whole block; ends with a barrier.
-__device__ __forceinline__ void find_bin(SelectSmem &sm, int nbins, int k) {
+// The whole block; the bins are there, and zero behind it.
+__device__ __forceinline__ void find_bin(SelectSmem &sm, int k) {
+    constexpr int PER = BINS / SELECT;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // thread i holds bins top - 2 i and top - 2 i - 1
-    const int hi = nbins - 1 - 2 * threadIdx.x;
-    const int a = hi >= 0 ? sm.bins[hi] : 0, b = hi >= 1 ? sm.bins[hi - 1] : 0;
-    int inc = a + b;
+    __syncthreads();
+    // thread i holds the bins from top - PER i downwards
+    int n[PER], mine = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        n[j] = sm.bins[BINS - 1 - PER * (int)threadIdx.x - j];
+        mine += n[j];
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) sm.bins[BINS - 1 - PER * (int)threadIdx.x - j] = 0;
+    int before = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+        const int v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
     }
-    if (lane == 31) sm.warp_gt[warp] = inc;
+    if (lane == 31) sm.warp_gt[warp] = before;
+    before -= mine;
     __syncthreads();
-    if (warp == 0) {
-        int v = sm.warp_gt[lane];
+    before += __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_gt[lane] : 0);
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, v, o);
-            if (lane >= o) v += u;
+    for (int j = 0; j < PER; ++j) {
+        if (before < k && k <= before + n[j]) {
+            sm.digit = BINS - 1 - PER * (int)threadIdx.x - j;
+            sm.above = before;
         }
-        sm.warp_eq[lane] = v;
-    }
-    __syncthreads();
-    const int before = (warp ? sm.warp_eq[warp - 1] : 0) + inc - a - b;
-    if (before < k && k <= before + a) {
-        sm.digit = hi;
-        sm.above = before;
-    } else if (before + a < k && k <= before + a + b) {
-        sm.digit = hi - 1;
-        sm.above = before + a;
+        before += n[j];
     }
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(SELECT, 1) evict_select_kernel(EvictArgs a, DevCtx ctx) {
+__global__ void __launch_bounds__(SELECT, 2) evict_select_kernel(EvictArgs a, DevCtx ctx) {
     extern __shared__ __align__(16) uint8_t raw[];
     SelectSmem &sm = *reinterpret_cast<SelectSmem *>(raw);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -97,76 +102,136 @@ __global__ void __launch_bounds__(SELECT, 1) evict_select_kernel(EvictArgs a, De
     }
     const int lo = a.first, hi = len - a.last;  // the rows that compete
     int need = a.keep - a.first - a.last;       // of which so many stay; fewer than there are
-    auto bits = [&](int i) { return i < CACHED ? sm.w[i] : order_bits(__ldg(w + i)); };
-    for (int i0 = tid; i0 < min(len, CACHED); i0 += 4 * SELECT) {
-        float x[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            x[u] = i0 + u * SELECT < len ? __ldg(w + i0 + u * SELECT) : 0.f;
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            if (i0 + u * SELECT < min(len, CACHED)) sm.w[i0 + u * SELECT] = order_bits(x[u]);
-    }
-    uint32_t T = 0xffffffffu;  // nothing is above it
-    if (need > 0) {
-        T = 0;
-        constexpr int SHIFT[3] = {21, 10, 0}, WIDTH[3] = {11, 11, 10};
-#pragma unroll 1
-        for (int d = 0; d < 3; ++d) {
-            const int shift = SHIFT[d], nbins = 1 << WIDTH[d], top = shift + WIDTH[d];
-            for (int i = tid; i < nbins; i += SELECT) sm.bins[i] = 0;
-            __syncthreads();
-            for (int i = lo + tid; i < hi; i += SELECT) {
-                const uint32_t x = bits(i);
-                if (top == 32 || x >> top == T >> top) atomicAdd(&sm.bins[x >> shift & (nbins - 1)], 1);
+    // A row as a number: the weight's bits, more than any weight's for a row that stays anyway.
+    auto value = [&](int i, float x) { return i < lo || i >= hi ? ALWAYS : order_bits(x); };
+    // f(i, x) with the values of rows i .. i + 3, for the multiples of 4 below len that are this
+    // thread's (behind len: 0); a warp's are 128 rows each time, the lanes' in order.
+    const int per = ((len + WARPS - 1) / WARPS + 127) & ~127, from = min(len, warp * per),
+              to = min(len, from + per);
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i = from + 4 * lane; i - 4 * lane < to; i += 128) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (i + 3 < CACHED) {
+                x = *reinterpret_cast<const uint4 *>(sm.w + i);
+            } else {
+                if (i < to) x.x = value(i, __ldg(w + i));
+                if (i + 1 < to) x.y = value(i + 1, __ldg(w + i + 1));
+                if (i + 2 < to) x.z = value(i + 2, __ldg(w + i + 2));
+                if (i + 3 < to) x.w = value(i + 3, __ldg(w + i + 3));
             }
-            __syncthreads();
-            find_bin(sm, nbins, need);
-            T |= (uint32_t)sm.digit << shift;
-            need -= sm.above;
+            const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+            f(i, v);
+        }
+    };
+    for (int i = tid; i < BINS; i += SELECT) sm.bins[i] = 0;
+    // into shared memory; how many of those that compete are above 0, and their range
+    constexpr int U = 8;
+    int npos = 0;
+    uint32_t least = 0xffffffffu, most = 0;
+    for (int i0 = tid; i0 < ((len + 127) & ~127); i0 += U * SELECT) {
+        float x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) x[u] = i0 + u * SELECT < len ? __ldg(w + i0 + u * SELECT) : 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * SELECT;
+            const uint32_t v = i < len ? value(i, x[u]) : 0;
+            if (i < CACHED) sm.w[i] = v;
+            if (v - 1 < ALWAYS - 1) {
+                ++npos;
+                least = min(least, v);
+                most = max(most, v);
+            }
         }
     }
-    __syncthreads();
-    // `need` of the rows equal to T stay, the lowest ones; warp i has a run of rows
-    const int per = ((len + 31) / 32 + 31) & ~31, from = min(len, warp * per), to = min(len, from + per);
-    auto flags = [&](int i, bool &gt, bool &eq) {
-        const bool in = i < to;
-        const uint32_t x = in ? bits(i) : 0;
-        const bool always = i < lo || i >= hi;
-        gt = in && (always || x > T);
-        eq = in && !always && x == T;
-    };
-    int ngt = 0, neq = 0;
-    for (int i = from + lane; i - lane < to; i += 32) {
-        bool gt, eq;
-        flags(i, gt, eq);
-        ngt += __popc(__ballot_sync(0xffffffffu, gt));
-        neq += __popc(__ballot_sync(0xffffffffu, eq));
+    npos = __reduce_add_sync(0xffffffffu, npos);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+        sm.warp_gt[warp] = npos;
+        sm.warp_eq[warp] = (int)least;
+        sm.warp_most[warp] = most;
     }
+    __syncthreads();
+    npos = __reduce_add_sync(0xffffffffu, sm.warp_gt[lane]);
+    least = __reduce_min_sync(0xffffffffu, (uint32_t)sm.warp_eq[lane]);
+    most = __reduce_max_sync(0xffffffffu, sm.warp_most[lane]);
+    uint32_t T = 0;
+    if (need == 0) {
+        T = ALWAYS - 1;  // no weight is above it
+    } else if (need > npos) {
+        need -= npos;  // so many of those at 0
+    } else {
+        // the range that T lies in, in BINS parts, until a part is one number
+        while (least < most) {
+            const int shift = max(0, 32 - __clz(most - least) - LOG_BINS);
+            const uint32_t range = most - least;
+            __syncthreads();
+            each([&](int, const uint32_t(&x)[4]) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (x[e] - least <= range) atomicAdd(&sm.bins[(x[e] - least) >> shift], 1);
+            });
+            find_bin(sm, need);
+            need -= sm.above;
+            least += (uint32_t)sm.digit << shift;
+            most = min(most, least + ((1u << shift) - 1));
+        }
+        T = least;
+    }
+    __syncthreads();
+    // `need` of the rows equal to T stay, the lowest ones. Rows above T and equal to it
+    int ngt = 0, neq = 0;
+    each([&](int i, const uint32_t(&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            ngt += x[e] > T;
+            neq += x[e] == T && i + e < to;
+        }
+    });
+    ngt = __reduce_add_sync(0xffffffffu, ngt);
+    neq = __reduce_add_sync(0xffffffffu, neq);
     if (lane == 0) {
         sm.warp_gt[warp] = ngt;
         sm.warp_eq[warp] = neq;
     }
     __syncthreads();
-    int gt0 = 0, eq0 = 0;
-    for (int i = 0; i < warp; ++i) {
-        gt0 += sm.warp_gt[i];
-        eq0 += sm.warp_eq[i];
-    }
-    const unsigned below = (1u << lane) - 1;
-    for (int i = from + lane; i - lane < to; i += 32) {
-        bool gt, eq;
-        flags(i, gt, eq);
-        const unsigned mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-        const int g = gt0 + __popc(mg & below), q = eq0 + __popc(me & below);
-        if (gt || (eq && q < need)) {
-            const int at = g + min(q, need);
-            rows[at] = i;
-            wout[at] = __ldg(w + i);
+    int gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_gt[lane] : 0);
+    int eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? sm.warp_eq[lane] : 0);
+    each([&](int i, const uint32_t(&x)[4]) {
+        int mine = 0;  // rows above T, and 2^16 times those equal to it
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            mine += x[e] > T ? 1 : x[e] == T && i + e < to ? 1 << 16 : 0;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
         }
-        gt0 += __popc(mg);
-        eq0 += __popc(me);
-    }
+        const int all = __shfl_sync(0xffffffffu, upto, 31);
+        upto -= mine;
+        int g = gt0 + (upto & 0xffff), q = eq0 + (upto >> 16);
+        int at[4];
+        float kept_w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool gt = x[e] > T, eq = x[e] == T && i + e < to;
+            at[e] = gt || (eq && q < need) ? g + min(q, need) : -1;
+            if (at[e] >= 0) kept_w[e] = __ldg(w + i + e);
+            g += gt;
+            q += eq;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (at[e] >= 0) {
+                rows[at[e]] = i + e;
+                wout[at[e]] = kept_w[e];
+            }
+        gt0 += all & 0xffff;
+        eq0 += all >> 16;
+    });
 }
 
 // UNITS: 16-byte units a row.
