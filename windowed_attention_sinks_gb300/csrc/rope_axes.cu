@@ -17,7 +17,7 @@
 namespace sattn {
 namespace {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int MAX_HALF = 128;  // pairs a head
 constexpr int MAX_TOKENS = 16;  // tokens a block
 
@@ -37,8 +37,8 @@ FastDiv fast_div(uint32_t n) {
 
 struct Args {
     RopeArgs r;
-    int tokens;       // a block
-    FastDiv heads, items, half;
+    int tokens, heads;   // a block
+    FastDiv head, items, half;
     int turned, copied;  // items a head that turn; vectors a head behind column rd
 };
 
@@ -96,17 +96,94 @@ template <> struct Vec<__nv_bfloat16> {
     }
 };
 
+// Two vectors of a head, on their way.
+template <typename T> struct Item {
+    const T *src;
+    T *dst;
+    uint4 x, y;
+    int tok, c, off;  // token of the block, item of the head, distance of the vectors
+    bool two;
+
+    template <bool NEIGHBOURS>
+    __device__ __forceinline__ void load(const Args &a, long long t0, int h0, int e, int total) {
+        constexpr int N = Vec<T>::N;
+        const RopeArgs &r = a.r;
+        src = nullptr;
+        if (e >= total) return;
+        const int th = a.items.div(e);
+        c = e - th * (int)a.items.n;
+        tok = a.head.div(th);
+        const int h = h0 + th - tok * (int)a.head.n;
+        const bool key = h >= r.H;
+        const size_t t = (size_t)(t0 + tok);
+        const T *in = key ? (const T *)r.k + t * r.k_stride + (size_t)(h - r.H) * r.d
+                          : (const T *)r.q + t * r.q_stride + (size_t)h * r.d;
+        T *out = key ? (T *)r.k_out + t * r.k_out_stride + (size_t)(h - r.H) * r.d
+                     : (T *)r.q_out + t * r.q_out_stride + (size_t)h * r.d;
+        const bool turn = c < a.turned;
+        const int first =
+            turn ? (NEIGHBOURS ? 2 * N * c : N * c) : r.rd + 2 * N * (c - a.turned);
+        off = turn && !NEIGHBOURS ? r.rd / 2 : N;
+        two = turn || 2 * (c - a.turned) + 1 < a.copied;
+        dst = out + first;
+        if (!turn && in == out) return;  // in place: these columns stay
+        src = in + first;
+        x = *reinterpret_cast<const uint4 *>(src);
+        if (two) y = *reinterpret_cast<const uint4 *>(src + off);
+    }
+    template <bool NEIGHBOURS>
+    __device__ __forceinline__ void turn(const Args &a, const float2 *table) {
+        constexpr int N = Vec<T>::N;
+        if (!src) return;
+        if (c < a.turned) {
+            const float2 *cs = table + tok * (a.r.rd / 2) + c * N;
+            float p[N], q[N];
+            Vec<T>::get(x, p);
+            Vec<T>::get(y, q);
+            if (NEIGHBOURS) {
+#pragma unroll
+                for (int i = 0; i < N; i += 2) {
+                    const float2 w = cs[i / 2], z = cs[N / 2 + i / 2];
+                    const float p0 = p[i], q0 = q[i];
+                    p[i] = p0 * w.x - p[i + 1] * w.y;
+                    p[i + 1] = p[i + 1] * w.x + p0 * w.y;
+                    q[i] = q0 * z.x - q[i + 1] * z.y;
+                    q[i + 1] = q[i + 1] * z.x + q0 * z.y;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const float2 w = cs[i];
+                    const float p0 = p[i];
+                    p[i] = p0 * w.x - q[i] * w.y;
+                    q[i] = q[i] * w.x + p0 * w.y;
+                }
+            }
+            x = Vec<T>::put(p);
+            y = Vec<T>::put(q);
+        }
+        *reinterpret_cast<uint4 *>(dst) = x;
+        if (two) *reinterpret_cast<uint4 *>(dst + off) = y;
+    }
+};
+
 template <typename T, bool NEIGHBOURS>
-__global__ void __launch_bounds__(THREADS) rope_axes_kernel(const __grid_constant__ Args a,
+__global__ void __launch_bounds__(THREADS, 10) rope_axes_kernel(const __grid_constant__ Args a,
                                                             const __grid_constant__ DevCtx ctx) {
-    constexpr int N = Vec<T>::N;
     extern __shared__ float2 table[];  // [tokens][rd / 2]
     const RopeArgs &r = a.r;
     const int half = r.rd / 2;
     const long long t0 = (long long)blockIdx.x * a.tokens;
-    const int nt = (int)min((long long)a.tokens, r.T - t0);
-    for (int e = threadIdx.x; e < nt * half; e += THREADS) {
-        const int t = a.half.div(e), i = e - t * half;
+    const int nt = (int)min((long long)a.tokens, r.T - t0), h0 = (int)blockIdx.y * a.heads;
+    const int total = nt * (int)(a.head.n * a.items.n);
+    constexpr int B = 2;  // items in flight a thread
+    Item<T> it[B];
+    int e = threadIdx.x;
+    // the first ones are on their way while the angles are computed
+#pragma unroll
+    for (int u = 0; u < B; ++u) it[u].template load<NEIGHBOURS>(a, t0, h0, e + u * THREADS, total);
+    for (int x = threadIdx.x; x < nt * half; x += THREADS) {
+        const int t = a.half.div(x), i = x - t * half;
         const int axis = __ldg(r.axis + i);
         float2 cs = make_float2(1.f, 0.f);
         if (axis < r.axes) {
@@ -116,80 +193,17 @@ __global__ void __launch_bounds__(THREADS) rope_axes_kernel(const __grid_constan
         } else if (blockIdx.x == 0) {
             record_error(ctx, DEVERR_INDEX);
         }
-        table[e] = make_float2(cs.x, r.inverse ? -cs.y : cs.y);
+        table[x] = make_float2(cs.x, r.inverse ? -cs.y : cs.y);
     }
     __syncthreads();
-    const int total = nt * (int)(a.heads.n * a.items.n);
-    constexpr int B = 2;  // items in flight a thread
-    for (int e0 = threadIdx.x; e0 < total; e0 += B * THREADS) {
-        uint4 x[B], y[B];
-        const T *src[B];
-        T *dst[B];
-        int tok[B], c[B], off[B];
-        bool two[B];
+    for (;;) {
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
-            const int e = e0 + u * THREADS;
-            two[u] = false;
-            src[u] = nullptr;
-            if (e >= total) continue;
-            const int th = a.items.div(e);
-            c[u] = e - th * (int)a.items.n;
-            tok[u] = a.heads.div(th);
-            const int h = th - tok[u] * (int)a.heads.n;
-            const bool key = h >= r.H;
-            const size_t t = (size_t)(t0 + tok[u]);
-            const T *in = key ? (const T *)r.k + t * r.k_stride + (size_t)(h - r.H) * r.d
-                              : (const T *)r.q + t * r.q_stride + (size_t)h * r.d;
-            T *out = key ? (T *)r.k_out + t * r.k_out_stride + (size_t)(h - r.H) * r.d
-                         : (T *)r.q_out + t * r.q_out_stride + (size_t)h * r.d;
-            const bool turn = c[u] < a.turned;
-            const int first = turn ? (NEIGHBOURS ? 2 * N * c[u] : N * c[u])
-                                   : r.rd + 2 * N * (c[u] - a.turned);
-            off[u] = turn && !NEIGHBOURS ? half : N;
-            two[u] = turn || 2 * (c[u] - a.turned) + 1 < a.copied;
-            src[u] = in + first;
-            dst[u] = out + first;
-            if (!turn && src[u] == dst[u]) {  // in place: these columns stay
-                src[u] = nullptr;
-                continue;
-            }
-            x[u] = *reinterpret_cast<const uint4 *>(src[u]);
-            if (two[u]) y[u] = *reinterpret_cast<const uint4 *>(src[u] + off[u]);
-        }
+        for (int u = 0; u < B; ++u) it[u].template turn<NEIGHBOURS>(a, table);
+        e += B * THREADS;
+        if (e >= total) break;
 #pragma unroll
-        for (int u = 0; u < B; ++u) {
-            if (!src[u]) continue;
-            if (c[u] < a.turned) {
-                const float2 *cs = table + tok[u] * half + c[u] * N;
-                float p[N], q[N];
-                Vec<T>::get(x[u], p);
-                Vec<T>::get(y[u], q);
-                if (NEIGHBOURS) {
-#pragma unroll
-                    for (int i = 0; i < N; i += 2) {
-                        const float2 w = cs[i / 2], z = cs[N / 2 + i / 2];
-                        const float p0 = p[i], q0 = q[i];
-                        p[i] = p0 * w.x - p[i + 1] * w.y;
-                        p[i + 1] = p[i + 1] * w.x + p0 * w.y;
-                        q[i] = q0 * z.x - q[i + 1] * z.y;
-                        q[i + 1] = q[i + 1] * z.x + q0 * z.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        const float2 w = cs[i];
-                        const float p0 = p[i];
-                        p[i] = p0 * w.x - q[i] * w.y;
-                        q[i] = q[i] * w.x + p0 * w.y;
-                    }
-                }
-                x[u] = Vec<T>::put(p);
-                y[u] = Vec<T>::put(q);
-            }
-            *reinterpret_cast<uint4 *>(dst[u]) = x[u];
-            if (two[u]) *reinterpret_cast<uint4 *>(dst[u] + off[u]) = y[u];
-        }
+        for (int u = 0; u < B; ++u)
+            it[u].template load<NEIGHBOURS>(a, t0, h0, e + u * THREADS, total);
     }
 }
 
@@ -201,17 +215,24 @@ template <typename T> cudaError_t launch(const RopeArgs &r, const DevInfo &dev, 
     a.turned = r.rd / (2 * N);
     a.copied = (r.d - r.rd) / N;
     const int items = a.turned + (a.copied + 1) / 2;
-    a.heads = fast_div(heads);
-    a.items = fast_div(items);
-    a.half = fast_div(r.rd / 2);
+    // Blocks of about 512 items (four a thread); with few tokens a token's heads are spread
+    // over several (16 tokens, 40 heads of 128: 6.2 us in blocks of 3 tokens).
     const long long per_token = (long long)heads * items;
     a.tokens = (int)max(1ll, min((long long)MAX_TOKENS, 4 * THREADS / per_token));
+    while (a.tokens > 1 && (r.T + a.tokens - 1) / a.tokens < 2 * dev.sm_count) a.tokens /= 2;
     const long long blocks = ((long long)r.T + a.tokens - 1) / a.tokens;
+    const int want = (int)max(1ll, min(per_token / THREADS, 2 * dev.sm_count / blocks));
+    int split = 1;  // of the heads, evenly
+    for (int i = 2; i <= want; ++i)
+        if (heads % i == 0) split = i;
+    a.heads = heads / split;
+    a.head = fast_div(a.heads);
+    a.items = fast_div(items);
+    a.half = fast_div(r.rd / 2);
     const size_t smem = (size_t)a.tokens * (r.rd / 2) * sizeof(float2);  // 16 KB at most
-    if (r.interleaved)
-        rope_axes_kernel<T, true><<<(unsigned)blocks, THREADS, smem, s>>>(a, make_ctx(dev));
-    else
-        rope_axes_kernel<T, false><<<(unsigned)blocks, THREADS, smem, s>>>(a, make_ctx(dev));
+    const dim3 grid((unsigned)blocks, (unsigned)split);
+    if (r.interleaved) rope_axes_kernel<T, true><<<grid, THREADS, smem, s>>>(a, make_ctx(dev));
+    else rope_axes_kernel<T, false><<<grid, THREADS, smem, s>>>(a, make_ctx(dev));
     return cudaGetLastError();
 }
 
