@@ -632,7 +632,8 @@ def rope_axes(q, k, positions, inv_freq, axis, interleaved=False, inverse=False,
 
 def _states(q, k, cu_seqlens, kv_starts, kv_lens):
     """Checks queries [T, H, d] and keys [S, Hkv, d] of B sequences; returns (device
-    index, T, S, H, Hkv, d, B, q's and k's token strides)."""
+    index, dtype code, T, S, H, Hkv, d, B, q's and k's token strides). Flat, as for
+    _paged_cache: a decode step's calls are a few microseconds of GPU work each."""
     import torch
 
     i32 = torch.int32
@@ -640,27 +641,29 @@ def _states(q, k, cu_seqlens, kv_starts, kv_lens):
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q must be [T, H, d], k [S, Hkv, d]")
     T, H, d = q.shape
-    S, Hkv = k.shape[0], k.shape[1]
+    S, Hkv, _ = k.shape
     B = kv_starts.numel()
-    for t, name, n in ((kv_starts, "kv_starts", B), (kv_lens, "kv_lens", B),
-                       (cu_seqlens, "cu_seqlens", B + 1)):
-        _vector(t, name, n, i32, dev)
-    return (dev, T, S, H, Hkv, d, B, _token_rows(q, "q", T, H, d, q.dtype, dev),
-            _token_rows(k, "k", S, Hkv, d, q.dtype, dev))
+    if not (cu_seqlens.dtype is i32 and kv_starts.dtype is i32 and kv_lens.dtype is i32
+            and cu_seqlens.shape == (B + 1,) and kv_starts.shape == (B,)
+            and kv_lens.shape == (B,) and cu_seqlens.get_device() == dev
+            and kv_starts.get_device() == dev and kv_lens.get_device() == dev
+            and cu_seqlens.is_contiguous() and kv_starts.is_contiguous()
+            and kv_lens.is_contiguous()):
+        raise ValueError("cu_seqlens, kv_starts and kv_lens must be contiguous int32 [B + 1], "
+                         "[B] and [B] on cuda:%d" % dev)
+    dt = q.dtype
+    return (dev, _dtype_code(q), T, S, H, Hkv, d, B, _token_rows(q, "q", T, H, d, dt, dev),
+            _token_rows(k, "k", S, Hkv, d, dt, dev))
 
 
-def _workspace(t, nbytes, dev, device, stream):
-    """(tensor, address, bytes) of a given workspace, or of one of nbytes for this call."""
-    import torch
+def _given(t, dev):
+    """Address and bytes of a workspace that the caller gave."""
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous on cuda:%d" % dev)
+    return t.data_ptr(), t.numel() * t.element_size()
 
-    if t is not None:
-        if t.get_device() != dev or not t.is_contiguous():
-            raise ValueError("workspace must be contiguous on cuda:%d" % dev)
-        return t, t.data_ptr(), t.numel() * t.element_size()
-    if not nbytes:
-        return None, None, 0
-    t = _empty(nbytes, torch.uint8, device, stream)
-    return t, t.data_ptr(), nbytes
+
+_sizes = {}  # workspace bytes by a call's shape
 
 
 def cross_workspace_bytes(max_q_len, H, Hkv, d):
@@ -679,19 +682,27 @@ def cross_fwd(q, k, v, cu_seqlens, kv_starts, kv_lens, max_q_len=None, sinks=Non
     the call runs on."""
     import torch
 
-    dev, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
+    dev, code, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
     dt = q.dtype
-    code = _dtype_code(q)
     vs = _token_rows(v, "v", S, Hkv, d, dt, dev)
     sp = None if sinks is None else _vector(sinks, "sinks", H, torch.float32, dev)
     n = (-(-T // B) if B else 0) if max_q_len is None else int(max_q_len)
     L = lib()
+    nb, wp = 0, None
     with _OnDevice(dev, stream) as s:
         device = q.device
         o = _out(o, "o", (T, H, d), dt, device, stream)
         lse = _out(lse, "lse", (T, H), torch.float32, device, stream)
-        nb = L.sattn_cross_workspace_bytes(n, H, Hkv, d) if code == BF16 else 0
-        workspace, wp, nb = _workspace(workspace, nb, dev, device, stream)
+        if workspace is not None:
+            wp, nb = _given(workspace, dev)
+        elif code == BF16:
+            key = (min(n, 65), H, Hkv, d)  # more rows than 64 need the same
+            nb = _sizes.get(key)
+            if nb is None:
+                nb = _sizes[key] = L.sattn_cross_workspace_bytes(n, H, Hkv, d)
+            if nb:
+                workspace = _empty(nb, torch.uint8, device, stream)
+                wp = workspace.data_ptr()
         rc = L.sattn_cross_fwd(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
                                cu_seqlens.data_ptr(), kv_starts.data_ptr(), kv_lens.data_ptr(), B,
                                T, S, n, H, Hkv, d, sp, int(sink_mode),
@@ -710,19 +721,25 @@ def cross_key_weights(q, k, lse, cu_seqlens, kv_starts, kv_lens, weights, max_q_
     [Hkv, S], or added to them. Returns weights."""
     import torch
 
-    dev, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
-    code = _dtype_code(q)
+    dev, code, T, S, H, Hkv, d, B, qs, ks = _states(q, k, cu_seqlens, kv_starts, kv_lens)
     device = q.device
-    for t, name, shape in ((lse, "lse", (T, H)), (weights, "weights", (Hkv, S))):
-        if t is None:
-            raise ValueError("%s is needed" % name)
-        _out(t, name, shape, torch.float32, device, stream)
+    if lse is None or weights is None:
+        raise ValueError("lse and weights are needed")
+    _out(lse, "lse", (T, H), torch.float32, device, stream)
+    _out(weights, "weights", (Hkv, S), torch.float32, device, stream)
     sp = None if sinks is None else _vector(sinks, "sinks", H, torch.float32, dev)
     n = (-(-T // B) if B else 0) if max_q_len is None else int(max_q_len)
     L = lib()
+    nb, wp = 0, None
     with _OnDevice(dev, stream) as s:
-        nb = L.sattn_cross_key_weights_workspace_bytes() if code == BF16 else 0
-        workspace, wp, nb = _workspace(workspace, nb, dev, device, stream)
+        if workspace is not None:
+            wp, nb = _given(workspace, dev)
+        elif code == BF16:
+            nb = _sizes.get("weights")
+            if nb is None:
+                nb = _sizes["weights"] = L.sattn_cross_key_weights_workspace_bytes()
+            workspace = _empty(nb, torch.uint8, device, stream)
+            wp = workspace.data_ptr()
         rc = L.sattn_cross_key_weights(q.data_ptr(), qs, k.data_ptr(), ks, lse.data_ptr(),
                                        cu_seqlens.data_ptr(), kv_starts.data_ptr(),
                                        kv_lens.data_ptr(), B, T, S, n, H, Hkv, d, sp,
