@@ -40,6 +40,9 @@ constexpr int NTHREADS = 512;
 constexpr int SOFTMAX = 8;   // first softmax warp
 constexpr int UNITS = 4;     // units handed on ahead
 constexpr int ADDERS = 2;    // warps that add up a unit's streams (FEW)
+// What a step costs; with one half's rows alone 0.63 of it. A unit by itself: 2 steps, 1 or
+// 3 in the FEW form (by cycles of CTAs with other shares of each).
+constexpr int COST = 8, LESS = 5;
 constexpr int CHUNK = 64;    // keys whose P is handed on at a time
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
 constexpr float FAR = 1 << 20;  // m up to which x - m may be taken in one rounding
@@ -119,7 +122,6 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
 #pragma unroll 1
     for (; it.live && ok; it.next(p.line, sm.line)) {
         const LineUnit &u = it.u;
-        if (u.begin == u.end) continue;
         ok = sm.units.put(index, u, ctx, abort);
         const bool tail = ragged(u);
         auto ask = [&]() {  // for the unit's queries
@@ -779,32 +781,34 @@ template <int E> __device__ __forceinline__ void load_row(const float *p, float 
     }
 }
 
-// Joins the parts of a cut unit, for its rows w, w + ADDERS, ...: two rows at a time, for the loads
-// in flight. Lane i holds part i's sums, the columns are spread over the lanes.
+// Joins the parts of a cut unit, for its rows q, q + ADDERS, ... below `end`: a warp, two
+// rows at a time, for the loads in flight. Lane i holds part i's sums, the columns
+// are spread over the lanes. w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
+// null logit), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces.
 template <int D, int FEW, typename F>
-__device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int parts, int rows, int w,
+__device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int parts, int q, int end,
                                            F orow) {
-    constexpr int E = D / 32, N = 2;
+    constexpr int E = D / 32, N = 2, K = 4;  // rows, and parts, at a time
     const int lane = threadIdx.x & 31;
     const float2 *sums = part_sums(p.ws);
     const float *prows = reinterpret_cast<const float *>(p.ws + plan_rows_offset(FEW));
     // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ..
     auto slot = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * FEW; };
 #pragma unroll 1
-    for (int q0 = w; q0 < rows; q0 += N * ADDERS) {
+    for (; q < end; q += N * ADDERS) {
         float m[N], z[N], inv[N], f[N], acc[N][E] = {};
         size_t at[N];
-        int q[N];
+        int r[N];
 #pragma unroll
-        for (int a = 0; a < N; ++a) {  // (a row behind the last is the one before, not written)
-            q[a] = q0 + a * ADDERS < rows ? q0 + a * ADDERS : q0;
-            at[a] = orow(q[a]);
+        for (int a = 0; a < N; ++a) {  // (in the place of rows behind the last, q again)
+            r[a] = q + a * ADDERS < end ? q + a * ADDERS : q;
+            at[a] = orow(r[a]);
         }
 #pragma unroll
         for (int a = 0; a < N; ++a) {
             const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + (int)(at[a] % p.H))) : 0.f;
             f[a] = join_weights(parts, null, p.sink_mode == 2, m[a], z[a],
-                                [&](int i) { return __ldcg(sums + slot(i) + q[a]); });
+                                [&](int i) { return __ldcg(sums + slot(i) + r[a]); });
             // (over their sum, so that values near fp32's largest do not overflow)
             inv[a] = z[a] == 0.f ? 0.f : 1.f / z[a];
         }
@@ -813,7 +817,7 @@ __device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int par
 #pragma unroll
             for (int a = 0; a < N; ++a) {
                 if (i0 > 0) {
-                    const float2 s = i0 + lane < parts ? __ldcg(sums + slot(i0 + lane) + q[a])
+                    const float2 s = i0 + lane < parts ? __ldcg(sums + slot(i0 + lane) + r[a])
                                                        : make_float2(m[a], 0.f);
                     f[a] = s.y * ex2(s.x - m[a]);
                 }
@@ -821,16 +825,16 @@ __device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int par
             }
             const int cnt = min(32, parts - i0);
 #pragma unroll 1
-            for (int k = 0; k < cnt; k += 4) {
-                float x[4][N][E];
+            for (int k = 0; k < cnt; k += K) {
+                float x[K][N][E];
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
+                for (int d = 0; d < K; ++d)
 #pragma unroll
                     for (int a = 0; a < N; ++a)
-                        load_row<E>(prows + (slot(i0 + min(k + d, cnt - 1)) + q[a]) * D + lane * E,
+                        load_row<E>(prows + (slot(i0 + min(k + d, cnt - 1)) + r[a]) * D + lane * E,
                                     x[d][a]);
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
+                for (int d = 0; d < K; ++d)
 #pragma unroll
                     for (int a = 0; a < N; ++a) {
                         const float fk = __shfl_sync(0xffffffffu, f[a], min(k + d, 31));
@@ -842,7 +846,7 @@ __device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int par
         }
 #pragma unroll
         for (int a = 0; a < N; ++a) {
-            if (q0 + a * ADDERS >= rows) break;
+            if (q + a * ADDERS >= end) break;
             store_row<D>(p.o + at[a] * D, acc[a], lane);
             if (p.lse && lane == 0)
                 p.lse[at[a]] = z[a] == 0.f ? -INFINITY : (m[a] + log2f(z[a])) * LN2;
@@ -921,7 +925,7 @@ __device__ void add_up(const CrossParams &p, Smem<D> &sm, int w, const DevCtx &c
         }
         if (!__shfl_sync(0xffffffffu, last, 0)) continue;
         __threadfence();
-        join_parts<D, FEW>(p, u.c0, u.parts, rows, w, orow);
+        join_parts<D, FEW>(p, u.c0, u.parts, w, rows, orow);
     }
 }
 
@@ -1049,9 +1053,11 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.tokens = FEW ? min(FEW / G, max(1, a.max_q_len)) : 128 / G;
     p.rows = p.tokens * G;
     const int grid = min(dev.sm_count, MAX_PIECES);
-    p.line = line_args(a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
-                       FEW ? p.tokens : 2 * p.tokens, FEW ? (D == 128 ? 1 : 3) : 2,
-                       a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D), grid);
+    const bool split = a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D);
+    p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
+                      FEW ? p.tokens : 2 * p.tokens, FEW ? 0 : p.tokens, COST, FEW ? COST : LESS,
+                      FEW ? (D == 128 ? 1 : 3) * COST : 2 * COST, split};
+    line_grid(p.line, grid);
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sinks;
     p.sink_mode = a.sink_mode;

@@ -100,7 +100,6 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
 #pragma unroll 1
     for (; it.live && ok; it.next(p.line, sm.line)) {
         const LineUnit &u = it.u;
-        if (u.begin == u.end) continue;
         ok = sm.units.put(index++, u, ctx, abort);
 #pragma unroll
         for (int g = 0; g < TILES; ++g) {
@@ -469,8 +468,10 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
     const int tokens = min((int)p.n / G, n);
     p.rows = tokens * G;
     const int grid = min(dev.sm_count, MAX_PIECES);
-    p.line = line_args(a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 1,
-                       a.workspace && a.workspace_bytes >= WORKSPACE, grid);
+    const bool split = a.workspace && a.workspace_bytes >= WORKSPACE;
+    p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 0,
+                      TILES, 1, TILES, split};
+    line_grid(p.line, grid);
     p.lse = a.lse;
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sink_mode == 1 ? a.sinks : nullptr;

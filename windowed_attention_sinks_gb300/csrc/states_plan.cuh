@@ -3,7 +3,8 @@
 // A unit is a tile of one sequence and KV head with all that it meets: a tile of query rows
 // with its steps over 128-key tiles (the attention), or 512 keys with their steps over tiles
 // of query rows (KEYS: the key weights). Units are numbered sequence by sequence, KV
-// head by KV head; their steps in a row, and before each unit's steps `extra` for what a
+// head by KV head; their steps in a row, by what one costs (the last unit of a head, whose
+// tiles are not all there, less), and before each unit's steps `extra` for what a
 // unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
 // piece may begin and end inside a unit: a ragged batch then keeps every SM busy for the
 // same time, whatever its lengths, and a few units spread over all SMs. The
@@ -25,7 +26,9 @@ struct LineArgs {
     const int32_t *cu, *starts, *lens;
     int B, T, S, Hkv;
     int tokens;  // of a tile of query rows
-    int extra;   // a unit's own cost, in steps
+    int half;    // tokens up to which such a tile costs less
+    int cost, less;  // a step's cost, and with such a tile
+    int extra;   // a unit's own cost
     int split;   // 0: no workspace, pieces end at unit boundaries
     uint32_t grid_mul, grid_shift;  // x / grid = (high(mul x) + x) >> shift for 0 <= x < 2^31
 };
@@ -34,9 +37,11 @@ struct LineUnit {
     StateSeq s;
     int b, h, u, nu;     // sequence, KV head, unit of its nu
     int steps;           // at least one (an empty one's is masked)
+    int one, last;       // a step's cost, and in the last of a head's units
     int begin, end;      // the steps of this piece, 0 .. steps
     int c0, parts;       // of a cut unit: its first piece, and how many
     __device__ __forceinline__ bool cut() const { return begin > 0 || end < steps; }
+    __device__ __forceinline__ int step_cost() const { return u == nu - 1 ? last : one; }
 };
 
 // Sequence b's units; false if it has none.
@@ -50,7 +55,17 @@ __device__ __forceinline__ bool line_seq(const LineArgs &a, int b, LineUnit &u, 
     const int rows = (int)(((uint32_t)u.s.n + a.tokens - 1) / (uint32_t)a.tokens);
     u.nu = KEYS ? keys : rows;
     u.steps = max(1, KEYS ? rows : keys);
+    u.one = a.cost;
+    if (KEYS)  // of UNIT_TILES, so many are there
+        u.last = (u.s.len - (keys - 1) * TILE_KEYS + STATE_KEYS - 1) / STATE_KEYS * a.less;
+    else
+        u.last = u.s.n - (rows - 1) * a.tokens <= a.half ? a.less : a.cost;
     return u.nu > 0;
+}
+// The line of one KV head of that sequence.
+__device__ __forceinline__ long long line_head(const LineArgs &a, const LineUnit &u) {
+    return (long long)u.nu * ((long long)u.steps * u.one + a.extra) -
+           (long long)u.steps * (u.one - u.last);
 }
 
 // What a CTA starts from (in shared memory).
@@ -97,8 +112,9 @@ __device__ __forceinline__ long long warp_prefix64(long long v) {  // over the l
 __device__ __forceinline__ void line_ends(const LineArgs &a, LineStart &ls, long long total,
                                           bool writes, long long &x0, long long &x1) {
     const long long up = total + gridDim.x - 1;
-    const long long per = up >> 31 ? up / gridDim.x
-                                   : (__umulhi(a.grid_mul, (uint32_t)up) + (uint32_t)up) >> a.grid_shift;
+    long long per = up >> 31 ? up / gridDim.x
+                             : (__umulhi(a.grid_mul, (uint32_t)up) + (uint32_t)up) >> a.grid_shift;
+    per = max(per, (long long)a.cost);  // so that no piece between others lacks a step
     x0 = min(total, blockIdx.x * per);
     x1 = min(total, x0 + per);
     if (writes) {
@@ -110,11 +126,12 @@ __device__ __forceinline__ void line_ends(const LineArgs &a, LineStart &ls, long
 // The unit of position x0, which lies in sequence u.b, whose line starts at `before`.
 __device__ __forceinline__ void line_unit(const LineArgs &a, LineStart &ls, LineUnit &u,
                                           long long x0, long long before) {
-    const long long one = u.steps + a.extra, i = line_div(x0 - before, one);
-    u.h = (int)line_div(i, u.nu);
-    u.u = (int)(i - (long long)u.h * u.nu);
+    const long long head = line_head(a, u), one = (long long)u.steps * u.one + a.extra;
+    u.h = (int)line_div(x0 - before, head);
+    before += u.h * head;
+    u.u = min(u.nu - 1, (int)line_div(x0 - before, one));
     ls.u = u;
-    ls.ustart = before + i * one;
+    ls.ustart = before + u.u * one;
 }
 
 // Batches that one warp plans (line_start_warp), a lane a few sequences: the loading warp does it
@@ -130,7 +147,7 @@ __device__ __forceinline__ void line_start_warp(const LineArgs &a, LineStart &ls
     bool bad = false, wrong;
     long long mine = 0;
     for (int b = b0; b < b1; ++b) {
-        if (line_seq<KEYS>(a, b, u, wrong)) mine += (long long)a.Hkv * u.nu * (u.steps + a.extra);
+        if (line_seq<KEYS>(a, b, u, wrong)) mine += a.Hkv * line_head(a, u);
         bad |= wrong;
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
@@ -141,7 +158,7 @@ __device__ __forceinline__ void line_start_warp(const LineArgs &a, LineStart &ls
 #pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             if (per > 1 && !line_seq<KEYS>(a, b, u, wrong)) continue;
-            const long long all = (long long)a.Hkv * u.nu * (u.steps + a.extra);
+            const long long all = a.Hkv * line_head(a, u);
             if (x0 < before + all) {
                 line_unit(a, ls, u, x0, before);
                 break;
@@ -167,7 +184,7 @@ __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, lon
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
         bool wrong;
-        if (line_seq<KEYS>(a, b, u, wrong)) mine += (long long)a.Hkv * u.nu * (u.steps + a.extra);
+        if (line_seq<KEYS>(a, b, u, wrong)) mine += a.Hkv * line_head(a, u);
         bad |= wrong;
     }
     if (bad && blockIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
@@ -183,7 +200,7 @@ __device__ __forceinline__ void line_start(const LineArgs &a, LineStart &ls, lon
         for (int b = b0; b < b1; ++b) {
             bool wrong;
             if (!line_seq<KEYS>(a, b, u, wrong)) continue;
-            const long long all = (long long)a.Hkv * u.nu * (u.steps + a.extra);
+            const long long all = a.Hkv * line_head(a, u);
             if (x0 < before + all) {
                 line_unit(a, ls, u, x0, before);
                 break;
@@ -213,28 +230,33 @@ template <bool KEYS> struct LineIter {
         if (!live) return;
         u = ls.u;
         ustart = ls.ustart;
-        u.begin = (int)max(0ll, ls.x0 - ustart - a.extra);
+        // a step is the piece's that its first position lies in
+        const long long into = ls.x0 - ustart - a.extra, w = u.step_cost();
+        u.begin = into <= 0 ? 0 : (int)line_div(into + w - 1, w);
         // uncut, the unit is all of the piece's that its first step lies in
         if (!a.split && u.begin > 0) u.begin = u.steps;
         clip(a, ls);
+        if (live && u.begin == u.end) next(a, ls);
     }
-    // The steps of u in this piece (there may be none of the first unit).
+    // The steps of u in this piece.
     __device__ __forceinline__ void clip(const LineArgs &a, const LineStart &ls) {
-        const long long t0 = ustart + a.extra;
-        live = live && t0 + u.begin < x1;
-        u.end = a.split ? (int)min((long long)u.steps, x1 - t0) : u.steps;
+        const long long t0 = ustart + a.extra, w = u.step_cost();
+        live = live && t0 + u.begin * w < x1;
+        u.end = u.steps;
         u.c0 = 0;
         u.parts = 1;
-        if (live && a.split && u.cut()) {
+        if (!live || !a.split) return;
+        if (t0 + (u.steps - 1) * w >= x1) u.end = (int)line_div(x1 - t0 + w - 1, w);
+        if (u.cut()) {
             u.c0 = line_piece(ls, t0);
-            u.parts = line_piece(ls, t0 + u.steps - 1) - u.c0 + 1;
+            u.parts = line_piece(ls, t0 + (u.steps - 1) * w) - u.c0 + 1;
         }
     }
     // To the next unit of the line; there may be none behind this piece.
     __device__ __forceinline__ void next(const LineArgs &a, const LineStart &ls) {
         live = u.end == u.steps;
         if (!live) return;
-        ustart += u.steps + a.extra;
+        ustart += (long long)u.steps * u.step_cost() + a.extra;
         if (++u.u == u.nu) {
             u.u = 0;
             if (++u.h == a.Hkv) {
@@ -316,12 +338,11 @@ __device__ __forceinline__ bool count_wait(uint32_t at, int n, const DevCtx &ctx
     return false;
 }
 
-inline LineArgs line_args(const int32_t *cu, const int32_t *starts, const int32_t *lens, int B, int T,
-                          int S, int Hkv, int tokens, int extra, bool split, int grid) {
-    uint32_t s = 0;
-    while ((1ll << s) < grid) ++s;
-    const uint32_t mul = (uint32_t)((((1ull << s) - grid) << 32) / (uint32_t)grid + 1);
-    return LineArgs{cu, starts, lens, B, T, S, Hkv, tokens, extra, split, mul, s};
+// The division by the grid.
+inline void line_grid(LineArgs &a, int grid) {
+    a.grid_shift = 0;
+    while ((1ll << a.grid_shift) < grid) ++a.grid_shift;
+    a.grid_mul = (uint32_t)((((1ull << a.grid_shift) - grid) << 32) / (uint32_t)grid + 1);
 }
 
 // Rows of heads x d elements, `stride` elements apart, as boxes of 64 columns, `heads_box`
