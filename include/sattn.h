@@ -555,7 +555,8 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
  * h / (H / Hkv). Sinks as for the other entry points (key 0 is the sequence's first state;
  * finite ones beyond 2e38 in size count as that). A row without states has o = 0 and lse =
  * -inf (the sink with NULL_LOGIT). Rows of k and v outside a sequence's range may hold anything,
- * NaN too. A sequence whose numbers contradict one another or the tensors' sizes is skipped
+ * NaN too; inside, a NaN key or query makes its rows NaN, a NaN value its column, and an
+ * infinite value its column infinite or NaN. A sequence whose numbers contradict one another or the tensors' sizes is skipped
  * and reported by sattn_check_device; its rows, and rows behind the last sequence, are not
  * written.
  *   max_q_len >= every sequence's number of queries: a hint that chooses the kernel's
@@ -569,7 +570,8 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
  * denominator and lse from the unrounded ones. fp32: everything in fp32, by a kernel that takes
  * 100 times as long and more.
  * Requirements: H % Hkv == 0, d in {64, 128}; for bf16 H / Hkv <= 128
- * (SATTN_ERR_UNSUPPORTED otherwise); T * H below 2^31; tensors 16-byte aligned.
+ * (SATTN_ERR_UNSUPPORTED otherwise); T * H below 2^31, S at most 2^30; q, k, v and o 16-byte
+ * aligned.
  */
 size_t sattn_cross_workspace_bytes(int32_t max_q_len, int32_t H, int32_t Hkv, int32_t d);
 sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
@@ -619,7 +621,7 @@ sattn_status sattn_cross_key_weights(const void *q, int64_t q_stride, const void
  * A sequence whose range is not in [0, S) is reported and comes out with length 0. Outputs
  * must not overlap inputs (SATTN_ERR_INVALID_ARG where they start at the same address).
  * Requirements: keep >= 1, first, last >= 0, first + last <= keep, d in {64, 128},
- * B * keep * Hkv below 2^31; k, v, k_out, v_out 16-byte aligned.
+ * B * keep * Hkv below 2^31, S at most 2^30; k, v, k_out, v_out 16-byte aligned.
  */
 sattn_status sattn_evict_keys(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                               const float *weights, const int32_t *kv_starts,
@@ -642,13 +644,13 @@ void sattn_set_debug(int on);
 sattn_status sattn_check_device(void *cuda_stream);
 
 /* Upper bound, in nanoseconds, on any single wait inside a kernel (default
- * one second; the paged FP8 kernels wait four seconds at most). A value of 0
+ * one second; the paged FP8 and the encoder-state kernels wait four seconds at most). A value of 0
  * restores the default. */
 void sattn_set_wait_limit_ns(uint64_t ns);
 
 /* Test hook for the failure path of the tensor-core kernels (window,
  * block-sparse, gathered, gathered FP8, paged FP8, block-selection stats and
- * sums). With
+ * sums, cross attention and its key weights). With
  * `on` nonzero, launches made afterwards start with their MMA-issuing thread
  * waiting for a barrier phase that nothing completes: that wait runs out
  * after the wait limit, the kernel records SATTN_ERR_TIMEOUT in the device

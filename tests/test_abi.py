@@ -272,7 +272,7 @@ def test_encoder_state_refusals(lib):
     assert rope(T=0, q=None) == 0  # empty: no work
 
     shape = dict(B=2, T=4, S=100, n=1, H=32, Hkv=8, d=128)
-    common = (dict(B=-1), dict(T=-1), dict(S=-1), dict(n=-1), dict(H=0), dict(H=12), dict(Hkv=0),
+    common = (dict(B=-1), dict(T=-1), dict(S=-1), dict(S=(1 << 30) + 1), dict(n=-1), dict(H=0), dict(H=12), dict(Hkv=0),
               dict(d=96), dict(sinks=None), dict(mode=3), dict(scale=0.0),
               dict(scale=float("nan")), dict(scale=float("inf")), dict(dtype=7), dict(qs=4095),
               dict(qs=4100), dict(ks=1020), dict(ks=1028), dict(q=None), dict(k=None),
@@ -307,7 +307,7 @@ def test_encoder_state_refusals(lib):
                          d=128, keep=8, first=2, last=3, ko=ctypes.c_void_p(0x20000),
                          vo=ctypes.c_void_p(0x30000), wo=g, rows=g, so=g, lo=g, dtype=1), kw)
 
-    for bad in (dict(B=-1), dict(S=-1), dict(Hkv=0), dict(d=32), dict(keep=0), dict(first=-1),
+    for bad in (dict(B=-1), dict(S=-1), dict(S=(1 << 30) + 1), dict(Hkv=0), dict(d=32), dict(keep=0), dict(first=-1),
                 dict(last=-1), dict(first=6), dict(first=2 ** 31 - 1, last=2 ** 31 - 1),
                 dict(dtype=2), dict(ks=1020), dict(vs=1028), dict(keep=1 << 30),
                 dict(keep=1 << 27, B=2, Hkv=8), dict(k=None), dict(v=None), dict(w=None),

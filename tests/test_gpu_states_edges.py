@@ -245,6 +245,21 @@ def test_malformed_sequences_are_skipped_and_reported():
                 sa.check_device()
 
 
+@pytest.mark.parametrize("n", [1, 50])
+def test_a_batch_without_queries(n):
+    c = Case([(0, 100), (0, 3)], 4, 2, 64, tail=5)
+    q, k, v = c.tensors()
+    o, lse = torch.full_like(q, 77.0), torch.full((5, 4), 77.0, device="cuda")
+    sa.cross_fwd(q, k, v, *c.ranges(), max_q_len=n, o=o, lse=lse)
+    w = torch.full((2, c.S), 77.0, device="cuda")
+    sa.cross_key_weights(q, k, lse, *c.ranges(), w, max_q_len=n)
+    sa.check_device()
+    assert torch.all(o == 77.0) and torch.all(lse == 77.0)
+    for s, l in zip(c.start, c.len):
+        assert torch.all(w[:, s:s + l] == 0.0)
+    assert (w == 77.0).sum().item() == 2 * (c.S - 103)
+
+
 def test_no_states_and_no_queries():
     q = torch.randn(3, 4, 64, device="cuda").bfloat16()
     none = torch.empty(0, 2, 64, device="cuda").bfloat16()

@@ -183,8 +183,8 @@ bool valid_rows(int64_t stride, int heads, int d, int64_t unit) {
 
 // Queries [T, H, d] and encoder states [S, Hkv, d] of B sequences.
 bool valid_states(int B, int T, int S, int max_q_len, int H, int Hkv, int d) {
-    return B >= 0 && T >= 0 && S >= 0 && max_q_len >= 0 && H > 0 && Hkv > 0 && H % Hkv == 0 &&
-           (d == 64 || d == 128) && (int64_t)T * H <= INT32_MAX;
+    return B >= 0 && T >= 0 && S >= 0 && S <= 1 << 30 && max_q_len >= 0 && H > 0 && Hkv > 0 &&
+           H % Hkv == 0 && (d == 64 || d == 128) && (int64_t)T * H <= INT32_MAX;
 }
 
 // sm_103 only: the fatbin carries sm_103a code and nothing else.
@@ -730,7 +730,7 @@ sattn_status sattn_evict_keys(const void *k, int64_t k_stride, const void *v, in
                               void *v_out, float *weights_out, int32_t *rows_out,
                               int32_t *out_starts, int32_t *out_lens, sattn_dtype dtype,
                               void *cuda_stream) {
-    if (B < 0 || S < 0 || Hkv <= 0 || (d != 64 && d != 128) || keep < 1 || first < 0 || last < 0 ||
+    if (B < 0 || S < 0 || S > 1 << 30 || Hkv <= 0 || (d != 64 && d != 128) || keep < 1 || first < 0 || last < 0 ||
         (int64_t)first + last > keep || !valid_dtype(dtype))
         return SATTN_ERR_INVALID_ARG;
     if (B > 0 && ((int64_t)B * keep > INT32_MAX || (int64_t)B * keep * Hkv > INT32_MAX))
