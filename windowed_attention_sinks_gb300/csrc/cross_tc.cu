@@ -416,12 +416,12 @@ struct Row {
     bool fresh;  // some row has seen no key yet
 };
 
-// One step: P of the C columns x, packed, and their sum into l. `there`: how many of the
+// One step: P of the C columns x, packed, to store(), and their sum into l. `there`: how many of the
 // columns are keys; key0: the first is the sequence's first, with a biased logit. rescale(alpha)
 // is called (by whole warps) where m moves and O with it; returns false if that gave up.
-template <int C, typename F>
-__device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], uint32_t (&pw)[C / 2], float sx,
-                                      int there, bool key0, float sink, F rescale) {
+template <int C, typename F, typename G>
+__device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], float sx, int there, bool key0,
+                                      float sink, F rescale, G store) {
     if (there < C) {
 #pragma unroll
         for (int e = 0; e < C; ++e) hide_unless(x[e], e < there);
@@ -445,7 +445,9 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], uint32_t (&pw)
             row.far = __any_sync(0xffffffffu, row.m != NOTHING && fabsf(row.m) > FAR);
             if (!rescale(alpha)) return false;
         }
-        // P with m as it is, and its sum
+        // P with m as it is, and its sum, which is looked at while P is on its way: x is
+        // still here should m have to move
+        uint32_t pw[C / 2];
         const float off = row.m == NOTHING ? 0.f : -row.m;
         if (row.far) {  // x - m in two roundings, as above: never above 0 there
             sum = 0.f;
@@ -458,6 +460,7 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], uint32_t (&pw)
                 sum += a + b;
                 pw[e >> 1] = pack_bf16x2(a, b);
             }
+            store(pw);
         } else {
             const uint64_t f2 = f2_pack(sx, sx), off2 = f2_pack(off, off);
             uint64_t part[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
@@ -472,6 +475,7 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], uint32_t (&pw)
                 part[e >> 1 & 1] = f2_add(part[e >> 1 & 1], f2_pack(a, b));
                 pw[e >> 1] = pack_bf16x2(a, b);
             }
+            store(pw);
             float a, b;
             f2_unpack(f2_add(part[0], part[1]), a, b);
             sum = a + b;
@@ -532,19 +536,19 @@ __device__ void softmax_many(const CrossParams &p, Smem<D> &sm, uint32_t tmem_ba
                 const uint32_t s_tmem = tmem + (uint32_t)((x & 1) * CHUNK);
                 if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
                 tc_fence_after();
-                uint32_t xs[CHUNK], pw[CHUNK / 2];
+                uint32_t xs[CHUNK];
                 load_s(s_tmem, xs);
                 tc_wait_ld();
-                if (!weigh(row, xs, pw, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0,
-                           sink, [&](float alpha) {
+                if (!weigh(row, xs, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0, sink,
+                           [&](float alpha) {
                                if (j == u.begin && c == 0) return true;  // no O yet
                                if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
                                tc_fence_after();
                                scale_o<D>(tmem + O_COL, alpha);
                                return true;
-                           }))
+                           },
+                           [&](const uint32_t(&w)[CHUNK / 2]) { store_p<CHUNK>(s_tmem, w); }))
                     return;
-                store_p<CHUNK>(s_tmem, pw);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -687,7 +691,7 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
                 const uint32_t s_tmem = tmem + (uint32_t)((x & 1) * CHUNK);
                 if (!wait(sm.s_full[half][x & 1], x >> 1)) return;
                 tc_fence_after();
-                uint32_t xs[C], pw[C / 2];
+                uint32_t xs[C];
                 load_s(s_tmem + (uint32_t)(copy * C), xs);
                 tc_wait_ld();
                 {  // the other warps' keys
@@ -696,16 +700,18 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
                     for (int k = 1; k < COPIES; ++k)
                         store_p<C>(s_tmem + (uint32_t)(((copy + k) % COPIES) * (C / 2)), zero);
                 }
-                if (!weigh(row, xs, pw, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0,
-                           bias, [&](float alpha) {
+                if (!weigh(row, xs, p.scale_l2, u.s.len - kpos0, p.sink_mode == 1 && kpos0 == 0, bias,
+                           [&](float alpha) {
                                if (j == first && c == 0) return true;  // no O yet
                                if (!wait(sm.pv_done[half][(x - 1) & 1], (x - 1) >> 1)) return false;
                                tc_fence_after();
                                scale_o<D>(tmem + O_COL, alpha);
                                return true;
+                           },
+                           [&](const uint32_t(&w)[C / 2]) {
+                               store_p<C>(s_tmem + (uint32_t)(copy * (C / 2)), w);
                            }))
                     return;
-                store_p<C>(s_tmem + (uint32_t)(copy * (C / 2)), pw);
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
