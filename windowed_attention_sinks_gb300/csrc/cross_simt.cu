@@ -7,7 +7,9 @@
 // registers; the rows of the group pass through shared memory, 16 at a time.
 //
 // Bound by the chain of one key at a time and by fp32 arithmetic: the exact fp32 form, the
-// bf16 kernels are the fast ones.
+// bf16 kernels are the fast ones (with bf16 data, 16 prompts of 17 to 900 queries over 257 to
+// 4100 states: 27 ms against 0.18). bf16 comes here without states, where no tensor map can be
+// made, and the weights also without queries.
 #include <math.h>
 
 #include "internal.h"

@@ -26,7 +26,25 @@
 //               takes longer than its load. The pieces of a unit that is cut between
 //               CTAs are joined by the last of them to arrive.
 // Roles: warp 0 units and TMA; 1, 3 S of the halves; 4, 5 P V; 2 the last V tile's rows;
-// 8-11, 12-15 softmax and epilogue, a thread a row.
+// 6, 7 (FEW) the sums over a unit's streams; 8-11, 12-15 softmax and epilogue, a thread a row.
+//
+// Bound, many rows: what an SM reads from shared memory. S of 64 keys takes 48 cycles an MMA where
+// 128 would take 32 for as many (Q is read again for each), so a tile of 128 keys costs both
+// halves 2560 cycles of operand reads and TMA writes; it takes 2700 to 3000. 4097 queries
+// over 16411 states, 32 heads on 8, d = 128: 725 us, 1.51 PFLOP/s, 0.79 of the bf16 peak (0.74 where
+// the clock falls under the load); 16 prompts of 17 to 900 queries over 257 to 4100 states 183 us,
+// of which the join of cut units is 15 and a unit by itself (first maximum, O) 2 tiles' time.
+// Measured on the way, us for the first:
+//   MMAs issued by single threads, S of 128 keys in one buffer a half       1016
+//     the same by converged warps that elect a lane (states_plan.cuh)        945
+//     and the halves made to take turns (P V and the next S of one, then
+//     of the other; else both wait for products at the same time)            780
+//   S of 64 keys in two buffers, no turns                                    736
+//   P stored before its sum is looked at                                     725
+// Bound, few rows: the memory, 7.2 TB/s while tiles stream; 64 single tokens over 257 to 6404
+// states 156 us, 6.0 TB/s; a unit costs 2200 cycles by itself, a cut one 2600 more. One token
+// over 1601 states 16.4 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
+// loads and divisions), the first tile, one step, the join, in a row.
 #include <math.h>
 #include <stdio.h>
 
@@ -379,7 +397,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t a, const uint32_t *r) {
                  "r"(r[7])
                  : "memory");
 }
-// C columns of S, as W calls of a width that there is; and C / 2 of P.
+// C columns of S, and the C / 2 of P.
 template <int C> __device__ __forceinline__ void load_s(uint32_t at, uint32_t (&x)[C]) {
 #pragma unroll
     for (int i = 0; i < C / 16; ++i) {

@@ -11,7 +11,12 @@
 //
 // A block takes a few tokens: first the cosines and sines of all their pairs, once for all
 // heads, into shared memory, then the heads, two 16-byte vectors an item: the
-// vectors that turn into one another (halves), or neighbours.
+// vectors that turn into one another (halves), or neighbours; the first ones are on their way
+// while the angles are computed.
+//
+// Bound by memory: 65521 tokens of 32 heads, fp32, d = 64: 159 us for 1.07 GB, 0.99 of the copy
+// rate; 14343 tokens of 24 bf16 heads out of rows of 32, d = 128: 35 us for 176 MB, 0.74 (blocks of
+// 256 threads 37, of 512 43; eight rows a thread in a block 37). 16 tokens: 4.4 us, latency.
 #include "internal.h"
 
 namespace sattn {
