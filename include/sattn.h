@@ -550,7 +550,7 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
  *     kv_lens[b] - 1 of k and v. So states may be packed, padded, or shared: sequences may
  *     name the same rows (several hypotheses over the same states can also be the queries
  *     of one sequence: no order is kept between them, and their states are read once).
- *   o [T, H, d] (dtype, contiguous), lse [T, H] float32 or NULL.
+ *   o [T, H, d] (dtype, contiguous; not over q, k or v), lse [T, H] float32 or NULL.
  * Every query of a sequence sees all of its states. Query head h reads KV head
  * h / (H / Hkv). Sinks as for the other entry points (key 0 is the sequence's first state;
  * finite ones beyond 2e38 in size count as that). A row without states has o = 0 and lse =
