@@ -486,3 +486,12 @@ def test_rope_axes_captured_and_on_a_side_stream(dtype):
     got = sa.rope_axes(x, None, pos, f, ax, stream=s)[0]
     s.synchronize()
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("mode", [0, 1, 2])
+@pytest.mark.parametrize("n,G,d", [(1, 8, 128), (6, 1, 64), (6, 5, 128), (15, 4, 64), (8, 8, 128),
+                                   (100, 2, 64)])
+def test_one_sequence_in_more_pieces_than_a_warp_has_lanes(n, G, d, mode):
+    # 129 tiles of keys: a piece each on up to 152 SMs
+    c = Case([(n, 16411)], G, 1, d, seed=n)
+    c.check(*attend(c, mode), mode)

@@ -23,8 +23,8 @@
 //               a sum over its own keys. Every warp runs a softmax of its own (eight in
 //               all, or four with 64 rows); they are joined at a unit's end. What bounds is the
 //               memory, and a tile's chain of products and exponentials, a row a thread,
-//               takes longer than its load. The pieces of a unit that is cut between
-//               CTAs are joined by the last of them to arrive.
+//               takes longer than its load.
+// The pieces of a unit that is cut between CTAs are joined by a second launch.
 // Roles: warp 0 units and TMA; 1, 3 S of the halves; 4, 5 P V; 2 the last V tile's rows;
 // 6, 7 (FEW) the sums over a unit's streams; 8-11, 12-15 softmax and epilogue, a thread a row.
 //
@@ -42,9 +42,12 @@
 //   S of 64 keys in two buffers, no turns                                    736
 //   P stored before its sum is looked at                                     725
 // Bound, few rows: the memory, 7.2 TB/s while tiles stream; 64 single tokens over 257 to 6404
-// states 156 us, 6.0 TB/s; a unit costs 2200 cycles by itself, a cut one 2600 more. One token
-// over 1601 states 16.4 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
-// loads and divisions), the first tile, one step, the join, in a row.
+// states 154 us, 6.1 TB/s; a unit costs 2200 cycles by itself. One token over 1601 states
+// 16.5 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
+// loads and divisions), the first tile, one step, the join, in a row. (Joined by the last
+// piece to arrive, its two warps that add up the streams, and without the launch: the same for
+// this one; 8 tokens of 32 heads over 1500 states 57 us, with the launch 21; 60 rows of one
+// KV head over 16000 states 333 and 37.)
 #include <math.h>
 #include <stdio.h>
 
@@ -85,6 +88,13 @@ struct CrossParams {
     }
 };
 
+// A piece's note for the join launch: of the unit that begins in it and goes on behind it, its
+// first token, KV head, rows (0: there is none) and parts.
+struct JoinNote {
+    int t0, h, rows, parts;
+};
+static_assert(sizeof(JoinNote) <= sizeof(PlanNote), "the notes' part of the workspace");
+
 template <int D> struct alignas(1024) Smem {
     static constexpr int NH = D / 64;                     // 64-column parts of a row
     static constexpr uint32_t PART = 128 * 128;           // 128 rows of 64 bf16
@@ -121,19 +131,8 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
     if ((threadIdx.x & 31) != 0) return;
     volatile int *abort = &sm.abort;
     LineIter<false> it(p.line, sm.line);
-    if (!FEW && p.line.split) {
-        PlanNote n{};
-        if (it.live) {
-            const LineUnit &u = it.u;
-            n.cont = u.begin > 0;
-            n.through = u.begin > 0 && u.end < u.steps;
-            n.t0 = u.s.t0;
-            n.h = u.h;
-            n.row0 = u.u * p.line.tokens * p.G;
-            n.nrows = min(p.line.tokens, u.s.n - u.u * p.line.tokens) * p.G;
-        }
-        reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
-    }
+    JoinNote *note = reinterpret_cast<JoinNote *>(p.ws) + blockIdx.x;
+    if (p.line.split) *note = JoinNote{};
     int t = 0, index = 0, queries = 0;  // loads into the ring; units; loads of Q
     uint32_t raws = 0, on_raw = 0;      // bit i: raw[i]'s phase; slot i's last load counts there
     bool ok = true;
@@ -141,6 +140,9 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
     for (; it.live && ok; it.next(p.line, sm.line)) {
         const LineUnit &u = it.u;
         ok = sm.units.put(index, u, ctx, abort);
+        if (p.line.split && u.begin == 0 && u.end < u.steps)
+            *note = JoinNote{u.s.t0 + u.u * p.line.tokens, u.h,
+                             min(p.line.tokens, u.s.n - u.u * p.line.tokens) * p.G, u.parts};
         const bool tail = ragged(u);
         auto ask = [&]() {  // for the unit's queries
             if (index >= 1) ok = ok && bar_wait(smem_u32(&sm.q_empty), (index - 1) & 1, ctx, abort);
@@ -625,26 +627,6 @@ __device__ void softmax_many(const CrossParams &p, Smem<D> &sm, uint32_t tmem_ba
     }
 }
 
-// A row's weights over `n` partial results with maxima m and sums z get(i): the maximum and sum
-// of all (and of a null logit); returns, in lane i < 32, part i's weight z_i 2^(m_i - m).
-template <typename G>
-__device__ __forceinline__ float join_weights(int n, float sink, bool null_sink, float &m, float &z,
-                                              G get) {
-    const int lane = threadIdx.x & 31;
-    float2 mine = lane < n ? get(lane) : make_float2(NOTHING, 0.f);
-    m = fmaxf(null_sink ? sink : NOTHING, mine.x);
-    for (int i = 32 + lane; i < n; i += 32) m = fmaxf(m, get(i).x);
-    m = warp_max(fmaxf(m, NOTHING));
-    const float w = mine.y * ex2(mine.x - m);
-    z = warp_sum(w);
-    for (int i = 32; i < n; i += 32) {
-        const float2 s = i + lane < n ? get(i + lane) : make_float2(NOTHING, 0.f);
-        z += warp_sum(s.y * ex2(s.x - m));
-    }
-    if (null_sink) z += ex2(sink - m);
-    return w;
-}
-
 template <int D> __device__ __forceinline__ void store_row(__nv_bfloat16 *o, const float *acc, int lane) {
     constexpr int E = D / 32;
     uint32_t w[E / 2];
@@ -664,6 +646,8 @@ template <int D, int FEW> struct Out {
         width = min(D, (int)Smem<D>::TILE_BYTES / (STREAMS * cap * 4));
         buffer = reinterpret_cast<float4 *>(sm.q[1]);
     }
+    // A warp adds up 2^shift pieces of 16 bytes of 32 / 2^shift rows at a time
+    __device__ __forceinline__ int shift() const { return 29 - __clz(width); }
     // 16-byte piece c of row r of a stream (neighbouring rows' in different banks)
     __device__ __forceinline__ float4 *piece(int stream, int r, int c) const {
         const int n = width / 4, sw = min(n, 8) - 1;
@@ -758,6 +742,20 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
         float lse2 = z == 0.f ? -INFINITY : m + __log2f(z), inv = z == 0.f ? 0.f : __fdividef(1.f, z);
         if (!cut && p.sink_mode == 2) with_null_sink(bias, lse2, inv);
         const float f = ex2(row.m - m) * inv;
+        if (stream == 0 && r < rows) {
+            if (cut) {
+                part_sums(p.ws)[((size_t)blockIdx.x * 2 + (u.begin > 0 ? 0 : 1)) * FEW + r] =
+                    make_float2(m, z);
+            } else if (p.lse) {
+                if (p.sink_mode == 2) {
+                    const float top = fmaxf(m, bias);
+                    z = fmaf(z, ex2(m - top), ex2(bias - top));
+                    m = top;
+                }
+                p.lse[(size_t)(u.s.t0 + u.u * p.line.tokens + tok) * p.H + head] =
+                    z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
+            }
+        }
         if (worked) {
             if (!wait(sm.o_full[half], units)) return;
             ++units;
@@ -794,101 +792,17 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
     }
 }
 
-// E columns of fp32 that another CTA wrote.
-template <int E> __device__ __forceinline__ void load_row(const float *p, float (&v)[E]) {
-    if constexpr (E == 4) {
-        const float4 x = __ldcg(reinterpret_cast<const float4 *>(p));
-        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-    } else {
-        const float2 x = __ldcg(reinterpret_cast<const float2 *>(p));
-        v[0] = x.x, v[1] = x.y;
-    }
-}
-
-// Joins the parts of a cut unit, for its rows q, q + ADDERS, ... below `end`: a warp, two
-// rows at a time, for the loads in flight. Lane i holds part i's sums, the columns
-// are spread over the lanes. w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
-// null logit), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces.
-template <int D, int FEW, typename F>
-__device__ __forceinline__ void join_parts(const CrossParams &p, int c0, int parts, int q, int end,
-                                           F orow) {
-    constexpr int E = D / 32, N = 2, K = 4;  // rows, and parts, at a time
-    const int lane = threadIdx.x & 31;
-    const float2 *sums = part_sums(p.ws);
-    const float *prows = reinterpret_cast<const float *>(p.ws + plan_rows_offset(FEW));
-    // part i of the unit: the last of piece c0, then the first of c0 + 1, c0 + 2, ..
-    auto slot = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * FEW; };
-#pragma unroll 1
-    for (; q < end; q += N * ADDERS) {
-        float m[N], z[N], inv[N], f[N], acc[N][E] = {};
-        size_t at[N];
-        int r[N];
-#pragma unroll
-        for (int a = 0; a < N; ++a) {  // (in the place of rows behind the last, q again)
-            r[a] = q + a * ADDERS < end ? q + a * ADDERS : q;
-            at[a] = orow(r[a]);
-        }
-#pragma unroll
-        for (int a = 0; a < N; ++a) {
-            const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + (int)(at[a] % p.H))) : 0.f;
-            f[a] = join_weights(parts, null, p.sink_mode == 2, m[a], z[a],
-                                [&](int i) { return __ldcg(sums + slot(i) + r[a]); });
-            // (over their sum, so that values near fp32's largest do not overflow)
-            inv[a] = z[a] == 0.f ? 0.f : 1.f / z[a];
-        }
-#pragma unroll 1
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-#pragma unroll
-            for (int a = 0; a < N; ++a) {
-                if (i0 > 0) {
-                    const float2 s = i0 + lane < parts ? __ldcg(sums + slot(i0 + lane) + r[a])
-                                                       : make_float2(m[a], 0.f);
-                    f[a] = s.y * ex2(s.x - m[a]);
-                }
-                f[a] *= inv[a];
-            }
-            const int cnt = min(32, parts - i0);
-#pragma unroll 1
-            for (int k = 0; k < cnt; k += K) {
-                float x[K][N][E];
-#pragma unroll
-                for (int d = 0; d < K; ++d)
-#pragma unroll
-                    for (int a = 0; a < N; ++a)
-                        load_row<E>(prows + (slot(i0 + min(k + d, cnt - 1)) + r[a]) * D + lane * E,
-                                    x[d][a]);
-#pragma unroll
-                for (int d = 0; d < K; ++d)
-#pragma unroll
-                    for (int a = 0; a < N; ++a) {
-                        const float fk = __shfl_sync(0xffffffffu, f[a], min(k + d, 31));
-                        if (k + d < cnt)
-#pragma unroll
-                            for (int e = 0; e < E; ++e) acc[a][e] = fmaf(fk, x[d][a][e], acc[a][e]);
-                    }
-            }
-        }
-#pragma unroll
-        for (int a = 0; a < N; ++a) {
-            if (q + a * ADDERS >= end) break;
-            store_row<D>(p.o + at[a] * D, acc[a], lane);
-            if (p.lse && lane == 0)
-                p.lse[at[a]] = z[a] == 0.f ? -INFINITY : (m[a] + log2f(z[a])) * LN2;
-        }
-    }
-}
-
-// Adds up the streams of a unit's rows, a warp a row, its columns spread over the lanes, and
-// writes them; the last of a cut unit's pieces joins them.
+// Adds up the streams of a unit's rows, a lane 16 bytes of a row, and writes them.
 template <int D, int FEW>
 __device__ void add_up(const CrossParams &p, Smem<D> &sm, int w, const DevCtx &ctx) {
-    constexpr int STREAMS = 256 / FEW, E = D / 32;
+    constexpr int STREAMS = 256 / FEW;
     const int lane = threadIdx.x & 31;
     volatile int *abort = &sm.abort;
     auto wait = [&](uint64_t &bar, int phase) {
         return __all_sync(0xffffffffu, bar_wait(smem_u32(&bar), phase & 1, ctx, abort));
     };
     const Out<D, FEW> out(p, sm);
+    const int shift = out.shift(), c = lane & ((1 << shift) - 1), each = 32 >> shift;
     int outs = 0;
     for (int i = 0;; ++i) {
         if (!__all_sync(0xffffffffu, sm.units.wait(i, ctx, abort))) return;
@@ -908,48 +822,24 @@ __device__ void add_up(const CrossParams &p, Smem<D> &sm, int w, const DevCtx &c
         for (int c0 = 0; c0 < D; c0 += out.width, ++outs) {
             if (!wait(sm.out_full, outs)) return;
 #pragma unroll 1
-            for (int q = w; q < rows; q += ADDERS) {
-                const size_t at = orow(q);
-                if (c0 == 0) {  // the row's maximum and sum, as its threads have them too
-                    float m, z;
-                    const float null = p.sink_mode == 2 ? sink_log2(__ldg(p.sinks + (int)(at % p.H))) : 0.f;
-                    join_weights(STREAMS, null, p.sink_mode == 2 && !cut, m, z,
-                                 [&](int st) { return sm.ml[st * FEW + q]; });
-                    if (lane == 0 && cut) part_sums(p.ws)[slot0 + q] = make_float2(m, z);
-                    else if (lane == 0 && p.lse) p.lse[at] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
-                }
-                if (lane * E >= out.width) continue;
-                float acc[E] = {};
+            for (int q = w * each + (lane >> shift); q < rows; q += ADDERS * each) {
+                float4 acc = *out.piece(0, q, c);
 #pragma unroll
-                for (int st = 0; st < STREAMS; ++st) {
-                    const float *x = reinterpret_cast<const float *>(out.piece(st, q, lane * E / 4)) +
-                                     (lane * E & 3);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += x[e];
+                for (int st = 1; st < STREAMS; ++st) {
+                    const float4 x = *out.piece(st, q, c);
+                    acc.x += x.x, acc.y += x.y, acc.z += x.z, acc.w += x.w;
                 }
-                if (cut) {
-                    float *prow = reinterpret_cast<float *>(p.ws + plan_rows_offset(FEW)) +
-                                  (slot0 + q) * D + c0 + lane * E;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) prow[e] = acc[e];
-                } else {
-                    store_row<D>(p.o + at * D + c0, acc, lane);
-                }
+                if (cut)
+                    *reinterpret_cast<float4 *>(
+                        reinterpret_cast<float *>(p.ws + plan_rows_offset(FEW)) + (slot0 + q) * D +
+                        c0 + 4 * c) = acc;
+                else
+                    *reinterpret_cast<uint2 *>(p.o + orow(q) * D + c0 + 4 * c) =
+                        make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&sm.out_empty));
         }
-        if (!cut) continue;
-        // the last of the pieces' warps w to get here joins their rows
-        __threadfence();
-        int last = 0;
-        if (lane == 0) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are zero
-            last = atomicAdd(join_counters(p.ws) + w * MAX_PIECES + u.c0, 1u) == (unsigned)u.parts - 1;
-        }
-        if (!__shfl_sync(0xffffffffu, last, 0)) continue;
-        __threadfence();
-        join_parts<D, FEW>(p, u.c0, u.parts, w, rows, orow);
     }
 }
 
@@ -962,7 +852,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     using S = Smem<D>;
     S &sm = *reinterpret_cast<S *>(dsmem);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (!FEW) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.line.split) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (smem_u32(dsmem) & 1023u) {  // the swizzle is anchored to 1024-byte boundaries
         if (threadIdx.x == 0) record_error(ctx, DEVERR_LAYOUT);
         return;
@@ -1041,24 +931,85 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
     }
     tc_fence_before();
     __syncthreads();
-    if (threadIdx.x == 0) {
-        // (no CTA ends before the counters are zero: they are the next call's then)
-        if (FEW) asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
-    }
+    if (threadIdx.x == 0 && sm.abort == TIMED_OUT) record_error(ctx, DEVERR_TIMEOUT);
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
     }
 }
 
-// Zeroes a call's join counters, which lie in its workspace so that no call meets another
-// one's: the kernel, its programmatic dependent, starts beside it and waits for it before a
-// piece arrives.
-__global__ void __launch_bounds__(ADDERS *MAX_PIECES) zero_cross_counters(uint8_t *ws) {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    static_assert(ADDERS * sizeof(unsigned) <= sizeof(PlanNote), "the counters' part of the workspace");
-    join_counters(ws)[threadIdx.x] = 0;
+// Joins the parts of cut units, a programmatic dependent of the kernel that wrote them: block x
+// has the unit that is cut behind piece x, a warp a row of it. w_i = z_i 2^(m_i - m),
+// lse = m + log2 sum_i w_i (+ the null logit), o = sum_i w_i o_i / sum_i w_i, in the order of the
+// pieces. Lane i holds part i's sums, the columns are spread over the lanes. It is latency
+// that counts, of three rounds of loads (note, sums, rows): K rows are on their way at a time.
+constexpr int JOIN_THREADS = 256;
+template <int D, int K>
+__global__ void __launch_bounds__(JOIN_THREADS)
+cross_join(const uint8_t *ws, int slots, int H, int G, const float *sinks, int null_sink,
+            __nv_bfloat16 *o, float *lse) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int E = D / 32, BLOCKS = MAX_PIECES / 32;
+    const int lane = threadIdx.x & 31;
+    const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
+    const JoinNote n = reinterpret_cast<const JoinNote *>(ws)[blockIdx.x];
+    if (r >= n.rows) return;
+    // part i of the unit: the last of piece x, then the first of x + 1, x + 2, ..
+    auto slot = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * slots + r; };
+    const float2 *sums = reinterpret_cast<const float2 *>(ws + plan_sums_offset());
+    const float *rows = reinterpret_cast<const float *>(ws + plan_rows_offset(slots)) + lane * E;
+    const int tok = r / G, head = n.h * G + r - tok * G;
+    const size_t out = (size_t)(n.t0 + tok) * H + head;
+    const float null = null_sink ? sink_log2(__ldg(sinks + head)) : -INFINITY;
+    auto get = [&](int i) { return i < n.parts ? sums[slot(i)] : make_float2(NOTHING, 0.f); };
+    const float2 mine = get(lane);
+    float m = fmaxf(fmaxf(null, NOTHING), mine.x);
+    if (n.parts > 32) {
+#pragma unroll
+        for (int b = 1; b < BLOCKS; ++b) m = fmaxf(m, get(32 * b + lane).x);
+    }
+    m = warp_max(m);
+    float w = mine.y * ex2(mine.x - m), z = w;
+    if (n.parts > 32) {
+#pragma unroll
+        for (int b = 1; b < BLOCKS; ++b) {
+            const float2 s = get(32 * b + lane);
+            z += s.y * ex2(s.x - m);
+        }
+    }
+    z = warp_sum(z) + ex2(null - m);  // (0 without a null logit)
+    // (over their sum, so that values near fp32's largest do not overflow)
+    const float inv = z == 0.f ? 0.f : 1.f / z;
+    float acc[E] = {};
+#pragma unroll 1
+    for (int i0 = 0; i0 < n.parts; i0 += 32) {
+        if (i0 > 0) {
+            const float2 s = get(i0 + lane);
+            w = s.y * ex2(s.x - m);
+        }
+        w *= inv;
+        const int cnt = min(32, n.parts - i0);
+#pragma unroll 1
+        for (int k = 0; k < cnt; k += K) {
+            float x[K][E];
+#pragma unroll
+            for (int d = 0; d < K; ++d) {
+                if (k + d >= cnt) continue;
+                const float *at = rows + slot(i0 + k + d) * D;
+                if constexpr (E == 4) *reinterpret_cast<float4 *>(x[d]) = *reinterpret_cast<const float4 *>(at);
+                else *reinterpret_cast<float2 *>(x[d]) = *reinterpret_cast<const float2 *>(at);
+            }
+#pragma unroll
+            for (int d = 0; d < K; ++d) {
+                const float f = __shfl_sync(0xffffffffu, w, k + d & 31);
+                if (k + d < cnt)
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = fmaf(f, x[d][e], acc[e]);
+            }
+        }
+    }
+    store_row<D>(o + out * D, acc, lane);
+    if (lse && lane == 0) lse[out] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
 }
 
 // Rows of a unit in the FEW form, or 0 where a sequence has more of a KV head.
@@ -1108,27 +1059,19 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     cfg.blockDim = dim3(NTHREADS);
     cfg.dynamicSmemBytes = sizeof(Smem<D>);
     cfg.stream = s;
+    e = cudaLaunchKernelEx(&cfg, cross_kernel<D, FEW>, tq, tk, tv, p, make_ctx(dev));
+    if (e != cudaSuccess || !split) return e;
+    constexpr int K = FEW ? 8 : 4;  // (parts; of 256 rows there are few, and warps enough)
+    cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows * (FEW ? 1 : 2) + 7) / 8);
+    cfg.blockDim = dim3(JOIN_THREADS);
+    cfg.dynamicSmemBytes = 0;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    if (FEW && p.line.split) {
-        zero_cross_counters<<<1, ADDERS * MAX_PIECES, 0, s>>>(p.ws);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        cfg.numAttrs = 1;
-    }
-    e = cudaLaunchKernelEx(&cfg, cross_kernel<D, FEW>, tq, tk, tv, p, make_ctx(dev));
-    if (e != cudaSuccess || FEW || !p.line.split) return e;
-    PagedArgs j{};  // what the join looks at
-    j.H = a.H;
-    j.Hkv = a.Hkv;
-    j.d = a.d;
-    j.sinks = a.sinks;
-    j.sink_mode = a.sink_mode;
-    j.o = a.o;
-    j.lse = a.lse;
-    j.workspace = a.workspace;
-    return launch_paged_join(j, ROWS, grid, s);
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cross_join<D, K>, (const uint8_t *)p.ws, ROWS, a.H, G, a.sinks,
+                              (int)(a.sink_mode == 2), p.o, a.lse);
 }
 
 }  // namespace

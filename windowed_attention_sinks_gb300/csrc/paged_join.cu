@@ -1,5 +1,5 @@
 // Joins the partial results of units that were cut between CTAs (the workspace of the paged
-// cache's kernels, and of cross attention's): w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
+// cache's kernels): w_c = z_c 2^(m_c - m), lse = m + log2 sum_c w_c (+ the
 // null-logit sink, once), o = sum_c w_c o_c / sum_c w_c, in the order of the pieces.
 //
 // A warp takes a row of the unit that a piece boundary cuts, if that boundary is the
