@@ -128,7 +128,8 @@ bool verbose() {
 
 CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, uint32_t rank, void *base,
                            const uint64_t *dims, const uint64_t *strides_bytes,
-                           const uint32_t *box, CUtensorMapSwizzle swizzle) {
+                           const uint32_t *box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion) {
     std::call_once(g_encode_once, [] {
         void *fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -142,7 +143,7 @@ CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, uint32_t
     return g_encode(map, dtype, rank, base, reinterpret_cast<const cuuint64_t *>(dims),
                     reinterpret_cast<const cuuint64_t *>(strides_bytes),
                     reinterpret_cast<const cuuint32_t *>(box), estride,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, promotion,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 

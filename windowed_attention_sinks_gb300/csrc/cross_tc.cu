@@ -42,11 +42,11 @@
 //   S of 64 keys in two buffers, no turns                                    736
 //   P stored before its sum is looked at                                     725
 // Bound, few rows: the memory, 7.2 TB/s while tiles stream; 64 single tokens over 257 to 6404
-// states 154 us, 6.1 TB/s; a unit costs 2200 cycles by itself. One token over 1601 states
-// 16.5 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
+// states 148 us, 6.4 TB/s, with d = 64 82 us, 5.7 TB/s; a unit costs 2200 cycles by itself. One
+// token over 1601 states 14.6 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
 // loads and divisions), the first tile, one step, the join, in a row. (Joined by the last
 // piece to arrive, its two warps that add up the streams, and without the launch: the same for
-// this one; 8 tokens of 32 heads over 1500 states 57 us, with the launch 21; 60 rows of one
+// this one token; 8 tokens of 32 heads over 1500 states 57 us, with the launch 21; 60 rows of one
 // KV head over 16000 states 333 and 37.)
 #include <math.h>
 #include <stdio.h>
@@ -138,7 +138,8 @@ __device__ void load_tiles(const CrossParams &p, const CUtensorMap *tq,
     bool ok = true;
 #pragma unroll 1
     for (; it.live && ok; it.next(p.line, sm.line)) {
-        const LineUnit &u = it.u;
+        LineUnit u = it.u;
+        u.h = p.line.head(u.h);
         ok = sm.units.put(index, u, ctx, abort);
         if (p.line.split && u.begin == 0 && u.end < u.steps)
             *note = JoinNote{u.s.t0 + u.u * p.line.tokens, u.h,
@@ -946,7 +947,7 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 constexpr int JOIN_THREADS = 256;
 template <int D, int K>
 __global__ void __launch_bounds__(JOIN_THREADS)
-cross_join(const uint8_t *ws, int slots, int H, int G, const float *sinks, int null_sink,
+cross_join(const uint8_t *ws, int slots, int side, int H, int G, const float *sinks, int null_sink,
             __nv_bfloat16 *o, float *lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int E = D / 32, BLOCKS = MAX_PIECES / 32;
@@ -954,8 +955,8 @@ cross_join(const uint8_t *ws, int slots, int H, int G, const float *sinks, int n
     const int r = blockIdx.y * (JOIN_THREADS / 32) + (threadIdx.x >> 5);
     const JoinNote n = reinterpret_cast<const JoinNote *>(ws)[blockIdx.x];
     if (r >= n.rows) return;
-    // part i of the unit: the last of piece x, then the first of x + 1, x + 2, ..
-    auto slot = [&](int i) { return ((size_t)(blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * slots + r; };
+    // part i of the unit: the last of CTA x, then the first of x + side, x + 2 side, ..
+    auto slot = [&](int i) { return ((size_t)(blockIdx.x + i * side) * 2 + (i == 0 ? 1 : 0)) * slots + r; };
     const float2 *sums = reinterpret_cast<const float2 *>(ws + plan_sums_offset());
     const float *rows = reinterpret_cast<const float *>(ws + plan_rows_offset(slots)) + lane * E;
     const int tok = r / G, head = n.h * G + r - tok * G;
@@ -1027,12 +1028,13 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.G = G;
     p.tokens = FEW ? min(FEW / G, max(1, a.max_q_len)) : 128 / G;
     p.rows = p.tokens * G;
-    const int grid = min(dev.sm_count, MAX_PIECES);
     const bool split = a.workspace && a.workspace_bytes >= plan_workspace(ROWS, D);
     p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv,
                       FEW ? p.tokens : 2 * p.tokens, FEW ? 0 : p.tokens, COST, FEW ? COST : LESS,
                       FEW ? (D == 128 ? 1 : 3) * COST : 2 * COST, split};
-    line_grid(p.line, grid);
+    // (many rows are not bound by the memory: no gain)
+    const int side = FEW && a.Hkv % 2 == 0 && dev.sm_count > 1 ? 2 : 1;
+    const int grid = line_grid(p.line, min(dev.sm_count, MAX_PIECES), side);
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sinks;
     p.sink_mode = a.sink_mode;
@@ -1070,7 +1072,7 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cross_join<D, K>, (const uint8_t *)p.ws, ROWS, a.H, G, a.sinks,
+    return cudaLaunchKernelEx(&cfg, cross_join<D, K>, (const uint8_t *)p.ws, ROWS, side, a.H, G, a.sinks,
                               (int)(a.sink_mode == 2), p.o, a.lse);
 }
 

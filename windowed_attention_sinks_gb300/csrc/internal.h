@@ -45,7 +45,8 @@ bool verbose();
 // cuTensorMapEncodeTiled through the driver entry point (no libcuda link).
 CUresult encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, uint32_t rank,
                            void *base, const uint64_t *dims, const uint64_t *strides_bytes,
-                           const uint32_t *box, CUtensorMapSwizzle swizzle);
+                           const uint32_t *box, CUtensorMapSwizzle swizzle,
+                           CUtensorMapL2promotion promotion = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 struct WindowArgs {
     const void *q, *k, *v;

@@ -21,8 +21,8 @@
 // room for a second. 8 prompts of 100 to 2000 queries over 1000 to 8000 states, 32 heads on 8,
 // d = 128: 171 us, 1.35 PFLOP/s, 0.70 of the bf16 peak. (Two tiles a unit, a group of warps each, its
 // rows' denominators loaded by itself: 252. The tile that is ready first issued first: 187.)
-// Bound, few rows: the memory. 64 single tokens over 257 to 6404 states: 86 us with the second
-// launch, 5.6 TB/s.
+// Bound, few rows: the memory. 64 single tokens over 257 to 6404 states: 90 us with the second
+// launch, 5.4 TB/s; with d = 64 48 us (66 with pieces of one head and rows of two, states_plan.cuh).
 #include <math.h>
 #include <stdio.h>
 
@@ -99,7 +99,7 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
             n.cont = u.begin > 0;
             n.through = u.begin > 0 && u.end < u.steps;
             n.t0 = u.s.s0 + u.u * UNIT_KEYS;
-            n.h = u.h;
+            n.h = p.line.head(u.h);
             n.nrows = min(UNIT_KEYS, u.s.len - u.u * UNIT_KEYS);
         }
         reinterpret_cast<PlanNote *>(p.ws)[blockIdx.x] = n;
@@ -108,7 +108,8 @@ __device__ void load_tiles(const WeightParams &p, const CUtensorMap *tq, const C
     bool ok = true;
 #pragma unroll 1
     for (; it.live && ok; it.next(p.line, sm.line)) {
-        const LineUnit &u = it.u;
+        LineUnit u = it.u;
+        u.h = p.line.head(u.h);
         ok = sm.units.put(index++, u, ctx, abort);
 #pragma unroll
         for (int g = 0; g < TILES; ++g) {
@@ -447,18 +448,18 @@ weights_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ C
 }
 
 // Adds up the sums of units that were cut, in the order of their pieces: block i takes the unit
-// that the boundary behind piece i cuts, if that is the first inside the unit.
+// that the boundary behind CTA i's piece cuts, if that is the first inside the unit.
 __global__ void __launch_bounds__(UNIT_KEYS)
-add_kernel(const uint8_t *ws, int pieces, int S, float *weights, int accumulate) {
+add_kernel(const uint8_t *ws, int grid, int side, int S, float *weights, int accumulate) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PlanNote *notes = reinterpret_cast<const PlanNote *>(ws);
     const float *sums = reinterpret_cast<const float *>(ws + SUMS_OFFSET);
-    const int c = blockIdx.x + 1, key = threadIdx.x;
-    const PlanNote me = notes[c], prev = notes[c - 1];
+    const int c = blockIdx.x + side, key = threadIdx.x;
+    const PlanNote me = notes[c], prev = notes[c - side];
     if (!me.cont || key >= me.nrows || (prev.cont && prev.through)) return;
-    float w = sums[((size_t)(c - 1) * 2 + 1) * UNIT_KEYS + key] + sums[(size_t)c * 2 * UNIT_KEYS + key];
+    float w = sums[((size_t)(c - side) * 2 + 1) * UNIT_KEYS + key] + sums[(size_t)c * 2 * UNIT_KEYS + key];
     bool on = me.through;
-    for (int i = c + 1; on && i < pieces; ++i) {
+    for (int i = c + side; on && i < grid; i += side) {
         w += sums[(size_t)i * 2 * UNIT_KEYS + key];
         on = notes[i].through;
     }
@@ -476,11 +477,11 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
     p.n = need <= 32 ? 32 : need <= 64 ? 64 : 128;
     const int tokens = min((int)p.n / G, n);
     p.rows = tokens * G;
-    const int grid = min(dev.sm_count, MAX_PIECES);
     const bool split = a.workspace && a.workspace_bytes >= WORKSPACE;
     p.line = LineArgs{a.cu_seqlens, a.kv_starts, a.kv_lens, a.B, a.T, a.S, a.Hkv, tokens, 0,
                       TILES, 1, TILES, split};
-    line_grid(p.line, grid);
+    const int side = p.n < 128 && a.Hkv % 2 == 0 && dev.sm_count > 1 ? 2 : 1;
+    const int grid = line_grid(p.line, min(dev.sm_count, MAX_PIECES), side);
     p.lse = a.lse;
     p.scale_l2 = a.scale * LOG2E;
     p.sinks = a.sink_mode == 1 ? a.sinks : nullptr;
@@ -502,9 +503,9 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
                 p.rows, p.line.split);
     weights_kernel<D><<<grid, NTHREADS, sizeof(Smem<D>), s>>>(tq, tk, p, make_ctx(dev));
     e = cudaGetLastError();
-    if (e != cudaSuccess || !p.line.split || grid < 2) return e;
+    if (e != cudaSuccess || !p.line.split || grid <= side) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(grid - 1));
+    cfg.gridDim = dim3((unsigned)(grid - side));
     cfg.blockDim = dim3(UNIT_KEYS);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -512,7 +513,7 @@ cudaError_t launch(const KeyWeightArgs &a, const DevInfo &dev, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, add_kernel, static_cast<const uint8_t *>(p.ws), grid, a.S,
+    return cudaLaunchKernelEx(&cfg, add_kernel, static_cast<const uint8_t *>(p.ws), grid, side, a.S,
                               a.weights, a.accumulate);
 }
 

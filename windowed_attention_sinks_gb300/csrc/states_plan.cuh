@@ -7,7 +7,11 @@
 // tiles are not all there, less), and before each unit's steps `extra` for what a
 // unit costs by itself, form one line that is cut into equal pieces, one a CTA. A
 // piece may begin and end inside a unit: a ragged batch then keeps every SM busy for the
-// same time, whatever its lengths, and a few units spread over all SMs. The
+// same time, whatever its lengths, and a few units spread over all SMs. Where the memory
+// bounds, two CTAs take a piece side by side, of a group of two heads one each: a token's rows of
+// both lie next to each other, and come from memory as one. (64 tokens over 32 to 6400 states of
+// 8 KV heads, d = 64: 112 us with pieces of one head, of which 23 were rows of other heads that L2
+// fetched and lost, 89 without those (map_rows), 79 so; d = 128, rows of twice the length: 77 and 76.) The
 // pieces of a unit that is cut leave partial results in the workspace, which are joined in a
 // fixed order. Everything is computed from the lengths on the device, so a
 // call needs no host copy of them and can be captured and replayed with other lengths.
@@ -24,13 +28,19 @@ constexpr int UNIT_TILES = 4;    // and tiles in a unit of keys
 
 struct LineArgs {
     const int32_t *cu, *starts, *lens;
-    int B, T, S, Hkv;
+    int B, T, S, Hkv;  // Hkv: heads, or groups of them that CTAs take side by side
     int tokens;  // of a tile of query rows
     int half;    // tokens up to which such a tile costs less
     int cost, less;  // a step's cost, and with such a tile
     int extra;   // a unit's own cost
     int split;   // 0: no workspace, pieces end at unit boundaries
-    uint32_t grid_mul, grid_shift;  // x / grid = (high(mul x) + x) >> shift for 0 <= x < 2^31
+    int side;    // CTAs that share a piece, a head of a group each
+    int pieces;
+    uint32_t mul, shift;  // x / pieces = (high(mul x) + x) >> shift for 0 <= x < 2^31
+
+    __device__ __forceinline__ int piece() const { return side == 2 ? blockIdx.x >> 1 : blockIdx.x; }
+    // The CTA's head of group h.
+    __device__ __forceinline__ int head(int h) const { return side == 2 ? 2 * h + (blockIdx.x & 1) : h; }
 };
 
 struct LineUnit {
@@ -39,7 +49,7 @@ struct LineUnit {
     int steps;           // at least one (an empty one's is masked)
     int one, last;       // a step's cost, and in the last of a head's units
     int begin, end;      // the steps of this piece, 0 .. steps
-    int c0, parts;       // of a cut unit: its first piece, and how many
+    int parts;           // pieces of a unit that begins in this one (not KEYS)
     __device__ __forceinline__ bool cut() const { return begin > 0 || end < steps; }
     __device__ __forceinline__ int step_cost() const { return u == nu - 1 ? last : one; }
 };
@@ -111,11 +121,11 @@ __device__ __forceinline__ long long warp_prefix64(long long v) {  // over the l
 // The CTA's piece of a line of that length.
 __device__ __forceinline__ void line_ends(const LineArgs &a, LineStart &ls, long long total,
                                           bool writes, long long &x0, long long &x1) {
-    const long long up = total + gridDim.x - 1;
-    long long per = up >> 31 ? up / gridDim.x
-                             : (__umulhi(a.grid_mul, (uint32_t)up) + (uint32_t)up) >> a.grid_shift;
+    const long long up = total + a.pieces - 1;
+    long long per = up >> 31 ? up / a.pieces
+                             : (__umulhi(a.mul, (uint32_t)up) + (uint32_t)up) >> a.shift;
     per = max(per, (long long)a.cost);  // so that no piece between others lacks a step
-    x0 = min(total, blockIdx.x * per);
+    x0 = min(total, a.piece() * per);
     x1 = min(total, x0 + per);
     if (writes) {
         ls.x0 = x0;
@@ -243,14 +253,11 @@ template <bool KEYS> struct LineIter {
         const long long t0 = ustart + a.extra, w = u.step_cost();
         live = live && t0 + u.begin * w < x1;
         u.end = u.steps;
-        u.c0 = 0;
         u.parts = 1;
         if (!live || !a.split) return;
         if (t0 + (u.steps - 1) * w >= x1) u.end = (int)line_div(x1 - t0 + w - 1, w);
-        if (u.cut()) {
-            u.c0 = line_piece(ls, t0);
-            u.parts = line_piece(ls, t0 + (u.steps - 1) * w) - u.c0 + 1;
-        }
+        if (!KEYS && u.begin == 0 && u.end < u.steps)
+            u.parts = line_piece(ls, t0 + (u.steps - 1) * w) - a.piece() + 1;
     }
     // To the next unit of the line; there may be none behind this piece.
     __device__ __forceinline__ void next(const LineArgs &a, const LineStart &ls) {
@@ -338,22 +345,29 @@ __device__ __forceinline__ bool count_wait(uint32_t at, int n, const DevCtx &ctx
     return false;
 }
 
-// The division by the grid.
-inline void line_grid(LineArgs &a, int grid) {
-    a.grid_shift = 0;
-    while ((1ll << a.grid_shift) < grid) ++a.grid_shift;
-    a.grid_mul = (uint32_t)((((1ull << a.grid_shift) - grid) << 32) / (uint32_t)grid + 1);
+// Shares the line out to `grid` CTAs, `side` of them a piece; returns the CTAs in use.
+inline int line_grid(LineArgs &a, int grid, int side) {
+    a.side = side;
+    a.Hkv /= side;
+    a.pieces = grid / side;
+    a.shift = 0;
+    while ((1ll << a.shift) < a.pieces) ++a.shift;
+    a.mul = (uint32_t)((((1ull << a.shift) - a.pieces) << 32) / (uint32_t)a.pieces + 1);
+    return a.pieces * side;
 }
 
 // Rows of heads x d elements, `stride` elements apart, as boxes of 64 columns, `heads_box`
-// heads and `rows_box` rows.
+// heads and `rows_box` rows. A row of 64 is half of what L2 would fetch by default: it would read
+// a neighbouring head's as well, which may be gone before it is used.
 inline bool map_rows(CUtensorMap *m, const void *p, int64_t stride, int heads, int d, int rows,
                      int heads_box, int rows_box) {
     const uint64_t dims[3] = {(uint64_t)d, (uint64_t)heads, (uint64_t)rows};
     const uint64_t strides[2] = {(uint64_t)d * 2, (uint64_t)stride * 2};
     const uint32_t box[3] = {64, (uint32_t)heads_box, (uint32_t)rows_box};
     return encode_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims,
-                             strides, box, CU_TENSOR_MAP_SWIZZLE_128B) == CUDA_SUCCESS;
+                             strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                             d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                     : CU_TENSOR_MAP_L2_PROMOTION_L2_256B) == CUDA_SUCCESS;
 }
 
 }  // namespace sattn
