@@ -22,7 +22,8 @@
 // d = 128: 171 us, 1.35 PFLOP/s, 0.70 of the bf16 peak. (Two tiles a unit, a group of warps each, its
 // rows' denominators loaded by itself: 252. The tile that is ready first issued first: 187.)
 // Bound, few rows: the memory. 64 single tokens over 257 to 6404 states: 90 us with the second
-// launch, 5.4 TB/s; with d = 64 48 us (66 with pieces of one head and rows of two, states_plan.cuh).
+// launch, 5.4 TB/s; with d = 64 48 us (128 tokens over as many 91, and 117 before neighbouring
+// heads were taken side by side, states_plan.cuh).
 #include <math.h>
 #include <stdio.h>
 
