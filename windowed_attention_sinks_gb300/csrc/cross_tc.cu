@@ -942,13 +942,15 @@ cross_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUt
 // Joins the parts of cut units, a programmatic dependent of the kernel that wrote them: block x
 // has the unit that is cut behind piece x, a warp a row of it. w_i = z_i 2^(m_i - m),
 // lse = m + log2 sum_i w_i (+ the null logit), o = sum_i w_i o_i / sum_i w_i, in the order of the
-// pieces. Lane i holds part i's sums, the columns are spread over the lanes. It is latency
-// that counts, of three rounds of loads (note, sums, rows): K rows are on their way at a time.
+// pieces, the columns spread over the lanes. Few parts (nearly all units of many rows have two):
+// every lane weighs them all, sums and rows come in one round of loads, and what bounds is
+// the instructions; more: lane i holds part i's sums, and it is latency that counts, so K rows
+// are on their way at a time.
 constexpr int JOIN_THREADS = 256;
 template <int D, int K>
 __global__ void __launch_bounds__(JOIN_THREADS)
-cross_join(const uint8_t *ws, int slots, int side, int H, int G, const float *sinks, int null_sink,
-            __nv_bfloat16 *o, float *lse) {
+cross_join(const uint8_t *ws, int slots, int side, int H, int G, uint32_t g_mul, uint32_t g_shift,
+           const float *sinks, int null_sink, __nv_bfloat16 *o, float *lse) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int E = D / 32, BLOCKS = MAX_PIECES / 32;
     const int lane = threadIdx.x & 31;
@@ -959,18 +961,50 @@ cross_join(const uint8_t *ws, int slots, int side, int H, int G, const float *si
     auto slot = [&](int i) { return ((size_t)(blockIdx.x + i * side) * 2 + (i == 0 ? 1 : 0)) * slots + r; };
     const float2 *sums = reinterpret_cast<const float2 *>(ws + plan_sums_offset());
     const float *rows = reinterpret_cast<const float *>(ws + plan_rows_offset(slots)) + lane * E;
-    const int tok = r / G, head = n.h * G + r - tok * G;
+    const int tok = (int)((__umulhi(g_mul, (uint32_t)r) + (uint32_t)r) >> g_shift), head = n.h * G + r - tok * G;
     const size_t out = (size_t)(n.t0 + tok) * H + head;
     const float null = null_sink ? sink_log2(__ldg(sinks + head)) : -INFINITY;
+    auto load = [&](int i, float (&x)[E]) {
+        const float *at = rows + slot(i) * D;
+        if constexpr (E == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(at);
+        else *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(at);
+    };
+    float acc[E] = {}, x[K][E], m = fmaxf(null, NOTHING), z;
+    if (n.parts <= 4) {
+        float2 part[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            part[d] = make_float2(NOTHING, 0.f);
+            if (d >= n.parts) continue;
+            part[d] = sums[slot(d)];
+            load(d, x[d]);
+        }
+#pragma unroll
+        for (int d = 0; d < 4; ++d) m = fmaxf(m, part[d].x);
+        z = ex2(null - m);  // (0 without a null logit)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) z += part[d].y *= ex2(part[d].x - m);
+        // (over their sum, so that values near fp32's largest do not overflow)
+        const float inv = z == 0.f ? 0.f : 1.f / z;
+#pragma unroll
+        for (int d = 0; d < 4; ++d)
+            if (d < n.parts)
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(part[d].y * inv, x[d][e], acc[e]);
+        store_row<D>(o + out * D, acc, lane);
+        if (lse && lane == 0) lse[out] = z == 0.f ? -INFINITY : (m + log2f(z)) * LN2;
+        return;
+    }
     auto get = [&](int i) { return i < n.parts ? sums[slot(i)] : make_float2(NOTHING, 0.f); };
     const float2 mine = get(lane);
-    float m = fmaxf(fmaxf(null, NOTHING), mine.x);
+    m = fmaxf(m, mine.x);
     if (n.parts > 32) {
 #pragma unroll
         for (int b = 1; b < BLOCKS; ++b) m = fmaxf(m, get(32 * b + lane).x);
     }
     m = warp_max(m);
-    float w = mine.y * ex2(mine.x - m), z = w;
+    float w = mine.y * ex2(mine.x - m);
+    z = w;
     if (n.parts > 32) {
 #pragma unroll
         for (int b = 1; b < BLOCKS; ++b) {
@@ -978,10 +1012,8 @@ cross_join(const uint8_t *ws, int slots, int side, int H, int G, const float *si
             z += s.y * ex2(s.x - m);
         }
     }
-    z = warp_sum(z) + ex2(null - m);  // (0 without a null logit)
-    // (over their sum, so that values near fp32's largest do not overflow)
+    z = warp_sum(z) + ex2(null - m);
     const float inv = z == 0.f ? 0.f : 1.f / z;
-    float acc[E] = {};
 #pragma unroll 1
     for (int i0 = 0; i0 < n.parts; i0 += 32) {
         if (i0 > 0) {
@@ -992,14 +1024,9 @@ cross_join(const uint8_t *ws, int slots, int side, int H, int G, const float *si
         const int cnt = min(32, n.parts - i0);
 #pragma unroll 1
         for (int k = 0; k < cnt; k += K) {
-            float x[K][E];
 #pragma unroll
-            for (int d = 0; d < K; ++d) {
-                if (k + d >= cnt) continue;
-                const float *at = rows + slot(i0 + k + d) * D;
-                if constexpr (E == 4) *reinterpret_cast<float4 *>(x[d]) = *reinterpret_cast<const float4 *>(at);
-                else *reinterpret_cast<float2 *>(x[d]) = *reinterpret_cast<const float2 *>(at);
-            }
+            for (int d = 0; d < K; ++d)
+                if (k + d < cnt) load(i0 + k + d, x[d]);
 #pragma unroll
             for (int d = 0; d < K; ++d) {
                 const float f = __shfl_sync(0xffffffffu, w, k + d & 31);
@@ -1072,7 +1099,7 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cross_join<D, K>, (const uint8_t *)p.ws, ROWS, side, a.H, G, a.sinks,
+    return cudaLaunchKernelEx(&cfg, cross_join<D, K>, (const uint8_t *)p.ws, ROWS, side, a.H, G, p.g_mul, p.g_shift, a.sinks,
                               (int)(a.sink_mode == 2), p.o, a.lse);
 }
 
