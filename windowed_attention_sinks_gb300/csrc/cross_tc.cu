@@ -32,8 +32,8 @@
 // 128 would take 32 for as many (Q is read again for each), so a tile of 128 keys costs both
 // halves 2560 cycles of operand reads and TMA writes; it takes 2700 to 3000. 4097 queries
 // over 16411 states, 32 heads on 8, d = 128: 725 us, 1.51 PFLOP/s, 0.79 of the bf16 peak (0.74 where
-// the clock falls under the load); 16 prompts of 17 to 900 queries over 257 to 4100 states 183 us,
-// of which the join of cut units is 15 and a unit by itself (first maximum, O) 2 tiles' time.
+// the clock falls under the load); 16 prompts of 17 to 900 queries over 257 to 4100 states 180 us,
+// of which the join of cut units is 11 and a unit by itself (first maximum, O) 2 tiles' time.
 // Measured on the way, us for the first:
 //   MMAs issued by single threads, S of 128 keys in one buffer a half       1016
 //     the same by converged warps that elect a lane (states_plan.cuh)        945
@@ -1090,7 +1090,7 @@ cudaError_t launch(const CrossArgs &a, const DevInfo &dev, cudaStream_t s) {
     cfg.stream = s;
     e = cudaLaunchKernelEx(&cfg, cross_kernel<D, FEW>, tq, tk, tv, p, make_ctx(dev));
     if (e != cudaSuccess || !split) return e;
-    constexpr int K = FEW ? 8 : 4;  // (parts; of 256 rows there are few, and warps enough)
+    constexpr int K = FEW ? 8 : 4;  // (of 256 rows there are few parts, and warps enough)
     cfg.gridDim = dim3((unsigned)grid, (unsigned)(p.rows * (FEW ? 1 : 2) + 7) / 8);
     cfg.blockDim = dim3(JOIN_THREADS);
     cfg.dynamicSmemBytes = 0;
