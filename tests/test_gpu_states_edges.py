@@ -495,3 +495,28 @@ def test_one_sequence_in_more_pieces_than_a_warp_has_lanes(n, G, d, mode):
     # 129 tiles of keys: a piece each on up to 152 SMs
     c = Case([(n, 16411)], G, 1, d, seed=n)
     c.check(*attend(c, mode), mode)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,Hkv", [(1, 2), (9, 2), (3, 3), (2, 4)])
+def test_heads_side_by_side_in_many_pieces(n, Hkv, d):
+    # an even number of KV heads goes by pairs; a unit's pieces are then every other CTA's
+    c = Case([(n, 16411), (n, 3)], 3 * Hkv, Hkv, d, seed=Hkv)
+    c.check(*attend(c, 2), 2)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("Hkv,d", [(2, 64), (2, 128), (3, 64)])
+def test_key_weights_of_more_queries_than_the_hint_says(Hkv, d, accumulate):
+    # the form of few rows with many steps a unit: its units are cut between CTAs
+    c = Case([(700, 513), (1, 4), (33, 90)], 2 * Hkv, Hkv, d, seed=d)
+    lse = c.check(*attend(c, 1), 1)
+    full = np.zeros((c.T, 2 * Hkv), np.float32)
+    full[:len(lse)] = lse
+    before = np.random.default_rng(1).random((Hkv, c.S)).astype(np.float32)
+    w = cuda(before)
+    q, k, _ = c.tensors()
+    sa.cross_key_weights(q, k, cuda(full), *c.ranges(), w, max_q_len=1, accumulate=accumulate,
+                         sinks=cuda(c.sinks), sink_mode=1)
+    sa.check_device()
+    c.check_weights(w.cpu().numpy(), full, before, accumulate, 1)
