@@ -458,8 +458,8 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], float sx, int 
             for (int e = 0; e < C; e += 2)
                 mx = max3(mx, e == 0 && key0 ? -INFINITY : __uint_as_float(x[e]),
                           __uint_as_float(x[e + 1]));
-            float top = mx * sx;
-            if (key0) top = fmaxf(top, __uint_as_float(x[0]) * sx + sink);
+            float top = __fmul_rn(mx, sx);
+            if (key0) top = fmaxf(top, __fadd_rn(__fmul_rn(__uint_as_float(x[0]), sx), sink));
             const float mn = fmaxf(row.m, top), alpha = ex2(row.m - mn);
             row.m = mn;
             row.l *= alpha;
@@ -471,14 +471,16 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], float sx, int 
         // still here should m have to move
         uint32_t pw[C / 2];
         const float off = row.m == NOTHING ? 0.f : -row.m;
-        if (row.far) {  // x - m in two roundings, as above: never above 0 there
+        // x - m in two roundings, as m has them: never above 0 there. (One rounding, an fma, would
+        // differ from m by half a step of it, and 2^ of that.)
+        if (row.far) {
             sum = 0.f;
 #pragma unroll
             for (int e = 0; e < C; e += 2) {
-                float a = __uint_as_float(x[e]) * sx;
-                if (e == 0 && key0) a += sink;
-                a = ex2(a + off);
-                const float b = ex2(__uint_as_float(x[e + 1]) * sx + off);
+                float a = __fmul_rn(__uint_as_float(x[e]), sx);
+                if (e == 0 && key0) a = __fadd_rn(a, sink);
+                a = ex2(__fadd_rn(a, off));
+                const float b = ex2(__fadd_rn(__fmul_rn(__uint_as_float(x[e + 1]), sx), off));
                 sum += a + b;
                 pw[e >> 1] = pack_bf16x2(a, b);
             }
