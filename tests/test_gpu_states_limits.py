@@ -56,3 +56,23 @@ def test_logits_so_large_that_one_key_has_it_all(n, spread, dtype, mode):
     rel = 2 * 2.0 ** -8 if dtype == "bf16" else 2.0 ** -20
     got = o.float().cpu().numpy()
     assert np.all(np.abs(got[clear] - wo[clear]) <= rel * np.abs(wo[clear]))
+
+
+# ------------------------------------------------------------------ maxima that move
+
+@pytest.mark.parametrize("G", [1, 6])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 8, 20, 150])
+def test_a_maximum_that_rises_in_every_step(n, d, G):
+    """Keys whose logits climb by 20 every 32 keys, for every other row down instead of up: each
+    step's probabilities are taken twice, and what is kept is in the last maximum's terms."""
+    c = Case([(n, 1111), (n, 640), (n, 64)], 2 * G, 2, d, seed=n + d, tail=0)
+    climb = np.zeros((c.S, 2, 1), np.float32)
+    for s, l in zip(c.start, c.len):
+        climb[s:s + l, :, 0] = (np.arange(l) // 32 * 20.0)[:, None]
+    side = np.where(np.arange(c.T) % 2, 1.0, -1.0)[:, None]
+    c.q[..., 0] = oracle.bf16_round((side * np.ones((1, 2 * G))).astype(np.float32))
+    live = ~np.isnan(c.k[..., :1])
+    c.k[..., :1] = np.where(live, oracle.bf16_round((climb / c.scale).astype(np.float32)), np.nan)
+    o, lse = attend(c)
+    c.check(o, lse, 0)

@@ -452,6 +452,9 @@ __device__ __forceinline__ bool weigh(Row &row, uint32_t (&x)[C], float sx, int 
     float sum;
 #pragma unroll 1
     for (int pass = 0;; ++pass) {
+        // the first pass's P has landed before the second's goes to the same columns: nothing
+        // else orders two stores
+        if (pass > 0) tc_wait_st();
         if (moves) {  // m from these columns, and O and l in its terms
             float mx = -INFINITY;
 #pragma unroll
