@@ -22,6 +22,12 @@ def attend(c, mode=0, hint=None, **kw):
     return o, lse
 
 
+def reported():
+    with pytest.raises(sa.SattnError) as e:
+        sa.check_device()
+    assert e.value.code == 4
+
+
 # ------------------------------------------------------------------ large logits
 
 @pytest.mark.parametrize("mode", [0, 1, 2])
@@ -76,3 +82,76 @@ def test_a_maximum_that_rises_in_every_step(n, d, G):
     c.k[..., :1] = np.where(live, oracle.bf16_round((climb / c.scale).astype(np.float32)), np.nan)
     o, lse = attend(c)
     c.check(o, lse, 0)
+
+
+# ------------------------------------------------------------------ malformed sequences
+
+@pytest.mark.parametrize("bad", ["in front", "behind", "negative"])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_bad_range_of_a_sequence_without_queries_is_reported(dtype, bad):
+    c = Case([(3, 100), (0, 50), (2, 64)], 4, 2, 64, dtype, seed=1)
+    q, k, v = c.tensors()
+    cu, start, lens = c.ranges()
+    if bad == "in front":
+        start[1] = -1
+    else:
+        lens[1] = c.S if bad == "behind" else -1
+    o = torch.full_like(q, 77.0)
+    lse = torch.full((c.T, 4), 77.0, device="cuda")
+    sa.cross_fwd(q, k, v, cu, start, lens, max_q_len=3, o=o, lse=lse)
+    reported()
+    c.check(o, lse, 0)  # the others are right
+    assert torch.all(o[5:] == 77.0) and torch.all(lse[5:] == 77.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_bad_range_where_there_are_no_states_is_reported(dtype):
+    q = torch.randn(4, 4, 64, device="cuda").to(DT[dtype])
+    none = torch.empty(0, 2, 64, device="cuda", dtype=DT[dtype])
+    cu, start, lens = (cuda(np.array(x, np.int32)) for x in ([0, 3, 3], [0, 0], [0, 5]))
+    o, lse = torch.full_like(q, 77.0), torch.full((4, 4), 77.0, device="cuda")
+    sa.cross_fwd(q, none, none, cu, start, lens, o=o, lse=lse)
+    reported()
+    assert torch.all(o[:3] == 0) and torch.isneginf(lse[:3]).all()
+    assert torch.all(o[3:] == 77.0) and torch.all(lse[3:] == 77.0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_malformed_sequences_are_skipped_and_reported(dtype):
+    n, H, Hkv, d = 3, 4, 2, 64
+    c = Case([(n, 100), (n, 50), (n, 80), (n, 64)], H, Hkv, d, dtype, seed=n, tail=0)
+    q, k, v = c.tensors()
+    cu, start, lens = c.ranges()
+    start[1], lens[2] = -1, c.S
+    o, lse = torch.full_like(q, 77.0), torch.full((c.T, H), 77.0, device="cuda")
+    w = torch.full((Hkv, c.S), 7.0, device="cuda")
+    sa.cross_fwd(q, k, v, cu, start, lens, max_q_len=n, o=o, lse=lse)
+    reported()
+    assert torch.all(o[n:3 * n] == 77.0) and torch.all(lse[n:3 * n] == 77.0)
+    ok, wl = attend(c)
+    good = [*range(n), *range(3 * n, 4 * n)]
+    assert torch.equal(o[good], ok[good]) and torch.equal(lse[good], wl[good])
+    sa.cross_key_weights(q, k, wl, cu, start, lens, w, max_q_len=n)
+    reported()
+    for b in (1, 2):
+        assert torch.all(w[:, c.start[b]:c.start[b] + c.len[b]] == 7.0)
+    sa.evict_keys(k, v, w, start, lens, 16)
+    reported()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_cu_seqlens_that_fall_leave_the_others_their_rows(dtype):
+    # sequence 0 has rows 0 .. 4, 1 is malformed, 2 claims row 3 as well, 3 has none
+    c = Case([(5, 90), (0, 40), (0, 130), (0, 20)], 4, 2, 64, dtype, seed=4, tail=1)
+    q, k, v = c.tensors()
+    o, lse = torch.full_like(q, 77.0), torch.full((c.T, 4), 77.0, device="cuda")
+    cu = cuda(np.array([0, 5, 3, 4, 4], np.int32))
+    sa.cross_fwd(q, k, v, cu, *c.ranges()[1:], max_q_len=5, o=o, lse=lse)
+    reported()
+    assert torch.all(o[5:] == 77.0) and torch.all(lse[5:] == 77.0)
+    want, wl = attend(c)
+    rows = [0, 1, 2, 4]
+    assert torch.equal(o[rows], want[rows]) and torch.equal(lse[rows], wl[rows])
+    for bad in ([1, 2, 3, 4, 4], [0, 1, 2, 3, c.T + 1]):
+        sa.cross_fwd(q, k, v, cuda(np.array(bad, np.int32)), *c.ranges()[1:], max_q_len=5)
+        reported()
