@@ -155,3 +155,31 @@ def test_cu_seqlens_that_fall_leave_the_others_their_rows(dtype):
     for bad in ([1, 2, 3, 4, 4], [0, 1, 2, 3, c.T + 1]):
         sa.cross_fwd(q, k, v, cuda(np.array(bad, np.int32)), *c.ranges()[1:], max_q_len=5)
         reported()
+
+
+# ------------------------------------------------------------------ rows without a denominator
+
+@pytest.mark.parametrize("value", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 12, 60, 130])
+def test_a_row_with_an_infinite_lse_weighs_nothing(n, dtype, mode, value):
+    """Whatever its query holds: rows that a caller masks by their lse are often padding."""
+    H, Hkv, d = 8, 4, 64
+    c = Case([(n, 300), (n + 1, 77), (n, 520)], H, Hkv, d, dtype, seed=n)
+    _, wl = oracle.cross_attend(c.q, c.k, np.zeros_like(c.k), c.cu, c.start, c.len, c.sinks, mode,
+                                c.scale)
+    lse = np.where(np.isnan(wl), 0.0, wl).astype(np.float32)
+    rng = np.random.default_rng(n)
+    out = rng.random((c.T, H)) < 0.3
+    out[0, :3], out[n, 1] = True, True
+    lse[out] = np.where(rng.random(out.sum()) < 0.5, np.inf, -np.inf)
+    q, k, _ = c.tensors()
+    poison = q.clone()
+    poison[cuda(out)] = float(value)
+    before = rng.random((Hkv, c.S)).astype(np.float32)
+    w = cuda(before)
+    sa.cross_key_weights(poison, k, cuda(lse), *c.ranges(), w, max_q_len=n + 1, accumulate=True,
+                         sinks=cuda(c.sinks) if mode else None, sink_mode=mode)
+    sa.check_device()
+    c.check_weights(w.cpu().numpy(), lse, before, True, mode)

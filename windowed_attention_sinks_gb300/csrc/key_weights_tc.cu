@@ -67,6 +67,7 @@ template <int D> struct alignas(1024) Smem {
     uint8_t k[TILES][KR][TILE_BYTES];
     uint8_t q[QR][TILE_BYTES];
     float lse[LR][128];  // -lse log2(e), -inf where a row does not count
+    int odd[LR];         // whether a row of the sequence does not count
     LineStart line;
     LineRing<UNITS> units;
     uint64_t k_full[TILES][KR], k_empty[TILES][KR], q_full[QR], q_empty[QR];
@@ -177,14 +178,17 @@ __device__ void load_lse(const WeightParams &p, Smem<D> &sm, const DevCtx &ctx) 
 #pragma unroll 1
         for (int j0 = u.begin; j0 < u.end; j0 += 4) {
             float x[4][4];
+            uint32_t rows = 0;  // bit 4 s + e: x[s][e] is a row's
 #pragma unroll
             for (int s = 0; s < 4; ++s)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int t = (j0 + s) * p.line.tokens + tok[e];
                     x[s][e] = INFINITY;
-                    if (j0 + s < u.end && lane + 32 * e < p.rows && t < u.s.n)
+                    if (j0 + s < u.end && lane + 32 * e < p.rows && t < u.s.n) {
                         x[s][e] = __ldg(p.lse + (size_t)(u.s.t0 + t) * p.H + u.h * p.G + head[e]);
+                        rows |= 1u << (4 * s + e);
+                    }
                 }
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
@@ -196,6 +200,12 @@ __device__ void load_lse(const WeightParams &p, Smem<D> &sm, const DevCtx &ctx) 
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     sm.lse[b][lane + 32 * e] = isinf(x[s][e]) ? -INFINITY : -x[s][e] * LOG2E;
+                bool odd = false;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    odd |= isinf(x[s][e]) && rows >> (4 * s + e) & 1;
+                odd = __any_sync(0xffffffffu, odd);
+                if (lane == 0) sm.odd[b] = odd;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.lse_full[b]));
                 ++q;
@@ -318,9 +328,10 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
             ++x;
             tc_fence_after();
             const float *lse = sm.lse[b];
+            const bool odd = sm.odd[b];
             const int cols = min(p.line.tokens, u.s.n - j * p.line.tokens) * p.G;
             float sum = 0.f;
-            if (cols > 96 && !first) {  // the next 32 columns come while these are summed
+            if (cols > 96 && !first && !odd) {  // the next 32 columns come while these are summed
                 uint32_t xs[2][32];
                 tmem_ld32(tmem, xs[0]);
                 tc_wait_ld();
@@ -348,6 +359,10 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
                     if (cols - c < 32) {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) hide_unless(xs[e], e < cols - c);
+                    }
+                    if (odd) {  // the query of a row that does not count may hold anything
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) hide_unless(xs[e], lse[c + e] != -INFINITY);
                     }
                     if (!first) {
                         sum += sum32(xs, sx2, lse + c);
