@@ -183,3 +183,50 @@ def test_a_row_with_an_infinite_lse_weighs_nothing(n, dtype, mode, value):
                          sinks=cuda(c.sinks) if mode else None, sink_mode=mode)
     sa.check_device()
     c.check_weights(w.cpu().numpy(), lse, before, True, mode)
+
+
+# ------------------------------------------------------------------ large sinks and logits
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 20, 90])
+def test_key_weights_with_extreme_sinks(n, dtype):
+    """A sink so large that the logits are lost in it leaves key 0 everything, one so low nothing
+    where there are other keys; the only key of a sequence has it all in both cases."""
+    H, Hkv, d = 8, 2, 64
+    c = Case([(n, 150), (n, 1), (n, 0), (1, 700)], H, Hkv, d, dtype, seed=n, tail=0)
+    c.sinks = np.array([-3.4e38, -1e30, -np.inf, 40.0, 3.4e38, 1e30, 2.1e38, -3.0], np.float32)
+    _, lse = attend(c, 1)
+    before = np.zeros((Hkv, c.S), np.float32)
+    w = torch.zeros(Hkv, c.S, device="cuda")
+    q, k, _ = c.tensors()
+    sa.cross_key_weights(q, k, lse, *c.ranges(), w, max_q_len=n, sinks=cuda(c.sinks), sink_mode=1)
+    sa.check_device()
+    got = w.cpu().numpy()
+    most = 3e38 * np.log(2)
+    sinks = np.clip(c.sinks.astype(np.float64), -most, most)
+    sinks[2] = -np.inf
+    _, wl = oracle.cross_attend(c.q, c.k, np.zeros_like(c.k), c.cu, c.start, c.len, sinks, 1, c.scale)
+    want = oracle.cross_key_weights(c.q, c.k, wl, c.cu, c.start, c.len, before, False, sinks, 1,
+                                    c.scale)
+    # a weight's and its lse's own error, the largest lse that is not a sink's below 64
+    rel = 3 * c.eps().max() + 2.0 ** -20 + 2.0 ** -21 + 2.0 ** -21 * 64 + 4 * n * 2.0 ** -24
+    assert np.all(np.abs(got - want) <= rel * want + 1e-30)
+
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70])
+def test_key_weights_of_huge_logits_stay_shares(n, dtype, mode):
+    """Logits up to 10^12, of which an fp32 lse is off by thousands: a weight is then no more than
+    its formula says of that lse, and never above 1 a row."""
+    H, Hkv, d = 4, 2, 64
+    c = Case([(n, 300), (n, 33)], H, Hkv, d, dtype, seed=n, tail=0, spread=1e12)
+    c.sinks = np.array([1e10, -1e10, 1e9, 0.0], np.float32)
+    _, lse = attend(c, mode)
+    assert torch.isfinite(lse).all()
+    w = torch.zeros(Hkv, c.S, device="cuda")
+    q, k, _ = c.tensors()
+    sa.cross_key_weights(q, k, lse, *c.ranges(), w, max_q_len=n,
+                         sinks=cuda(c.sinks) if mode else None, sink_mode=mode)
+    sa.check_device()
+    assert torch.isfinite(w).all() and w.max().item() <= 2 * n * (1 + 2 * n * 2.0 ** -24)

@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kWarps * 32) cross_simt_kernel(CrossArgs a, De
     }
     load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b, a.T, a.S, s);
     if (t < s.t0 || t - s.t0 >= s.n) return;  // behind the last sequence
-    const float sink = a.sinks ? sink_log2(__ldg(a.sinks + h)) : 0.f;
+    const float sink = a.sinks ? state_sink(__ldg(a.sinks + h)) : 0.f;
     float q[E], acc[E], kv[E];
     load<T, E>(static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)h * D + lane * E, q);
 #pragma unroll
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(KEYS) weights_simt_kernel(KeyWeightArgs a, Dev
                     float x = INFINITY;  // a row without a denominator weighs nothing
                     if (r < n) x = a.lse[(size_t)(s.t0 + r / G) * a.H + head] * LOG2E;
                     lse2[threadIdx.x] = x == -INFINITY ? INFINITY : x;
-                    sinks[threadIdx.x] = a.sinks ? sink_log2(__ldg(a.sinks + head)) : 0.f;
+                    sinks[threadIdx.x] = a.sinks ? state_sink(__ldg(a.sinks + head)) : 0.f;
                 }
                 __syncthreads();
                 const int c = (int)min((long long)STAGED, n - r0);
@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(KEYS) weights_simt_kernel(KeyWeightArgs a, Dev
 #pragma unroll
                     for (int e = 0; e < D; ++e) x += rows[r][e] * k[e];
                     if (a.sink_mode == 1 && key == 0) x += sinks[r];
-                    w += lse2[r] == INFINITY ? 0.f : ex2(x - lse2[r]);
+                    x -= lse2[r];
+                    if (x > 0.f) x = 0.f;  // (by the rounding of a large lse; a NaN stays)
+                    w += lse2[r] == INFINITY ? 0.f : ex2(x);
                 }
             }
             if (in) {

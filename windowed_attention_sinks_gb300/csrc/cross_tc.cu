@@ -552,7 +552,7 @@ __device__ void softmax_many(const CrossParams &p, Smem<D> &sm, uint32_t tmem_ba
         if (tokens <= 0) continue;
         const bool in = r < p.rows && tok < tokens;
         const int head = u.h * p.G + r - tok * p.G;
-        const float sink = p.sinks && in ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+        const float sink = p.sinks && in ? state_sink(__ldg(p.sinks + head)) : 0.f;
         Row row = {NOTHING, 0.f, false, true};
 #pragma unroll 1
         for (int j = u.begin; j < u.end; ++j) {
@@ -688,7 +688,7 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
         const int rows = min(p.tokens, u.s.n - u.u * p.line.tokens) * p.G;  // of the unit
         const int head = u.h * p.G + r - tok * p.G;
         // of key 0, or of the denominator
-        const float bias = p.sinks && r < rows ? sink_log2(__ldg(p.sinks + head)) : 0.f;
+        const float bias = p.sinks && r < rows ? state_sink(__ldg(p.sinks + head)) : 0.f;
         Row row = {NOTHING, 0.f, false, true};
         const int first = u.begin + half;
 #pragma unroll 1
@@ -969,7 +969,7 @@ cross_join(const uint8_t *ws, int slots, int side, int H, int G, uint32_t g_mul,
     const float *rows = reinterpret_cast<const float *>(ws + plan_rows_offset(slots)) + lane * E;
     const int tok = (int)((__umulhi(g_mul, (uint32_t)r) + (uint32_t)r) >> g_shift), head = n.h * G + r - tok * G;
     const size_t out = (size_t)(n.t0 + tok) * H + head;
-    const float null = null_sink ? sink_log2(__ldg(sinks + head)) : -INFINITY;
+    const float null = null_sink ? state_sink(__ldg(sinks + head)) : -INFINITY;
     auto load = [&](int i, float (&x)[E]) {
         const float *at = rows + slot(i) * D;
         if constexpr (E == 4) *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(at);

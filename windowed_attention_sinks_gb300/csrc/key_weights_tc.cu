@@ -38,6 +38,9 @@ constexpr int SUMS = 4;    // first warp of the sums
 constexpr int UNITS = 4;   // units handed on ahead
 constexpr int TILES = UNIT_TILES, UNIT_KEYS = TILES * STATE_KEYS;
 constexpr int LR = 4;                // steps whose denominators are ahead
+// lse in size from which its rounding counts: where it is off by a thousandth and more, a
+// weight is taken no larger than 1 (of lse 10^10 it could be 2^1000)
+constexpr float LARGE = 1 << 14;
 constexpr uint32_t TMEM_COLS = 512;  // 128 a tile
 
 struct WeightParams {
@@ -67,7 +70,7 @@ template <int D> struct alignas(1024) Smem {
     uint8_t k[TILES][KR][TILE_BYTES];
     uint8_t q[QR][TILE_BYTES];
     float lse[LR][128];  // -lse log2(e), -inf where a row does not count
-    int odd[LR];         // whether a row of the sequence does not count
+    int odd[LR];         // whether a row of the sequence does not count, or has a large one
     LineStart line;
     LineRing<UNITS> units;
     uint64_t k_full[TILES][KR], k_empty[TILES][KR], q_full[QR], q_empty[QR];
@@ -203,7 +206,7 @@ __device__ void load_lse(const WeightParams &p, Smem<D> &sm, const DevCtx &ctx) 
                 bool odd = false;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    odd |= isinf(x[s][e]) && rows >> (4 * s + e) & 1;
+                    odd |= fabsf(x[s][e]) > LARGE && rows >> (4 * s + e) & 1;
                 odd = __any_sync(0xffffffffu, odd);
                 if (lane == 0) sm.odd[b] = odd;
                 __syncwarp();
@@ -272,6 +275,9 @@ __device__ void issue(const WeightParams &p, Smem<D> &sm, uint32_t tmem, int w, 
     int zero = 0;
     bar_wait(smem_u32(&sm.drain[w]), 0, ctx, &zero);
 }
+
+// 0 at most; a NaN stays
+__device__ __forceinline__ float cap(float y) { return y > 0.f ? 0.f : y; }
 
 // The sum of 2^(x sx + l) over 32 columns, l from shared memory.
 __device__ __forceinline__ float sum32(const uint32_t (&xs)[32], uint64_t sx, const float *lse) {
@@ -364,16 +370,16 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
 #pragma unroll
                         for (int e = 0; e < 32; ++e) hide_unless(xs[e], lse[c + e] != -INFINITY);
                     }
-                    if (!first) {
+                    if (!first && !odd) {
                         sum += sum32(xs, sx2, lse + c);
                         continue;
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int col = c + e, h = col - p.token(col) * p.G;
-                        const float z = lane == 0 ? sink_log2(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
+                        const float z = first && lane == 0 ? state_sink(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
                         const float y = fmaf(__uint_as_float(xs[e]), sx, lse[col]);
-                        sum += ex2(y == -INFINITY ? y : y + z);  // (whatever the sink)
+                        sum += ex2(y == -INFINITY ? y : cap(y + z));  // (whatever the sink)
                     }
                 }
                 tc_fence_before();

@@ -23,4 +23,12 @@ __device__ __forceinline__ bool load_states(const int32_t *cu, const int32_t *st
            (long long)s.s0 + s.len <= S;
 }
 
+// A sink in log2 units. The largest finite values stay finite, at a number that
+// fp32's factors ln 2 and log2 e take to an lse and back to itself: a row that a sink decides has
+// this lse, and its one key the weight 2^0. (So do all smaller sinks that decide a row: checked
+// for every mantissa.)
+__device__ __forceinline__ float state_sink(float s) {
+    return isinf(s) ? s : fminf(fmaxf(s * LOG2E, -2.9999998e38f), 2.9999998e38f);
+}
+
 }  // namespace sattn
