@@ -70,7 +70,7 @@ template <int D> struct alignas(1024) Smem {
     uint8_t k[TILES][KR][TILE_BYTES];
     uint8_t q[QR][TILE_BYTES];
     float lse[LR][128];  // -lse log2(e), -inf where a row does not count
-    int odd[LR];         // whether a row of the sequence does not count, or has a large one
+    int cols[LR];        // the step's rows; ~rows where one does not count, or has a large lse
     LineStart line;
     LineRing<UNITS> units;
     uint64_t k_full[TILES][KR], k_empty[TILES][KR], q_full[QR], q_empty[QR];
@@ -208,7 +208,8 @@ __device__ void load_lse(const WeightParams &p, Smem<D> &sm, const DevCtx &ctx) 
                 for (int e = 0; e < 4; ++e)
                     odd |= fabsf(x[s][e]) > LARGE && rows >> (4 * s + e) & 1;
                 odd = __any_sync(0xffffffffu, odd);
-                if (lane == 0) sm.odd[b] = odd;
+                const int cols = min(p.line.tokens, u.s.n - (j0 + s) * p.line.tokens) * p.G;
+                if (lane == 0) sm.cols[b] = odd ? ~cols : cols;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.lse_full[b]));
                 ++q;
@@ -298,6 +299,30 @@ __device__ __forceinline__ float sum32(const uint32_t (&xs)[32], uint64_t sx, co
     return a0 + a1;
 }
 
+// The same of all columns of a step with such rows: without those that do not count, whose
+// query may hold anything, and no more than 1 of each; with the sinks of key 0 for the thread that
+// has it. (A call, told by the sign of the step's rows: with its code inside the loop of the
+// other steps 64 single tokens of d = 64 take 59 us instead of 56.)
+__device__ __noinline__ float sum_apart(const WeightParams &p, uint32_t tmem, int cols,
+                                        const float *lse, const float *sinks) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        uint32_t xs[32];
+        tmem_ld32(tmem + (uint32_t)c, xs);
+        tc_wait_ld();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+            const int col = c + e;
+            const float l = lse[col];  // (-inf behind the last column too)
+            float y = fmaf(__uint_as_float(xs[e]), p.scale_l2, l);
+            if (sinks) y += state_sink(__ldg(sinks + col - p.token(col) * p.G));
+            sum += l == -INFINITY ? 0.f : ex2(cap(y));
+        }
+    }
+    return sum;
+}
+
 // The sums of tile g.
 template <int D>
 __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, const DevCtx &ctx) {
@@ -334,10 +359,9 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
             ++x;
             tc_fence_after();
             const float *lse = sm.lse[b];
-            const bool odd = sm.odd[b];
-            const int cols = min(p.line.tokens, u.s.n - j * p.line.tokens) * p.G;
+            const int cols = sm.cols[b];
             float sum = 0.f;
-            if (cols > 96 && !first && !odd) {  // the next 32 columns come while these are summed
+            if (cols > 96 && !first) {  // the next 32 columns come while these are summed
                 uint32_t xs[2][32];
                 tmem_ld32(tmem, xs[0]);
                 tc_wait_ld();
@@ -366,22 +390,21 @@ __device__ void sum_up(const WeightParams &p, Smem<D> &sm, uint32_t tmem_base, c
 #pragma unroll
                         for (int e = 0; e < 32; ++e) hide_unless(xs[e], e < cols - c);
                     }
-                    if (odd) {  // the query of a row that does not count may hold anything
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) hide_unless(xs[e], lse[c + e] != -INFINITY);
-                    }
-                    if (!first && !odd) {
+                    if (!first) {
                         sum += sum32(xs, sx2, lse + c);
                         continue;
                     }
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         const int col = c + e, h = col - p.token(col) * p.G;
-                        const float z = first && lane == 0 ? state_sink(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
+                        const float z = lane == 0 ? state_sink(__ldg(p.sinks + u.h * p.G + h)) : 0.f;
                         const float y = fmaf(__uint_as_float(xs[e]), sx, lse[col]);
-                        sum += ex2(y == -INFINITY ? y : cap(y + z));  // (whatever the sink)
+                        sum += ex2(y == -INFINITY ? y : y + z);  // (whatever the sink)
                     }
                 }
+                if (cols < 0)
+                    sum = sum_apart(p, tmem, ~cols, lse,
+                                    first && lane == 0 ? p.sinks + u.h * p.G : nullptr);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sm.s_empty[g]));
