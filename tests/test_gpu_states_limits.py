@@ -7,7 +7,7 @@ import torch
 import oracle
 import windowed_attention_sinks_gb300 as sa
 
-from test_gpu_states import DT, Case, cuda
+from test_gpu_states import DT, LENS, Case, cuda
 
 pytestmark = pytest.mark.gpu
 
@@ -230,3 +230,128 @@ def test_key_weights_of_huge_logits_stay_shares(n, dtype, mode):
                          sinks=cuda(c.sinks) if mode else None, sink_mode=mode)
     sa.check_device()
     assert torch.isfinite(w).all() and w.max().item() <= 2 * n * (1 + 2 * n * 2.0 ** -24)
+
+
+# ------------------------------------------------------------------ other forms of the calls
+
+@pytest.mark.parametrize("mode", [0, 1])
+@pytest.mark.parametrize("hint", [1, 4000])
+@pytest.mark.parametrize("lens", ["tokens", "ragged", "long"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_key_weights_without_a_workspace(d, lens, hint, mode):
+    c = Case(LENS[lens], 8, 2, d, seed=5)
+    _, wl = oracle.cross_attend(c.q, c.k, np.zeros_like(c.k), c.cu, c.start, c.len, c.sinks, mode,
+                                c.scale)
+    lse = np.where(np.isnan(wl), 0.0, wl).astype(np.float32)
+    before = np.random.default_rng(1).random((2, c.S)).astype(np.float32)
+    q, k, _ = c.tensors()
+    small = torch.empty(256, dtype=torch.uint8, device="cuda")
+    for add in (False, True):
+        w = cuda(before)
+        sa.cross_key_weights(q, k, cuda(lse), *c.ranges(), w, max_q_len=hint, accumulate=add,
+                             sinks=cuda(c.sinks) if mode else None, sink_mode=mode,
+                             workspace=small)
+        sa.check_device()
+        c.check_weights(w.cpu().numpy(), lse, before, add, mode)
+
+
+@pytest.mark.parametrize("B", [33, 700])
+def test_many_sequences_fp32(B):
+    rng = np.random.default_rng(B)
+    c = Case([(int(rng.integers(0, 3)), int(rng.integers(0, 100))) for _ in range(B)], 2, 1, 64,
+             "f32", seed=B)
+    o, lse = attend(c, 1)
+    wl = c.check(o, lse, 1)
+    full = np.zeros((c.T, 2), np.float32)
+    full[:len(wl)] = wl
+    w = torch.zeros(1, c.S, device="cuda")
+    q, k, _ = c.tensors()
+    sa.cross_key_weights(q, k, cuda(full), *c.ranges(), w, sinks=cuda(c.sinks), sink_mode=1)
+    sa.check_device()
+    c.check_weights(w.cpu().numpy(), full, np.zeros((1, c.S), np.float32), False, 1)
+
+
+def test_sequences_share_states_fp32():
+    H, Hkv, d = 8, 4, 128
+    c = Case([(5, 700)], H, Hkv, d, "f32", seed=1, tail=0)
+    q, k, v = c.tensors()
+    c.n, c.cu = np.ones(5, np.int64), np.arange(6, dtype=np.int32)
+    c.start = c.start[0] + np.array([0, 0, 0, 130, 0], np.int32)
+    c.len = np.array([700, 700, 1, 129, 700], np.int32)
+    o, lse = sa.cross_fwd(q, k, v, *c.ranges(), max_q_len=1)
+    sa.check_device()
+    c.check(o, lse, 0)
+
+
+def test_far_states_fp32():
+    """Rows whose elements lie behind 2^31 elements."""
+    H, Hkv, d, S = 4, 4, 128, 2_110_000
+    kv = torch.empty(S, 2 * Hkv, d, device="cuda")
+    lens, starts = [133, 50], [S - 133, 2_100_000]
+    for s, l in zip(starts, lens):
+        kv[s:s + l] = torch.randn(l, 2 * Hkv, d, device="cuda")
+    c = Case([(3, 133), (3, 50)], H, Hkv, d, "f32", tail=0)
+    c.kv = torch.cat([kv[s:s + l] for s, l in zip(starts, lens)]).cpu().numpy()
+    c.k, c.v, c.S = c.kv[:, :Hkv], c.kv[:, Hkv:], 183
+    c.start, c.len = np.array([0, 133], np.int32), np.array(lens, np.int32)
+    at = cuda(c.cu), cuda(np.array(starts, np.int32)), cuda(c.len)
+    q, k, v = cuda(c.q), kv[:, :Hkv], kv[:, Hkv:]
+    o, lse = sa.cross_fwd(q, k, v, *at)
+    sa.check_device()
+    wl = c.check(o, lse, 0)
+    w = torch.zeros(Hkv, S, device="cuda")
+    sa.cross_key_weights(q, k, lse, *at, w)
+    sa.check_device()
+    near = np.concatenate([w[:, s:s + l].cpu().numpy() for s, l in zip(starts, lens)], 1)
+    c.check_weights(near, wl.astype(np.float32), np.zeros_like(near), False, 0)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("mode", [0, 2])
+@pytest.mark.parametrize("n", [1, 14, 130])
+def test_cross_attention_without_lse(n, mode, dtype):
+    """lse = NULL in C; the binding always makes one."""
+    H, Hkv, d = 8, 2, 128
+    c = Case([(n, 900), (1, 64), (n, 0)], H, Hkv, d, dtype, seed=n)
+    want, _ = attend(c, mode)
+    q, k, v = c.tensors()
+    cu, start, lens = c.ranges()
+    o = torch.full_like(q, 77.0)
+    sinks = cuda(c.sinks)
+    nb = sa.cross_workspace_bytes(n, H, Hkv, d)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    rc = sa.lib().sattn_cross_fwd(
+        q.data_ptr(), H * d, k.data_ptr(), 2 * Hkv * d, v.data_ptr(), 2 * Hkv * d, cu.data_ptr(),
+        start.data_ptr(), lens.data_ptr(), 3, c.T, c.S, n, H, Hkv, d, sinks.data_ptr(), mode,
+        c.scale, o.data_ptr(), None, ws.data_ptr(), nb, 1 if dtype == "bf16" else 0,
+        torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    sa.check_device()
+    live = int(c.cu[-1])
+    assert torch.equal(o[:live], want[:live]) and torch.all(o[live:] == 77.0)
+
+
+def test_evict_of_shared_and_of_no_states():
+    Hkv, d, keep = 2, 64, 40
+    rng = np.random.default_rng(0)
+    k = torch.randn(300, 2 * Hkv, d, device="cuda").bfloat16()
+    w = rng.random((Hkv, 300)).astype(np.float32)
+    start, lens = [0, 0, 100, 299, 7, 300], [300, 300, 150, 1, 0, 0]
+    got = sa.evict_keys(k[:, :Hkv], k[:, Hkv:], cuda(w), cuda(np.array(start, np.int32)),
+                        cuda(np.array(lens, np.int32)), keep, 3, 5)
+    sa.check_device()
+    want = oracle.evict_keys(w, start, lens, keep, 3, 5)
+    assert np.array_equal(got[3].cpu().numpy(), want)
+    at = np.repeat(np.array(start), keep)[None] + want
+    for h in range(Hkv):
+        live = want[h] >= 0
+        rows = cuda(at[h][live].astype(np.int64))
+        assert torch.equal(got[0][cuda(live), h], k[rows, h])
+        assert torch.equal(got[1][cuda(live), h], k[rows, Hkv + h])
+    none = torch.empty(0, Hkv, d, device="cuda").bfloat16()
+    zero = torch.zeros(2, dtype=torch.int32, device="cuda")
+    ko, vo, wo, rows, at, kept = sa.evict_keys(none, none, torch.empty(Hkv, 0, device="cuda"),
+                                               zero, zero, 3)
+    sa.check_device()
+    assert torch.all(ko == 0) and torch.all(vo == 0) and torch.all(wo == 0)
+    assert torch.all(rows == -1) and kept.tolist() == [0, 0] and at.tolist() == [0, 3]
