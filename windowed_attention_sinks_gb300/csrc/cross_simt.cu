@@ -27,38 +27,46 @@ template <typename T, int E> __device__ __forceinline__ void load(const T *p, fl
     for (int e = 0; e < E; ++e) v[e] = to_f32<T>(p[e]);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32) cross_simt_kernel(CrossArgs a, DevCtx ctx) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    // every block looks at all sequences, also those without queries
+// Reports malformed sequences, those without queries too. A block.
+__device__ __noinline__ void report_bad(const CrossArgs &a, const DevCtx &ctx) {
     StateSeq s;
     bool bad = false;
     for (int b = threadIdx.x; b < a.B; b += kWarps * 32)
         bad |= !load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b, a.T, a.S, s);
-    bad = __syncthreads_or(bad);
-    if (bad && blockIdx.x == 0 && threadIdx.x == 0) record_error(ctx, DEVERR_SEQLENS);
+    if (bad) record_error(ctx, DEVERR_SEQLENS);
+}
+
+// The first good sequence that has token t, or -1: where cu_seqlens falls, a search misses some.
+// A warp.
+__device__ __noinline__ int first_with(const CrossArgs &a, int t) {
+    const int lane = threadIdx.x & 31;
+    StateSeq s;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const bool has = b0 + lane < a.B &&
+                         load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b0 + lane, a.T, a.S, s) &&
+                         t >= s.t0 && t - s.t0 < s.n;
+        const uint32_t found = __ballot_sync(0xffffffffu, has);
+        if (found) return b0 + __ffs(found) - 1;
+    }
+    return -1;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32) cross_simt_kernel(CrossArgs a, DevCtx ctx) {
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0) report_bad(a, ctx);
     const long long row = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
     if (row >= (long long)a.T * a.H) return;
     const int t = (int)(row / a.H), h = (int)(row % a.H), g = h / (a.H / a.Hkv);
-    int b = a.B;  // the row's sequence
-    if (!bad) {
-        b = warp_find(a.B, t, [&](int i) { return (long long)__ldg(a.cu_seqlens + i); });
-    } else {  // the first good one that has it: the starts may be in any order
-        for (int b0 = 0; b0 < a.B; b0 += 32) {
-            const bool has = b0 + lane < a.B &&
-                             load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b0 + lane, a.T, a.S, s) &&
-                             t >= s.t0 && t - s.t0 < s.n;
-            const uint32_t found = __ballot_sync(0xffffffffu, has);
-            if (found) {
-                b = b0 + __ffs(found) - 1;
-                break;
-            }
-        }
-        if (b == a.B) return;  // of no sequence, or of one that is skipped
+    const int b = warp_find(a.B, t, [&](int i) { return (long long)__ldg(a.cu_seqlens + i); });
+    StateSeq s;
+    if (!load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b, a.T, a.S, s) || t < s.t0 ||
+        t - s.t0 >= s.n) {
+        const int other = first_with(a, t);
+        if (other < 0) return;  // of no sequence, or of one that is skipped
+        load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, other, a.T, a.S, s);
     }
-    load_states(a.cu_seqlens, a.kv_starts, a.kv_lens, b, a.T, a.S, s);
-    if (t < s.t0 || t - s.t0 >= s.n) return;  // behind the last sequence
     const float sink = a.sinks ? state_sink(__ldg(a.sinks + h)) : 0.f;
     float q[E], acc[E], kv[E];
     load<T, E>(static_cast<const T *>(a.q) + (size_t)t * a.q_stride + (size_t)h * D + lane * E, q);
