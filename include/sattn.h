@@ -524,7 +524,7 @@ sattn_status sattn_paged_fp8_fwd(const void *q, int64_t q_stride, const uint8_t 
  *     or one another.
  *   positions int32 [axes, T]; inv_freq float32 [rd / 2]; axis uint8 [rd / 2]: column pair i
  *     turns by the angle positions[axis[i]][t] * inv_freq[i] (an axis that is not there is
- *     reported, the pair stays as it is). Pair i is column i with i + rd / 2, or with
+ *     reported, and its angle counts as 0). Pair i is column i with i + rd / 2, or with
  *     interleaved = 1 column 2 i with 2 i + 1, of the first rd columns; the others are
  *     copied. (a, b) becomes (a cos - b sin, b cos + a sin); with inverse = 1 (a cos + b sin,
  *     b cos - a sin), which undoes it and takes gradients of the outputs to the inputs.
@@ -551,14 +551,17 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
  *     name the same rows (several hypotheses over the same states can also be the queries
  *     of one sequence: no order is kept between them, and their states are read once).
  *   o [T, H, d] (dtype, contiguous; not over q, k or v), lse [T, H] float32 or NULL.
- * Every query of a sequence sees all of its states. Query head h reads KV head
- * h / (H / Hkv). Sinks as for the other entry points (key 0 is the sequence's first state;
- * finite ones beyond 2e38 in size count as that). A row without states has o = 0 and lse =
+ * Every query of a sequence sees all of its states. Logits are scale * <q, k> with scale > 0.
+ * Query head h reads KV head h / (H / Hkv). Sinks as for the other entry points, finite or
+ * -infinity (key 0 is the sequence's first state; finite ones beyond 2e38 in size count as
+ * that). A row without states has o = 0 and lse =
  * -inf (the sink with NULL_LOGIT). Rows of k and v outside a sequence's range may hold anything,
  * NaN too; inside, a NaN key or query makes its rows NaN, a NaN value its column, and an
- * infinite value its column infinite or NaN. A sequence whose numbers contradict one another or the tensors' sizes is skipped
- * and reported by sattn_check_device; its rows, and rows behind the last sequence, are not
- * written.
+ * infinite value its column infinite or NaN; sums of finite values beyond 1e30 in size may
+ * overflow before they are divided. A sequence whose numbers contradict one another or the
+ * tensors' sizes is skipped and reported by sattn_check_device, whether it has queries or not
+ * (a call with T = 0 or B = 0 looks at nothing); its rows, and rows behind the last sequence,
+ * are not written. (Where cu_seqlens falls, a row that two good sequences claim is either's.)
  *   max_q_len >= every sequence's number of queries: a hint that chooses the kernel's
  *     form; any value gives right results.
  *   workspace: NULL or a caller-owned device buffer of at least
@@ -566,9 +569,9 @@ sattn_status sattn_rope_axes(const void *q, int64_t q_stride, void *q_out, int64
  *     results and is free again when the call's work has run. Calls that may overlap on
  *     the GPU need one each. Without one, units of work are not cut, which is slower where there
  *     are few.
- * bf16: the tensor cores, probabilities rounded to bf16 for the product with V, the
- * denominator and lse from the unrounded ones. fp32: everything in fp32, by a kernel that takes
- * 100 times as long and more.
+ * bf16: the tensor cores, probabilities rounded to bf16 for the product with V (off by 2^-8 of
+ * sum p |v| at most), the denominator and lse from the unrounded ones. fp32: everything in fp32,
+ * by a kernel that takes 30 (single tokens) to 380 times as long.
  * Requirements: H % Hkv == 0, d in {64, 128}; for bf16 H / Hkv <= 128
  * (SATTN_ERR_UNSUPPORTED otherwise); T * H below 2^31, S at most 2^30; q, k, v and o 16-byte
  * aligned.
@@ -588,7 +591,9 @@ sattn_status sattn_cross_fwd(const void *q, int64_t q_stride, const void *k, int
  *   h of group g of exp(scale <q[i, h], k[kv_starts[b] + j, g]> (+ the key-0 sink) - lse[i, h]),
  * added to what is there with accumulate = 1. Rows of no sequence are left as they are; a
  * sequence without queries gives its rows 0. lse [T, H] is that of sattn_cross_fwd for the same
- * arguments (a row with an infinite one weighs nothing). The row ranges of the sequences
+ * arguments; a row with an infinite one weighs nothing, whatever its query holds. A weight is off
+ * by what its logits are and by 2^-22 |lse| + 2^-20 + 2^-24 a row of it: an fp32 lse says no
+ * more. Where |lse| is above 2^14 a row gives a key 1 at most. The row ranges of the sequences
  * must not overlap (the weights of shared rows are unspecified): pass hypotheses over
  * the same states as the queries of one sequence. Sums are fp32, in a fixed order: the
  * same call gives the same bits. Everything else as for sattn_cross_fwd; the workspace's

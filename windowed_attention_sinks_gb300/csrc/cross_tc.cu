@@ -7,7 +7,8 @@
 //   P = 2^(S scale log2(e) - m), bf16, 64 keys at a time over the columns of S that
 //       have been read; l += its sum, unrounded
 //   O += P V    P from TMEM, 64 keys at a time: while the second half of P is computed the
-//       product with the first runs
+//       product with the first runs. (bf16 because V is: an MMA's operands have one type. It takes
+//       a bf16 output's error from 1.65e-3 to 2.2e-3 of its size.)
 // m is the maximum of a row's first 64 keys and stays unless 64 keys' P sum up to more than
 // 2^15: P is computed on trust in one pass over S that looks for no maximum, and where the
 // sum says that this was wrong m moves, O is rescaled and the pass is repeated.
@@ -28,13 +29,17 @@
 // Roles: warp 0 units and TMA; 1, 3 S of the halves; 4, 5 P V; 2 the last V tile's rows;
 // 6, 7 (FEW) the sums over a unit's streams; 8-11, 12-15 softmax and epilogue, a thread a row.
 //
-// Bound, many rows: what an SM reads from shared memory. S of 64 keys takes 48 cycles an MMA where
-// 128 would take 32 for as many (Q is read again for each), so a tile of 128 keys costs both
-// halves 2560 cycles of operand reads and TMA writes; it takes 2700 to 3000. 4097 queries
-// over 16411 states, 32 heads on 8, d = 128: 725 us, 1.51 PFLOP/s, 0.79 of the bf16 peak (0.74 where
-// the clock falls under the load); 16 prompts of 17 to 900 queries over 257 to 4100 states 180 us,
-// of which the join of cut units is 11 and a unit by itself (first maximum, O) 2 tiles' time.
-// Measured on the way, us for the first:
+// Bound, many rows: the chain from S over exponentials and the store of P to the next product, of
+// two softmax warps a scheduler. 4097 queries over 16411 states, 32 heads on 8, take 3240 cycles a
+// tile of 128 keys (256 rows) with d = 128 and 3110 with d = 64, where operand reads and products
+// halve and no unit of the SM is above 46 % busy (the MMA unit with its operand reads 46, its
+// products 34, exponentials 34, issue 44; counters at 2048 over 8192). With d = 128 that unit is
+// at 74 %: S of 64 keys takes 48 cycles an MMA where 128 would take 32 for as many (Q is read again
+// for each), 2560 cycles a tile with the TMA writes. d = 128: 725 to 740 us, 1.5 PFLOP/s, 0.78 of the bf16 peak, and less where the clock falls
+// under the load; d = 64: 663 us. 16 prompts of 17 to 900 queries over 257 to 4100 states: 181 us,
+// d = 64 159, of which the join of cut units is 11 and a unit by itself (first maximum, O) 2 tiles'
+// time.
+// Measured on the way, us for the first with d = 128:
 //   MMAs issued by single threads, S of 128 keys in one buffer a half       1016
 //     the same by converged warps that elect a lane (states_plan.cuh)        945
 //     and the halves made to take turns (P V and the next S of one, then
@@ -42,8 +47,8 @@
 //   S of 64 keys in two buffers, no turns                                    736
 //   P stored before its sum is looked at                                     725
 // Bound, few rows: the memory, 7.2 TB/s while tiles stream; 64 single tokens over 257 to 6404
-// states 148 us, 6.4 TB/s, with d = 64 82 us, 5.7 TB/s; a unit costs 2200 cycles by itself. One
-// token over 1601 states 14.6 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
+// states 150 us, 6.3 TB/s, with d = 64 83 us, 5.7 TB/s; a unit costs 2200 cycles by itself. One
+// token over 1601 states 14.3 us, where a trivial kernel takes 4: the plan (3000 cycles of dependent
 // loads and divisions), the first tile, one step, the join, in a row. (Joined by the last
 // piece to arrive, its two warps that add up the streams, and without the launch: the same for
 // this one token; 8 tokens of 32 heads over 1500 states 57 us, with the launch 21; 60 rows of one
@@ -67,7 +72,7 @@ constexpr int COST = 8, LESS = 5;
 constexpr int CHUNK = 64;    // keys whose P is handed on at a time
 constexpr float SUM_LIMIT = 32768.f;  // m moves when 64 keys' P sum up to more
 constexpr float FAR = 1 << 20;  // m up to which x - m may be taken in one rounding
-// (d = 64 leaves room for a third buffer of S a half: no gain, 229 us for 230)
+// (d = 64 leaves room for a third buffer of S a half: no gain where it was tried)
 constexpr uint32_t TMEM_COLS = 512, HALF_COLS = 256, O_COL = 128;
 
 struct CrossParams {
@@ -746,6 +751,7 @@ __device__ void softmax_few(const CrossParams &p, Smem<D> &sm, uint32_t tmem_bas
 #pragma unroll
             for (int st = 0; st < STREAMS; ++st) z = fmaf(v[st].y, ex2(v[st].x - m), z);
         }
+        // (__log2f and __fdividef for O alone, a bf16: off by 2^-21)
         float lse2 = z == 0.f ? -INFINITY : m + __log2f(z), inv = z == 0.f ? 0.f : __fdividef(1.f, z);
         if (!cut && p.sink_mode == 2) with_null_sink(bias, lse2, inv);
         const float f = ex2(row.m - m) * inv;

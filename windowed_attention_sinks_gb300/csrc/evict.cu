@@ -5,10 +5,11 @@
 // among equal ones. Weights count as max(w, 0) (NaN as 0), so their bits order them;
 // the least bits T that still stay are found from histograms of the range that they can lie in,
 // in 2048 parts, until a part is one number: three rounds at most, of which the later ones
-// meet few rows. Then each warp counts its run of rows above T
+// count few rows. Then each warp counts its run of rows above T
 // and equal to T, one scan over the warps places them, and the kept rows are written in
-// ascending order. The weights are read once into shared memory (the first CACHED of a head)
-// and four times from there.
+// ascending order. The first CACHED weights of a head are read once into shared memory, and in two
+// to five passes from there (the rounds, the counting, the placing); those behind it come from
+// global memory in every pass, and a kept row's weight once more when it is written.
 // Bound by instructions over few SMs (16000 rows: 16 us, two blocks an SM): load 4 us, the rounds 4,
 // the placing 4; digits of the bits as bins 30.
 // evict_gather: copies the kept rows of k and v, 16 bytes an item, in the order of the

@@ -15,15 +15,19 @@
 // Roles: warp 0 units and TMA; 1, 2 the products of two tiles each; 3 the rows' denominators;
 // 4-19 the tiles' sums.
 //
+// Sums are fp32, one running sum a key, in the order of the steps, of ex2.approx's 2^-22.
+//
 // Bound, many rows: products, exponentials and instructions of the sums would each take about
-// 2050 cycles a step of 512 keys by 128 rows; it takes 3500, tensor pipe and exponential unit
-// 58 and 61 % busy, as a tile's S cannot be made again before its sums have read it and TMEM has no
-// room for a second. 8 prompts of 100 to 2000 queries over 1000 to 8000 states, 32 heads on 8,
-// d = 128: 171 us, 1.35 PFLOP/s, 0.70 of the bf16 peak. (Two tiles a unit, a group of warps each, its
+// 2050 cycles a step of 512 keys by 128 rows; it takes 3590, tensor pipe and exponential unit
+// 62 and 61 % busy, as a tile's S cannot be made again before its sums have read it and TMEM has no
+// room for a second. With d = 64, half the products, 3310 cycles, exponentials 67 %: it is
+// the sums' turn that counts. 8 prompts of 100 to 2000 queries over 1000 to 8000 states, 32 heads on
+// 8, d = 128: 173 us, 1.34 PFLOP/s, 0.70 of the bf16 peak; d = 64 153 us. With inputs that L2 does
+// not hold yet 184 and 160. (Two tiles a unit, a group of warps each, its
 // rows' denominators loaded by itself: 252. The tile that is ready first issued first: 187.)
 // Bound, few rows: the memory. 64 single tokens over 257 to 6404 states: 90 us with the second
-// launch, 5.4 TB/s; with d = 64 48 us (128 tokens over as many 91, and 117 before neighbouring
-// heads were taken side by side, states_plan.cuh).
+// launch, 5.4 TB/s; with d = 64, added up, 56 us (128 tokens 91 written, and 117 before
+// neighbouring heads were taken side by side, states_plan.cuh).
 #include <math.h>
 #include <stdio.h>
 

@@ -48,7 +48,7 @@ struct Args {
 };
 
 // f / (2 pi) as a fraction of 2^64: the float's 24-bit integer times 2^64 / (2 pi), shifted
-// by its exponent. Off by at most 2^-62 |f|.
+// by its exponent. Off by less than 2^-64 (what is shifted out) + 2^-65 |f| (C's own rounding).
 __device__ __forceinline__ uint64_t turns(float f) {
     const uint32_t b = __float_as_uint(f);
     const int e = (int)(b >> 23 & 255);

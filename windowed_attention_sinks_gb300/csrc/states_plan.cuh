@@ -10,8 +10,8 @@
 // same time, whatever its lengths, and a few units spread over all SMs. Where the memory
 // bounds, two CTAs take a piece side by side, of a group of two heads one each: a token's rows of
 // both lie next to each other, and come from memory as one. (64 tokens over 257 to 6400 states of
-// 8 KV heads, d = 64: 112 us with pieces of one head, of which 23 were rows of other heads that L2
-// fetched and lost, 89 without those (map_rows), 79 so; d = 128, rows of twice the length: 77 and 76.) The
+// 8 KV heads, d = 64: 94 us with pieces of one head, 83 so, and 23 more where L2 fetched rows of
+// other heads and lost them (map_rows); d = 128, rows of twice the length: 152 and 150.) The
 // pieces of a unit that is cut leave partial results in the workspace, which are joined in a
 // fixed order. Everything is computed from the lengths on the device, so a
 // call needs no host copy of them and can be captured and replayed with other lengths.
