@@ -35,8 +35,8 @@
 // halve and no unit of the SM is above 46 % busy (the MMA unit with its operand reads 46, its
 // products 34, exponentials 34, issue 44; counters at 2048 over 8192). With d = 128 that unit is
 // at 74 %: S of 64 keys takes 48 cycles an MMA where 128 would take 32 for as many (Q is read again
-// for each), 2560 cycles a tile with the TMA writes. d = 128: 725 to 740 us, 1.5 PFLOP/s, 0.78 of the bf16 peak, and less where the clock falls
-// under the load; d = 64: 663 us. 16 prompts of 17 to 900 queries over 257 to 4100 states: 181 us,
+// for each), 2560 cycles a tile with the TMA writes. d = 128: 725 to 740 us, 1.5 PFLOP/s, 0.78 of
+// the bf16 peak, and less where the clock falls under the load; d = 64: 663 us. 16 prompts of 17 to 900 queries over 257 to 4100 states: 181 us,
 // d = 64 159, of which the join of cut units is 11 and a unit by itself (first maximum, O) 2 tiles'
 // time.
 // Measured on the way, us for the first with d = 128:
